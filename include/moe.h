@@ -415,6 +415,137 @@ MOE_API int moe_device_info(int32_t* sm_count, int32_t* supported);
 MOE_API int moe_route_static(const moe_config* cfg, const float* logits, int32_t* topk_idx, float* topk_w,
                              int32_t* slot, int32_t* ret_slot, int32_t* offsets, void* stream);
 
+/* ---- operators of a training and serving block around the expert layer --------------------------
+ *
+ * A dense gated feed-forward block (forward, backward and its form for few tokens), layer norm
+ * (forward, backward) and the AdamW step. Same rules as above: the caller owns every buffer and the
+ * stream, nothing is allocated or synchronised (moe_ffn_status synchronises), an argument error is
+ * returned before any launch. The tile-level pages have no counterpart of these operators.
+ */
+
+/* Types of values. */
+#define MOE_DTYPE_F32 0
+#define MOE_DTYPE_BF16 1
+#define MOE_DTYPE_F16 2
+
+/*
+ * Gated feed-forward block, bf16 operands, fp32 accumulation:
+ *   y = h W2^T, h = silu(x W1^T) * (x W3^T); x, y [T, d]; W1, W3 [ffn, d]; W2 [d, ffn].
+ * Limits: T >= 0, d and ffn positive multiples of 8 below 2^20, T < 2^24. reserved must be zero.
+ * timeout_us bounds every device-side wait (0 = 2,000,000 us).
+ */
+typedef struct moe_ffn_config {
+    int32_t T, d, ffn;
+    uint32_t timeout_us;
+    int32_t reserved[4];
+} moe_ffn_config;
+
+#define MOE_FFN_STATUS_BYTES 256
+
+/* Bytes of the workspace of both passes, and of the buffer in which the forward pass keeps what the
+ * backward pass needs (h in bf16, the two projections in fp32). Host arithmetic only. */
+MOE_API int moe_ffn_workspace_size(const moe_ffn_config* cfg, size_t* bytes);
+MOE_API int moe_ffn_saved_size(const moe_ffn_config* cfg, size_t* bytes);
+
+/*
+ * moe_ffn_forward: x, W1, W3, W2, y device bf16 as above, 16-byte aligned and contiguous.
+ *   saved  device buffer of moe_ffn_saved_size bytes for a later moe_ffn_backward, or NULL
+ *   ws     device workspace of ws_bytes >= moe_ffn_workspace_size(cfg)
+ * saved and ws are 256-byte aligned; the first MOE_FFN_STATUS_BYTES of ws are zeroed by the caller once,
+ * before its first call (the status words). h is rounded to bf16 once, as the operand of the second
+ * product; everything else stays fp32 until y is rounded. With saved NULL and few tokens the weights
+ * are streamed once by kernels made for that (the form of single-token decoding); the sums then
+ * run in another order, so y may differ in its last bit from the call with saved.
+ */
+MOE_API int moe_ffn_forward(const moe_ffn_config* cfg, const uint16_t* x, const uint16_t* W1, const uint16_t* W3,
+                            const uint16_t* W2, uint16_t* y, void* saved, void* ws, size_t ws_bytes, void* stream);
+
+/*
+ * moe_ffn_backward: gradients of a loss whose gradient at y is dy (device bf16 [T, d]), given the
+ * forward pass's inputs and its saved buffer (read only: more than one backward pass may use it).
+ *   dx device bf16 [T, d]; dW1, dW3 [ffn, d]; dW2 [d, ffn] (all overwritten; 16-byte aligned)
+ * With T = 0 the weight gradients are set to zero.
+ */
+MOE_API int moe_ffn_backward(const moe_ffn_config* cfg, const uint16_t* x, const uint16_t* W1, const uint16_t* W3,
+                             const uint16_t* W2, const uint16_t* dy, const void* saved, uint16_t* dx, uint16_t* dW1,
+                             uint16_t* dW3, uint16_t* dW2, void* ws, size_t ws_bytes, void* stream);
+
+/* Synchronises `stream`, then reads the device status word of the calls on `ws` since its first bytes
+ * were zeroed: MOE_OK, or MOE_ERR_TIMEOUT with *detail = where a bounded wait ran out. */
+MOE_API int moe_ffn_status(const moe_ffn_config* cfg, const void* ws, void* stream, int32_t* detail);
+
+/*
+ * Layer norm over rows of d values: y = (x - mean) * rstd * w + b, rstd = 1 / sqrt(var + eps), var
+ * the mean of (x - mean)^2. x, y, dy, dx have type dtype (MOE_DTYPE_*), w, b, dw, db type wdtype
+ * (MOE_DTYPE_F32 or dtype); mean, rstd [rows] and every sum are fp32.
+ * Limits: rows >= 0, 1 <= d <= 16384, eps >= 0. Contiguous; pointers aligned to their type.
+ */
+typedef struct moe_layernorm_config {
+    int64_t rows;
+    int32_t d, dtype, wdtype;
+    float eps;
+    int32_t reserved[4];
+} moe_layernorm_config;
+
+/* w, b may be NULL (1 and 0); mean, rstd may be NULL when no backward pass follows. y may be x. */
+MOE_API int moe_layernorm_forward(const moe_layernorm_config* cfg, const void* x, const void* w, const void* b,
+                                  void* y, float* mean, float* rstd, void* stream);
+
+/* Bytes of the backward pass's workspace (partial sums of dw and db). */
+MOE_API int moe_layernorm_workspace_size(const moe_layernorm_config* cfg, size_t* bytes);
+
+/* dx, and dw = sum over rows of dy * (x - mean) * rstd, db = sum of dy: summed in an order that
+ * depends on the config and the device alone, so results repeat bit for bit. w may be NULL; dw and db may be NULL
+ * (then ws may be NULL too). dx may be dy. */
+MOE_API int moe_layernorm_backward(const moe_layernorm_config* cfg, const void* dy, const void* x, const void* w,
+                                   const float* mean, const float* rstd, void* dx, void* dw, void* db, void* ws,
+                                   size_t ws_bytes, void* stream);
+
+/*
+ * AdamW step over a list of tensors:
+ *   g' = g * grad_scale; m = beta1 m + (1 - beta1) g'; v = beta2 v + (1 - beta2) g'^2
+ *   p = p (1 - lr weight_decay) - lr / (1 - beta1^step) * m / (sqrt(v) / sqrt(1 - beta2^step) + eps)
+ * bits = 32: m and v fp32. bits = 8: m and v are held in blocks of MOE_ADAMW_BLOCK consecutive values
+ * of a tensor, one byte a value and one scale byte a block for each; scale byte s stands for
+ * 2^(s - 127), 0 for 0 and 255 for NaN (a block that a non-finite value has entered reads as NaN).
+ * A byte of m is sign, 4 exponent bits (bias 7) and 3 mantissa bits; a byte of v 5 exponent bits
+ * (bias 15) and 3 mantissa bits; exponent 0 is subnormal. A zeroed buffer is a zero state. p is
+ * updated from m and v before they are rounded. The rounding is stochastic (unbiased), so an average
+ * that moves by less than a rounding step a call still moves: up or down is decided by 16 bits of a
+ * hash of (seed, step, rng_base + i) for value i, so the result repeats for the same arguments.
+ */
+#define MOE_ADAMW_BLOCK 128
+typedef struct moe_adamw_config {
+    double lr, beta1, beta2, eps, weight_decay;
+    int64_t step;  /* of this call, from 1 */
+    uint64_t seed; /* of the stochastic rounding (bits = 8) */
+    int32_t bits;  /* 32 or 8 */
+    int32_t reserved[3];
+} moe_adamw_config;
+
+typedef struct moe_adamw_tensor {
+    void* p;          /* parameters, fp32 or bf16, updated */
+    const void* g;    /* gradients, fp32 or bf16 */
+    void* copy;       /* bf16 copy of the updated parameters, or NULL */
+    void* m;          /* fp32 [n], or uint8 [n] with bits = 8 */
+    void* v;
+    uint8_t* m_scale; /* uint8 [ceil(n / MOE_ADAMW_BLOCK)] with bits = 8, else unused */
+    uint8_t* v_scale;
+    int64_t n;        /* values; 0 is allowed */
+    int64_t rng_base; /* index of value 0 among all the values that the seed serves */
+    int32_t p_dtype, g_dtype;
+} moe_adamw_tensor;
+
+/* tensors: host array, read during the call; grad_scale: device fp32 scalar, or NULL for 1. Pointers
+ * need only the alignment of their type (16-byte aligned ones are faster). Tensors must not overlap. */
+MOE_API int moe_adamw_step(const moe_adamw_config* cfg, const moe_adamw_tensor* tensors, int32_t count,
+                           const float* grad_scale, void* stream);
+
+/* The values that 8-bit states stand for: fp32 m and v of tensor i into m_out[i] and v_out[i] (host
+ * arrays of device pointers; an entry may be NULL). For checkpoints and inspection. */
+MOE_API int moe_adamw_read_state(const moe_adamw_tensor* tensors, int32_t count, float* const* m_out,
+                                 float* const* v_out, void* stream);
+
 /* Message of the last error on the calling thread ("" if none). The pointer stays valid until
  * the thread's next call into the library. */
 MOE_API const char* moe_last_error(void);

@@ -43,10 +43,19 @@ TRACE_GEMM2_START, TRACE_GEMM2_END, TRACE_COPY_START, TRACE_COPY_END = 0, 1, 2, 
 TRACE_BAND_DONE, TRACE_LAST_ACQUIRE, TRACE_LAST_LOAD, TRACE_LAST_DRAIN = 4, 5, 6, 7
 TRACE_UP_CYCLES, TRACE_UP_NS, TRACE_DOWN_CYCLES, TRACE_DOWN_NS = 8, 9, 10, 11
 
+# types of values, block of the 8-bit optimiser states, status bytes of a feed-forward workspace
+MOE_DTYPE_F32, MOE_DTYPE_BF16, MOE_DTYPE_F16 = 0, 1, 2
+MOE_ADAMW_BLOCK = 128
+MOE_FFN_STATUS_BYTES = 256
+_DTYPES = {torch.float32: MOE_DTYPE_F32, torch.bfloat16: MOE_DTYPE_BF16, torch.float16: MOE_DTYPE_F16}
+
 # names of the C entry points (each declared in include/moe.h)
 EXPORTS = ("moe_workspace_size", "moe_workspace_layout", "moe_plan", "moe_forward", "moe_forward_sequential",
            "moe_forward_ex", "moe_forward_host", "moe_forward_host_pipelined", "moe_copy_only", "moe_dma_host_bytes",
-           "moe_forward_dma", "moe_status", "moe_device_info", "moe_route_static", "moe_last_error")
+           "moe_forward_dma", "moe_status", "moe_device_info", "moe_route_static", "moe_ffn_workspace_size",
+           "moe_ffn_saved_size", "moe_ffn_forward", "moe_ffn_backward", "moe_ffn_status", "moe_layernorm_forward",
+           "moe_layernorm_workspace_size", "moe_layernorm_backward", "moe_adamw_step", "moe_adamw_read_state",
+           "moe_last_error")
 
 # stage events of moe_forward_ex
 EV_BEGIN, EV_PLANNED, EV_UP, EV_DOWN, EV_COPIED, EV_END, EV_COUNT = range(7)
@@ -104,6 +113,26 @@ class Config:
         return cls(T=w.T, d=w.d, ffn=w.ffn, E=w.E, topk=w.topk, R=w.R, tile_M=w.tile_M, **kw)
 
 
+class _FFNConfig(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("T", "d", "ffn")] + [
+        ("timeout_us", ctypes.c_uint32), ("reserved", ctypes.c_int32 * 4)]
+
+
+class _LayerNormConfig(ctypes.Structure):
+    _fields_ = [("rows", ctypes.c_int64), ("d", ctypes.c_int32), ("dtype", ctypes.c_int32),
+                ("wdtype", ctypes.c_int32), ("eps", ctypes.c_float), ("reserved", ctypes.c_int32 * 4)]
+
+
+class _AdamWConfig(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_double) for n in ("lr", "beta1", "beta2", "eps", "weight_decay")] + [
+        ("step", ctypes.c_int64), ("seed", ctypes.c_uint64), ("bits", ctypes.c_int32), ("reserved", ctypes.c_int32 * 3)]
+
+
+class _AdamWTensor(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_void_p) for n in ("p", "g", "copy", "m", "v", "m_scale", "v_scale")] + [
+        ("n", ctypes.c_int64), ("rng_base", ctypes.c_int64), ("p_dtype", ctypes.c_int32), ("g_dtype", ctypes.c_int32)]
+
+
 _lib = None
 
 
@@ -131,6 +160,18 @@ def lib() -> ctypes.CDLL:
         L.moe_status.argtypes = [cfgp, vp, vp, i32p]
         L.moe_device_info.argtypes = [i32p, i32p]
         L.moe_route_static.argtypes = [cfgp, vp, vp, vp, vp, vp, vp, vp]
+        fcfg, lcfg, acfg = (ctypes.POINTER(t) for t in (_FFNConfig, _LayerNormConfig, _AdamWConfig))
+        szp, tens, vpp = ctypes.POINTER(sz), ctypes.POINTER(_AdamWTensor), ctypes.POINTER(vp)
+        L.moe_ffn_workspace_size.argtypes = [fcfg, szp]
+        L.moe_ffn_saved_size.argtypes = [fcfg, szp]
+        L.moe_ffn_forward.argtypes = [fcfg] + [vp] * 7 + [sz, vp]
+        L.moe_ffn_backward.argtypes = [fcfg] + [vp] * 11 + [sz, vp]
+        L.moe_ffn_status.argtypes = [fcfg, vp, vp, i32p]
+        L.moe_layernorm_forward.argtypes = [lcfg] + [vp] * 7
+        L.moe_layernorm_workspace_size.argtypes = [lcfg, szp]
+        L.moe_layernorm_backward.argtypes = [lcfg] + [vp] * 9 + [sz, vp]
+        L.moe_adamw_step.argtypes = [acfg, tens, ctypes.c_int32, vp, vp]
+        L.moe_adamw_read_state.argtypes = [tens, ctypes.c_int32, vpp, vpp, vp]
         L.moe_last_error.restype = ctypes.c_char_p
         for n in EXPORTS[:-1]:
             getattr(L, n).restype = ctypes.c_int
@@ -343,3 +384,257 @@ def device_info():
     sms, ok = ctypes.c_int32(), ctypes.c_int32()
     _check(lib().moe_device_info(ctypes.byref(sms), ctypes.byref(ok)))
     return sms.value, bool(ok.value)
+
+
+# ---- operators of a training and serving block around the layer -----------------------------------
+
+
+def _shape(t: Optional[torch.Tensor], shape, name: str) -> None:
+    if t is not None and tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+
+
+@dataclasses.dataclass
+class FFNConfig:
+    """Gated feed-forward block (mirrors moe_ffn_config): x, y [T, d]; W1, W3 [ffn, d]; W2 [d, ffn]."""
+
+    T: int
+    d: int
+    ffn: int
+    timeout_us: int = 0
+
+    def to_c(self) -> _FFNConfig:
+        return _FFNConfig(int(self.T), int(self.d), int(self.ffn), int(self.timeout_us))
+
+
+class FFNWorkspace:
+    """Device workspace of one feed-forward config; its status words start as zero."""
+
+    def __init__(self, cfg: FFNConfig, device="cuda"):
+        n, c = ctypes.c_size_t(), cfg.to_c()
+        _check(lib().moe_ffn_workspace_size(ctypes.byref(c), ctypes.byref(n)))
+        self.nbytes = n.value
+        self.buf = torch.empty(self.nbytes, dtype=torch.uint8, device=device)
+        self.buf[:MOE_FFN_STATUS_BYTES].zero_()
+
+    @property
+    def ptr(self) -> ctypes.c_void_p:
+        return ctypes.c_void_p(self.buf.data_ptr())
+
+
+def ffn_saved(cfg: FFNConfig, device="cuda") -> torch.Tensor:
+    """Buffer in which ffn_forward keeps what ffn_backward needs (uint8, opaque)."""
+    n, c = ctypes.c_size_t(), cfg.to_c()
+    _check(lib().moe_ffn_saved_size(ctypes.byref(c), ctypes.byref(n)))
+    return torch.empty(n.value, dtype=torch.uint8, device=device)
+
+
+def _ffn_weights(cfg: FFNConfig, W1, W3, W2, prefix=""):
+    bf, up, down = torch.bfloat16, (cfg.ffn, cfg.d), (cfg.d, cfg.ffn)
+    _shape(W1, up, prefix + "W1")
+    _shape(W3, up, prefix + "W3")
+    _shape(W2, down, prefix + "W2")
+    return (_ptr(W1, bf, "cuda", prefix + "W1"), _ptr(W3, bf, "cuda", prefix + "W3"),
+            _ptr(W2, bf, "cuda", prefix + "W2"))
+
+
+def _ffn_rows(cfg: FFNConfig, t, name):
+    _shape(t, (cfg.T, cfg.d), name)
+    return _ptr(t, torch.bfloat16, "cuda", name)
+
+
+def _ffn_saved_ptr(cfg: FFNConfig, c, saved):
+    if saved is None:
+        return None
+    n = ctypes.c_size_t()
+    _check(lib().moe_ffn_saved_size(ctypes.byref(c), ctypes.byref(n)))
+    if saved.numel() * saved.element_size() < n.value:
+        raise ValueError(f"saved has {saved.numel() * saved.element_size()} bytes, needs {n.value}")
+    return _ptr(saved, None, "cuda", "saved")
+
+
+def ffn_forward(cfg: FFNConfig, x: torch.Tensor, W1: torch.Tensor, W3: torch.Tensor, W2: torch.Tensor,
+                y: torch.Tensor, ws: FFNWorkspace, saved: Optional[torch.Tensor] = None, stream=None) -> None:
+    """moe_ffn_forward: y = (silu(x W1^T) * (x W3^T)) W2^T; saved (ffn_saved) for a backward pass."""
+    c = cfg.to_c()
+    _check(lib().moe_ffn_forward(ctypes.byref(c), _ffn_rows(cfg, x, "x"), *_ffn_weights(cfg, W1, W3, W2),
+                                 _ffn_rows(cfg, y, "y"), _ffn_saved_ptr(cfg, c, saved), ws.ptr, ws.nbytes,
+                                 _stream(stream)))
+
+
+def ffn_backward(cfg: FFNConfig, x: torch.Tensor, W1: torch.Tensor, W3: torch.Tensor, W2: torch.Tensor,
+                 dy: torch.Tensor, saved: torch.Tensor, dx: torch.Tensor, dW1: torch.Tensor, dW3: torch.Tensor,
+                 dW2: torch.Tensor, ws: FFNWorkspace, stream=None) -> None:
+    """moe_ffn_backward: gradients of x and the weights from dy and the forward pass's saved buffer."""
+    c = cfg.to_c()
+    _check(lib().moe_ffn_backward(ctypes.byref(c), _ffn_rows(cfg, x, "x"), *_ffn_weights(cfg, W1, W3, W2),
+                                  _ffn_rows(cfg, dy, "dy"), _ffn_saved_ptr(cfg, c, saved), _ffn_rows(cfg, dx, "dx"),
+                                  *_ffn_weights(cfg, dW1, dW3, dW2, "d"), ws.ptr, ws.nbytes, _stream(stream)))
+
+
+def ffn_status(cfg: FFNConfig, ws: FFNWorkspace, stream=None):
+    """(return code, detail) of the calls on ws; synchronises the stream."""
+    c, detail = cfg.to_c(), ctypes.c_int32()
+    rc = lib().moe_ffn_status(ctypes.byref(c), ws.ptr, _stream(stream), ctypes.byref(detail))
+    return rc, detail.value
+
+
+@dataclasses.dataclass
+class LayerNormConfig:
+    """Layer norm over rows of d values (mirrors moe_layernorm_config)."""
+
+    rows: int
+    d: int
+    dtype: torch.dtype = torch.bfloat16
+    wdtype: torch.dtype = torch.float32
+    eps: float = 1e-5
+
+    def to_c(self) -> _LayerNormConfig:
+        if self.dtype not in _DTYPES or self.wdtype not in _DTYPES:
+            raise ValueError(f"layer norm takes float32, bfloat16 or float16, got {self.dtype}, {self.wdtype}")
+        return _LayerNormConfig(int(self.rows), int(self.d), _DTYPES[self.dtype], _DTYPES[self.wdtype],
+                                float(self.eps))
+
+
+class LayerNormWorkspace:
+    """Device workspace of layernorm_backward."""
+
+    def __init__(self, cfg: LayerNormConfig, device="cuda"):
+        n, c = ctypes.c_size_t(), cfg.to_c()
+        _check(lib().moe_layernorm_workspace_size(ctypes.byref(c), ctypes.byref(n)))
+        self.nbytes = n.value
+        self.buf = torch.empty(self.nbytes, dtype=torch.uint8, device=device)
+
+    @property
+    def ptr(self) -> ctypes.c_void_p:
+        return ctypes.c_void_p(self.buf.data_ptr())
+
+
+def _ln_rows(cfg: LayerNormConfig, t, name):
+    if t.numel() != cfg.rows * cfg.d or t.shape[-1] != cfg.d:
+        raise ValueError(f"{name} must hold {cfg.rows} rows of {cfg.d} values, got {tuple(t.shape)}")
+    return _ptr(t, cfg.dtype, "cuda", name)
+
+
+def _ln_vec(t, n, dtype, name):
+    if t is not None and t.numel() != n:
+        raise ValueError(f"{name} must hold {n} values, got {t.numel()}")
+    return _ptr(t, dtype, "cuda", name)
+
+
+def layernorm_forward(cfg: LayerNormConfig, x: torch.Tensor, w: Optional[torch.Tensor], b: Optional[torch.Tensor],
+                      y: torch.Tensor, mean: Optional[torch.Tensor] = None, rstd: Optional[torch.Tensor] = None,
+                      stream=None) -> None:
+    """moe_layernorm_forward: y = (x - mean) * rstd * w + b; mean and rstd [rows] for a backward pass."""
+    c, f32 = cfg.to_c(), torch.float32
+    _check(lib().moe_layernorm_forward(ctypes.byref(c), _ln_rows(cfg, x, "x"), _ln_vec(w, cfg.d, cfg.wdtype, "w"),
+                                       _ln_vec(b, cfg.d, cfg.wdtype, "b"), _ln_rows(cfg, y, "y"),
+                                       _ln_vec(mean, cfg.rows, f32, "mean"), _ln_vec(rstd, cfg.rows, f32, "rstd"),
+                                       _stream(stream)))
+
+
+def layernorm_backward(cfg: LayerNormConfig, dy: torch.Tensor, x: torch.Tensor, w: Optional[torch.Tensor],
+                       mean: torch.Tensor, rstd: torch.Tensor, dx: torch.Tensor, dw: Optional[torch.Tensor] = None,
+                       db: Optional[torch.Tensor] = None, ws: Optional[LayerNormWorkspace] = None,
+                       stream=None) -> None:
+    """moe_layernorm_backward: dx, and dw, db summed over the rows (both may be None, then ws too)."""
+    c, f32 = cfg.to_c(), torch.float32
+    _check(lib().moe_layernorm_backward(
+        ctypes.byref(c), _ln_rows(cfg, dy, "dy"), _ln_rows(cfg, x, "x"), _ln_vec(w, cfg.d, cfg.wdtype, "w"),
+        _ln_vec(mean, cfg.rows, f32, "mean"), _ln_vec(rstd, cfg.rows, f32, "rstd"), _ln_rows(cfg, dx, "dx"),
+        _ln_vec(dw, cfg.d, cfg.wdtype, "dw"), _ln_vec(db, cfg.d, cfg.wdtype, "db"),
+        None if ws is None else ws.ptr, 0 if ws is None else ws.nbytes, _stream(stream)))
+
+
+@dataclasses.dataclass
+class AdamWConfig:
+    """AdamW's numbers (mirrors moe_adamw_config; the step is an argument of adamw_step). bits: 32 or 8."""
+
+    lr: float
+    beta1: float = 0.9
+    beta2: float = 0.999
+    eps: float = 1e-8
+    weight_decay: float = 0.01
+    bits: int = 32
+    seed: int = 0
+
+    def to_c(self, step: int) -> _AdamWConfig:
+        return _AdamWConfig(self.lr, self.beta1, self.beta2, self.eps, self.weight_decay, int(step),
+                            int(self.seed) & (2 ** 64 - 1), int(self.bits))
+
+
+class AdamWList:
+    """The tensors of an AdamW step, marshalled once: parameters p and gradients g (float32 or bfloat16),
+    states m and v (float32; with bits = 8 uint8 codes with one uint8 scale per MOE_ADAMW_BLOCK values in
+    m_scale, v_scale), and optional bfloat16 copies of the updated parameters. rng_base: index of each
+    tensor's first value under the config's seed (default: one tensor after another, each rounded up
+    to whole blocks). The list keeps its tensors alive; a tensor that moves needs a new list."""
+
+    def __init__(self, cfg: AdamWConfig, p, g, m, v, m_scale=None, v_scale=None, copy=None, rng_base=None):
+        n, f32, bf, u8 = len(p), torch.float32, torch.bfloat16, torch.uint8
+        eight = cfg.bits == 8
+        if eight != (m_scale is not None) or eight != (v_scale is not None):
+            raise ValueError("m_scale and v_scale go with bits = 8")
+        for name, l in (("g", g), ("m", m), ("v", v), ("m_scale", m_scale), ("v_scale", v_scale), ("copy", copy),
+                        ("rng_base", rng_base)):
+            if l is not None and len(l) != n:
+                raise ValueError(f"{name} must have one entry per tensor")
+        self.bits, self.count = cfg.bits, n
+        self.c = (_AdamWTensor * max(n, 1))()
+        self.keep = [p, g, m, v, m_scale, v_scale, copy]
+        base = 0
+        for i in range(n):
+            k = p[i].numel()
+            blocks = -(-k // MOE_ADAMW_BLOCK)
+            for name, t, dt, want in (("p", p[i], (f32, bf), k), ("g", g[i], (f32, bf), k),
+                                      ("m", m[i], (u8,) if eight else (f32,), k),
+                                      ("v", v[i], (u8,) if eight else (f32,), k),
+                                      ("m_scale", m_scale[i] if eight else None, (u8,), blocks),
+                                      ("v_scale", v_scale[i] if eight else None, (u8,), blocks),
+                                      ("copy", copy[i] if copy is not None else None, (bf,), k)):
+                if t is None:
+                    continue
+                if t.dtype not in dt:
+                    raise ValueError(f"{name}[{i}] must be {' or '.join(map(str, dt))}, got {t.dtype}")
+                if t.numel() != want:
+                    raise ValueError(f"{name}[{i}] must hold {want} values, got {t.numel()}")
+                setattr(self.c[i], name, (_ptr(t, None, "cuda", f"{name}[{i}]")))
+            e = self.c[i]
+            e.n, e.rng_base = k, base if rng_base is None else int(rng_base[i])
+            e.p_dtype, e.g_dtype = _DTYPES[p[i].dtype], _DTYPES[g[i].dtype]
+            base += blocks * MOE_ADAMW_BLOCK
+
+
+class AdamWValues:
+    """Where adamw_read_state writes: float32 tensors, one m and one v for each tensor of the list."""
+
+    def __init__(self, tensors: AdamWList, m, v):
+        if len(m) != tensors.count or len(v) != tensors.count:
+            raise ValueError("m and v must have one entry per tensor")
+        arr = ctypes.c_void_p * max(tensors.count, 1)
+        for name, l in (("m", m), ("v", v)):
+            for i, t in enumerate(l):
+                if t.numel() != tensors.c[i].n:
+                    raise ValueError(f"{name}[{i}] must hold {tensors.c[i].n} values, got {t.numel()}")
+        self.m = arr(*[_ptr(t, torch.float32, "cuda", "m") for t in m])
+        self.v = arr(*[_ptr(t, torch.float32, "cuda", "v") for t in v])
+        self.keep = [m, v]
+
+
+def adamw_step(cfg: AdamWConfig, tensors: AdamWList, step: int, grad_scale: Optional[torch.Tensor] = None,
+               stream=None) -> None:
+    """moe_adamw_step: one step (counted from 1) over every tensor; grad_scale: a float32 value on the GPU."""
+    if cfg.bits != tensors.bits:
+        raise ValueError(f"the list was made for {tensors.bits}-bit states")
+    if grad_scale is not None and grad_scale.numel() != 1:
+        raise ValueError("grad_scale must hold one value")
+    c = cfg.to_c(step)
+    _check(lib().moe_adamw_step(ctypes.byref(c), tensors.c, tensors.count,
+                                _ptr(grad_scale, torch.float32, "cuda", "grad_scale"), _stream(stream)))
+
+
+def adamw_read_state(cfg: AdamWConfig, tensors: AdamWList, out: AdamWValues, stream=None) -> None:
+    """moe_adamw_read_state: the float32 values that the list's 8-bit states stand for."""
+    if cfg.bits != 8 or tensors.bits != 8:
+        raise ValueError("32-bit states are read as they are")
+    _check(lib().moe_adamw_read_state(tensors.c, tensors.count, out.m, out.v, _stream(stream)))

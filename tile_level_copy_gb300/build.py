@@ -18,7 +18,7 @@ CSRC = os.path.join(HERE, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 OUT_DIR = os.path.join(HERE, "_lib")
 LIB = os.path.join(OUT_DIR, "libmoe.so")
-SOURCES = ["route_plan.cu", "gemm.cu", "combine.cu", "moe_abi.cu"]
+SOURCES = ["route_plan.cu", "gemm.cu", "combine.cu", "moe_abi.cu", "ffn.cu", "layernorm.cu", "adamw.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC,-fvisibility=hidden", "-I", INCLUDE]
 

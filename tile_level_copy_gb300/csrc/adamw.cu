@@ -1,0 +1,486 @@
+// AdamW over a list of tensors in one launch, states in 32 or in 8 bits.
+//
+//   g' = g * grad_scale
+//   m  = beta1 m + (1 - beta1) g'            v = beta2 v + (1 - beta2) g'^2
+//   p  = p (1 - lr wd) - lr / (1 - beta1^t) * m / (sqrt(v) / sqrt(1 - beta2^t) + eps)
+//
+// Every value is read and written once, so the bound is HBM traffic: 28 bytes a value with fp32
+// states, bf16 gradients and a bf16 copy, 16 with 8-bit states. The list travels in the launch's
+// parameters (no table in device memory to keep in step with the caller's pointers, nothing to copy
+// before the launch, and a captured graph holds it).
+//
+// 8-bit states. A block of 128 consecutive values has one power-of-two scale for m and one for v, so
+// scaling is exact and costs no precision; within a block m keeps 4 exponent bits and 3 mantissa
+// bits beside its sign, v (never negative, and spread over twice the exponent range) 5 and 3. Both
+// averages change by less than half a rounding step a call (v by 0.1 % with beta2 = 0.999, against
+// steps of 6-12 %), so rounding to nearest would never move them: the rounding is stochastic, up
+// with a probability equal to the part that is cut off. A value scaled to its code's exponent
+// range is an fp32 number whose top bits are the code (subnormal codes are subnormal fp32 numbers),
+// so encoding is: add 20 random bits to the bit pattern, shift right by 20.
+#include <math.h>
+
+#include "host_internal.h"
+#include "moe_internal.cuh"
+
+namespace moe {
+namespace {
+
+constexpr int AW_THREADS = 256;
+constexpr int AW_CHUNK = 4096;  // values of a tensor that a CTA takes at a time
+constexpr int AW_BLOCK = MOE_ADAMW_BLOCK;
+static_assert(AW_CHUNK % AW_BLOCK == 0, "a chunk holds whole blocks");
+
+struct AwTensor {
+    void* p;
+    const void* g;
+    __nv_bfloat16* copy;
+    void* m;
+    void* v;
+    uint8_t* ms;
+    uint8_t* vs;
+    int64_t n;
+    int64_t base;
+};
+
+enum : uint8_t { AW_P16 = 1, AW_G16 = 2, AW_VEC = 4 };  // bf16 p, bf16 g, pointers aligned for vectors
+
+template <int MAXT>
+struct AwList {
+    AwTensor t[MAXT];
+    int32_t first[MAXT + 1];  // first chunk of each tensor
+    uint8_t flags[MAXT];
+    int32_t count;
+};
+
+struct AwScalars {
+    float b1, b1c, b2, b2c;  // beta1, 1 - beta1, beta2, 1 - beta2
+    float decay, step, vscale, eps;
+    uint32_t k0, k1;
+    const float* grad_scale;
+};
+
+__host__ __device__ __forceinline__ uint32_t mix32(uint32_t x, uint32_t k) {
+    // multiply-xorshift rounds (the constants of Wellons' published low-bias 32-bit mixer), with a
+    // second key added between the two
+    x ^= x >> 16;
+    x *= 0x7FEB352Du;
+    x = (x ^ (x >> 15)) + k;
+    x *= 0x846CA68Bu;
+    return x ^ (x >> 16);
+}
+
+// m and v of one value. The products and sums are rounded one by one (no contraction), so that a
+// state in 8 bits, whose rounding turns on every bit, is the one the formulas give in fp32.
+__device__ __forceinline__ void moments(const AwScalars& s, float g, float& m, float& v) {
+    m = __fadd_rn(__fmul_rn(m, s.b1), __fmul_rn(g, s.b1c));
+    v = __fadd_rn(__fmul_rn(v, s.b2), __fmul_rn(__fmul_rn(g, g), s.b2c));
+}
+__device__ __forceinline__ float updated(const AwScalars& s, float p, float m, float v) {
+    float r;
+    asm("sqrt.approx.f32 %0, %1;" : "=f"(r) : "f"(v));
+    return p * s.decay - s.step * __fdividef(m, r * s.vscale + s.eps);
+}
+
+struct Four {
+    float a[4];
+};
+template <bool VEC>
+__device__ __forceinline__ Four load4_f32(const void* base, int64_t i, int k) {
+    const float* p = static_cast<const float*>(base) + i;
+    Four r{{0.f, 0.f, 0.f, 0.f}};
+    if (VEC && k == 4) {
+        const float4 q = *reinterpret_cast<const float4*>(p);
+        r.a[0] = q.x, r.a[1] = q.y, r.a[2] = q.z, r.a[3] = q.w;
+    } else {
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            if (j < k) r.a[j] = p[j];
+    }
+    return r;
+}
+template <bool VEC>
+__device__ __forceinline__ Four load4_bf16(const void* base, int64_t i, int k) {
+    const __nv_bfloat16* p = static_cast<const __nv_bfloat16*>(base) + i;
+    Four r{{0.f, 0.f, 0.f, 0.f}};
+    if (VEC && k == 4) {
+        const uint2 q = *reinterpret_cast<const uint2*>(p);
+        r.a[0] = __uint_as_float(q.x << 16), r.a[1] = __uint_as_float(q.x & 0xffff0000u);
+        r.a[2] = __uint_as_float(q.y << 16), r.a[3] = __uint_as_float(q.y & 0xffff0000u);
+    } else {
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            if (j < k) r.a[j] = __bfloat162float(p[j]);
+    }
+    return r;
+}
+template <bool VEC>
+__device__ __forceinline__ void store4_f32(void* base, int64_t i, int k, const Four& r) {
+    float* p = static_cast<float*>(base) + i;
+    if (VEC && k == 4) {
+        *reinterpret_cast<float4*>(p) = make_float4(r.a[0], r.a[1], r.a[2], r.a[3]);
+    } else {
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            if (j < k) p[j] = r.a[j];
+    }
+}
+template <bool VEC>
+__device__ __forceinline__ void store4_bf16(void* base, int64_t i, int k, const Four& r) {
+    __nv_bfloat16* p = static_cast<__nv_bfloat16*>(base) + i;
+    if (VEC && k == 4) {
+        *reinterpret_cast<uint2*>(p) = make_uint2(pack_bf16x2(r.a[0], r.a[1]), pack_bf16x2(r.a[2], r.a[3]));
+    } else {
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            if (j < k) p[j] = __float2bfloat16_rn(r.a[j]);
+    }
+}
+template <bool VEC>
+__device__ __forceinline__ uint32_t load4_u8(const void* base, int64_t i, int k) {
+    const uint8_t* p = static_cast<const uint8_t*>(base) + i;
+    if (VEC && k == 4) return *reinterpret_cast<const uint32_t*>(p);
+    uint32_t r = 0;
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+        if (j < k) r |= (uint32_t)p[j] << (8 * j);
+    return r;
+}
+template <bool VEC>
+__device__ __forceinline__ void store4_u8(void* base, int64_t i, int k, uint32_t r) {
+    uint8_t* p = static_cast<uint8_t*>(base) + i;
+    if (VEC && k == 4) {
+        *reinterpret_cast<uint32_t*>(p) = r;
+    } else {
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            if (j < k) p[j] = (uint8_t)(r >> (8 * j));
+    }
+}
+
+// ---- 8-bit codes -------------------------------------------------------------------------------
+constexpr int M_TOP = 7, V_TOP = 15;  // a block's largest value is scaled into [2^TOP, 2^(TOP + 1))
+
+__device__ __forceinline__ float scale_value(uint32_t s) {
+    return s == 255u ? __uint_as_float(0x7fc00000u) : __uint_as_float(s << 23);  // 0: 0
+}
+__device__ __forceinline__ float m_value(uint32_t c, float scale) {
+    const float a = __fmul_rn(__uint_as_float((c & 0x7fu) << 20), 0x1p120f);
+    return __fmul_rn(__uint_as_float(__float_as_uint(a) | ((c & 0x80u) << 24)), scale);
+}
+__device__ __forceinline__ float v_value(uint32_t c, float scale) {
+    return __fmul_rn(__fmul_rn(__uint_as_float(c << 20), 0x1p112f), scale);
+}
+// Scale byte for a block whose largest magnitude has the bit pattern `most`.
+__device__ __forceinline__ uint32_t block_scale(uint32_t most, int top) {
+    if (most >= 0x7f800000u) return 255u;
+    const int k = (int)(most >> 23) - 127 - top;
+    return (uint32_t)((k < -126 ? -126 : k) + 127);  // k <= 127 - 7
+}
+__device__ __forceinline__ float inverse_scale(uint32_t s) {
+    return s == 255u ? 0.f : __uint_as_float((254u - s) << 23);
+}
+// 20 random bits from 16: the half step keeps the rounding centred.
+__device__ __forceinline__ uint32_t rnd20(uint32_t r16) { return (r16 << 4) + 8u; }
+
+// One CTA's chunk of one tensor.
+template <bool EIGHT, bool VEC>
+__device__ __forceinline__ void chunk_step(const AwTensor& t, uint32_t flags, const AwScalars& s, float gs, int64_t at) {
+    const int64_t left = t.n - at;
+    const int len = left < AW_CHUNK ? (int)left : AW_CHUNK;
+    const bool p16 = flags & AW_P16, g16 = flags & AW_G16;
+    // a warp takes 128 consecutive values (one block of an 8-bit state), a lane four of them
+#pragma unroll 2
+    for (int o = threadIdx.x * 4; o < AW_CHUNK; o += AW_THREADS * 4) {
+        if ((o & ~(AW_BLOCK - 1)) >= len) break;  // the same for the whole warp
+        const int k = min(4, max(0, len - o));
+        const int64_t i = at + o;
+        Four p = p16 ? load4_bf16<VEC>(t.p, i, k) : load4_f32<VEC>(t.p, i, k);
+        Four g = g16 ? load4_bf16<VEC>(t.g, i, k) : load4_f32<VEC>(t.g, i, k);
+        Four m, v;
+        if (EIGHT) {
+            const int64_t b = i / AW_BLOCK;
+            const float ms = scale_value(t.ms[b]), vs = scale_value(t.vs[b]);
+            const uint32_t mc = load4_u8<VEC>(t.m, i, k), vc = load4_u8<VEC>(t.v, i, k);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                m.a[j] = m_value((mc >> (8 * j)) & 0xffu, ms);
+                v.a[j] = v_value((vc >> (8 * j)) & 0xffu, vs);
+            }
+        } else {
+            m = load4_f32<VEC>(t.m, i, k);
+            v = load4_f32<VEC>(t.v, i, k);
+        }
+        uint32_t mm = 0, vm = 0;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            moments(s, __fmul_rn(g.a[j], gs), m.a[j], v.a[j]);
+            p.a[j] = updated(s, p.a[j], m.a[j], v.a[j]);
+            if (EIGHT && j < k) {
+                mm = max(mm, __float_as_uint(m.a[j]) & 0x7fffffffu);
+                vm = max(vm, __float_as_uint(v.a[j]) & 0x7fffffffu);
+            }
+        }
+        if (p16) store4_bf16<VEC>(t.p, i, k, p);
+        else store4_f32<VEC>(t.p, i, k, p);
+        if (t.copy) store4_bf16<VEC>(t.copy, i, k, p);
+        if (EIGHT) {
+            const uint32_t sm = block_scale(__reduce_max_sync(0xffffffffu, mm), M_TOP);
+            const uint32_t sv = block_scale(__reduce_max_sync(0xffffffffu, vm), V_TOP);
+            const float im = inverse_scale(sm), iv = inverse_scale(sv);
+            const uint64_t idx = (uint64_t)(t.base + i);
+            uint32_t mc = 0, vc = 0;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const uint64_t e = idx + j;
+                const uint32_t r = mix32((uint32_t)e ^ s.k0, s.k1 + (uint32_t)(e >> 32) * 0x9E3779B9u);
+                const uint32_t mb = __float_as_uint(__fmul_rn(__fmul_rn(m.a[j], im), 0x1p-120f));
+                const uint32_t vb = __float_as_uint(__fmul_rn(__fmul_rn(v.a[j], iv), 0x1p-112f));
+                const uint32_t cm = (((mb & 0x7fffffffu) + rnd20(r & 0xffffu)) >> 20) | ((mb >> 24) & 0x80u);
+                const uint32_t cv = ((vb & 0x7fffffffu) + rnd20(r >> 16)) >> 20;
+                mc |= (sm == 255u ? 0u : cm & 0xffu) << (8 * j);
+                vc |= (sv == 255u ? 0u : cv & 0xffu) << (8 * j);
+            }
+            store4_u8<VEC>(t.m, i, k, mc);
+            store4_u8<VEC>(t.v, i, k, vc);
+            if ((threadIdx.x & 31) == 0) {
+                const int64_t b = i / AW_BLOCK;
+                t.ms[b] = (uint8_t)sm;
+                t.vs[b] = (uint8_t)sv;
+            }
+        } else {
+            store4_f32<VEC>(t.m, i, k, m);
+            store4_f32<VEC>(t.v, i, k, v);
+        }
+    }
+}
+
+template <int MAXT>
+__device__ __forceinline__ int tensor_of(const AwList<MAXT>& l, int c) {
+    int lo = 0, hi = l.count - 1;  // the last tensor whose first chunk is at or before c
+    while (lo < hi) {
+        const int mid = (lo + hi + 1) >> 1;
+        if (l.first[mid] <= c) lo = mid;
+        else hi = mid - 1;
+    }
+    return lo;
+}
+
+template <bool EIGHT, int MAXT>
+__global__ void __launch_bounds__(AW_THREADS) adamw_kernel(const __grid_constant__ AwList<MAXT> l, const AwScalars s) {
+    griddep_wait();
+    griddep_launch();
+    const float gs = s.grad_scale ? *s.grad_scale : 1.0f;
+    for (int c = blockIdx.x; c < l.first[l.count]; c += gridDim.x) {
+        const int i = tensor_of(l, c);
+        const int64_t at = (int64_t)(c - l.first[i]) * AW_CHUNK;
+        if (l.flags[i] & AW_VEC) chunk_step<EIGHT, true>(l.t[i], l.flags[i], s, gs, at);
+        else chunk_step<EIGHT, false>(l.t[i], l.flags[i], s, gs, at);
+    }
+}
+
+// Values of 8-bit states (AwTensor.p: fp32 m, .copy: fp32 v, each may be null).
+template <int MAXT>
+__global__ void __launch_bounds__(AW_THREADS) adamw_read_kernel(const __grid_constant__ AwList<MAXT> l) {
+    griddep_wait();
+    griddep_launch();
+    for (int c = blockIdx.x; c < l.first[l.count]; c += gridDim.x) {
+        const int ti = tensor_of(l, c);
+        const AwTensor& t = l.t[ti];
+        const int64_t at = (int64_t)(c - l.first[ti]) * AW_CHUNK, left = t.n - at;
+        const int len = left < AW_CHUNK ? (int)left : AW_CHUNK;
+        const bool vec = l.flags[ti] & AW_VEC;
+        for (int o = threadIdx.x * 4; o < len; o += AW_THREADS * 4) {
+            const int k = min(4, len - o);
+            const int64_t i = at + o, b = i / AW_BLOCK;
+            if (t.p) {
+                const float sc = scale_value(t.ms[b]);
+                const uint32_t q = vec ? load4_u8<true>(t.m, i, k) : load4_u8<false>(t.m, i, k);
+                Four r;
+#pragma unroll
+                for (int j = 0; j < 4; ++j) r.a[j] = m_value((q >> (8 * j)) & 0xffu, sc);
+                if (vec) store4_f32<true>(t.p, i, k, r);
+                else store4_f32<false>(t.p, i, k, r);
+            }
+            if (t.copy) {
+                const float sc = scale_value(t.vs[b]);
+                const uint32_t q = vec ? load4_u8<true>(t.v, i, k) : load4_u8<false>(t.v, i, k);
+                Four r;
+#pragma unroll
+                for (int j = 0; j < 4; ++j) r.a[j] = v_value((q >> (8 * j)) & 0xffu, sc);
+                if (vec) store4_f32<true>(t.copy, i, k, r);
+                else store4_f32<false>(t.copy, i, k, r);
+            }
+        }
+    }
+}
+
+// Lists longer than MAXT tensors take several launches; a short list takes the small parameter block.
+constexpr int AW_SMALL = 32, AW_LARGE = 352;
+static_assert(sizeof(AwList<AW_LARGE>) + sizeof(AwScalars) < 32000, "launch parameters");
+
+// Calls run(list, chunks) for each launch's part of the list, made by put(i, &tensor, &flags).
+template <int MAXT, typename Put, typename Run>
+int over_list(int count, Put put, Run run) {
+    AwList<MAXT> l;
+    for (int i = 0; i < count;) {
+        int k = 0;
+        int64_t chunks = 0;
+        for (; i < count && k < MAXT; ++i) {
+            uint8_t f = 0;
+            put(i, &l.t[k], &f);
+            if (l.t[k].n == 0) continue;
+            const int64_t more = (l.t[k].n + AW_CHUNK - 1) / AW_CHUNK;
+            if (chunks + more > INT_MAX) break;
+            l.flags[k] = f;
+            l.first[k++] = (int32_t)chunks;
+            chunks += more;
+        }
+        if (k == 0) {
+            if (i >= count) break;
+            return fail(MOE_ERR_ARG, "tensor %d is too long", i);
+        }
+        l.first[k] = (int32_t)chunks;
+        l.count = k;
+        const int rc = run(l, (int)chunks);
+        if (rc) return rc;
+    }
+    return MOE_OK;
+}
+
+int check_device(DeviceInfo* di) {
+    const int rc = device_info(di);
+    if (rc) return rc;
+    return di->supported ? MOE_OK : fail(MOE_ERR_DEVICE, "current device is not sm_103 (GB300)");
+}
+
+int grid_of(const DeviceInfo& di, int chunks) { return chunks < di.sms * 8 ? chunks : di.sms * 8; }
+
+template <int MAXT>
+int step_list(const moe_adamw_config& c, const moe_adamw_tensor* ts, int count, const AwScalars& s,
+              const DeviceInfo& di, cudaStream_t st) {
+    const bool eight = c.bits == 8;
+    return over_list<MAXT>(
+        count,
+        [&](int i, AwTensor* t, uint8_t* f) {
+            const moe_adamw_tensor& a = ts[i];
+            *t = AwTensor{a.p, a.g, static_cast<__nv_bfloat16*>(a.copy), a.m, a.v, a.m_scale, a.v_scale, a.n, a.rng_base};
+            const size_t sa = eight ? 4 : 16;
+            const bool vec = aligned(a.p, a.p_dtype == MOE_DTYPE_F32 ? 16 : 8) &&
+                             aligned(a.g, a.g_dtype == MOE_DTYPE_F32 ? 16 : 8) && aligned(a.copy, 8) &&
+                             aligned(a.m, sa) && aligned(a.v, sa);
+            *f = (a.p_dtype == MOE_DTYPE_BF16 ? AW_P16 : 0) | (a.g_dtype == MOE_DTYPE_BF16 ? AW_G16 : 0) |
+                 (vec ? AW_VEC : 0);
+        },
+        [&](const AwList<MAXT>& l, int chunks) {
+            const dim3 grid(grid_of(di, chunks)), block(AW_THREADS);
+            const cudaError_t e = eight ? launch_k(adamw_kernel<true, MAXT>, grid, block, 0, st, true, l, s)
+                                        : launch_k(adamw_kernel<false, MAXT>, grid, block, 0, st, true, l, s);
+            return e == cudaSuccess ? MOE_OK : cuda_fail(e, "AdamW kernel launch");
+        });
+}
+
+template <int MAXT>
+int read_list(const moe_adamw_tensor* ts, int count, float* const* mo, float* const* vo, const DeviceInfo& di,
+              cudaStream_t st) {
+    return over_list<MAXT>(
+        count,
+        [&](int i, AwTensor* t, uint8_t* f) {
+            const moe_adamw_tensor& a = ts[i];
+            float *m = mo ? mo[i] : nullptr, *v = vo ? vo[i] : nullptr;
+            *t = AwTensor{m, nullptr, reinterpret_cast<__nv_bfloat16*>(v), a.m, a.v, a.m_scale, a.v_scale,
+                          (m || v) ? a.n : 0, 0};
+            *f = (aligned(m, 16) && aligned(v, 16) && aligned(a.m, 4) && aligned(a.v, 4)) ? AW_VEC : 0;
+        },
+        [&](const AwList<MAXT>& l, int chunks) {
+            const cudaError_t e =
+                launch_k(adamw_read_kernel<MAXT>, dim3(grid_of(di, chunks)), dim3(AW_THREADS), 0, st, true, l);
+            return e == cudaSuccess ? MOE_OK : cuda_fail(e, "AdamW state kernel launch");
+        });
+}
+
+}  // namespace
+}  // namespace moe
+
+using namespace moe;
+
+extern "C" {
+
+MOE_API int moe_adamw_step(const moe_adamw_config* c, const moe_adamw_tensor* ts, int32_t count,
+                           const float* grad_scale, void* stream) {
+    clear_error();
+    if (!c) return fail(MOE_ERR_ARG, "config is NULL");
+    if (c->bits != 32 && c->bits != 8) return fail(MOE_ERR_ARG, "bits=%d must be 32 or 8", c->bits);
+    if (c->step < 1) return fail(MOE_ERR_ARG, "step=%lld must be >= 1", (long long)c->step);
+    if (!(c->beta1 >= 0 && c->beta1 < 1) || !(c->beta2 >= 0 && c->beta2 < 1))
+        return fail(MOE_ERR_ARG, "beta1=%g and beta2=%g must be in [0, 1)", c->beta1, c->beta2);
+    if (!(c->eps >= 0) || !isfinite(c->eps) || !isfinite(c->lr) || !isfinite(c->weight_decay))
+        return fail(MOE_ERR_ARG, "eps=%g must be >= 0, eps, lr=%g and weight_decay=%g finite", c->eps, c->lr,
+                    c->weight_decay);
+    for (int i = 0; i < 3; ++i)
+        if (c->reserved[i]) return fail(MOE_ERR_ARG, "reserved fields must be zero");
+    if (count < 0) return fail(MOE_ERR_ARG, "count=%d must be >= 0", count);
+    if (count && !ts) return fail(MOE_ERR_ARG, "tensors is NULL");
+    if (!aligned(grad_scale, 4)) return fail(MOE_ERR_ARG, "grad_scale must be 4-byte aligned");
+    const bool eight = c->bits == 8;
+    int64_t values = 0;
+    for (int i = 0; i < count; ++i) {
+        const moe_adamw_tensor& t = ts[i];
+        if (t.n < 0) return fail(MOE_ERR_ARG, "tensor %d: n=%lld must be >= 0", i, (long long)t.n);
+        if ((t.p_dtype != MOE_DTYPE_F32 && t.p_dtype != MOE_DTYPE_BF16) ||
+            (t.g_dtype != MOE_DTYPE_F32 && t.g_dtype != MOE_DTYPE_BF16))
+            return fail(MOE_ERR_ARG, "tensor %d: p and g must be fp32 or bf16", i);
+        if (t.n == 0) continue;
+        values += t.n;
+        if (!t.p || !t.g || !t.m || !t.v) return fail(MOE_ERR_ARG, "tensor %d: p, g, m or v is NULL", i);
+        if (eight && (!t.m_scale || !t.v_scale)) return fail(MOE_ERR_ARG, "tensor %d: m_scale or v_scale is NULL", i);
+        if (!aligned(t.p, t.p_dtype == MOE_DTYPE_F32 ? 4 : 2) || !aligned(t.g, t.g_dtype == MOE_DTYPE_F32 ? 4 : 2) ||
+            !aligned(t.copy, 2) || (!eight && (!aligned(t.m, 4) || !aligned(t.v, 4))))
+            return fail(MOE_ERR_ARG, "tensor %d: a pointer is not aligned to its type", i);
+    }
+    if (values == 0) return MOE_OK;
+    DeviceInfo di;
+    const int rc = check_device(&di);
+    if (rc) return rc;
+    AwScalars s;
+    s.b1 = (float)c->beta1;
+    s.b1c = (float)(1.0 - c->beta1);
+    s.b2 = (float)c->beta2;
+    s.b2c = (float)(1.0 - c->beta2);
+    s.decay = (float)(1.0 - c->lr * c->weight_decay);
+    s.step = (float)(c->lr / (1.0 - pow(c->beta1, (double)c->step)));
+    s.vscale = (float)(1.0 / sqrt(1.0 - pow(c->beta2, (double)c->step)));
+    s.eps = (float)c->eps;
+    s.k0 = mix32((uint32_t)c->seed ^ (uint32_t)c->step, (uint32_t)(c->seed >> 32));
+    s.k1 = mix32(s.k0 ^ 0x9E3779B9u, (uint32_t)((uint64_t)c->step >> 32));
+    s.grad_scale = grad_scale;
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    return count <= AW_SMALL ? step_list<AW_SMALL>(*c, ts, count, s, di, st)
+                             : step_list<AW_LARGE>(*c, ts, count, s, di, st);
+}
+
+MOE_API int moe_adamw_read_state(const moe_adamw_tensor* ts, int32_t count, float* const* m_out, float* const* v_out,
+                                 void* stream) {
+    clear_error();
+    if (count < 0) return fail(MOE_ERR_ARG, "count=%d must be >= 0", count);
+    if (count && !ts) return fail(MOE_ERR_ARG, "tensors is NULL");
+    int64_t values = 0;
+    for (int i = 0; i < count; ++i) {
+        const moe_adamw_tensor& t = ts[i];
+        const float *m = m_out ? m_out[i] : nullptr, *v = v_out ? v_out[i] : nullptr;
+        if (t.n < 0) return fail(MOE_ERR_ARG, "tensor %d: n=%lld must be >= 0", i, (long long)t.n);
+        if (t.n == 0 || (!m && !v)) continue;
+        values += t.n;
+        if ((m && (!t.m || !t.m_scale)) || (v && (!t.v || !t.v_scale)))
+            return fail(MOE_ERR_ARG, "tensor %d: a state pointer is NULL", i);
+        if (!aligned(m, 4) || !aligned(v, 4)) return fail(MOE_ERR_ARG, "tensor %d: outputs must be 4-byte aligned", i);
+    }
+    if (values == 0) return MOE_OK;
+    DeviceInfo di;
+    const int rc = check_device(&di);
+    if (rc) return rc;
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    return count <= AW_SMALL ? read_list<AW_SMALL>(ts, count, m_out, v_out, di, st)
+                             : read_list<AW_LARGE>(ts, count, m_out, v_out, di, st);
+}
+
+}  // extern "C"

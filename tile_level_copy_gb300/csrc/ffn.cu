@@ -1,0 +1,678 @@
+// Dense gated feed-forward block: forward and backward pass.
+//
+//   g = x W1^T, u = x W3^T, h = silu(g) * u, y = h W2^T
+//   dh = dy W2, s = 1 / (1 + exp(-g)), dg = dh u s (1 + g (1 - s)), du = dh g s
+//   dx = dg W1 + du W3, dW1 = dg^T x, dW3 = du^T x, dW2 = dy^T h
+//
+// Every product runs in dense_kernel, a persistent tcgen05 GEMM on CTA pairs (UMMA 256 x 256 x 16,
+// cta_group::2, fp32 accumulators in TMEM, operands by TMA through a six-stage ring) that takes a
+// list of products per launch and reads either operand K-major or MN-major, so no transposed copy is
+// ever written: dh, dx read the weights and dW1, dW3, dW2 read both operands along their rows.
+//   launch 1 (forward)   g and u side by side in one accumulator; epilogue: h, and g, u in fp32
+//   launch 2 (forward)   y
+//   launch 3 (backward)  dh; epilogue: dg, du from the kept g, u
+//   launch 4 (backward)  dx (one sum over dg W1 and du W3), dW1, dW3, dW2 as one list of tiles
+// The block is bound by the tensor cores (18 T d ffn flops against 2 (4 T d + 6 d ffn) bytes of
+// tensors). g and u are kept in fp32: rounding them would round dg and du twice, and computing them
+// again costs 4 T d ffn flops where keeping them costs 16 T ffn bytes of traffic (at d = 2048 and the
+// measured rates a quarter of that time, and hidden behind the products).
+// h, dg and du are rounded to bf16 because they are operands of the next product.
+#include "host_internal.h"
+#include "moe_internal.cuh"
+
+namespace moe {
+namespace {
+
+constexpr int FT_M = 256, FT_N = 256;   // tile of a CTA pair
+constexpr int FF_STAGES = 6;
+constexpr int FF_HALF = 128 * BK * 2;   // one CTA's half of an operand's stage: 16 KB
+constexpr int FF_STAGE = 2 * FF_HALF;
+constexpr int FF_MISC = 1024;
+constexpr int FF_SMEM = FF_STAGES * FF_STAGE + EPI_BYTES + FF_MISC + 1024;
+static_assert(FF_SMEM <= 227 * 1024, "dense GEMM shared memory");
+constexpr int FF_PROBLEMS = 4;
+
+enum FfMode : int { FF_PLAIN = 0, FF_SWIGLU = 1, FF_DACT = 2 };
+
+// One product out[M, N] = sum_k A B of a launch.
+struct FfProblem {
+    CUtensorMap a[2], b[2], out[2];  // the sum runs over operand pair 0, then pair 1 (dx)
+    int M, N, kb0, kb;               // k-blocks of 64: of pair 0, of both
+    int tiles_m, tiles_n, tile0;     // first tile of the product in the launch
+    int a_mn, b_mn;                  // operand stored along its M / N dimension
+};
+struct FfLaunch {
+    FfProblem p[FF_PROBLEMS];
+    int count, tiles;
+    float* gu;         // kept g and u (FF_SWIGLU writes, may be null; FF_DACT reads)
+    int gu_cols;       // 32-column blocks of a row of it
+    int32_t* status;   // [2] first error of the calls on a workspace, and where
+    unsigned long long timeout_ns;
+};
+
+struct FfSmem {
+    uint8_t* stages;
+    uint8_t* epi;
+    uint64_t *full, *empty, *acc_full, *acc_empty, *drain;
+    uint32_t *tmem_base, *peer_base;
+    volatile uint32_t* peer_k;
+    volatile int* abort;
+};
+__device__ __forceinline__ FfSmem ff_carve(uint8_t* raw) {
+    FfSmem s;
+    const uint32_t a = smem_u32(raw);
+    uint8_t* base = raw + (((a + 1023u) & ~1023u) - a);
+    s.stages = base;
+    s.epi = base + FF_STAGES * FF_STAGE;
+    s.full = reinterpret_cast<uint64_t*>(s.epi + EPI_BYTES);
+    s.empty = s.full + FF_STAGES;
+    s.acc_full = s.empty + FF_STAGES;
+    s.acc_empty = s.acc_full + 2;
+    s.drain = s.acc_empty + 2;
+    s.tmem_base = reinterpret_cast<uint32_t*>(s.drain + 1);
+    s.peer_base = s.tmem_base + 1;
+    s.peer_k = s.peer_base + 1;
+    s.abort = reinterpret_cast<volatile int*>(s.tmem_base + 3);
+    return s;
+}
+
+__device__ __forceinline__ void ff_status(int32_t* status, int detail) {
+    if (atomicCAS(&status[0], 0, (int)ST_PIPE_TIMEOUT) == 0) atomicExch(&status[1], detail);
+}
+__device__ __forceinline__ void ff_abort(const FfSmem& s, uint32_t rank) {
+    *s.abort = 1;
+    st_cluster_u32(mapa_shared(smem_u32(const_cast<int*>(s.abort)), rank ^ 1u), 1u);
+}
+// Abort path (rank 0, after both CTAs have stopped issuing): rank 0 armed and loaded `a` k-blocks,
+// rank 1 loaded `b`. Bytes that will never come are completed, phases that were never armed are
+// armed, then every stage's last phase is waited for: no load is in flight when the CTAs leave.
+__device__ __forceinline__ void ff_settle(const FfSmem& s, uint32_t a, uint32_t b, unsigned long long tmo) {
+    const uint32_t lo = a < b ? a : b, hi = a < b ? b : a;
+    for (uint32_t i = lo; i < hi; ++i) {
+        uint64_t* bar = &s.full[i % FF_STAGES];
+        if (i < a) mbar_complete_tx(bar, FF_STAGE);
+        else mbar_arrive_expect_tx(bar, FF_STAGE);
+    }
+    int never = 0;
+    for (uint32_t i = hi > (uint32_t)FF_STAGES ? hi - FF_STAGES : 0u; i < hi; ++i)
+        mbar_wait(&s.full[i % FF_STAGES], (i / FF_STAGES) & 1u, tmo, &never);
+}
+
+// Shared-memory descriptor of an operand with the 128-byte swizzle. K-major: rows of 64 k values,
+// eight rows 1024 bytes apart. MN-major: blocks of 64 consecutive m (n) by 64 k, a row of 128
+// bytes per k, eight k 1024 bytes apart (stride offset), the next 64 m (n) 8 KB on (leading offset).
+__device__ __forceinline__ uint64_t ff_sdesc(uint32_t addr, int mn) {
+    uint64_t d = sdesc_sw128(addr);
+    if (mn) d = (d & ~(uint64_t(0x3FFF) << 16)) | (uint64_t((64 * BK * 2) >> 4) << 16);
+    return d;
+}
+// One operand half (128 rows of M or N from `row`, k-block at `k`) into `dst`.
+template <bool PEER>
+__device__ __forceinline__ void ff_load(uint8_t* dst, const CUtensorMap* m, uint64_t* bar, uint32_t bar0, int mn,
+                                        int row, int k) {
+    if (!mn) {
+        if (PEER) tma_load_2d_pair(dst, m, bar0, k, row);
+        else tma_load_2d(dst, m, bar, k, row);
+        return;
+    }
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        if (PEER) tma_load_2d_pair(dst + i * (FF_HALF / 2), m, bar0, row + 64 * i, k);
+        else tma_load_2d(dst + i * (FF_HALF / 2), m, bar, row + 64 * i, k);
+    }
+}
+
+struct FfTile {
+    const FfProblem* p;
+    int m, n;
+};
+__device__ __forceinline__ FfTile ff_tile(const FfLaunch& l, int t) {
+    int i = 0;
+    while (i + 1 < l.count && t >= l.p[i + 1].tile0) ++i;
+    const FfProblem* p = &l.p[i];
+    const int q = t - p->tile0;
+    // M tiles in groups of 16, N tiles outer in a group: tiles that run together share operands in L2
+    const int per = 16 * p->tiles_n, grp = q / per, first = grp * 16;
+    const int rows = min(16, p->tiles_m - first), r = q - grp * per;
+    return FfTile{p, first + r % rows, r / rows};
+}
+
+// One epilogue warp's two staging chunks (32 rows x 32 columns of bf16), stored by TMA.
+struct FfStage {
+    uint8_t* buf;
+    int eb;
+    __device__ __forceinline__ void put(const CUtensorMap* tm, const uint32_t (&pk)[16], int x, int y, int lane) {
+        if (lane == 0) bulk_wait_read_1();
+        __syncwarp();
+        uint4* dst = reinterpret_cast<uint4*>(buf + eb * EPI_CHUNK_BYTES + lane * (EPI_CHUNK * 2));
+        const uint4 u[4] = {make_uint4(pk[0], pk[1], pk[2], pk[3]), make_uint4(pk[4], pk[5], pk[6], pk[7]),
+                            make_uint4(pk[8], pk[9], pk[10], pk[11]), make_uint4(pk[12], pk[13], pk[14], pk[15])};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {  // lane-rotated order: no bank conflicts
+            const int pi = (i + lane) & 3;
+            dst[pi] = pi == 0 ? u[0] : pi == 1 ? u[1] : pi == 2 ? u[2] : u[3];
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) {
+            tma_store_2d(tm, buf + eb * EPI_CHUNK_BYTES, x, y);
+            bulk_commit();
+        }
+        eb ^= 1;
+    }
+};
+
+__device__ __forceinline__ float ff_sigmoid(float g) { return __fdividef(1.0f, 1.0f + __expf(-g)); }
+
+// Kept g and u of a 32 x 32 block: [8 pieces of 4 columns][32 rows][4] fp32, g then u, so that a
+// warp whose lanes hold rows reads and writes 512 contiguous bytes at a time.
+__device__ __forceinline__ float4* ff_gu(const FfLaunch& l, int row0, int col0, int which, int lane) {
+    const size_t block = (size_t)(row0 >> 5) * l.gu_cols + (col0 >> 5);
+    return reinterpret_cast<float4*>(l.gu + (block * 2 + which) * 1024) + lane;
+}
+
+template <int MODE>
+__device__ __forceinline__ void ff_epilogue(const FfLaunch& l, const FfTile& t, FfStage& es, uint32_t tb, int row0,
+                                            int lane) {
+    const FfProblem& p = *t.p;
+    if (row0 >= p.M) return;
+    if (MODE == FF_SWIGLU) {
+#pragma unroll 1
+        for (int c = 0; c < 4; ++c) {
+            const int col0 = t.n * 128 + c * 32;
+            if (col0 >= p.N) return;
+            uint32_t g[32], u[32];
+            tmem_ld32(tb + c * 32, g);
+            tmem_ld32(tb + 128 + c * 32, u);
+            uint32_t pk[16];
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+                const float g0 = __uint_as_float(g[2 * i]), g1 = __uint_as_float(g[2 * i + 1]);
+                pk[i] = pack_bf16x2(g0 * ff_sigmoid(g0) * __uint_as_float(u[2 * i]),
+                                    g1 * ff_sigmoid(g1) * __uint_as_float(u[2 * i + 1]));
+            }
+            if (l.gu) {
+                float4 *og = ff_gu(l, row0, col0, 0, lane), *ou = ff_gu(l, row0, col0, 1, lane);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    og[i * 32] = make_float4(__uint_as_float(g[4 * i]), __uint_as_float(g[4 * i + 1]),
+                                             __uint_as_float(g[4 * i + 2]), __uint_as_float(g[4 * i + 3]));
+                    ou[i * 32] = make_float4(__uint_as_float(u[4 * i]), __uint_as_float(u[4 * i + 1]),
+                                             __uint_as_float(u[4 * i + 2]), __uint_as_float(u[4 * i + 3]));
+                }
+            }
+            es.put(&p.out[0], pk, col0, row0, lane);
+        }
+    } else if (MODE == FF_DACT) {
+#pragma unroll 1
+        for (int c = 0; c < 8; ++c) {
+            const int col0 = t.n * FT_N + c * 32;
+            if (col0 >= p.N) return;
+            const float4 *ig = ff_gu(l, row0, col0, 0, lane), *iu = ff_gu(l, row0, col0, 1, lane);
+            float4 g[8], u[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                g[i] = ig[i * 32];
+                u[i] = iu[i * 32];
+            }
+            uint32_t d[32];
+            tmem_ld32(tb + c * 32, d);
+            uint32_t pg[16], pu[16];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const float gv[4] = {g[i].x, g[i].y, g[i].z, g[i].w}, uv[4] = {u[i].x, u[i].y, u[i].z, u[i].w};
+                float dg[4], du[4];
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const float dh = __uint_as_float(d[4 * i + j]), s = ff_sigmoid(gv[j]);
+                    du[j] = dh * (gv[j] * s);
+                    dg[j] = dh * uv[j] * (s * (1.0f + gv[j] * (1.0f - s)));
+                }
+                pg[2 * i] = pack_bf16x2(dg[0], dg[1]);
+                pg[2 * i + 1] = pack_bf16x2(dg[2], dg[3]);
+                pu[2 * i] = pack_bf16x2(du[0], du[1]);
+                pu[2 * i + 1] = pack_bf16x2(du[2], du[3]);
+            }
+            es.put(&p.out[0], pg, col0, row0, lane);
+            es.put(&p.out[1], pu, col0, row0, lane);
+        }
+    } else {
+#pragma unroll 1
+        for (int c = 0; c < 8; ++c) {
+            const int col0 = t.n * FT_N + c * 32;
+            if (col0 >= p.N) return;
+            uint32_t v[32], pk[16];
+            tmem_ld32(tb + c * 32, v);
+#pragma unroll
+            for (int i = 0; i < 16; ++i) pk[i] = pack_bf16x2(__uint_as_float(v[2 * i]), __uint_as_float(v[2 * i + 1]));
+            es.put(&p.out[0], pk, col0, row0, lane);
+        }
+    }
+}
+
+// Persistent GEMM on CTA pairs: cluster c takes tiles c, c + clusters, ... of the launch's list.
+// Warp 0: TMA loads (each CTA its 128 rows of A and 128 of B; both CTAs' loads complete on rank 0's
+// stage barrier). Warp 1: TMEM, and on rank 0 the UMMAs. Warps 2-5: epilogue of the CTA's 128 rows,
+// overlapping the next tile's products through two accumulators. Every wait is bounded; one that
+// runs out raises the pair's abort word and the status word, and the loads in flight are settled.
+template <int MODE>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(GEMM_THREADS, 1)
+    dense_kernel(const __grid_constant__ FfLaunch l) {
+    extern __shared__ uint8_t smem_raw[];
+    const FfSmem sm = ff_carve(smem_raw);
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const uint32_t rank = cluster_ctarank();
+    const int cluster = blockIdx.x >> 1, clusters = gridDim.x >> 1;
+    const unsigned long long tmo = l.timeout_ns;
+    if (tid == 0) {
+        for (int i = 0; i < FF_STAGES; ++i) {
+            mbar_init(&sm.full[i], 1);
+            mbar_init(&sm.empty[i], 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&sm.acc_full[i], 1);
+            mbar_init(&sm.acc_empty[i], 8);
+        }
+        mbar_init(sm.drain, 1);
+        *sm.abort = 0;
+        mbar_fence_init();
+    }
+    __syncthreads();
+    if (warp == 1) {
+        tmem_alloc_pair(sm.tmem_base, TMEM_COLS);
+        tmem_relinquish_pair();
+    }
+    tc_fence_before();
+    __syncthreads();
+    cluster_sync();
+    tc_fence_after();
+    if (rank == 1 && tid == 0) st_cluster_u32(mapa_shared(smem_u32(sm.peer_base), 0u), *sm.tmem_base);
+    cluster_sync();
+    griddep_wait();
+    griddep_launch();
+    const uint32_t tmem = *sm.tmem_base;
+    const bool bad = rank == 0 && *sm.peer_base != tmem;
+    uint32_t nk = 0;
+
+    if (warp == 0 && lane == 0) {
+        int st = 0;
+        uint32_t ph = 0;
+        bool ok = !bad;
+        for (int t = cluster; ok && t < l.tiles; t += clusters) {
+            const FfTile tr = ff_tile(l, t);
+            const FfProblem& p = *tr.p;
+            const int arow = tr.m * FT_M + (int)rank * 128;
+            const int brow = MODE == FF_SWIGLU ? tr.n * 128 : tr.n * FT_N + (int)rank * 128;
+            for (int kb = 0; kb < p.kb; ++kb) {
+                if (!mbar_wait(&sm.empty[st], ph ^ 1u, tmo, sm.abort)) {
+                    ok = false;
+                    break;
+                }
+                uint8_t* a = sm.stages + st * FF_STAGE;
+                uint8_t* b = a + FF_HALF;
+                const int second = kb >= p.kb0 ? 1 : 0, k = (kb - (second ? p.kb0 : 0)) * BK;
+                const CUtensorMap* ma = &p.a[second];
+                const CUtensorMap* mb = &p.b[MODE == FF_SWIGLU ? (int)rank : second];
+                if (rank == 0) {
+                    mbar_arrive_expect_tx(&sm.full[st], 2 * FF_STAGE);
+                    ff_load<false>(a, ma, &sm.full[st], 0u, p.a_mn, arow, k);
+                    ff_load<false>(b, mb, &sm.full[st], 0u, p.b_mn, brow, k);
+                } else {
+                    const uint32_t full0 = mapa_shared(smem_u32(&sm.full[st]), 0u);
+                    ff_load<true>(a, ma, nullptr, full0, p.a_mn, arow, k);
+                    ff_load<true>(b, mb, nullptr, full0, p.b_mn, brow, k);
+                }
+                ++nk;
+                if (++st == FF_STAGES) {
+                    st = 0;
+                    ph ^= 1u;
+                }
+            }
+        }
+        if (!ok) {
+            if (!*sm.abort) ff_status(l.status, 10 + (int)rank);
+            ff_abort(sm, rank);
+        }
+    } else if (warp == 1 && lane == 0) {
+        bool ok = !bad;
+        if (bad) {
+            ff_status(l.status, 9);
+            ff_abort(sm, rank);
+        }
+        if (rank == 0) {
+            int st = 0, b = 0;
+            uint32_t ph = 0, aph = 0;
+            for (int t = cluster; ok && t < l.tiles; t += clusters) {
+                const FfProblem& p = *ff_tile(l, t).p;
+                const uint32_t idesc = umma_idesc_bf16(FT_M, FT_N) | ((uint32_t)p.a_mn << 15) | ((uint32_t)p.b_mn << 16);
+                const uint32_t astep = p.a_mn ? 128 : 2, bstep = p.b_mn ? 128 : 2;  // 16 k, in 16 bytes
+                if (!mbar_wait_cluster(&sm.acc_empty[b], aph ^ 1u, tmo, sm.abort)) {
+                    ok = false;
+                    break;
+                }
+                tc_fence_after();
+                const uint32_t dt = tmem + (uint32_t)(b * 256);
+                for (int kb = 0; kb < p.kb; ++kb) {
+                    if (!mbar_wait_cluster(&sm.full[st], ph, tmo, sm.abort)) {
+                        ok = false;
+                        break;
+                    }
+                    tc_fence_after();
+                    const uint32_t addr = smem_u32(sm.stages + st * FF_STAGE);
+                    const uint64_t ad = ff_sdesc(addr, p.a_mn), bd = ff_sdesc(addr + FF_HALF, p.b_mn);
+#pragma unroll
+                    for (int kk = 0; kk < BK / 16; ++kk)
+                        umma_bf16_pair(dt, ad + astep * kk, bd + bstep * kk, idesc, (kb | kk) != 0);
+                    umma_commit_pair(&sm.empty[st], 0x3);
+                    if (++st == FF_STAGES) {
+                        st = 0;
+                        ph ^= 1u;
+                    }
+                }
+                if (!ok) break;
+                umma_commit_pair(&sm.acc_full[b], 0x3);
+                b ^= 1;
+                if (b == 0) aph ^= 1u;
+            }
+            umma_commit_pair(sm.drain, 0x3);  // fires when every UMMA issued has completed
+        }
+        if (!ok) {
+            if (!*sm.abort) ff_status(l.status, 12 + (int)rank);
+            ff_abort(sm, rank);
+        }
+        int never = 0;
+        if (!mbar_wait(sm.drain, 0, tmo, &never) && !*sm.abort) ff_status(l.status, 14 + (int)rank);
+    } else if (warp >= 2) {
+        const int q = warp & 3;
+        FfStage es{sm.epi + (warp - 2) * 2 * EPI_CHUNK_BYTES, 0};
+        const uint32_t acc_empty0 = mapa_shared(smem_u32(sm.acc_empty), 0u);
+        int b = 0;
+        uint32_t aph = 0;
+        for (int t = cluster; !bad && t < l.tiles; t += clusters) {
+            const FfTile tr = ff_tile(l, t);
+            if (!mbar_wait(&sm.acc_full[b], aph, tmo, sm.abort)) {
+                if (!*sm.abort) ff_status(l.status, 16 + (int)rank);
+                if (lane == 0) ff_abort(sm, rank);
+                break;
+            }
+            tc_fence_after();
+            __syncwarp();
+            const uint32_t tb = tmem + ((uint32_t)(q * 32) << 16) + (uint32_t)(b * 256);
+            ff_epilogue<MODE>(l, tr, es, tb, tr.m * FT_M + (int)rank * 128 + q * 32, lane);
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive_cluster(acc_empty0 + b * 8u);
+            b ^= 1;
+            if (b == 0) aph ^= 1u;
+        }
+        if (lane == 0) bulk_wait_all();
+        __syncwarp();
+    }
+    __syncwarp();
+    tc_fence_before();
+    cluster_sync();  // both CTAs: all roles done, all UMMAs complete, every abort word written
+    if (*sm.abort) {
+        if (tid == 0 && rank == 1) st_cluster_u32(mapa_shared(smem_u32(const_cast<uint32_t*>(sm.peer_k)), 0u), nk);
+        cluster_sync();
+        if (tid == 0 && rank == 0) ff_settle(sm, nk, *sm.peer_k, tmo);
+        cluster_sync();
+    }
+    if (warp == 1) {
+        __syncwarp();
+        tc_fence_after();
+        tmem_dealloc_pair(tmem, TMEM_COLS);
+    }
+    __syncwarp();
+    cluster_sync();
+}
+
+// ---- host side -----------------------------------------------------------------------------------
+
+struct FfLayout {
+    size_t T, d, F;
+    size_t h, dg, du, ws_bytes;        // workspace: status words, then h (or dg), du
+    size_t saved_h, saved_gu, saved_bytes;
+    int gu_cols;
+    unsigned long long timeout_ns;
+};
+
+int ff_layout(const moe_ffn_config* c, FfLayout* o) {
+    if (!c) return fail(MOE_ERR_ARG, "config is NULL");
+    if (c->T < 0 || c->T >= (1 << 24)) return fail(MOE_ERR_ARG, "T=%d must be in [0, 2^24)", c->T);
+    if (c->d <= 0 || c->d % 8 || c->d >= (1 << 20))
+        return fail(MOE_ERR_ARG, "d=%d must be a positive multiple of 8 below 2^20", c->d);
+    if (c->ffn <= 0 || c->ffn % 8 || c->ffn >= (1 << 20))
+        return fail(MOE_ERR_ARG, "ffn=%d must be a positive multiple of 8 below 2^20", c->ffn);
+    for (int i = 0; i < 4; ++i)
+        if (c->reserved[i]) return fail(MOE_ERR_ARG, "reserved fields must be zero");
+    FfLayout L;
+    L.T = c->T;
+    L.d = c->d;
+    L.F = c->ffn;
+    const size_t hidden = align_up(L.T * L.F * 2, 1024);
+    L.h = L.dg = 1024;
+    L.du = L.dg + hidden;
+    L.ws_bytes = L.du + hidden;
+    L.gu_cols = (int)((L.F + 31) / 32);
+    L.saved_h = 0;
+    L.saved_gu = hidden;
+    L.saved_bytes = hidden + (L.T + 31) / 32 * L.gu_cols * 8192;
+    L.timeout_ns = (unsigned long long)(c->timeout_us ? c->timeout_us : 2000000u) * 1000ull;
+    *o = L;
+    return MOE_OK;
+}
+
+// bf16 matrix [rows][inner]; operand boxes are 64 inner values by `box` rows with the 128-byte
+// swizzle, output boxes 32 x 32 without. Out-of-bounds elements read as zero and are not stored.
+int ff_map(CUtensorMap* m, const void* ptr, uint64_t rows, uint64_t inner, uint32_t box, bool out) {
+    EncodeTiledFn fn = encode_fn();
+    if (!fn) return fail(MOE_ERR_CUDA, "cuTensorMapEncodeTiled is not available from the driver");
+    const cuuint64_t dims[2] = {inner, rows}, strides[1] = {inner * 2};
+    const cuuint32_t bx[2] = {out ? (cuuint32_t)EPI_CHUNK : (cuuint32_t)BK, box}, es[2] = {1, 1};
+    const CUresult r = fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(ptr), dims, strides, bx, es,
+                          CU_TENSOR_MAP_INTERLEAVE_NONE, out ? CU_TENSOR_MAP_SWIZZLE_NONE : CU_TENSOR_MAP_SWIZZLE_128B,
+                          CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    return r == CUDA_SUCCESS ? MOE_OK : fail(MOE_ERR_CUDA, "cuTensorMapEncodeTiled failed: %d", (int)r);
+}
+
+// Operand [mn, k] (K-major) or, with mn set, stored as [k, mn]; its TMA map.
+int ff_operand(CUtensorMap* m, const void* ptr, uint64_t mn, uint64_t k, int along_mn) {
+    return along_mn ? ff_map(m, ptr, k, mn, BK, false) : ff_map(m, ptr, mn, k, 128, false);
+}
+
+struct FfList {
+    FfLaunch l;
+    int rc = MOE_OK;
+    FfList() {
+        l.count = l.tiles = 0;
+        l.gu = nullptr;
+        l.gu_cols = 0;
+    }
+    // Adds out[M, N] = A[M, K] B[N, K]^T; a2, b2: a second pair of operands of the same shapes.
+    FfProblem& add(const void* a, int a_mn, const void* b, int b_mn, void* out, size_t M, size_t N, size_t K,
+                   const void* a2 = nullptr, const void* b2 = nullptr) {
+        FfProblem& p = l.p[l.count++];
+        p.M = (int)M;
+        p.N = (int)N;
+        p.kb0 = (int)((K + BK - 1) / BK);
+        p.kb = a2 ? 2 * p.kb0 : p.kb0;
+        p.a_mn = a_mn;
+        p.b_mn = b_mn;
+        p.tiles_m = (int)((M + FT_M - 1) / FT_M);
+        p.tiles_n = (int)((N + FT_N - 1) / FT_N);
+        p.tile0 = l.tiles;
+        l.tiles += p.tiles_m * p.tiles_n;
+        try_(ff_operand(&p.a[0], a, M, K, a_mn));
+        try_(ff_operand(&p.b[0], b, N, K, b_mn));
+        try_(ff_operand(&p.a[1], a2 ? a2 : a, M, K, a_mn));
+        try_(ff_operand(&p.b[1], b2 ? b2 : b, N, K, b_mn));
+        try_(ff_map(&p.out[0], out, M, N, EPI_CHUNK, true));
+        p.out[1] = p.out[0];
+        return p;
+    }
+    void try_(int r) {
+        if (rc == MOE_OK) rc = r;
+    }
+};
+
+// Co-resident CTA pairs of a kernel on the current device (cached per device).
+template <int MODE>
+cudaError_t ff_clusters(int* out) {
+    const void* fn = reinterpret_cast<const void*>(&dense_kernel<MODE>);
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+    static int cache[64] = {0};
+    if (cache[dev] == 0) {
+        e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, FF_SMEM);
+        if (e != cudaSuccess) return e;
+        cudaLaunchConfig_t q = {};
+        q.gridDim = dim3(2, 1, 1);
+        q.blockDim = dim3(GEMM_THREADS, 1, 1);
+        q.dynamicSmemBytes = FF_SMEM;
+        int n = 0;
+        e = cudaOccupancyMaxActiveClusters(&n, fn, &q);
+        if (e != cudaSuccess) return e;
+        if (n < 1) return cudaErrorInvalidConfiguration;
+        cache[dev] = n;
+    }
+    *out = cache[dev];
+    return cudaSuccess;
+}
+
+template <int MODE>
+int ff_run(FfList& list, const FfLayout& L, void* ws, cudaStream_t st, const char* what) {
+    if (list.rc) return list.rc;
+    list.l.status = static_cast<int32_t*>(ws);
+    list.l.timeout_ns = L.timeout_ns;
+    int clusters = 0;
+    cudaError_t e = ff_clusters<MODE>(&clusters);
+    if (e == cudaSuccess) {
+        const int n = list.l.tiles < clusters ? list.l.tiles : clusters;
+        e = launch_k(dense_kernel<MODE>, dim3(2 * n), dim3(GEMM_THREADS), FF_SMEM, st, true, list.l);
+    }
+    return e == cudaSuccess ? MOE_OK : cuda_fail(e, what);
+}
+
+int ff_begin(const moe_ffn_config* c, void* ws, size_t ws_bytes, FfLayout* L) {
+    clear_error();
+    int rc = ff_layout(c, L);
+    if (rc) return rc;
+    if (!ws) return fail(MOE_ERR_ARG, "workspace is NULL");
+    if (!aligned(ws, 256)) return fail(MOE_ERR_ARG, "workspace must be 256-byte aligned");
+    if (ws_bytes < L->ws_bytes) return fail(MOE_ERR_WORKSPACE, "workspace has %zu bytes, needs %zu", ws_bytes, L->ws_bytes);
+    DeviceInfo di;
+    if ((rc = device_info(&di))) return rc;
+    return di.supported ? MOE_OK : fail(MOE_ERR_DEVICE, "current device is not sm_103 (GB300)");
+}
+
+}  // namespace
+}  // namespace moe
+
+using namespace moe;
+
+extern "C" {
+
+MOE_API int moe_ffn_workspace_size(const moe_ffn_config* c, size_t* bytes) {
+    clear_error();
+    FfLayout L;
+    const int rc = ff_layout(c, &L);
+    if (rc) return rc;
+    if (!bytes) return fail(MOE_ERR_ARG, "bytes is NULL");
+    *bytes = L.ws_bytes;
+    return MOE_OK;
+}
+
+MOE_API int moe_ffn_saved_size(const moe_ffn_config* c, size_t* bytes) {
+    clear_error();
+    FfLayout L;
+    const int rc = ff_layout(c, &L);
+    if (rc) return rc;
+    if (!bytes) return fail(MOE_ERR_ARG, "bytes is NULL");
+    *bytes = L.saved_bytes;
+    return MOE_OK;
+}
+
+MOE_API int moe_ffn_forward(const moe_ffn_config* c, const uint16_t* x, const uint16_t* W1, const uint16_t* W3,
+                            const uint16_t* W2, uint16_t* y, void* saved, void* ws, size_t ws_bytes, void* stream) {
+    FfLayout L;
+    int rc = ff_begin(c, ws, ws_bytes, &L);
+    if (rc) return rc;
+    if (L.T == 0) return MOE_OK;
+    if (!x || !W1 || !W3 || !W2 || !y) return fail(MOE_ERR_ARG, "NULL input or output pointer");
+    if (!aligned(x, 16) || !aligned(W1, 16) || !aligned(W3, 16) || !aligned(W2, 16) || !aligned(y, 16))
+        return fail(MOE_ERR_ARG, "x, W1, W3, W2, y must be 16-byte aligned");
+    if (!aligned(saved, 256)) return fail(MOE_ERR_ARG, "saved must be 256-byte aligned");
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    uint8_t* s = static_cast<uint8_t*>(saved);
+    uint8_t* h = s ? s + L.saved_h : static_cast<uint8_t*>(ws) + L.h;
+    FfList up;
+    FfProblem& p = up.add(x, 0, W1, 0, h, L.T, L.F, L.d);
+    up.try_(ff_operand(&p.b[1], W3, L.F, L.d, 0));
+    p.tiles_n = (int)((L.F + 127) / 128);  // 128 columns of g beside 128 of u
+    up.l.tiles = p.tiles_m * p.tiles_n;
+    up.l.gu = s ? reinterpret_cast<float*>(s + L.saved_gu) : nullptr;
+    up.l.gu_cols = L.gu_cols;
+    if ((rc = ff_run<FF_SWIGLU>(up, L, ws, st, "gate and up projections"))) return rc;
+    FfList down;
+    down.add(h, 0, W2, 0, y, L.T, L.d, L.F);
+    return ff_run<FF_PLAIN>(down, L, ws, st, "down projection");
+}
+
+MOE_API int moe_ffn_backward(const moe_ffn_config* c, const uint16_t* x, const uint16_t* W1, const uint16_t* W3,
+                             const uint16_t* W2, const uint16_t* dy, const void* saved, uint16_t* dx, uint16_t* dW1,
+                             uint16_t* dW3, uint16_t* dW2, void* ws, size_t ws_bytes, void* stream) {
+    FfLayout L;
+    int rc = ff_begin(c, ws, ws_bytes, &L);
+    if (rc) return rc;
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    if (!dW1 || !dW3 || !dW2) return fail(MOE_ERR_ARG, "NULL weight gradient pointer");
+    if (!aligned(dW1, 16) || !aligned(dW3, 16) || !aligned(dW2, 16))
+        return fail(MOE_ERR_ARG, "dW1, dW3, dW2 must be 16-byte aligned");
+    if (L.T == 0) {
+        cudaError_t e = cudaMemsetAsync(dW1, 0, L.F * L.d * 2, st);
+        if (e == cudaSuccess) e = cudaMemsetAsync(dW3, 0, L.F * L.d * 2, st);
+        if (e == cudaSuccess) e = cudaMemsetAsync(dW2, 0, L.F * L.d * 2, st);
+        return e == cudaSuccess ? MOE_OK : cuda_fail(e, "clearing the weight gradients");
+    }
+    if (!x || !W1 || !W3 || !W2 || !dy || !saved || !dx) return fail(MOE_ERR_ARG, "NULL input or output pointer");
+    if (!aligned(x, 16) || !aligned(W1, 16) || !aligned(W3, 16) || !aligned(W2, 16) || !aligned(dy, 16) ||
+        !aligned(dx, 16))
+        return fail(MOE_ERR_ARG, "x, W1, W3, W2, dy, dx must be 16-byte aligned");
+    if (!aligned(saved, 256)) return fail(MOE_ERR_ARG, "saved must be 256-byte aligned");
+    const uint8_t* s = static_cast<const uint8_t*>(saved);
+    const uint8_t* h = s + L.saved_h;
+    uint8_t* dg = static_cast<uint8_t*>(ws) + L.dg;
+    uint8_t* du = static_cast<uint8_t*>(ws) + L.du;
+    FfList act;
+    FfProblem& p = act.add(dy, 0, W2, 1, dg, L.T, L.F, L.d);
+    act.try_(ff_map(&p.out[1], du, L.T, L.F, EPI_CHUNK, true));
+    act.l.gu = reinterpret_cast<float*>(const_cast<uint8_t*>(s) + L.saved_gu);
+    act.l.gu_cols = L.gu_cols;
+    if ((rc = ff_run<FF_DACT>(act, L, ws, st, "hidden gradients"))) return rc;
+    FfList grad;
+    grad.add(dg, 0, W1, 1, dx, L.T, L.d, L.F, du, W3);
+    grad.add(dg, 1, x, 1, dW1, L.F, L.d, L.T);
+    grad.add(du, 1, x, 1, dW3, L.F, L.d, L.T);
+    grad.add(dy, 1, h, 1, dW2, L.d, L.F, L.T);
+    return ff_run<FF_PLAIN>(grad, L, ws, st, "input and weight gradients");
+}
+
+MOE_API int moe_ffn_status(const moe_ffn_config* c, const void* ws, void* stream, int32_t* detail) {
+    clear_error();
+    FfLayout L;
+    const int rc = ff_layout(c, &L);
+    if (rc) return rc;
+    if (!ws) return fail(MOE_ERR_ARG, "workspace is NULL");
+    cudaError_t e = cudaStreamSynchronize(static_cast<cudaStream_t>(stream));
+    if (e != cudaSuccess) return cuda_fail(e, "stream synchronize");
+    int32_t w[2] = {0, 0};
+    e = cudaMemcpy(w, ws, sizeof(w), cudaMemcpyDeviceToHost);
+    if (e != cudaSuccess) return cuda_fail(e, "status read");
+    if (detail) *detail = w[1];
+    if (w[0] == ST_OK) return MOE_OK;
+    return fail(MOE_ERR_TIMEOUT, "a bounded wait of the feed-forward block ran out (status %d, detail %d)", w[0], w[1]);
+}
+
+}  // extern "C"

@@ -8,14 +8,15 @@
 #include <string>
 #include <vector>
 
+#include "host_internal.h"
 #include "moe_internal.cuh"
 
 namespace moe {
-namespace {
 
-thread_local std::string g_err;
+static thread_local std::string g_err;
 
-int fail(int code, const char* fmt, ...) __attribute__((format(printf, 2, 3)));
+void clear_error() { g_err.clear(); }
+
 int fail(int code, const char* fmt, ...) {
     char buf[512];
     va_list ap;
@@ -30,7 +31,7 @@ int cuda_fail(cudaError_t e, const char* what) {
     return fail(MOE_ERR_CUDA, "%s: %s (%s)", what, cudaGetErrorName(e), cudaGetErrorString(e));
 }
 
-size_t align_up(size_t v, size_t a) { return (v + a - 1) / a * a; }
+namespace {
 
 struct Layout {
     moe_layout L;
@@ -208,12 +209,9 @@ PlanPtrs plan_ptrs(const moe_layout& L, void* ws) {
     return p;
 }
 
-// ---- device query ------------------------------------------------------------------------------
-struct DeviceInfo {
-    int sms = 0;
-    bool supported = false;
-};
+}  // namespace
 
+// ---- device query ------------------------------------------------------------------------------
 int device_info(DeviceInfo* di) {
     int dev = 0, major = 0, minor = 0, sms = 0;
     cudaError_t e = cudaGetDevice(&dev);
@@ -227,10 +225,6 @@ int device_info(DeviceInfo* di) {
 }
 
 // ---- TMA descriptors ---------------------------------------------------------------------------
-typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
-                                  const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
-                                  CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-
 EncodeTiledFn encode_fn() {
     static EncodeTiledFn fn = nullptr;
     static std::once_flag once;
@@ -244,6 +238,8 @@ EncodeTiledFn encode_fn() {
     });
     return fn;
 }
+
+namespace {
 
 // bf16 tensor [outer][mid][inner] (rank 3) or [mid][inner] (rank 2, outer = 1); box box_inner x
 // box_mid (x 1). Operand maps: 64-element inner box with the 128-byte swizzle the UMMA descriptors
@@ -264,8 +260,6 @@ int make_map(CUtensorMap* m, const void* ptr, int rank, uint64_t inner, uint64_t
     if (r != CUDA_SUCCESS) return fail(MOE_ERR_CUDA, "cuTensorMapEncodeTiled(%s) failed: %d", what, (int)r);
     return MOE_OK;
 }
-
-bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
 
 struct Call {
     Layout lay;
