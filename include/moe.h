@@ -495,7 +495,7 @@ MOE_API int moe_layernorm_forward(const moe_layernorm_config* cfg, const void* x
 MOE_API int moe_layernorm_workspace_size(const moe_layernorm_config* cfg, size_t* bytes);
 
 /* dx, and dw = sum over rows of dy * (x - mean) * rstd, db = sum of dy: summed in an order that
- * depends on the config and the device alone, so results repeat bit for bit. w may be NULL; dw and db may be NULL
+ * depends on the config, the pointers' alignment and the device alone, so results repeat bit for bit. w may be NULL; dw and db may be NULL
  * (then ws may be NULL too). dx may be dy. */
 MOE_API int moe_layernorm_backward(const moe_layernorm_config* cfg, const void* dy, const void* x, const void* w,
                                    const float* mean, const float* rstd, void* dx, void* dw, void* db, void* ws,

@@ -389,13 +389,59 @@ def device_info():
 # ---- operators of a training and serving block around the layer -----------------------------------
 
 
-def _shape(t: Optional[torch.Tensor], shape, name: str) -> None:
-    if t is not None and tuple(t.shape) != tuple(shape):
+# The checks below are written for the calls of a decoding step, where a microsecond counts: one test of
+# everything that is right, and the search for what is wrong only after it has failed.
+
+
+def _dev(t: Optional[torch.Tensor], dtype, shape, name: str):
+    """Device pointer of a contiguous tensor of this type and shape (None: NULL)."""
+    if t is None:
+        return None
+    if t.dtype is dtype and t.is_cuda and t.shape == shape and t.is_contiguous():
+        return t.data_ptr()
+    if t.shape != shape:
         raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    return _ptr(t, dtype, "cuda", name)
+
+
+def _flat(t: Optional[torch.Tensor], dtype, n: int, name: str):
+    """The same for a tensor of n values of any shape."""
+    if t is None:
+        return None
+    if t.dtype is dtype and t.is_cuda and t.numel() == n and t.is_contiguous():
+        return t.data_ptr()
+    if t.numel() != n:
+        raise ValueError(f"{name} must hold {n} values, got {t.numel()}")
+    return _ptr(t, dtype, "cuda", name)
+
+
+def _raw_stream(stream, t: torch.Tensor):
+    """Raw stream handle; the default is the current stream of t's device."""
+    if stream is None:
+        return torch._C._cuda_getCurrentRawStream(t.get_device())
+    return _stream(stream)
+
+
+class _Marshalled:
+    """A config that keeps its C form, and a pointer to it, until one of its fields is set."""
+
+    def __setattr__(self, name, value):
+        object.__setattr__(self, name, value)
+        object.__setattr__(self, "_kept", None)
+
+    def ref(self):
+        """Pointer to the C form (and whatever sizes the config's class keeps beside it)."""
+        if self._kept is None:
+            object.__setattr__(self, "_kept", self._make())
+        return self._kept
+
+    def _make(self):
+        c = self.to_c()
+        return (ctypes.byref(c), c)
 
 
 @dataclasses.dataclass
-class FFNConfig:
+class FFNConfig(_Marshalled):
     """Gated feed-forward block (mirrors moe_ffn_config): x, y [T, d]; W1, W3 [ffn, d]; W2 [d, ffn]."""
 
     T: int
@@ -405,6 +451,11 @@ class FFNConfig:
 
     def to_c(self) -> _FFNConfig:
         return _FFNConfig(int(self.T), int(self.d), int(self.ffn), int(self.timeout_us))
+
+    def _make(self):
+        c, n = self.to_c(), ctypes.c_size_t()
+        _check(lib().moe_ffn_saved_size(ctypes.byref(c), ctypes.byref(n)))
+        return (ctypes.byref(c), c, (self.T, self.d), (self.ffn, self.d), (self.d, self.ffn), n.value)
 
 
 class FFNWorkspace:
@@ -416,71 +467,54 @@ class FFNWorkspace:
         self.nbytes = n.value
         self.buf = torch.empty(self.nbytes, dtype=torch.uint8, device=device)
         self.buf[:MOE_FFN_STATUS_BYTES].zero_()
-
-    @property
-    def ptr(self) -> ctypes.c_void_p:
-        return ctypes.c_void_p(self.buf.data_ptr())
+        self.ptr = self.buf.data_ptr()
 
 
 def ffn_saved(cfg: FFNConfig, device="cuda") -> torch.Tensor:
     """Buffer in which ffn_forward keeps what ffn_backward needs (uint8, opaque)."""
-    n, c = ctypes.c_size_t(), cfg.to_c()
-    _check(lib().moe_ffn_saved_size(ctypes.byref(c), ctypes.byref(n)))
-    return torch.empty(n.value, dtype=torch.uint8, device=device)
+    return torch.empty(cfg.ref()[5], dtype=torch.uint8, device=device)
 
 
-def _ffn_weights(cfg: FFNConfig, W1, W3, W2, prefix=""):
-    bf, up, down = torch.bfloat16, (cfg.ffn, cfg.d), (cfg.d, cfg.ffn)
-    _shape(W1, up, prefix + "W1")
-    _shape(W3, up, prefix + "W3")
-    _shape(W2, down, prefix + "W2")
-    return (_ptr(W1, bf, "cuda", prefix + "W1"), _ptr(W3, bf, "cuda", prefix + "W3"),
-            _ptr(W2, bf, "cuda", prefix + "W2"))
-
-
-def _ffn_rows(cfg: FFNConfig, t, name):
-    _shape(t, (cfg.T, cfg.d), name)
-    return _ptr(t, torch.bfloat16, "cuda", name)
-
-
-def _ffn_saved_ptr(cfg: FFNConfig, c, saved):
+def _saved(saved, need: int):
     if saved is None:
         return None
-    n = ctypes.c_size_t()
-    _check(lib().moe_ffn_saved_size(ctypes.byref(c), ctypes.byref(n)))
-    if saved.numel() * saved.element_size() < n.value:
-        raise ValueError(f"saved has {saved.numel() * saved.element_size()} bytes, needs {n.value}")
+    n = saved.numel() * saved.element_size()
+    if n < need:
+        raise ValueError(f"saved has {n} bytes, needs {need}")
     return _ptr(saved, None, "cuda", "saved")
 
 
 def ffn_forward(cfg: FFNConfig, x: torch.Tensor, W1: torch.Tensor, W3: torch.Tensor, W2: torch.Tensor,
                 y: torch.Tensor, ws: FFNWorkspace, saved: Optional[torch.Tensor] = None, stream=None) -> None:
     """moe_ffn_forward: y = (silu(x W1^T) * (x W3^T)) W2^T; saved (ffn_saved) for a backward pass."""
-    c = cfg.to_c()
-    _check(lib().moe_ffn_forward(ctypes.byref(c), _ffn_rows(cfg, x, "x"), *_ffn_weights(cfg, W1, W3, W2),
-                                 _ffn_rows(cfg, y, "y"), _ffn_saved_ptr(cfg, c, saved), ws.ptr, ws.nbytes,
-                                 _stream(stream)))
+    bf = torch.bfloat16
+    c, _, rows, up, down, need = cfg.ref()
+    _check(lib().moe_ffn_forward(c, _dev(x, bf, rows, "x"), _dev(W1, bf, up, "W1"), _dev(W3, bf, up, "W3"),
+                                 _dev(W2, bf, down, "W2"), _dev(y, bf, rows, "y"), _saved(saved, need), ws.ptr,
+                                 ws.nbytes, _raw_stream(stream, x)))
 
 
 def ffn_backward(cfg: FFNConfig, x: torch.Tensor, W1: torch.Tensor, W3: torch.Tensor, W2: torch.Tensor,
                  dy: torch.Tensor, saved: torch.Tensor, dx: torch.Tensor, dW1: torch.Tensor, dW3: torch.Tensor,
                  dW2: torch.Tensor, ws: FFNWorkspace, stream=None) -> None:
     """moe_ffn_backward: gradients of x and the weights from dy and the forward pass's saved buffer."""
-    c = cfg.to_c()
-    _check(lib().moe_ffn_backward(ctypes.byref(c), _ffn_rows(cfg, x, "x"), *_ffn_weights(cfg, W1, W3, W2),
-                                  _ffn_rows(cfg, dy, "dy"), _ffn_saved_ptr(cfg, c, saved), _ffn_rows(cfg, dx, "dx"),
-                                  *_ffn_weights(cfg, dW1, dW3, dW2, "d"), ws.ptr, ws.nbytes, _stream(stream)))
+    bf = torch.bfloat16
+    c, _, rows, up, down, need = cfg.ref()
+    _check(lib().moe_ffn_backward(c, _dev(x, bf, rows, "x"), _dev(W1, bf, up, "W1"), _dev(W3, bf, up, "W3"),
+                                  _dev(W2, bf, down, "W2"), _dev(dy, bf, rows, "dy"), _saved(saved, need),
+                                  _dev(dx, bf, rows, "dx"), _dev(dW1, bf, up, "dW1"), _dev(dW3, bf, up, "dW3"),
+                                  _dev(dW2, bf, down, "dW2"), ws.ptr, ws.nbytes, _raw_stream(stream, x)))
 
 
 def ffn_status(cfg: FFNConfig, ws: FFNWorkspace, stream=None):
     """(return code, detail) of the calls on ws; synchronises the stream."""
-    c, detail = cfg.to_c(), ctypes.c_int32()
-    rc = lib().moe_ffn_status(ctypes.byref(c), ws.ptr, _stream(stream), ctypes.byref(detail))
+    detail = ctypes.c_int32()
+    rc = lib().moe_ffn_status(cfg.ref()[0], ws.ptr, _stream(stream), ctypes.byref(detail))
     return rc, detail.value
 
 
 @dataclasses.dataclass
-class LayerNormConfig:
+class LayerNormConfig(_Marshalled):
     """Layer norm over rows of d values (mirrors moe_layernorm_config)."""
 
     rows: int
@@ -500,37 +534,22 @@ class LayerNormWorkspace:
     """Device workspace of layernorm_backward."""
 
     def __init__(self, cfg: LayerNormConfig, device="cuda"):
-        n, c = ctypes.c_size_t(), cfg.to_c()
-        _check(lib().moe_layernorm_workspace_size(ctypes.byref(c), ctypes.byref(n)))
+        n = ctypes.c_size_t()
+        _check(lib().moe_layernorm_workspace_size(cfg.ref()[0], ctypes.byref(n)))
         self.nbytes = n.value
         self.buf = torch.empty(self.nbytes, dtype=torch.uint8, device=device)
-
-    @property
-    def ptr(self) -> ctypes.c_void_p:
-        return ctypes.c_void_p(self.buf.data_ptr())
-
-
-def _ln_rows(cfg: LayerNormConfig, t, name):
-    if t.numel() != cfg.rows * cfg.d or t.shape[-1] != cfg.d:
-        raise ValueError(f"{name} must hold {cfg.rows} rows of {cfg.d} values, got {tuple(t.shape)}")
-    return _ptr(t, cfg.dtype, "cuda", name)
-
-
-def _ln_vec(t, n, dtype, name):
-    if t is not None and t.numel() != n:
-        raise ValueError(f"{name} must hold {n} values, got {t.numel()}")
-    return _ptr(t, dtype, "cuda", name)
+        self.ptr = self.buf.data_ptr()
 
 
 def layernorm_forward(cfg: LayerNormConfig, x: torch.Tensor, w: Optional[torch.Tensor], b: Optional[torch.Tensor],
                       y: torch.Tensor, mean: Optional[torch.Tensor] = None, rstd: Optional[torch.Tensor] = None,
                       stream=None) -> None:
     """moe_layernorm_forward: y = (x - mean) * rstd * w + b; mean and rstd [rows] for a backward pass."""
-    c, f32 = cfg.to_c(), torch.float32
-    _check(lib().moe_layernorm_forward(ctypes.byref(c), _ln_rows(cfg, x, "x"), _ln_vec(w, cfg.d, cfg.wdtype, "w"),
-                                       _ln_vec(b, cfg.d, cfg.wdtype, "b"), _ln_rows(cfg, y, "y"),
-                                       _ln_vec(mean, cfg.rows, f32, "mean"), _ln_vec(rstd, cfg.rows, f32, "rstd"),
-                                       _stream(stream)))
+    dt, wt, rows, d = cfg.dtype, cfg.wdtype, cfg.rows, cfg.d
+    n, f32 = rows * d, torch.float32
+    _check(lib().moe_layernorm_forward(cfg.ref()[0], _flat(x, dt, n, "x"), _flat(w, wt, d, "w"), _flat(b, wt, d, "b"),
+                                       _flat(y, dt, n, "y"), _flat(mean, f32, rows, "mean"),
+                                       _flat(rstd, f32, rows, "rstd"), _raw_stream(stream, x)))
 
 
 def layernorm_backward(cfg: LayerNormConfig, dy: torch.Tensor, x: torch.Tensor, w: Optional[torch.Tensor],
@@ -538,16 +557,17 @@ def layernorm_backward(cfg: LayerNormConfig, dy: torch.Tensor, x: torch.Tensor, 
                        db: Optional[torch.Tensor] = None, ws: Optional[LayerNormWorkspace] = None,
                        stream=None) -> None:
     """moe_layernorm_backward: dx, and dw, db summed over the rows (both may be None, then ws too)."""
-    c, f32 = cfg.to_c(), torch.float32
+    dt, wt, rows, d = cfg.dtype, cfg.wdtype, cfg.rows, cfg.d
+    n, f32 = rows * d, torch.float32
     _check(lib().moe_layernorm_backward(
-        ctypes.byref(c), _ln_rows(cfg, dy, "dy"), _ln_rows(cfg, x, "x"), _ln_vec(w, cfg.d, cfg.wdtype, "w"),
-        _ln_vec(mean, cfg.rows, f32, "mean"), _ln_vec(rstd, cfg.rows, f32, "rstd"), _ln_rows(cfg, dx, "dx"),
-        _ln_vec(dw, cfg.d, cfg.wdtype, "dw"), _ln_vec(db, cfg.d, cfg.wdtype, "db"),
-        None if ws is None else ws.ptr, 0 if ws is None else ws.nbytes, _stream(stream)))
+        cfg.ref()[0], _flat(dy, dt, n, "dy"), _flat(x, dt, n, "x"), _flat(w, wt, d, "w"),
+        _flat(mean, f32, rows, "mean"), _flat(rstd, f32, rows, "rstd"), _flat(dx, dt, n, "dx"),
+        _flat(dw, wt, d, "dw"), _flat(db, wt, d, "db"), None if ws is None else ws.ptr,
+        0 if ws is None else ws.nbytes, _raw_stream(stream, x)))
 
 
 @dataclasses.dataclass
-class AdamWConfig:
+class AdamWConfig(_Marshalled):
     """AdamW's numbers (mirrors moe_adamw_config; the step is an argument of adamw_step). bits: 32 or 8."""
 
     lr: float
@@ -558,7 +578,7 @@ class AdamWConfig:
     bits: int = 32
     seed: int = 0
 
-    def to_c(self, step: int) -> _AdamWConfig:
+    def to_c(self, step: int = 1) -> _AdamWConfig:
         return _AdamWConfig(self.lr, self.beta1, self.beta2, self.eps, self.weight_decay, int(step),
                             int(self.seed) & (2 ** 64 - 1), int(self.bits))
 
@@ -604,6 +624,9 @@ class AdamWList:
             e.p_dtype, e.g_dtype = _DTYPES[p[i].dtype], _DTYPES[g[i].dtype]
             base += blocks * MOE_ADAMW_BLOCK
 
+    def stream(self, stream):
+        return _raw_stream(stream, self.keep[0][0]) if self.count else _stream(stream)
+
 
 class AdamWValues:
     """Where adamw_read_state writes: float32 tensors, one m and one v for each tensor of the list."""
@@ -626,15 +649,14 @@ def adamw_step(cfg: AdamWConfig, tensors: AdamWList, step: int, grad_scale: Opti
     """moe_adamw_step: one step (counted from 1) over every tensor; grad_scale: a float32 value on the GPU."""
     if cfg.bits != tensors.bits:
         raise ValueError(f"the list was made for {tensors.bits}-bit states")
-    if grad_scale is not None and grad_scale.numel() != 1:
-        raise ValueError("grad_scale must hold one value")
-    c = cfg.to_c(step)
-    _check(lib().moe_adamw_step(ctypes.byref(c), tensors.c, tensors.count,
-                                _ptr(grad_scale, torch.float32, "cuda", "grad_scale"), _stream(stream)))
+    ref, c = cfg.ref()
+    c.step = step
+    _check(lib().moe_adamw_step(ref, tensors.c, tensors.count, _flat(grad_scale, torch.float32, 1, "grad_scale"),
+                                tensors.stream(stream)))
 
 
 def adamw_read_state(cfg: AdamWConfig, tensors: AdamWList, out: AdamWValues, stream=None) -> None:
     """moe_adamw_read_state: the float32 values that the list's 8-bit states stand for."""
     if cfg.bits != 8 or tensors.bits != 8:
         raise ValueError("32-bit states are read as they are")
-    _check(lib().moe_adamw_read_state(tensors.c, tensors.count, out.m, out.v, _stream(stream)))
+    _check(lib().moe_adamw_read_state(tensors.c, tensors.count, out.m, out.v, tensors.stream(stream)))

@@ -5,160 +5,281 @@
 //             dx = rstd (gy - sum(gy) / d - xh sum(gy xh) / d), dw = sum_rows dy xh, db = sum_rows dy
 //
 // The forward pass reads x and writes y, the backward pass reads x and dy and writes dx: both are
-// bound by HBM. A group of threads holds its whole row in registers (16 values a thread, 32 for rows above 8192), so the
-// variance is the mean of squared differences (no cancellation) without a second read, and the
-// next row's values are loaded while this row's sums are taken. Groups keep their columns'
-// weights, and in the backward pass their columns' partial sums of dw and db, in registers over all
-// their rows; the partial sums of each CTA are added up in a second launch in CTA order.
+// bound by HBM as long as enough loads are in flight and the arithmetic (about a dozen operations a
+// value; sums and products two at a time, f32x2) stays below it.
+//
+// Forward: a row belongs to one warp as far as it fits its registers (2048 values, 4096 in 16 bits and whole vectors),
+// so the variance is the mean of squared differences without a second read, no barrier is
+// waited for, and a warp's loads are all in flight at once (8 KB). Weights come from L1. Longer
+// rows, and rows of a launch with few of them, are shared by several warps.
+// Backward: a thread keeps the same columns over all its rows, with their partial sums of dw and db
+// in registers, and takes several rows at a time (32 values in all) so that one reduction and one
+// barrier serve all of them. The CTAs' partial sums are added up in CTA order by a second launch.
 #include "host_internal.h"
 #include "moe_internal.cuh"
 
 #include <cuda_fp16.h>
 
+#include <type_traits>
+
 namespace moe {
 namespace {
 
-constexpr int LN_MAX_THREADS = 512;
-constexpr int LN_WIDE = 16 * LN_MAX_THREADS;  // rows above this take 32 values a thread
-constexpr int LN_MAX_D = 32 * LN_MAX_THREADS;
-constexpr int LN_THREADS = 256;   // threads of a CTA when a row takes fewer
-constexpr int LN_RED_COLS = 32;   // columns of a CTA of the second launch
-constexpr int LN_RED_ROWS = 16;   // partial sums it adds side by side
+constexpr int LN_FWD_THREADS = 256;
+constexpr int LN_BWD_THREADS = 256;  // a row above 4096 values takes up to 512
+constexpr int LN_MAX_D = 16384;
+constexpr int LN_RED_COLS = 32;   // columns of a CTA of the reduction
+constexpr int LN_RED_ROWS = 32;   // partial sums it adds side by side
 
-__device__ __forceinline__ float num(float v) { return v; }
-__device__ __forceinline__ float num(__nv_bfloat16 v) { return __bfloat162float(v); }
-__device__ __forceinline__ float num(__half v) { return __half2float(v); }
-template <typename T>
-__device__ __forceinline__ T rounded(float v);
-template <>
-__device__ __forceinline__ float rounded<float>(float v) { return v; }
-template <>
-__device__ __forceinline__ __nv_bfloat16 rounded<__nv_bfloat16>(float v) { return __float2bfloat16_rn(v); }
-template <>
-__device__ __forceinline__ __half rounded<__half>(float v) { return __float2half_rn(v); }
+template <int N>
+struct Int {
+    static constexpr int value = N;
+};
 
+// ---- values, one (float) or two (f2: a pair of fp32 in 64 bits) at a time -------------------------
+typedef unsigned long long f2;
+__device__ __forceinline__ f2 pair(float lo, float hi) {
+    f2 r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+    return r;
+}
+__device__ __forceinline__ float2 split(f2 v) {
+    float2 r;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
+    return r;
+}
+__device__ __forceinline__ f2 add_(f2 a, f2 b) {
+    f2 r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ f2 mul_(f2 a, f2 b) {
+    f2 r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ f2 fma_(f2 a, f2 b, f2 c) {
+    f2 r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+__device__ __forceinline__ float add_(float a, float b) { return a + b; }
+__device__ __forceinline__ float mul_(float a, float b) { return a * b; }
+__device__ __forceinline__ float fma_(float a, float b, float c) { return fmaf(a, b, c); }
+__device__ __forceinline__ float total(f2 v) {
+    const float2 s = split(v);
+    return s.x + s.y;
+}
+__device__ __forceinline__ float total(float v) { return v; }
+template <typename V>
+__device__ __forceinline__ V both(float v);
+template <>
+__device__ __forceinline__ f2 both<f2>(float v) { return pair(v, v); }
+template <>
+__device__ __forceinline__ float both<float>(float v) { return v; }
+
+// VEC consecutive values of a row as they lie in memory, and as fp32.
 template <typename T, int VEC>
 struct alignas(sizeof(T) * VEC) Pack {
     T v[VEC];
 };
+template <int VEC>
+struct Lanes {
+    typedef f2 V;
+    static constexpr int N = VEC / 2;
+};
+template <>
+struct Lanes<1> {
+    typedef float V;
+    static constexpr int N = 1;
+};
 
-// How the threads of a launch share the rows: `tpr` threads a row (a power of two up to 32, or whole
-// warps), `groups` rows at a time in a CTA.
+__device__ __forceinline__ float num(float v) { return v; }
+__device__ __forceinline__ float num(__nv_bfloat16 v) { return __bfloat162float(v); }
+__device__ __forceinline__ float num(__half v) { return __half2float(v); }
+__device__ __forceinline__ void put(float& o, float v) { o = v; }
+__device__ __forceinline__ void put(__nv_bfloat16& o, float v) { o = __float2bfloat16_rn(v); }
+__device__ __forceinline__ void put(__half& o, float v) { o = __float2half_rn(v); }
+
+template <typename T, int VEC>
+__device__ __forceinline__ void widen(const Pack<T, VEC>& p, f2 (&o)[VEC / 2]) {
+#pragma unroll
+    for (int i = 0; i < VEC / 2; ++i) o[i] = pair(num(p.v[2 * i]), num(p.v[2 * i + 1]));
+}
+template <int VEC>
+__device__ __forceinline__ void widen(const Pack<__nv_bfloat16, VEC>& p, f2 (&o)[VEC / 2]) {
+    const uint32_t* w = reinterpret_cast<const uint32_t*>(&p);
+#pragma unroll
+    for (int i = 0; i < VEC / 2; ++i) o[i] = pair(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xffff0000u));
+}
+template <typename T>
+__device__ __forceinline__ void widen(const Pack<T, 1>& p, float (&o)[1]) {
+    o[0] = num(p.v[0]);
+}
+template <typename T, int VEC>
+__device__ __forceinline__ std::enable_if_t<(sizeof(T) == 4), Pack<T, VEC>> narrow(const f2 (&f)[VEC / 2]) {
+    Pack<T, VEC> r;
+#pragma unroll
+    for (int i = 0; i < VEC / 2; ++i) {
+        const float2 s = split(f[i]);
+        put(r.v[2 * i], s.x);
+        put(r.v[2 * i + 1], s.y);
+    }
+    return r;
+}
+template <typename T, int VEC>
+__device__ __forceinline__ std::enable_if_t<(sizeof(T) == 2), Pack<T, VEC>> narrow(const f2 (&f)[VEC / 2]) {
+    Pack<T, VEC> r;
+    uint32_t* w = reinterpret_cast<uint32_t*>(&r);
+#pragma unroll
+    for (int i = 0; i < VEC / 2; ++i) {
+        const float2 s = split(f[i]);
+        if constexpr (std::is_same_v<T, __half>) {
+            const __half2 h = __floats2half2_rn(s.x, s.y);
+            w[i] = *reinterpret_cast<const uint32_t*>(&h);
+        } else {
+            w[i] = pack_bf16x2(s.x, s.y);
+        }
+    }
+    return r;
+}
+template <typename T, int VEC>
+__device__ __forceinline__ Pack<T, 1> narrow(const float (&f)[1]) {
+    Pack<T, 1> r;
+    put(r.v[0], f[0]);
+    return r;
+}
+// Keeps the compiler from holding a piece's fp32 form from one pass over the row to the next (it would
+// take two registers a 16-bit pair and spill): each pass widens it again, one operation a value.
+template <typename T, int VEC>
+__device__ __forceinline__ void opaque(Pack<T, VEC>& p) {
+    if constexpr (sizeof(p) == 2) {
+        asm volatile("" : "+h"(*reinterpret_cast<uint16_t*>(&p)));
+    } else {
+#pragma unroll
+        for (int i = 0; i < (int)sizeof(p) / 4; ++i) asm volatile("" : "+r"(reinterpret_cast<uint32_t*>(&p)[i]));
+    }
+}
+// How a launch reads its weights: fp32 or the rows' type, both vectors there and aligned for whole
+// pieces, or one value at a time (a null vector stands for `none`).
+enum LnWeights : int { LN_W_F32, LN_W_SAME, LN_W_ANY };
+
+template <typename T, int VEC, int W>
+__device__ __forceinline__ void weights(const void* w, bool f32, float none, int c,
+                                        typename Lanes<VEC>::V (&o)[Lanes<VEC>::N]) {
+    if (W == LN_W_SAME) {
+        widen(*reinterpret_cast<const Pack<T, VEC>*>(static_cast<const T*>(w) + c), o);
+        return;
+    }
+    const float* p = static_cast<const float*>(w) + c;
+    Pack<float, VEC> v;
+    if (W == LN_W_F32 && VEC >= 4) {
+#pragma unroll
+        for (int i = 0; i < VEC / 4; ++i)
+            *reinterpret_cast<float4*>(&v.v[4 * i]) = *reinterpret_cast<const float4*>(p + 4 * i);
+    } else {
+#pragma unroll
+        for (int i = 0; i < VEC; ++i) v.v[i] = !w ? none : f32 ? p[i] : num(static_cast<const T*>(w)[c + i]);
+    }
+    widen(v, o);
+}
+
+__device__ __forceinline__ float warp_sum(float a) {
+#pragma unroll
+    for (int o = 16; o; o >>= 1) a += __shfl_xor_sync(0xffffffffu, a, o);
+    return a;
+}
+
+// How a launch's threads share the rows: groups of `warps` warps, `groups` of them in a CTA.
 struct LnShape {
     int64_t rows;
-    int d, tpr, groups;
+    int d, warps, groups;
     float eps, inv_d;
 };
 
-// A thread's E values of a row as VEC-wide pieces: piece q covers columns (q * tpr + t) * VEC...
-template <typename T, int VEC, int E>
-struct RowPart {
-    static constexpr int NP = E / VEC;
-    Pack<T, VEC> p[NP];
-    __device__ __forceinline__ void load(const T* row, int t, const LnShape& s) {
-#pragma unroll
-        for (int q = 0; q < NP; ++q) {
-            const int c = (q * s.tpr + t) * VEC;
-            if (c < s.d) p[q] = *reinterpret_cast<const Pack<T, VEC>*>(row + c);
-        }
-    }
-    __device__ __forceinline__ void floats(float (&f)[E], int t, const LnShape& s) const {
-#pragma unroll
-        for (int q = 0; q < NP; ++q) {
-            const bool in = (q * s.tpr + t) * VEC < s.d;
-#pragma unroll
-            for (int j = 0; j < VEC; ++j) f[q * VEC + j] = in ? num(p[q].v[j]) : 0.f;
-        }
-    }
-};
-
-template <typename T, int VEC, int E>
-__device__ __forceinline__ void store_row(T* row, const float (&f)[E], int t, const LnShape& s) {
-#pragma unroll
-    for (int q = 0; q < E / VEC; ++q) {
-        const int c = (q * s.tpr + t) * VEC;
-        if (c >= s.d) continue;
-        Pack<T, VEC> o;
-#pragma unroll
-        for (int j = 0; j < VEC; ++j) o.v[j] = rounded<T>(f[q * VEC + j]);
-        *reinterpret_cast<Pack<T, VEC>*>(row + c) = o;
-    }
-}
-
-// Weights of a thread's columns (w null: `none`).
-template <typename T, int VEC, int E>
-__device__ __forceinline__ void load_weights(const void* w, bool f32, float none, float (&f)[E], int t,
-                                             const LnShape& s) {
-#pragma unroll
-    for (int i = 0; i < E; ++i) {
-        const int c = ((i / VEC) * s.tpr + t) * VEC + i % VEC;
-        f[i] = none;
-        if (w && c < s.d) f[i] = f32 ? static_cast<const float*>(w)[c] : num(static_cast<const T*>(w)[c]);
-    }
-}
-
-// Sum of a and b over a row's group of threads, the same in all of them. Groups of whole warps pass
-// their warps' sums through `red` (32 float2 a group, used alternately by `flip` so that one
-// barrier a sum is enough).
-__device__ __forceinline__ float2 group_sum(float a, float b, int tpr, int group, float2* red, int& flip) {
-    for (int o = min(tpr, 32) >> 1; o; o >>= 1) {
-        a += __shfl_xor_sync(0xffffffffu, a, o);
-        b += __shfl_xor_sync(0xffffffffu, b, o);
-    }
-    if (tpr <= 32) return make_float2(a, b);
-    const int warps = tpr >> 5, w = (threadIdx.x % tpr) >> 5, lane = threadIdx.x & 31;
-    float2* r = red + (flip * (blockDim.x / 32)) + group * warps;
-    flip ^= 1;
-    if (lane == 0) r[w] = make_float2(a, b);
-    named_bar_sync(1 + group, tpr);
-    float2 v = lane < warps ? r[lane] : make_float2(0.f, 0.f);
-    for (int o = 16; o; o >>= 1) {
-        v.x += __shfl_xor_sync(0xffffffffu, v.x, o);
-        v.y += __shfl_xor_sync(0xffffffffu, v.y, o);
-    }
-    return v;
-}
-
-template <typename T, int VEC, int E>
-__global__ void __launch_bounds__(LN_MAX_THREADS) ln_forward_kernel(LnShape s, const T* x, const void* w, const void* b,
-                                                          bool wf32, T* y, float* mean, float* rstd) {
-    __shared__ float2 red[64];
+// NV values of a row a thread, in NV / VEC pieces: piece q covers columns (q * 32 warps + t) VEC...
+template <typename T, int VEC, int NV>
+__global__ void __launch_bounds__(LN_FWD_THREADS, 2)
+    ln_forward_kernel(LnShape s, const T* x, const void* w, const void* b, bool wf32, int form, T* y, float* mean,
+                      float* rstd) {
+    typedef typename Lanes<VEC>::V V;
+    constexpr int NP = NV / VEC, N = Lanes<VEC>::N;
+    __shared__ float red[2][LN_FWD_THREADS / 32];
     griddep_wait();
     griddep_launch();
-    const int t = threadIdx.x % s.tpr, group = threadIdx.x / s.tpr;
-    const int64_t stride = (int64_t)gridDim.x * s.groups;
-    float wf[E], bf[E];
-    load_weights<T, VEC, E>(w, wf32, 1.f, wf, t, s);
-    load_weights<T, VEC, E>(b, wf32, 0.f, bf, t, s);
+    const int tpr = s.warps * 32, t = threadIdx.x % tpr, group = threadIdx.x / tpr, lane = threadIdx.x & 31;
+    const int step = tpr * VEC, c0 = t * VEC;
+    const int np = c0 < s.d ? min(NP, (s.d - c0 + step - 1) / step) : 0;  // this thread's pieces
     int flip = 0;
-    RowPart<T, VEC, E> next;
-    int64_t r = (int64_t)blockIdx.x * s.groups + group;
-    // groups that share a warp take part in its shuffles until all of them are done
-    const int64_t last = s.tpr < 32 ? r - group % (32 / s.tpr) : r;
-    if (r < s.rows) next.load(x + r * s.d, t, s);
-    for (int64_t r0 = last; r0 < s.rows; r0 += stride, r += stride) {
-        const RowPart<T, VEC, E> part = next;
-        const bool in = r < s.rows;
-        if (r + stride < s.rows) next.load(x + (r + stride) * s.d, t, s);
-        float f[E];
-        part.floats(f, t, s);
+    auto row_sum = [&](float a) {
+        a = warp_sum(a);
+        if (s.warps == 1) return a;
+        float* r = red[flip] + group * s.warps;  // the two halves in turn: one barrier a sum is enough
+        flip ^= 1;
+        if (lane == 0) r[t >> 5] = a;
+        named_bar_sync(1 + group, tpr);
+        a = 0.f;
+        for (int i = 0; i < s.warps; ++i) a += r[i];
+        return a;
+    };
+    for (int64_t r = (int64_t)blockIdx.x * s.groups + group; r < s.rows; r += (int64_t)gridDim.x * s.groups) {
+        const T* xr = x + r * s.d + c0;
+        Pack<T, VEC> p[NP];
+#pragma unroll
+        for (int q = 0; q < NP; ++q)
+            if (q < np) p[q] = *reinterpret_cast<const Pack<T, VEC>*>(xr + q * step);
+        V f[N], acc[N];
+#pragma unroll
+        for (int i = 0; i < N; ++i) acc[i] = both<V>(0.f);
+#pragma unroll
+        for (int q = 0; q < NP; ++q) {
+            if (q >= np) break;
+            widen(p[q], f);
+#pragma unroll
+            for (int i = 0; i < N; ++i) acc[i] = add_(acc[i], f[i]);
+        }
         float a = 0.f;
 #pragma unroll
-        for (int i = 0; i < E; ++i) a += f[i];
-        const float mu = group_sum(a, 0.f, s.tpr, group, red, flip).x * s.inv_d;
+        for (int i = 0; i < N; ++i) a += total(acc[i]);
+        const float mu = row_sum(a) * s.inv_d;
+        const V neg = both<V>(-mu);
+#pragma unroll
+        for (int i = 0; i < N; ++i) acc[i] = both<V>(0.f);
+#pragma unroll
+        for (int q = 0; q < NP; ++q) {
+            if (q >= np) break;
+            opaque(p[q]);
+            widen(p[q], f);
+#pragma unroll
+            for (int i = 0; i < N; ++i) {
+                f[i] = add_(f[i], neg);
+                acc[i] = fma_(f[i], f[i], acc[i]);
+            }
+        }
         a = 0.f;
 #pragma unroll
-        for (int i = 0; i < E; ++i) {
-            const int c = ((i / VEC) * s.tpr + t) * VEC;
-            f[i] = c < s.d ? f[i] - mu : 0.f;
-            a = fmaf(f[i], f[i], a);
-        }
-        const float var = group_sum(a, 0.f, s.tpr, group, red, flip).x * s.inv_d;
-        const float rs = 1.0f / sqrtf(var + s.eps);
-        if (!in) continue;
+        for (int i = 0; i < N; ++i) a += total(acc[i]);
+        const float rs = rsqrtf(fmaf(row_sum(a), s.inv_d, s.eps));
+        const V vrs = both<V>(rs);
+        T* yr = y + r * s.d + c0;
+        auto finish = [&](auto form) {
+            constexpr int W = decltype(form)::value;
 #pragma unroll
-        for (int i = 0; i < E; ++i) f[i] = fmaf(f[i] * rs, wf[i], bf[i]);
-        store_row<T, VEC>(y + r * s.d, f, t, s);
+            for (int q = 0; q < NP; ++q) {
+                if (q >= np) break;
+                V wv[N], bv[N];
+                weights<T, VEC, W>(w, wf32, 1.f, c0 + q * step, wv);
+                weights<T, VEC, W>(b, wf32, 0.f, c0 + q * step, bv);
+                opaque(p[q]);
+                widen(p[q], f);
+#pragma unroll
+                for (int i = 0; i < N; ++i) f[i] = fma_(mul_(add_(f[i], neg), vrs), wv[i], bv[i]);
+                *reinterpret_cast<Pack<T, VEC>*>(yr + q * step) = narrow<T, VEC>(f);
+            }
+        };
+        if (VEC == 1 || form == LN_W_ANY) finish(Int<LN_W_ANY>());
+        else if (form == LN_W_SAME) finish(Int<LN_W_SAME>());
+        else finish(Int<LN_W_F32>());
         if (t == 0) {
             if (mean) mean[r] = mu;
             if (rstd) rstd[r] = rs;
@@ -166,76 +287,160 @@ __global__ void __launch_bounds__(LN_MAX_THREADS) ln_forward_kernel(LnShape s, c
     }
 }
 
-template <typename T, int VEC, int E>
-__global__ void __launch_bounds__(LN_MAX_THREADS) ln_backward_kernel(LnShape s, const T* dy, const T* x, const void* w, bool wf32,
-                                                           const float* mean, const float* rstd, T* dx, float* part) {
-    __shared__ float2 red[64];
-    griddep_wait();
-    griddep_launch();
-    const int t = threadIdx.x % s.tpr, group = threadIdx.x / s.tpr;
-    const int64_t stride = (int64_t)gridDim.x * s.groups;
-    float wf[E], dw[E], db[E];
-    load_weights<T, VEC, E>(w, wf32, 1.f, wf, t, s);
+// Sums of K values (a power of two up to 32) over a warp: lane l gets the total of value l / (32 / K).
+template <int K>
+__device__ __forceinline__ float warp_sums(float (&v)[K], int lane) {
 #pragma unroll
-    for (int i = 0; i < E; ++i) dw[i] = db[i] = 0.f;
-    int flip = 0;
-    RowPart<T, VEC, E> nx, ny;
-    float nmu = 0.f, nrs = 0.f;
-    int64_t r = (int64_t)blockIdx.x * s.groups + group;
-    const int64_t last = s.tpr < 32 ? r - group % (32 / s.tpr) : r;
-    auto fetch = [&](int64_t q) {
-        nx.load(x + q * s.d, t, s);
-        ny.load(dy + q * s.d, t, s);
-        nmu = mean[q];
-        nrs = rstd[q];
-    };
-    if (r < s.rows) fetch(r);
-    for (int64_t r0 = last; r0 < s.rows; r0 += stride, r += stride) {
-        const RowPart<T, VEC, E> px = nx, py = ny;
-        const float mu = nmu, rs = nrs;
-        const bool in = r < s.rows;
-        if (r + stride < s.rows) fetch(r + stride);
-        float xh[E], g[E];
-        px.floats(xh, t, s);
-        py.floats(g, t, s);
-        float a = 0.f, b = 0.f;
+    for (int half = K / 2, o = 16; half >= 1; half >>= 1, o >>= 1) {
+        const bool hi = lane & o;  // this half of the warp keeps the upper half of the values
 #pragma unroll
-        for (int i = 0; i < E; ++i) {
-            const int c = ((i / VEC) * s.tpr + t) * VEC;
-            const bool on = in && c < s.d;
-            xh[i] = on ? (xh[i] - mu) * rs : 0.f;
-            g[i] = on ? g[i] : 0.f;
-            dw[i] = fmaf(g[i], xh[i], dw[i]);
-            db[i] += g[i];
-            g[i] *= wf[i];
-            a += g[i];
-            b = fmaf(g[i], xh[i], b);
+        for (int i = 0; i < half; ++i) {
+            const float send = hi ? v[i] : v[i + half], keep = hi ? v[i + half] : v[i];
+            v[i] = keep + __shfl_xor_sync(0xffffffffu, send, o);
         }
-        const float2 c = group_sum(a, b, s.tpr, group, red, flip);
-        if (!in) continue;
-        const float c1 = c.x * s.inv_d, c2 = c.y * s.inv_d;
-#pragma unroll
-        for (int i = 0; i < E; ++i) g[i] = rs * (g[i] - c1 - xh[i] * c2);
-        store_row<T, VEC>(dx + r * s.d, g, t, s);
     }
-    if (!part) return;
-    // this CTA's sums: its groups' one after another, so that the order is the same every time
-    float* pw = part + (size_t)blockIdx.x * 2 * s.d;
-    for (int q = 0; q < s.groups; ++q) {
-        if (group == q) {
+    float a = v[0];
 #pragma unroll
-            for (int i = 0; i < E; ++i) {
-                const int c = ((i / VEC) * s.tpr + t) * VEC + i % VEC;
-                if (c >= s.d) continue;
-                pw[c] = q ? pw[c] + dw[i] : dw[i];
-                pw[s.d + c] = q ? pw[s.d + c] + db[i] : db[i];
-            }
-        }
-        __syncthreads();
-    }
+    for (int o = 16 / K; o; o >>= 1) a += __shfl_xor_sync(0xffffffffu, a, o);
+    return a;
 }
 
-// dw and db from the CTAs' partial sums [parts][2][d]: CTA (column block, 0 for dw / 1 for db).
+// Rows a group takes at a time: 32 values a thread, 16 where a value takes a register of its own.
+__host__ __device__ constexpr int bwd_rows(size_t size, int vec, int nv) {
+    return nv == 32 ? 1 : (vec == 1 || size == 4 ? 16 : 32) / nv;
+}
+
+// R rows at a time, NV columns a thread.
+template <typename T, int VEC, int NV>
+__global__ void __launch_bounds__(NV > 8 ? 512 : 256, NV > 8 ? 1 : 2)
+    ln_backward_kernel(LnShape s, const T* dy, const T* x, const void* w, bool wf32, const float* mean,
+                       const float* rstd, T* dx, float* part) {
+    typedef typename Lanes<VEC>::V V;
+    constexpr int NP = NV / VEC, N = Lanes<VEC>::N, R = bwd_rows(sizeof(T), VEC, NV);
+    __shared__ float red[2][16 * 2 * R];
+    extern __shared__ float sums[];  // [2][d]: the CTA's partial sums
+    griddep_wait();
+    griddep_launch();
+    const int tpr = s.warps * 32, t = threadIdx.x % tpr, group = threadIdx.x / tpr, lane = threadIdx.x & 31;
+    const int step = tpr * VEC, c0 = t * VEC;
+    V wv[NP][N], dw[NP][N], db[NP][N];
+#pragma unroll
+    for (int q = 0; q < NP; ++q) {
+#pragma unroll
+        for (int i = 0; i < N; ++i) wv[q][i] = dw[q][i] = db[q][i] = both<V>(0.f);
+        if (c0 + q * step < s.d) weights<T, VEC, LN_W_ANY>(w, wf32, 1.f, c0 + q * step, wv[q]);
+    }
+    int flip = 0;
+    // a group takes R consecutive rows; rows past the end read as zero and are not stored
+    for (int64_t r0 = ((int64_t)blockIdx.x * s.groups + group) * R; r0 < s.rows;
+         r0 += (int64_t)gridDim.x * s.groups * R) {
+        Pack<T, VEC> px[R][NP], py[R][NP];
+        float mu[R], rs[R];
+#pragma unroll
+        for (int j = 0; j < R; ++j) {
+            const bool on = r0 + j < s.rows;
+            const int64_t at = (r0 + j) * s.d + c0;
+            mu[j] = on ? mean[r0 + j] : 0.f;
+            rs[j] = on ? rstd[r0 + j] : 0.f;
+#pragma unroll
+            for (int q = 0; q < NP; ++q) {
+                if (on && c0 + q * step < s.d) {
+                    px[j][q] = *reinterpret_cast<const Pack<T, VEC>*>(x + at + q * step);
+                    py[j][q] = *reinterpret_cast<const Pack<T, VEC>*>(dy + at + q * step);
+                } else {
+                    memset(&px[j][q], 0, sizeof(px[j][q]));
+                    memset(&py[j][q], 0, sizeof(py[j][q]));
+                }
+            }
+        }
+        float v[2 * R];
+#pragma unroll
+        for (int j = 0; j < R; ++j) {
+            const V neg = both<V>(-mu[j]), vrs = both<V>(rs[j]);
+            V a = both<V>(0.f), b = both<V>(0.f);
+#pragma unroll
+            for (int q = 0; q < NP; ++q) {
+                V f[N], g[N];
+                widen(px[j][q], f);
+                widen(py[j][q], g);
+#pragma unroll
+                for (int i = 0; i < N; ++i) {
+                    f[i] = mul_(add_(f[i], neg), vrs);
+                    dw[q][i] = fma_(g[i], f[i], dw[q][i]);
+                    db[q][i] = add_(db[q][i], g[i]);
+                    g[i] = mul_(g[i], wv[q][i]);
+                    a = add_(a, g[i]);
+                    b = fma_(g[i], f[i], b);
+                }
+            }
+            v[2 * j] = total(a);
+            v[2 * j + 1] = total(b);
+        }
+        float c[2 * R];
+        const float mine = warp_sums<2 * R>(v, lane);
+        if (s.warps == 1) {
+#pragma unroll
+            for (int i = 0; i < 2 * R; ++i) c[i] = __shfl_sync(0xffffffffu, mine, i * (16 / R)) * s.inv_d;
+        } else {
+            // [value][warp]; a lane adds every (16 / R)-th warp of its value, then those lanes add up
+            constexpr int S = 16 / R;
+            float* sh = red[flip] + group * s.warps * 2 * R;
+            flip ^= 1;
+            if (lane % S == 0) sh[(lane / S) * s.warps + (t >> 5)] = mine;
+            named_bar_sync(1 + group, tpr);
+            float a = 0.f;
+            for (int k = lane % S; k < s.warps; k += S) a += sh[(lane / S) * s.warps + k];
+#pragma unroll
+            for (int o = S / 2; o; o >>= 1) a += __shfl_xor_sync(0xffffffffu, a, o);
+#pragma unroll
+            for (int i = 0; i < 2 * R; ++i) c[i] = __shfl_sync(0xffffffffu, a, i * S) * s.inv_d;
+        }
+#pragma unroll
+        for (int j = 0; j < R; ++j) {
+            if (r0 + j >= s.rows) break;
+            const V neg = both<V>(-mu[j]), vrs = both<V>(rs[j]), c1 = both<V>(-c[2 * j]), c2 = both<V>(-c[2 * j + 1]);
+            T* o = dx + (r0 + j) * s.d + c0;
+#pragma unroll
+            for (int q = 0; q < NP; ++q) {
+                if (c0 + q * step >= s.d) break;
+                V f[N], g[N];
+                opaque(px[j][q]);
+                opaque(py[j][q]);
+                widen(px[j][q], f);
+                widen(py[j][q], g);
+#pragma unroll
+                for (int i = 0; i < N; ++i)
+                    g[i] = mul_(vrs, fma_(mul_(add_(f[i], neg), vrs), c2, fma_(g[i], wv[q][i], c1)));
+                *reinterpret_cast<Pack<T, VEC>*>(o + q * step) = narrow<T, VEC>(g);
+            }
+        }
+    }
+    if (!part) return;
+    // the groups' sums one after another in shared memory, so that the order is the same every time
+    float* pw = part + (size_t)blockIdx.x * 2 * s.d;
+    for (int k = 0; k < s.groups; ++k) {
+        if (group == k) {
+            float* to = s.groups == 1 ? pw : sums;
+#pragma unroll
+            for (int q = 0; q < NP; ++q) {
+                if (c0 + q * step >= s.d) break;
+#pragma unroll
+                for (int i = 0; i < VEC; ++i) {
+                    const int c = c0 + q * step + i;
+                    const float* fw = reinterpret_cast<const float*>(&dw[q][0]);
+                    const float* fb = reinterpret_cast<const float*>(&db[q][0]);
+                    to[c] = k ? to[c] + fw[i] : fw[i];
+                    to[s.d + c] = k ? to[s.d + c] + fb[i] : fb[i];
+                }
+            }
+        }
+        if (s.groups > 1) __syncthreads();
+    }
+    if (s.groups > 1)
+        for (int c = threadIdx.x; c < 2 * s.d; c += blockDim.x) pw[c] = sums[c];
+}
+
+// dw (blockIdx.y 0) and db (1) from the CTAs' partial sums [parts][2][d].
 template <typename T>
 __global__ void __launch_bounds__(LN_RED_COLS* LN_RED_ROWS)
     ln_reduce_kernel(const float* part, int parts, int d, bool wf32, void* dw, void* db) {
@@ -246,15 +451,24 @@ __global__ void __launch_bounds__(LN_RED_COLS* LN_RED_ROWS)
     const int c = blockIdx.x * LN_RED_COLS + lane;
     void* out = blockIdx.y ? db : dw;
     float a = 0.f;
-    if (c < d)
-        for (int q = row; q < parts; q += LN_RED_ROWS) a += part[((size_t)q * 2 + blockIdx.y) * d + c];
+    if (c < d) {
+        const float* from = part + (size_t)blockIdx.y * d + c;
+        for (int q = row; q < parts; q += 8 * LN_RED_ROWS) {  // eight loads in flight
+            float v[8];
+#pragma unroll
+            for (int k = 0; k < 8; ++k) v[k] = q + k * LN_RED_ROWS < parts ? from[(size_t)(q + k * LN_RED_ROWS) * 2 * d] : 0.f;
+#pragma unroll
+            for (int k = 0; k < 8; ++k) a += v[k];
+        }
+    }
     acc[row][lane] = a;
     __syncthreads();
     if (row || c >= d || !out) return;
     a = 0.f;
+#pragma unroll
     for (int q = 0; q < LN_RED_ROWS; ++q) a += acc[q][lane];
     if (wf32) static_cast<float*>(out)[c] = a;
-    else static_cast<T*>(out)[c] = rounded<T>(a);
+    else put(static_cast<T*>(out)[c], a);
 }
 
 size_t dtype_size(int t) { return t == MOE_DTYPE_F32 ? 4 : 2; }
@@ -276,33 +490,23 @@ int check(const moe_layernorm_config* c) {
 // Widest piece (in values) that divides the rows and keeps every row's pieces aligned.
 int vector_width(const moe_layernorm_config& c, const void* a, const void* b, const void* e) {
     const size_t size = dtype_size(c.dtype);
-    for (int v = (int)(16 / size); v > 1; v /= 2)
+    for (int v = (int)(16 / size); v > 1; v = v > 2 ? 2 : 1)
         if (c.d % v == 0 && aligned(a, v * size) && aligned(b, v * size) && aligned(e, v * size)) return v;
     return 1;
 }
 
-LnShape shape_of(const moe_layernorm_config& c, int vec, int threads) {
+// Groups of `warps` warps in CTAs of about `threads` threads.
+LnShape shape_of(const moe_layernorm_config& c, int warps, int threads) {
     LnShape s;
     s.rows = c.rows;
     s.d = c.d;
     s.eps = c.eps;
     s.inv_d = 1.0f / (float)c.d;
-    // 16 or 32 values a thread, in whole pieces: np pieces of vec values each
-    const int values = c.d > LN_WIDE ? 32 : 16;
-    const int np = values / vec, pieces = (c.d + vec - 1) / vec;
-    int tpr = (pieces + np - 1) / np;
-    if (tpr <= 32) {
-        int p2 = 1;
-        while (p2 < tpr) p2 *= 2;
-        tpr = p2;
-    } else {
-        tpr = (tpr + 31) / 32 * 32;
-    }
-    s.tpr = tpr;
-    s.groups = tpr < threads ? threads / tpr : 1;
-    if (tpr > 32 && s.groups > 8) s.groups = 8;
+    s.warps = warps;
+    s.groups = warps * 32 < threads ? threads / (warps * 32) : 1;
     return s;
 }
+int warps_for(int d, int values) { return (d + 32 * values - 1) / (32 * values); }
 
 int check_device(DeviceInfo* di) {
     const int rc = device_info(di);
@@ -310,44 +514,28 @@ int check_device(DeviceInfo* di) {
     return di->supported ? MOE_OK : fail(MOE_ERR_DEVICE, "current device is not sm_103 (GB300)");
 }
 
-// f(Pack<T, VEC>, E) for the config's type, piece width and values a thread.
-template <int N>
-struct Int {
-    static constexpr int value = N;
-};
-template <typename E, typename F>
-cudaError_t dispatch_type(int dtype, int vec, E n, F f) {
-    if (dtype == MOE_DTYPE_F32) {
-        if (vec == 4) return f(Pack<float, 4>(), n);
-        if (vec == 2) return f(Pack<float, 2>(), n);
-        return f(Pack<float, 1>(), n);
-    }
-    if (dtype == MOE_DTYPE_BF16) {
-        if (vec == 8) return f(Pack<__nv_bfloat16, 8>(), n);
-        if (vec == 4) return f(Pack<__nv_bfloat16, 4>(), n);
-        if (vec == 2) return f(Pack<__nv_bfloat16, 2>(), n);
-        return f(Pack<__nv_bfloat16, 1>(), n);
-    }
-    if (vec == 8) return f(Pack<__half, 8>(), n);
-    if (vec == 4) return f(Pack<__half, 4>(), n);
-    if (vec == 2) return f(Pack<__half, 2>(), n);
-    return f(Pack<__half, 1>(), n);
-}
-
+// f(Pack<T, VEC>) for the config's type and piece width.
 template <typename F>
-cudaError_t dispatch(const moe_layernorm_config& c, int vec, F f) {
-    return c.d > LN_WIDE ? dispatch_type(c.dtype, vec, Int<32>(), f) : dispatch_type(c.dtype, vec, Int<16>(), f);
+cudaError_t dispatch(int dtype, int vec, F f) {
+    if (dtype == MOE_DTYPE_F32)
+        return vec == 4 ? f(Pack<float, 4>()) : vec == 2 ? f(Pack<float, 2>()) : f(Pack<float, 1>());
+    if (dtype == MOE_DTYPE_BF16)
+        return vec == 8   ? f(Pack<__nv_bfloat16, 8>())
+               : vec == 2 ? f(Pack<__nv_bfloat16, 2>())
+                          : f(Pack<__nv_bfloat16, 1>());
+    return vec == 8 ? f(Pack<__half, 8>()) : vec == 2 ? f(Pack<__half, 2>()) : f(Pack<__half, 1>());
 }
 
-int64_t ctas_for(const LnShape& s, int64_t most) {
-    const int64_t n = (s.rows + s.groups - 1) / s.groups;
+// Backward: columns a thread keeps, and with them the warps of a row and the CTAs of the launch.
+int backward_values(int d) { return d <= 2048 ? 8 : d <= 8192 ? 16 : 32; }
+LnShape backward_shape(const moe_layernorm_config& c) {
+    return shape_of(c, warps_for(c.d, backward_values(c.d)), LN_BWD_THREADS);
+}
+int64_t backward_ctas(const moe_layernorm_config& c, int vec, int sms) {
+    const LnShape s = backward_shape(c);
+    const int rows = s.groups * bwd_rows(dtype_size(c.dtype), vec, backward_values(c.d));  // rows a CTA takes at a time
+    const int64_t n = (c.rows + rows - 1) / rows, most = (int64_t)sms * (s.warps * s.groups > 8 ? 1 : 2);
     return n < most ? n : most;
-}
-
-// CTAs of the backward launch: as many as the device holds at once.
-int backward_ctas(const LnShape& s, int sms) {
-    const int threads = s.tpr * s.groups;
-    return (int)ctas_for(s, (int64_t)sms * (threads > 512 ? 1 : 512 / threads < 1 ? 1 : 512 / threads));
 }
 constexpr int LN_MAX_SMS = 256;
 
@@ -371,16 +559,27 @@ MOE_API int moe_layernorm_forward(const moe_layernorm_config* c, const void* x, 
     DeviceInfo di;
     if ((rc = check_device(&di))) return rc;
     const int vec = vector_width(*c, x, y, y);
-    const LnShape s = shape_of(*c, vec, LN_THREADS);
-    const int threads = s.tpr * s.groups;
-    const int64_t ctas = ctas_for(s, (int64_t)di.sms * (1024 / threads < 1 ? 1 : 1024 / threads));
+    // values a thread holds: as few as 8 for short rows; a whole row a warp up to 64 registers; with few
+    // rows (less than two a SM) 32, so that more warps load at once
+    const int whole = vec == 8 ? 128 : 64;
+    const int values = c->d <= 256 ? 8 : (c->d <= 1024 || (c->rows < 2 * di.sms && c->d <= LN_FWD_THREADS * 32)) ? 32 : whole;
+    const LnShape s = shape_of(*c, warps_for(c->d, values), LN_FWD_THREADS);
+    const int64_t n = (c->rows + s.groups - 1) / s.groups, most = (int64_t)di.sms * 64;
+    const dim3 grid((unsigned)(n < most ? n : most)), block(32 * s.warps * s.groups);
     cudaStream_t st = static_cast<cudaStream_t>(stream);
-    const cudaError_t err = dispatch(*c, vec, [&](auto pk, auto n) {
+    const cudaError_t err = dispatch(c->dtype, vec, [&](auto pk) {
         typedef decltype(pk) P;
         typedef std::remove_reference_t<decltype(pk.v[0])> T;
-        constexpr int V = (int)(sizeof(P) / sizeof(T)), E = decltype(n)::value;
-        return launch_k(ln_forward_kernel<T, V, E>, dim3((unsigned)ctas), dim3(threads), 0, st, true, s,
-                        static_cast<const T*>(x), w, b, c->wdtype == MOE_DTYPE_F32, static_cast<T*>(y), mean, rstd);
+        constexpr int V = (int)(sizeof(P) / sizeof(T)), WHOLE = V == 8 ? 128 : 64;
+        const bool wf32 = c->wdtype == MOE_DTYPE_F32, whole_pieces = w && b && aligned(w, 16) && aligned(b, 16);
+        const int form = !whole_pieces || (wf32 && V < 4) ? LN_W_ANY : wf32 ? LN_W_F32 : LN_W_SAME;
+        auto go = [&](auto kernel) {
+            return launch_k(kernel, grid, block, 0, st, true, s, static_cast<const T*>(x), w, b, wf32, form,
+                            static_cast<T*>(y), mean, rstd);
+        };
+        return values == 8    ? go(ln_forward_kernel<T, V, 8>)
+               : values == 32 ? go(ln_forward_kernel<T, V, 32>)
+                              : go(ln_forward_kernel<T, V, WHOLE>);
     });
     return err == cudaSuccess ? MOE_OK : cuda_fail(err, "layer norm launch");
 }
@@ -390,11 +589,8 @@ MOE_API int moe_layernorm_workspace_size(const moe_layernorm_config* c, size_t* 
     const int rc = check(c);
     if (rc) return rc;
     if (!bytes) return fail(MOE_ERR_ARG, "bytes is NULL");
-    // a backward launch's CTAs are largest for the narrowest pieces' fewest threads: 512 threads an
-    // SM of at least 64, on the largest device, and never more than the rows
-    const int64_t most = (int64_t)LN_MAX_SMS * 8;
-    const int64_t n = c->rows < most ? c->rows : most;
-    *bytes = (size_t)(n < 1 ? 1 : n) * 2 * c->d * 4;
+    *bytes = (size_t)backward_ctas(*c, 1, LN_MAX_SMS) * 2 * c->d * 4;
+    if (*bytes == 0) *bytes = 8;
     return MOE_OK;
 }
 
@@ -421,8 +617,8 @@ MOE_API int moe_layernorm_backward(const moe_layernorm_config* c, const void* dy
         return fail(MOE_ERR_ARG, "a pointer is not aligned to its type");
     if ((rc = check_device(&di))) return rc;
     const int vec = vector_width(*c, dy, x, dx);
-    const LnShape s = shape_of(*c, vec, LN_THREADS);
-    const int ctas = backward_ctas(s, di.sms);
+    const LnShape s = backward_shape(*c);
+    const int ctas = (int)backward_ctas(*c, vec, di.sms);
     float* part = nullptr;
     if (dw || db) {
         const size_t need = (size_t)ctas * 2 * c->d * 4;
@@ -432,13 +628,20 @@ MOE_API int moe_layernorm_backward(const moe_layernorm_config* c, const void* dy
         part = static_cast<float*>(ws);
     }
     const bool wf32 = c->wdtype == MOE_DTYPE_F32;
-    const cudaError_t err = dispatch(*c, vec, [&](auto pk, auto n) {
+    const int values = backward_values(c->d);
+    const size_t smem = s.groups > 1 ? (size_t)2 * c->d * 4 : 0;  // at most 2 x 1024 values
+    const cudaError_t err = dispatch(c->dtype, vec, [&](auto pk) {
         typedef decltype(pk) P;
         typedef std::remove_reference_t<decltype(pk.v[0])> T;
-        constexpr int V = (int)(sizeof(P) / sizeof(T)), E = decltype(n)::value;
-        cudaError_t e1 = launch_k(ln_backward_kernel<T, V, E>, dim3(ctas), dim3(s.tpr * s.groups), 0, st, true, s,
-                                  static_cast<const T*>(dy), static_cast<const T*>(x), w, wf32, mean, rstd,
-                                  static_cast<T*>(dx), part);
+        constexpr int V = (int)(sizeof(P) / sizeof(T));
+        auto go = [&](auto kernel) {
+            return launch_k(kernel, dim3(ctas), dim3(32 * s.warps * s.groups), smem, st, true, s,
+                            static_cast<const T*>(dy), static_cast<const T*>(x), w, wf32, mean, rstd,
+                            static_cast<T*>(dx), part);
+        };
+        const cudaError_t e1 = values == 8    ? go(ln_backward_kernel<T, V, 8>)
+                               : values == 16 ? go(ln_backward_kernel<T, V, 16>)
+                                              : go(ln_backward_kernel<T, V, 32>);
         if (e1 != cudaSuccess || !part) return e1;
         return launch_k(ln_reduce_kernel<T>, dim3((c->d + LN_RED_COLS - 1) / LN_RED_COLS, 2),
                         dim3(LN_RED_COLS * LN_RED_ROWS), 0, st, true, (const float*)part, ctas, c->d, wf32, dw, db);
