@@ -287,6 +287,14 @@ __global__ void __launch_bounds__(LN_FWD_THREADS, 2)
     }
 }
 
+template <int BYTES>
+__device__ __forceinline__ void copy_async(void* to, const void* from) {
+    if constexpr (BYTES == 16)
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(to)), "l"(from) : "memory");
+    else if constexpr (BYTES >= 4)
+        asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(smem_u32(to)), "l"(from), "n"(BYTES) : "memory");
+}
+
 // Sums of K values (a power of two up to 32) over a warp: lane l gets the total of value l / (32 / K).
 template <int K>
 __device__ __forceinline__ float warp_sums(float (&v)[K], int lane) {
@@ -311,18 +319,20 @@ __host__ __device__ constexpr int bwd_rows(size_t size, int vec, int nv) {
 }
 
 // R rows at a time, NV columns a thread.
-template <typename T, int VEC, int NV>
+template <typename T, int VEC, int NV, int SLOTS>
 __global__ void __launch_bounds__(NV > 8 ? 512 : 256, NV > 8 ? 1 : 2)
     ln_backward_kernel(LnShape s, const T* dy, const T* x, const void* w, bool wf32, const float* mean,
                        const float* rstd, T* dx, float* part) {
     typedef typename Lanes<VEC>::V V;
     constexpr int NP = NV / VEC, N = Lanes<VEC>::N, R = bwd_rows(sizeof(T), VEC, NV);
     __shared__ float red[2][16 * 2 * R];
-    extern __shared__ float sums[];  // [2][d]: the CTA's partial sums
+    extern __shared__ __align__(16) uint8_t ln_smem[];
+    float* const sums = reinterpret_cast<float*>(ln_smem);  // at the end, [2][d]: the CTA's partial sums
     griddep_wait();
     griddep_launch();
     const int tpr = s.warps * 32, t = threadIdx.x % tpr, group = threadIdx.x / tpr, lane = threadIdx.x & 31;
     const int step = tpr * VEC, c0 = t * VEC;
+    const int np = c0 < s.d ? min(NP, (s.d - c0 + step - 1) / step) : 0;
     V wv[NP][N], dw[NP][N], db[NP][N];
 #pragma unroll
     for (int q = 0; q < NP; ++q) {
@@ -330,47 +340,90 @@ __global__ void __launch_bounds__(NV > 8 ? 512 : 256, NV > 8 ? 1 : 2)
         for (int i = 0; i < N; ++i) wv[q][i] = dw[q][i] = db[q][i] = both<V>(0.f);
         if (c0 + q * step < s.d) weights<T, VEC, LN_W_ANY>(w, wf32, 1.f, c0 + q * step, wv[q]);
     }
-    int flip = 0;
-    // a group takes R consecutive rows; rows past the end read as zero and are not stored
-    for (int64_t r0 = ((int64_t)blockIdx.x * s.groups + group) * R; r0 < s.rows;
-         r0 += (int64_t)gridDim.x * s.groups * R) {
-        Pack<T, VEC> px[R][NP], py[R][NP];
-        float mu[R], rs[R];
+    // Pieces travel through SLOTS slots of shared memory by cp.async, a batch of rows a slot. A thread
+    // copies the pieces that it reads itself, so no barrier guards the slots; 2-byte pieces are loaded
+    // directly. Groups take R consecutive rows at a time; rows past the end are left out.
+    constexpr bool ASYNC = sizeof(Pack<T, VEC>) >= 4;
+    Pack<T, VEC>* const slot = reinterpret_cast<Pack<T, VEC>*>(ln_smem) + threadIdx.x;
+    const int64_t first = ((int64_t)blockIdx.x * s.groups + group) * R, stride = (int64_t)gridDim.x * s.groups * R;
+    const int slot_pieces = 2 * R * NP * blockDim.x;
+    auto issue = [&](int64_t r0, int stage) {
+        if (ASYNC && r0 < s.rows) {
+            Pack<T, VEC>* to = slot + stage * slot_pieces;
+            const T *fx = x + r0 * s.d + c0, *fy = dy + r0 * s.d + c0;
 #pragma unroll
-        for (int j = 0; j < R; ++j) {
-            const bool on = r0 + j < s.rows;
-            const int64_t at = (r0 + j) * s.d + c0;
-            mu[j] = on ? mean[r0 + j] : 0.f;
-            rs[j] = on ? rstd[r0 + j] : 0.f;
+            for (int j = 0; j < R; ++j) {
+                if (r0 + j >= s.rows) break;
 #pragma unroll
-            for (int q = 0; q < NP; ++q) {
-                if (on && c0 + q * step < s.d) {
-                    px[j][q] = *reinterpret_cast<const Pack<T, VEC>*>(x + at + q * step);
-                    py[j][q] = *reinterpret_cast<const Pack<T, VEC>*>(dy + at + q * step);
-                } else {
-                    memset(&px[j][q], 0, sizeof(px[j][q]));
-                    memset(&py[j][q], 0, sizeof(py[j][q]));
+                for (int q = 0; q < NP; ++q) {
+                    if (q >= np) break;
+                    copy_async<sizeof(Pack<T, VEC>)>(to + (2 * (j * NP + q)) * blockDim.x, fx + (j * s.d + q * step));
+                    copy_async<sizeof(Pack<T, VEC>)>(to + (2 * (j * NP + q) + 1) * blockDim.x, fy + (j * s.d + q * step));
                 }
             }
         }
+        if (ASYNC) asm volatile("cp.async.commit_group;" ::: "memory");
+    };
+    float mu[R], rs[R], nmu[R], nrs[R];
+    auto stats = [&](int64_t r0) {
+#pragma unroll
+        for (int j = 0; j < R; ++j) {
+            nmu[j] = r0 + j < s.rows ? mean[r0 + j] : 0.f;
+            nrs[j] = r0 + j < s.rows ? rstd[r0 + j] : 0.f;
+        }
+    };
+    int flip = 0, stage = 0;
+    for (int k = 0; k < SLOTS - 1; ++k) issue(first + k * stride, k);
+    stats(first);
+    for (int64_t r0 = first; r0 < s.rows; r0 += stride) {
+        issue(r0 + (SLOTS - 1) * stride, stage == 0 ? SLOTS - 1 : stage - 1);
+#pragma unroll
+        for (int j = 0; j < R; ++j) {
+            mu[j] = nmu[j];
+            rs[j] = nrs[j];
+        }
+        stats(r0 + stride);
+        const int rows = s.rows - r0 < R ? (int)(s.rows - r0) : R;
+        const int64_t at = r0 * s.d + c0;
+        Pack<T, VEC> px[R][NP], py[R][NP];
+        if (ASYNC) asm volatile("cp.async.wait_group %0;" ::"n"(SLOTS - 1) : "memory");
+#pragma unroll
+        for (int j = 0; j < R; ++j) {
+#pragma unroll
+            for (int q = 0; q < NP; ++q) {
+                memset(&px[j][q], 0, sizeof(px[j][q]));
+                memset(&py[j][q], 0, sizeof(py[j][q]));
+                if (j < rows && q < np) {
+                    if (ASYNC) {
+                        px[j][q] = slot[stage * slot_pieces + (2 * (j * NP + q)) * blockDim.x];
+                        py[j][q] = slot[stage * slot_pieces + (2 * (j * NP + q) + 1) * blockDim.x];
+                    } else {
+                        px[j][q] = *reinterpret_cast<const Pack<T, VEC>*>(x + at + (j * s.d + q * step));
+                        py[j][q] = *reinterpret_cast<const Pack<T, VEC>*>(dy + at + (j * s.d + q * step));
+                    }
+                }
+            }
+        }
+        if (++stage == SLOTS) stage = 0;
         float v[2 * R];
+        V xh[R][NP][N], g[R][NP][N];
 #pragma unroll
         for (int j = 0; j < R; ++j) {
             const V neg = both<V>(-mu[j]), vrs = both<V>(rs[j]);
             V a = both<V>(0.f), b = both<V>(0.f);
 #pragma unroll
             for (int q = 0; q < NP; ++q) {
-                V f[N], g[N];
-                widen(px[j][q], f);
-                widen(py[j][q], g);
+                widen(px[j][q], xh[j][q]);
+                widen(py[j][q], g[j][q]);
 #pragma unroll
                 for (int i = 0; i < N; ++i) {
-                    f[i] = mul_(add_(f[i], neg), vrs);
-                    dw[q][i] = fma_(g[i], f[i], dw[q][i]);
-                    db[q][i] = add_(db[q][i], g[i]);
-                    g[i] = mul_(g[i], wv[q][i]);
-                    a = add_(a, g[i]);
-                    b = fma_(g[i], f[i], b);
+                    V &h = xh[j][q][i], &e = g[j][q][i];
+                    h = mul_(add_(h, neg), vrs);
+                    dw[q][i] = fma_(e, h, dw[q][i]);
+                    db[q][i] = add_(db[q][i], e);
+                    e = mul_(e, wv[q][i]);
+                    a = add_(a, e);
+                    b = fma_(e, h, b);
                 }
             }
             v[2 * j] = total(a);
@@ -397,26 +450,21 @@ __global__ void __launch_bounds__(NV > 8 ? 512 : 256, NV > 8 ? 1 : 2)
         }
 #pragma unroll
         for (int j = 0; j < R; ++j) {
-            if (r0 + j >= s.rows) break;
-            const V neg = both<V>(-mu[j]), vrs = both<V>(rs[j]), c1 = both<V>(-c[2 * j]), c2 = both<V>(-c[2 * j + 1]);
-            T* o = dx + (r0 + j) * s.d + c0;
+            if (j >= rows) break;
+            const V vrs = both<V>(rs[j]), c1 = both<V>(-c[2 * j]), c2 = both<V>(-c[2 * j + 1]);
 #pragma unroll
             for (int q = 0; q < NP; ++q) {
-                if (c0 + q * step >= s.d) break;
-                V f[N], g[N];
-                opaque(px[j][q]);
-                opaque(py[j][q]);
-                widen(px[j][q], f);
-                widen(py[j][q], g);
+                if (q >= np) break;
+                V o[N];
 #pragma unroll
-                for (int i = 0; i < N; ++i)
-                    g[i] = mul_(vrs, fma_(mul_(add_(f[i], neg), vrs), c2, fma_(g[i], wv[q][i], c1)));
-                *reinterpret_cast<Pack<T, VEC>*>(o + q * step) = narrow<T, VEC>(g);
+                for (int i = 0; i < N; ++i) o[i] = mul_(vrs, fma_(xh[j][q][i], c2, add_(g[j][q][i], c1)));
+                *reinterpret_cast<Pack<T, VEC>*>(dx + at + (j * s.d + q * step)) = narrow<T, VEC>(o);
             }
         }
     }
     if (!part) return;
     // the groups' sums one after another in shared memory, so that the order is the same every time
+    if (s.groups > 1) __syncthreads();
     float* pw = part + (size_t)blockIdx.x * 2 * s.d;
     for (int k = 0; k < s.groups; ++k) {
         if (group == k) {
@@ -629,19 +677,25 @@ MOE_API int moe_layernorm_backward(const moe_layernorm_config* c, const void* dy
     }
     const bool wf32 = c->wdtype == MOE_DTYPE_F32;
     const int values = backward_values(c->d);
-    const size_t smem = s.groups > 1 ? (size_t)2 * c->d * 4 : 0;  // at most 2 x 1024 values
     const cudaError_t err = dispatch(c->dtype, vec, [&](auto pk) {
         typedef decltype(pk) P;
         typedef std::remove_reference_t<decltype(pk.v[0])> T;
         constexpr int V = (int)(sizeof(P) / sizeof(T));
-        auto go = [&](auto kernel) {
-            return launch_k(kernel, dim3(ctas), dim3(32 * s.warps * s.groups), smem, st, true, s,
-                            static_cast<const T*>(dy), static_cast<const T*>(x), w, wf32, mean, rstd,
-                            static_cast<T*>(dx), part);
+        auto go = [&](auto kernel, int stages) {
+            const int threads = 32 * s.warps * s.groups;
+            size_t smem = sizeof(P) < 4 ? 0 : (size_t)stages * 2 * bwd_rows(sizeof(T), V, values) * (values / V) * threads * sizeof(P);
+            if (s.groups > 1 && smem < (size_t)2 * c->d * 4) smem = (size_t)2 * c->d * 4;
+            const cudaError_t e0 = cudaFuncSetAttribute(reinterpret_cast<const void*>(kernel),
+                                                        cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+            if (e0 != cudaSuccess) return e0;
+            return launch_k(kernel, dim3(ctas), dim3(threads), smem, st, true, s, static_cast<const T*>(dy),
+                            static_cast<const T*>(x), w, wf32, mean, rstd, static_cast<T*>(dx), part);
         };
-        const cudaError_t e1 = values == 8    ? go(ln_backward_kernel<T, V, 8>)
-                               : values == 16 ? go(ln_backward_kernel<T, V, 16>)
-                                              : go(ln_backward_kernel<T, V, 32>);
+        // 96 KB of slots and two CTAs a SM up to 2048 columns, 192 KB for one CTA above
+        constexpr int WIDE = sizeof(T) == 4 ? 1 : 3;
+        const cudaError_t e1 = values == 8    ? go(ln_backward_kernel<T, V, 8, 3>, 3)
+                               : values == 16 ? go(ln_backward_kernel<T, V, 16, 3>, 3)
+                                              : go(ln_backward_kernel<T, V, 32, WIDE>, WIDE);
         if (e1 != cudaSuccess || !part) return e1;
         return launch_k(ln_reduce_kernel<T>, dim3((c->d + LN_RED_COLS - 1) / LN_RED_COLS, 2),
                         dim3(LN_RED_COLS * LN_RED_ROWS), 0, st, true, (const float*)part, ctas, c->d, wf32, dw, db);
