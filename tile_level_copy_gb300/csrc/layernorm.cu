@@ -345,65 +345,78 @@ __global__ void __launch_bounds__(NV > 8 ? 512 : 256, NV > 8 ? 1 : 2)
     // directly. Groups take R consecutive rows at a time; rows past the end are left out.
     constexpr bool ASYNC = sizeof(Pack<T, VEC>) >= 4;
     Pack<T, VEC>* const slot = reinterpret_cast<Pack<T, VEC>*>(ln_smem) + threadIdx.x;
+    const int threads = blockDim.x, slot_pieces = 2 * R * NP * threads;
     const int64_t first = ((int64_t)blockIdx.x * s.groups + group) * R, stride = (int64_t)gridDim.x * s.groups * R;
-    const int slot_pieces = 2 * R * NP * blockDim.x;
-    auto issue = [&](int64_t r0, int stage) {
-        if (ASYNC && r0 < s.rows) {
-            Pack<T, VEC>* to = slot + stage * slot_pieces;
-            const T *fx = x + r0 * s.d + c0, *fy = dy + r0 * s.d + c0;
+    const int64_t hop = stride * s.d;
+    const T *ax = x + first * s.d + c0, *ay = dy + first * s.d + c0;  // of the batch to be issued next
+    int64_t ar = first;
+    auto issue_rows = [&](int stage, auto rows) {
+        Pack<T, VEC>* to = slot + stage * slot_pieces;
 #pragma unroll
-            for (int j = 0; j < R; ++j) {
-                if (r0 + j >= s.rows) break;
+        for (int j = 0; j < R; ++j) {
+            if (j >= rows) break;
 #pragma unroll
-                for (int q = 0; q < NP; ++q) {
-                    if (q >= np) break;
-                    copy_async<sizeof(Pack<T, VEC>)>(to + (2 * (j * NP + q)) * blockDim.x, fx + (j * s.d + q * step));
-                    copy_async<sizeof(Pack<T, VEC>)>(to + (2 * (j * NP + q) + 1) * blockDim.x, fy + (j * s.d + q * step));
-                }
+            for (int q = 0; q < NP; ++q) {
+                if (q >= np) break;
+                const int o = j * s.d + q * step;
+                copy_async<sizeof(Pack<T, VEC>)>(to + 2 * (j * NP + q) * threads, ax + o);
+                copy_async<sizeof(Pack<T, VEC>)>(to + (2 * (j * NP + q) + 1) * threads, ay + o);
             }
         }
-        if (ASYNC) asm volatile("cp.async.commit_group;" ::: "memory");
     };
-    float mu[R], rs[R], nmu[R], nrs[R];
+    auto issue = [&](int stage) {
+        if (!ASYNC) return;
+        if (ar + R <= s.rows) issue_rows(stage, R);
+        else if (ar < s.rows) issue_rows(stage, (int)(s.rows - ar));
+        asm volatile("cp.async.commit_group;" ::: "memory");
+        ar += stride;
+        ax += hop;
+        ay += hop;
+    };
+    // the batch's statistics: lane j holds row j's mean, lane R + j its rstd
     auto stats = [&](int64_t r0) {
-#pragma unroll
-        for (int j = 0; j < R; ++j) {
-            nmu[j] = r0 + j < s.rows ? mean[r0 + j] : 0.f;
-            nrs[j] = r0 + j < s.rows ? rstd[r0 + j] : 0.f;
-        }
+        const int j = lane % R;
+        return lane < 2 * R && r0 + j < s.rows ? (lane < R ? mean : rstd)[r0 + j] : 0.f;
     };
     int flip = 0, stage = 0;
-    for (int k = 0; k < SLOTS - 1; ++k) issue(first + k * stride, k);
-    stats(first);
+    for (int k = 0; k < SLOTS - 1; ++k) issue(k);
+    float next = stats(first);
     for (int64_t r0 = first; r0 < s.rows; r0 += stride) {
-        issue(r0 + (SLOTS - 1) * stride, stage == 0 ? SLOTS - 1 : stage - 1);
+        issue(stage == 0 ? SLOTS - 1 : stage - 1);
+        float mu[R], rs[R];
 #pragma unroll
         for (int j = 0; j < R; ++j) {
-            mu[j] = nmu[j];
-            rs[j] = nrs[j];
+            mu[j] = __shfl_sync(0xffffffffu, next, j);
+            rs[j] = __shfl_sync(0xffffffffu, next, R + j);
         }
-        stats(r0 + stride);
+        next = stats(r0 + stride);
         const int rows = s.rows - r0 < R ? (int)(s.rows - r0) : R;
         const int64_t at = r0 * s.d + c0;
         Pack<T, VEC> px[R][NP], py[R][NP];
         if (ASYNC) asm volatile("cp.async.wait_group %0;" ::"n"(SLOTS - 1) : "memory");
+        const Pack<T, VEC>* from = slot + stage * slot_pieces;
+        auto take = [&](int rows, int np) {
 #pragma unroll
-        for (int j = 0; j < R; ++j) {
+            for (int j = 0; j < R; ++j) {
 #pragma unroll
-            for (int q = 0; q < NP; ++q) {
-                memset(&px[j][q], 0, sizeof(px[j][q]));
-                memset(&py[j][q], 0, sizeof(py[j][q]));
-                if (j < rows && q < np) {
-                    if (ASYNC) {
-                        px[j][q] = slot[stage * slot_pieces + (2 * (j * NP + q)) * blockDim.x];
-                        py[j][q] = slot[stage * slot_pieces + (2 * (j * NP + q) + 1) * blockDim.x];
+                for (int q = 0; q < NP; ++q) {
+                    if (j < rows && q < np) {
+                        if (ASYNC) {
+                            px[j][q] = from[2 * (j * NP + q) * threads];
+                            py[j][q] = from[(2 * (j * NP + q) + 1) * threads];
+                        } else {
+                            px[j][q] = *reinterpret_cast<const Pack<T, VEC>*>(x + at + (j * s.d + q * step));
+                            py[j][q] = *reinterpret_cast<const Pack<T, VEC>*>(dy + at + (j * s.d + q * step));
+                        }
                     } else {
-                        px[j][q] = *reinterpret_cast<const Pack<T, VEC>*>(x + at + (j * s.d + q * step));
-                        py[j][q] = *reinterpret_cast<const Pack<T, VEC>*>(dy + at + (j * s.d + q * step));
+                        memset(&px[j][q], 0, sizeof(px[j][q]));
+                        memset(&py[j][q], 0, sizeof(py[j][q]));
                     }
                 }
             }
-        }
+        };
+        if (rows == R && np == NP) take(R, NP);
+        else take(rows, np);
         if (++stage == SLOTS) stage = 0;
         float v[2 * R];
         V xh[R][NP][N], g[R][NP][N];
@@ -448,19 +461,24 @@ __global__ void __launch_bounds__(NV > 8 ? 512 : 256, NV > 8 ? 1 : 2)
 #pragma unroll
             for (int i = 0; i < 2 * R; ++i) c[i] = __shfl_sync(0xffffffffu, a, i * S) * s.inv_d;
         }
+        T* out = dx + at;
+        auto give = [&](int rows, int np) {
 #pragma unroll
-        for (int j = 0; j < R; ++j) {
-            if (j >= rows) break;
-            const V vrs = both<V>(rs[j]), c1 = both<V>(-c[2 * j]), c2 = both<V>(-c[2 * j + 1]);
+            for (int j = 0; j < R; ++j) {
+                if (j >= rows) break;
+                const V vrs = both<V>(rs[j]), c1 = both<V>(-c[2 * j]), c2 = both<V>(-c[2 * j + 1]);
 #pragma unroll
-            for (int q = 0; q < NP; ++q) {
-                if (q >= np) break;
-                V o[N];
+                for (int q = 0; q < NP; ++q) {
+                    if (q >= np) break;
+                    V o[N];
 #pragma unroll
-                for (int i = 0; i < N; ++i) o[i] = mul_(vrs, fma_(xh[j][q][i], c2, add_(g[j][q][i], c1)));
-                *reinterpret_cast<Pack<T, VEC>*>(dx + at + (j * s.d + q * step)) = narrow<T, VEC>(o);
+                    for (int i = 0; i < N; ++i) o[i] = mul_(vrs, fma_(xh[j][q][i], c2, add_(g[j][q][i], c1)));
+                    *reinterpret_cast<Pack<T, VEC>*>(out + (j * s.d + q * step)) = narrow<T, VEC>(o);
+                }
             }
-        }
+        };
+        if (rows == R && np == NP) give(R, NP);
+        else give(rows, np);
     }
     if (!part) return;
     // the groups' sums one after another in shared memory, so that the order is the same every time
