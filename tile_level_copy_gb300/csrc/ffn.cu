@@ -426,6 +426,239 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(GEMM_THREADS, 1)
     cluster_sync();
 }
 
+// ---- few tokens or few tiles: flex_kernel ----------------------------------------------------------
+//
+// One CTA computes 128 features by NT tokens (NT a multiple of 16 up to 128) of a product in which the
+// features come from a weight matrix: the weights are the UMMA's A operand (128 rows), the tokens its B
+// operand (N = NT), so few tokens waste no tensor-core rows and every byte of the weights is read once.
+// The k-blocks of a tile are split over a cluster of S CTAs, whose partial sums meet in shared memory:
+// CTA r of the cluster adds up and finishes the r-th part of the tokens, in CTA order. That puts
+// enough CTAs on the weights to read them at the memory's rate when there are few tiles.
+// A launch that follows another of the same call (`early`) starts loading weights before it waits for
+// the previous kernel: that kernel does not write them, and whatever came before it had finished when it let
+// this launch begin (it waits for its predecessor before it triggers its dependants).
+struct FxArgs {
+    CUtensorMap a[2], b[2];
+    int M, T;             // features, tokens
+    int kb0, kb;          // k-blocks of operand pair 0, of both (FF_SWIGLU: a[0] and a[1] side by side)
+    int a_mn, nt, splits, tiles_t;
+    int stages, early;
+    __nv_bfloat16 *out0, *out1;  // [T][M]
+    float2* gu;                  // kept g and u, [T][M]
+    int32_t* status;
+    unsigned long long timeout_ns;
+};
+constexpr int FX_MAX_STAGES = 8;
+constexpr int FX_A = 128 * BK * 2;  // bytes of a stage's 128 weight rows
+__host__ __device__ inline int fx_stage_bytes(bool dual, int nt) { return (dual ? 2 : 1) * FX_A + nt * BK * 2; }
+
+// One value (or pair of values) of the result: feature f of token t.
+template <int MODE>
+__device__ __forceinline__ void fx_finish(const FxArgs& p, int t, int f, float v, float w, float2 kept) {
+    const size_t at = (size_t)t * p.M + f;
+    if (MODE == FF_SWIGLU) {
+        p.out0[at] = __float2bfloat16_rn(v * ff_sigmoid(v) * w);
+        if (p.gu) p.gu[at] = make_float2(v, w);
+    } else if (MODE == FF_DACT) {
+        const float s = ff_sigmoid(kept.x);
+        p.out0[at] = __float2bfloat16_rn(v * kept.y * (s * (1.0f + kept.x * (1.0f - s))));
+        p.out1[at] = __float2bfloat16_rn(v * (kept.x * s));
+    } else {
+        p.out0[at] = __float2bfloat16_rn(v);
+    }
+}
+
+__device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];\n\t"
+        "tcgen05.wait::ld.sync.aligned;"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+          "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+        : "r"(taddr)
+        : "memory");
+}
+__device__ __forceinline__ void st_cluster_f32(uint32_t cluster_addr, float v) {
+    asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(cluster_addr), "f"(v) : "memory");
+}
+
+template <int MODE>
+__global__ void __launch_bounds__(GEMM_THREADS, 1) flex_kernel(const __grid_constant__ FxArgs p) {
+    constexpr bool DUAL = MODE == FF_SWIGLU;
+    extern __shared__ uint8_t smem_raw[];
+    __shared__ uint64_t full[FX_MAX_STAGES], empty[FX_MAX_STAGES], done;
+    __shared__ uint32_t tmem_base;
+    __shared__ volatile int abort_word;
+    uint8_t* const ring = smem_raw + (((smem_u32(smem_raw) + 1023u) & ~1023u) - smem_u32(smem_raw));
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int S = p.splits, split = S > 1 ? (int)cluster_ctarank() : 0;
+    const int tile = (int)blockIdx.x / S, mt = tile / p.tiles_t, tt = tile - mt * p.tiles_t;
+    const int f0 = mt * 128, t0 = tt * p.nt;
+    const int k0 = (int)((int64_t)p.kb * split / S), nkb = (int)((int64_t)p.kb * (split + 1) / S) - k0;
+    const int stage_bytes = fx_stage_bytes(DUAL, p.nt);
+    const unsigned long long tmo = p.timeout_ns;
+    uint32_t cols = 32;
+    while (cols < (uint32_t)(DUAL ? 2 * p.nt : p.nt)) cols *= 2;
+    if (tid == 0) {
+        for (int i = 0; i < p.stages; ++i) {
+            mbar_init(&full[i], 1);
+            mbar_init(&empty[i], 1);
+        }
+        mbar_init(&done, 1);
+        abort_word = 0;
+        mbar_fence_init();
+    }
+    if (warp == 1) {
+        tmem_alloc(&tmem_base, cols);
+        tmem_relinquish();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = tmem_base;
+    bool ok = true;
+
+    if (warp == 0) {
+        if (lane == 0) {
+            auto weights = [&](int i) {
+                const int kb = k0 + i, second = kb >= p.kb0 ? 1 : 0, k = (kb - (second ? p.kb0 : 0)) * BK;
+                uint8_t* a = ring + (i % p.stages) * stage_bytes;
+                uint64_t* bar = &full[i % p.stages];
+                mbar_arrive_expect_tx(bar, stage_bytes);
+                ff_load<false>(a, &p.a[second], bar, 0u, p.a_mn, f0, k);
+                if (DUAL) ff_load<false>(a + FX_A, &p.a[1], bar, 0u, p.a_mn, f0, k);
+            };
+            auto tokens = [&](int i) {
+                const int kb = k0 + i, second = kb >= p.kb0 ? 1 : 0, k = (kb - (second ? p.kb0 : 0)) * BK;
+                uint8_t* b = ring + (i % p.stages) * stage_bytes + (DUAL ? 2 : 1) * FX_A;
+                tma_load_2d(b, &p.b[second], &full[i % p.stages], k, t0);
+            };
+            const int head = nkb < p.stages ? nkb : p.stages;
+            if (p.early)
+                for (int i = 0; i < head; ++i) weights(i);
+            griddep_wait();
+            griddep_launch();
+            int issued = 0;
+            for (; issued < head; ++issued) {
+                if (!p.early) weights(issued);
+                tokens(issued);
+            }
+            for (; issued < nkb; ++issued) {
+                if (!mbar_wait(&empty[issued % p.stages], ((uint32_t)(issued / p.stages) & 1u) ^ 1u, tmo, &abort_word)) {
+                    ok = false;
+                    break;
+                }
+                weights(issued);
+                tokens(issued);
+            }
+            if (!ok) {
+                if (!abort_word) ff_status(p.status, 20);
+                abort_word = 1;
+            }
+            // no load is in flight when the CTA leaves: each stage's last phase has completed
+            int never = 0;
+            for (int i = issued > p.stages ? issued - p.stages : 0; i < issued; ++i)
+                if (!mbar_wait(&full[i % p.stages], (uint32_t)(i / p.stages) & 1u, tmo, &never)) ff_status(p.status, 21);
+        }
+    } else if (warp == 1) {
+        griddep_wait();
+        griddep_launch();
+        if (lane == 0) {
+            const uint32_t idesc = umma_idesc_bf16(128, p.nt) | ((uint32_t)p.a_mn << 15);
+            const uint32_t astep = p.a_mn ? 128 : 2;
+            for (int i = 0; i < nkb; ++i) {
+                const int st = i % p.stages;
+                if (!mbar_wait(&full[st], (uint32_t)(i / p.stages) & 1u, tmo, &abort_word)) {
+                    if (!abort_word) ff_status(p.status, 22);
+                    abort_word = 1;
+                    break;
+                }
+                tc_fence_after();
+                const uint32_t a = smem_u32(ring + st * stage_bytes), b = a + (DUAL ? 2 : 1) * FX_A;
+                const uint64_t ad = ff_sdesc(a, p.a_mn), ud = ff_sdesc(a + FX_A, p.a_mn), bd = sdesc_sw128(b);
+#pragma unroll
+                for (int kk = 0; kk < BK / 16; ++kk) {
+                    umma_bf16(tmem, ad + astep * kk, bd + 2 * kk, idesc, (i | kk) != 0);
+                    if (DUAL) umma_bf16(tmem + p.nt, ud + astep * kk, bd + 2 * kk, idesc, (i | kk) != 0);
+                }
+                umma_commit(&empty[st]);
+            }
+            umma_commit(&done);  // fires when every UMMA issued has completed
+            int never = 0;
+            if (!mbar_wait(&done, 0, tmo, &never)) {
+                ff_status(p.status, 23);
+                abort_word = 1;
+            }
+        }
+        __syncwarp();
+    } else {
+        griddep_wait();
+        griddep_launch();
+    }
+    // every role has ended: all loads landed, all products done
+    __syncthreads();
+    tc_fence_after();
+    if (S > 1) cluster_sync();  // in every CTA of the tile: the rings are free for the partial sums
+    const int q = warp & 3, f = f0 + q * 32 + lane;
+    const bool dead = abort_word != 0;
+    float* const parts = reinterpret_cast<float*>(ring);  // [split][value][own token][128]
+    const int own = p.nt / S;                              // tokens this CTA finishes
+    constexpr int VALS = DUAL ? 2 : 1;
+    if (warp >= 2) {
+        const uint32_t tb = tmem + ((uint32_t)(q * 32) << 16);
+        for (int c = 0; c < p.nt; c += 16) {
+            if (t0 + c >= p.T) break;  // no tokens from here on
+            uint32_t v[16], w[16];
+            tmem_ld16(tb + c, v);
+            if (DUAL) tmem_ld16(tb + p.nt + c, w);
+            if (S > 1) {
+#pragma unroll
+                for (int j = 0; j < 16; ++j) {
+                    const int to = (c + j) / own, i = c + j - to * own;
+                    const uint32_t at = smem_u32(parts + ((split * VALS) * own + i) * 128 + q * 32 + lane);
+                    const uint32_t peer = mapa_shared(at, (uint32_t)to);
+                    st_cluster_f32(peer, nkb ? __uint_as_float(v[j]) : 0.f);
+                    if (DUAL) st_cluster_f32(peer + own * 512u, nkb ? __uint_as_float(w[j]) : 0.f);
+                }
+            } else if (!dead && f < p.M) {
+                float2 kept[16];
+                if (MODE == FF_DACT) {
+#pragma unroll
+                    for (int j = 0; j < 16; ++j)
+                        kept[j] = t0 + c + j < p.T ? p.gu[(size_t)(t0 + c + j) * p.M + f] : make_float2(0.f, 0.f);
+                }
+#pragma unroll
+                for (int j = 0; j < 16; ++j)
+                    if (t0 + c + j < p.T)
+                        fx_finish<MODE>(p, t0 + c + j, f, __uint_as_float(v[j]), DUAL ? __uint_as_float(w[j]) : 0.f, kept[j]);
+            }
+        }
+    }
+    tc_fence_before();
+    if (S > 1) {
+        cluster_sync();  // every partial sum has arrived
+        if (warp >= 2 && !dead && f < p.M) {
+            for (int i = 0; i < own; ++i) {
+                const int t = t0 + split * own + i;
+                if (t >= p.T) break;
+                float2 kept = make_float2(0.f, 0.f);
+                if (MODE == FF_DACT) kept = p.gu[(size_t)t * p.M + f];
+                float v = 0.f, w = 0.f;
+                for (int r = 0; r < S; ++r) {
+                    v += parts[((r * VALS) * own + i) * 128 + q * 32 + lane];
+                    if (DUAL) w += parts[((r * VALS + 1) * own + i) * 128 + q * 32 + lane];
+                }
+                fx_finish<MODE>(p, t, f, v, w, kept);
+            }
+        }
+    }
+    __syncthreads();
+    if (warp == 1) {
+        tc_fence_after();
+        tmem_dealloc(tmem, cols);
+    }
+}
+
 // ---- host side -----------------------------------------------------------------------------------
 
 struct FfLayout {
@@ -456,7 +689,7 @@ int ff_layout(const moe_ffn_config* c, FfLayout* o) {
     L.gu_cols = (int)((L.F + 31) / 32);
     L.saved_h = 0;
     L.saved_gu = hidden;
-    L.saved_bytes = hidden + (L.T + 31) / 32 * L.gu_cols * 8192;
+    L.saved_bytes = hidden + (L.T + 31) / 32 * L.gu_cols * 8192;  // at least T F pairs, the flex layout
     L.timeout_ns = (unsigned long long)(c->timeout_us ? c->timeout_us : 2000000u) * 1000ull;
     *o = L;
     return MOE_OK;
@@ -555,7 +788,93 @@ int ff_run(FfList& list, const FfLayout& L, void* ws, cudaStream_t st, const cha
     return e == cudaSuccess ? MOE_OK : cuda_fail(e, what);
 }
 
-int ff_begin(const moe_ffn_config* c, void* ws, size_t ws_bytes, FfLayout* L) {
+// How a product runs: on dense_kernel (nt = 0) or on flex_kernel with these numbers.
+struct FxPlan {
+    int nt, splits, stages;
+    float us;  // the estimate it was chosen by
+};
+
+// Estimated time of a product out[T][M] over kb k-blocks on either kernel; the smaller one runs. Per SM
+// and k-block: a dense pair tile (256 x 256) keeps the tensor cores busy for 512 cycles; a flex tile
+// takes VALS x 4 UMMAs of max(nt / 2, 32 + nt / 4) cycles (tensor cores, or the shared memory that
+// feeds them 128 x 16 weights and nt x 16 tokens), and its stage's bytes come at about 64 a cycle.
+FxPlan ff_choose_flex(int M, int T, int kb, bool dual, int sms) {
+    constexpr float GHZ = 1.9f;
+    FxPlan best{0, 1, 0, 1e30f};
+    const float hbm = (float)M * kb * BK * 2 * (dual ? 2 : 1) / 6.5e6f;
+    for (int nt = 16; nt <= 128; nt += nt < 64 ? 16 : 32) {
+        if (nt > 16 && nt - (nt <= 64 ? 16 : 32) >= T) break;  // a narrower tile holds every token
+        const int stage = fx_stage_bytes(dual, nt), tiles = ((M + 127) / 128) * ((T + nt - 1) / nt);
+        const int room = 108 * 1024 / stage >= 3 ? 108 * 1024 : 216 * 1024;  // two CTAs a SM, or one
+        const int stages = room / stage < FX_MAX_STAGES ? room / stage : FX_MAX_STAGES;
+        for (int S = 1; S <= 8; S *= 2) {
+            if (S > kb || nt % S || (S > 1 && (dual ? 2 : 1) * nt * 512 > stages * stage)) continue;
+            const int load = (tiles * S + sms - 1) / sms, mine = (kb + S - 1) / S;
+            const float mma = load * mine * (dual ? 2 : 1) * 4 * (nt / 2 > 32 + nt / 4 ? nt / 2 : 32 + nt / 4) / (GHZ * 1e3f);
+            const float bytes = load * (float)mine * stage / (64 * GHZ * 1e3f);
+            float us = mma > bytes ? mma : bytes;
+            if (us < hbm) us = hbm;
+            us += 3.0f + (S > 1 ? 1.5f : 0.0f) + nt * 0.02f;
+            if (us < best.us) best = FxPlan{nt, S, stages, us};
+        }
+    }
+    return best;
+}
+
+FxPlan ff_choose(int M, int T, int kb, bool dual, int sms) {
+    const int tiles = ((T + FT_M - 1) / FT_M) * ((M + (dual ? 127 : FT_N - 1)) / (dual ? 128 : FT_N)), pairs = sms / 2;
+    const FxPlan flex = ff_choose_flex(M, T, kb, dual, sms);
+    const float dense = ((tiles + pairs - 1) / pairs) * kb * 512.0f / 1.9e3f + 5.0f;
+    return flex.us < dense ? flex : FxPlan{0, 1, 0, dense};
+}
+
+template <int MODE>
+int fx_run(FxArgs& p, const FxPlan& plan, const FfLayout& L, void* ws, cudaStream_t st, const char* what) {
+    p.nt = plan.nt;
+    p.splits = plan.splits;
+    p.stages = plan.stages;
+    p.tiles_t = (p.T + p.nt - 1) / p.nt;
+    p.status = static_cast<int32_t*>(ws);
+    p.timeout_ns = L.timeout_ns;
+    const size_t smem = (size_t)p.stages * fx_stage_bytes(MODE == FF_SWIGLU, p.nt) + 1024;
+    const void* fn = reinterpret_cast<const void*>(&flex_kernel<MODE>);
+    cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    if (e != cudaSuccess) return cuda_fail(e, what);
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)((p.M + 127) / 128 * p.tiles_t * p.splits));
+    cfg.blockDim = dim3(GEMM_THREADS);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = st;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim = {(unsigned)p.splits, 1, 1};
+    cfg.attrs = attr;
+    cfg.numAttrs = p.splits > 1 ? 2 : 1;
+    e = cudaLaunchKernelEx(&cfg, flex_kernel<MODE>, p);
+    return e == cudaSuccess ? MOE_OK : cuda_fail(e, what);
+}
+// Weights [M, K] (K-major, or stored [K, M]) and tokens [T, K] of operand pair i.
+int fx_operands(FxArgs& p, int i, const void* w, int a_mn, const void* x, size_t M, size_t T, size_t K, int nt) {
+    p.a_mn = a_mn;
+    const int rc = ff_operand(&p.a[i], w, M, K, a_mn);
+    return rc ? rc : ff_map(&p.b[i], x, T, K, (uint32_t)nt, false);
+}
+FxArgs fx_args(size_t M, size_t T, int kb0, int kb, void* out, int early) {
+    FxArgs p;
+    p.M = (int)M;
+    p.T = (int)T;
+    p.kb0 = kb0;
+    p.kb = kb;
+    p.out0 = static_cast<__nv_bfloat16*>(out);
+    p.out1 = nullptr;
+    p.gu = nullptr;
+    p.early = early;
+    return p;
+}
+
+int ff_begin(const moe_ffn_config* c, void* ws, size_t ws_bytes, FfLayout* L, int* sms) {
     clear_error();
     int rc = ff_layout(c, L);
     if (rc) return rc;
@@ -564,6 +883,7 @@ int ff_begin(const moe_ffn_config* c, void* ws, size_t ws_bytes, FfLayout* L) {
     if (ws_bytes < L->ws_bytes) return fail(MOE_ERR_WORKSPACE, "workspace has %zu bytes, needs %zu", ws_bytes, L->ws_bytes);
     DeviceInfo di;
     if ((rc = device_info(&di))) return rc;
+    *sms = di.sms;
     return di.supported ? MOE_OK : fail(MOE_ERR_DEVICE, "current device is not sm_103 (GB300)");
 }
 
@@ -597,7 +917,7 @@ MOE_API int moe_ffn_saved_size(const moe_ffn_config* c, size_t* bytes) {
 MOE_API int moe_ffn_forward(const moe_ffn_config* c, const uint16_t* x, const uint16_t* W1, const uint16_t* W3,
                             const uint16_t* W2, uint16_t* y, void* saved, void* ws, size_t ws_bytes, void* stream) {
     FfLayout L;
-    int rc = ff_begin(c, ws, ws_bytes, &L);
+    int sms = 0, rc = ff_begin(c, ws, ws_bytes, &L, &sms);
     if (rc) return rc;
     if (L.T == 0) return MOE_OK;
     if (!x || !W1 || !W3 || !W2 || !y) return fail(MOE_ERR_ARG, "NULL input or output pointer");
@@ -607,14 +927,33 @@ MOE_API int moe_ffn_forward(const moe_ffn_config* c, const uint16_t* x, const ui
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     uint8_t* s = static_cast<uint8_t*>(saved);
     uint8_t* h = s ? s + L.saved_h : static_cast<uint8_t*>(ws) + L.h;
-    FfList up;
-    FfProblem& p = up.add(x, 0, W1, 0, h, L.T, L.F, L.d);
-    up.try_(ff_operand(&p.b[1], W3, L.F, L.d, 0));
-    p.tiles_n = (int)((L.F + 127) / 128);  // 128 columns of g beside 128 of u
-    up.l.tiles = p.tiles_m * p.tiles_n;
-    up.l.gu = s ? reinterpret_cast<float*>(s + L.saved_gu) : nullptr;
-    up.l.gu_cols = L.gu_cols;
-    if ((rc = ff_run<FF_SWIGLU>(up, L, ws, st, "gate and up projections"))) return rc;
+    // g, u and h; the backward pass's hidden gradients have the same shape and take the same kernel, which
+    // fixes the layout in which g and u are kept
+    const int kd = (int)((L.d + BK - 1) / BK), kf = (int)((L.F + BK - 1) / BK);
+    float* gu = s ? reinterpret_cast<float*>(s + L.saved_gu) : nullptr;
+    const FxPlan up_plan = ff_choose((int)L.F, (int)L.T, kd, true, sms);
+    if (up_plan.nt) {
+        FxArgs p = fx_args(L.F, L.T, kd, kd, h, 0);
+        p.gu = reinterpret_cast<float2*>(gu);
+        if ((rc = fx_operands(p, 0, W1, 0, x, L.F, L.T, L.d, up_plan.nt))) return rc;
+        if ((rc = fx_operands(p, 1, W3, 0, x, L.F, L.T, L.d, up_plan.nt))) return rc;
+        if ((rc = fx_run<FF_SWIGLU>(p, up_plan, L, ws, st, "gate and up projections"))) return rc;
+    } else {
+        FfList up;
+        FfProblem& p = up.add(x, 0, W1, 0, h, L.T, L.F, L.d);
+        up.try_(ff_operand(&p.b[1], W3, L.F, L.d, 0));
+        p.tiles_n = (int)((L.F + 127) / 128);  // 128 columns of g beside 128 of u
+        up.l.tiles = p.tiles_m * p.tiles_n;
+        up.l.gu = gu;
+        up.l.gu_cols = L.gu_cols;
+        if ((rc = ff_run<FF_SWIGLU>(up, L, ws, st, "gate and up projections"))) return rc;
+    }
+    const FxPlan down_plan = ff_choose((int)L.d, (int)L.T, kf, false, sms);
+    if (down_plan.nt) {
+        FxArgs p = fx_args(L.d, L.T, kf, kf, y, 1);
+        if ((rc = fx_operands(p, 0, W2, 0, h, L.d, L.T, L.F, down_plan.nt))) return rc;
+        return fx_run<FF_PLAIN>(p, down_plan, L, ws, st, "down projection");
+    }
     FfList down;
     down.add(h, 0, W2, 0, y, L.T, L.d, L.F);
     return ff_run<FF_PLAIN>(down, L, ws, st, "down projection");
@@ -624,7 +963,7 @@ MOE_API int moe_ffn_backward(const moe_ffn_config* c, const uint16_t* x, const u
                              const uint16_t* W2, const uint16_t* dy, const void* saved, uint16_t* dx, uint16_t* dW1,
                              uint16_t* dW3, uint16_t* dW2, void* ws, size_t ws_bytes, void* stream) {
     FfLayout L;
-    int rc = ff_begin(c, ws, ws_bytes, &L);
+    int sms = 0, rc = ff_begin(c, ws, ws_bytes, &L, &sms);
     if (rc) return rc;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     if (!dW1 || !dW3 || !dW2) return fail(MOE_ERR_ARG, "NULL weight gradient pointer");
@@ -645,14 +984,33 @@ MOE_API int moe_ffn_backward(const moe_ffn_config* c, const uint16_t* x, const u
     const uint8_t* h = s + L.saved_h;
     uint8_t* dg = static_cast<uint8_t*>(ws) + L.dg;
     uint8_t* du = static_cast<uint8_t*>(ws) + L.du;
-    FfList act;
-    FfProblem& p = act.add(dy, 0, W2, 1, dg, L.T, L.F, L.d);
-    act.try_(ff_map(&p.out[1], du, L.T, L.F, EPI_CHUNK, true));
-    act.l.gu = reinterpret_cast<float*>(const_cast<uint8_t*>(s) + L.saved_gu);
-    act.l.gu_cols = L.gu_cols;
-    if ((rc = ff_run<FF_DACT>(act, L, ws, st, "hidden gradients"))) return rc;
+    const int kd = (int)((L.d + BK - 1) / BK), kf = (int)((L.F + BK - 1) / BK);
+    float* gu = reinterpret_cast<float*>(const_cast<uint8_t*>(s) + L.saved_gu);
+    if (ff_choose((int)L.F, (int)L.T, kd, true, sms).nt) {  // the forward pass's choice
+        const FxPlan plan = ff_choose_flex((int)L.F, (int)L.T, kd, false, sms);
+        FxArgs p = fx_args(L.F, L.T, kd, kd, dg, 0);
+        p.out1 = reinterpret_cast<__nv_bfloat16*>(du);
+        p.gu = reinterpret_cast<float2*>(gu);
+        if ((rc = fx_operands(p, 0, W2, 1, dy, L.F, L.T, L.d, plan.nt))) return rc;
+        if ((rc = fx_run<FF_DACT>(p, plan, L, ws, st, "hidden gradients"))) return rc;
+    } else {
+        FfList act;
+        FfProblem& p = act.add(dy, 0, W2, 1, dg, L.T, L.F, L.d);
+        act.try_(ff_map(&p.out[1], du, L.T, L.F, EPI_CHUNK, true));
+        act.l.gu = gu;
+        act.l.gu_cols = L.gu_cols;
+        if ((rc = ff_run<FF_DACT>(act, L, ws, st, "hidden gradients"))) return rc;
+    }
     FfList grad;
-    grad.add(dg, 0, W1, 1, dx, L.T, L.d, L.F, du, W3);
+    const FxPlan dx_plan = ff_choose((int)L.d, (int)L.T, 2 * kf, false, sms);
+    if (dx_plan.nt) {
+        FxArgs p = fx_args(L.d, L.T, kf, 2 * kf, dx, 1);
+        if ((rc = fx_operands(p, 0, W1, 1, dg, L.d, L.T, L.F, dx_plan.nt))) return rc;
+        if ((rc = fx_operands(p, 1, W3, 1, du, L.d, L.T, L.F, dx_plan.nt))) return rc;
+        if ((rc = fx_run<FF_PLAIN>(p, dx_plan, L, ws, st, "input gradients"))) return rc;
+    } else {
+        grad.add(dg, 0, W1, 1, dx, L.T, L.d, L.F, du, W3);
+    }
     grad.add(dg, 1, x, 1, dW1, L.F, L.d, L.T);
     grad.add(du, 1, x, 1, dW3, L.F, L.d, L.T);
     grad.add(dy, 1, h, 1, dW2, L.d, L.F, L.T);
