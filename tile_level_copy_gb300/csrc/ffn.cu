@@ -17,6 +17,8 @@
 // again costs 4 T d ffn flops where keeping them costs 16 T ffn bytes of traffic (at d = 2048 and the
 // measured rates a quarter of that time, and hidden behind the products).
 // h, dg and du are rounded to bf16 because they are operands of the next product.
+#include <atomic>
+
 #include "host_internal.h"
 #include "moe_internal.cuh"
 
@@ -449,24 +451,40 @@ struct FxArgs {
     unsigned long long timeout_ns;
 };
 constexpr int FX_MAX_STAGES = 8;
+constexpr int FX_ROOM = 108 * 1024;  // a CTA's ring: two CTAs fit a SM
 constexpr int FX_A = 128 * BK * 2;  // bytes of a stage's 128 weight rows
 __host__ __device__ inline int fx_stage_bytes(bool dual, int nt) { return (dual ? 2 : 1) * FX_A + nt * BK * 2; }
 
-// One value (or pair of values) of the result: feature f of token t.
+// Where a thread's results go: its feature of some token, the next token M values on.
 template <int MODE>
-__device__ __forceinline__ void fx_finish(const FxArgs& p, int t, int f, float v, float w, float2 kept) {
-    const size_t at = (size_t)t * p.M + f;
-    if (MODE == FF_SWIGLU) {
-        p.out0[at] = __float2bfloat16_rn(v * ff_sigmoid(v) * w);
-        if (p.gu) p.gu[at] = make_float2(v, w);
-    } else if (MODE == FF_DACT) {
-        const float s = ff_sigmoid(kept.x);
-        p.out0[at] = __float2bfloat16_rn(v * kept.y * (s * (1.0f + kept.x * (1.0f - s))));
-        p.out1[at] = __float2bfloat16_rn(v * (kept.x * s));
-    } else {
-        p.out0[at] = __float2bfloat16_rn(v);
+struct FxOut {
+    __nv_bfloat16 *o0, *o1;
+    float2* gu;
+    int M;
+    __device__ __forceinline__ FxOut(const FxArgs& p, int t, int f) : M(p.M) {
+        const size_t at = (size_t)t * p.M + f;
+        o0 = p.out0 + at;
+        o1 = p.out1 + at;
+        gu = p.gu ? p.gu + at : nullptr;
     }
-}
+    __device__ __forceinline__ float2 kept(int j) const {
+        return MODE == FF_DACT ? gu[(size_t)j * M] : make_float2(0.f, 0.f);
+    }
+    // Token j on from the first: its value (and, for h, the second product's).
+    __device__ __forceinline__ void put(int j, float v, float w, float2 k) const {
+        const size_t at = (size_t)j * M;
+        if (MODE == FF_SWIGLU) {
+            o0[at] = __float2bfloat16_rn(v * ff_sigmoid(v) * w);
+            if (gu) gu[at] = make_float2(v, w);
+        } else if (MODE == FF_DACT) {
+            const float s = ff_sigmoid(k.x);
+            o0[at] = __float2bfloat16_rn(v * k.y * (s * (1.0f + k.x * (1.0f - s))));
+            o1[at] = __float2bfloat16_rn(v * (k.x * s));
+        } else {
+            o0[at] = __float2bfloat16_rn(v);
+        }
+    }
+};
 
 __device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) {
     asm volatile(
@@ -478,9 +496,24 @@ __device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) {
         : "r"(taddr)
         : "memory");
 }
-__device__ __forceinline__ void st_cluster_f32(uint32_t cluster_addr, float v) {
-    asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(cluster_addr), "f"(v) : "memory");
+// W (2 or 4) consecutive floats into a peer's shared memory / from our own.
+template <int W>
+__device__ __forceinline__ void st_cluster_vec(uint32_t cluster_addr, const uint32_t* v) {
+    if (W == 4)
+        asm volatile("st.shared::cluster.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(cluster_addr), "r"(v[0]), "r"(v[1]),
+                     "r"(v[2]), "r"(v[3])
+                     : "memory");
+    else
+        asm volatile("st.shared::cluster.v2.b32 [%0], {%1, %2};" ::"r"(cluster_addr), "r"(v[0]), "r"(v[1]) : "memory");
 }
+template <int N>
+struct FxInt {
+    static constexpr int value = N;
+};
+template <int W>
+struct alignas(4 * W) FxVec {
+    float v[W];
+};
 
 template <int MODE>
 __global__ void __launch_bounds__(GEMM_THREADS, 1) flex_kernel(const __grid_constant__ FxArgs p) {
@@ -601,57 +634,83 @@ __global__ void __launch_bounds__(GEMM_THREADS, 1) flex_kernel(const __grid_cons
     if (S > 1) cluster_sync();  // in every CTA of the tile: the rings are free for the partial sums
     const int q = warp & 3, f = f0 + q * 32 + lane;
     const bool dead = abort_word != 0;
-    float* const parts = reinterpret_cast<float*>(ring);  // [split][value][own token][128]
-    const int own = p.nt / S;                              // tokens this CTA finishes
+    const int own = p.nt / S;  // tokens this CTA finishes
     constexpr int VALS = DUAL ? 2 : 1;
-    if (warp >= 2) {
-        const uint32_t tb = tmem + ((uint32_t)(q * 32) << 16);
-        for (int c = 0; c < p.nt; c += 16) {
-            if (t0 + c >= p.T) break;  // no tokens from here on
-            uint32_t v[16], w[16];
-            tmem_ld16(tb + c, v);
-            if (DUAL) tmem_ld16(tb + p.nt + c, w);
-            if (S > 1) {
-#pragma unroll
-                for (int j = 0; j < 16; ++j) {
-                    const int to = (c + j) / own, i = c + j - to * own;
-                    const uint32_t at = smem_u32(parts + ((split * VALS) * own + i) * 128 + q * 32 + lane);
-                    const uint32_t peer = mapa_shared(at, (uint32_t)to);
-                    st_cluster_f32(peer, nkb ? __uint_as_float(v[j]) : 0.f);
-                    if (DUAL) st_cluster_f32(peer + own * 512u, nkb ? __uint_as_float(w[j]) : 0.f);
-                }
-            } else if (!dead && f < p.M) {
-                float2 kept[16];
-                if (MODE == FF_DACT) {
+    const uint32_t tb = tmem + ((uint32_t)(q * 32) << 16);
+    const int here = min(p.nt, p.T - t0);  // tokens of the tile
+    if (S == 1) {
+        if (warp >= 2) {
+            const FxOut<MODE> out(p, t0, f);
+            for (int c = 0; c < here; c += 16) {
+                uint32_t v[16], w[16];
+                __syncwarp();
+                tmem_ld16(tb + c, v);
+                if (DUAL) tmem_ld16(tb + p.nt + c, w);
+                if (dead || f >= p.M) continue;
+                auto finish = [&](int n) {
+                    float2 k[16];
 #pragma unroll
                     for (int j = 0; j < 16; ++j)
-                        kept[j] = t0 + c + j < p.T ? p.gu[(size_t)(t0 + c + j) * p.M + f] : make_float2(0.f, 0.f);
+                        if (j < n) k[j] = out.kept(c + j);
+#pragma unroll
+                    for (int j = 0; j < 16; ++j)
+                        if (j < n) out.put(c + j, __uint_as_float(v[j]), DUAL ? __uint_as_float(w[j]) : 0.f, k[j]);
+                };
+                if (here - c >= 16) finish(16);
+                else finish(here - c);
+            }
+        }
+    } else {
+        // partial sums in shared memory: [split][value][own token / W][128 features][W]
+        auto exchange = [&](auto width) {
+            constexpr int W = decltype(width)::value;
+            FxVec<W>* const parts = reinterpret_cast<FxVec<W>*>(ring);
+            const int row = q * 32 + lane, groups = own / W;
+            if (warp >= 2) {
+                for (int c = 0; c < here; c += 16) {
+                    uint32_t v[16], w[16];
+                    tmem_ld16(tb + c, v);
+                    if (DUAL) tmem_ld16(tb + p.nt + c, w);
+#pragma unroll
+                    for (int j = 0; j < 16; j += W) {
+                        const int to = (c + j) / own, i = (c + j - to * own) / W;
+                        const uint32_t at = smem_u32(parts + ((split * VALS) * groups + i) * 128 + row);
+                        const uint32_t peer = mapa_shared(at, (uint32_t)to);
+                        st_cluster_vec<W>(peer, v + j);
+                        if (DUAL) st_cluster_vec<W>(peer + groups * 128 * 4 * W, w + j);
+                    }
+                }
+            }
+            tc_fence_before();
+            cluster_sync();  // every partial sum has arrived
+            const int mine = min(own, here - split * own);
+            if (warp < 2 || dead || f >= p.M || mine <= 0) return;
+            const FxOut<MODE> out(p, t0 + split * own, f);
+            for (int i = 0; i * W < mine; ++i) {
+                float2 k[W];
+                FxVec<W> v{}, w{};
+#pragma unroll
+                for (int j = 0; j < W; ++j)
+                    if (i * W + j < mine) k[j] = out.kept(i * W + j);
+                for (int r = 0; r < S; ++r) {
+                    const FxVec<W> a = parts[((r * VALS) * groups + i) * 128 + row];
+#pragma unroll
+                    for (int j = 0; j < W; ++j) v.v[j] += a.v[j];
+                    if (DUAL) {
+                        const FxVec<W> b = parts[((r * VALS + 1) * groups + i) * 128 + row];
+#pragma unroll
+                        for (int j = 0; j < W; ++j) w.v[j] += b.v[j];
+                    }
                 }
 #pragma unroll
-                for (int j = 0; j < 16; ++j)
-                    if (t0 + c + j < p.T)
-                        fx_finish<MODE>(p, t0 + c + j, f, __uint_as_float(v[j]), DUAL ? __uint_as_float(w[j]) : 0.f, kept[j]);
+                for (int j = 0; j < W; ++j)
+                    if (i * W + j < mine) out.put(i * W + j, v.v[j], w.v[j], k[j]);
             }
-        }
+        };
+        if (own % 4 == 0) exchange(FxInt<4>());
+        else exchange(FxInt<2>());
     }
     tc_fence_before();
-    if (S > 1) {
-        cluster_sync();  // every partial sum has arrived
-        if (warp >= 2 && !dead && f < p.M) {
-            for (int i = 0; i < own; ++i) {
-                const int t = t0 + split * own + i;
-                if (t >= p.T) break;
-                float2 kept = make_float2(0.f, 0.f);
-                if (MODE == FF_DACT) kept = p.gu[(size_t)t * p.M + f];
-                float v = 0.f, w = 0.f;
-                for (int r = 0; r < S; ++r) {
-                    v += parts[((r * VALS) * own + i) * 128 + q * 32 + lane];
-                    if (DUAL) w += parts[((r * VALS + 1) * own + i) * 128 + q * 32 + lane];
-                }
-                fx_finish<MODE>(p, t, f, v, w, kept);
-            }
-        }
-    }
     __syncthreads();
     if (warp == 1) {
         tc_fence_after();
@@ -805,8 +864,7 @@ FxPlan ff_choose_flex(int M, int T, int kb, bool dual, int sms) {
     for (int nt = 16; nt <= 128; nt += nt < 64 ? 16 : 32) {
         if (nt > 16 && nt - (nt <= 64 ? 16 : 32) >= T) break;  // a narrower tile holds every token
         const int stage = fx_stage_bytes(dual, nt), tiles = ((M + 127) / 128) * ((T + nt - 1) / nt);
-        const int room = 108 * 1024 / stage >= 3 ? 108 * 1024 : 216 * 1024;  // two CTAs a SM, or one
-        const int stages = room / stage < FX_MAX_STAGES ? room / stage : FX_MAX_STAGES;
+        const int stages = FX_ROOM / stage < FX_MAX_STAGES ? FX_ROOM / stage : FX_MAX_STAGES;
         for (int S = 1; S <= 8; S *= 2) {
             if (S > kb || nt % S || (S > 1 && (dual ? 2 : 1) * nt * 512 > stages * stage)) continue;
             const int load = (tiles * S + sms - 1) / sms, mine = (kb + S - 1) / S;
@@ -828,6 +886,21 @@ FxPlan ff_choose(int M, int T, int kb, bool dual, int sms) {
     return flex.us < dense ? flex : FxPlan{0, 1, 0, dense};
 }
 
+// Once per device: the kernel may take FX_ROOM of shared memory.
+template <int MODE>
+cudaError_t fx_prepare() {
+    static std::atomic<bool> done[64];
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+    if (done[dev].load(std::memory_order_relaxed)) return cudaSuccess;
+    e = cudaFuncSetAttribute(reinterpret_cast<const void*>(&flex_kernel<MODE>),
+                             cudaFuncAttributeMaxDynamicSharedMemorySize, FX_ROOM + 1024);
+    if (e == cudaSuccess) done[dev].store(true, std::memory_order_relaxed);
+    return e;
+}
+
 template <int MODE>
 int fx_run(FxArgs& p, const FxPlan& plan, const FfLayout& L, void* ws, cudaStream_t st, const char* what) {
     p.nt = plan.nt;
@@ -837,8 +910,7 @@ int fx_run(FxArgs& p, const FxPlan& plan, const FfLayout& L, void* ws, cudaStrea
     p.status = static_cast<int32_t*>(ws);
     p.timeout_ns = L.timeout_ns;
     const size_t smem = (size_t)p.stages * fx_stage_bytes(MODE == FF_SWIGLU, p.nt) + 1024;
-    const void* fn = reinterpret_cast<const void*>(&flex_kernel<MODE>);
-    cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    cudaError_t e = fx_prepare<MODE>();
     if (e != cudaSuccess) return cuda_fail(e, what);
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)((p.M + 127) / 128 * p.tiles_t * p.splits));
