@@ -440,7 +440,7 @@ typedef struct moe_ffn_config {
     int32_t reserved[4];
 } moe_ffn_config;
 
-#define MOE_FFN_STATUS_BYTES 256
+#define MOE_FFN_STATUS_BYTES 8192
 
 /* Bytes of the workspace of both passes, and of the buffer in which the forward pass keeps what the
  * backward pass needs (h in bf16, the two projections in fp32). Host arithmetic only. */
@@ -452,7 +452,7 @@ MOE_API int moe_ffn_saved_size(const moe_ffn_config* cfg, size_t* bytes);
  *   saved  device buffer of moe_ffn_saved_size bytes for a later moe_ffn_backward, or NULL
  *   ws     device workspace of ws_bytes >= moe_ffn_workspace_size(cfg)
  * saved and ws are 256-byte aligned; the first MOE_FFN_STATUS_BYTES of ws are zeroed by the caller once,
- * before its first call (the status words). h is rounded to bf16 once, as the operand of the second
+ * before its first call, and again after a MOE_ERR_TIMEOUT (status words and counts that are zero between calls). h is rounded to bf16 once, as the operand of the second
  * product; everything else stays fp32 until y is rounded. With saved NULL and few tokens the weights
  * are streamed once by kernels made for that (the form of single-token decoding); the sums then
  * run in another order, so y may differ in its last bit from the call with saved.

@@ -46,7 +46,7 @@ TRACE_UP_CYCLES, TRACE_UP_NS, TRACE_DOWN_CYCLES, TRACE_DOWN_NS = 8, 9, 10, 11
 # types of values, block of the 8-bit optimiser states, status bytes of a feed-forward workspace
 MOE_DTYPE_F32, MOE_DTYPE_BF16, MOE_DTYPE_F16 = 0, 1, 2
 MOE_ADAMW_BLOCK = 128
-MOE_FFN_STATUS_BYTES = 256
+MOE_FFN_STATUS_BYTES = 8192
 _DTYPES = {torch.float32: MOE_DTYPE_F32, torch.bfloat16: MOE_DTYPE_BF16, torch.float16: MOE_DTYPE_F16}
 
 # names of the C entry points (each declared in include/moe.h)

@@ -33,6 +33,7 @@ constexpr int FF_MISC = 1024;
 constexpr int FF_SMEM = FF_STAGES * FF_STAGE + EPI_BYTES + FF_MISC + 1024;
 static_assert(FF_SMEM <= 227 * 1024, "dense GEMM shared memory");
 constexpr int FF_PROBLEMS = 4;
+constexpr float FF_CUT_COST = 12.0f;  // k-blocks' time that a part of a cut tile costs beside its products
 
 enum FfMode : int { FF_PLAIN = 0, FF_SWIGLU = 1, FF_DACT = 2 };
 
@@ -46,6 +47,9 @@ struct FfProblem {
 struct FfLaunch {
     FfProblem p[FF_PROBLEMS];
     int count, tiles;
+    int full, parts, units;  // tiles from `full` on are cut into `parts` pieces of their k-blocks
+    float* partial;          // their partial sums, and
+    uint32_t* arrived;       // a count of the pieces done for each 32 rows of a cut tile (zero between calls)
     float* gu;         // kept g and u (FF_SWIGLU writes, may be null; FF_DACT reads)
     int gu_cols;       // 32-column blocks of a row of it
     int32_t* status;   // [2] first error of the calls on a workspace, and where
@@ -124,11 +128,19 @@ __device__ __forceinline__ void ff_load(uint8_t* dst, const CUtensorMap* m, uint
     }
 }
 
+// One unit of work: a tile, or one part of a cut tile (cut: its number among them, -1: none).
 struct FfTile {
     const FfProblem* p;
-    int m, n;
+    int m, n, k0, k1, cut, part;
 };
-__device__ __forceinline__ FfTile ff_tile(const FfLaunch& l, int t) {
+__device__ __forceinline__ FfTile ff_tile(const FfLaunch& l, int unit) {
+    int t = unit, part = 0, cut = -1;
+    if (unit >= l.full) {
+        const int v = unit - l.full;
+        cut = v / l.parts;
+        part = v - cut * l.parts;
+        t = l.full + cut;
+    }
     int i = 0;
     while (i + 1 < l.count && t >= l.p[i + 1].tile0) ++i;
     const FfProblem* p = &l.p[i];
@@ -136,7 +148,12 @@ __device__ __forceinline__ FfTile ff_tile(const FfLaunch& l, int t) {
     // M tiles in groups of 16, N tiles outer in a group: tiles that run together share operands in L2
     const int per = 16 * p->tiles_n, grp = q / per, first = grp * 16;
     const int rows = min(16, p->tiles_m - first), r = q - grp * per;
-    return FfTile{p, first + r % rows, r / rows};
+    FfTile o{p, first + r % rows, r / rows, 0, p->kb, cut, part};
+    if (cut >= 0) {
+        o.k0 = p->kb * part / l.parts;
+        o.k1 = p->kb * (part + 1) / l.parts;
+    }
+    return o;
 }
 
 // One epilogue warp's two staging chunks (32 rows x 32 columns of bf16), stored by TMA.
@@ -173,19 +190,79 @@ __device__ __forceinline__ float4* ff_gu(const FfLaunch& l, int row0, int col0, 
     return reinterpret_cast<float4*>(l.gu + (block * 2 + which) * 1024) + lane;
 }
 
+// Partial sums of a cut tile's part: for each 32 rows (slab = rank x 4 + warp) 8 chunks of 32 columns,
+// each [8 pieces of 4 columns][32 rows][4] fp32.
+__device__ __forceinline__ float4* ff_partial(const FfLaunch& l, int cut, int part, int slab, int lane) {
+    return reinterpret_cast<float4*>(l.partial + (((size_t)cut * l.parts + part) * 8 + slab) * 8192) + lane;
+}
+// A part of a cut tile: keeps this warp's sums and counts them as done. True for the part that comes
+// last, which then adds up all of them (in the order of the parts, its own from TMEM) and finishes the
+// rows. Nothing waits for another CTA.
+__device__ __forceinline__ bool ff_arrive(const FfLaunch& l, const FfTile& t, uint32_t tb, int slab, int lane) {
+    float4* o = ff_partial(l, t.cut, t.part, slab, lane);
+#pragma unroll 1
+    for (int c = 0; c < 8; ++c) {
+        uint32_t v[32];
+        tmem_ld32(tb + c * 32, v);
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            __stcg(o + c * 256 + i * 32, make_float4(__uint_as_float(v[4 * i]), __uint_as_float(v[4 * i + 1]),
+                                                     __uint_as_float(v[4 * i + 2]), __uint_as_float(v[4 * i + 3])));
+    }
+    __threadfence();
+    __syncwarp();
+    uint32_t before = 0;
+    if (lane == 0) {
+        uint32_t* count = l.arrived + t.cut * 8 + slab;
+        before = atom_acq_rel_gpu_add(count, 1u);
+        if (before + 1 == (uint32_t)l.parts) *count = 0;  // for the next launch
+    }
+    before = __shfl_sync(0xffffffffu, before, 0);
+    __threadfence();
+    return before + 1 == (uint32_t)l.parts;
+}
+// 32 columns of this warp's rows: the accumulator, or the sum over a cut tile's parts.
+__device__ __forceinline__ void ff_chunk(const FfLaunch& l, const FfTile& t, uint32_t tb, int c, int slab, int lane,
+                                         uint32_t (&v)[32]) {
+    tmem_ld32(tb + c * 32, v);
+    if (t.cut < 0) return;
+    float sum[32];
+#pragma unroll
+    for (int i = 0; i < 32; ++i) sum[i] = 0.f;
+    for (int q = 0; q < l.parts; ++q) {
+        if (q == t.part) {
+#pragma unroll
+            for (int i = 0; i < 32; ++i) sum[i] += __uint_as_float(v[i]);
+            continue;
+        }
+        const float4* o = ff_partial(l, t.cut, q, slab, lane) + c * 256;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const float4 a = __ldcg(o + i * 32);
+            sum[4 * i] += a.x;
+            sum[4 * i + 1] += a.y;
+            sum[4 * i + 2] += a.z;
+            sum[4 * i + 3] += a.w;
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < 32; ++i) v[i] = __float_as_uint(sum[i]);
+}
+
 template <int MODE>
 __device__ __forceinline__ void ff_epilogue(const FfLaunch& l, const FfTile& t, FfStage& es, uint32_t tb, int row0,
-                                            int lane) {
+                                            int slab, int lane) {
     const FfProblem& p = *t.p;
     if (row0 >= p.M) return;
+    if (t.cut >= 0 && !ff_arrive(l, t, tb, slab, lane)) return;
     if (MODE == FF_SWIGLU) {
 #pragma unroll 1
         for (int c = 0; c < 4; ++c) {
             const int col0 = t.n * 128 + c * 32;
             if (col0 >= p.N) return;
             uint32_t g[32], u[32];
-            tmem_ld32(tb + c * 32, g);
-            tmem_ld32(tb + 128 + c * 32, u);
+            ff_chunk(l, t, tb, c, slab, lane, g);
+            ff_chunk(l, t, tb, c + 4, slab, lane, u);
             uint32_t pk[16];
 #pragma unroll
             for (int i = 0; i < 16; ++i) {
@@ -218,7 +295,7 @@ __device__ __forceinline__ void ff_epilogue(const FfLaunch& l, const FfTile& t, 
                 u[i] = iu[i * 32];
             }
             uint32_t d[32];
-            tmem_ld32(tb + c * 32, d);
+            ff_chunk(l, t, tb, c, slab, lane, d);
             uint32_t pg[16], pu[16];
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
@@ -244,7 +321,7 @@ __device__ __forceinline__ void ff_epilogue(const FfLaunch& l, const FfTile& t, 
             const int col0 = t.n * FT_N + c * 32;
             if (col0 >= p.N) return;
             uint32_t v[32], pk[16];
-            tmem_ld32(tb + c * 32, v);
+            ff_chunk(l, t, tb, c, slab, lane, v);
 #pragma unroll
             for (int i = 0; i < 16; ++i) pk[i] = pack_bf16x2(__uint_as_float(v[2 * i]), __uint_as_float(v[2 * i + 1]));
             es.put(&p.out[0], pk, col0, row0, lane);
@@ -300,12 +377,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(GEMM_THREADS, 1)
         int st = 0;
         uint32_t ph = 0;
         bool ok = !bad;
-        for (int t = cluster; ok && t < l.tiles; t += clusters) {
+        for (int t = cluster; ok && t < l.units; t += clusters) {
             const FfTile tr = ff_tile(l, t);
             const FfProblem& p = *tr.p;
             const int arow = tr.m * FT_M + (int)rank * 128;
             const int brow = MODE == FF_SWIGLU ? tr.n * 128 : tr.n * FT_N + (int)rank * 128;
-            for (int kb = 0; kb < p.kb; ++kb) {
+            for (int kb = tr.k0; kb < tr.k1; ++kb) {
                 if (!mbar_wait(&sm.empty[st], ph ^ 1u, tmo, sm.abort)) {
                     ok = false;
                     break;
@@ -344,8 +421,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(GEMM_THREADS, 1)
         if (rank == 0) {
             int st = 0, b = 0;
             uint32_t ph = 0, aph = 0;
-            for (int t = cluster; ok && t < l.tiles; t += clusters) {
-                const FfProblem& p = *ff_tile(l, t).p;
+            for (int t = cluster; ok && t < l.units; t += clusters) {
+                const FfTile tr = ff_tile(l, t);
+                const FfProblem& p = *tr.p;
                 const uint32_t idesc = umma_idesc_bf16(FT_M, FT_N) | ((uint32_t)p.a_mn << 15) | ((uint32_t)p.b_mn << 16);
                 const uint32_t astep = p.a_mn ? 128 : 2, bstep = p.b_mn ? 128 : 2;  // 16 k, in 16 bytes
                 if (!mbar_wait_cluster(&sm.acc_empty[b], aph ^ 1u, tmo, sm.abort)) {
@@ -354,7 +432,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(GEMM_THREADS, 1)
                 }
                 tc_fence_after();
                 const uint32_t dt = tmem + (uint32_t)(b * 256);
-                for (int kb = 0; kb < p.kb; ++kb) {
+                for (int kb = tr.k0; kb < tr.k1; ++kb) {
                     if (!mbar_wait_cluster(&sm.full[st], ph, tmo, sm.abort)) {
                         ok = false;
                         break;
@@ -364,7 +442,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(GEMM_THREADS, 1)
                     const uint64_t ad = ff_sdesc(addr, p.a_mn), bd = ff_sdesc(addr + FF_HALF, p.b_mn);
 #pragma unroll
                     for (int kk = 0; kk < BK / 16; ++kk)
-                        umma_bf16_pair(dt, ad + astep * kk, bd + bstep * kk, idesc, (kb | kk) != 0);
+                        umma_bf16_pair(dt, ad + astep * kk, bd + bstep * kk, idesc, kb != tr.k0 || kk != 0);
                     umma_commit_pair(&sm.empty[st], 0x3);
                     if (++st == FF_STAGES) {
                         st = 0;
@@ -390,7 +468,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(GEMM_THREADS, 1)
         const uint32_t acc_empty0 = mapa_shared(smem_u32(sm.acc_empty), 0u);
         int b = 0;
         uint32_t aph = 0;
-        for (int t = cluster; !bad && t < l.tiles; t += clusters) {
+        for (int t = cluster; !bad && t < l.units; t += clusters) {
             const FfTile tr = ff_tile(l, t);
             if (!mbar_wait(&sm.acc_full[b], aph, tmo, sm.abort)) {
                 if (!*sm.abort) ff_status(l.status, 16 + (int)rank);
@@ -400,7 +478,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(GEMM_THREADS, 1)
             tc_fence_after();
             __syncwarp();
             const uint32_t tb = tmem + ((uint32_t)(q * 32) << 16) + (uint32_t)(b * 256);
-            ff_epilogue<MODE>(l, tr, es, tb, tr.m * FT_M + (int)rank * 128 + q * 32, lane);
+            ff_epilogue<MODE>(l, tr, es, tb, tr.m * FT_M + (int)rank * 128 + q * 32, (int)rank * 4 + q, lane);
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive_cluster(acc_empty0 + b * 8u);
@@ -720,9 +798,13 @@ __global__ void __launch_bounds__(GEMM_THREADS, 1) flex_kernel(const __grid_cons
 
 // ---- host side -----------------------------------------------------------------------------------
 
+// Parts of cut tiles in a launch, and words of the status area: [0] status, [1] detail, [128...] arrivals.
+constexpr int FF_MAX_CUT = 160, FF_ARRIVED = 128;
+static_assert((FF_ARRIVED + FF_MAX_CUT / 2 * 8) * 4 <= MOE_FFN_STATUS_BYTES, "arrival counts");
+
 struct FfLayout {
     size_t T, d, F;
-    size_t h, dg, du, ws_bytes;        // workspace: status words, then h (or dg), du
+    size_t h, dg, du, partial, ws_bytes;  // workspace: status words, then h (or dg), du, partial sums
     size_t saved_h, saved_gu, saved_bytes;
     int gu_cols;
     unsigned long long timeout_ns;
@@ -742,9 +824,14 @@ int ff_layout(const moe_ffn_config* c, FfLayout* o) {
     L.d = c->d;
     L.F = c->ffn;
     const size_t hidden = align_up(L.T * L.F * 2, 1024);
-    L.h = L.dg = 1024;
+    L.h = L.dg = MOE_FFN_STATUS_BYTES;
     L.du = L.dg + hidden;
-    L.ws_bytes = L.du + hidden;
+    L.partial = L.du + hidden;
+    // room for the parts of cut tiles: at most FF_MAX_CUT, and no more than 8 parts of every tile there is
+    auto tiles = [](size_t m, size_t n) { return (m + FT_M - 1) / FT_M * ((n + FT_N - 1) / FT_N); };
+    size_t parts = 8 * (tiles(L.T, 2 * L.F) + tiles(L.T, L.d) + 3 * tiles(L.F, L.d));
+    if (parts > FF_MAX_CUT) parts = FF_MAX_CUT;
+    L.ws_bytes = L.partial + parts * FT_M * FT_N * 4;
     L.gu_cols = (int)((L.F + 31) / 32);
     L.saved_h = 0;
     L.saved_gu = hidden;
@@ -807,6 +894,25 @@ struct FfList {
     }
 };
 
+// Tiles come in waves of one a cluster; the tiles of an incomplete last wave are cut along k into as many
+// parts as finish soonest: ceil(rest x parts / clusters) rounds of 1 / parts of a tile each, plus what
+// keeping and adding up a part costs.
+struct FfCut {
+    int full, parts;
+    float waves;  // of whole tiles, with that cost
+};
+FfCut ff_cut(int tiles, int kb, int clusters) {
+    const int full = tiles / clusters * clusters, rest = tiles - full;
+    FfCut best{tiles, 1, (float)(tiles / clusters + (rest ? 1 : 0))};
+    for (int parts = 2; rest && parts <= 8; ++parts) {
+        if (rest * parts > FF_MAX_CUT || rest > FF_MAX_CUT / 2 || parts * 4 > kb) break;
+        const int rounds = (rest * parts + clusters - 1) / clusters;
+        const float w = tiles / clusters + rounds * (1.0f / parts + FF_CUT_COST / kb);
+        if (w < best.waves) best = FfCut{full, parts, w};
+    }
+    return best;
+}
+
 // Co-resident CTA pairs of a kernel on the current device (cached per device).
 template <int MODE>
 cudaError_t ff_clusters(int* out) {
@@ -836,12 +942,21 @@ cudaError_t ff_clusters(int* out) {
 template <int MODE>
 int ff_run(FfList& list, const FfLayout& L, void* ws, cudaStream_t st, const char* what) {
     if (list.rc) return list.rc;
-    list.l.status = static_cast<int32_t*>(ws);
-    list.l.timeout_ns = L.timeout_ns;
+    FfLaunch& l = list.l;
+    l.status = static_cast<int32_t*>(ws);
+    l.timeout_ns = L.timeout_ns;
+    l.partial = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + L.partial);
+    l.arrived = static_cast<uint32_t*>(ws) + FF_ARRIVED;
     int clusters = 0;
     cudaError_t e = ff_clusters<MODE>(&clusters);
     if (e == cudaSuccess) {
-        const int n = list.l.tiles < clusters ? list.l.tiles : clusters;
+        int kb = 1 << 30;
+        for (int i = 0; i < l.count; ++i) kb = l.p[i].kb < kb ? l.p[i].kb : kb;
+        const FfCut cut = ff_cut(l.tiles, kb, clusters);
+        l.full = cut.full;
+        l.parts = cut.parts;
+        l.units = cut.full + (l.tiles - cut.full) * cut.parts;
+        const int n = l.units < clusters ? l.units : clusters;
         e = launch_k(dense_kernel<MODE>, dim3(2 * n), dim3(GEMM_THREADS), FF_SMEM, st, true, list.l);
     }
     return e == cudaSuccess ? MOE_OK : cuda_fail(e, what);
@@ -882,7 +997,7 @@ FxPlan ff_choose_flex(int M, int T, int kb, bool dual, int sms) {
 FxPlan ff_choose(int M, int T, int kb, bool dual, int sms) {
     const int tiles = ((T + FT_M - 1) / FT_M) * ((M + (dual ? 127 : FT_N - 1)) / (dual ? 128 : FT_N)), pairs = sms / 2;
     const FxPlan flex = ff_choose_flex(M, T, kb, dual, sms);
-    const float dense = ((tiles + pairs - 1) / pairs) * kb * 512.0f / 1.9e3f + 5.0f;
+    const float dense = ff_cut(tiles, kb, pairs).waves * kb * 512.0f / 1.9e3f + 5.0f;
     return flex.us < dense ? flex : FxPlan{0, 1, 0, dense};
 }
 
