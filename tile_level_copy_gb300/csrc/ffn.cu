@@ -33,9 +33,15 @@ constexpr int FF_MISC = 1024;
 constexpr int FF_SMEM = FF_STAGES * FF_STAGE + EPI_BYTES + FF_MISC + 1024;
 static_assert(FF_SMEM <= 227 * 1024, "dense GEMM shared memory");
 constexpr int FF_PROBLEMS = 4;
-constexpr float FF_CUT_COST = 12.0f;  // k-blocks' time that a part of a cut tile costs beside its products
+// k-blocks' time that a cut tile costs beside its products: keeping a part, and adding up each of the others
+constexpr float FF_CUT_KEEP = 6.0f, FF_CUT_ADD = 8.0f;
 
 enum FfMode : int { FF_PLAIN = 0, FF_SWIGLU = 1, FF_DACT = 2 };
+
+template <int N>
+struct FxInt {
+    static constexpr int value = N;
+};
 
 // One product out[M, N] = sum_k A B of a launch.
 struct FfProblem {
@@ -112,26 +118,77 @@ __device__ __forceinline__ uint64_t ff_sdesc(uint32_t addr, int mn) {
     if (mn) d = (d & ~(uint64_t(0x3FFF) << 16)) | (uint64_t((64 * BK * 2) >> 4) << 16);
     return d;
 }
-// One operand half (128 rows of M or N from `row`, k-block at `k`) into `dst`.
-template <bool PEER>
-__device__ __forceinline__ void ff_load(uint8_t* dst, const CUtensorMap* m, uint64_t* bar, uint32_t bar0, int mn,
-                                        int row, int k) {
-    if (!mn) {
+// One operand half (128 rows of M or N from `row`, k-block at `k`) into `dst`; PEER: the odd CTA of a
+// pair, whose loads complete on the even CTA's barrier (bar0). How the operands are stored is known at
+// compile time here and in the loops below: with run-time branches around the TMA and UMMA issue a
+// prompt's products took 10 % longer (930 against 840 us).
+template <bool MN, bool PEER>
+__device__ __forceinline__ void ff_load(uint8_t* dst, const CUtensorMap* m, uint64_t* bar, uint32_t bar0, int row, int k) {
+    if constexpr (!MN) {
         if (PEER) tma_load_2d_pair(dst, m, bar0, k, row);
         else tma_load_2d(dst, m, bar, k, row);
-        return;
-    }
+    } else {
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-        if (PEER) tma_load_2d_pair(dst + i * (FF_HALF / 2), m, bar0, row + 64 * i, k);
-        else tma_load_2d(dst + i * (FF_HALF / 2), m, bar, row + 64 * i, k);
+        for (int i = 0; i < 2; ++i) {
+            if (PEER) tma_load_2d_pair(dst + i * (FF_HALF / 2), m, bar0, row + 64 * i, k);
+            else tma_load_2d(dst + i * (FF_HALF / 2), m, bar, row + 64 * i, k);
+        }
     }
+}
+// Place in the ring of stages: stage, phase parity, k-blocks so far.
+struct FfRing {
+    int st = 0;
+    uint32_t ph = 0, done = 0;
+    __device__ __forceinline__ void next() {
+        ++done;
+        if (++st == FF_STAGES) {
+            st = 0;
+            ph ^= 1u;
+        }
+    }
+};
+// TMA thread: k-blocks [from, to) of one operand pair. False if a wait ran out.
+template <bool A_MN, bool B_MN, bool PEER>
+__device__ __forceinline__ bool ff_produce(const FfSmem& sm, FfRing& r, const CUtensorMap* ma, const CUtensorMap* mb,
+                                           int arow, int brow, int from, int to, unsigned long long tmo) {
+    for (int kb = from; kb < to; ++kb) {
+        if (!mbar_wait(&sm.empty[r.st], r.ph ^ 1u, tmo, sm.abort)) return false;
+        uint8_t* a = sm.stages + r.st * FF_STAGE;
+        uint64_t* full = &sm.full[r.st];
+        uint32_t full0 = 0;
+        if (PEER) full0 = mapa_shared(smem_u32(full), 0u);
+        else mbar_arrive_expect_tx(full, 2 * FF_STAGE);
+        ff_load<A_MN, PEER>(a, ma, full, full0, arow, kb * BK);
+        ff_load<B_MN, PEER>(a + FF_HALF, mb, full, full0, brow, kb * BK);
+        r.next();
+    }
+    return true;
+}
+// UMMA thread (even CTA): `count` k-blocks into the accumulator at dt. False if a wait ran out.
+template <bool A_MN, bool B_MN>
+__device__ __forceinline__ bool ff_multiply(const FfSmem& sm, FfRing& r, uint32_t dt, int count, unsigned long long tmo) {
+    constexpr uint32_t idesc = umma_idesc_bf16(FT_M, FT_N) | ((uint32_t)A_MN << 15) | ((uint32_t)B_MN << 16);
+    constexpr uint32_t astep = A_MN ? 128 : 2, bstep = B_MN ? 128 : 2;  // 16 k, in 16 bytes
+    for (int kb = 0; kb < count; ++kb) {
+        if (!mbar_wait_cluster(&sm.full[r.st], r.ph, tmo, sm.abort)) return false;
+        tc_fence_after();
+        const uint32_t addr = smem_u32(sm.stages + r.st * FF_STAGE);
+        const uint64_t ad = ff_sdesc(addr, A_MN), bd = ff_sdesc(addr + FF_HALF, B_MN);
+#pragma unroll
+        for (int kk = 0; kk < BK / 16; ++kk) umma_bf16_pair(dt, ad + astep * kk, bd + bstep * kk, idesc, (kb | kk) != 0);
+        umma_commit_pair(&sm.empty[r.st], 0x3);
+        r.next();
+    }
+    return true;
 }
 
 // One unit of work: a tile, or one part of a cut tile (cut: its number among them, -1: none).
+// The product's numbers are copied here, into registers: read through the pointer into the launch's
+// parameters they would be loaded again for every k-block.
 struct FfTile {
     const FfProblem* p;
     int m, n, k0, k1, cut, part;
+    int M, N, kb0, a_mn, b_mn;
 };
 __device__ __forceinline__ FfTile ff_tile(const FfLaunch& l, int unit) {
     int t = unit, part = 0, cut = -1;
@@ -148,10 +205,11 @@ __device__ __forceinline__ FfTile ff_tile(const FfLaunch& l, int unit) {
     // M tiles in groups of 16, N tiles outer in a group: tiles that run together share operands in L2
     const int per = 16 * p->tiles_n, grp = q / per, first = grp * 16;
     const int rows = min(16, p->tiles_m - first), r = q - grp * per;
-    FfTile o{p, first + r % rows, r / rows, 0, p->kb, cut, part};
+    FfTile o{p, first + r % rows, r / rows, 0, p->kb, cut, part, p->M, p->N, p->kb0, p->a_mn, p->b_mn};
     if (cut >= 0) {
-        o.k0 = p->kb * part / l.parts;
-        o.k1 = p->kb * (part + 1) / l.parts;
+        const int kb = o.k1;
+        o.k0 = kb * part / l.parts;
+        o.k1 = kb * (part + 1) / l.parts;
     }
     return o;
 }
@@ -221,45 +279,72 @@ __device__ __forceinline__ bool ff_arrive(const FfLaunch& l, const FfTile& t, ui
     __threadfence();
     return before + 1 == (uint32_t)l.parts;
 }
-// 32 columns of this warp's rows: the accumulator, or the sum over a cut tile's parts.
+// 32 columns of this warp's rows: the accumulator, or the sum over a cut tile's parts in their order
+// (each part's loads are in flight while the one before is added).
 __device__ __forceinline__ void ff_chunk(const FfLaunch& l, const FfTile& t, uint32_t tb, int c, int slab, int lane,
                                          uint32_t (&v)[32]) {
+    if (t.cut < 0) {
+        tmem_ld32(tb + c * 32, v);
+        return;
+    }
+    float4 next[8];
+    auto load = [&](int q) {
+        if (q >= l.parts || q == t.part) return;
+        const float4* o = ff_partial(l, t.cut, q, slab, lane) + c * 256;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) next[i] = __ldcg(o + i * 32);
+    };
+    load(0);
     tmem_ld32(tb + c * 32, v);
-    if (t.cut < 0) return;
     float sum[32];
 #pragma unroll
     for (int i = 0; i < 32; ++i) sum[i] = 0.f;
     for (int q = 0; q < l.parts; ++q) {
-        if (q == t.part) {
+        float4 cur[8];
 #pragma unroll
-            for (int i = 0; i < 32; ++i) sum[i] += __uint_as_float(v[i]);
-            continue;
-        }
-        const float4* o = ff_partial(l, t.cut, q, slab, lane) + c * 256;
+        for (int i = 0; i < 8; ++i)
+            cur[i] = q == t.part ? make_float4(__uint_as_float(v[4 * i]), __uint_as_float(v[4 * i + 1]),
+                                               __uint_as_float(v[4 * i + 2]), __uint_as_float(v[4 * i + 3]))
+                                 : next[i];
+        load(q + 1);
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-            const float4 a = __ldcg(o + i * 32);
-            sum[4 * i] += a.x;
-            sum[4 * i + 1] += a.y;
-            sum[4 * i + 2] += a.z;
-            sum[4 * i + 3] += a.w;
+            sum[4 * i] += cur[i].x;
+            sum[4 * i + 1] += cur[i].y;
+            sum[4 * i + 2] += cur[i].z;
+            sum[4 * i + 3] += cur[i].w;
         }
     }
 #pragma unroll
     for (int i = 0; i < 32; ++i) v[i] = __float_as_uint(sum[i]);
 }
 
+// Kept g and u of 16 columns of this warp's rows, fetched ahead of their use.
+struct FfKept {
+    float4 g[4], u[4];
+    __device__ __forceinline__ void load(const FfLaunch& l, const FfTile& t, int row0, int half, int lane) {
+        const int col0 = t.n * FT_N + (half & ~1) * 16;
+        if (row0 >= t.M || half >= 16 || col0 >= t.N) return;
+        const float4 *ig = ff_gu(l, row0, col0, 0, lane) + (half & 1) * 128, *iu = ff_gu(l, row0, col0, 1, lane) + (half & 1) * 128;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            g[i] = __ldcs(ig + i * 32);
+            u[i] = __ldcs(iu + i * 32);
+        }
+    }
+};
+
 template <int MODE>
 __device__ __forceinline__ void ff_epilogue(const FfLaunch& l, const FfTile& t, FfStage& es, uint32_t tb, int row0,
-                                            int slab, int lane) {
-    const FfProblem& p = *t.p;
-    if (row0 >= p.M) return;
+                                            int slab, int lane, FfKept& next) {
+    const CUtensorMap* out = t.p->out;
+    if (row0 >= t.M) return;
     if (t.cut >= 0 && !ff_arrive(l, t, tb, slab, lane)) return;
     if (MODE == FF_SWIGLU) {
 #pragma unroll 1
         for (int c = 0; c < 4; ++c) {
             const int col0 = t.n * 128 + c * 32;
-            if (col0 >= p.N) return;
+            if (col0 >= t.N) return;
             uint32_t g[32], u[32];
             ff_chunk(l, t, tb, c, slab, lane, g);
             ff_chunk(l, t, tb, c + 4, slab, lane, u);
@@ -280,53 +365,63 @@ __device__ __forceinline__ void ff_epilogue(const FfLaunch& l, const FfTile& t, 
                                              __uint_as_float(u[4 * i + 2]), __uint_as_float(u[4 * i + 3]));
                 }
             }
-            es.put(&p.out[0], pk, col0, row0, lane);
+            es.put(out, pk, col0, row0, lane);
         }
     } else if (MODE == FF_DACT) {
 #pragma unroll 1
         for (int c = 0; c < 8; ++c) {
             const int col0 = t.n * FT_N + c * 32;
-            if (col0 >= p.N) return;
-            const float4 *ig = ff_gu(l, row0, col0, 0, lane), *iu = ff_gu(l, row0, col0, 1, lane);
-            float4 g[8], u[8];
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                g[i] = ig[i * 32];
-                u[i] = iu[i * 32];
-            }
+            if (col0 >= t.N) return;
             uint32_t d[32];
             ff_chunk(l, t, tb, c, slab, lane, d);
             uint32_t pg[16], pu[16];
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                const float gv[4] = {g[i].x, g[i].y, g[i].z, g[i].w}, uv[4] = {u[i].x, u[i].y, u[i].z, u[i].w};
-                float dg[4], du[4];
+            for (int half = 0; half < 2; ++half) {
+                const FfKept k = next;
+                next.load(l, t, row0, 2 * c + half + 1, lane);
 #pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    const float dh = __uint_as_float(d[4 * i + j]), s = ff_sigmoid(gv[j]);
-                    du[j] = dh * (gv[j] * s);
-                    dg[j] = dh * uv[j] * (s * (1.0f + gv[j] * (1.0f - s)));
+                for (int i = 0; i < 4; ++i) {
+                    const float gv[4] = {k.g[i].x, k.g[i].y, k.g[i].z, k.g[i].w};
+                    const float uv[4] = {k.u[i].x, k.u[i].y, k.u[i].z, k.u[i].w};
+                    float dg[4], du[4];
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        const float dh = __uint_as_float(d[half * 16 + 4 * i + j]), s = ff_sigmoid(gv[j]);
+                        du[j] = dh * (gv[j] * s);
+                        dg[j] = dh * uv[j] * (s * (1.0f + gv[j] * (1.0f - s)));
+                    }
+                    pg[half * 8 + 2 * i] = pack_bf16x2(dg[0], dg[1]);
+                    pg[half * 8 + 2 * i + 1] = pack_bf16x2(dg[2], dg[3]);
+                    pu[half * 8 + 2 * i] = pack_bf16x2(du[0], du[1]);
+                    pu[half * 8 + 2 * i + 1] = pack_bf16x2(du[2], du[3]);
                 }
-                pg[2 * i] = pack_bf16x2(dg[0], dg[1]);
-                pg[2 * i + 1] = pack_bf16x2(dg[2], dg[3]);
-                pu[2 * i] = pack_bf16x2(du[0], du[1]);
-                pu[2 * i + 1] = pack_bf16x2(du[2], du[3]);
             }
-            es.put(&p.out[0], pg, col0, row0, lane);
-            es.put(&p.out[1], pu, col0, row0, lane);
+            es.put(out, pg, col0, row0, lane);
+            es.put(out + 1, pu, col0, row0, lane);
         }
     } else {
 #pragma unroll 1
         for (int c = 0; c < 8; ++c) {
             const int col0 = t.n * FT_N + c * 32;
-            if (col0 >= p.N) return;
+            if (col0 >= t.N) return;
             uint32_t v[32], pk[16];
             ff_chunk(l, t, tb, c, slab, lane, v);
 #pragma unroll
             for (int i = 0; i < 16; ++i) pk[i] = pack_bf16x2(__uint_as_float(v[2 * i]), __uint_as_float(v[2 * i + 1]));
-            es.put(&p.out[0], pk, col0, row0, lane);
+            es.put(out, pk, col0, row0, lane);
         }
     }
+}
+
+// f(FxInt<bit 0: A, bit 1: B stored along M / N>) for the forms that a kernel's products take: the
+// forward products (0), dh and dx (2), the weight gradients (3).
+template <int MODE, typename F>
+__device__ __forceinline__ void ff_forms(int form, F f) {
+    if (MODE == FF_SWIGLU) f(FxInt<0>());
+    else if (MODE == FF_DACT) f(FxInt<2>());
+    else if (form == 0) f(FxInt<0>());
+    else if (form == 2) f(FxInt<2>());
+    else f(FxInt<3>());
 }
 
 // Persistent GEMM on CTA pairs: cluster c takes tiles c, c + clusters, ... of the launch's list.
@@ -357,6 +452,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(GEMM_THREADS, 1)
         mbar_fence_init();
     }
     __syncthreads();
+    if (warp == 0 && lane < l.count) {
+        tma_prefetch_desc(&l.p[lane].a[0]);
+        tma_prefetch_desc(&l.p[lane].b[MODE == FF_SWIGLU ? (int)rank : 0]);
+        tma_prefetch_desc(&l.p[lane].out[0]);
+    }
     if (warp == 1) {
         tmem_alloc_pair(sm.tmem_base, TMEM_COLS);
         tmem_relinquish_pair();
@@ -374,40 +474,25 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(GEMM_THREADS, 1)
     uint32_t nk = 0;
 
     if (warp == 0 && lane == 0) {
-        int st = 0;
-        uint32_t ph = 0;
+        FfRing ring;
         bool ok = !bad;
         for (int t = cluster; ok && t < l.units; t += clusters) {
             const FfTile tr = ff_tile(l, t);
-            const FfProblem& p = *tr.p;
             const int arow = tr.m * FT_M + (int)rank * 128;
             const int brow = MODE == FF_SWIGLU ? tr.n * 128 : tr.n * FT_N + (int)rank * 128;
-            for (int kb = tr.k0; kb < tr.k1; ++kb) {
-                if (!mbar_wait(&sm.empty[st], ph ^ 1u, tmo, sm.abort)) {
-                    ok = false;
-                    break;
+            auto load = [&](auto form) {
+                constexpr bool A_MN = decltype(form)::value & 1, B_MN = (decltype(form)::value & 2) != 0;
+                // the first pair of operands, then (dx) the second
+                for (int i = 0; ok && i < 2; ++i) {
+                    const int from = i ? max(0, tr.k0 - tr.kb0) : tr.k0, to = i ? tr.k1 - tr.kb0 : min(tr.k1, tr.kb0);
+                    const CUtensorMap *ma = tr.p->a + i, *mb = tr.p->b + (MODE == FF_SWIGLU ? (int)rank : i);
+                    if (rank == 0) ok = ff_produce<A_MN, B_MN, false>(sm, ring, ma, mb, arow, brow, from, to, tmo);
+                    else ok = ff_produce<A_MN, B_MN, true>(sm, ring, ma, mb, arow, brow, from, to, tmo);
                 }
-                uint8_t* a = sm.stages + st * FF_STAGE;
-                uint8_t* b = a + FF_HALF;
-                const int second = kb >= p.kb0 ? 1 : 0, k = (kb - (second ? p.kb0 : 0)) * BK;
-                const CUtensorMap* ma = &p.a[second];
-                const CUtensorMap* mb = &p.b[MODE == FF_SWIGLU ? (int)rank : second];
-                if (rank == 0) {
-                    mbar_arrive_expect_tx(&sm.full[st], 2 * FF_STAGE);
-                    ff_load<false>(a, ma, &sm.full[st], 0u, p.a_mn, arow, k);
-                    ff_load<false>(b, mb, &sm.full[st], 0u, p.b_mn, brow, k);
-                } else {
-                    const uint32_t full0 = mapa_shared(smem_u32(&sm.full[st]), 0u);
-                    ff_load<true>(a, ma, nullptr, full0, p.a_mn, arow, k);
-                    ff_load<true>(b, mb, nullptr, full0, p.b_mn, brow, k);
-                }
-                ++nk;
-                if (++st == FF_STAGES) {
-                    st = 0;
-                    ph ^= 1u;
-                }
-            }
+            };
+            ff_forms<MODE>(tr.a_mn | tr.b_mn << 1, load);
         }
+        nk = ring.done;
         if (!ok) {
             if (!*sm.abort) ff_status(l.status, 10 + (int)rank);
             ff_abort(sm, rank);
@@ -419,36 +504,20 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(GEMM_THREADS, 1)
             ff_abort(sm, rank);
         }
         if (rank == 0) {
-            int st = 0, b = 0;
-            uint32_t ph = 0, aph = 0;
+            FfRing ring;
+            int b = 0;
+            uint32_t aph = 0;
             for (int t = cluster; ok && t < l.units; t += clusters) {
                 const FfTile tr = ff_tile(l, t);
-                const FfProblem& p = *tr.p;
-                const uint32_t idesc = umma_idesc_bf16(FT_M, FT_N) | ((uint32_t)p.a_mn << 15) | ((uint32_t)p.b_mn << 16);
-                const uint32_t astep = p.a_mn ? 128 : 2, bstep = p.b_mn ? 128 : 2;  // 16 k, in 16 bytes
                 if (!mbar_wait_cluster(&sm.acc_empty[b], aph ^ 1u, tmo, sm.abort)) {
                     ok = false;
                     break;
                 }
                 tc_fence_after();
-                const uint32_t dt = tmem + (uint32_t)(b * 256);
-                for (int kb = tr.k0; kb < tr.k1; ++kb) {
-                    if (!mbar_wait_cluster(&sm.full[st], ph, tmo, sm.abort)) {
-                        ok = false;
-                        break;
-                    }
-                    tc_fence_after();
-                    const uint32_t addr = smem_u32(sm.stages + st * FF_STAGE);
-                    const uint64_t ad = ff_sdesc(addr, p.a_mn), bd = ff_sdesc(addr + FF_HALF, p.b_mn);
-#pragma unroll
-                    for (int kk = 0; kk < BK / 16; ++kk)
-                        umma_bf16_pair(dt, ad + astep * kk, bd + bstep * kk, idesc, kb != tr.k0 || kk != 0);
-                    umma_commit_pair(&sm.empty[st], 0x3);
-                    if (++st == FF_STAGES) {
-                        st = 0;
-                        ph ^= 1u;
-                    }
-                }
+                ff_forms<MODE>(tr.a_mn | tr.b_mn << 1, [&](auto form) {
+                    constexpr bool A_MN = decltype(form)::value & 1, B_MN = (decltype(form)::value & 2) != 0;
+                    ok = ff_multiply<A_MN, B_MN>(sm, ring, tmem + (uint32_t)(b * 256), tr.k1 - tr.k0, tmo);
+                });
                 if (!ok) break;
                 umma_commit_pair(&sm.acc_full[b], 0x3);
                 b ^= 1;
@@ -470,6 +539,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(GEMM_THREADS, 1)
         uint32_t aph = 0;
         for (int t = cluster; !bad && t < l.units; t += clusters) {
             const FfTile tr = ff_tile(l, t);
+            const int row0 = tr.m * FT_M + (int)rank * 128 + q * 32;
+            FfKept kept;
+            if (MODE == FF_DACT) kept.load(l, tr, row0, 0, lane);
             if (!mbar_wait(&sm.acc_full[b], aph, tmo, sm.abort)) {
                 if (!*sm.abort) ff_status(l.status, 16 + (int)rank);
                 if (lane == 0) ff_abort(sm, rank);
@@ -478,7 +550,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(GEMM_THREADS, 1)
             tc_fence_after();
             __syncwarp();
             const uint32_t tb = tmem + ((uint32_t)(q * 32) << 16) + (uint32_t)(b * 256);
-            ff_epilogue<MODE>(l, tr, es, tb, tr.m * FT_M + (int)rank * 128 + q * 32, (int)rank * 4 + q, lane);
+            ff_epilogue<MODE>(l, tr, es, tb, row0, (int)rank * 4 + q, lane, kept);
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive_cluster(acc_empty0 + b * 8u);
@@ -521,7 +593,7 @@ struct FxArgs {
     CUtensorMap a[2], b[2];
     int M, T;             // features, tokens
     int kb0, kb;          // k-blocks of operand pair 0, of both (FF_SWIGLU: a[0] and a[1] side by side)
-    int a_mn, nt, splits, tiles_t;
+    int nt, splits, tiles_t;
     int stages, early;
     __nv_bfloat16 *out0, *out1;  // [T][M]
     float2* gu;                  // kept g and u, [T][M]
@@ -584,16 +656,12 @@ __device__ __forceinline__ void st_cluster_vec(uint32_t cluster_addr, const uint
     else
         asm volatile("st.shared::cluster.v2.b32 [%0], {%1, %2};" ::"r"(cluster_addr), "r"(v[0]), "r"(v[1]) : "memory");
 }
-template <int N>
-struct FxInt {
-    static constexpr int value = N;
-};
 template <int W>
 struct alignas(4 * W) FxVec {
     float v[W];
 };
 
-template <int MODE>
+template <int MODE, bool A_MN>
 __global__ void __launch_bounds__(GEMM_THREADS, 1) flex_kernel(const __grid_constant__ FxArgs p) {
     constexpr bool DUAL = MODE == FF_SWIGLU;
     extern __shared__ uint8_t smem_raw[];
@@ -619,6 +687,11 @@ __global__ void __launch_bounds__(GEMM_THREADS, 1) flex_kernel(const __grid_cons
         abort_word = 0;
         mbar_fence_init();
     }
+    if (warp == 0 && lane == 1) {
+        tma_prefetch_desc(&p.a[0]);
+        tma_prefetch_desc(&p.b[0]);
+        if (DUAL) tma_prefetch_desc(&p.a[1]);
+    }
     if (warp == 1) {
         tmem_alloc(&tmem_base, cols);
         tmem_relinquish();
@@ -631,36 +704,40 @@ __global__ void __launch_bounds__(GEMM_THREADS, 1) flex_kernel(const __grid_cons
 
     if (warp == 0) {
         if (lane == 0) {
-            auto weights = [&](int i) {
-                const int kb = k0 + i, second = kb >= p.kb0 ? 1 : 0, k = (kb - (second ? p.kb0 : 0)) * BK;
-                uint8_t* a = ring + (i % p.stages) * stage_bytes;
-                uint64_t* bar = &full[i % p.stages];
-                mbar_arrive_expect_tx(bar, stage_bytes);
-                ff_load<false>(a, &p.a[second], bar, 0u, p.a_mn, f0, k);
-                if (DUAL) ff_load<false>(a + FX_A, &p.a[1], bar, 0u, p.a_mn, f0, k);
+            auto pair_of = [&](int kb) { return kb >= p.kb0 ? 1 : 0; };
+            auto weights = [&](int kb, int st) {
+                const int second = pair_of(kb), k = (kb - (second ? p.kb0 : 0)) * BK;
+                uint8_t* a = ring + st * stage_bytes;
+                mbar_arrive_expect_tx(&full[st], stage_bytes);
+                ff_load<A_MN, false>(a, &p.a[second], &full[st], 0u, f0, k);
+                if (DUAL) ff_load<A_MN, false>(a + FX_A, &p.a[1], &full[st], 0u, f0, k);
             };
-            auto tokens = [&](int i) {
-                const int kb = k0 + i, second = kb >= p.kb0 ? 1 : 0, k = (kb - (second ? p.kb0 : 0)) * BK;
-                uint8_t* b = ring + (i % p.stages) * stage_bytes + (DUAL ? 2 : 1) * FX_A;
-                tma_load_2d(b, &p.b[second], &full[i % p.stages], k, t0);
+            auto tokens = [&](int kb, int st) {
+                const int second = pair_of(kb), k = (kb - (second ? p.kb0 : 0)) * BK;
+                tma_load_2d(ring + st * stage_bytes + (DUAL ? 2 : 1) * FX_A, &p.b[second], &full[st], k, t0);
             };
             const int head = nkb < p.stages ? nkb : p.stages;
             if (p.early)
-                for (int i = 0; i < head; ++i) weights(i);
+                for (int i = 0; i < head; ++i) weights(k0 + i, i);
             griddep_wait();
             griddep_launch();
-            int issued = 0;
+            int issued = 0, st = 0;
+            uint32_t ph = 0;
             for (; issued < head; ++issued) {
-                if (!p.early) weights(issued);
-                tokens(issued);
+                if (!p.early) weights(k0 + issued, issued);
+                tokens(k0 + issued, issued);
             }
-            for (; issued < nkb; ++issued) {
-                if (!mbar_wait(&empty[issued % p.stages], ((uint32_t)(issued / p.stages) & 1u) ^ 1u, tmo, &abort_word)) {
+            for (; issued < nkb; ++issued) {  // stage st is free once its products of round ph are done
+                if (!mbar_wait(&empty[st], ph, tmo, &abort_word)) {
                     ok = false;
                     break;
                 }
-                weights(issued);
-                tokens(issued);
+                weights(k0 + issued, st);
+                tokens(k0 + issued, st);
+                if (++st == p.stages) {
+                    st = 0;
+                    ph ^= 1u;
+                }
             }
             if (!ok) {
                 if (!abort_word) ff_status(p.status, 20);
@@ -675,24 +752,29 @@ __global__ void __launch_bounds__(GEMM_THREADS, 1) flex_kernel(const __grid_cons
         griddep_wait();
         griddep_launch();
         if (lane == 0) {
-            const uint32_t idesc = umma_idesc_bf16(128, p.nt) | ((uint32_t)p.a_mn << 15);
-            const uint32_t astep = p.a_mn ? 128 : 2;
+            const uint32_t idesc = umma_idesc_bf16(128, p.nt) | ((uint32_t)A_MN << 15);
+            constexpr uint32_t astep = A_MN ? 128 : 2;
+            int st = 0;
+            uint32_t ph = 0;
             for (int i = 0; i < nkb; ++i) {
-                const int st = i % p.stages;
-                if (!mbar_wait(&full[st], (uint32_t)(i / p.stages) & 1u, tmo, &abort_word)) {
+                if (!mbar_wait(&full[st], ph, tmo, &abort_word)) {
                     if (!abort_word) ff_status(p.status, 22);
                     abort_word = 1;
                     break;
                 }
                 tc_fence_after();
                 const uint32_t a = smem_u32(ring + st * stage_bytes), b = a + (DUAL ? 2 : 1) * FX_A;
-                const uint64_t ad = ff_sdesc(a, p.a_mn), ud = ff_sdesc(a + FX_A, p.a_mn), bd = sdesc_sw128(b);
+                const uint64_t ad = ff_sdesc(a, A_MN), ud = ff_sdesc(a + FX_A, A_MN), bd = sdesc_sw128(b);
 #pragma unroll
                 for (int kk = 0; kk < BK / 16; ++kk) {
                     umma_bf16(tmem, ad + astep * kk, bd + 2 * kk, idesc, (i | kk) != 0);
                     if (DUAL) umma_bf16(tmem + p.nt, ud + astep * kk, bd + 2 * kk, idesc, (i | kk) != 0);
                 }
                 umma_commit(&empty[st]);
+                if (++st == p.stages) {
+                    st = 0;
+                    ph ^= 1u;
+                }
             }
             umma_commit(&done);  // fires when every UMMA issued has completed
             int never = 0;
@@ -907,7 +989,7 @@ FfCut ff_cut(int tiles, int kb, int clusters) {
     for (int parts = 2; rest && parts <= 8; ++parts) {
         if (rest * parts > FF_MAX_CUT || rest > FF_MAX_CUT / 2 || parts * 4 > kb) break;
         const int rounds = (rest * parts + clusters - 1) / clusters;
-        const float w = tiles / clusters + rounds * (1.0f / parts + FF_CUT_COST / kb);
+        const float w = tiles / clusters + rounds * (1.0f / parts + FF_CUT_KEEP / kb) + FF_CUT_ADD * (parts - 1) / kb;
         if (w < best.waves) best = FfCut{full, parts, w};
     }
     return best;
@@ -1002,7 +1084,7 @@ FxPlan ff_choose(int M, int T, int kb, bool dual, int sms) {
 }
 
 // Once per device: the kernel may take FX_ROOM of shared memory.
-template <int MODE>
+template <int MODE, bool A_MN>
 cudaError_t fx_prepare() {
     static std::atomic<bool> done[64];
     int dev = 0;
@@ -1010,13 +1092,13 @@ cudaError_t fx_prepare() {
     if (e != cudaSuccess) return e;
     if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
     if (done[dev].load(std::memory_order_relaxed)) return cudaSuccess;
-    e = cudaFuncSetAttribute(reinterpret_cast<const void*>(&flex_kernel<MODE>),
+    e = cudaFuncSetAttribute(reinterpret_cast<const void*>(&flex_kernel<MODE, A_MN>),
                              cudaFuncAttributeMaxDynamicSharedMemorySize, FX_ROOM + 1024);
     if (e == cudaSuccess) done[dev].store(true, std::memory_order_relaxed);
     return e;
 }
 
-template <int MODE>
+template <int MODE, bool A_MN>
 int fx_run(FxArgs& p, const FxPlan& plan, const FfLayout& L, void* ws, cudaStream_t st, const char* what) {
     p.nt = plan.nt;
     p.splits = plan.splits;
@@ -1025,7 +1107,7 @@ int fx_run(FxArgs& p, const FxPlan& plan, const FfLayout& L, void* ws, cudaStrea
     p.status = static_cast<int32_t*>(ws);
     p.timeout_ns = L.timeout_ns;
     const size_t smem = (size_t)p.stages * fx_stage_bytes(MODE == FF_SWIGLU, p.nt) + 1024;
-    cudaError_t e = fx_prepare<MODE>();
+    cudaError_t e = fx_prepare<MODE, A_MN>();
     if (e != cudaSuccess) return cuda_fail(e, what);
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)((p.M + 127) / 128 * p.tiles_t * p.splits));
@@ -1039,12 +1121,11 @@ int fx_run(FxArgs& p, const FxPlan& plan, const FfLayout& L, void* ws, cudaStrea
     attr[1].val.clusterDim = {(unsigned)p.splits, 1, 1};
     cfg.attrs = attr;
     cfg.numAttrs = p.splits > 1 ? 2 : 1;
-    e = cudaLaunchKernelEx(&cfg, flex_kernel<MODE>, p);
+    e = cudaLaunchKernelEx(&cfg, flex_kernel<MODE, A_MN>, p);
     return e == cudaSuccess ? MOE_OK : cuda_fail(e, what);
 }
 // Weights [M, K] (K-major, or stored [K, M]) and tokens [T, K] of operand pair i.
 int fx_operands(FxArgs& p, int i, const void* w, int a_mn, const void* x, size_t M, size_t T, size_t K, int nt) {
-    p.a_mn = a_mn;
     const int rc = ff_operand(&p.a[i], w, M, K, a_mn);
     return rc ? rc : ff_map(&p.b[i], x, T, K, (uint32_t)nt, false);
 }
@@ -1124,7 +1205,7 @@ MOE_API int moe_ffn_forward(const moe_ffn_config* c, const uint16_t* x, const ui
         p.gu = reinterpret_cast<float2*>(gu);
         if ((rc = fx_operands(p, 0, W1, 0, x, L.F, L.T, L.d, up_plan.nt))) return rc;
         if ((rc = fx_operands(p, 1, W3, 0, x, L.F, L.T, L.d, up_plan.nt))) return rc;
-        if ((rc = fx_run<FF_SWIGLU>(p, up_plan, L, ws, st, "gate and up projections"))) return rc;
+        if ((rc = fx_run<FF_SWIGLU, false>(p, up_plan, L, ws, st, "gate and up projections"))) return rc;
     } else {
         FfList up;
         FfProblem& p = up.add(x, 0, W1, 0, h, L.T, L.F, L.d);
@@ -1139,7 +1220,7 @@ MOE_API int moe_ffn_forward(const moe_ffn_config* c, const uint16_t* x, const ui
     if (down_plan.nt) {
         FxArgs p = fx_args(L.d, L.T, kf, kf, y, 1);
         if ((rc = fx_operands(p, 0, W2, 0, h, L.d, L.T, L.F, down_plan.nt))) return rc;
-        return fx_run<FF_PLAIN>(p, down_plan, L, ws, st, "down projection");
+        return fx_run<FF_PLAIN, false>(p, down_plan, L, ws, st, "down projection");
     }
     FfList down;
     down.add(h, 0, W2, 0, y, L.T, L.d, L.F);
@@ -1179,7 +1260,7 @@ MOE_API int moe_ffn_backward(const moe_ffn_config* c, const uint16_t* x, const u
         p.out1 = reinterpret_cast<__nv_bfloat16*>(du);
         p.gu = reinterpret_cast<float2*>(gu);
         if ((rc = fx_operands(p, 0, W2, 1, dy, L.F, L.T, L.d, plan.nt))) return rc;
-        if ((rc = fx_run<FF_DACT>(p, plan, L, ws, st, "hidden gradients"))) return rc;
+        if ((rc = fx_run<FF_DACT, true>(p, plan, L, ws, st, "hidden gradients"))) return rc;
     } else {
         FfList act;
         FfProblem& p = act.add(dy, 0, W2, 1, dg, L.T, L.F, L.d);
@@ -1194,7 +1275,7 @@ MOE_API int moe_ffn_backward(const moe_ffn_config* c, const uint16_t* x, const u
         FxArgs p = fx_args(L.d, L.T, kf, 2 * kf, dx, 1);
         if ((rc = fx_operands(p, 0, W1, 1, dg, L.d, L.T, L.F, dx_plan.nt))) return rc;
         if ((rc = fx_operands(p, 1, W3, 1, du, L.d, L.T, L.F, dx_plan.nt))) return rc;
-        if ((rc = fx_run<FF_PLAIN>(p, dx_plan, L, ws, st, "input gradients"))) return rc;
+        if ((rc = fx_run<FF_PLAIN, true>(p, dx_plan, L, ws, st, "input gradients"))) return rc;
     } else {
         grad.add(dg, 0, W1, 1, dx, L.T, L.d, L.F, du, W3);
     }
