@@ -33,8 +33,6 @@ constexpr int FF_MISC = 1024;
 constexpr int FF_SMEM = FF_STAGES * FF_STAGE + EPI_BYTES + FF_MISC + 1024;
 static_assert(FF_SMEM <= 227 * 1024, "dense GEMM shared memory");
 constexpr int FF_PROBLEMS = 4;
-// k-blocks' time that a cut tile costs beside its products: keeping a part, and adding up each of the others
-constexpr float FF_CUT_KEEP = 6.0f, FF_CUT_ADD = 8.0f;
 
 enum FfMode : int { FF_PLAIN = 0, FF_SWIGLU = 1, FF_DACT = 2 };
 
@@ -976,21 +974,36 @@ struct FfList {
     }
 };
 
-// Tiles come in waves of one a cluster; the tiles of an incomplete last wave are cut along k into as many
-// parts as finish soonest: ceil(rest x parts / clusters) rounds of 1 / parts of a tile each, plus what
-// keeping and adding up a part costs.
+// Times in microseconds that the choices below go by, fitted to 5100 measured launches (products of
+// 512 to 14336 features, 1 to 2048 tokens and 512 to 5632 k, every plan of each; the plan that these
+// numbers choose took 1.04 times the best one's time on average, 1.29 times at worst).
+constexpr float US_HBM = 6.3e6f;                             // bytes a microsecond from memory
+constexpr float US_DENSE = 5.2f, US_DENSE_KB = 0.275f;       // a launch; a k-block of a 256 x 256 tile
+constexpr float US_DENSE_WAVE = 2.8f, US_DENSE_REST = 2.65f; // a full wave of tiles; the last one
+constexpr float US_CUT_ROUND = 7.0f, US_CUT_PART = 2.0f;     // a round of parts; adding up each further part
+constexpr float US_FLEX = 1.7f, US_FLEX_CTA = 0.93f;         // a launch; a CTA beside its k-blocks
+constexpr float US_FLEX_BYTES = 155.6e3f;                    // bytes a microsecond into a SM
+constexpr float US_FLEX_LATENCY = 1.13f;                     // of a load, shared by the stages in flight
+constexpr float US_FLEX_CYCLES = 1.47f / 1.9e3f;             // a cycle of the tensor cores
+constexpr float US_FLEX_VALUE = 0.0025f;                     // a token's values in the epilogue
+constexpr float US_FLEX_SPLIT = 0.55f, US_FLEX_EXCHANGE = 0.024f;  // a cluster; a token's partial sums
+constexpr float US_FLEX_TWO = 1.57f, US_FLEX_MORE = 0.94f;   // two CTAs' fixed part on one SM; each CTA beyond
+
+// Tiles come in waves of one a cluster. The tiles of an incomplete last wave are cut along k into as many
+// parts as finish soonest.
 struct FfCut {
     int full, parts;
-    float waves;  // of whole tiles, with that cost
+    float us;  // of the whole launch
 };
 FfCut ff_cut(int tiles, int kb, int clusters) {
-    const int full = tiles / clusters * clusters, rest = tiles - full;
-    FfCut best{tiles, 1, (float)(tiles / clusters + (rest ? 1 : 0))};
-    for (int parts = 2; rest && parts <= 8; ++parts) {
-        if (rest * parts > FF_MAX_CUT || rest > FF_MAX_CUT / 2 || parts * 4 > kb) break;
+    const int full = tiles / clusters, rest = tiles - full * clusters;
+    const float before = US_DENSE + full * (kb * US_DENSE_KB + US_DENSE_WAVE) + US_DENSE_REST;
+    FfCut best{tiles, 1, before + (rest ? kb * US_DENSE_KB : 0.0f)};
+    if (!rest || rest > FF_MAX_CUT / 2) return best;
+    for (int parts = 2; parts <= 8 && rest * parts <= FF_MAX_CUT && parts * 4 <= kb; ++parts) {
         const int rounds = (rest * parts + clusters - 1) / clusters;
-        const float w = tiles / clusters + rounds * (1.0f / parts + FF_CUT_KEEP / kb) + FF_CUT_ADD * (parts - 1) / kb;
-        if (w < best.waves) best = FfCut{full, parts, w};
+        const float us = before + rounds * ((kb + parts - 1) / parts * US_DENSE_KB + US_CUT_ROUND) + US_CUT_PART * (parts - 1);
+        if (us < best.us) best = FfCut{full * clusters, parts, us};
     }
     return best;
 }
@@ -1050,36 +1063,41 @@ struct FxPlan {
     float us;  // the estimate it was chosen by
 };
 
-// Estimated time of a product out[T][M] over kb k-blocks on either kernel; the smaller one runs. Per SM
-// and k-block: a dense pair tile (256 x 256) keeps the tensor cores busy for 512 cycles; a flex tile
-// takes VALS x 4 UMMAs of max(nt / 2, 32 + nt / 4) cycles (tensor cores, or the shared memory that
-// feeds them 128 x 16 weights and nt x 16 tokens), and its stage's bytes come at about 64 a cycle.
+// The quickest flex_kernel plan for a product out[T][M] over kb k-blocks. A k-block costs a CTA the
+// tensor cores' time (VALS x 4 UMMAs of max(nt / 2, 32 + nt / 4) cycles: their own, or the shared
+// memory's that feeds them 128 x 16 weights and nt x 16 tokens), its bytes' way into the SM, or its share
+// of a load's latency; two CTAs on a SM share the first two. Clusters of 4 and 8 do not fill every SM.
 FxPlan ff_choose_flex(int M, int T, int kb, bool dual, int sms) {
-    constexpr float GHZ = 1.9f;
     FxPlan best{0, 1, 0, 1e30f};
-    const float hbm = (float)M * kb * BK * 2 * (dual ? 2 : 1) / 6.5e6f;
+    const int vals = dual ? 2 : 1;
+    const float hbm = (float)M * kb * BK * 2 * vals / US_HBM + 1.6f;
     for (int nt = 16; nt <= 128; nt += nt < 64 ? 16 : 32) {
         if (nt > 16 && nt - (nt <= 64 ? 16 : 32) >= T) break;  // a narrower tile holds every token
         const int stage = fx_stage_bytes(dual, nt), tiles = ((M + 127) / 128) * ((T + nt - 1) / nt);
         const int stages = FX_ROOM / stage < FX_MAX_STAGES ? FX_ROOM / stage : FX_MAX_STAGES;
+        const float cycles = US_FLEX_CYCLES * vals * 4 * (nt / 2 > 32 + nt / 4 ? nt / 2 : 32 + nt / 4);
+        const float bytes = stage / US_FLEX_BYTES, work = cycles > bytes ? cycles : bytes, wait = US_FLEX_LATENCY / stages;
+        const float one = work > wait ? work : wait, two = 2 * work > wait ? 2 * work : wait;
         for (int S = 1; S <= 8; S *= 2) {
-            if (S > kb || nt % S || (S > 1 && (dual ? 2 : 1) * nt * 512 > stages * stage)) continue;
-            const int load = (tiles * S + sms - 1) / sms, mine = (kb + S - 1) / S;
-            const float mma = load * mine * (dual ? 2 : 1) * 4 * (nt / 2 > 32 + nt / 4 ? nt / 2 : 32 + nt / 4) / (GHZ * 1e3f);
-            const float bytes = load * (float)mine * stage / (64 * GHZ * 1e3f);
-            float us = mma > bytes ? mma : bytes;
-            if (us < hbm) us = hbm;
-            us += 3.0f + (S > 1 ? 1.5f : 0.0f) + nt * 0.02f;
+            if (S > kb || nt % S || (S > 1 && vals * nt * 512 > stages * stage)) continue;
+            const int slots = S == 8 ? sms * 85 / 100 : S == 4 ? sms * 93 / 100 : sms;
+            const int load = (tiles * S + slots - 1) / slots, mine = (kb + S - 1) / S;
+            const float fixed = US_FLEX_CTA + US_FLEX_VALUE * nt * vals / S +
+                                (S > 1 ? US_FLEX_SPLIT + US_FLEX_EXCHANGE * nt * vals : 0.0f);
+            float us = load / 2 * (mine * two + fixed * US_FLEX_TWO) + load % 2 * (mine * one + fixed) +
+                       (load > 2 ? US_FLEX_MORE * (load - 2) : 0.0f);
+            us = US_FLEX + (us > hbm ? us : hbm);
             if (us < best.us) best = FxPlan{nt, S, stages, us};
         }
     }
     return best;
 }
-
+// How a product runs: the quicker of flex_kernel's best plan and dense_kernel.
 FxPlan ff_choose(int M, int T, int kb, bool dual, int sms) {
-    const int tiles = ((T + FT_M - 1) / FT_M) * ((M + (dual ? 127 : FT_N - 1)) / (dual ? 128 : FT_N)), pairs = sms / 2;
+    const int tiles = ((T + FT_M - 1) / FT_M) * ((M + (dual ? 127 : FT_N - 1)) / (dual ? 128 : FT_N));
     const FxPlan flex = ff_choose_flex(M, T, kb, dual, sms);
-    const float dense = ff_cut(tiles, kb, pairs).waves * kb * 512.0f / 1.9e3f + 5.0f;
+    const float hbm = (float)M * kb * BK * 2 * (dual ? 2 : 1) / US_HBM + 6.0f, us = ff_cut(tiles, kb, sms / 2).us;
+    const float dense = us > hbm ? us : hbm;
     return flex.us < dense ? flex : FxPlan{0, 1, 0, dense};
 }
 
