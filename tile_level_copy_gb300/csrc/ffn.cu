@@ -30,7 +30,10 @@ constexpr int FF_STAGES = 6;
 constexpr int FF_HALF = 128 * BK * 2;   // one CTA's half of an operand's stage: 16 KB
 constexpr int FF_STAGE = 2 * FF_HALF;
 constexpr int FF_MISC = 1024;
-constexpr int FF_SMEM = FF_STAGES * FF_STAGE + EPI_BYTES + FF_MISC + 1024;
+constexpr int FF_WARPS = 8;             // epilogue warps: two for each 32 rows, half of the columns each
+constexpr int FF_THREADS = 64 + 32 * FF_WARPS;
+constexpr int FF_EPI = FF_WARPS * 2 * EPI_CHUNK_BYTES;
+constexpr int FF_SMEM = FF_STAGES * FF_STAGE + FF_EPI + FF_MISC + 1024;
 static_assert(FF_SMEM <= 227 * 1024, "dense GEMM shared memory");
 constexpr int FF_PROBLEMS = 4;
 
@@ -53,7 +56,7 @@ struct FfLaunch {
     int count, tiles;
     int full, parts, units;  // tiles from `full` on are cut into `parts` pieces of their k-blocks
     float* partial;          // their partial sums, and
-    uint32_t* arrived;       // a count of the pieces done for each 32 rows of a cut tile (zero between calls)
+    uint32_t* arrived;       // counts of the parts done, one for each epilogue warp of a cut tile (zero between calls)
     float* gu;         // kept g and u (FF_SWIGLU writes, may be null; FF_DACT reads)
     int gu_cols;       // 32-column blocks of a row of it
     int32_t* status;   // [2] first error of the calls on a workspace, and where
@@ -74,7 +77,7 @@ __device__ __forceinline__ FfSmem ff_carve(uint8_t* raw) {
     uint8_t* base = raw + (((a + 1023u) & ~1023u) - a);
     s.stages = base;
     s.epi = base + FF_STAGES * FF_STAGE;
-    s.full = reinterpret_cast<uint64_t*>(s.epi + EPI_BYTES);
+    s.full = reinterpret_cast<uint64_t*>(s.epi + FF_EPI);
     s.empty = s.full + FF_STAGES;
     s.acc_full = s.empty + FF_STAGES;
     s.acc_empty = s.acc_full + 2;
@@ -212,6 +215,20 @@ __device__ __forceinline__ FfTile ff_tile(const FfLaunch& l, int unit) {
     return o;
 }
 
+// 32 registers of each lane into 32 lanes x 32 columns of TMEM, then wait.
+__device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t (&r)[32]) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x32.b32 [%32], "
+        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+        "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31};\n\t"
+        "tcgen05.wait::st.sync.aligned;" ::"r"(r[0]),
+        "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]),
+        "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]), "r"(r[19]),
+        "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]),
+        "r"(r[29]), "r"(r[30]), "r"(r[31]), "r"(taddr)
+        : "memory");
+}
+
 // One epilogue warp's two staging chunks (32 rows x 32 columns of bf16), stored by TMA.
 struct FfStage {
     uint8_t* buf;
@@ -246,84 +263,90 @@ __device__ __forceinline__ float4* ff_gu(const FfLaunch& l, int row0, int col0, 
     return reinterpret_cast<float4*>(l.gu + (block * 2 + which) * 1024) + lane;
 }
 
-// Partial sums of a cut tile's part: for each 32 rows (slab = rank x 4 + warp) 8 chunks of 32 columns,
-// each [8 pieces of 4 columns][32 rows][4] fp32.
-__device__ __forceinline__ float4* ff_partial(const FfLaunch& l, int cut, int part, int slab, int lane) {
-    return reinterpret_cast<float4*>(l.partial + (((size_t)cut * l.parts + part) * 8 + slab) * 8192) + lane;
+// The accumulator's 32-column chunk that is the i-th of an epilogue warp's four (half: its half of the
+// columns). FF_SWIGLU: chunks 0-3 hold g, 4-7 u of the same features.
+template <int MODE>
+__device__ __forceinline__ int ff_chunk(int half, int i) {
+    return MODE == FF_SWIGLU ? 2 * half + (i & 1) + (i & 2) * 2 : 4 * half + i;
 }
-// A part of a cut tile: keeps this warp's sums and counts them as done. True for the part that comes
-// last, which then adds up all of them (in the order of the parts, its own from TMEM) and finishes the
-// rows. Nothing waits for another CTA.
-__device__ __forceinline__ bool ff_arrive(const FfLaunch& l, const FfTile& t, uint32_t tb, int slab, int lane) {
+// Partial sums of a cut tile's part, for each epilogue warp of the pair (slab): its four chunks, each
+// [8 pieces of 4 columns][32 rows][4] fp32.
+__device__ __forceinline__ float4* ff_partial(const FfLaunch& l, int cut, int part, int slab, int lane) {
+    return reinterpret_cast<float4*>(l.partial + (((size_t)cut * l.parts + part) * 16 + slab) * 4096) + lane;
+}
+// A part of a cut tile: keeps this warp's sums and counts them as done. In the part that comes last,
+// all parts' sums are added up in their order, put back into the accumulator, and the warp goes on to
+// finish its values (true). Nothing waits for another CTA.
+template <int MODE>
+__device__ __forceinline__ bool ff_collect(const FfLaunch& l, const FfTile& t, uint32_t tb, int half, int slab, int lane) {
     float4* o = ff_partial(l, t.cut, t.part, slab, lane);
 #pragma unroll 1
-    for (int c = 0; c < 8; ++c) {
+    for (int i = 0; i < 4; ++i) {
         uint32_t v[32];
-        tmem_ld32(tb + c * 32, v);
+        tmem_ld32(tb + ff_chunk<MODE>(half, i) * 32, v);
 #pragma unroll
-        for (int i = 0; i < 8; ++i)
-            __stcg(o + c * 256 + i * 32, make_float4(__uint_as_float(v[4 * i]), __uint_as_float(v[4 * i + 1]),
-                                                     __uint_as_float(v[4 * i + 2]), __uint_as_float(v[4 * i + 3])));
+        for (int k = 0; k < 8; ++k)
+            __stcg(o + i * 256 + k * 32, make_float4(__uint_as_float(v[4 * k]), __uint_as_float(v[4 * k + 1]),
+                                                     __uint_as_float(v[4 * k + 2]), __uint_as_float(v[4 * k + 3])));
     }
     __threadfence();
     __syncwarp();
     uint32_t before = 0;
     if (lane == 0) {
-        uint32_t* count = l.arrived + t.cut * 8 + slab;
+        uint32_t* count = l.arrived + t.cut * 16 + slab;
         before = atom_acq_rel_gpu_add(count, 1u);
         if (before + 1 == (uint32_t)l.parts) *count = 0;  // for the next launch
     }
     before = __shfl_sync(0xffffffffu, before, 0);
+    if (before + 1 != (uint32_t)l.parts) return false;
     __threadfence();
-    return before + 1 == (uint32_t)l.parts;
-}
-// 32 columns of this warp's rows: the accumulator, or the sum over a cut tile's parts in their order
-// (each part's loads are in flight while the one before is added).
-__device__ __forceinline__ void ff_chunk(const FfLaunch& l, const FfTile& t, uint32_t tb, int c, int slab, int lane,
-                                         uint32_t (&v)[32]) {
-    if (t.cut < 0) {
-        tmem_ld32(tb + c * 32, v);
-        return;
-    }
-    float4 next[8];
-    auto load = [&](int q) {
-        if (q >= l.parts || q == t.part) return;
-        const float4* o = ff_partial(l, t.cut, q, slab, lane) + c * 256;
+#pragma unroll 1
+    for (int i = 0; i < 4; ++i) {
+        uint32_t v[32];
+        float4 next[8];  // a part's sums are in flight while the one before is added
+        auto load = [&](int q) {
+            if (q >= l.parts || q == t.part) return;
+            const float4* from = ff_partial(l, t.cut, q, slab, lane) + i * 256;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) next[i] = __ldcg(o + i * 32);
-    };
-    load(0);
-    tmem_ld32(tb + c * 32, v);
-    float sum[32];
+            for (int k = 0; k < 8; ++k) next[k] = __ldcg(from + k * 32);
+        };
+        load(0);
+        tmem_ld32(tb + ff_chunk<MODE>(half, i) * 32, v);
+        float sum[32];
 #pragma unroll
-    for (int i = 0; i < 32; ++i) sum[i] = 0.f;
-    for (int q = 0; q < l.parts; ++q) {
-        float4 cur[8];
+        for (int k = 0; k < 32; ++k) sum[k] = 0.f;
+        for (int q = 0; q < l.parts; ++q) {
+            float4 cur[8];
 #pragma unroll
-        for (int i = 0; i < 8; ++i)
-            cur[i] = q == t.part ? make_float4(__uint_as_float(v[4 * i]), __uint_as_float(v[4 * i + 1]),
-                                               __uint_as_float(v[4 * i + 2]), __uint_as_float(v[4 * i + 3]))
-                                 : next[i];
-        load(q + 1);
+            for (int k = 0; k < 8; ++k)
+                cur[k] = q == t.part ? make_float4(__uint_as_float(v[4 * k]), __uint_as_float(v[4 * k + 1]),
+                                                   __uint_as_float(v[4 * k + 2]), __uint_as_float(v[4 * k + 3]))
+                                     : next[k];
+            load(q + 1);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            sum[4 * i] += cur[i].x;
-            sum[4 * i + 1] += cur[i].y;
-            sum[4 * i + 2] += cur[i].z;
-            sum[4 * i + 3] += cur[i].w;
+            for (int k = 0; k < 8; ++k) {
+                sum[4 * k] += cur[k].x;
+                sum[4 * k + 1] += cur[k].y;
+                sum[4 * k + 2] += cur[k].z;
+                sum[4 * k + 3] += cur[k].w;
+            }
         }
-    }
 #pragma unroll
-    for (int i = 0; i < 32; ++i) v[i] = __float_as_uint(sum[i]);
+        for (int k = 0; k < 32; ++k) v[k] = __float_as_uint(sum[k]);
+        __syncwarp();
+        tmem_st32(tb + ff_chunk<MODE>(half, i) * 32, v);
+    }
+    return true;
 }
 
 // Kept g and u of 16 columns of this warp's rows, fetched ahead of their use.
 struct FfKept {
     float4 g[4], u[4];
-    __device__ __forceinline__ void load(const FfLaunch& l, const FfTile& t, int row0, int half, int lane) {
-        const int col0 = t.n * FT_N + (half & ~1) * 16;
-        if (row0 >= t.M || half >= 16 || col0 >= t.N) return;
-        const float4 *ig = ff_gu(l, row0, col0, 0, lane) + (half & 1) * 128, *iu = ff_gu(l, row0, col0, 1, lane) + (half & 1) * 128;
+    // the k-th 16 of a warp's 128 columns
+    __device__ __forceinline__ void load(const FfLaunch& l, const FfTile& t, int row0, int half, int k, int lane) {
+        const int col0 = t.n * FT_N + half * 128 + (k & ~1) * 16;
+        if (row0 >= t.M || k >= 8 || col0 >= t.N) return;
+        const float4 *ig = ff_gu(l, row0, col0, 0, lane) + (k & 1) * 128, *iu = ff_gu(l, row0, col0, 1, lane) + (k & 1) * 128;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             g[i] = __ldcs(ig + i * 32);
@@ -334,18 +357,18 @@ struct FfKept {
 
 template <int MODE>
 __device__ __forceinline__ void ff_epilogue(const FfLaunch& l, const FfTile& t, FfStage& es, uint32_t tb, int row0,
-                                            int slab, int lane, FfKept& next) {
+                                            int half, int slab, int lane, FfKept& next) {
     const CUtensorMap* out = t.p->out;
     if (row0 >= t.M) return;
-    if (t.cut >= 0 && !ff_arrive(l, t, tb, slab, lane)) return;
+    if (t.cut >= 0 && !ff_collect<MODE>(l, t, tb, half, slab, lane)) return;
     if (MODE == FF_SWIGLU) {
 #pragma unroll 1
-        for (int c = 0; c < 4; ++c) {
+        for (int c = 2 * half; c < 2 * half + 2; ++c) {
             const int col0 = t.n * 128 + c * 32;
             if (col0 >= t.N) return;
             uint32_t g[32], u[32];
-            ff_chunk(l, t, tb, c, slab, lane, g);
-            ff_chunk(l, t, tb, c + 4, slab, lane, u);
+            tmem_ld32(tb + c * 32, g);
+            tmem_ld32(tb + 128 + c * 32, u);
             uint32_t pk[16];
 #pragma unroll
             for (int i = 0; i < 16; ++i) {
@@ -367,16 +390,16 @@ __device__ __forceinline__ void ff_epilogue(const FfLaunch& l, const FfTile& t, 
         }
     } else if (MODE == FF_DACT) {
 #pragma unroll 1
-        for (int c = 0; c < 8; ++c) {
-            const int col0 = t.n * FT_N + c * 32;
+        for (int c = 0; c < 4; ++c) {
+            const int col0 = t.n * FT_N + half * 128 + c * 32;
             if (col0 >= t.N) return;
             uint32_t d[32];
-            ff_chunk(l, t, tb, c, slab, lane, d);
+            tmem_ld32(tb + (4 * half + c) * 32, d);
             uint32_t pg[16], pu[16];
 #pragma unroll
-            for (int half = 0; half < 2; ++half) {
+            for (int h = 0; h < 2; ++h) {
                 const FfKept k = next;
-                next.load(l, t, row0, 2 * c + half + 1, lane);
+                next.load(l, t, row0, half, 2 * c + h + 1, lane);
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
                     const float gv[4] = {k.g[i].x, k.g[i].y, k.g[i].z, k.g[i].w};
@@ -384,14 +407,14 @@ __device__ __forceinline__ void ff_epilogue(const FfLaunch& l, const FfTile& t, 
                     float dg[4], du[4];
 #pragma unroll
                     for (int j = 0; j < 4; ++j) {
-                        const float dh = __uint_as_float(d[half * 16 + 4 * i + j]), s = ff_sigmoid(gv[j]);
+                        const float dh = __uint_as_float(d[h * 16 + 4 * i + j]), s = ff_sigmoid(gv[j]);
                         du[j] = dh * (gv[j] * s);
                         dg[j] = dh * uv[j] * (s * (1.0f + gv[j] * (1.0f - s)));
                     }
-                    pg[half * 8 + 2 * i] = pack_bf16x2(dg[0], dg[1]);
-                    pg[half * 8 + 2 * i + 1] = pack_bf16x2(dg[2], dg[3]);
-                    pu[half * 8 + 2 * i] = pack_bf16x2(du[0], du[1]);
-                    pu[half * 8 + 2 * i + 1] = pack_bf16x2(du[2], du[3]);
+                    pg[h * 8 + 2 * i] = pack_bf16x2(dg[0], dg[1]);
+                    pg[h * 8 + 2 * i + 1] = pack_bf16x2(dg[2], dg[3]);
+                    pu[h * 8 + 2 * i] = pack_bf16x2(du[0], du[1]);
+                    pu[h * 8 + 2 * i + 1] = pack_bf16x2(du[2], du[3]);
                 }
             }
             es.put(out, pg, col0, row0, lane);
@@ -399,11 +422,11 @@ __device__ __forceinline__ void ff_epilogue(const FfLaunch& l, const FfTile& t, 
         }
     } else {
 #pragma unroll 1
-        for (int c = 0; c < 8; ++c) {
+        for (int c = 4 * half; c < 4 * half + 4; ++c) {
             const int col0 = t.n * FT_N + c * 32;
             if (col0 >= t.N) return;
             uint32_t v[32], pk[16];
-            ff_chunk(l, t, tb, c, slab, lane, v);
+            tmem_ld32(tb + c * 32, v);
 #pragma unroll
             for (int i = 0; i < 16; ++i) pk[i] = pack_bf16x2(__uint_as_float(v[2 * i]), __uint_as_float(v[2 * i + 1]));
             es.put(out, pk, col0, row0, lane);
@@ -424,11 +447,11 @@ __device__ __forceinline__ void ff_forms(int form, F f) {
 
 // Persistent GEMM on CTA pairs: cluster c takes tiles c, c + clusters, ... of the launch's list.
 // Warp 0: TMA loads (each CTA its 128 rows of A and 128 of B; both CTAs' loads complete on rank 0's
-// stage barrier). Warp 1: TMEM, and on rank 0 the UMMAs. Warps 2-5: epilogue of the CTA's 128 rows,
+// stage barrier). Warp 1: TMEM, and on rank 0 the UMMAs. Warps 2-9: epilogue of the CTA's 128 rows,
 // overlapping the next tile's products through two accumulators. Every wait is bounded; one that
 // runs out raises the pair's abort word and the status word, and the loads in flight are settled.
 template <int MODE>
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(GEMM_THREADS, 1)
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(FF_THREADS, 1)
     dense_kernel(const __grid_constant__ FfLaunch l) {
     extern __shared__ uint8_t smem_raw[];
     const FfSmem sm = ff_carve(smem_raw);
@@ -443,7 +466,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(GEMM_THREADS, 1)
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(&sm.acc_full[i], 1);
-            mbar_init(&sm.acc_empty[i], 8);
+            mbar_init(&sm.acc_empty[i], 2 * FF_WARPS);
         }
         mbar_init(sm.drain, 1);
         *sm.abort = 0;
@@ -530,7 +553,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(GEMM_THREADS, 1)
         int never = 0;
         if (!mbar_wait(sm.drain, 0, tmo, &never) && !*sm.abort) ff_status(l.status, 14 + (int)rank);
     } else if (warp >= 2) {
-        const int q = warp & 3;
+        const int q = warp & 3, half = (warp - 2) >> 2;
         FfStage es{sm.epi + (warp - 2) * 2 * EPI_CHUNK_BYTES, 0};
         const uint32_t acc_empty0 = mapa_shared(smem_u32(sm.acc_empty), 0u);
         int b = 0;
@@ -539,7 +562,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(GEMM_THREADS, 1)
             const FfTile tr = ff_tile(l, t);
             const int row0 = tr.m * FT_M + (int)rank * 128 + q * 32;
             FfKept kept;
-            if (MODE == FF_DACT) kept.load(l, tr, row0, 0, lane);
+            if (MODE == FF_DACT) kept.load(l, tr, row0, half, 0, lane);
             if (!mbar_wait(&sm.acc_full[b], aph, tmo, sm.abort)) {
                 if (!*sm.abort) ff_status(l.status, 16 + (int)rank);
                 if (lane == 0) ff_abort(sm, rank);
@@ -548,7 +571,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(GEMM_THREADS, 1)
             tc_fence_after();
             __syncwarp();
             const uint32_t tb = tmem + ((uint32_t)(q * 32) << 16) + (uint32_t)(b * 256);
-            ff_epilogue<MODE>(l, tr, es, tb, row0, (int)rank * 4 + q, lane, kept);
+            ff_epilogue<MODE>(l, tr, es, tb, row0, half, (int)rank * FF_WARPS + warp - 2, lane, kept);
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive_cluster(acc_empty0 + b * 8u);
@@ -880,7 +903,7 @@ __global__ void __launch_bounds__(GEMM_THREADS, 1) flex_kernel(const __grid_cons
 
 // Parts of cut tiles in a launch, and words of the status area: [0] status, [1] detail, [128...] arrivals.
 constexpr int FF_MAX_CUT = 160, FF_ARRIVED = 128;
-static_assert((FF_ARRIVED + FF_MAX_CUT / 2 * 8) * 4 <= MOE_FFN_STATUS_BYTES, "arrival counts");
+static_assert((FF_ARRIVED + FF_MAX_CUT / 2 * 2 * FF_WARPS) * 4 <= MOE_FFN_STATUS_BYTES, "arrival counts");
 
 struct FfLayout {
     size_t T, d, F;
@@ -1022,7 +1045,7 @@ cudaError_t ff_clusters(int* out) {
         if (e != cudaSuccess) return e;
         cudaLaunchConfig_t q = {};
         q.gridDim = dim3(2, 1, 1);
-        q.blockDim = dim3(GEMM_THREADS, 1, 1);
+        q.blockDim = dim3(FF_THREADS, 1, 1);
         q.dynamicSmemBytes = FF_SMEM;
         int n = 0;
         e = cudaOccupancyMaxActiveClusters(&n, fn, &q);
@@ -1052,7 +1075,7 @@ int ff_run(FfList& list, const FfLayout& L, void* ws, cudaStream_t st, const cha
         l.parts = cut.parts;
         l.units = cut.full + (l.tiles - cut.full) * cut.parts;
         const int n = l.units < clusters ? l.units : clusters;
-        e = launch_k(dense_kernel<MODE>, dim3(2 * n), dim3(GEMM_THREADS), FF_SMEM, st, true, list.l);
+        e = launch_k(dense_kernel<MODE>, dim3(2 * n), dim3(FF_THREADS), FF_SMEM, st, true, list.l);
     }
     return e == cudaSuccess ? MOE_OK : cuda_fail(e, what);
 }
