@@ -509,7 +509,8 @@ MOE_API int moe_layernorm_backward(const moe_layernorm_config* cfg, const void* 
  * of a tensor, one byte a value and one scale byte a block for each; scale byte s stands for
  * 2^(s - 127), 0 for 0 and 255 for NaN (a block that a non-finite value has entered reads as NaN).
  * A byte of m is sign, 4 exponent bits (bias 7) and 3 mantissa bits; a byte of v 5 exponent bits
- * (bias 15) and 3 mantissa bits; exponent 0 is subnormal. A zeroed buffer is a zero state. p is
+ * (bias 15) and 3 mantissa bits; exponent 0 is subnormal; a step
+ * writes no magnitude above 0x78 (m) and 0xF8 (v). A zeroed buffer is a zero state. p is
  * updated from m and v before they are rounded. The rounding is stochastic (unbiased), so an average
  * that moves by less than a rounding step a call still moves: up or down is decided by 16 bits of a
  * hash of (seed, step, rng_base + i) for value i, so the result repeats for the same arguments.

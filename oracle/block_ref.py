@@ -76,8 +76,8 @@ def noise(n, seed, step, base=0):
     """32 random bits for each of values base .. base + n - 1."""
     k0 = mix32((seed & 0xFFFFFFFF) ^ (step & 0xFFFFFFFF), seed >> 32 & 0xFFFFFFFF)
     k1 = mix32(k0 ^ 0x9E3779B9, step >> 32 & 0xFFFFFFFF)
-    return np.array([mix32((base + i & 0xFFFFFFFF) ^ k0, k1 + (base + i >> 32) * 0x9E3779B9 & 0xFFFFFFFF)
-                     for i in range(n)], np.int64)
+    i = base + np.arange(n, dtype=np.int64)
+    return mix32((i & 0xFFFFFFFF) ^ k0, k1 + (i >> 32) * 0x9E3779B9 & 0xFFFFFFFF)
 
 
 def _formats(name):
@@ -98,24 +98,23 @@ def decode(codes, scales, name):
 
 
 def encode(x, r16, name):
-    """codes and scales of fp32 values x with 16 random bits each (stochastic rounding)."""
+    """Codes and scales of fp32 values x with 16 random bits each (stochastic rounding)."""
     top, bias, ebits, signed = _formats(name)
-    n, codes, scales = len(x), [], []
-    for at in range(0, n, BLOCK):
-        b, r = x[at:at + BLOCK].astype(np.float64), r16[at:at + BLOCK]
-        most = np.abs(b).max()
-        if not np.isfinite(most):
-            scales.append(255)
-            codes += [0] * len(b)
-            continue
-        k = int(np.floor(np.log2(most))) - top if most >= 2.0 ** -126 else -127 - top
-        k = max(k, -126)
-        scales.append(k + 127)
-        y = np.abs(b) * 2.0 ** -k
-        e = np.maximum(np.floor(np.log2(np.maximum(y, 2.0 ** -200))), 1 - bias)
-        q = np.floor(y / 2.0 ** (e - 3) + (r + 0.5) / 65536).astype(np.int64)  # 0 .. 16 steps of 2^(e-3)
-        code = np.where(q >= 8, ((e + bias).astype(np.int64) << 3) + (q - 8), q)
-        if signed:
-            code = np.where(np.signbit(b), code | 0x80, code)
-        codes += code.tolist()
-    return np.array(codes, np.uint8), np.array(scales, np.uint8)
+    n, blocks = len(x), -(-len(x) // BLOCK)
+    b = np.zeros(blocks * BLOCK)
+    b[:n] = x
+    r = np.zeros(blocks * BLOCK)
+    r[:n] = r16
+    b, r = b.reshape(blocks, BLOCK), r.reshape(blocks, BLOCK)
+    most = np.abs(b).max(1)
+    fine = np.isfinite(most)
+    k = np.frexp(np.where(fine & (most >= 2.0 ** -126), most, 2.0 ** -127))[1] - 1 - top  # floor(log2) - top
+    k = np.maximum(k, -126)
+    y = np.abs(np.where(fine[:, None], b, 0.0)) * 2.0 ** -k[:, None].astype(float)
+    e = np.maximum(np.frexp(y)[1] - 1, 1 - bias)
+    q = np.floor(y / 2.0 ** (e - 3.0) + (r + 0.5) / 65536).astype(np.int64)  # 0 .. 16 steps of 2^(e-3)
+    code = np.where(q >= 8, ((e + bias) << 3) + (q - 8), q)
+    if signed:
+        code = np.where(np.signbit(b), code | 0x80, code)
+    code = np.where(fine[:, None], code, 0).reshape(-1)[:n]
+    return code.astype(np.uint8), np.where(fine, k + 127, 255).astype(np.uint8)

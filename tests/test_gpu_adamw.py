@@ -46,6 +46,7 @@ def tensors(sizes, pt, gt, bits, seed=0, shift=0):
     return p, gr, m, v, ms, vs
 
 
+BIG = [1 << 20]  # one last bit of m or v that differs shows in a code once in some 50,000 values
 SIZES = [[1], [127, 128, 129], [3, 0, 5000, 4096, 4097, 1, 12289], [100] * 40, [17 + i for i in range(400)]]
 
 
@@ -74,7 +75,7 @@ def test_32_bits(sizes, pt, gt, copy, shift):
 
 @pytest.mark.parametrize("shift", [0, 3])
 @pytest.mark.parametrize("pt,gt", [(F32, BF), (F32, F32), (BF, BF)])
-@pytest.mark.parametrize("sizes", SIZES[:4])
+@pytest.mark.parametrize("sizes", SIZES[:4] + [BIG])
 def test_8_bits_equal_the_oracle(sizes, pt, gt, shift):
     p, g, m, v, ms, vs = tensors(sizes, pt, gt, 8, len(sizes), shift)
     base = [5 + (1 << 33) * i for i in range(len(sizes))]
@@ -97,7 +98,7 @@ def test_8_bits_equal_the_oracle(sizes, pt, gt, shift):
             wc, wsc = ref.encode(x, bits, name)
             np.testing.assert_array_equal(scales[i].cpu().numpy(), wsc)
             np.testing.assert_array_equal(codes[i].cpu().numpy(), wc)
-            np.testing.assert_array_equal(read[i].cpu().numpy(), ref.decode(wc, wsc, name).astype(np.float32))
+            assert np.array_equal(read[i].cpu().numpy(), ref.decode(wc, wsc, name).astype(np.float32))
         wp, _, wv = ref.adamw_step(p0[i], g0[i], dm.astype(np.float64), dv.astype(np.float64), step=step, **HYPER)
         den = np.sqrt(wv / (1 - 0.999 ** step)) + 1e-8
         far = 2.0 ** -23 * np.abs(p0[i]) + 2.0 ** -20 * (np.abs(wp - p0[i]) + 1e-4 * np.abs(p0[i])) + \

@@ -17,6 +17,7 @@
 // with a probability equal to the part that is cut off. A value scaled to its code's exponent
 // range is an fp32 number whose top bits are the code (subnormal codes are subnormal fp32 numbers),
 // so encoding is: add 20 random bits to the bit pattern, shift right by 20.
+#include <cuda_fp16.h>
 #include <math.h>
 
 #include "host_internal.h"
@@ -56,6 +57,7 @@ struct AwScalars {
     float b1, b1c, b2, b2c;  // beta1, 1 - beta1, beta2, 1 - beta2
     float decay, step, vscale, eps;
     uint32_t k0, k1;
+    int flush;  // eps is large enough for roots of subnormal values to be taken as zero
     const float* grad_scale;
 };
 
@@ -254,6 +256,221 @@ __device__ __forceinline__ void chunk_step(const AwTensor& t, uint32_t flags, co
     }
 }
 
+// ---- whole chunks of aligned tensors ----------------------------------------------------------------
+// The same arithmetic two values at a time (f32x2, each operation rounded to nearest, none contracted),
+// with the 8-bit form's bit work cut down: with it unvectorised the step took 101 instructions a value and
+// was bound by them (647 us for 149 M values against 350 us of memory traffic).
+typedef unsigned long long f2;
+__device__ __forceinline__ f2 pair2(float lo, float hi) {
+    f2 r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+    return r;
+}
+__device__ __forceinline__ float2 split2(f2 v) {
+    float2 r;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
+    return r;
+}
+// Sums of products, one by one: as f32x2 additions they came out contracted with the products (a code in
+// 50,000 differed), which __fadd_rn rules out.
+__device__ __forceinline__ f2 sum2(f2 a, f2 b) {
+    const float2 x = split2(a), y = split2(b);
+    return pair2(__fadd_rn(x.x, y.x), __fadd_rn(x.y, y.y));
+}
+__device__ __forceinline__ f2 mul2(f2 a, f2 b) {
+    f2 r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ f2 fma2(f2 a, f2 b, f2 c) {
+    f2 r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+__device__ __forceinline__ float max_abs_nan(float a, float b) {  // the larger magnitude, NaN if either is
+    float r;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(fabsf(a)), "f"(fabsf(b)));
+    return r;
+}
+
+// Four consecutive values: p, g (fp32 or bf16, as bits) and their states' bits.
+template <bool EIGHT, bool P16, bool G16>
+struct AwFour {
+    uint4 p, g, m, v;
+    uint32_t ms, vs;
+    __device__ __forceinline__ void load(const AwTensor& t, int64_t i) {
+        if (P16) {
+            const uint2 q = __ldcs(reinterpret_cast<const uint2*>(static_cast<const __nv_bfloat16*>(t.p) + i));
+            p.x = q.x, p.y = q.y;
+        } else {
+            p = __ldcs(reinterpret_cast<const uint4*>(static_cast<const float*>(t.p) + i));
+        }
+        if (G16) {
+            const uint2 q = __ldcs(reinterpret_cast<const uint2*>(static_cast<const __nv_bfloat16*>(t.g) + i));
+            g.x = q.x, g.y = q.y;
+        } else {
+            g = __ldcs(reinterpret_cast<const uint4*>(static_cast<const float*>(t.g) + i));
+        }
+        if (EIGHT) {
+            m.x = __ldcs(reinterpret_cast<const uint32_t*>(static_cast<const uint8_t*>(t.m) + i));
+            v.x = __ldcs(reinterpret_cast<const uint32_t*>(static_cast<const uint8_t*>(t.v) + i));
+            ms = t.ms[i / AW_BLOCK];
+            vs = t.vs[i / AW_BLOCK];
+        } else {
+            m = __ldcs(reinterpret_cast<const uint4*>(static_cast<const float*>(t.m) + i));
+            v = __ldcs(reinterpret_cast<const uint4*>(static_cast<const float*>(t.v) + i));
+        }
+    }
+    template <bool B16>
+    static __device__ __forceinline__ void widen(const uint4& q, f2 (&o)[2]) {
+        if (B16) {
+            o[0] = pair2(__uint_as_float(q.x << 16), __uint_as_float(q.x & 0xffff0000u));
+            o[1] = pair2(__uint_as_float(q.y << 16), __uint_as_float(q.y & 0xffff0000u));
+        } else {
+            o[0] = pair2(__uint_as_float(q.x), __uint_as_float(q.y));
+            o[1] = pair2(__uint_as_float(q.z), __uint_as_float(q.w));
+        }
+    }
+    // codes of m: two bytes are two fp8 (e4m3) values
+    static __device__ __forceinline__ void widen_m(uint32_t q, uint32_t scale, f2 (&o)[2]) {
+        const float f = scale_value(scale);
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            uint32_t w;
+            asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(w) : "h"((uint16_t)(q >> (16 * h))));
+            const float2 x = __half22float2(*reinterpret_cast<const __half2*>(&w));
+            o[h] = mul2(pair2(x.x, x.y), pair2(f, f));
+        }
+    }
+    static __device__ __forceinline__ void widen_v(uint32_t q, uint32_t scale, f2 (&o)[2]) {
+        // byte j at bits 20-27: an fp32 number that is 2^-112 of the code's
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const float a = __uint_as_float(__byte_perm(q, 0, h ? 0x4244 : 0x4044) << 4);
+            const float b = __uint_as_float(__byte_perm(q, 0, h ? 0x4344 : 0x4144) << 4);
+            const f2 x = pair2(a, b);
+            if (scale - 1u < 142u) {  // 2^112 and the scale in one factor
+                const float f = __uint_as_float((scale + 112u) << 23);
+                o[h] = mul2(x, pair2(f, f));
+            } else {
+                const float f = scale_value(scale);
+                o[h] = mul2(mul2(x, pair2(0x1p112f, 0x1p112f)), pair2(f, f));
+            }
+        }
+    }
+    __device__ __forceinline__ void step(const AwTensor& t, const AwScalars& s, float gs, int64_t i) {
+        f2 P[2], G[2], M[2], V[2];
+        widen<P16>(p, P);
+        widen<G16>(g, G);
+        if (EIGHT) {
+            widen_m(m.x, ms, M);
+            widen_v(v.x, vs, V);
+        } else {
+            widen<false>(m, M);
+            widen<false>(v, V);
+        }
+        const f2 scale = pair2(gs, gs), b1 = pair2(s.b1, s.b1), b1c = pair2(s.b1c, s.b1c), b2 = pair2(s.b2, s.b2);
+        const f2 b2c = pair2(s.b2c, s.b2c), vscale = pair2(s.vscale, s.vscale), eps = pair2(s.eps, s.eps);
+        const f2 decay = pair2(s.decay, s.decay), back = pair2(-s.step, -s.step);
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const f2 a = mul2(G[h], scale);
+            M[h] = sum2(mul2(M[h], b1), mul2(a, b1c));
+            V[h] = sum2(mul2(V[h], b2), mul2(mul2(a, a), b2c));
+            const float2 v = split2(V[h]);
+            const float2 d = split2(fma2(pair2(root(s, v.x), root(s, v.y)), vscale, eps));
+            const f2 u = mul2(M[h], pair2(inverse(s, d.x), inverse(s, d.y)));
+            P[h] = fma2(P[h], decay, mul2(u, back));
+        }
+        const float2 p0 = split2(P[0]), p1 = split2(P[1]);
+        const uint2 p16 = make_uint2(pack_bf16x2(p0.x, p0.y), pack_bf16x2(p1.x, p1.y));
+        if (P16) __stcs(reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(t.p) + i), p16);
+        else __stcs(reinterpret_cast<float4*>(static_cast<float*>(t.p) + i), make_float4(p0.x, p0.y, p1.x, p1.y));
+        if (t.copy) __stcs(reinterpret_cast<uint2*>(t.copy + i), p16);
+        const float2 m0 = split2(M[0]), m1 = split2(M[1]), v0 = split2(V[0]), v1 = split2(V[1]);
+        if (!EIGHT) {
+            __stcs(reinterpret_cast<float4*>(static_cast<float*>(t.m) + i), make_float4(m0.x, m0.y, m1.x, m1.y));
+            __stcs(reinterpret_cast<float4*>(static_cast<float*>(t.v) + i), make_float4(v0.x, v0.y, v1.x, v1.y));
+            return;
+        }
+        const float mm = max_abs_nan(max_abs_nan(m0.x, m0.y), max_abs_nan(m1.x, m1.y));
+        const float vm = max_abs_nan(max_abs_nan(v0.x, v0.y), max_abs_nan(v1.x, v1.y));
+        const uint32_t sm = block_scale(__reduce_max_sync(0xffffffffu, __float_as_uint(mm)), M_TOP);
+        const uint32_t sv = block_scale(__reduce_max_sync(0xffffffffu, __float_as_uint(vm)), V_TOP);
+        uint32_t mb[4], vb[4];
+        shifted(M, sm, 7u, 0x1p-120f, mb);
+        shifted(V, sv, 15u, 0x1p-112f, vb);
+        const uint64_t idx = (uint64_t)(t.base + i);
+        const uint32_t lo = (uint32_t)idx, key = s.k1 + (uint32_t)(idx >> 32) * 0x9E3779B9u;
+        const uint32_t wrap = lo > 0xfffffffcu ? 0x9E3779B9u : 0u;  // the index's low word overflows within the four
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const uint32_t e = lo + j;
+            const uint32_t r = mix32(e ^ s.k0, wrap && e < lo ? key + wrap : key);
+            // code to the top byte: m's 7 bits come from 20-26 and its sign stays, v's 8 from 20-27
+            const uint32_t a = mb[j] + ((r << 4) & 0xffff0u) + 8u;
+            mb[j] = ((a << 4) & 0x7f000000u) | (a & 0x80000000u);
+            vb[j] = (vb[j] + ((r >> 12) & 0xffff0u) + 8u) << 4;
+        }
+        const uint32_t mc = __byte_perm(__byte_perm(mb[0], mb[1], 0x0073), __byte_perm(mb[2], mb[3], 0x0073), 0x5410);
+        const uint32_t vc = __byte_perm(__byte_perm(vb[0], vb[1], 0x0073), __byte_perm(vb[2], vb[3], 0x0073), 0x5410);
+        __stcs(reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(t.m) + i), sm == 255u ? 0u : mc);
+        __stcs(reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(t.v) + i), sv == 255u ? 0u : vc);
+        if ((threadIdx.x & 31) == 0) {
+            t.ms[i / AW_BLOCK] = (uint8_t)sm;
+            t.vs[i / AW_BLOCK] = (uint8_t)sv;
+        }
+    }
+    // Values over their scale, times `down` (2^-(127 - bias)): the bits that encoding starts from. Both
+    // factors are one, 2^(bias - scale), where it is a normal number.
+    static __device__ __forceinline__ void shifted(const f2 (&x)[2], uint32_t scale, uint32_t bias, float down, uint32_t (&o)[4]) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            f2 y;
+            if (scale < 127u + bias) {
+                const float f = __uint_as_float((127u + bias - scale) << 23);
+                y = mul2(x[h], pair2(f, f));
+            } else {
+                const float f = inverse_scale(scale);
+                y = mul2(mul2(x[h], pair2(f, f)), pair2(down, down));
+            }
+            const float2 z = split2(y);
+            o[2 * h] = __float_as_uint(z.x);
+            o[2 * h + 1] = __float_as_uint(z.y);
+        }
+    }
+    // Square root and reciprocal to a few units of the last place, subnormals as zero where eps (at least
+    // 1e-10, against at most 2^-63 of a subnormal v's root) makes that invisible.
+    static __device__ __forceinline__ float root(const AwScalars& s, float v) {
+        float r;
+        if (s.flush) asm("sqrt.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
+        else asm("sqrt.approx.f32 %0, %1;" : "=f"(r) : "f"(v));
+        return r;
+    }
+    static __device__ __forceinline__ float inverse(const AwScalars& s, float v) {
+        float r;
+        if (s.flush) asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
+        else r = __fdividef(1.0f, v);
+        return r;
+    }
+};
+
+template <bool EIGHT, bool P16, bool G16>
+__device__ __forceinline__ void chunk_whole(const AwTensor& t, const AwScalars& s, float gs, int64_t at) {
+    // fours of a thread in flight: with 8-bit states 4 (488 us; 2: 641, and 707 with one more CTA a SM), with
+    // 32-bit states 1 in more CTAs (624 us; 2: 637, 4: 661)
+    constexpr int AHEAD = EIGHT ? 4 : 1;
+    const int64_t i = at + threadIdx.x * 4;
+#pragma unroll 1
+    for (int o = 0; o < AW_CHUNK; o += AW_THREADS * 4 * AHEAD) {
+        AwFour<EIGHT, P16, G16> f[AHEAD];
+#pragma unroll
+        for (int k = 0; k < AHEAD; ++k) f[k].load(t, i + o + k * AW_THREADS * 4);
+#pragma unroll
+        for (int k = 0; k < AHEAD; ++k) f[k].step(t, s, gs, i + o + k * AW_THREADS * 4);
+    }
+}
+
 template <int MAXT>
 __device__ __forceinline__ int tensor_of(const AwList<MAXT>& l, int c) {
     int lo = 0, hi = l.count - 1;  // the last tensor whose first chunk is at or before c
@@ -266,15 +483,19 @@ __device__ __forceinline__ int tensor_of(const AwList<MAXT>& l, int c) {
 }
 
 template <bool EIGHT, int MAXT>
-__global__ void __launch_bounds__(AW_THREADS) adamw_kernel(const __grid_constant__ AwList<MAXT> l, const AwScalars s) {
+__global__ void __launch_bounds__(AW_THREADS, EIGHT ? 3 : 5) adamw_kernel(const __grid_constant__ AwList<MAXT> l, const AwScalars s) {
     griddep_wait();
     griddep_launch();
     const float gs = s.grad_scale ? *s.grad_scale : 1.0f;
     for (int c = blockIdx.x; c < l.first[l.count]; c += gridDim.x) {
         const int i = tensor_of(l, c);
         const int64_t at = (int64_t)(c - l.first[i]) * AW_CHUNK;
-        if (l.flags[i] & AW_VEC) chunk_step<EIGHT, true>(l.t[i], l.flags[i], s, gs, at);
-        else chunk_step<EIGHT, false>(l.t[i], l.flags[i], s, gs, at);
+        const AwTensor t = l.t[i];
+        const uint32_t f = l.flags[i];
+        if (!(f & AW_VEC)) chunk_step<EIGHT, false>(t, f, s, gs, at);
+        else if (t.n - at < AW_CHUNK) chunk_step<EIGHT, true>(t, f, s, gs, at);
+        else if (f & AW_P16) (f & AW_G16) ? chunk_whole<EIGHT, true, true>(t, s, gs, at) : chunk_whole<EIGHT, true, false>(t, s, gs, at);
+        else (f & AW_G16) ? chunk_whole<EIGHT, false, true>(t, s, gs, at) : chunk_whole<EIGHT, false, false>(t, s, gs, at);
     }
 }
 
@@ -289,6 +510,33 @@ __global__ void __launch_bounds__(AW_THREADS) adamw_read_kernel(const __grid_con
         const int64_t at = (int64_t)(c - l.first[ti]) * AW_CHUNK, left = t.n - at;
         const int len = left < AW_CHUNK ? (int)left : AW_CHUNK;
         const bool vec = l.flags[ti] & AW_VEC;
+        if (vec && len == AW_CHUNK && t.p && t.copy) {  // whole chunks: 16 values of a thread in flight
+            constexpr int N = AW_CHUNK / (AW_THREADS * 4);
+            const int64_t i = at + threadIdx.x * 4;
+            uint32_t m[N], v[N];
+            float ms[N], vs[N];
+#pragma unroll
+            for (int k = 0; k < N; ++k) {
+                const int64_t e = i + k * AW_THREADS * 4;
+                m[k] = load4_u8<true>(t.m, e, 4);
+                v[k] = load4_u8<true>(t.v, e, 4);
+                ms[k] = scale_value(t.ms[e / AW_BLOCK]);
+                vs[k] = scale_value(t.vs[e / AW_BLOCK]);
+            }
+#pragma unroll
+            for (int k = 0; k < N; ++k) {
+                const int64_t e = i + k * AW_THREADS * 4;
+                Four a, b;
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    a.a[j] = m_value((m[k] >> (8 * j)) & 0xffu, ms[k]);
+                    b.a[j] = v_value((v[k] >> (8 * j)) & 0xffu, vs[k]);
+                }
+                store4_f32<true>(t.p, e, 4, a);
+                store4_f32<true>(t.copy, e, 4, b);
+            }
+            continue;
+        }
         for (int o = threadIdx.x * 4; o < len; o += AW_THREADS * 4) {
             const int k = min(4, len - o);
             const int64_t i = at + o, b = i / AW_BLOCK;
@@ -450,6 +698,7 @@ MOE_API int moe_adamw_step(const moe_adamw_config* c, const moe_adamw_tensor* ts
     s.step = (float)(c->lr / (1.0 - pow(c->beta1, (double)c->step)));
     s.vscale = (float)(1.0 / sqrt(1.0 - pow(c->beta2, (double)c->step)));
     s.eps = (float)c->eps;
+    s.flush = c->eps >= 1e-10 && c->eps < 1e30;
     s.k0 = mix32((uint32_t)c->seed ^ (uint32_t)c->step, (uint32_t)(c->seed >> 32));
     s.k1 = mix32(s.k0 ^ 0x9E3779B9u, (uint32_t)((uint64_t)c->step >> 32));
     s.grad_scale = grad_scale;
