@@ -965,7 +965,7 @@ int ff_operand(CUtensorMap* m, const void* ptr, uint64_t mn, uint64_t k, int alo
 struct FfList {
     FfLaunch l;
     int rc = MOE_OK;
-    FfList() {
+    FfList() {  // the products' maps are written as they are added, the others not at all
         l.count = l.tiles = 0;
         l.gu = nullptr;
         l.gu_cols = 0;
@@ -986,10 +986,11 @@ struct FfList {
         l.tiles += p.tiles_m * p.tiles_n;
         try_(ff_operand(&p.a[0], a, M, K, a_mn));
         try_(ff_operand(&p.b[0], b, N, K, b_mn));
-        try_(ff_operand(&p.a[1], a2 ? a2 : a, M, K, a_mn));
-        try_(ff_operand(&p.b[1], b2 ? b2 : b, N, K, b_mn));
+        if (a2) {
+            try_(ff_operand(&p.a[1], a2, M, K, a_mn));
+            try_(ff_operand(&p.b[1], b2, N, K, b_mn));
+        }
         try_(ff_map(&p.out[0], out, M, N, EPI_CHUNK, true));
-        p.out[1] = p.out[0];
         return p;
     }
     void try_(int r) {
@@ -1183,6 +1184,24 @@ FxArgs fx_args(size_t M, size_t T, int kb0, int kb, void* out, int early) {
     return p;
 }
 
+// The plans of a config's products.
+struct FfPlans {
+    int T, d, F, sms;
+    FxPlan up, act, down, dx;  // act: the hidden gradients, which take the kernel that h took
+};
+const FfPlans& ff_plans(const FfLayout& L, int sms) {
+    static thread_local FfPlans last[4] = {};  // a program alternates between few configs
+    static thread_local int turn = 0;
+    const int T = (int)L.T, d = (int)L.d, F = (int)L.F;
+    for (const FfPlans& p : last)
+        if (p.T == T && p.d == d && p.F == F && p.sms == sms) return p;
+    FfPlans& p = last[turn++ & 3];
+    const int kd = (d + BK - 1) / BK, kf = (F + BK - 1) / BK;
+    p = FfPlans{T, d, F, sms, ff_choose(F, T, kd, true, sms), ff_choose_flex(F, T, kd, false, sms),
+                ff_choose(d, T, kf, false, sms), ff_choose(d, T, 2 * kf, false, sms)};
+    return p;
+}
+
 int ff_begin(const moe_ffn_config* c, void* ws, size_t ws_bytes, FfLayout* L, int* sms) {
     clear_error();
     int rc = ff_layout(c, L);
@@ -1240,7 +1259,8 @@ MOE_API int moe_ffn_forward(const moe_ffn_config* c, const uint16_t* x, const ui
     // fixes the layout in which g and u are kept
     const int kd = (int)((L.d + BK - 1) / BK), kf = (int)((L.F + BK - 1) / BK);
     float* gu = s ? reinterpret_cast<float*>(s + L.saved_gu) : nullptr;
-    const FxPlan up_plan = ff_choose((int)L.F, (int)L.T, kd, true, sms);
+    const FfPlans& plans = ff_plans(L, sms);
+    const FxPlan& up_plan = plans.up;
     if (up_plan.nt) {
         FxArgs p = fx_args(L.F, L.T, kd, kd, h, 0);
         p.gu = reinterpret_cast<float2*>(gu);
@@ -1257,7 +1277,7 @@ MOE_API int moe_ffn_forward(const moe_ffn_config* c, const uint16_t* x, const ui
         up.l.gu_cols = L.gu_cols;
         if ((rc = ff_run<FF_SWIGLU>(up, L, ws, st, "gate and up projections"))) return rc;
     }
-    const FxPlan down_plan = ff_choose((int)L.d, (int)L.T, kf, false, sms);
+    const FxPlan& down_plan = plans.down;
     if (down_plan.nt) {
         FxArgs p = fx_args(L.d, L.T, kf, kf, y, 1);
         if ((rc = fx_operands(p, 0, W2, 0, h, L.d, L.T, L.F, down_plan.nt))) return rc;
@@ -1295,8 +1315,9 @@ MOE_API int moe_ffn_backward(const moe_ffn_config* c, const uint16_t* x, const u
     uint8_t* du = static_cast<uint8_t*>(ws) + L.du;
     const int kd = (int)((L.d + BK - 1) / BK), kf = (int)((L.F + BK - 1) / BK);
     float* gu = reinterpret_cast<float*>(const_cast<uint8_t*>(s) + L.saved_gu);
-    if (ff_choose((int)L.F, (int)L.T, kd, true, sms).nt) {  // the forward pass's choice
-        const FxPlan plan = ff_choose_flex((int)L.F, (int)L.T, kd, false, sms);
+    const FfPlans& plans = ff_plans(L, sms);
+    if (plans.up.nt) {  // the forward pass's choice
+        const FxPlan& plan = plans.act;
         FxArgs p = fx_args(L.F, L.T, kd, kd, dg, 0);
         p.out1 = reinterpret_cast<__nv_bfloat16*>(du);
         p.gu = reinterpret_cast<float2*>(gu);
@@ -1311,7 +1332,7 @@ MOE_API int moe_ffn_backward(const moe_ffn_config* c, const uint16_t* x, const u
         if ((rc = ff_run<FF_DACT>(act, L, ws, st, "hidden gradients"))) return rc;
     }
     FfList grad;
-    const FxPlan dx_plan = ff_choose((int)L.d, (int)L.T, 2 * kf, false, sms);
+    const FxPlan& dx_plan = plans.dx;
     if (dx_plan.nt) {
         FxArgs p = fx_args(L.d, L.T, kf, 2 * kf, dx, 1);
         if ((rc = fx_operands(p, 0, W1, 1, dg, L.d, L.T, L.F, dx_plan.nt))) return rc;

@@ -215,12 +215,22 @@ PlanPtrs plan_ptrs(const moe_layout& L, void* ws) {
 int device_info(DeviceInfo* di) {
     int dev = 0, major = 0, minor = 0, sms = 0;
     cudaError_t e = cudaGetDevice(&dev);
-    if (e == cudaSuccess) e = cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, dev);
+    if (e != cudaSuccess) return cuda_fail(e, "device query");
+    // a device's answers do not change: bit 0 known, bit 1 supported, the rest the SMs
+    static std::atomic<int> known[64];
+    const bool listed = dev >= 0 && dev < 64;
+    if (const int k = listed ? known[dev].load(std::memory_order_relaxed) : 0) {
+        di->sms = k >> 2;
+        di->supported = k & 2;
+        return MOE_OK;
+    }
+    e = cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, dev);
     if (e == cudaSuccess) e = cudaDeviceGetAttribute(&minor, cudaDevAttrComputeCapabilityMinor, dev);
     if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
     if (e != cudaSuccess) return cuda_fail(e, "device query");
     di->sms = sms;
     di->supported = (major == 10 && minor == 3);
+    if (listed) known[dev].store(sms << 2 | (di->supported ? 2 : 0) | 1, std::memory_order_relaxed);
     return MOE_OK;
 }
 
