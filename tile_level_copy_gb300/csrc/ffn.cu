@@ -26,14 +26,13 @@ namespace moe {
 namespace {
 
 constexpr int FT_M = 256, FT_N = 256;   // tile of a CTA pair
-constexpr int FF_STAGES = 6;
+constexpr int FF_STAGES = 7;
 constexpr int FF_HALF = 128 * BK * 2;   // one CTA's half of an operand's stage: 16 KB
 constexpr int FF_STAGE = 2 * FF_HALF;
 constexpr int FF_MISC = 1024;
 constexpr int FF_WARPS = 8;             // epilogue warps: two for each 32 rows, half of the columns each
 constexpr int FF_THREADS = 64 + 32 * FF_WARPS;
-constexpr int FF_EPI = FF_WARPS * 2 * EPI_CHUNK_BYTES;
-constexpr int FF_SMEM = FF_STAGES * FF_STAGE + FF_EPI + FF_MISC + 1024;
+constexpr int FF_SMEM = FF_STAGES * FF_STAGE + FF_MISC + 1024;
 static_assert(FF_SMEM <= 227 * 1024, "dense GEMM shared memory");
 constexpr int FF_PROBLEMS = 4;
 
@@ -46,7 +45,8 @@ struct FxInt {
 
 // One product out[M, N] = sum_k A B of a launch.
 struct FfProblem {
-    CUtensorMap a[2], b[2], out[2];  // the sum runs over operand pair 0, then pair 1 (dx)
+    CUtensorMap a[2], b[2];          // the sum runs over operand pair 0, then pair 1 (dx)
+    __nv_bfloat16* out[2];           // [M][N]
     int M, N, kb0, kb;               // k-blocks of 64: of pair 0, of both
     int tiles_m, tiles_n, tile0;     // first tile of the product in the launch
     int a_mn, b_mn;                  // operand stored along its M / N dimension
@@ -65,7 +65,6 @@ struct FfLaunch {
 
 struct FfSmem {
     uint8_t* stages;
-    uint8_t* epi;
     uint64_t *full, *empty, *acc_full, *acc_empty, *drain;
     uint32_t *tmem_base, *peer_base;
     volatile uint32_t* peer_k;
@@ -76,8 +75,7 @@ __device__ __forceinline__ FfSmem ff_carve(uint8_t* raw) {
     const uint32_t a = smem_u32(raw);
     uint8_t* base = raw + (((a + 1023u) & ~1023u) - a);
     s.stages = base;
-    s.epi = base + FF_STAGES * FF_STAGE;
-    s.full = reinterpret_cast<uint64_t*>(s.epi + FF_EPI);
+    s.full = reinterpret_cast<uint64_t*>(base + FF_STAGES * FF_STAGE);
     s.empty = s.full + FF_STAGES;
     s.acc_full = s.empty + FF_STAGES;
     s.acc_empty = s.acc_full + 2;
@@ -229,30 +227,25 @@ __device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t (&r)[32
         : "memory");
 }
 
-// One epilogue warp's two staging chunks (32 rows x 32 columns of bf16), stored by TMA.
-struct FfStage {
-    uint8_t* buf;
-    int eb;
-    __device__ __forceinline__ void put(const CUtensorMap* tm, const uint32_t (&pk)[16], int x, int y, int lane) {
-        if (lane == 0) bulk_wait_read_1();
-        __syncwarp();
-        uint4* dst = reinterpret_cast<uint4*>(buf + eb * EPI_CHUNK_BYTES + lane * (EPI_CHUNK * 2));
-        const uint4 u[4] = {make_uint4(pk[0], pk[1], pk[2], pk[3]), make_uint4(pk[4], pk[5], pk[6], pk[7]),
-                            make_uint4(pk[8], pk[9], pk[10], pk[11]), make_uint4(pk[12], pk[13], pk[14], pk[15])};
+// 32 columns of a lane's row as bf16, straight from registers: whole 32-byte sectors where the rows are so
+// aligned (`wide`), else 16 bytes at a time. (Staged in shared memory and stored by TMA, a 256 x 256 tile's
+// values took 3.8 us instead of 1.9 us, most of it the proxy fences, and bound products with a short k.)
+__device__ __forceinline__ void ff_store(__nv_bfloat16* to, const uint32_t (&pk)[16], int columns, bool wide) {
+    if (wide) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {  // lane-rotated order: no bank conflicts
-            const int pi = (i + lane) & 3;
-            dst[pi] = pi == 0 ? u[0] : pi == 1 ? u[1] : pi == 2 ? u[2] : u[3];
-        }
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) {
-            tma_store_2d(tm, buf + eb * EPI_CHUNK_BYTES, x, y);
-            bulk_commit();
-        }
-        eb ^= 1;
+        for (int i = 0; i < 2; ++i)
+            if (16 * i < columns)
+                asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(to + 16 * i), "r"(pk[8 * i]),
+                             "r"(pk[8 * i + 1]), "r"(pk[8 * i + 2]), "r"(pk[8 * i + 3]), "r"(pk[8 * i + 4]),
+                             "r"(pk[8 * i + 5]), "r"(pk[8 * i + 6]), "r"(pk[8 * i + 7])
+                             : "memory");
+    } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            if (8 * i < columns)
+                *reinterpret_cast<uint4*>(to + 8 * i) = make_uint4(pk[4 * i], pk[4 * i + 1], pk[4 * i + 2], pk[4 * i + 3]);
     }
-};
+}
 
 __device__ __forceinline__ float ff_sigmoid(float g) { return __fdividef(1.0f, 1.0f + __expf(-g)); }
 
@@ -356,10 +349,13 @@ struct FfKept {
 };
 
 template <int MODE>
-__device__ __forceinline__ void ff_epilogue(const FfLaunch& l, const FfTile& t, FfStage& es, uint32_t tb, int row0,
+__device__ __forceinline__ void ff_epilogue(const FfLaunch& l, const FfTile& t, uint32_t tb, int row0,
                                             int half, int slab, int lane, FfKept& next) {
-    const CUtensorMap* out = t.p->out;
     if (row0 >= t.M) return;
+    __nv_bfloat16* const out = t.p->out[0] + (size_t)(row0 + lane) * t.N;
+    __nv_bfloat16* const out1 = MODE == FF_DACT ? t.p->out[1] + (size_t)(row0 + lane) * t.N : nullptr;
+    const bool in = row0 + lane < t.M;
+    const bool wide = t.N % 16 == 0 && ((reinterpret_cast<uintptr_t>(out) | reinterpret_cast<uintptr_t>(out1)) & 31) == 0;
     if (t.cut >= 0 && !ff_collect<MODE>(l, t, tb, half, slab, lane)) return;
     if (MODE == FF_SWIGLU) {
 #pragma unroll 1
@@ -386,7 +382,8 @@ __device__ __forceinline__ void ff_epilogue(const FfLaunch& l, const FfTile& t, 
                                              __uint_as_float(u[4 * i + 2]), __uint_as_float(u[4 * i + 3]));
                 }
             }
-            es.put(out, pk, col0, row0, lane);
+            if (in) ff_store(out + col0, pk, t.N - col0, wide);
+            __syncwarp();
         }
     } else if (MODE == FF_DACT) {
 #pragma unroll 1
@@ -417,8 +414,11 @@ __device__ __forceinline__ void ff_epilogue(const FfLaunch& l, const FfTile& t, 
                     pu[h * 8 + 2 * i + 1] = pack_bf16x2(du[2], du[3]);
                 }
             }
-            es.put(out, pg, col0, row0, lane);
-            es.put(out + 1, pu, col0, row0, lane);
+            if (in) {
+                ff_store(out + col0, pg, t.N - col0, wide);
+                ff_store(out1 + col0, pu, t.N - col0, wide);
+            }
+            __syncwarp();
         }
     } else {
 #pragma unroll 1
@@ -429,7 +429,8 @@ __device__ __forceinline__ void ff_epilogue(const FfLaunch& l, const FfTile& t, 
             tmem_ld32(tb + c * 32, v);
 #pragma unroll
             for (int i = 0; i < 16; ++i) pk[i] = pack_bf16x2(__uint_as_float(v[2 * i]), __uint_as_float(v[2 * i + 1]));
-            es.put(out, pk, col0, row0, lane);
+            if (in) ff_store(out + col0, pk, t.N - col0, wide);
+            __syncwarp();
         }
     }
 }
@@ -476,7 +477,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(FF_THREADS, 1)
     if (warp == 0 && lane < l.count) {
         tma_prefetch_desc(&l.p[lane].a[0]);
         tma_prefetch_desc(&l.p[lane].b[MODE == FF_SWIGLU ? (int)rank : 0]);
-        tma_prefetch_desc(&l.p[lane].out[0]);
     }
     if (warp == 1) {
         tmem_alloc_pair(sm.tmem_base, TMEM_COLS);
@@ -554,7 +554,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(FF_THREADS, 1)
         if (!mbar_wait(sm.drain, 0, tmo, &never) && !*sm.abort) ff_status(l.status, 14 + (int)rank);
     } else if (warp >= 2) {
         const int q = warp & 3, half = (warp - 2) >> 2;
-        FfStage es{sm.epi + (warp - 2) * 2 * EPI_CHUNK_BYTES, 0};
         const uint32_t acc_empty0 = mapa_shared(smem_u32(sm.acc_empty), 0u);
         int b = 0;
         uint32_t aph = 0;
@@ -571,14 +570,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(FF_THREADS, 1)
             tc_fence_after();
             __syncwarp();
             const uint32_t tb = tmem + ((uint32_t)(q * 32) << 16) + (uint32_t)(b * 256);
-            ff_epilogue<MODE>(l, tr, es, tb, row0, half, (int)rank * FF_WARPS + warp - 2, lane, kept);
+            ff_epilogue<MODE>(l, tr, tb, row0, half, (int)rank * FF_WARPS + warp - 2, lane, kept);
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive_cluster(acc_empty0 + b * 8u);
             b ^= 1;
             if (b == 0) aph ^= 1u;
         }
-        if (lane == 0) bulk_wait_all();
         __syncwarp();
     }
     __syncwarp();
@@ -944,22 +942,22 @@ int ff_layout(const moe_ffn_config* c, FfLayout* o) {
     return MOE_OK;
 }
 
-// bf16 matrix [rows][inner]; operand boxes are 64 inner values by `box` rows with the 128-byte
-// swizzle, output boxes 32 x 32 without. Out-of-bounds elements read as zero and are not stored.
-int ff_map(CUtensorMap* m, const void* ptr, uint64_t rows, uint64_t inner, uint32_t box, bool out) {
+// bf16 matrix [rows][inner], boxes of 64 inner values by `box` rows with the 128-byte swizzle.
+// Out-of-bounds elements read as zero.
+int ff_map(CUtensorMap* m, const void* ptr, uint64_t rows, uint64_t inner, uint32_t box) {
     EncodeTiledFn fn = encode_fn();
     if (!fn) return fail(MOE_ERR_CUDA, "cuTensorMapEncodeTiled is not available from the driver");
     const cuuint64_t dims[2] = {inner, rows}, strides[1] = {inner * 2};
-    const cuuint32_t bx[2] = {out ? (cuuint32_t)EPI_CHUNK : (cuuint32_t)BK, box}, es[2] = {1, 1};
+    const cuuint32_t bx[2] = {(cuuint32_t)BK, box}, es[2] = {1, 1};
     const CUresult r = fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(ptr), dims, strides, bx, es,
-                          CU_TENSOR_MAP_INTERLEAVE_NONE, out ? CU_TENSOR_MAP_SWIZZLE_NONE : CU_TENSOR_MAP_SWIZZLE_128B,
-                          CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+                          CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                          CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
     return r == CUDA_SUCCESS ? MOE_OK : fail(MOE_ERR_CUDA, "cuTensorMapEncodeTiled failed: %d", (int)r);
 }
 
 // Operand [mn, k] (K-major) or, with mn set, stored as [k, mn]; its TMA map.
 int ff_operand(CUtensorMap* m, const void* ptr, uint64_t mn, uint64_t k, int along_mn) {
-    return along_mn ? ff_map(m, ptr, k, mn, BK, false) : ff_map(m, ptr, mn, k, 128, false);
+    return along_mn ? ff_map(m, ptr, k, mn, BK) : ff_map(m, ptr, mn, k, 128);
 }
 
 struct FfList {
@@ -990,7 +988,7 @@ struct FfList {
             try_(ff_operand(&p.a[1], a2, M, K, a_mn));
             try_(ff_operand(&p.b[1], b2, N, K, b_mn));
         }
-        try_(ff_map(&p.out[0], out, M, N, EPI_CHUNK, true));
+        p.out[0] = p.out[1] = static_cast<__nv_bfloat16*>(out);
         return p;
     }
     void try_(int r) {
@@ -1169,7 +1167,7 @@ int fx_run(FxArgs& p, const FxPlan& plan, const FfLayout& L, void* ws, cudaStrea
 // Weights [M, K] (K-major, or stored [K, M]) and tokens [T, K] of operand pair i.
 int fx_operands(FxArgs& p, int i, const void* w, int a_mn, const void* x, size_t M, size_t T, size_t K, int nt) {
     const int rc = ff_operand(&p.a[i], w, M, K, a_mn);
-    return rc ? rc : ff_map(&p.b[i], x, T, K, (uint32_t)nt, false);
+    return rc ? rc : ff_map(&p.b[i], x, T, K, (uint32_t)nt);
 }
 FxArgs fx_args(size_t M, size_t T, int kb0, int kb, void* out, int early) {
     FxArgs p;
@@ -1326,7 +1324,7 @@ MOE_API int moe_ffn_backward(const moe_ffn_config* c, const uint16_t* x, const u
     } else {
         FfList act;
         FfProblem& p = act.add(dy, 0, W2, 1, dg, L.T, L.F, L.d);
-        act.try_(ff_map(&p.out[1], du, L.T, L.F, EPI_CHUNK, true));
+        p.out[1] = reinterpret_cast<__nv_bfloat16*>(du);
         act.l.gu = gu;
         act.l.gu_cols = L.gu_cols;
         if ((rc = ff_run<FF_DACT>(act, L, ws, st, "hidden gradients"))) return rc;
