@@ -5,7 +5,7 @@
 //   dx = dg W1 + du W3, dW1 = dg^T x, dW3 = du^T x, dW2 = dy^T h
 //
 // Every product runs in dense_kernel, a persistent tcgen05 GEMM on CTA pairs (UMMA 256 x 256 x 16,
-// cta_group::2, fp32 accumulators in TMEM, operands by TMA through a six-stage ring) that takes a
+// cta_group::2, fp32 accumulators in TMEM, operands by TMA through a seven-stage ring) that takes a
 // list of products per launch and reads either operand K-major or MN-major, so no transposed copy is
 // ever written: dh, dx read the weights and dW1, dW3, dW2 read both operands along their rows.
 //   launch 1 (forward)   g and u side by side in one accumulator; epilogue: h, and g, u in fp32
@@ -181,6 +181,13 @@ __device__ __forceinline__ bool ff_multiply(const FfSmem& sm, FfRing& r, uint32_
     return true;
 }
 
+// Arrive on a barrier of the pair without ordering this thread's memory operations: the epilogue's signal
+// that it has read the accumulator (its tcgen05 loads are complete); a releasing arrive would wait for
+// the stores in flight.
+__device__ __forceinline__ void ff_arrive_relaxed(uint32_t cluster_addr) {
+    asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
+}
+
 // One unit of work: a tile, or one part of a cut tile (cut: its number among them, -1: none).
 // The product's numbers are copied here, into registers: read through the pointer into the launch's
 // parameters they would be loaded again for every k-block.
@@ -228,8 +235,8 @@ __device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t (&r)[32
 }
 
 // 32 columns of a lane's row as bf16, straight from registers: whole 32-byte sectors where the rows are so
-// aligned (`wide`), else 16 bytes at a time. (Staged in shared memory and stored by TMA, a 256 x 256 tile's
-// values took 3.8 us instead of 1.9 us, most of it the proxy fences, and bound products with a short k.)
+// aligned (`wide`), else 16 bytes at a time. (Staged in shared memory and stored by TMA, 3376 x 3656 values
+// took 15.0 us instead of 10.8 us, most of it the proxy fences.)
 __device__ __forceinline__ void ff_store(__nv_bfloat16* to, const uint32_t (&pk)[16], int columns, bool wide) {
     if (wide) {
 #pragma unroll
@@ -348,20 +355,27 @@ struct FfKept {
     }
 };
 
-template <int MODE>
+// `release` is called once per tile, when the warp has read its part of the accumulator.
+template <int MODE, typename Release>
 __device__ __forceinline__ void ff_epilogue(const FfLaunch& l, const FfTile& t, uint32_t tb, int row0,
-                                            int half, int slab, int lane, FfKept& next) {
-    if (row0 >= t.M) return;
+                                            int half, int slab, int lane, FfKept& next, Release release) {
+    if (row0 >= t.M) {
+        release();
+        return;
+    }
     __nv_bfloat16* const out = t.p->out[0] + (size_t)(row0 + lane) * t.N;
     __nv_bfloat16* const out1 = MODE == FF_DACT ? t.p->out[1] + (size_t)(row0 + lane) * t.N : nullptr;
     const bool in = row0 + lane < t.M;
     const bool wide = t.N % 16 == 0 && ((reinterpret_cast<uintptr_t>(out) | reinterpret_cast<uintptr_t>(out1)) & 31) == 0;
-    if (t.cut >= 0 && !ff_collect<MODE>(l, t, tb, half, slab, lane)) return;
+    if (t.cut >= 0 && !ff_collect<MODE>(l, t, tb, half, slab, lane)) {
+        release();
+        return;
+    }
     if (MODE == FF_SWIGLU) {
 #pragma unroll 1
         for (int c = 2 * half; c < 2 * half + 2; ++c) {
             const int col0 = t.n * 128 + c * 32;
-            if (col0 >= t.N) return;
+            if (col0 >= t.N) break;
             uint32_t g[32], u[32];
             tmem_ld32(tb + c * 32, g);
             tmem_ld32(tb + 128 + c * 32, u);
@@ -385,11 +399,12 @@ __device__ __forceinline__ void ff_epilogue(const FfLaunch& l, const FfTile& t, 
             if (in) ff_store(out + col0, pk, t.N - col0, wide);
             __syncwarp();
         }
+        release();
     } else if (MODE == FF_DACT) {
 #pragma unroll 1
         for (int c = 0; c < 4; ++c) {
             const int col0 = t.n * FT_N + half * 128 + c * 32;
-            if (col0 >= t.N) return;
+            if (col0 >= t.N) break;
             uint32_t d[32];
             tmem_ld32(tb + (4 * half + c) * 32, d);
             uint32_t pg[16], pu[16];
@@ -420,17 +435,23 @@ __device__ __forceinline__ void ff_epilogue(const FfLaunch& l, const FfTile& t, 
             }
             __syncwarp();
         }
+        release();
     } else {
-#pragma unroll 1
-        for (int c = 4 * half; c < 4 * half + 4; ++c) {
-            const int col0 = t.n * FT_N + c * 32;
-            if (col0 >= t.N) return;
-            uint32_t v[32], pk[16];
-            tmem_ld32(tb + c * 32, v);
+        // everything out of the accumulator first, so that the next products may have it while these values
+        // are stored
+        uint32_t pk[4][16];
 #pragma unroll
-            for (int i = 0; i < 16; ++i) pk[i] = pack_bf16x2(__uint_as_float(v[2 * i]), __uint_as_float(v[2 * i + 1]));
-            if (in) ff_store(out + col0, pk, t.N - col0, wide);
-            __syncwarp();
+        for (int i = 0; i < 4; ++i) {
+            uint32_t v[32];
+            tmem_ld32(tb + (4 * half + i) * 32, v);
+#pragma unroll
+            for (int k = 0; k < 16; ++k) pk[i][k] = pack_bf16x2(__uint_as_float(v[2 * k]), __uint_as_float(v[2 * k + 1]));
+        }
+        release();
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int col0 = t.n * FT_N + (4 * half + i) * 32;
+            if (in && col0 < t.N) ff_store(out + col0, pk[i], t.N - col0, wide);
         }
     }
 }
@@ -570,10 +591,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(FF_THREADS, 1)
             tc_fence_after();
             __syncwarp();
             const uint32_t tb = tmem + ((uint32_t)(q * 32) << 16) + (uint32_t)(b * 256);
-            ff_epilogue<MODE>(l, tr, tb, row0, half, (int)rank * FF_WARPS + warp - 2, lane, kept);
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive_cluster(acc_empty0 + b * 8u);
+            ff_epilogue<MODE>(l, tr, tb, row0, half, (int)rank * FF_WARPS + warp - 2, lane, kept, [&] {
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) ff_arrive_relaxed(acc_empty0 + b * 8u);
+            });
             b ^= 1;
             if (b == 0) aph ^= 1u;
         }
