@@ -1018,20 +1018,24 @@ struct FfList {
     }
 };
 
-// Times in microseconds that the choices below go by, fitted to 5100 measured launches (products of
-// 512 to 14336 features, 1 to 2048 tokens and 512 to 5632 k, every plan of each; the plan that these
-// numbers choose took 1.04 times the best one's time on average, 1.29 times at worst).
-constexpr float US_HBM = 6.3e6f;                             // bytes a microsecond from memory
-constexpr float US_DENSE = 5.2f, US_DENSE_KB = 0.275f;       // a launch; a k-block of a 256 x 256 tile
-constexpr float US_DENSE_WAVE = 2.8f, US_DENSE_REST = 2.65f; // a full wave of tiles; the last one
-constexpr float US_CUT_ROUND = 7.0f, US_CUT_PART = 2.0f;     // a round of parts; adding up each further part
-constexpr float US_FLEX = 1.7f, US_FLEX_CTA = 0.93f;         // a launch; a CTA beside its k-blocks
-constexpr float US_FLEX_BYTES = 155.6e3f;                    // bytes a microsecond into a SM
-constexpr float US_FLEX_LATENCY = 1.13f;                     // of a load, shared by the stages in flight
-constexpr float US_FLEX_CYCLES = 1.47f / 1.9e3f;             // a cycle of the tensor cores
-constexpr float US_FLEX_VALUE = 0.0025f;                     // a token's values in the epilogue
-constexpr float US_FLEX_SPLIT = 0.55f, US_FLEX_EXCHANGE = 0.024f;  // a cluster; a token's partial sums
-constexpr float US_FLEX_TWO = 1.57f, US_FLEX_MORE = 0.94f;   // two CTAs' fixed part on one SM; each CTA beyond
+// Kinds of products, by their epilogue: plain; h; h with g and u kept; the hidden gradients.
+enum FfKind : int { FK_PLAIN = 0, FK_H = 1, FK_H_KEPT = 2, FK_ACT = 3 };
+
+// Times in microseconds that the choices below go by, fitted to 15,400 measured launches (products of
+// 360 to 14336 features, 1 to 4096 tokens and 216 to 14336 k, of every kind, every plan of each; the
+// plan that these numbers choose took 1.03 times the best one's time on average, 1.47 times at worst).
+constexpr float US_HBM = 6.3e6f;                            // bytes a microsecond from memory
+constexpr float US_DENSE = 4.9f, US_DENSE_KB = 0.287f;      // a launch; a k-block of a 256 x 256 tile
+constexpr float US_DENSE_WAVE = 1.9f;                       // a wave beside its k-blocks or epilogue
+constexpr float US_DENSE_EPI[4] = {1.5f, 0.6f, 2.9f, 9.3f};  // a tile's epilogue, by kind
+constexpr float US_CUT_ROUND = 6.3f, US_CUT_PART = 1.1f;    // a round of parts; adding up each further part
+constexpr float US_FLEX = 1.45f, US_FLEX_CTA = 1.09f;       // a launch; a CTA beside its k-blocks
+constexpr float US_FLEX_BYTES = 150.9e3f;                   // bytes a microsecond into a SM
+constexpr float US_FLEX_LATENCY = 1.15f;                    // of a load, shared by the stages in flight
+constexpr float US_FLEX_CYCLES = 1.45f / 1.9e3f;            // a cycle of the tensor cores
+constexpr float US_FLEX_TOKEN[4] = {0.0015f, 0.0143f, 0.0259f, 0.0325f};  // a token's values, by kind
+constexpr float US_FLEX_SPLIT = 0.55f, US_FLEX_EXCHANGE = 0.0236f;  // a cluster; a token's partial sums
+constexpr float US_FLEX_TWO = 1.57f, US_FLEX_MORE = 0.86f;  // two CTAs' fixed part on one SM; each CTA beyond
 
 // Tiles come in waves of one a cluster. The tiles of an incomplete last wave are cut along k into as many
 // parts as finish soonest.
@@ -1039,10 +1043,11 @@ struct FfCut {
     int full, parts;
     float us;  // of the whole launch
 };
-FfCut ff_cut(int tiles, int kb, int clusters) {
+FfCut ff_cut(int tiles, int kb, int clusters, int kind = FK_PLAIN) {
     const int full = tiles / clusters, rest = tiles - full * clusters;
-    const float before = US_DENSE + full * (kb * US_DENSE_KB + US_DENSE_WAVE) + US_DENSE_REST;
-    FfCut best{tiles, 1, before + (rest ? kb * US_DENSE_KB : 0.0f)};
+    const float work = kb * US_DENSE_KB, epi = US_DENSE_EPI[kind];
+    const float before = US_DENSE + full * ((work > epi ? work : epi) + US_DENSE_WAVE) + epi;
+    FfCut best{tiles, 1, before + (rest ? work : 0.0f)};
     if (!rest || rest > FF_MAX_CUT / 2) return best;
     for (int parts = 2; parts <= 8 && rest * parts <= FF_MAX_CUT && parts * 4 <= kb; ++parts) {
         const int rounds = (rest * parts + clusters - 1) / clusters;
@@ -1111,10 +1116,11 @@ struct FxPlan {
 // tensor cores' time (VALS x 4 UMMAs of max(nt / 2, 32 + nt / 4) cycles: their own, or the shared
 // memory's that feeds them 128 x 16 weights and nt x 16 tokens), its bytes' way into the SM, or its share
 // of a load's latency; two CTAs on a SM share the first two. Clusters of 4 and 8 do not fill every SM.
-FxPlan ff_choose_flex(int M, int T, int kb, bool dual, int sms) {
+FxPlan ff_choose_flex(int M, int T, int kb, int kind, int sms) {
     FxPlan best{0, 1, 0, 1e30f};
+    const bool dual = kind == FK_H || kind == FK_H_KEPT;
     const int vals = dual ? 2 : 1;
-    const float hbm = (float)M * kb * BK * 2 * vals / US_HBM + 1.6f;
+    const float hbm = (float)M * kb * BK * 2 * vals / US_HBM + 1.7f;
     for (int nt = 16; nt <= 128; nt += nt < 64 ? 16 : 32) {
         if (nt > 16 && nt - (nt <= 64 ? 16 : 32) >= T) break;  // a narrower tile holds every token
         const int stage = fx_stage_bytes(dual, nt), tiles = ((M + 127) / 128) * ((T + nt - 1) / nt);
@@ -1126,7 +1132,7 @@ FxPlan ff_choose_flex(int M, int T, int kb, bool dual, int sms) {
             if (S > kb || nt % S || (S > 1 && vals * nt * 512 > stages * stage)) continue;
             const int slots = S == 8 ? sms * 85 / 100 : S == 4 ? sms * 93 / 100 : sms;
             const int load = (tiles * S + slots - 1) / slots, mine = (kb + S - 1) / S;
-            const float fixed = US_FLEX_CTA + US_FLEX_VALUE * nt * vals / S +
+            const float fixed = US_FLEX_CTA + US_FLEX_TOKEN[kind] * nt / S +
                                 (S > 1 ? US_FLEX_SPLIT + US_FLEX_EXCHANGE * nt * vals : 0.0f);
             float us = load / 2 * (mine * two + fixed * US_FLEX_TWO) + load % 2 * (mine * one + fixed) +
                        (load > 2 ? US_FLEX_MORE * (load - 2) : 0.0f);
@@ -1136,13 +1142,17 @@ FxPlan ff_choose_flex(int M, int T, int kb, bool dual, int sms) {
     }
     return best;
 }
-// How a product runs: the quicker of flex_kernel's best plan and dense_kernel.
-FxPlan ff_choose(int M, int T, int kb, bool dual, int sms) {
+// dense_kernel's estimate.
+FxPlan ff_dense(int M, int T, int kb, int kind, int sms) {
+    const bool dual = kind == FK_H || kind == FK_H_KEPT;
     const int tiles = ((T + FT_M - 1) / FT_M) * ((M + (dual ? 127 : FT_N - 1)) / (dual ? 128 : FT_N));
-    const FxPlan flex = ff_choose_flex(M, T, kb, dual, sms);
-    const float hbm = (float)M * kb * BK * 2 * (dual ? 2 : 1) / US_HBM + 6.0f, us = ff_cut(tiles, kb, sms / 2).us;
-    const float dense = us > hbm ? us : hbm;
-    return flex.us < dense ? flex : FxPlan{0, 1, 0, dense};
+    const float hbm = (float)M * kb * BK * 2 * (dual ? 2 : 1) / US_HBM + 6.7f, us = ff_cut(tiles, kb, sms / 2, kind).us;
+    return FxPlan{0, 1, 0, us > hbm ? us : hbm};
+}
+// The quicker of the two.
+FxPlan ff_choose(int M, int T, int kb, int kind, int sms) {
+    const FxPlan flex = ff_choose_flex(M, T, kb, kind, sms), dense = ff_dense(M, T, kb, kind, sms);
+    return flex.us < dense.us ? flex : dense;
 }
 
 // Once per device: the kernel may take FX_ROOM of shared memory.
@@ -1204,10 +1214,11 @@ FxArgs fx_args(size_t M, size_t T, int kb0, int kb, void* out, int early) {
     return p;
 }
 
-// The plans of a config's products.
+// The plans of a config's products. h for a backward pass (kept) and the hidden gradients (act) take the
+// same kernel, because it fixes the layout in which g and u are kept.
 struct FfPlans {
     int T, d, F, sms;
-    FxPlan up, act, down, dx;  // act: the hidden gradients, which take the kernel that h took
+    FxPlan h, kept, act, down, dx;
 };
 const FfPlans& ff_plans(const FfLayout& L, int sms) {
     static thread_local FfPlans last[4] = {};  // a program alternates between few configs
@@ -1217,8 +1228,14 @@ const FfPlans& ff_plans(const FfLayout& L, int sms) {
         if (p.T == T && p.d == d && p.F == F && p.sms == sms) return p;
     FfPlans& p = last[turn++ & 3];
     const int kd = (d + BK - 1) / BK, kf = (F + BK - 1) / BK;
-    p = FfPlans{T, d, F, sms, ff_choose(F, T, kd, true, sms), ff_choose_flex(F, T, kd, false, sms),
-                ff_choose(d, T, kf, false, sms), ff_choose(d, T, 2 * kf, false, sms)};
+    FxPlan kept = ff_choose_flex(F, T, kd, FK_H_KEPT, sms), act = ff_choose_flex(F, T, kd, FK_ACT, sms);
+    const FxPlan dk = ff_dense(F, T, kd, FK_H_KEPT, sms), da = ff_dense(F, T, kd, FK_ACT, sms);
+    if (dk.us + da.us < kept.us + act.us) {
+        kept = dk;
+        act = da;
+    }
+    p = FfPlans{T, d, F, sms, ff_choose(F, T, kd, FK_H, sms), kept, act, ff_choose(d, T, kf, FK_PLAIN, sms),
+                ff_choose(d, T, 2 * kf, FK_PLAIN, sms)};
     return p;
 }
 
@@ -1275,12 +1292,10 @@ MOE_API int moe_ffn_forward(const moe_ffn_config* c, const uint16_t* x, const ui
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     uint8_t* s = static_cast<uint8_t*>(saved);
     uint8_t* h = s ? s + L.saved_h : static_cast<uint8_t*>(ws) + L.h;
-    // g, u and h; the backward pass's hidden gradients have the same shape and take the same kernel, which
-    // fixes the layout in which g and u are kept
     const int kd = (int)((L.d + BK - 1) / BK), kf = (int)((L.F + BK - 1) / BK);
     float* gu = s ? reinterpret_cast<float*>(s + L.saved_gu) : nullptr;
     const FfPlans& plans = ff_plans(L, sms);
-    const FxPlan& up_plan = plans.up;
+    const FxPlan& up_plan = gu ? plans.kept : plans.h;
     if (up_plan.nt) {
         FxArgs p = fx_args(L.F, L.T, kd, kd, h, 0);
         p.gu = reinterpret_cast<float2*>(gu);
@@ -1336,7 +1351,7 @@ MOE_API int moe_ffn_backward(const moe_ffn_config* c, const uint16_t* x, const u
     const int kd = (int)((L.d + BK - 1) / BK), kf = (int)((L.F + BK - 1) / BK);
     float* gu = reinterpret_cast<float*>(const_cast<uint8_t*>(s) + L.saved_gu);
     const FfPlans& plans = ff_plans(L, sms);
-    if (plans.up.nt) {  // the forward pass's choice
+    if (plans.act.nt) {
         const FxPlan& plan = plans.act;
         FxArgs p = fx_args(L.F, L.T, kd, kd, dg, 0);
         p.out1 = reinterpret_cast<__nv_bfloat16*>(du);
