@@ -8,13 +8,15 @@
 // bound by HBM as long as enough loads are in flight and the arithmetic (about a dozen operations a
 // value; sums and products two at a time, f32x2) stays below it.
 //
-// Forward: a row belongs to one warp as far as it fits its registers (2048 values, 4096 in 16 bits and whole vectors),
-// so the variance is the mean of squared differences without a second read, no barrier is
-// waited for, and a warp's loads are all in flight at once (8 KB). Weights come from L1. Longer
-// rows, and rows of a launch with few of them, are shared by several warps.
+// Forward: a row lies in the registers of as many warps as hold it with 32 values a thread, so the
+// variance is the mean of squared differences without a second read, and all of a row's loads are in
+// flight at once. Weights come from L1. 16384 x 4096 bf16 take 59 us, 4.5 TB/s; what bounds it is the
+// instructions (17 a value), not the memory (40 us).
 // Backward: a thread keeps the same columns over all its rows, with their partial sums of dw and db
 // in registers, and takes several rows at a time (32 values in all) so that one reduction and one
-// barrier serve all of them. The CTAs' partial sums are added up in CTA order by a second launch.
+// barrier serve all of them; the rows come through shared memory by cp.async, two batches ahead. The
+// CTAs' partial sums are added up in CTA order by a second launch. 16384 x 2048 bf16 take 49 us, 4.1 TB/s,
+// bound like the forward pass (20 instructions a value; memory 30 us).
 #include "host_internal.h"
 #include "moe_internal.cuh"
 
@@ -26,7 +28,7 @@ namespace moe {
 namespace {
 
 constexpr int LN_FWD_THREADS = 256;
-constexpr int LN_BWD_THREADS = 256;  // a row above 4096 values takes up to 512
+constexpr int LN_BWD_THREADS = 256;  // a row above 2048 values takes up to 512
 constexpr int LN_MAX_D = 16384;
 constexpr int LN_RED_COLS = 32;   // columns of a CTA of the reduction
 constexpr int LN_RED_ROWS = 32;   // partial sums it adds side by side
@@ -173,10 +175,11 @@ __device__ __forceinline__ void weights(const void* w, bool f32, float none, int
     }
     const float* p = static_cast<const float*>(w) + c;
     Pack<float, VEC> v;
-    if (W == LN_W_F32 && VEC >= 4) {
+    if (W == LN_W_F32) {
+        constexpr int L = VEC < 4 ? VEC : 4;
 #pragma unroll
-        for (int i = 0; i < VEC / 4; ++i)
-            *reinterpret_cast<float4*>(&v.v[4 * i]) = *reinterpret_cast<const float4*>(p + 4 * i);
+        for (int i = 0; i < VEC / L; ++i)
+            *reinterpret_cast<Pack<float, L>*>(&v.v[L * i]) = *reinterpret_cast<const Pack<float, L>*>(p + L * i);
     } else {
 #pragma unroll
         for (int i = 0; i < VEC; ++i) v.v[i] = !w ? none : f32 ? p[i] : num(static_cast<const T*>(w)[c + i]);
@@ -199,7 +202,7 @@ struct LnShape {
 
 // NV values of a row a thread, in NV / VEC pieces: piece q covers columns (q * 32 warps + t) VEC...
 template <typename T, int VEC, int NV>
-__global__ void __launch_bounds__(LN_FWD_THREADS, 2)
+__global__ void __launch_bounds__(LN_FWD_THREADS, NV <= 8 ? 6 : NV <= 16 ? 5 : NV <= 32 ? 4 : 2)
     ln_forward_kernel(LnShape s, const T* x, const void* w, const void* b, bool wf32, int form, T* y, float* mean,
                       float* rstd) {
     typedef typename Lanes<VEC>::V V;
@@ -277,7 +280,7 @@ __global__ void __launch_bounds__(LN_FWD_THREADS, 2)
                 *reinterpret_cast<Pack<T, VEC>*>(yr + q * step) = narrow<T, VEC>(f);
             }
         };
-        if (VEC == 1 || form == LN_W_ANY) finish(Int<LN_W_ANY>());
+        if (form == LN_W_ANY) finish(Int<LN_W_ANY>());
         else if (form == LN_W_SAME) finish(Int<LN_W_SAME>());
         else finish(Int<LN_W_F32>());
         if (t == 0) {
@@ -320,7 +323,7 @@ __host__ __device__ constexpr int bwd_rows(size_t size, int vec, int nv) {
 
 // R rows at a time, NV columns a thread.
 template <typename T, int VEC, int NV, int SLOTS>
-__global__ void __launch_bounds__(NV > 8 ? 512 : 256, NV > 8 ? 1 : 2)
+__global__ void __launch_bounds__(512, 1)
     ln_backward_kernel(LnShape s, const T* dy, const T* x, const void* w, bool wf32, const float* mean,
                        const float* rstd, T* dx, float* part) {
     typedef typename Lanes<VEC>::V V;
@@ -593,7 +596,8 @@ cudaError_t dispatch(int dtype, int vec, F f) {
 }
 
 // Backward: columns a thread keeps, and with them the warps of a row and the CTAs of the launch.
-int backward_values(int d) { return d <= 2048 ? 8 : d <= 8192 ? 16 : 32; }
+// (8 rather than 16 between 2048 and 4096: 16384 x 4096 bf16 91 us against 110 us)
+int backward_values(int d) { return d <= 4096 ? 8 : d <= 8192 ? 16 : 32; }
 LnShape backward_shape(const moe_layernorm_config& c) {
     return shape_of(c, warps_for(c.d, backward_values(c.d)), LN_BWD_THREADS);
 }
@@ -625,10 +629,14 @@ MOE_API int moe_layernorm_forward(const moe_layernorm_config* c, const void* x, 
     DeviceInfo di;
     if ((rc = check_device(&di))) return rc;
     const int vec = vector_width(*c, x, y, y);
-    // values a thread holds: as few as 8 for short rows; a whole row a warp up to 64 registers; with few
-    // rows (less than two a SM) 32, so that more warps load at once
-    const int whole = vec == 8 ? 128 : 64;
-    const int values = c->d <= 256 ? 8 : (c->d <= 1024 || (c->rows < 2 * di.sms && c->d <= LN_FWD_THREADS * 32)) ? 32 : whole;
+    // Values a thread holds: 32 in as many warps as the row takes (64 above 8192 columns); 16 or 8 for short
+    // rows, and where there are too few rows to fill the device (16 warps a SM). 64 values were slower
+    // (4575 x 6651 fp32: 111 us against 75 us; 1511 x 1969 fp32: 18 us against 10.6 us with 16), 128 in
+    // whole vectors no faster (16384 x 4096 bf16: 59 us both).
+    int values = c->d <= 32 * LN_FWD_THREADS ? 32 : 64;
+    while (values > 8 && (c->d <= 32 * values / 2 || c->rows * warps_for(c->d, values) < 16 * di.sms) &&
+           warps_for(c->d, values / 2) <= LN_FWD_THREADS / 32)
+        values /= 2;
     const LnShape s = shape_of(*c, warps_for(c->d, values), LN_FWD_THREADS);
     const int64_t n = (c->rows + s.groups - 1) / s.groups, most = (int64_t)di.sms * 64;
     const dim3 grid((unsigned)(n < most ? n : most)), block(32 * s.warps * s.groups);
@@ -636,16 +644,18 @@ MOE_API int moe_layernorm_forward(const moe_layernorm_config* c, const void* x, 
     const cudaError_t err = dispatch(c->dtype, vec, [&](auto pk) {
         typedef decltype(pk) P;
         typedef std::remove_reference_t<decltype(pk.v[0])> T;
-        constexpr int V = (int)(sizeof(P) / sizeof(T)), WHOLE = V == 8 ? 128 : 64;
-        const bool wf32 = c->wdtype == MOE_DTYPE_F32, whole_pieces = w && b && aligned(w, 16) && aligned(b, 16);
-        const int form = !whole_pieces || (wf32 && V < 4) ? LN_W_ANY : wf32 ? LN_W_F32 : LN_W_SAME;
+        constexpr int V = (int)(sizeof(P) / sizeof(T));
+        const bool wf32 = c->wdtype == MOE_DTYPE_F32;
+        const size_t piece = wf32 ? (V < 4 ? V : 4) * 4 : V * sizeof(T);
+        const int form = !w || !b || !aligned(w, piece) || !aligned(b, piece) ? LN_W_ANY : wf32 ? LN_W_F32 : LN_W_SAME;
         auto go = [&](auto kernel) {
             return launch_k(kernel, grid, block, 0, st, true, s, static_cast<const T*>(x), w, b, wf32, form,
                             static_cast<T*>(y), mean, rstd);
         };
         return values == 8    ? go(ln_forward_kernel<T, V, 8>)
+               : values == 16 ? go(ln_forward_kernel<T, V, 16>)
                : values == 32 ? go(ln_forward_kernel<T, V, 32>)
-                              : go(ln_forward_kernel<T, V, WHOLE>);
+                              : go(ln_forward_kernel<T, V, 64>);
     });
     return err == cudaSuccess ? MOE_OK : cuda_fail(err, "layer norm launch");
 }
