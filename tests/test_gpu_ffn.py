@@ -218,3 +218,27 @@ def test_refusals():
     with pytest.raises(tlc.MoEError) as e:
         tlc.ffn_forward(cfg, x, W1, W3, W2, y, small)
     assert e.value.code == tlc.MOE_ERR_WORKSPACE
+
+
+@pytest.mark.parametrize("T", [3, 2000])
+def test_a_wait_that_runs_out_is_reported(T):
+    """With a limit of 1 us some waits may run out (the limit is looked at between the hardware's own
+    suspended tries, so a short wait can also succeed): the calls end either way, the status says which,
+    the values are right if it says so, and the workspace is usable again once its status words are zero."""
+    d, f = 4096, 2048
+    x, W1, W3, W2, dy = make(T, d, f)
+    short, cfg = tlc.FFNConfig(T, d, f, timeout_us=1), tlc.FFNConfig(T, d, f)
+    ws, y, saved = tlc.FFNWorkspace(cfg), torch.empty_like(x), tlc.ffn_saved(cfg)
+    want = ref.ffn_forward(f64(x), f64(W1), f64(W3), f64(W2))
+    for _ in range(5):
+        tlc.ffn_forward(short, x, W1, W3, W2, y, ws, saved=saved)
+        tlc.ffn_backward(short, x, W1, W3, W2, dy, saved, *(torch.empty_like(t) for t in (x, W1, W3, W2)), ws)
+        rc, detail = tlc.ffn_status(short, ws)
+        assert rc in (tlc.MOE_OK, tlc.MOE_ERR_TIMEOUT)
+        if rc == tlc.MOE_OK:
+            close(y, want)
+        else:
+            assert detail > 0
+            ws.buf[:tlc.MOE_FFN_STATUS_BYTES].zero_()
+    y, _, _ = forward(cfg, x, W1, W3, W2, False, ws)
+    close(y, want)

@@ -94,6 +94,11 @@ __device__ __forceinline__ void ff_abort(const FfSmem& s, uint32_t rank) {
     *s.abort = 1;
     st_cluster_u32(mapa_shared(smem_u32(const_cast<int*>(s.abort)), rank ^ 1u), 1u);
 }
+// What a CTA waits for before it leaves, products and loads in flight, it waits for this long at least,
+// however short the caller's limit on the other waits.
+__device__ __forceinline__ unsigned long long ff_hold(unsigned long long tmo) {
+    return tmo > 2000000000ull ? tmo : 2000000000ull;
+}
 // Abort path (rank 0, after both CTAs have stopped issuing): rank 0 armed and loaded `a` k-blocks,
 // rank 1 loaded `b`. Bytes that will never come are completed, phases that were never armed are
 // armed, then every stage's last phase is waited for: no load is in flight when the CTAs leave.
@@ -572,7 +577,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(FF_THREADS, 1)
             ff_abort(sm, rank);
         }
         int never = 0;
-        if (!mbar_wait(sm.drain, 0, tmo, &never) && !*sm.abort) ff_status(l.status, 14 + (int)rank);
+        if (!mbar_wait(sm.drain, 0, ff_hold(tmo), &never) && !*sm.abort) ff_status(l.status, 14 + (int)rank);
     } else if (warp >= 2) {
         const int q = warp & 3, half = (warp - 2) >> 2;
         const uint32_t acc_empty0 = mapa_shared(smem_u32(sm.acc_empty), 0u);
@@ -583,13 +588,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(FF_THREADS, 1)
             const int row0 = tr.m * FT_M + (int)rank * 128 + q * 32;
             FfKept kept;
             if (MODE == FF_DACT) kept.load(l, tr, row0, half, 0, lane);
-            if (!mbar_wait(&sm.acc_full[b], aph, tmo, sm.abort)) {
-                if (!*sm.abort) ff_status(l.status, 16 + (int)rank);
-                if (lane == 0) ff_abort(sm, rank);
+            const bool got = mbar_wait(&sm.acc_full[b], aph, tmo, sm.abort);
+            if (!__all_sync(0xffffffffu, got)) {  // the whole warp goes on or none of it
+                if (lane == 0) {
+                    if (!*sm.abort) ff_status(l.status, 16 + (int)rank);
+                    ff_abort(sm, rank);
+                }
                 break;
             }
             tc_fence_after();
-            __syncwarp();
             const uint32_t tb = tmem + ((uint32_t)(q * 32) << 16) + (uint32_t)(b * 256);
             ff_epilogue<MODE>(l, tr, tb, row0, half, (int)rank * FF_WARPS + warp - 2, lane, kept, [&] {
                 tc_fence_before();
@@ -607,7 +614,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(FF_THREADS, 1)
     if (*sm.abort) {
         if (tid == 0 && rank == 1) st_cluster_u32(mapa_shared(smem_u32(const_cast<uint32_t*>(sm.peer_k)), 0u), nk);
         cluster_sync();
-        if (tid == 0 && rank == 0) ff_settle(sm, nk, *sm.peer_k, tmo);
+        if (tid == 0 && rank == 0) ff_settle(sm, nk, *sm.peer_k, ff_hold(tmo));
         cluster_sync();
     }
     if (warp == 1) {
@@ -787,7 +794,7 @@ __global__ void __launch_bounds__(GEMM_THREADS, 1) flex_kernel(const __grid_cons
             // no load is in flight when the CTA leaves: each stage's last phase has completed
             int never = 0;
             for (int i = issued > p.stages ? issued - p.stages : 0; i < issued; ++i)
-                if (!mbar_wait(&full[i % p.stages], (uint32_t)(i / p.stages) & 1u, tmo, &never)) ff_status(p.status, 21);
+                if (!mbar_wait(&full[i % p.stages], (uint32_t)(i / p.stages) & 1u, ff_hold(tmo), &never)) ff_status(p.status, 21);
         }
     } else if (warp == 1) {
         griddep_wait();
@@ -819,7 +826,7 @@ __global__ void __launch_bounds__(GEMM_THREADS, 1) flex_kernel(const __grid_cons
             }
             umma_commit(&done);  // fires when every UMMA issued has completed
             int never = 0;
-            if (!mbar_wait(&done, 0, tmo, &never)) {
+            if (!mbar_wait(&done, 0, ff_hold(tmo), &never)) {
                 ff_status(p.status, 23);
                 abort_word = 1;
             }
