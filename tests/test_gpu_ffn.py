@@ -220,6 +220,32 @@ def test_refusals():
     assert e.value.code == tlc.MOE_ERR_WORKSPACE
 
 
+@pytest.mark.parametrize("T,d,f", [(5, 512, 1024), (90, 2048, 1408), (700, 264, 2744), (1500, 1024, 1024)])
+def test_back_to_back_passes_equal_their_own_results(T, d, f):
+    """Passes over two inputs in turn, nothing waited for in between (each launch may start while the one
+    before it ends, the weight gradients beside the input gradients): every result is bit for bit the
+    one that a pass by itself gave."""
+    cfg = tlc.FFNConfig(T, d, f)
+    sets, ws, saved = [make(T, d, f, seed) for seed in (1, 2)], tlc.FFNWorkspace(cfg), tlc.ffn_saved(cfg)
+
+    def one(x, W1, W3, W2, dy):
+        y, outs = torch.empty_like(x), [torch.empty_like(t) for t in (x, W1, W3, W2)]
+        tlc.ffn_forward(cfg, x, W1, W3, W2, y, ws, saved=saved)
+        tlc.ffn_backward(cfg, x, W1, W3, W2, dy, saved, *outs, ws)
+        return [y, *outs]
+
+    alone = []
+    for s in sets:
+        alone.append(one(*s))
+        torch.cuda.synchronize()
+    runs = [one(*sets[i % 2]) for i in range(12)]
+    torch.cuda.synchronize()
+    for i, got in enumerate(runs):
+        for a, b in zip(got, alone[i % 2]):
+            assert torch.equal(a, b)
+    assert tlc.ffn_status(cfg, ws) == (tlc.MOE_OK, 0)
+
+
 @pytest.mark.parametrize("T", [3, 2000])
 def test_a_wait_that_runs_out_is_reported(T):
     """With a limit of 1 us some waits may run out (the limit is looked at between the hardware's own

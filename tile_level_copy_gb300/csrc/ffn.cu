@@ -61,6 +61,10 @@ struct FfLaunch {
     int gu_cols;       // 32-column blocks of a row of it
     int32_t* status;   // [2] first error of the calls on a workspace, and where
     unsigned long long timeout_ns;
+    // The launch before this one is not read or overwritten, and all of its CTAs had waited for what came
+    // before it when they let this one begin: this launch starts beside it, and waits for it at its
+    // end only, so that what follows this launch follows both.
+    int beside;
 };
 
 struct FfSmem {
@@ -514,7 +518,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(FF_THREADS, 1)
     tc_fence_after();
     if (rank == 1 && tid == 0) st_cluster_u32(mapa_shared(smem_u32(sm.peer_base), 0u), *sm.tmem_base);
     cluster_sync();
-    griddep_wait();
+    if (!l.beside) griddep_wait();
     griddep_launch();
     const uint32_t tmem = *sm.tmem_base;
     const bool bad = rank == 0 && *sm.peer_base != tmem;
@@ -624,6 +628,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(FF_THREADS, 1)
     }
     __syncwarp();
     cluster_sync();
+    if (l.beside) griddep_wait();
 }
 
 // ---- few tokens or few tiles: flex_kernel ----------------------------------------------------------
@@ -993,7 +998,7 @@ struct FfList {
     FfLaunch l;
     int rc = MOE_OK;
     FfList() {  // the products' maps are written as they are added, the others not at all
-        l.count = l.tiles = 0;
+        l.count = l.tiles = l.beside = 0;
         l.gu = nullptr;
         l.gu_cols = 0;
     }
@@ -1380,6 +1385,7 @@ MOE_API int moe_ffn_backward(const moe_ffn_config* c, const uint16_t* x, const u
         if ((rc = fx_operands(p, 0, W1, 1, dg, L.d, L.T, L.F, dx_plan.nt))) return rc;
         if ((rc = fx_operands(p, 1, W3, 1, du, L.d, L.T, L.F, dx_plan.nt))) return rc;
         if ((rc = fx_run<FF_PLAIN, true>(p, dx_plan, L, ws, st, "input gradients"))) return rc;
+        grad.l.beside = 1;  // the weight gradients do not need dx
     } else {
         grad.add(dg, 0, W1, 1, dx, L.T, L.d, L.F, du, W3);
     }
