@@ -57,7 +57,12 @@ def test_forward(T, d, f, save):
     close(y, ref.ffn_forward(f64(x), f64(W1), f64(W3), f64(W2)))
 
 
-@pytest.mark.parametrize("T,d,f", SHAPES)
+# Input and weight gradients in one launch, of more tiles than go at once: the input gradients' tiles
+# longer than the others (cut into parts or not), and shorter.
+LONG = [(300, 1032, 4104), (1100, 1032, 2056), (2500, 520, 2056), (4000, 136, 264)]
+
+
+@pytest.mark.parametrize("T,d,f", SHAPES + LONG)
 def test_backward(T, d, f):
     cfg = tlc.FFNConfig(T, d, f)
     x, W1, W3, W2, dy = make(T, d, f, T + f)

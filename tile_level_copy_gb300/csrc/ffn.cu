@@ -35,6 +35,9 @@ constexpr int FF_THREADS = 64 + 32 * FF_WARPS;
 constexpr int FF_SMEM = FF_STAGES * FF_STAGE + FF_MISC + 1024;
 static_assert(FF_SMEM <= 227 * 1024, "dense GEMM shared memory");
 constexpr int FF_PROBLEMS = 4;
+// Parts of cut tiles in a launch, and words of the status area: [0] status, [1] detail, [128...] arrivals.
+constexpr int FF_MAX_CUT = 160, FF_ARRIVED = 128;
+static_assert((FF_ARRIVED + FF_MAX_CUT / 2 * 2 * FF_WARPS) * 4 <= MOE_FFN_STATUS_BYTES, "arrival counts");
 
 enum FfMode : int { FF_PLAIN = 0, FF_SWIGLU = 1, FF_DACT = 2 };
 
@@ -48,14 +51,18 @@ struct FfProblem {
     CUtensorMap a[2], b[2];          // the sum runs over operand pair 0, then pair 1 (dx)
     __nv_bfloat16* out[2];           // [M][N]
     int M, N, kb0, kb;               // k-blocks of 64: of pair 0, of both
-    int tiles_m, tiles_n, tile0;     // first tile of the product in the launch
+    int tiles_m, tiles_n;
     int a_mn, b_mn;                  // operand stored along its M / N dimension
+    // Units of work: the first `whole` tiles, then each of the others in `parts` parts of its k-blocks.
+    int unit0, whole, parts, cut0, slot0;  // first unit, cut tile and part of a cut tile in the launch
+    int cut() const { return tiles_m * tiles_n - whole; }
+    int units() const { return whole + cut() * parts; }
 };
 struct FfLaunch {
     FfProblem p[FF_PROBLEMS];
-    int count, tiles;
-    int full, parts, units;  // tiles from `full` on are cut into `parts` pieces of their k-blocks
-    float* partial;          // their partial sums, and
+    int count, units;
+    int first, extra;        // see ff_unit
+    float* partial;          // partial sums of cut tiles, and
     uint32_t* arrived;       // counts of the parts done, one for each epilogue warp of a cut tile (zero between calls)
     float* gu;         // kept g and u (FF_SWIGLU writes, may be null; FF_DACT reads)
     int gu_cols;       // 32-column blocks of a row of it
@@ -202,29 +209,50 @@ __device__ __forceinline__ void ff_arrive_relaxed(uint32_t cluster_addr) {
 // parameters they would be loaded again for every k-block.
 struct FfTile {
     const FfProblem* p;
-    int m, n, k0, k1, cut, part;
+    int m, n, k0, k1, cut, part, parts;
     int M, N, kb0, a_mn, b_mn;
 };
-__device__ __forceinline__ FfTile ff_tile(const FfLaunch& l, int unit) {
-    int t = unit, part = 0, cut = -1;
-    if (unit >= l.full) {
-        const int v = unit - l.full;
-        cut = v / l.parts;
-        part = v - cut * l.parts;
-        t = l.full + cut;
+// The i-th unit of a cluster (-1: no more). The first l.first units, which take longer, go round the
+// clusters; those that got one less then take l.extra of the others; the rest goes round again, from them on.
+__device__ __forceinline__ int ff_unit(const FfLaunch& l, int cluster, int clusters, int i) {
+    int u = cluster + i * clusters;
+    if (u >= l.first) {
+        const int rounds = l.first / clusters, high = l.first - rounds * clusters;
+        int c = cluster - high;
+        i -= rounds;
+        u = l.first;
+        if (c < 0) {
+            i -= 1;
+            c += clusters;
+            u += l.extra * (clusters - high) + c + i * clusters;
+        } else if (i < l.extra) {
+            u += c + i * (clusters - high);
+        } else {
+            u += l.extra * (clusters - high) + c + (i - l.extra) * clusters;
+        }
     }
+    return u < l.units ? u : -1;
+}
+__device__ __forceinline__ FfTile ff_tile(const FfLaunch& l, int unit) {
     int i = 0;
-    while (i + 1 < l.count && t >= l.p[i + 1].tile0) ++i;
+    while (i + 1 < l.count && unit >= l.p[i + 1].unit0) ++i;
     const FfProblem* p = &l.p[i];
-    const int q = t - p->tile0;
+    int q = unit - p->unit0, part = 0, cut = -1;
+    const int whole = p->whole, parts = p->parts;
+    if (q >= whole) {
+        const int v = q - whole, c = v / parts;
+        part = v - c * parts;
+        cut = p->cut0 + c;
+        q = whole + c;
+    }
     // M tiles in groups of 16, N tiles outer in a group: tiles that run together share operands in L2
     const int per = 16 * p->tiles_n, grp = q / per, first = grp * 16;
     const int rows = min(16, p->tiles_m - first), r = q - grp * per;
-    FfTile o{p, first + r % rows, r / rows, 0, p->kb, cut, part, p->M, p->N, p->kb0, p->a_mn, p->b_mn};
+    FfTile o{p, first + r % rows, r / rows, 0, p->kb, cut, part, parts, p->M, p->N, p->kb0, p->a_mn, p->b_mn};
     if (cut >= 0) {
         const int kb = o.k1;
-        o.k0 = kb * part / l.parts;
-        o.k1 = kb * (part + 1) / l.parts;
+        o.k0 = kb * part / parts;
+        o.k1 = kb * (part + 1) / parts;
     }
     return o;
 }
@@ -280,15 +308,16 @@ __device__ __forceinline__ int ff_chunk(int half, int i) {
 }
 // Partial sums of a cut tile's part, for each epilogue warp of the pair (slab): its four chunks, each
 // [8 pieces of 4 columns][32 rows][4] fp32.
-__device__ __forceinline__ float4* ff_partial(const FfLaunch& l, int cut, int part, int slab, int lane) {
-    return reinterpret_cast<float4*>(l.partial + (((size_t)cut * l.parts + part) * 16 + slab) * 4096) + lane;
+__device__ __forceinline__ float4* ff_partial(const FfLaunch& l, const FfTile& t, int part, int slab, int lane) {
+    const int slot = t.p->slot0 + (t.cut - t.p->cut0) * t.parts + part;
+    return reinterpret_cast<float4*>(l.partial + ((size_t)slot * 16 + slab) * 4096) + lane;
 }
 // A part of a cut tile: keeps this warp's sums and counts them as done. In the part that comes last,
 // all parts' sums are added up in their order, put back into the accumulator, and the warp goes on to
 // finish its values (true). Nothing waits for another CTA.
 template <int MODE>
 __device__ __forceinline__ bool ff_collect(const FfLaunch& l, const FfTile& t, uint32_t tb, int half, int slab, int lane) {
-    float4* o = ff_partial(l, t.cut, t.part, slab, lane);
+    float4* o = ff_partial(l, t, t.part, slab, lane);
 #pragma unroll 1
     for (int i = 0; i < 4; ++i) {
         uint32_t v[32];
@@ -304,18 +333,18 @@ __device__ __forceinline__ bool ff_collect(const FfLaunch& l, const FfTile& t, u
     if (lane == 0) {
         uint32_t* count = l.arrived + t.cut * 16 + slab;
         before = atom_acq_rel_gpu_add(count, 1u);
-        if (before + 1 == (uint32_t)l.parts) *count = 0;  // for the next launch
+        if (before + 1 == (uint32_t)t.parts) *count = 0;  // for the next launch
     }
     before = __shfl_sync(0xffffffffu, before, 0);
-    if (before + 1 != (uint32_t)l.parts) return false;
+    if (before + 1 != (uint32_t)t.parts) return false;
     __threadfence();
 #pragma unroll 1
     for (int i = 0; i < 4; ++i) {
         uint32_t v[32];
         float4 next[8];  // a part's sums are in flight while the one before is added
         auto load = [&](int q) {
-            if (q >= l.parts || q == t.part) return;
-            const float4* from = ff_partial(l, t.cut, q, slab, lane) + i * 256;
+            if (q >= t.parts || q == t.part) return;
+            const float4* from = ff_partial(l, t, q, slab, lane) + i * 256;
 #pragma unroll
             for (int k = 0; k < 8; ++k) next[k] = __ldcg(from + k * 32);
         };
@@ -324,7 +353,7 @@ __device__ __forceinline__ bool ff_collect(const FfLaunch& l, const FfTile& t, u
         float sum[32];
 #pragma unroll
         for (int k = 0; k < 32; ++k) sum[k] = 0.f;
-        for (int q = 0; q < l.parts; ++q) {
+        for (int q = 0; q < t.parts; ++q) {
             float4 cur[8];
 #pragma unroll
             for (int k = 0; k < 8; ++k)
@@ -476,7 +505,7 @@ __device__ __forceinline__ void ff_forms(int form, F f) {
     else f(FxInt<3>());
 }
 
-// Persistent GEMM on CTA pairs: cluster c takes tiles c, c + clusters, ... of the launch's list.
+// Persistent GEMM on CTA pairs: each cluster takes the units of work that the launch gives it.
 // Warp 0: TMA loads (each CTA its 128 rows of A and 128 of B; both CTAs' loads complete on rank 0's
 // stage barrier). Warp 1: TMEM, and on rank 0 the UMMAs. Warps 2-9: epilogue of the CTA's 128 rows,
 // overlapping the next tile's products through two accumulators. Every wait is bounded; one that
@@ -527,16 +556,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(FF_THREADS, 1)
     if (warp == 0 && lane == 0) {
         FfRing ring;
         bool ok = !bad;
-        for (int t = cluster; ok && t < l.units; t += clusters) {
-            const FfTile tr = ff_tile(l, t);
+        for (int i = 0, u; ok && (u = ff_unit(l, cluster, clusters, i)) >= 0; ++i) {
+            const FfTile tr = ff_tile(l, u);
             const int arow = tr.m * FT_M + (int)rank * 128;
             const int brow = MODE == FF_SWIGLU ? tr.n * 128 : tr.n * FT_N + (int)rank * 128;
             auto load = [&](auto form) {
                 constexpr bool A_MN = decltype(form)::value & 1, B_MN = (decltype(form)::value & 2) != 0;
                 // the first pair of operands, then (dx) the second
-                for (int i = 0; ok && i < 2; ++i) {
-                    const int from = i ? max(0, tr.k0 - tr.kb0) : tr.k0, to = i ? tr.k1 - tr.kb0 : min(tr.k1, tr.kb0);
-                    const CUtensorMap *ma = tr.p->a + i, *mb = tr.p->b + (MODE == FF_SWIGLU ? (int)rank : i);
+                for (int h = 0; ok && h < 2; ++h) {
+                    const int from = h ? max(0, tr.k0 - tr.kb0) : tr.k0, to = h ? tr.k1 - tr.kb0 : min(tr.k1, tr.kb0);
+                    const CUtensorMap *ma = tr.p->a + h, *mb = tr.p->b + (MODE == FF_SWIGLU ? (int)rank : h);
                     if (rank == 0) ok = ff_produce<A_MN, B_MN, false>(sm, ring, ma, mb, arow, brow, from, to, tmo);
                     else ok = ff_produce<A_MN, B_MN, true>(sm, ring, ma, mb, arow, brow, from, to, tmo);
                 }
@@ -558,8 +587,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(FF_THREADS, 1)
             FfRing ring;
             int b = 0;
             uint32_t aph = 0;
-            for (int t = cluster; ok && t < l.units; t += clusters) {
-                const FfTile tr = ff_tile(l, t);
+            for (int i = 0, u; ok && (u = ff_unit(l, cluster, clusters, i)) >= 0; ++i) {
+                const FfTile tr = ff_tile(l, u);
                 if (!mbar_wait_cluster(&sm.acc_empty[b], aph ^ 1u, tmo, sm.abort)) {
                     ok = false;
                     break;
@@ -587,8 +616,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(FF_THREADS, 1)
         const uint32_t acc_empty0 = mapa_shared(smem_u32(sm.acc_empty), 0u);
         int b = 0;
         uint32_t aph = 0;
-        for (int t = cluster; !bad && t < l.units; t += clusters) {
-            const FfTile tr = ff_tile(l, t);
+        for (int i = 0, u; !bad && (u = ff_unit(l, cluster, clusters, i)) >= 0; ++i) {
+            const FfTile tr = ff_tile(l, u);
             const int row0 = tr.m * FT_M + (int)rank * 128 + q * 32;
             FfKept kept;
             if (MODE == FF_DACT) kept.load(l, tr, row0, half, 0, lane);
@@ -933,10 +962,6 @@ __global__ void __launch_bounds__(GEMM_THREADS, 1) flex_kernel(const __grid_cons
 
 // ---- host side -----------------------------------------------------------------------------------
 
-// Parts of cut tiles in a launch, and words of the status area: [0] status, [1] detail, [128...] arrivals.
-constexpr int FF_MAX_CUT = 160, FF_ARRIVED = 128;
-static_assert((FF_ARRIVED + FF_MAX_CUT / 2 * 2 * FF_WARPS) * 4 <= MOE_FFN_STATUS_BYTES, "arrival counts");
-
 struct FfLayout {
     size_t T, d, F;
     size_t h, dg, du, partial, ws_bytes;  // workspace: status words, then h (or dg), du, partial sums
@@ -998,7 +1023,7 @@ struct FfList {
     FfLaunch l;
     int rc = MOE_OK;
     FfList() {  // the products' maps are written as they are added, the others not at all
-        l.count = l.tiles = l.beside = 0;
+        l.count = l.units = l.first = l.extra = l.beside = 0;
         l.gu = nullptr;
         l.gu_cols = 0;
     }
@@ -1014,8 +1039,8 @@ struct FfList {
         p.b_mn = b_mn;
         p.tiles_m = (int)((M + FT_M - 1) / FT_M);
         p.tiles_n = (int)((N + FT_N - 1) / FT_N);
-        p.tile0 = l.tiles;
-        l.tiles += p.tiles_m * p.tiles_n;
+        p.whole = p.tiles_m * p.tiles_n;
+        p.parts = 1;
         try_(ff_operand(&p.a[0], a, M, K, a_mn));
         try_(ff_operand(&p.b[0], b, N, K, b_mn));
         if (a2) {
@@ -1041,6 +1066,7 @@ constexpr float US_DENSE = 4.9f, US_DENSE_KB = 0.287f;      // a launch; a k-blo
 constexpr float US_DENSE_WAVE = 1.9f;                       // a wave beside its k-blocks or epilogue
 constexpr float US_DENSE_EPI[4] = {1.5f, 0.6f, 2.9f, 9.3f};  // a tile's epilogue, by kind
 constexpr float US_CUT_ROUND = 6.3f, US_CUT_PART = 1.1f;    // a round of parts; adding up each further part
+constexpr float US_APART = 3.5f;                            // dx in a launch of its own, the next one beside it
 constexpr float US_FLEX = 1.45f, US_FLEX_CTA = 1.09f;       // a launch; a CTA beside its k-blocks
 constexpr float US_FLEX_BYTES = 150.9e3f;                   // bytes a microsecond into a SM
 constexpr float US_FLEX_LATENCY = 1.15f;                    // of a load, shared by the stages in flight
@@ -1095,6 +1121,33 @@ cudaError_t ff_clusters(int* out) {
     return cudaSuccess;
 }
 
+// Numbers the units. Where all tiles take alike, those of the last incomplete wave are cut before.
+void ff_lay_out(FfLaunch& l, int clusters) {
+    if (!l.first) {
+        int tiles = 0;
+        for (int i = 0; i < l.count; ++i) tiles += l.p[i].whole;
+        const FfCut cut = ff_cut(tiles, l.p[0].kb, clusters);
+        for (int i = l.count - 1, rest = cut.parts > 1 ? tiles - cut.full : 0; rest; --i) {
+            FfProblem& p = l.p[i];
+            const int n = rest < p.whole ? rest : p.whole;
+            p.whole -= n;
+            p.parts = cut.parts;
+            rest -= n;
+        }
+    }
+    int cuts = 0, slots = 0;
+    l.units = 0;
+    for (int i = 0; i < l.count; ++i) {
+        FfProblem& p = l.p[i];
+        p.unit0 = l.units;
+        p.cut0 = cuts;
+        p.slot0 = slots;
+        l.units += p.units();
+        cuts += p.cut();
+        slots += p.cut() * p.parts;
+    }
+}
+
 template <int MODE>
 int ff_run(FfList& list, const FfLayout& L, void* ws, cudaStream_t st, const char* what) {
     if (list.rc) return list.rc;
@@ -1106,12 +1159,7 @@ int ff_run(FfList& list, const FfLayout& L, void* ws, cudaStream_t st, const cha
     int clusters = 0;
     cudaError_t e = ff_clusters<MODE>(&clusters);
     if (e == cudaSuccess) {
-        int kb = 1 << 30;
-        for (int i = 0; i < l.count; ++i) kb = l.p[i].kb < kb ? l.p[i].kb : kb;
-        const FfCut cut = ff_cut(l.tiles, kb, clusters);
-        l.full = cut.full;
-        l.parts = cut.parts;
-        l.units = cut.full + (l.tiles - cut.full) * cut.parts;
+        ff_lay_out(l, clusters);
         const int n = l.units < clusters ? l.units : clusters;
         e = launch_k(dense_kernel<MODE>, dim3(2 * n), dim3(FF_THREADS), FF_SMEM, st, true, list.l);
     }
@@ -1226,11 +1274,46 @@ FxArgs fx_args(size_t M, size_t T, int kb0, int kb, void* out, int early) {
     return p;
 }
 
+// A dense launch over the tiles of products of two lengths, `cuttable` ones and `fixed` ones: in how many
+// parts each cuttable tile goes, and how the units go round (ff_unit), the longer kind first.
+struct FfSchedule {
+    int parts, cut_last, extra;
+    float us;
+};
+FfSchedule ff_schedule(int cuttable, int cuttable_kb, int fixed, int fixed_kb, int clusters) {
+    auto tile = [](float work) {
+        const float epi = US_DENSE_EPI[FK_PLAIN];
+        return (work > epi ? work : epi) + US_DENSE_WAVE;
+    };
+    const float fixed_us = tile(fixed_kb * US_DENSE_KB);
+    FfSchedule best{1, 0, 0, 1e30f};
+    for (int parts = 1; parts <= 8; ++parts) {
+        if (parts > 1 && (cuttable > FF_MAX_CUT / 2 || cuttable * parts > FF_MAX_CUT || parts * 4 > cuttable_kb)) break;
+        const float part = (cuttable_kb + parts - 1) / parts * US_DENSE_KB;
+        const float cut_us = parts > 1 ? part + US_CUT_ROUND : tile(part);
+        const int cut_last = cut_us < fixed_us;
+        const int n1 = cut_last ? fixed : cuttable * parts, n2 = cut_last ? cuttable * parts : fixed;
+        const float t1 = cut_last ? fixed_us : cut_us, t2 = cut_last ? cut_us : fixed_us;
+        const int rounds = n1 / clusters, high = n1 % clusters, low = clusters - high;
+        const int most = high ? (int)(t1 / t2) + 1 : 0;
+        for (int extra = 0; extra <= most && extra * low <= n2; ++extra) {
+            const int left = n2 - extra * low, more = left / clusters, rest = left % clusters;
+            const float end_low = rounds * t1 + (extra + more + (rest > 0)) * t2;
+            const float end_high = high ? (rounds + 1) * t1 + (more + (rest > low)) * t2 : 0.0f;
+            const float us = US_DENSE + (end_low > end_high ? end_low : end_high) + US_DENSE_EPI[FK_PLAIN] +
+                             US_CUT_PART * (parts - 1);
+            if (us < best.us) best = FfSchedule{parts, cut_last, extra, us};
+        }
+    }
+    return best;
+}
+
 // The plans of a config's products. h for a backward pass (kept) and the hidden gradients (act) take the
 // same kernel, because it fixes the layout in which g and u are kept.
 struct FfPlans {
     int T, d, F, sms;
     FxPlan h, kept, act, down, dx;
+    FfSchedule grad;  // of dx and the weight gradients in one launch, unless dx has a plan on flex_kernel
 };
 const FfPlans& ff_plans(const FfLayout& L, int sms) {
     static thread_local FfPlans last[4] = {};  // a program alternates between few configs
@@ -1246,8 +1329,21 @@ const FfPlans& ff_plans(const FfLayout& L, int sms) {
         kept = dk;
         act = da;
     }
-    p = FfPlans{T, d, F, sms, ff_choose(F, T, kd, FK_H, sms), kept, act, ff_choose(d, T, kf, FK_PLAIN, sms),
-                ff_choose(d, T, 2 * kf, FK_PLAIN, sms)};
+    p.T = T;
+    p.d = d;
+    p.F = F;
+    p.sms = sms;
+    p.h = ff_choose(F, T, kd, FK_H, sms);
+    p.kept = kept;
+    p.act = act;
+    p.down = ff_choose(d, T, kf, FK_PLAIN, sms);
+    // dx with the weight gradients in one launch, or on flex_kernel with them beside it
+    p.dx = ff_choose_flex(d, T, 2 * kf, FK_PLAIN, sms);
+    const int kt = (T + BK - 1) / BK;
+    auto tiles = [](int m, int n) { return (m + FT_M - 1) / FT_M * ((n + FT_N - 1) / FT_N); };
+    const int dw = 2 * tiles(F, d) + tiles(d, F);
+    p.grad = ff_schedule(tiles(T, d), 2 * kf, dw, kt, sms / 2);
+    if (p.grad.us <= p.dx.us + ff_cut(dw, kt, sms / 2).us + US_APART) p.dx.nt = 0;
     return p;
 }
 
@@ -1319,7 +1415,7 @@ MOE_API int moe_ffn_forward(const moe_ffn_config* c, const uint16_t* x, const ui
         FfProblem& p = up.add(x, 0, W1, 0, h, L.T, L.F, L.d);
         up.try_(ff_operand(&p.b[1], W3, L.F, L.d, 0));
         p.tiles_n = (int)((L.F + 127) / 128);  // 128 columns of g beside 128 of u
-        up.l.tiles = p.tiles_m * p.tiles_n;
+        p.whole = p.tiles_m * p.tiles_n;
         up.l.gu = gu;
         up.l.gu_cols = L.gu_cols;
         if ((rc = ff_run<FF_SWIGLU>(up, L, ws, st, "gate and up projections"))) return rc;
@@ -1386,12 +1482,29 @@ MOE_API int moe_ffn_backward(const moe_ffn_config* c, const uint16_t* x, const u
         if ((rc = fx_operands(p, 1, W3, 1, du, L.d, L.T, L.F, dx_plan.nt))) return rc;
         if ((rc = fx_run<FF_PLAIN, true>(p, dx_plan, L, ws, st, "input gradients"))) return rc;
         grad.l.beside = 1;  // the weight gradients do not need dx
-    } else {
-        grad.add(dg, 0, W1, 1, dx, L.T, L.d, L.F, du, W3);
     }
+    const FfSchedule& order = plans.grad;
+    auto units = [&] {
+        int n = 0;
+        for (int i = 0; i < grad.l.count; ++i) n += grad.l.p[i].units();
+        return n;
+    };
+    auto add_dx = [&] {
+        FfProblem& p = grad.add(dg, 0, W1, 1, dx, L.T, L.d, L.F, du, W3);
+        if (order.parts > 1) p.whole = 0;
+        p.parts = order.parts;
+    };
+    if (!dx_plan.nt && !order.cut_last) add_dx();
+    int first = units();
     grad.add(dg, 1, x, 1, dW1, L.F, L.d, L.T);
     grad.add(du, 1, x, 1, dW3, L.F, L.d, L.T);
     grad.add(dy, 1, h, 1, dW2, L.d, L.F, L.T);
+    if (!dx_plan.nt && order.cut_last) {
+        first = units();
+        add_dx();
+    }
+    grad.l.first = first;  // none where dx has a launch of its own
+    grad.l.extra = first ? order.extra : 0;
     return ff_run<FF_PLAIN>(grad, L, ws, st, "input and weight gradients");
 }
 
