@@ -4,16 +4,26 @@
 //   dh = dy W2, s = 1 / (1 + exp(-g)), dg = dh u s (1 + g (1 - s)), du = dh g s
 //   dx = dg W1 + du W3, dW1 = dg^T x, dW3 = du^T x, dW2 = dy^T h
 //
-// Every product runs in dense_kernel, a persistent tcgen05 GEMM on CTA pairs (UMMA 256 x 256 x 16,
-// cta_group::2, fp32 accumulators in TMEM, operands by TMA through a seven-stage ring) that takes a
-// list of products per launch and reads either operand K-major or MN-major, so no transposed copy is
-// ever written: dh, dx read the weights and dW1, dW3, dW2 read both operands along their rows.
+// Two kernels run the products. dense_kernel is a persistent tcgen05 GEMM on CTA pairs (UMMA 256 x 256 x 16,
+// cta_group::2, fp32 accumulators in TMEM, operands by TMA through a seven-stage ring) over a list of
+// products. flex_kernel is for few tokens or few tiles: 128 features by 16 to 128 tokens a CTA, the k-blocks
+// split over a cluster. An estimate of both, fitted to 15,400 measured launches, says which one a product
+// takes (ff_choose). Both read an operand K-major or MN-major, so no transposed copy is ever written: dh, dx
+// read the weights and dW1, dW3, dW2 read both operands along their rows.
 //   launch 1 (forward)   g and u side by side in one accumulator; epilogue: h, and g, u in fp32
 //   launch 2 (forward)   y
 //   launch 3 (backward)  dh; epilogue: dg, du from the kept g, u
-//   launch 4 (backward)  dx (one sum over dg W1 and du W3), dW1, dW3, dW2 as one list of tiles
-// The block is bound by the tensor cores (18 T d ffn flops against 2 (4 T d + 6 d ffn) bytes of
-// tensors). g and u are kept in fp32: rounding them would round dg and du twice, and computing them
+//   launch 4 (backward)  dx (one sum over dg W1 and du W3), dW1, dW3, dW2 as one list of tiles; for few
+//                        tokens dx on flex_kernel and the weight gradients beside it
+// With many tokens the block is bound by the tensor cores (18 T d ffn flops against 2 (4 T d + 6 d ffn)
+// bytes of tensors), with few by HBM (the weights) or, for a single token of a small block, by the two
+// launches that follow one another. Measured (d, ffn; shares of a measured copy's and product's rates):
+//   forward, 4096 tokens (4096, 14336)      850 us in a long run under the power limit, 1.70 PF (99 % of the
+//                                           sustained rate), 741-764 us in a short one
+//   forward, 37 tokens (4096, 14336)        66 us, 5.3 TB/s (78 %)
+//   forward, 1 token (2048, 1408)           10 us, two launches of 3.5 to 5 us
+//   both passes, 8192 tokens (2048, 5632)   1142 us, 1.49 PF (79 %; 87 % of the sustained rate)
+// g and u are kept in fp32: rounding them would round dg and du twice, and computing them
 // again costs 4 T d ffn flops where keeping them costs 16 T ffn bytes of traffic (at d = 2048 and the
 // measured rates a quarter of that time, and hidden behind the products).
 // h, dg and du are rounded to bf16 because they are operands of the next product.
