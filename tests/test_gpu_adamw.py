@@ -106,6 +106,27 @@ def test_8_bits_equal_the_oracle(sizes, pt, gt, shift):
         assert (np.abs(f64(p[i]) - wp) <= far + (2.0 ** -8 * np.abs(wp) if pt == BF else 0)).all()
 
 
+@pytest.mark.parametrize("gt", [F32, BF])
+def test_8_bits_long_list(gt):
+    """More chunks than a launch has under way, in tensors of whole and of odd chunks, one with scales off an
+    aligned start: the states are those of the same tensors one by one, off an aligned start."""
+    sizes = [4096 * 700 + 5, 3, 4096 * 300, 130, 4096 * 250 + 4095, 77, 4096 * 40]
+    one, two = ([list(l) for l in tensors(sizes, F32, gt, 8, 1, shift)] for shift in (0, 3))
+    odd = torch.zeros(one[4][2].numel() + 1, dtype=torch.uint8, device="cuda")
+    odd[1:] = one[4][2]
+    one[4][2] = odd[1:]
+    base = [7 * i for i in range(len(sizes))]
+    cfg = tlc.AdamWConfig(**HYPER, bits=8, seed=9)
+    tlc.adamw_step(cfg, tlc.AdamWList(cfg, *one, rng_base=base), 3)
+    for i in range(len(sizes)):
+        tlc.adamw_step(cfg, tlc.AdamWList(cfg, *([l[i]] for l in two), rng_base=base[i:i + 1]), 3)
+    for a, b in zip(one[2:], two[2:]):
+        for x, y in zip(a, b):
+            assert torch.equal(x, y)
+    for x, y in zip(one[0], two[0]):  # one rounding more or less of the sum, and of its smaller term
+        assert ((x - y).abs() <= 2.0 ** -22 * x.abs() + 1e-3 * 2.0 ** -18).all()
+
+
 def test_small_changes_are_not_lost():
     """v decays by 0.1 % a step with no gradient: after 1000 steps its mean has fallen by 1/e, although
     one step is far below half a rounding step. Rounding adds variance but no drift: the mean over

@@ -18,7 +18,7 @@
 // With many tokens the block is bound by the tensor cores (18 T d ffn flops against 2 (4 T d + 6 d ffn)
 // bytes of tensors), with few by HBM (the weights) or, for a single token of a small block, by the two
 // launches that follow one another. Measured (d, ffn; shares of a measured copy's and product's rates):
-//   forward, 4096 tokens (4096, 14336)      850 us in a long run under the power limit, 1.70 PF (99 % of the
+//   forward, 4096 tokens (4096, 14336)      849 us in a long run under the power limit, 1.70 PF (99 % of the
 //                                           sustained rate), 741-764 us in a short one
 //   forward, 37 tokens (4096, 14336)        66 us, 5.3 TB/s (78 %)
 //   forward, 1 token (2048, 1408)           10 us, two launches of 3.5 to 5 us
