@@ -9,7 +9,7 @@
 // parameters (no table in device memory to keep in step with the caller's pointers, nothing to copy
 // before the launch, and a captured graph holds it).
 // Measured with 24 tensors, 149 million values, bf16 gradients and copies: fp32 states 623 us, 6.7 TB/s
-// (98 % of a copy's rate); 8-bit states 467 us, 5.1 TB/s, bound by the 77 instructions a value that
+// (98 % of a copy's rate); 8-bit states 467 us, 5.1 TB/s, bound by the 73 instructions a value that
 // decoding, the roots and the random roundings take; reading 8-bit states back 250 us, 6.0 TB/s.
 //
 // 8-bit states. A block of 128 consecutive values has one power-of-two scale for m and one for v, so
