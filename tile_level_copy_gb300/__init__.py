@@ -649,10 +649,10 @@ def adamw_step(cfg: AdamWConfig, tensors: AdamWList, step: int, grad_scale: Opti
     """moe_adamw_step: one step (counted from 1) over every tensor; grad_scale: a float32 value on the GPU."""
     if cfg.bits != tensors.bits:
         raise ValueError(f"the list was made for {tensors.bits}-bit states")
-    ref, c = cfg.ref()
+    c = _AdamWConfig.from_buffer_copy(cfg.ref()[1])  # its own: threads may step at once with one config
     c.step = step
-    _check(lib().moe_adamw_step(ref, tensors.c, tensors.count, _flat(grad_scale, torch.float32, 1, "grad_scale"),
-                                tensors.stream(stream)))
+    _check(lib().moe_adamw_step(ctypes.byref(c), tensors.c, tensors.count,
+                                _flat(grad_scale, torch.float32, 1, "grad_scale"), tensors.stream(stream)))
 
 
 def adamw_read_state(cfg: AdamWConfig, tensors: AdamWList, out: AdamWValues, stream=None) -> None:
