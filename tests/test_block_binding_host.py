@@ -1,4 +1,8 @@
 """Host-only checks of the block operators' binding: what it hands to the library, and what it refuses."""
+import copy
+import dataclasses
+import pickle
+
 import pytest
 import torch
 
@@ -35,3 +39,13 @@ def test_adamw_step_hands_over_its_own_step(monkeypatch):
     tlc.adamw_step(cfg, lst, 5, stream=0)
     assert seen == [None, 9, 5]
     assert cfg.ref()[1].step == 1  # the config's own struct stays as it was made
+
+
+@pytest.mark.parametrize("cfg", [tlc.FFNConfig(4, 128, 256), tlc.LayerNormConfig(4, 64), tlc.AdamWConfig(lr=1e-3, seed=7)],
+                         ids=lambda c: type(c).__name__)
+def test_a_used_config_is_copied_and_pickled(built_library, cfg):
+    cfg.ref()
+    for other in (copy.copy(cfg), copy.deepcopy(cfg), pickle.loads(pickle.dumps(cfg)), dataclasses.replace(cfg)):
+        assert other == cfg and type(other) is type(cfg)
+        assert other.ref()[1] is not cfg.ref()[1]  # a C form of its own
+        assert bytes(other.ref()[1]) == bytes(cfg.ref()[1])

@@ -429,6 +429,9 @@ class _Marshalled:
         object.__setattr__(self, name, value)
         object.__setattr__(self, "_kept", None)
 
+    def __getstate__(self):  # a copy, and a pickle, is made without the C form and its pointer
+        return {**self.__dict__, "_kept": None}
+
     def ref(self):
         """Pointer to the C form (and whatever sizes the config's class keeps beside it)."""
         if self._kept is None:
