@@ -419,8 +419,8 @@ MOE_API int moe_route_static(const moe_config* cfg, const float* logits, int32_t
  *
  * A dense gated feed-forward block (forward, backward and its form for few tokens), layer norm
  * (forward, backward) and the AdamW step. Same rules as above: the caller owns every buffer and the
- * stream, nothing is allocated or synchronised (moe_ffn_status synchronises), an argument error is
- * returned before any launch. The tile-level pages have no counterpart of these operators.
+ * stream, all of them of the calling thread's current device, nothing is allocated or synchronised
+ * (moe_ffn_status synchronises), an argument error is returned before any launch. The tile-level pages have no counterpart of these operators.
  */
 
 /* Types of values. */

@@ -393,32 +393,52 @@ def device_info():
 # everything that is right, and the search for what is wrong only after it has failed.
 
 
-def _dev(t: Optional[torch.Tensor], dtype, shape, name: str):
-    """Device pointer of a contiguous tensor of this type and shape (None: NULL)."""
+def _device() -> int:
+    """The current device. The kernels are launched there, so every tensor of a call has to be on it."""
+    return torch._C._cuda_getDevice()
+
+
+def _local(t: torch.Tensor, dtype, dev: int, name: str):
+    """Device pointer of a contiguous tensor of this type (None: of any) on device dev."""
+    p = _ptr(t, dtype, "cuda", name)
+    if t.get_device() != dev:
+        raise ValueError(f"{name} is on cuda:{t.get_device()}, the call is for cuda:{dev}")
+    return p
+
+
+def _dev(t: Optional[torch.Tensor], dtype, shape, dev: int, name: str):
+    """Device pointer of a contiguous tensor of this type and shape on device dev (None: NULL)."""
     if t is None:
         return None
-    if t.dtype is dtype and t.is_cuda and t.shape == shape and t.is_contiguous():
+    if t.dtype is dtype and t.get_device() == dev and t.shape == shape and t.is_contiguous():
         return t.data_ptr()
     if t.shape != shape:
         raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
-    return _ptr(t, dtype, "cuda", name)
+    return _local(t, dtype, dev, name)
 
 
-def _flat(t: Optional[torch.Tensor], dtype, n: int, name: str):
+def _flat(t: Optional[torch.Tensor], dtype, n: int, dev: int, name: str):
     """The same for a tensor of n values of any shape."""
     if t is None:
         return None
-    if t.dtype is dtype and t.is_cuda and t.numel() == n and t.is_contiguous():
+    if t.dtype is dtype and t.get_device() == dev and t.numel() == n and t.is_contiguous():
         return t.data_ptr()
     if t.numel() != n:
         raise ValueError(f"{name} must hold {n} values, got {t.numel()}")
-    return _ptr(t, dtype, "cuda", name)
+    return _local(t, dtype, dev, name)
 
 
-def _raw_stream(stream, t: torch.Tensor):
-    """Raw stream handle; the default is the current stream of t's device."""
+def _space(ws, dev: int):
+    """Pointer to a workspace on device dev."""
+    if ws.buf.get_device() != dev:
+        raise ValueError(f"the workspace is on {ws.buf.device}, the call is for cuda:{dev}")
+    return ws.ptr
+
+
+def _raw_stream(stream, dev: int):
+    """Raw stream handle; the default is the current stream of device dev."""
     if stream is None:
-        return torch._C._cuda_getCurrentRawStream(t.get_device())
+        return torch._C._cuda_getCurrentRawStream(dev)
     return _stream(stream)
 
 
@@ -478,41 +498,42 @@ def ffn_saved(cfg: FFNConfig, device="cuda") -> torch.Tensor:
     return torch.empty(cfg.ref()[5], dtype=torch.uint8, device=device)
 
 
-def _saved(saved, need: int):
+def _saved(saved, need: int, dev: int):
     if saved is None:
         return None
     n = saved.numel() * saved.element_size()
     if n < need:
         raise ValueError(f"saved has {n} bytes, needs {need}")
-    return _ptr(saved, None, "cuda", "saved")
+    return _local(saved, None, dev, "saved")
 
 
 def ffn_forward(cfg: FFNConfig, x: torch.Tensor, W1: torch.Tensor, W3: torch.Tensor, W2: torch.Tensor,
                 y: torch.Tensor, ws: FFNWorkspace, saved: Optional[torch.Tensor] = None, stream=None) -> None:
     """moe_ffn_forward: y = (silu(x W1^T) * (x W3^T)) W2^T; saved (ffn_saved) for a backward pass."""
-    bf = torch.bfloat16
+    bf, on = torch.bfloat16, _device()
     c, _, rows, up, down, need = cfg.ref()
-    _check(lib().moe_ffn_forward(c, _dev(x, bf, rows, "x"), _dev(W1, bf, up, "W1"), _dev(W3, bf, up, "W3"),
-                                 _dev(W2, bf, down, "W2"), _dev(y, bf, rows, "y"), _saved(saved, need), ws.ptr,
-                                 ws.nbytes, _raw_stream(stream, x)))
+    _check(lib().moe_ffn_forward(c, _dev(x, bf, rows, on, "x"), _dev(W1, bf, up, on, "W1"), _dev(W3, bf, up, on, "W3"),
+                                 _dev(W2, bf, down, on, "W2"), _dev(y, bf, rows, on, "y"), _saved(saved, need, on),
+                                 _space(ws, on), ws.nbytes, _raw_stream(stream, on)))
 
 
 def ffn_backward(cfg: FFNConfig, x: torch.Tensor, W1: torch.Tensor, W3: torch.Tensor, W2: torch.Tensor,
                  dy: torch.Tensor, saved: torch.Tensor, dx: torch.Tensor, dW1: torch.Tensor, dW3: torch.Tensor,
                  dW2: torch.Tensor, ws: FFNWorkspace, stream=None) -> None:
     """moe_ffn_backward: gradients of x and the weights from dy and the forward pass's saved buffer."""
-    bf = torch.bfloat16
+    bf, on = torch.bfloat16, _device()
     c, _, rows, up, down, need = cfg.ref()
-    _check(lib().moe_ffn_backward(c, _dev(x, bf, rows, "x"), _dev(W1, bf, up, "W1"), _dev(W3, bf, up, "W3"),
-                                  _dev(W2, bf, down, "W2"), _dev(dy, bf, rows, "dy"), _saved(saved, need),
-                                  _dev(dx, bf, rows, "dx"), _dev(dW1, bf, up, "dW1"), _dev(dW3, bf, up, "dW3"),
-                                  _dev(dW2, bf, down, "dW2"), ws.ptr, ws.nbytes, _raw_stream(stream, x)))
+    _check(lib().moe_ffn_backward(c, _dev(x, bf, rows, on, "x"), _dev(W1, bf, up, on, "W1"),
+                                  _dev(W3, bf, up, on, "W3"), _dev(W2, bf, down, on, "W2"),
+                                  _dev(dy, bf, rows, on, "dy"), _saved(saved, need, on), _dev(dx, bf, rows, on, "dx"),
+                                  _dev(dW1, bf, up, on, "dW1"), _dev(dW3, bf, up, on, "dW3"),
+                                  _dev(dW2, bf, down, on, "dW2"), _space(ws, on), ws.nbytes, _raw_stream(stream, on)))
 
 
 def ffn_status(cfg: FFNConfig, ws: FFNWorkspace, stream=None):
     """(return code, detail) of the calls on ws; synchronises the stream."""
     detail = ctypes.c_int32()
-    rc = lib().moe_ffn_status(cfg.ref()[0], ws.ptr, _stream(stream), ctypes.byref(detail))
+    rc = lib().moe_ffn_status(cfg.ref()[0], _space(ws, _device()), _stream(stream), ctypes.byref(detail))
     return rc, detail.value
 
 
@@ -548,11 +569,12 @@ def layernorm_forward(cfg: LayerNormConfig, x: torch.Tensor, w: Optional[torch.T
                       y: torch.Tensor, mean: Optional[torch.Tensor] = None, rstd: Optional[torch.Tensor] = None,
                       stream=None) -> None:
     """moe_layernorm_forward: y = (x - mean) * rstd * w + b; mean and rstd [rows] for a backward pass."""
-    dt, wt, rows, d = cfg.dtype, cfg.wdtype, cfg.rows, cfg.d
+    dt, wt, rows, d, on = cfg.dtype, cfg.wdtype, cfg.rows, cfg.d, _device()
     n, f32 = rows * d, torch.float32
-    _check(lib().moe_layernorm_forward(cfg.ref()[0], _flat(x, dt, n, "x"), _flat(w, wt, d, "w"), _flat(b, wt, d, "b"),
-                                       _flat(y, dt, n, "y"), _flat(mean, f32, rows, "mean"),
-                                       _flat(rstd, f32, rows, "rstd"), _raw_stream(stream, x)))
+    _check(lib().moe_layernorm_forward(
+        cfg.ref()[0], _flat(x, dt, n, on, "x"), _flat(w, wt, d, on, "w"), _flat(b, wt, d, on, "b"),
+        _flat(y, dt, n, on, "y"), _flat(mean, f32, rows, on, "mean"), _flat(rstd, f32, rows, on, "rstd"),
+        _raw_stream(stream, on)))
 
 
 def layernorm_backward(cfg: LayerNormConfig, dy: torch.Tensor, x: torch.Tensor, w: Optional[torch.Tensor],
@@ -560,13 +582,13 @@ def layernorm_backward(cfg: LayerNormConfig, dy: torch.Tensor, x: torch.Tensor, 
                        db: Optional[torch.Tensor] = None, ws: Optional[LayerNormWorkspace] = None,
                        stream=None) -> None:
     """moe_layernorm_backward: dx, and dw, db summed over the rows (both may be None, then ws too)."""
-    dt, wt, rows, d = cfg.dtype, cfg.wdtype, cfg.rows, cfg.d
+    dt, wt, rows, d, on = cfg.dtype, cfg.wdtype, cfg.rows, cfg.d, _device()
     n, f32 = rows * d, torch.float32
     _check(lib().moe_layernorm_backward(
-        cfg.ref()[0], _flat(dy, dt, n, "dy"), _flat(x, dt, n, "x"), _flat(w, wt, d, "w"),
-        _flat(mean, f32, rows, "mean"), _flat(rstd, f32, rows, "rstd"), _flat(dx, dt, n, "dx"),
-        _flat(dw, wt, d, "dw"), _flat(db, wt, d, "db"), None if ws is None else ws.ptr,
-        0 if ws is None else ws.nbytes, _raw_stream(stream, x)))
+        cfg.ref()[0], _flat(dy, dt, n, on, "dy"), _flat(x, dt, n, on, "x"), _flat(w, wt, d, on, "w"),
+        _flat(mean, f32, rows, on, "mean"), _flat(rstd, f32, rows, on, "rstd"), _flat(dx, dt, n, on, "dx"),
+        _flat(dw, wt, d, on, "dw"), _flat(db, wt, d, on, "db"), None if ws is None else _space(ws, on),
+        0 if ws is None else ws.nbytes, _raw_stream(stream, on)))
 
 
 @dataclasses.dataclass
@@ -603,6 +625,7 @@ class AdamWList:
             if l is not None and len(l) != n:
                 raise ValueError(f"{name} must have one entry per tensor")
         self.bits, self.count = cfg.bits, n
+        self.device = p[0].get_device() if n else None
         self.c = (_AdamWTensor * max(n, 1))()
         self.keep = [p, g, m, v, m_scale, v_scale, copy]
         base = 0
@@ -621,14 +644,18 @@ class AdamWList:
                     raise ValueError(f"{name}[{i}] must be {' or '.join(map(str, dt))}, got {t.dtype}")
                 if t.numel() != want:
                     raise ValueError(f"{name}[{i}] must hold {want} values, got {t.numel()}")
-                setattr(self.c[i], name, (_ptr(t, None, "cuda", f"{name}[{i}]")))
+                setattr(self.c[i], name, _local(t, None, self.device, f"{name}[{i}]"))
             e = self.c[i]
             e.n, e.rng_base = k, base if rng_base is None else int(rng_base[i])
             e.p_dtype, e.g_dtype = _DTYPES[p[i].dtype], _DTYPES[g[i].dtype]
             base += blocks * MOE_ADAMW_BLOCK
 
-    def stream(self, stream):
-        return _raw_stream(stream, self.keep[0][0]) if self.count else _stream(stream)
+    def here(self) -> int:
+        """The current device, on which the list's tensors have to be."""
+        dev = _device()
+        if self.count and self.device != dev:
+            raise ValueError(f"the list's tensors are on cuda:{self.device}, the call is for cuda:{dev}")
+        return dev
 
 
 class AdamWValues:
@@ -642,8 +669,8 @@ class AdamWValues:
             for i, t in enumerate(l):
                 if t.numel() != tensors.c[i].n:
                     raise ValueError(f"{name}[{i}] must hold {tensors.c[i].n} values, got {t.numel()}")
-        self.m = arr(*[_ptr(t, torch.float32, "cuda", "m") for t in m])
-        self.v = arr(*[_ptr(t, torch.float32, "cuda", "v") for t in v])
+        self.m = arr(*[_local(t, torch.float32, tensors.device, "m") for t in m])
+        self.v = arr(*[_local(t, torch.float32, tensors.device, "v") for t in v])
         self.keep = [m, v]
 
 
@@ -652,14 +679,16 @@ def adamw_step(cfg: AdamWConfig, tensors: AdamWList, step: int, grad_scale: Opti
     """moe_adamw_step: one step (counted from 1) over every tensor; grad_scale: a float32 value on the GPU."""
     if cfg.bits != tensors.bits:
         raise ValueError(f"the list was made for {tensors.bits}-bit states")
+    on = tensors.here()
     c = _AdamWConfig.from_buffer_copy(cfg.ref()[1])  # its own: threads may step at once with one config
     c.step = step
     _check(lib().moe_adamw_step(ctypes.byref(c), tensors.c, tensors.count,
-                                _flat(grad_scale, torch.float32, 1, "grad_scale"), tensors.stream(stream)))
+                                _flat(grad_scale, torch.float32, 1, on, "grad_scale"), _raw_stream(stream, on)))
 
 
 def adamw_read_state(cfg: AdamWConfig, tensors: AdamWList, out: AdamWValues, stream=None) -> None:
     """moe_adamw_read_state: the float32 values that the list's 8-bit states stand for."""
     if cfg.bits != 8 or tensors.bits != 8:
         raise ValueError("32-bit states are read as they are")
-    _check(lib().moe_adamw_read_state(tensors.c, tensors.count, out.m, out.v, tensors.stream(stream)))
+    on = tensors.here()
+    _check(lib().moe_adamw_read_state(tensors.c, tensors.count, out.m, out.v, _raw_stream(stream, on)))

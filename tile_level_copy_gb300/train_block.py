@@ -80,9 +80,9 @@ class PreNormBlock:
         """A function x [batch, d] -> y with the trained weights: the form of single-token decoding."""
         d, ffn = self.ffn_cfg.d, self.ffn_cfg.ffn
         fc, lc = tlc.FFNConfig(T=batch, d=d, ffn=ffn), tlc.LayerNormConfig(rows=batch, d=d, dtype=BF)
-        ws, normed, out = tlc.FFNWorkspace(fc), torch.empty(batch, d, dtype=BF, device="cuda"), torch.empty(
-            batch, d, dtype=BF, device="cuda")
-        W = self.weights
+        W, device = self.weights, self.dx.device
+        ws = tlc.FFNWorkspace(fc, device)
+        normed, out = (torch.empty(batch, d, dtype=BF, device=device) for _ in range(2))
 
         def run(x: torch.Tensor) -> torch.Tensor:
             tlc.layernorm_forward(lc, x, self.p["w"], self.p["b"], normed)
