@@ -1,7 +1,9 @@
 """Host-only checks of the block operators' binding: what it hands to the library, and what it refuses."""
 import copy
 import dataclasses
+import gc
 import pickle
+import weakref
 
 import pytest
 import torch
@@ -190,3 +192,22 @@ def test_a_status_of_another_device_is_refused(device_0, monkeypatch):
     ws.buf.index = 1
     with pytest.raises(ValueError, match="cuda:1"):
         tlc.ffn_status(tlc.FFNConfig(4, 128, 256), ws, stream=0)
+
+
+def test_a_list_keeps_its_tensors_whatever_becomes_of_the_callers(device_0):
+    """The library reads the pointers at every step: the tensors live as long as the list, although the
+    caller empties or refills the lists that it made it from."""
+    cfg = tlc.AdamWConfig(lr=1e-3, bits=8)
+    names = {"p": F32, "g": BF, "m": U8, "v": U8, "m_scale": U8, "v_scale": U8, "copy": BF}
+    mine = {n: [Device(d, 1 if "scale" in n else 100)] for n, d in names.items()}
+    lst = tlc.AdamWList(cfg, **mine)
+    m, v = [Device(F32, 100)], [Device(F32, 100)]
+    values = tlc.AdamWValues(lst, m, v)
+    alive = [weakref.ref(l[0]) for l in (*mine.values(), m, v)]
+    for l in (*mine.values(), m, v):
+        l.clear()
+    gc.collect()
+    assert all(r() is not None for r in alive)
+    del lst, values
+    gc.collect()
+    assert all(r() is None for r in alive)

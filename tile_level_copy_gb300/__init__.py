@@ -627,7 +627,7 @@ class AdamWList:
         self.bits, self.count = cfg.bits, n
         self.device = p[0].get_device() if n else None
         self.c = (_AdamWTensor * max(n, 1))()
-        self.keep = [p, g, m, v, m_scale, v_scale, copy]
+        self.keep = [list(l) for l in (p, g, m, v, m_scale, v_scale, copy) if l is not None]
         base = 0
         for i in range(n):
             k = p[i].numel()
@@ -671,7 +671,7 @@ class AdamWValues:
                     raise ValueError(f"{name}[{i}] must hold {tensors.c[i].n} values, got {t.numel()}")
         self.m = arr(*[_local(t, torch.float32, tensors.device, "m") for t in m])
         self.v = arr(*[_local(t, torch.float32, tensors.device, "v") for t in v])
-        self.keep = [m, v]
+        self.keep = [list(m), list(v)]
 
 
 def adamw_step(cfg: AdamWConfig, tensors: AdamWList, step: int, grad_scale: Optional[torch.Tensor] = None,
