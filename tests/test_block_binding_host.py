@@ -38,7 +38,7 @@ def test_adamw_step_hands_over_its_own_step(monkeypatch):
         return tlc.MOE_OK
 
     monkeypatch.setattr(tlc, "lib", lambda: Library(moe_adamw_step=step))
-    monkeypatch.setattr(torch._C, "_cuda_getDevice", lambda: 0, raising=False)
+    monkeypatch.setattr(tlc, "_device", lambda: 0)
     tlc.adamw_step(cfg, lst, 5, stream=0)
     assert seen == [None, 9, 5]
     assert cfg.ref()[1].step == 1  # the config's own struct stays as it was made
@@ -138,8 +138,8 @@ def device_0(monkeypatch):
     """A current device 0, and a library that notes its calls."""
     fake = Library()
     monkeypatch.setattr(tlc, "lib", lambda: fake)
-    monkeypatch.setattr(torch._C, "_cuda_getDevice", lambda: 0, raising=False)
-    monkeypatch.setattr(torch._C, "_cuda_getCurrentRawStream", lambda i: 1000 + i, raising=False)
+    monkeypatch.setattr(tlc, "_device", lambda: 0)
+    monkeypatch.setattr(tlc, "_current_stream", lambda i: 1000 + i)
     return fake
 
 
@@ -182,7 +182,7 @@ def test_a_list_made_on_another_device_is_refused(device_0, monkeypatch):
     lst = tlc.AdamWList(cfg, one(), one(), one(), one())
     with pytest.raises(ValueError, match="cuda:1"):
         tlc.adamw_step(cfg, lst, 1)
-    monkeypatch.setattr(torch._C, "_cuda_getDevice", lambda: 1, raising=False)
+    monkeypatch.setattr(tlc, "_device", lambda: 1)
     tlc.adamw_step(cfg, lst, 1)
     assert device_0.calls[-1][1][-1] == 1001
 

@@ -393,9 +393,9 @@ def device_info():
 # everything that is right, and the search for what is wrong only after it has failed.
 
 
-def _device() -> int:
-    """The current device. The kernels are launched there, so every tensor of a call has to be on it."""
-    return torch._C._cuda_getDevice()
+# The current device: the kernels are launched there, so every tensor of a call has to be on it.
+_device = getattr(torch._C, "_cuda_getDevice", None)
+_current_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 
 def _local(t: torch.Tensor, dtype, dev: int, name: str):
@@ -437,9 +437,7 @@ def _space(ws, dev: int):
 
 def _raw_stream(stream, dev: int):
     """Raw stream handle; the default is the current stream of device dev."""
-    if stream is None:
-        return torch._C._cuda_getCurrentRawStream(dev)
-    return _stream(stream)
+    return _current_stream(dev) if stream is None else _stream(stream)
 
 
 class _Marshalled:
@@ -650,13 +648,6 @@ class AdamWList:
             e.p_dtype, e.g_dtype = _DTYPES[p[i].dtype], _DTYPES[g[i].dtype]
             base += blocks * MOE_ADAMW_BLOCK
 
-    def here(self) -> int:
-        """The current device, on which the list's tensors have to be."""
-        dev = _device()
-        if self.count and self.device != dev:
-            raise ValueError(f"the list's tensors are on cuda:{self.device}, the call is for cuda:{dev}")
-        return dev
-
 
 class AdamWValues:
     """Where adamw_read_state writes: float32 tensors, one m and one v for each tensor of the list."""
@@ -674,12 +665,20 @@ class AdamWValues:
         self.keep = [list(m), list(v)]
 
 
+def _list_device(tensors: AdamWList) -> int:
+    """The current device, on which the list's tensors have to be."""
+    on = _device()
+    if tensors.device != on and tensors.count:
+        raise ValueError(f"the list's tensors are on cuda:{tensors.device}, the call is for cuda:{on}")
+    return on
+
+
 def adamw_step(cfg: AdamWConfig, tensors: AdamWList, step: int, grad_scale: Optional[torch.Tensor] = None,
                stream=None) -> None:
     """moe_adamw_step: one step (counted from 1) over every tensor; grad_scale: a float32 value on the GPU."""
     if cfg.bits != tensors.bits:
         raise ValueError(f"the list was made for {tensors.bits}-bit states")
-    on = tensors.here()
+    on = _list_device(tensors)
     c = _AdamWConfig.from_buffer_copy(cfg.ref()[1])  # its own: threads may step at once with one config
     c.step = step
     _check(lib().moe_adamw_step(ctypes.byref(c), tensors.c, tensors.count,
@@ -690,5 +689,5 @@ def adamw_read_state(cfg: AdamWConfig, tensors: AdamWList, out: AdamWValues, str
     """moe_adamw_read_state: the float32 values that the list's 8-bit states stand for."""
     if cfg.bits != 8 or tensors.bits != 8:
         raise ValueError("32-bit states are read as they are")
-    on = tensors.here()
+    on = _list_device(tensors)
     _check(lib().moe_adamw_read_state(tensors.c, tensors.count, out.m, out.v, _raw_stream(stream, on)))
