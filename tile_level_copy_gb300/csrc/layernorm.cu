@@ -22,6 +22,7 @@
 
 #include <cuda_fp16.h>
 
+#include <atomic>
 #include <type_traits>
 
 namespace moe {
@@ -29,6 +30,7 @@ namespace {
 
 constexpr int LN_FWD_THREADS = 256;
 constexpr int LN_BWD_THREADS = 256;  // a row above 2048 values takes up to 512
+constexpr int LN_BWD_MOST = 512;
 constexpr int LN_MAX_D = 16384;
 constexpr int LN_RED_COLS = 32;   // columns of a CTA of the reduction
 constexpr int LN_RED_ROWS = 32;   // partial sums it adds side by side
@@ -323,7 +325,7 @@ __host__ __device__ constexpr int bwd_rows(size_t size, int vec, int nv) {
 
 // R rows at a time, NV columns a thread.
 template <typename T, int VEC, int NV, int SLOTS>
-__global__ void __launch_bounds__(512, 1)
+__global__ void __launch_bounds__(LN_BWD_MOST, 1)
     ln_backward_kernel(LnShape s, const T* dy, const T* x, const void* w, bool wf32, const float* mean,
                        const float* rstd, T* dx, float* part) {
     typedef typename Lanes<VEC>::V V;
@@ -609,6 +611,21 @@ int64_t backward_ctas(const moe_layernorm_config& c, int vec, int sms) {
 }
 constexpr int LN_MAX_SMS = 256;
 
+// Once per device and kernel: it may take the most shared memory that a launch of it asks for. (What a kernel may
+// take is the process's: set to what one call needs, it could be too little for another thread's launch.)
+template <auto Kernel>
+cudaError_t ln_prepare(size_t most) {
+    static std::atomic<bool> done[64];
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+    if (done[dev].load(std::memory_order_relaxed)) return cudaSuccess;
+    e = cudaFuncSetAttribute(reinterpret_cast<const void*>(Kernel), cudaFuncAttributeMaxDynamicSharedMemorySize, (int)most);
+    if (e == cudaSuccess) done[dev].store(true, std::memory_order_relaxed);
+    return e;
+}
+
 }  // namespace
 }  // namespace moe
 
@@ -709,21 +726,26 @@ MOE_API int moe_layernorm_backward(const moe_layernorm_config* c, const void* dy
         typedef decltype(pk) P;
         typedef std::remove_reference_t<decltype(pk.v[0])> T;
         constexpr int V = (int)(sizeof(P) / sizeof(T));
-        auto go = [&](auto kernel, int stages) {
+        auto go = [&](auto columns, auto slots) {
+            constexpr int NV = decltype(columns)::value, SLOTS = decltype(slots)::value;
+            constexpr auto kernel = &ln_backward_kernel<T, V, NV, SLOTS>;
+            // bytes of the slots for each thread; 2-byte pieces have none
+            constexpr size_t each = sizeof(P) < 4 ? 0 : (size_t)SLOTS * 2 * bwd_rows(sizeof(T), V, NV) * (NV / V) * sizeof(P);
+            static_assert(each * LN_BWD_MOST <= 224 * 1024, "slots of the largest CTA");
             const int threads = 32 * s.warps * s.groups;
-            size_t smem = sizeof(P) < 4 ? 0 : (size_t)stages * 2 * bwd_rows(sizeof(T), V, values) * (values / V) * threads * sizeof(P);
+            size_t smem = each * threads;
             if (s.groups > 1 && smem < (size_t)2 * c->d * 4) smem = (size_t)2 * c->d * 4;
-            const cudaError_t e0 = cudaFuncSetAttribute(reinterpret_cast<const void*>(kernel),
-                                                        cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+            // (the partial sums of several groups are at most 8 KB: they share a CTA up to 1024 columns)
+            const cudaError_t e0 = ln_prepare<kernel>(each * LN_BWD_MOST > 8192 ? each * LN_BWD_MOST : 8192);
             if (e0 != cudaSuccess) return e0;
             return launch_k(kernel, dim3(ctas), dim3(threads), smem, st, true, s, static_cast<const T*>(dy),
                             static_cast<const T*>(x), w, wf32, mean, rstd, static_cast<T*>(dx), part);
         };
         // 96 KB of slots and two CTAs a SM up to 2048 columns, 192 KB for one CTA above
-        constexpr int WIDE = sizeof(T) == 4 ? 1 : 3;
-        const cudaError_t e1 = values == 8    ? go(ln_backward_kernel<T, V, 8, 3>, 3)
-                               : values == 16 ? go(ln_backward_kernel<T, V, 16, 3>, 3)
-                                              : go(ln_backward_kernel<T, V, 32, WIDE>, WIDE);
+        typedef Int<sizeof(T) == 4 ? 1 : 3> Wide;
+        const cudaError_t e1 = values == 8    ? go(Int<8>(), Int<3>())
+                               : values == 16 ? go(Int<16>(), Int<3>())
+                                              : go(Int<32>(), Wide());
         if (e1 != cudaSuccess || !part) return e1;
         return launch_k(ln_reduce_kernel<T>, dim3((c->d + LN_RED_COLS - 1) / LN_RED_COLS, 2),
                         dim3(LN_RED_COLS * LN_RED_ROWS), 0, st, true, (const float*)part, ctas, c->d, wf32, dw, db);
