@@ -393,7 +393,8 @@ def device_info():
 # everything that is right, and the search for what is wrong only after it has failed.
 
 
-# The current device: the kernels are launched there, so every tensor of a call has to be on it.
+# The current device: the kernels are launched there, so every tensor of a call has to be on it. The default
+# stream is the current one of that device (as a raw handle).
 _device = getattr(torch._C, "_cuda_getDevice", None)
 _current_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
@@ -433,11 +434,6 @@ def _space(ws, dev: int):
     if ws.buf.get_device() != dev:
         raise ValueError(f"the workspace is on {ws.buf.device}, the call is for cuda:{dev}")
     return ws.ptr
-
-
-def _raw_stream(stream, dev: int):
-    """Raw stream handle; the default is the current stream of device dev."""
-    return _current_stream(dev) if stream is None else _stream(stream)
 
 
 class _Marshalled:
@@ -512,7 +508,8 @@ def ffn_forward(cfg: FFNConfig, x: torch.Tensor, W1: torch.Tensor, W3: torch.Ten
     c, _, rows, up, down, need = cfg.ref()
     _check(lib().moe_ffn_forward(c, _dev(x, bf, rows, on, "x"), _dev(W1, bf, up, on, "W1"), _dev(W3, bf, up, on, "W3"),
                                  _dev(W2, bf, down, on, "W2"), _dev(y, bf, rows, on, "y"), _saved(saved, need, on),
-                                 _space(ws, on), ws.nbytes, _raw_stream(stream, on)))
+                                 _space(ws, on), ws.nbytes,
+                                 _current_stream(on) if stream is None else _stream(stream)))
 
 
 def ffn_backward(cfg: FFNConfig, x: torch.Tensor, W1: torch.Tensor, W3: torch.Tensor, W2: torch.Tensor,
@@ -525,7 +522,8 @@ def ffn_backward(cfg: FFNConfig, x: torch.Tensor, W1: torch.Tensor, W3: torch.Te
                                   _dev(W3, bf, up, on, "W3"), _dev(W2, bf, down, on, "W2"),
                                   _dev(dy, bf, rows, on, "dy"), _saved(saved, need, on), _dev(dx, bf, rows, on, "dx"),
                                   _dev(dW1, bf, up, on, "dW1"), _dev(dW3, bf, up, on, "dW3"),
-                                  _dev(dW2, bf, down, on, "dW2"), _space(ws, on), ws.nbytes, _raw_stream(stream, on)))
+                                  _dev(dW2, bf, down, on, "dW2"), _space(ws, on), ws.nbytes,
+                                  _current_stream(on) if stream is None else _stream(stream)))
 
 
 def ffn_status(cfg: FFNConfig, ws: FFNWorkspace, stream=None):
@@ -572,7 +570,7 @@ def layernorm_forward(cfg: LayerNormConfig, x: torch.Tensor, w: Optional[torch.T
     _check(lib().moe_layernorm_forward(
         cfg.ref()[0], _flat(x, dt, n, on, "x"), _flat(w, wt, d, on, "w"), _flat(b, wt, d, on, "b"),
         _flat(y, dt, n, on, "y"), _flat(mean, f32, rows, on, "mean"), _flat(rstd, f32, rows, on, "rstd"),
-        _raw_stream(stream, on)))
+        _current_stream(on) if stream is None else _stream(stream)))
 
 
 def layernorm_backward(cfg: LayerNormConfig, dy: torch.Tensor, x: torch.Tensor, w: Optional[torch.Tensor],
@@ -586,7 +584,7 @@ def layernorm_backward(cfg: LayerNormConfig, dy: torch.Tensor, x: torch.Tensor, 
         cfg.ref()[0], _flat(dy, dt, n, on, "dy"), _flat(x, dt, n, on, "x"), _flat(w, wt, d, on, "w"),
         _flat(mean, f32, rows, on, "mean"), _flat(rstd, f32, rows, on, "rstd"), _flat(dx, dt, n, on, "dx"),
         _flat(dw, wt, d, on, "dw"), _flat(db, wt, d, on, "db"), None if ws is None else _space(ws, on),
-        0 if ws is None else ws.nbytes, _raw_stream(stream, on)))
+        0 if ws is None else ws.nbytes, _current_stream(on) if stream is None else _stream(stream)))
 
 
 @dataclasses.dataclass
@@ -665,12 +663,10 @@ class AdamWValues:
         self.keep = [list(m), list(v)]
 
 
-def _list_device(tensors: AdamWList) -> int:
-    """The current device, on which the list's tensors have to be."""
-    on = _device()
-    if tensors.device != on and tensors.count:
+def _list_device(tensors: AdamWList, on: int) -> None:
+    """Refuses a list whose tensors are not on the current device."""
+    if tensors.count and tensors.device != on:
         raise ValueError(f"the list's tensors are on cuda:{tensors.device}, the call is for cuda:{on}")
-    return on
 
 
 def adamw_step(cfg: AdamWConfig, tensors: AdamWList, step: int, grad_scale: Optional[torch.Tensor] = None,
@@ -678,16 +674,21 @@ def adamw_step(cfg: AdamWConfig, tensors: AdamWList, step: int, grad_scale: Opti
     """moe_adamw_step: one step (counted from 1) over every tensor; grad_scale: a float32 value on the GPU."""
     if cfg.bits != tensors.bits:
         raise ValueError(f"the list was made for {tensors.bits}-bit states")
-    on = _list_device(tensors)
+    on = _device()
+    if tensors.device != on:
+        _list_device(tensors, on)
     c = _AdamWConfig.from_buffer_copy(cfg.ref()[1])  # its own: threads may step at once with one config
     c.step = step
     _check(lib().moe_adamw_step(ctypes.byref(c), tensors.c, tensors.count,
-                                _flat(grad_scale, torch.float32, 1, on, "grad_scale"), _raw_stream(stream, on)))
+                                None if grad_scale is None else _flat(grad_scale, torch.float32, 1, on, "grad_scale"),
+                                _current_stream(on) if stream is None else _stream(stream)))
 
 
 def adamw_read_state(cfg: AdamWConfig, tensors: AdamWList, out: AdamWValues, stream=None) -> None:
     """moe_adamw_read_state: the float32 values that the list's 8-bit states stand for."""
     if cfg.bits != 8 or tensors.bits != 8:
         raise ValueError("32-bit states are read as they are")
-    on = _list_device(tensors)
-    _check(lib().moe_adamw_read_state(tensors.c, tensors.count, out.m, out.v, _raw_stream(stream, on)))
+    on = _device()
+    _list_device(tensors, on)
+    _check(lib().moe_adamw_read_state(tensors.c, tensors.count, out.m, out.v,
+                                      _current_stream(on) if stream is None else _stream(stream)))
