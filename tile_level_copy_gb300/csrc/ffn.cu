@@ -1113,8 +1113,8 @@ cudaError_t ff_clusters(int* out) {
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
     if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
-    static int cache[64] = {0};
-    if (cache[dev] == 0) {
+    static std::atomic<int> cache[64];
+    if ((*out = cache[dev].load(std::memory_order_relaxed)) == 0) {
         e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, FF_SMEM);
         if (e != cudaSuccess) return e;
         cudaLaunchConfig_t q = {};
@@ -1125,9 +1125,9 @@ cudaError_t ff_clusters(int* out) {
         e = cudaOccupancyMaxActiveClusters(&n, fn, &q);
         if (e != cudaSuccess) return e;
         if (n < 1) return cudaErrorInvalidConfiguration;
-        cache[dev] = n;
+        cache[dev].store(n, std::memory_order_relaxed);
+        *out = n;
     }
-    *out = cache[dev];
     return cudaSuccess;
 }
 
