@@ -420,7 +420,8 @@ MOE_API int moe_route_static(const moe_config* cfg, const float* logits, int32_t
  * A dense gated feed-forward block (forward, backward and its form for few tokens), layer norm
  * (forward, backward) and the AdamW step. Same rules as above: the caller owns every buffer and the
  * stream, all of them of the calling thread's current device, nothing is allocated or synchronised
- * (moe_ffn_status synchronises), an argument error is returned before any launch. The tile-level pages have no counterpart of these operators.
+ * (moe_ffn_status synchronises), an argument error is returned before any launch. The tile-level pages have
+ * no counterpart of these operators.
  */
 
 /* Types of values. */
@@ -452,10 +453,12 @@ MOE_API int moe_ffn_saved_size(const moe_ffn_config* cfg, size_t* bytes);
  *   saved  device buffer of moe_ffn_saved_size bytes for a later moe_ffn_backward, or NULL
  *   ws     device workspace of ws_bytes >= moe_ffn_workspace_size(cfg)
  * saved and ws are 256-byte aligned; the first MOE_FFN_STATUS_BYTES of ws are zeroed by the caller once,
- * before its first call, and again after a MOE_ERR_TIMEOUT (status words and counts that are zero between calls). h is rounded to bf16 once, as the operand of the second
- * product; everything else stays fp32 until y is rounded. With saved NULL and few tokens the weights
- * are streamed once by kernels made for that (the form of single-token decoding); the sums then
- * run in another order, so y may differ in its last bit from the call with saved.
+ * before its first call (complete, or ordered before it on its stream), and again after a MOE_ERR_TIMEOUT
+ * (status words and counts that are zero between calls). Calls on one ws follow one another: on one stream, or
+ * ordered by the caller. h is rounded to bf16 once, as the operand of the second product; everything else stays
+ * fp32 until y is rounded. With saved NULL and few tokens the weights are streamed once by kernels made for that
+ * (the form of single-token decoding); the sums then run in another order, so y may differ in its last bit
+ * from the call with saved.
  */
 MOE_API int moe_ffn_forward(const moe_ffn_config* cfg, const uint16_t* x, const uint16_t* W1, const uint16_t* W3,
                             const uint16_t* W2, uint16_t* y, void* saved, void* ws, size_t ws_bytes, void* stream);

@@ -74,3 +74,14 @@ def test_layernorm_backward_of_two_widths_in_a_graph():
     torch.cuda.synchronize()
     for t, want in zip((*a, *b), alone):
         assert torch.equal(t, want)
+
+
+def test_a_new_ffn_workspace_is_ready_on_every_stream():
+    """The workspace's status words and counts have to be zero before a call on any stream reads them: nothing
+    of their clearing is left on the stream that was current when the workspace was made."""
+    cfg = tlc.FFNConfig(4, 128, 256)
+    torch.cuda.synchronize()
+    torch.cuda._sleep(20_000_000)  # about 10 ms on the current stream
+    ws = tlc.FFNWorkspace(cfg)
+    assert torch.cuda.current_stream().query()
+    assert not ws.buf[:tlc.MOE_FFN_STATUS_BYTES].any()

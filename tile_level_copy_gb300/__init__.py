@@ -476,7 +476,8 @@ class FFNConfig(_Marshalled):
 
 
 class FFNWorkspace:
-    """Device workspace of one feed-forward config; its status words start as zero."""
+    """Device workspace of one feed-forward config; its status words start as zero, and are so for calls on
+    any stream (the constructor waits for their clearing, unless the current stream is being captured)."""
 
     def __init__(self, cfg: FFNConfig, device="cuda"):
         n, c = ctypes.c_size_t(), cfg.to_c()
@@ -484,6 +485,8 @@ class FFNWorkspace:
         self.nbytes = n.value
         self.buf = torch.empty(self.nbytes, dtype=torch.uint8, device=device)
         self.buf[:MOE_FFN_STATUS_BYTES].zero_()
+        if self.buf.is_cuda and not torch.cuda.is_current_stream_capturing():
+            torch.cuda.current_stream(self.buf.device).synchronize()
         self.ptr = self.buf.data_ptr()
 
 
