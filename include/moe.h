@@ -452,6 +452,7 @@ MOE_API int moe_ffn_saved_size(const moe_ffn_config* cfg, size_t* bytes);
  * moe_ffn_forward: x, W1, W3, W2, y device bf16 as above, 16-byte aligned and contiguous.
  *   saved  device buffer of moe_ffn_saved_size bytes for a later moe_ffn_backward, or NULL
  *   ws     device workspace of ws_bytes >= moe_ffn_workspace_size(cfg)
+ * y may be x; it may not share memory with W2 or saved (MOE_ERR_ARG), nor with ws.
  * saved and ws are 256-byte aligned; the first MOE_FFN_STATUS_BYTES of ws are zeroed by the caller once,
  * before its first call (complete, or ordered before it on its stream), and again after a MOE_ERR_TIMEOUT
  * (status words and counts that are zero between calls). Calls on one ws follow one another: on one stream, or
@@ -466,7 +467,8 @@ MOE_API int moe_ffn_forward(const moe_ffn_config* cfg, const uint16_t* x, const 
 /*
  * moe_ffn_backward: gradients of a loss whose gradient at y is dy (device bf16 [T, d]), given the
  * forward pass's inputs and its saved buffer (read only: more than one backward pass may use it).
- *   dx device bf16 [T, d]; dW1, dW3 [ffn, d]; dW2 [d, ffn] (all overwritten; 16-byte aligned)
+ *   dx device bf16 [T, d]; dW1, dW3 [ffn, d]; dW2 [d, ffn] (all overwritten; 16-byte aligned); none may share
+ *   memory with an input or with another of them (MOE_ERR_ARG; dx is written while dy is still read), nor with ws
  * With T = 0 the weight gradients are set to zero.
  */
 MOE_API int moe_ffn_backward(const moe_ffn_config* cfg, const uint16_t* x, const uint16_t* W1, const uint16_t* W3,

@@ -6,6 +6,8 @@ import pytest
 import torch
 
 import tile_level_copy_gb300 as tlc
+from oracle import block_ref as ref
+from tests.test_gpu_ffn import close, f64, forward, make
 
 pytestmark = pytest.mark.gpu
 F32, BF = torch.float32, torch.bfloat16
@@ -85,3 +87,37 @@ def test_a_new_ffn_workspace_is_ready_on_every_stream():
     ws = tlc.FFNWorkspace(cfg)
     assert torch.cuda.current_stream().query()
     assert not ws.buf[:tlc.MOE_FFN_STATUS_BYTES].any()
+
+
+@pytest.mark.parametrize("T", [5, 700])
+def test_backward_outputs_over_inputs_are_refused(T):
+    """dx is written while dy is still read for the weight gradients (and the weights and x beside it): an
+    output that shares memory with an input or with another output is refused."""
+    d, f = 264, 264  # so that every matrix has the shape of every other
+    cfg = tlc.FFNConfig(T, d, f)
+    x, W1, W3, W2, dy = make(T, d, f)
+    _, saved, ws = forward(cfg, x, W1, W3, W2, True)
+    outs = [torch.empty_like(t) for t in (x, W1, W3, W2)]
+    for i, others in ((0, (dy, x)), (1, (W1, W3, W2, outs[2], outs[3])), (2, (W1, W2, outs[3])), (3, (W3,))):
+        for o in others:
+            bad = list(outs)
+            bad[i] = o
+            with pytest.raises(tlc.MoEError) as e:
+                tlc.ffn_backward(cfg, x, W1, W3, W2, dy, saved, *bad, ws)
+            assert e.value.code == tlc.MOE_ERR_ARG
+    tlc.ffn_backward(cfg, x, W1, W3, W2, dy, saved, *outs, ws)
+    for got, want in zip(outs, ref.ffn_backward(*(f64(t) for t in (x, W1, W3, W2, dy)))):
+        close(got, want)
+
+
+def test_forward_in_place_and_over_its_inputs():
+    """y may be x, which the second product no longer needs; over W2, which it reads, it is refused."""
+    T, d, f = 264, 264, 264
+    cfg = tlc.FFNConfig(T, d, f)
+    x, W1, W3, W2, _ = make(T, d, f)
+    y, saved, ws = forward(cfg, x, W1, W3, W2, True)
+    with pytest.raises(tlc.MoEError) as e:
+        tlc.ffn_forward(cfg, x, W1, W3, W2, W2, ws)
+    assert e.value.code == tlc.MOE_ERR_ARG
+    tlc.ffn_forward(cfg, x, W1, W3, W2, x, ws, saved=saved)
+    assert torch.equal(x, y)

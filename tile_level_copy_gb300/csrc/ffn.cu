@@ -1357,6 +1357,28 @@ const FfPlans& ff_plans(const FfLayout& L, int sms) {
     return p;
 }
 
+// A call's tensors: the address range of each, by name.
+struct FfRange {
+    const char* name;
+    const void* ptr;
+    size_t bytes;
+};
+// Refuses an output that shares memory with an input, or with an output after it in the list.
+template <int NO, int NI>
+int ff_apart(const FfRange (&outs)[NO], const FfRange (&ins)[NI]) {
+    auto meet = [](const FfRange& a, const FfRange& b) {
+        const uintptr_t p = reinterpret_cast<uintptr_t>(a.ptr), q = reinterpret_cast<uintptr_t>(b.ptr);
+        return p < q + b.bytes && q < p + a.bytes;
+    };
+    for (int i = 0; i < NO; ++i) {
+        for (const FfRange& r : ins)
+            if (meet(outs[i], r)) return fail(MOE_ERR_ARG, "%s overlaps %s", outs[i].name, r.name);
+        for (int k = i + 1; k < NO; ++k)
+            if (meet(outs[i], outs[k])) return fail(MOE_ERR_ARG, "%s overlaps %s", outs[i].name, outs[k].name);
+    }
+    return MOE_OK;
+}
+
 int ff_begin(const moe_ffn_config* c, void* ws, size_t ws_bytes, FfLayout* L, int* sms) {
     clear_error();
     int rc = ff_layout(c, L);
@@ -1407,6 +1429,9 @@ MOE_API int moe_ffn_forward(const moe_ffn_config* c, const uint16_t* x, const ui
     if (!aligned(x, 16) || !aligned(W1, 16) || !aligned(W3, 16) || !aligned(W2, 16) || !aligned(y, 16))
         return fail(MOE_ERR_ARG, "x, W1, W3, W2, y must be 16-byte aligned");
     if (!aligned(saved, 256)) return fail(MOE_ERR_ARG, "saved must be 256-byte aligned");
+    const size_t tokens = L.T * L.d * 2, matrix = L.F * L.d * 2;
+    const FfRange outs[] = {{"y", y, tokens}}, ins[] = {{"W2", W2, matrix}, {"saved", saved, saved ? L.saved_bytes : 0}};
+    if ((rc = ff_apart(outs, ins))) return rc;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     uint8_t* s = static_cast<uint8_t*>(saved);
     uint8_t* h = s ? s + L.saved_h : static_cast<uint8_t*>(ws) + L.h;
@@ -1462,6 +1487,12 @@ MOE_API int moe_ffn_backward(const moe_ffn_config* c, const uint16_t* x, const u
         !aligned(dx, 16))
         return fail(MOE_ERR_ARG, "x, W1, W3, W2, dy, dx must be 16-byte aligned");
     if (!aligned(saved, 256)) return fail(MOE_ERR_ARG, "saved must be 256-byte aligned");
+    // dx is written beside the weight gradients, which read dy, x and saved, and beside the reads of W1 and W3
+    const size_t tokens = L.T * L.d * 2, matrix = L.F * L.d * 2;
+    const FfRange outs[] = {{"dx", dx, tokens}, {"dW1", dW1, matrix}, {"dW3", dW3, matrix}, {"dW2", dW2, matrix}};
+    const FfRange ins[] = {{"x", x, tokens},   {"W1", W1, matrix},  {"W3", W3, matrix},
+                           {"W2", W2, matrix}, {"dy", dy, tokens}, {"saved", saved, L.saved_bytes}};
+    if ((rc = ff_apart(outs, ins))) return rc;
     const uint8_t* s = static_cast<const uint8_t*>(saved);
     const uint8_t* h = s + L.saved_h;
     uint8_t* dg = static_cast<uint8_t*>(ws) + L.dg;
