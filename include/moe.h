@@ -433,13 +433,19 @@ MOE_API int moe_route_static(const moe_config* cfg, const float* logits, int32_t
  * Gated feed-forward block, bf16 operands, fp32 accumulation:
  *   y = h W2^T, h = silu(x W1^T) * (x W3^T); x, y [T, d]; W1, W3 [ffn, d]; W2 [d, ffn].
  * Limits: T >= 0, d and ffn positive multiples of 8 below 2^20, T < 2^24. reserved must be zero.
- * timeout_us bounds every device-side wait (0 = 2,000,000 us).
+ * timeout_us bounds every device-side wait (0 = 2,000,000 us). flags: 0, or the test hooks below.
  */
 typedef struct moe_ffn_config {
     int32_t T, d, ffn;
     uint32_t timeout_us;
-    int32_t reserved[4];
+    uint32_t flags;
+    int32_t reserved[3];
 } moe_ffn_config;
+
+#define MOE_FFN_TEST_STALL0 0x1u /* test hooks: in the CTA-pair products the TMA thread of rank 0 (STALL0) or rank 1 */
+#define MOE_FFN_TEST_STALL1 0x2u /* (STALL1) of every pair stops issuing loads halfway through its first tile, in    */
+                                 /* the products for few tokens that of every CTA (STALL0), so the bounded waits run */
+                                 /* out (MOE_ERR_TIMEOUT) and the abort path settles the loads still in flight       */
 
 #define MOE_FFN_STATUS_BYTES 8192
 

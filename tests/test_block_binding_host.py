@@ -1,5 +1,6 @@
 """Host-only checks of the block operators' binding: what it hands to the library, and what it refuses."""
 import copy
+import ctypes
 import dataclasses
 import gc
 import pickle
@@ -211,3 +212,11 @@ def test_a_list_keeps_its_tensors_whatever_becomes_of_the_callers(device_0):
     del lst, values
     gc.collect()
     assert all(r() is None for r in alive)
+
+
+def test_unknown_ffn_flags_are_refused(built_library):
+    n = ctypes.c_size_t()
+    for flags, rc in ((0, tlc.MOE_OK), (tlc.MOE_FFN_TEST_STALL0 | tlc.MOE_FFN_TEST_STALL1, tlc.MOE_OK), (4, tlc.MOE_ERR_ARG),
+                      (1 << 31, tlc.MOE_ERR_ARG)):
+        c = tlc.FFNConfig(4, 128, 256, flags=flags).to_c()
+        assert built_library.moe_ffn_workspace_size(ctypes.byref(c), ctypes.byref(n)) == rc

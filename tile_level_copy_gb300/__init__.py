@@ -47,6 +47,7 @@ TRACE_UP_CYCLES, TRACE_UP_NS, TRACE_DOWN_CYCLES, TRACE_DOWN_NS = 8, 9, 10, 11
 MOE_DTYPE_F32, MOE_DTYPE_BF16, MOE_DTYPE_F16 = 0, 1, 2
 MOE_ADAMW_BLOCK = 128
 MOE_FFN_STATUS_BYTES = 8192
+MOE_FFN_TEST_STALL0, MOE_FFN_TEST_STALL1 = 0x1, 0x2
 _DTYPES = {torch.float32: MOE_DTYPE_F32, torch.bfloat16: MOE_DTYPE_BF16, torch.float16: MOE_DTYPE_F16}
 
 # names of the C entry points (each declared in include/moe.h)
@@ -115,7 +116,7 @@ class Config:
 
 class _FFNConfig(ctypes.Structure):
     _fields_ = [(n, ctypes.c_int32) for n in ("T", "d", "ffn")] + [
-        ("timeout_us", ctypes.c_uint32), ("reserved", ctypes.c_int32 * 4)]
+        ("timeout_us", ctypes.c_uint32), ("flags", ctypes.c_uint32), ("reserved", ctypes.c_int32 * 3)]
 
 
 class _LayerNormConfig(ctypes.Structure):
@@ -465,9 +466,10 @@ class FFNConfig(_Marshalled):
     d: int
     ffn: int
     timeout_us: int = 0
+    flags: int = 0
 
     def to_c(self) -> _FFNConfig:
-        return _FFNConfig(int(self.T), int(self.d), int(self.ffn), int(self.timeout_us))
+        return _FFNConfig(int(self.T), int(self.d), int(self.ffn), int(self.timeout_us), int(self.flags))
 
     def _make(self):
         c, n = self.to_c(), ctypes.c_size_t()

@@ -82,6 +82,7 @@ struct FfLaunch {
     // before it when they let this one begin: this launch starts beside it, and waits for it at its
     // end only, so that what follows this launch follows both.
     int beside;
+    uint32_t stall;    // test hook, one bit for each rank: stop loading in the middle of the first tile
 };
 
 struct FfSmem {
@@ -566,8 +567,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(FF_THREADS, 1)
     if (warp == 0 && lane == 0) {
         FfRing ring;
         bool ok = !bad;
+        const bool stall = l.stall >> rank & 1u;
         for (int i = 0, u; ok && (u = ff_unit(l, cluster, clusters, i)) >= 0; ++i) {
-            const FfTile tr = ff_tile(l, u);
+            FfTile tr = ff_tile(l, u);
+            if (stall) tr.k1 = tr.k0 + (tr.k1 - tr.k0) / 2;
             const int arow = tr.m * FT_M + (int)rank * 128;
             const int brow = MODE == FF_SWIGLU ? tr.n * 128 : tr.n * FT_N + (int)rank * 128;
             auto load = [&](auto form) {
@@ -581,6 +584,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(FF_THREADS, 1)
                 }
             };
             ff_forms<MODE>(tr.a_mn | tr.b_mn << 1, load);
+            if (stall) break;
         }
         nk = ring.done;
         if (!ok) {
@@ -687,6 +691,7 @@ struct FxArgs {
     int kb0, kb;          // k-blocks of operand pair 0, of both (FF_SWIGLU: a[0] and a[1] side by side)
     int nt, splits, tiles_t;
     int stages, early;
+    uint32_t stall;       // test hook: stop loading halfway
     __nv_bfloat16 *out0, *out1;  // [T][M]
     float2* gu;                  // kept g and u, [T][M]
     int32_t* status;
@@ -808,7 +813,8 @@ __global__ void __launch_bounds__(GEMM_THREADS, 1) flex_kernel(const __grid_cons
                 const int second = pair_of(kb), k = (kb - (second ? p.kb0 : 0)) * BK;
                 tma_load_2d(ring + st * stage_bytes + (DUAL ? 2 : 1) * FX_A, &p.b[second], &full[st], k, t0);
             };
-            const int head = nkb < p.stages ? nkb : p.stages;
+            const int loads = p.stall ? nkb / 2 : nkb;
+            const int head = loads < p.stages ? loads : p.stages;
             if (p.early)
                 for (int i = 0; i < head; ++i) weights(k0 + i, i);
             griddep_wait();
@@ -819,7 +825,7 @@ __global__ void __launch_bounds__(GEMM_THREADS, 1) flex_kernel(const __grid_cons
                 if (!p.early) weights(k0 + issued, issued);
                 tokens(k0 + issued, issued);
             }
-            for (; issued < nkb; ++issued) {  // stage st is free once its products of round ph are done
+            for (; issued < loads; ++issued) {  // stage st is free once its products of round ph are done
                 if (!mbar_wait(&empty[st], ph, tmo, &abort_word)) {
                     ok = false;
                     break;
@@ -978,6 +984,7 @@ struct FfLayout {
     size_t saved_h, saved_gu, saved_bytes;
     int gu_cols;
     unsigned long long timeout_ns;
+    uint32_t flags;
 };
 
 int ff_layout(const moe_ffn_config* c, FfLayout* o) {
@@ -987,7 +994,8 @@ int ff_layout(const moe_ffn_config* c, FfLayout* o) {
         return fail(MOE_ERR_ARG, "d=%d must be a positive multiple of 8 below 2^20", c->d);
     if (c->ffn <= 0 || c->ffn % 8 || c->ffn >= (1 << 20))
         return fail(MOE_ERR_ARG, "ffn=%d must be a positive multiple of 8 below 2^20", c->ffn);
-    for (int i = 0; i < 4; ++i)
+    if (c->flags & ~(MOE_FFN_TEST_STALL0 | MOE_FFN_TEST_STALL1)) return fail(MOE_ERR_ARG, "flags=%#x is not known", c->flags);
+    for (int i = 0; i < 3; ++i)
         if (c->reserved[i]) return fail(MOE_ERR_ARG, "reserved fields must be zero");
     FfLayout L;
     L.T = c->T;
@@ -1006,6 +1014,7 @@ int ff_layout(const moe_ffn_config* c, FfLayout* o) {
     L.saved_h = 0;
     L.saved_gu = hidden;
     L.saved_bytes = hidden + (L.T + 31) / 32 * L.gu_cols * 8192;  // at least T F pairs, the flex layout
+    L.flags = c->flags;
     L.timeout_ns = (unsigned long long)(c->timeout_us ? c->timeout_us : 2000000u) * 1000ull;
     *o = L;
     return MOE_OK;
@@ -1164,6 +1173,7 @@ int ff_run(FfList& list, const FfLayout& L, void* ws, cudaStream_t st, const cha
     FfLaunch& l = list.l;
     l.status = static_cast<int32_t*>(ws);
     l.timeout_ns = L.timeout_ns;
+    l.stall = L.flags;  // the flags' bits are the ranks'
     l.partial = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + L.partial);
     l.arrived = static_cast<uint32_t*>(ws) + FF_ARRIVED;
     int clusters = 0;
@@ -1248,6 +1258,7 @@ int fx_run(FxArgs& p, const FxPlan& plan, const FfLayout& L, void* ws, cudaStrea
     p.tiles_t = (p.T + p.nt - 1) / p.nt;
     p.status = static_cast<int32_t*>(ws);
     p.timeout_ns = L.timeout_ns;
+    p.stall = L.flags & MOE_FFN_TEST_STALL0;
     const size_t smem = (size_t)p.stages * fx_stage_bytes(MODE == FF_SWIGLU, p.nt) + 1024;
     cudaError_t e = fx_prepare<MODE, A_MN>();
     if (e != cudaSuccess) return cuda_fail(e, what);
