@@ -525,6 +525,9 @@ MOE_API int moe_layernorm_backward(const moe_layernorm_config* cfg, const void* 
  * updated from m and v before they are rounded. The rounding is stochastic (unbiased), so an average
  * that moves by less than a rounding step a call still moves: up or down is decided by 16 bits of a
  * hash of (seed, step, rng_base + i) for value i, so the result repeats for the same arguments.
+ * The config's numbers, step among them, are arguments of the launch: a call captured into a graph is the same step
+ * at every replay, with its bias correction and its random bits. A training loop that replays graphs makes this call
+ * outside of them, or captures it again for each step.
  */
 #define MOE_ADAMW_BLOCK 128
 typedef struct moe_adamw_config {

@@ -7,6 +7,7 @@ import torch
 
 import tile_level_copy_gb300 as tlc
 from oracle import block_ref as ref
+from tests.test_gpu_adamw import HYPER, tensors
 from tests.test_gpu_ffn import close, f64, forward, make
 
 pytestmark = pytest.mark.gpu
@@ -121,3 +122,42 @@ def test_forward_in_place_and_over_its_inputs():
     assert e.value.code == tlc.MOE_ERR_ARG
     tlc.ffn_forward(cfg, x, W1, W3, W2, x, ws, saved=saved)
     assert torch.equal(x, y)
+
+
+@pytest.mark.parametrize("bits", [32, 8])
+def test_a_captured_step_is_the_same_step_at_every_replay(bits):
+    """The step is an argument of the launch: three replays give what three calls with its number give, bias
+    correction and random bits among it, and not what steps that count on give."""
+    def state():
+        p, g, m, v, ms, vs = tensors([5000, 77], F32, BF, bits, 4)
+        cfg = tlc.AdamWConfig(**HYPER, bits=bits, seed=11)
+        return cfg, tlc.AdamWList(cfg, p, g, m, v, ms, vs), (*p, *m, *v, *(ms or []), *(vs or []))
+
+    (cfg, lst, a), (_, calls, b), (_, counted, c) = state(), state(), state()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        tlc.adamw_step(cfg, lst, 2)
+    for i in range(3):
+        graph.replay()
+        tlc.adamw_step(cfg, calls, 2)
+        tlc.adamw_step(cfg, counted, 2 + i)
+    assert all(torch.equal(x, y) for x, y in zip(a, b))
+    assert not torch.equal(a[0], c[0])
+
+
+@pytest.mark.parametrize("bits", [32, 8])
+@pytest.mark.parametrize("eps", [1e-8, 1e-12])
+@pytest.mark.parametrize("pt,gt", [(F32, F32), (F32, BF), (BF, BF)])
+def test_a_step_does_not_depend_on_place_or_alignment(pt, gt, eps, bits):
+    """Whole aligned chunks take a path of their own: p, copy and states have the same bits as those of the
+    same values off an aligned start, and in a tensor's last chunk."""
+    n = 3 * 4096 + 77
+    out = []
+    for shift in (0, 1):
+        p, g, m, v, ms, vs = tensors([n], pt, gt, bits, 5, shift)
+        c = [torch.zeros(n + shift, dtype=BF, device="cuda")[shift:]]
+        cfg = tlc.AdamWConfig(**{**HYPER, "eps": eps}, bits=bits, seed=3)
+        tlc.adamw_step(cfg, tlc.AdamWList(cfg, p, g, m, v, ms, vs, copy=c), 5)
+        out.append((p[0], c[0], m[0], v[0]))
+    for a, b in zip(*out):
+        assert torch.equal(a, b)

@@ -676,7 +676,8 @@ def _list_device(tensors: AdamWList, on: int) -> None:
 
 def adamw_step(cfg: AdamWConfig, tensors: AdamWList, step: int, grad_scale: Optional[torch.Tensor] = None,
                stream=None) -> None:
-    """moe_adamw_step: one step (counted from 1) over every tensor; grad_scale: a float32 value on the GPU."""
+    """moe_adamw_step: one step (counted from 1) over every tensor; grad_scale: a float32 value on the GPU.
+    Captured into a graph, it is the same step, with the same random bits, at every replay."""
     if cfg.bits != tensors.bits:
         raise ValueError(f"the list was made for {tensors.bits}-bit states")
     on = _device()

@@ -7,7 +7,7 @@
 // Every value is read and written once, so the bound is HBM traffic: 28 bytes a value with fp32
 // states, bf16 gradients and a bf16 copy, 16 with 8-bit states. The list travels in the launch's
 // parameters (no table in device memory to keep in step with the caller's pointers, nothing to copy
-// before the launch, and a captured graph holds it).
+// before the launch). So do the step's numbers: a captured launch is the same step at every replay.
 // Measured with 24 tensors, 149 million values, bf16 gradients and copies: fp32 states 623 us, 6.7 TB/s
 // (98 % of a copy's rate); 8-bit states 467 us, 5.1 TB/s, bound by the 73 instructions a value that
 // decoding, the roots and the random roundings take; reading 8-bit states back 250 us, 6.0 TB/s.
