@@ -9,8 +9,9 @@
 // parameters (no table in device memory to keep in step with the caller's pointers, nothing to copy
 // before the launch). So do the step's numbers: a captured launch is the same step at every replay.
 // Measured with 24 tensors, 149 million values, bf16 gradients and copies: fp32 states 623 us, 6.7 TB/s
-// (98 % of a copy's rate); 8-bit states 467 us, 5.1 TB/s, bound by the 73 instructions a value that
-// decoding, the roots and the random roundings take; reading 8-bit states back 250 us, 6.0 TB/s.
+// (98 % of a copy's rate); 8-bit states 467 us, 5.1 TB/s: decoding, the roots and the random roundings take 73
+// instructions a value, which fill 59 % of the issue slots (270 us), in long chains, and a thread loads four fours
+// and works through them with no load in flight; reading 8-bit states back 250 us, 6.0 TB/s.
 //
 // 8-bit states. A block of 128 consecutive values has one power-of-two scale for m and one for v, so
 // scaling is exact and costs no precision; within a block m keeps 4 exponent bits and 3 mantissa
@@ -262,7 +263,7 @@ __device__ __forceinline__ void chunk_step(const AwTensor& t, uint32_t flags, co
 // ---- whole chunks of aligned tensors ----------------------------------------------------------------
 // The same arithmetic two values at a time (f32x2, each operation rounded to nearest, none contracted),
 // with the 8-bit form's bit work cut down: with it unvectorised the step took 101 instructions a value and
-// was bound by them (647 us for 149 M values against 350 us of memory traffic).
+// 647 us for 149 M values (350 us of memory traffic).
 typedef unsigned long long f2;
 __device__ __forceinline__ f2 pair2(float lo, float hi) {
     f2 r;

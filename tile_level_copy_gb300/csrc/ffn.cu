@@ -23,9 +23,10 @@
 //   forward, 37 tokens (4096, 14336)        66 us, 5.3 TB/s (78 %)
 //   forward, 1 token (2048, 1408)           10 us, two launches of 3.5 to 5 us
 //   both passes, 8192 tokens (2048, 5632)   1142 us, 1.49 PF (79 %; 87 % of the sustained rate)
-// g and u are kept in fp32: rounding them would round dg and du twice, and computing them
-// again costs 4 T d ffn flops where keeping them costs 16 T ffn bytes of traffic (at d = 2048 and the
-// measured rates a quarter of that time, and hidden behind the products).
+// g and u are kept in fp32: rounding them would round dg and du twice, and computing them again costs 4 T d ffn
+// flops where keeping them costs 16 T ffn bytes of traffic. At d = 2048 and the measured rates that is 199 us
+// against 109 us (8192 tokens, ffn 5632). The traffic is not hidden: launches 1 and 3 then keep the tensor pipes
+// 72 % and 54 % busy, where launch 4 reaches 88 %, which is about 105 us of the pass.
 // h, dg and du are rounded to bf16 because they are operands of the next product.
 #include <atomic>
 
@@ -209,8 +210,9 @@ __device__ __forceinline__ bool ff_multiply(const FfSmem& sm, FfRing& r, uint32_
 }
 
 // Arrive on a barrier of the pair without ordering this thread's memory operations: the epilogue's signal
-// that it has read the accumulator (its tcgen05 loads are complete); a releasing arrive would wait for
-// the stores in flight.
+// that it has read the accumulator. Its tcgen05 loads have completed (wait::ld) and
+// tcgen05.fence::before_thread_sync orders them before the arrive, as fence::after_thread_sync orders the UMMAs
+// after the wait for it; a releasing arrive would wait for the stores in flight as well.
 __device__ __forceinline__ void ff_arrive_relaxed(uint32_t cluster_addr) {
     asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
 }
@@ -1077,9 +1079,9 @@ struct FfList {
 // Kinds of products, by their epilogue: plain; h; h with g and u kept; the hidden gradients.
 enum FfKind : int { FK_PLAIN = 0, FK_H = 1, FK_H_KEPT = 2, FK_ACT = 3 };
 
-// Times in microseconds that the choices below go by, fitted to 15,400 measured launches (products of
-// 360 to 14336 features, 1 to 4096 tokens and 216 to 14336 k, of every kind, every plan of each; the
-// plan that these numbers choose took 1.03 times the best one's time on average, 1.47 times at worst).
+// Times in microseconds that the choices below go by, fitted to 15,400 measured launches: 1017 products of 360 to
+// 14336 features, 1 to 4096 tokens and 216 to 14336 k, of every kind, with up to 29 plans each. The plan that these
+// numbers choose took 1.03 times the time of the best one measured on average, 1.47 times at worst.
 constexpr float US_HBM = 6.3e6f;                            // bytes a microsecond from memory
 constexpr float US_DENSE = 4.9f, US_DENSE_KB = 0.287f;      // a launch; a k-block of a 256 x 256 tile
 constexpr float US_DENSE_WAVE = 1.9f;                       // a wave beside its k-blocks or epilogue

@@ -4,19 +4,23 @@
 //   backward  xh = (x - mean) rstd, gy = dy w
 //             dx = rstd (gy - sum(gy) / d - xh sum(gy xh) / d), dw = sum_rows dy xh, db = sum_rows dy
 //
-// The forward pass reads x and writes y, the backward pass reads x and dy and writes dx: both are
-// bound by HBM as long as enough loads are in flight and the arithmetic (about a dozen operations a
-// value; sums and products two at a time, f32x2) stays below it.
+// The forward pass reads x and writes y, the backward pass reads x and dy and writes dx: HBM would bound both if
+// enough loads were in flight all the time. They wait instead; see the figures below. Sums and products go two at a
+// time (f32x2).
 //
 // Forward: a row lies in the registers of as many warps as hold it with 32 values a thread, so the
 // variance is the mean of squared differences without a second read, and all of a row's loads are in
-// flight at once. Weights come from L1. 16384 x 4096 bf16 take 59 us, 4.5 TB/s; what bounds it is the
-// instructions (17 a value), not the memory (40 us).
+// flight at once. Weights come from L1. 16384 x 4096 bf16 take 59 us, 4.5 TB/s, where the memory needs 40 us and
+// the instructions (21 a value) fill 64 % of the issue slots. What is left are waits: a warp loads its row, waits for
+// it (3.4 of the 11.3 cycles between two instructions), reduces twice and stores, with no load of its next row
+// under way.
 // Backward: a thread keeps the same columns over all its rows, with their partial sums of dw and db
 // in registers, and takes several rows at a time (32 values in all) so that one reduction and one
 // barrier serve all of them; the rows come through shared memory by cp.async, two batches ahead. The
-// CTAs' partial sums are added up in CTA order by a second launch. 16384 x 2048 bf16 take 49 us, 4.1 TB/s,
-// bound like the forward pass (20 instructions a value; memory 30 us).
+// CTAs' partial sums are added up in CTA order by a second launch. 16384 x 2048 bf16 take 49 us, 4.1 TB/s, where
+// the memory needs 30 us and the instructions (21 a value) fill 45 % of the issue slots: 128 registers a thread
+// leave 15 warps a SM, and of the 8.4 cycles between two instructions of one it waits 2.6 for loads and
+// 1.2 at the barrier that a batch of rows has. The second launch is 7 us of it under the profiler.
 #include "host_internal.h"
 #include "moe_internal.cuh"
 
