@@ -504,7 +504,7 @@ typedef struct moe_layernorm_config {
 MOE_API int moe_layernorm_forward(const moe_layernorm_config* cfg, const void* x, const void* w, const void* b,
                                   void* y, float* mean, float* rstd, void* stream);
 
-/* Bytes of the backward pass's workspace (partial sums of dw and db). */
+/* Bytes of the backward pass's workspace (partial sums of dw and db). Calls on one workspace follow one another. */
 MOE_API int moe_layernorm_workspace_size(const moe_layernorm_config* cfg, size_t* bytes);
 
 /* dx, and dw = sum over rows of dy * (x - mean) * rstd, db = sum of dy: summed in an order that
