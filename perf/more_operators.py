@@ -276,7 +276,7 @@ def _own_bal(s):
                         saved=s["saved"])
     if "dgates" not in s:
         return {"loss": loss, "counts": counts, "lse": lse}
-    tlc.balance_backward(s["cfg"], s["logits"], s["idx"], lse, s["saved"], s["dlogits"], offsets=s["offsets"],
+    tlc.balance_backward(s["cfg"], s["logits"], s["idx"], s["saved"], s["dlogits"], offsets=s["offsets"],
                          mask=s["mask"], gates=s["gates"], dgates=s["dgates"], dloss=s["dloss"])
     return {"loss": loss, "counts": counts, "lse": lse, "dlogits": s["dlogits"]}
 
