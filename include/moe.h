@@ -418,7 +418,8 @@ MOE_API int moe_route_static(const moe_config* cfg, const float* logits, int32_t
 /* ---- operators of a training and serving block around the expert layer --------------------------
  *
  * A dense gated feed-forward block (forward, backward and its form for few tokens), layer norm
- * (forward, backward) and the AdamW step. Same rules as above: the caller owns every buffer and the
+ * (forward, backward), the AdamW step, the gradients' norm and clipping, the norms around a residual sum (forward,
+ * backward) and the router's balance loss (forward, backward). Same rules as above: the caller owns every buffer and the
  * stream, all of them of the calling thread's current device, nothing is allocated or synchronised
  * (moe_ffn_status synchronises), an argument error is returned before any launch. The tile-level pages have
  * no counterpart of these operators.
@@ -567,6 +568,131 @@ MOE_API int moe_adamw_step(const moe_adamw_config* cfg, const moe_adamw_tensor* 
  * arrays of device pointers; an entry may be NULL). For checkpoints and inspection. */
 MOE_API int moe_adamw_read_state(const moe_adamw_tensor* tensors, int32_t count, float* const* m_out,
                                  float* const* v_out, void* stream);
+
+/*
+ * Global norm of a list of gradients and the factor that clips it:
+ *   out[0] = norm = sqrt(sum over all tensors of g^2), out[1] = scale = min(1, max_norm / (norm + eps)).
+ * The squares' sum is held beyond fp32 in precision and range. A gradient that is infinite or NaN makes the norm so;
+ * scale is then 0 or NaN, as the formula gives it. An empty list has norm 0. out + 1 may be handed to
+ * moe_adamw_step as grad_scale and to moe_grad_clip. The order of the sums depends on the list, the pointers'
+ * alignment and the device alone, so results repeat bit for bit.
+ */
+#define MOE_GRAD_NORM_WORKSPACE_BYTES 32768
+typedef struct moe_grad_norm_config {
+    double max_norm; /* > 0; infinite: never clipped */
+    double eps;      /* >= 0 */
+    int32_t reserved[4];
+} moe_grad_norm_config;
+
+typedef struct moe_grad_tensor {
+    void* g; /* contiguous, aligned to its type */
+    int64_t n;
+    int32_t dtype; /* MOE_DTYPE_* */
+    int32_t reserved;
+} moe_grad_tensor;
+
+/* tensors: host array, read during the call; out: device fp32 [2]; ws: device workspace of
+ * MOE_GRAD_NORM_WORKSPACE_BYTES, 16-byte aligned, zeroed by the caller once, before its first call (complete, or
+ * ordered before it on its stream). Calls on one ws follow one another: on one stream, or ordered by the caller. */
+MOE_API int moe_grad_norm(const moe_grad_norm_config* cfg, const moe_grad_tensor* tensors, int32_t count, float* out,
+                          void* ws, size_t ws_bytes, void* stream);
+
+/* g = g * scale in place for every tensor of the list, in fp32, rounded once; scale: device fp32 scalar. With scale 1
+ * nothing is written. Tensors must not overlap, nor hold scale. */
+MOE_API int moe_grad_clip(const moe_grad_tensor* tensors, int32_t count, const float* scale, void* stream);
+
+/*
+ * Norms around a block, fused with its gate and the residual sum:
+ *   h = residual_scale * x + branch_scale * gate * post(u),  z = pre(h)
+ * x the residual stream, u the block's output, h the stream behind the block, z the next block's input. post and pre
+ * are MOE_NORM_NONE (the value itself; no z for pre), MOE_NORM_RMS (v / sqrt(mean v^2 + eps) * w) or MOE_NORM_LAYER
+ * ((v - mean) / sqrt(var + eps) * w + b). gate [ceil(rows / gate_rows), d]: gate_rows consecutive rows share one (all
+ * rows: a gate for each channel; fewer: a gate for each sample or token); gate_rows = 0: no gate. z is the norm of h as it is
+ * stored, rounded, which is what the backward pass reads. A pass with u NULL has no branch: h = residual_scale * x, and
+ * post and gate_rows are 0.
+ * x, u, h, z and their gradients have type dtype, weights, biases, gate and their gradients wdtype (MOE_DTYPE_F32 or
+ * dtype); all arithmetic and sums are fp32. Limits: rows >= 0, 1 <= d <= 16384, eps >= 0, 0 <= gate_rows.
+ * Contiguous; pointers aligned to their type (16-byte aligned ones are faster).
+ */
+#define MOE_NORM_NONE 0
+#define MOE_NORM_RMS 1
+#define MOE_NORM_LAYER 2
+typedef struct moe_residual_norm_config {
+    int64_t rows, gate_rows;
+    int32_t d, dtype, wdtype;
+    int32_t post, pre; /* MOE_NORM_* */
+    float eps, residual_scale, branch_scale;
+    int32_t reserved[4];
+} moe_residual_norm_config;
+
+/* post_w, pre_w: NULL for 1; post_b, pre_b: NULL for 0 (NULL with MOE_NORM_RMS). post_stats, pre_stats: fp32 [rows, 2],
+ * mean (0 for MOE_NORM_RMS) and 1 / sqrt(...) of each row for the backward pass, or NULL. h may be x or u, or NULL when
+ * it is not wanted; z is NULL exactly with pre = MOE_NORM_NONE and may be u, or x when that is not h. No other sharing. */
+MOE_API int moe_residual_norm_forward(const moe_residual_norm_config* cfg, const void* x, const void* u,
+                                      const void* post_w, const void* post_b, const void* gate, const void* pre_w,
+                                      const void* pre_b, void* h, void* z, float* post_stats, float* pre_stats,
+                                      void* stream);
+
+/* Bytes of the backward pass's workspace (partial sums). Calls on one workspace follow one another. Host arithmetic only. */
+MOE_API int moe_residual_norm_workspace_size(const moe_residual_norm_config* cfg, size_t* bytes);
+
+/*
+ * Gradients of a loss whose gradients at z and h (by whatever else reads h) are dz and dh; dz is NULL exactly with
+ * pre = MOE_NORM_NONE, dh may be NULL (0) otherwise. u: as in the forward pass, needed with a post norm or a gate; h: with a pre norm.
+ *   dx = residual_scale * (dh + pre' dz), du = post' (branch_scale * gate * (the same)); du NULL: not wanted
+ *   dpost_w, dpost_b, dgate, dpre_w, dpre_b: summed over the rows (dgate over the rows of each gate), each NULL when
+ *   not wanted; ws may be NULL when all are. dx may be dh or dz, du may be u or dz (not all at once); no other sharing.
+ * The order of the sums depends on the config, the pointers' alignment and the device alone. With rows = 0 the
+ * weights' gradients are set to zero.
+ */
+MOE_API int moe_residual_norm_backward(const moe_residual_norm_config* cfg, const void* dz, const void* dh, const void* u,
+                                       const void* h, const void* post_w, const void* post_b, const void* gate,
+                                       const void* pre_w, const float* post_stats, const float* pre_stats, void* dx,
+                                       void* du, void* dpost_w, void* dpost_b, void* dgate, void* dpre_w, void* dpre_b,
+                                       void* ws, size_t ws_bytes, void* stream);
+
+/*
+ * Balance loss and z loss of a router, with the experts' loads: for the tokens t of sequence s (n_s of them), logits
+ * l [T, E] and p = softmax(l) over all experts,
+ *   c[s, e] = pairs (t, j) with idx[t, j] = e,  f = E / (topk n_s) c,  P = sum_t p / n_s
+ *   balance = mean over the sequences with n_s > 0 of sum_e f[s, e] P[s, e]
+ *   z = mean over all tokens of lse^2, lse[t] = log(sum_e exp(l[t, e]))
+ *   loss = cfg.balance * balance + cfg.z * z
+ * A sequence is the tokens offsets[s] <= t < offsets[s + 1] (offsets [seqs + 1], not decreasing, within [0, T]; NULL: one
+ * sequence of all tokens, seqs = 1). Tokens outside of every sequence, tokens with mask[t] = 0 and tokens whose logits
+ * are all -inf are padding: they count nowhere and have no gradient. An entry of idx outside [0, E) is a dropped pair: it
+ * counts nowhere (topk stays the divisor). An expert that occurs twice in a token's idx counts twice. No token: losses 0.
+ * Limits: 0 <= T < 2^24, 1 <= E <= 256, 1 <= topk <= 8, 1 <= seqs < 2^24.
+ */
+typedef struct moe_balance_config {
+    int32_t T, E, topk, seqs;
+    float balance, z;
+    int32_t reserved[4];
+} moe_balance_config;
+
+/* Bytes of the forward pass's workspace (partial sums), and of the buffer that it keeps for moe_balance_backward. Host
+ * arithmetic only. */
+MOE_API int moe_balance_workspace_size(const moe_balance_config* cfg, size_t* bytes);
+MOE_API int moe_balance_saved_size(const moe_balance_config* cfg, size_t* bytes);
+
+/* logits device f32 [T, E]; idx device int32 [T, topk] (as moe_plan's topk_idx); offsets device int32 [seqs + 1] or NULL;
+ * mask device uint8 [T] or NULL; loss device f32 [3]: loss, balance, z; counts device int32 [seqs, E]: c; lse device f32 [T]
+ * or NULL (written for padding too); saved: moe_balance_saved_size bytes, or NULL without a backward pass. ws and
+ * saved 16-byte aligned. Calls on one ws follow one another. Sums repeat bit for bit. */
+MOE_API int moe_balance_forward(const moe_balance_config* cfg, const float* logits, const int32_t* idx,
+                                const int32_t* offsets, const uint8_t* mask, float* loss, int32_t* counts, float* lse,
+                                void* saved, void* ws, size_t ws_bytes, void* stream);
+
+/*
+ * The gradient at the logits, every row of dlogits [T, E] written (zeros for padding); dlogits may be logits.
+ *   dloss * (cfg.balance d balance / dl + cfg.z dz / dl)  + the gradient of the gates
+ * (counts are constants). dloss: device f32 scalar, or NULL for 1. gates, dgates device f32 [T, topk], or both NULL: gates as
+ * moe_plan's topk_w (softmax over the chosen logits) and the loss's gradients at them; to the logit of pair (t, j)
+ * comes gates[t, j] * (dgates[t, j] - sum_i gates[t, i] dgates[t, i]), to that of a dropped pair nothing.
+ */
+MOE_API int moe_balance_backward(const moe_balance_config* cfg, const float* logits, const int32_t* idx,
+                                 const int32_t* offsets, const uint8_t* mask, const void* saved, const float* gates,
+                                 const float* dgates, const float* dloss, float* dlogits, void* stream);
 
 /* Message of the last error on the calling thread ("" if none). The pointer stays valid until
  * the thread's next call into the library. */

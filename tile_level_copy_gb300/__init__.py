@@ -48,6 +48,8 @@ MOE_DTYPE_F32, MOE_DTYPE_BF16, MOE_DTYPE_F16 = 0, 1, 2
 MOE_ADAMW_BLOCK = 128
 MOE_FFN_STATUS_BYTES = 8192
 MOE_FFN_TEST_STALL0, MOE_FFN_TEST_STALL1 = 0x1, 0x2
+MOE_GRAD_NORM_WORKSPACE_BYTES = 32768
+MOE_NORM_NONE, MOE_NORM_RMS, MOE_NORM_LAYER = 0, 1, 2
 _DTYPES = {torch.float32: MOE_DTYPE_F32, torch.bfloat16: MOE_DTYPE_BF16, torch.float16: MOE_DTYPE_F16}
 
 # names of the C entry points (each declared in include/moe.h)
@@ -56,7 +58,9 @@ EXPORTS = ("moe_workspace_size", "moe_workspace_layout", "moe_plan", "moe_forwar
            "moe_forward_dma", "moe_status", "moe_device_info", "moe_route_static", "moe_ffn_workspace_size",
            "moe_ffn_saved_size", "moe_ffn_forward", "moe_ffn_backward", "moe_ffn_status", "moe_layernorm_forward",
            "moe_layernorm_workspace_size", "moe_layernorm_backward", "moe_adamw_step", "moe_adamw_read_state",
-           "moe_last_error")
+           "moe_grad_norm", "moe_grad_clip", "moe_residual_norm_forward", "moe_residual_norm_workspace_size",
+           "moe_residual_norm_backward", "moe_balance_workspace_size", "moe_balance_saved_size", "moe_balance_forward",
+           "moe_balance_backward", "moe_last_error")
 
 # stage events of moe_forward_ex
 EV_BEGIN, EV_PLANNED, EV_UP, EV_DOWN, EV_COPIED, EV_END, EV_COUNT = range(7)
@@ -134,6 +138,25 @@ class _AdamWTensor(ctypes.Structure):
         ("n", ctypes.c_int64), ("rng_base", ctypes.c_int64), ("p_dtype", ctypes.c_int32), ("g_dtype", ctypes.c_int32)]
 
 
+class _GradNormConfig(ctypes.Structure):
+    _fields_ = [("max_norm", ctypes.c_double), ("eps", ctypes.c_double), ("reserved", ctypes.c_int32 * 4)]
+
+
+class _GradTensor(ctypes.Structure):
+    _fields_ = [("g", ctypes.c_void_p), ("n", ctypes.c_int64), ("dtype", ctypes.c_int32), ("reserved", ctypes.c_int32)]
+
+
+class _ResidualNormConfig(ctypes.Structure):
+    _fields_ = [("rows", ctypes.c_int64), ("gate_rows", ctypes.c_int64)] + [
+        (n, ctypes.c_int32) for n in ("d", "dtype", "wdtype", "post", "pre")] + [
+        (n, ctypes.c_float) for n in ("eps", "residual_scale", "branch_scale")] + [("reserved", ctypes.c_int32 * 4)]
+
+
+class _BalanceConfig(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("T", "E", "topk", "seqs")] + [
+        ("balance", ctypes.c_float), ("z", ctypes.c_float), ("reserved", ctypes.c_int32 * 4)]
+
+
 _lib = None
 
 
@@ -173,6 +196,17 @@ def lib() -> ctypes.CDLL:
         L.moe_layernorm_backward.argtypes = [lcfg] + [vp] * 9 + [sz, vp]
         L.moe_adamw_step.argtypes = [acfg, tens, ctypes.c_int32, vp, vp]
         L.moe_adamw_read_state.argtypes = [tens, ctypes.c_int32, vpp, vpp, vp]
+        ncfg, rcfg, bcfg = (ctypes.POINTER(t) for t in (_GradNormConfig, _ResidualNormConfig, _BalanceConfig))
+        grads = ctypes.POINTER(_GradTensor)
+        L.moe_grad_norm.argtypes = [ncfg, grads, ctypes.c_int32, vp, vp, sz, vp]
+        L.moe_grad_clip.argtypes = [grads, ctypes.c_int32, vp, vp]
+        L.moe_residual_norm_forward.argtypes = [rcfg] + [vp] * 12
+        L.moe_residual_norm_workspace_size.argtypes = [rcfg, szp]
+        L.moe_residual_norm_backward.argtypes = [rcfg] + [vp] * 18 + [sz, vp]
+        L.moe_balance_workspace_size.argtypes = [bcfg, szp]
+        L.moe_balance_saved_size.argtypes = [bcfg, szp]
+        L.moe_balance_forward.argtypes = [bcfg] + [vp] * 9 + [sz, vp]
+        L.moe_balance_backward.argtypes = [bcfg] + [vp] * 10
         L.moe_last_error.restype = ctypes.c_char_p
         for n in EXPORTS[:-1]:
             getattr(L, n).restype = ctypes.c_int
@@ -668,7 +702,7 @@ class AdamWValues:
         self.keep = [list(m), list(v)]
 
 
-def _list_device(tensors: AdamWList, on: int) -> None:
+def _list_device(tensors, on: int) -> None:
     """Refuses a list whose tensors are not on the current device."""
     if tensors.count and tensors.device != on:
         raise ValueError(f"the list's tensors are on cuda:{tensors.device}, the call is for cuda:{on}")
@@ -698,3 +732,215 @@ def adamw_read_state(cfg: AdamWConfig, tensors: AdamWList, out: AdamWValues, str
     _list_device(tensors, on)
     _check(lib().moe_adamw_read_state(tensors.c, tensors.count, out.m, out.v,
                                       _current_stream(on) if stream is None else _stream(stream)))
+
+
+@dataclasses.dataclass
+class GradNormConfig(_Marshalled):
+    """Clipping by the global norm (mirrors moe_grad_norm_config): scale = min(1, max_norm / (norm + eps))."""
+
+    max_norm: float
+    eps: float = 1e-6
+
+    def to_c(self) -> _GradNormConfig:
+        return _GradNormConfig(self.max_norm, self.eps)
+
+
+class GradNormWorkspace:
+    """Device workspace of grad_norm; it starts as zero, and is so for calls on any stream (the constructor waits
+    for its clearing, unless the current stream is being captured)."""
+
+    def __init__(self, device="cuda"):
+        self.nbytes = MOE_GRAD_NORM_WORKSPACE_BYTES
+        self.buf = torch.zeros(self.nbytes, dtype=torch.uint8, device=device)
+        if self.buf.is_cuda and not torch.cuda.is_current_stream_capturing():
+            torch.cuda.current_stream(self.buf.device).synchronize()
+        self.ptr = self.buf.data_ptr()
+
+
+class GradList:
+    """Gradients (float32, bfloat16 or float16; any shapes and alignments), marshalled once. The list keeps its
+    tensors alive; a tensor that moves needs a new list. Tensors that share memory are refused: grad_clip would scale
+    it twice."""
+
+    def __init__(self, grads):
+        self.keep = list(grads)
+        self.count = len(self.keep)
+        self.device = self.keep[0].get_device() if self.keep else None
+        self.c = (_GradTensor * max(self.count, 1))()
+        spans = []
+        for i, g in enumerate(self.keep):
+            if g.dtype not in _DTYPES:
+                raise ValueError(f"grads[{i}] must be float32, bfloat16 or float16, got {g.dtype}")
+            e, n = self.c[i], g.numel()
+            e.g, e.n, e.dtype = _local(g, None, self.device, f"grads[{i}]"), n, _DTYPES[g.dtype]
+            if n:
+                spans.append((g.data_ptr(), g.data_ptr() + n * g.element_size(), i))
+        spans.sort()
+        for (_, end, i), (at, _, j) in zip(spans, spans[1:]):
+            if at < end:
+                raise ValueError(f"grads[{i}] and grads[{j}] share memory")
+
+
+def grad_norm(cfg: GradNormConfig, grads: GradList, out: torch.Tensor, ws: GradNormWorkspace, stream=None) -> None:
+    """moe_grad_norm: out (float32 [2]) = global norm, and the factor that clips it (for grad_clip, or for
+    adamw_step as grad_scale=out[1:])."""
+    on = _device()
+    _list_device(grads, on)
+    _check(lib().moe_grad_norm(cfg.ref()[0], grads.c, grads.count, _flat(out, torch.float32, 2, on, "out"),
+                               _space(ws, on), ws.nbytes, _current_stream(on) if stream is None else _stream(stream)))
+
+
+def grad_clip(grads: GradList, scale: torch.Tensor, stream=None) -> None:
+    """moe_grad_clip: every gradient times scale (a float32 value on the GPU), in place."""
+    on = _device()
+    _list_device(grads, on)
+    _check(lib().moe_grad_clip(grads.c, grads.count, _flat(scale, torch.float32, 1, on, "scale"),
+                               _current_stream(on) if stream is None else _stream(stream)))
+
+
+@dataclasses.dataclass
+class ResidualNormConfig(_Marshalled):
+    """Norms around a block with its gate and the residual sum (mirrors moe_residual_norm_config):
+    h = residual_scale * x + branch_scale * gate * post(u), z = pre(h). post, pre: MOE_NORM_*; gate_rows consecutive rows
+    share a gate (0: no gate)."""
+
+    rows: int
+    d: int
+    dtype: torch.dtype = torch.bfloat16
+    wdtype: torch.dtype = torch.float32
+    post: int = MOE_NORM_NONE
+    pre: int = MOE_NORM_RMS
+    gate_rows: int = 0
+    eps: float = 1e-5
+    residual_scale: float = 1.0
+    branch_scale: float = 1.0
+
+    def to_c(self) -> _ResidualNormConfig:
+        if self.dtype not in _DTYPES or self.wdtype not in _DTYPES:
+            raise ValueError(f"residual norm takes float32, bfloat16 or float16, got {self.dtype}, {self.wdtype}")
+        return _ResidualNormConfig(int(self.rows), int(self.gate_rows), int(self.d), _DTYPES[self.dtype],
+                                   _DTYPES[self.wdtype], int(self.post), int(self.pre), float(self.eps),
+                                   float(self.residual_scale), float(self.branch_scale))
+
+    def _make(self):
+        c = self.to_c()
+        gates = -(-self.rows // self.gate_rows) if self.gate_rows > 0 else 0
+        return (ctypes.byref(c), c, self.rows * self.d, gates * self.d, 2 * self.rows)
+
+
+class ResidualNormWorkspace:
+    """Device workspace of residual_norm_backward."""
+
+    def __init__(self, cfg: ResidualNormConfig, device="cuda"):
+        n = ctypes.c_size_t()
+        _check(lib().moe_residual_norm_workspace_size(cfg.ref()[0], ctypes.byref(n)))
+        self.nbytes = n.value
+        self.buf = torch.empty(self.nbytes, dtype=torch.uint8, device=device)
+        self.ptr = self.buf.data_ptr()
+
+
+def residual_norm_forward(cfg: ResidualNormConfig, x: torch.Tensor, u: Optional[torch.Tensor],
+                          post_w: Optional[torch.Tensor], post_b: Optional[torch.Tensor], gate: Optional[torch.Tensor],
+                          pre_w: Optional[torch.Tensor], pre_b: Optional[torch.Tensor], h: Optional[torch.Tensor],
+                          z: Optional[torch.Tensor], post_stats: Optional[torch.Tensor] = None,
+                          pre_stats: Optional[torch.Tensor] = None, stream=None) -> None:
+    """moe_residual_norm_forward: h = residual_scale * x + branch_scale * gate * post(u), z = pre(h); post_stats and
+    pre_stats (float32 [rows, 2]) for a backward pass."""
+    dt, wt, d, on, f32 = cfg.dtype, cfg.wdtype, cfg.d, _device(), torch.float32
+    c, _, n, gates, st = cfg.ref()
+    _check(lib().moe_residual_norm_forward(
+        c, _flat(x, dt, n, on, "x"), _flat(u, dt, n, on, "u"), _flat(post_w, wt, d, on, "post_w"),
+        _flat(post_b, wt, d, on, "post_b"), _flat(gate, wt, gates, on, "gate"), _flat(pre_w, wt, d, on, "pre_w"),
+        _flat(pre_b, wt, d, on, "pre_b"), _flat(h, dt, n, on, "h"), _flat(z, dt, n, on, "z"),
+        _flat(post_stats, f32, st, on, "post_stats"), _flat(pre_stats, f32, st, on, "pre_stats"),
+        _current_stream(on) if stream is None else _stream(stream)))
+
+
+def residual_norm_backward(cfg: ResidualNormConfig, dz: Optional[torch.Tensor], dh: Optional[torch.Tensor],
+                           u: Optional[torch.Tensor], h: Optional[torch.Tensor], post_w: Optional[torch.Tensor],
+                           post_b: Optional[torch.Tensor], gate: Optional[torch.Tensor], pre_w: Optional[torch.Tensor],
+                           post_stats: Optional[torch.Tensor], pre_stats: Optional[torch.Tensor], dx: torch.Tensor,
+                           du: Optional[torch.Tensor], dpost_w: Optional[torch.Tensor] = None,
+                           dpost_b: Optional[torch.Tensor] = None, dgate: Optional[torch.Tensor] = None,
+                           dpre_w: Optional[torch.Tensor] = None, dpre_b: Optional[torch.Tensor] = None,
+                           ws: Optional[ResidualNormWorkspace] = None, stream=None) -> None:
+    """moe_residual_norm_backward: dx and du from dz (at z) and dh (at h, by its other readers), and the weights' and
+    the gate's gradients, each None when not wanted (ws too, when all are)."""
+    dt, wt, d, on, f32 = cfg.dtype, cfg.wdtype, cfg.d, _device(), torch.float32
+    c, _, n, gates, st = cfg.ref()
+    _check(lib().moe_residual_norm_backward(
+        c, _flat(dz, dt, n, on, "dz"), _flat(dh, dt, n, on, "dh"), _flat(u, dt, n, on, "u"), _flat(h, dt, n, on, "h"),
+        _flat(post_w, wt, d, on, "post_w"), _flat(post_b, wt, d, on, "post_b"), _flat(gate, wt, gates, on, "gate"),
+        _flat(pre_w, wt, d, on, "pre_w"), _flat(post_stats, f32, st, on, "post_stats"),
+        _flat(pre_stats, f32, st, on, "pre_stats"), _flat(dx, dt, n, on, "dx"), _flat(du, dt, n, on, "du"),
+        _flat(dpost_w, wt, d, on, "dpost_w"), _flat(dpost_b, wt, d, on, "dpost_b"), _flat(dgate, wt, gates, on, "dgate"),
+        _flat(dpre_w, wt, d, on, "dpre_w"), _flat(dpre_b, wt, d, on, "dpre_b"), None if ws is None else _space(ws, on),
+        0 if ws is None else ws.nbytes, _current_stream(on) if stream is None else _stream(stream)))
+
+
+@dataclasses.dataclass
+class BalanceConfig(_Marshalled):
+    """Balance and z loss of a router (mirrors moe_balance_config): T tokens in seqs sequences, E experts, topk chosen;
+    balance and z: the losses' weights."""
+
+    T: int
+    E: int
+    topk: int
+    seqs: int = 1
+    balance: float = 0.01
+    z: float = 0.0
+
+    def to_c(self) -> _BalanceConfig:
+        return _BalanceConfig(int(self.T), int(self.E), int(self.topk), int(self.seqs), float(self.balance), float(self.z))
+
+    def _make(self):
+        c, n = self.to_c(), ctypes.c_size_t()
+        _check(lib().moe_balance_saved_size(ctypes.byref(c), ctypes.byref(n)))
+        return (ctypes.byref(c), c, (self.T, self.E), (self.T, self.topk), (self.seqs, self.E), n.value)
+
+
+class BalanceWorkspace:
+    """Device workspace of balance_forward."""
+
+    def __init__(self, cfg: BalanceConfig, device="cuda"):
+        n = ctypes.c_size_t()
+        _check(lib().moe_balance_workspace_size(cfg.ref()[0], ctypes.byref(n)))
+        self.nbytes = n.value
+        self.buf = torch.empty(self.nbytes, dtype=torch.uint8, device=device)
+        self.ptr = self.buf.data_ptr()
+
+
+def balance_saved(cfg: BalanceConfig, device="cuda") -> torch.Tensor:
+    """Buffer in which balance_forward keeps what balance_backward needs (uint8, opaque)."""
+    return torch.empty(cfg.ref()[5], dtype=torch.uint8, device=device)
+
+
+def balance_forward(cfg: BalanceConfig, logits: torch.Tensor, idx: torch.Tensor, loss: torch.Tensor, counts: torch.Tensor,
+                    lse: Optional[torch.Tensor], ws: BalanceWorkspace, offsets: Optional[torch.Tensor] = None,
+                    mask: Optional[torch.Tensor] = None, saved: Optional[torch.Tensor] = None, stream=None) -> None:
+    """moe_balance_forward: loss (float32 [3]: loss, balance, z), counts (int32 [seqs, E]) and lse (float32 [T] or None)
+    of the logits (float32 [T, E]) and choices idx (int32 [T, topk]); offsets (int32 [seqs + 1]): the sequences' starts
+    and the last one's end; mask (uint8 [T]): 0 for padding."""
+    i32, f32, on = torch.int32, torch.float32, _device()
+    c, _, rows, pairs, loads, need = cfg.ref()
+    _check(lib().moe_balance_forward(
+        c, _dev(logits, f32, rows, on, "logits"), _dev(idx, i32, pairs, on, "idx"),
+        _flat(offsets, i32, loads[0] + 1, on, "offsets"), _flat(mask, torch.uint8, rows[0], on, "mask"),
+        _flat(loss, f32, 3, on, "loss"), _dev(counts, i32, loads, on, "counts"), _flat(lse, f32, rows[0], on, "lse"),
+        _saved(saved, need, on), _space(ws, on), ws.nbytes, _current_stream(on) if stream is None else _stream(stream)))
+
+
+def balance_backward(cfg: BalanceConfig, logits: torch.Tensor, idx: torch.Tensor, saved: torch.Tensor,
+                     dlogits: torch.Tensor, offsets: Optional[torch.Tensor] = None, mask: Optional[torch.Tensor] = None,
+                     gates: Optional[torch.Tensor] = None, dgates: Optional[torch.Tensor] = None,
+                     dloss: Optional[torch.Tensor] = None, stream=None) -> None:
+    """moe_balance_backward: dlogits (float32 [T, E]) from the forward pass's inputs and its saved buffer; dloss: a
+    float32 value on the GPU (None: 1). gates and dgates (float32 [T, topk]): the router's gates, whose gradient joins."""
+    i32, f32, on = torch.int32, torch.float32, _device()
+    c, _, rows, pairs, loads, need = cfg.ref()
+    _check(lib().moe_balance_backward(
+        c, _dev(logits, f32, rows, on, "logits"), _dev(idx, i32, pairs, on, "idx"),
+        _flat(offsets, i32, loads[0] + 1, on, "offsets"), _flat(mask, torch.uint8, rows[0], on, "mask"),
+        _saved(saved, need, on), _dev(gates, f32, pairs, on, "gates"), _dev(dgates, f32, pairs, on, "dgates"),
+        _flat(dloss, f32, 1, on, "dloss"), _dev(dlogits, f32, rows, on, "dlogits"),
+        _current_stream(on) if stream is None else _stream(stream)))

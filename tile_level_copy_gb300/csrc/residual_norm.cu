@@ -1,0 +1,501 @@
+// Norms around a block fused with its gate and the residual sum: forward pass, sums over the rows, C entries.
+//
+//   h = a x + c gate * post(u), z = pre(h); a norm is (v - mean) rstd w + b, with mean 0 for the mean-square kind
+//
+// The pass reads x and u and writes h and z: HBM bounds it. A row lies in shared memory in the slots of the warps
+// that share it, fetched by cp.async while the rows before are worked on; a thread reads only pieces that it fetched
+// itself, so no barrier guards the slots. h is rounded to its type before the second norm (the value the backward
+// pass and every other reader sees) and waits in x's slot for the pass that writes z.
+#include "residual_norm.cuh"
+
+#include <math.h>
+
+namespace moe {
+namespace {
+
+constexpr int RN_FWD_THREADS = 256;
+constexpr int RN_UNROLL = 4;        // pieces worked on at a time
+constexpr int RN_RED_COLS = 32, RN_RED_ROWS = 32;
+constexpr int RN_MAX_SMS = 256;
+
+template <typename T, int VEC>
+__global__ void __launch_bounds__(RN_FWD_THREADS, 3)
+    rn_forward_kernel(RnShape s, const T* x, const T* u, RnWeights w, T* h, T* z, float2* post_stats, float2* pre_stats) {
+    typedef typename Lanes<VEC>::V V;
+    typedef Pack<T, VEC> P;
+    constexpr int N = Lanes<VEC>::N;
+    __shared__ float red[2][RN_FWD_THREADS / 32];
+    extern __shared__ __align__(16) uint8_t rn_smem[];
+    griddep_wait();
+    griddep_launch();
+    const int tpr = s.warps * 32, t = threadIdx.x % tpr, group = threadIdx.x / tpr, lane = threadIdx.x & 31;
+    const int threads = blockDim.x, step = tpr * VEC, c0 = t * VEC;
+    const int np = c0 < s.d ? (s.d - c0 + step - 1) / step : 0;  // this thread's pieces, at most s.pieces
+    P* const slot = reinterpret_cast<P*>(rn_smem) + threadIdx.x;
+    const int64_t stride = (int64_t)gridDim.x * s.groups;
+    auto piece = [&](int stage, int tensor, int q) { return slot + ((stage * 2 + tensor) * s.pieces + q) * threads; };
+    auto issue = [&](int64_t r, int stage) {
+        if (r < s.rows) {
+            const T* xr = x + r * s.d + c0;
+            const T* ur = u + r * s.d + c0;
+            for (int q = 0; q < np; ++q) fetch(piece(stage, 0, q), reinterpret_cast<const P*>(xr + q * step));
+            if (u)
+                for (int q = 0; q < np; ++q) fetch(piece(stage, 1, q), reinterpret_cast<const P*>(ur + q * step));
+        }
+        asm volatile("cp.async.commit_group;" ::: "memory");
+    };
+    int flip = 0;
+    auto row_sum = [&](V v) {
+        float a = warp_sum(total(v));
+        if (s.warps == 1) return a;
+        float* r = red[flip] + group * s.warps;  // the two halves in turn: one barrier a sum is enough
+        flip ^= 1;
+        if (lane == 0) r[t >> 5] = a;
+        named_bar_sync(1 + group, tpr);
+        a = 0.f;
+        for (int i = 0; i < s.warps; ++i) a += r[i];
+        return a;
+    };
+    // f(q) for every piece of the thread
+    auto over = [&](auto f) {
+        for (int q0 = 0; q0 < np; q0 += RN_UNROLL) {
+#pragma unroll
+            for (int k = 0; k < RN_UNROLL; ++k) {
+                if (q0 + k >= np) break;
+                f(q0 + k);
+            }
+        }
+    };
+    // mean and 1 / sqrt(mean square + eps) of the pieces of a tensor in a slot
+    auto statistics = [&](int kind, int stage, int tensor) {
+        V f[N], acc = both<V>(0.f);
+        float mu = 0.f;
+        if (kind == MOE_NORM_LAYER) {
+            over([&](int q) {
+                widen(*piece(stage, tensor, q), f);
+#pragma unroll
+                for (int i = 0; i < N; ++i) acc = add_(acc, f[i]);
+            });
+            mu = row_sum(acc) * s.inv_d;
+        }
+        const V neg = both<V>(-mu);
+        V sq[2] = {both<V>(0.f), both<V>(0.f)};
+        over([&](int q) {
+            widen(*piece(stage, tensor, q), f);
+#pragma unroll
+            for (int i = 0; i < N; ++i) {
+                f[i] = add_(f[i], neg);
+                sq[i & 1] = fma_(f[i], f[i], sq[i & 1]);
+            }
+        });
+        return make_float2(mu, rsqrtf(fmaf(row_sum(add_(sq[0], sq[1])), s.inv_d, s.eps)));
+    };
+
+    int stage = 0;
+    int64_t r = (int64_t)blockIdx.x * s.groups + group;
+    for (int k = 0; k < s.slots - 1; ++k) issue(r + k * stride, k);
+    for (; r < s.rows; r += stride) {
+        issue(r + (s.slots - 1) * stride, stage == 0 ? s.slots - 1 : stage - 1);
+        fetched(s.slots - 1);
+        const int64_t at = r * s.d + c0;
+        float2 st = make_float2(0.f, 1.f);
+        if (s.post) {
+            st = statistics(s.post, stage, 1);
+            if (t == 0 && post_stats) post_stats[r] = st;
+        }
+        const V neg = both<V>(-st.x), rs = both<V>(st.y), res = both<V>(s.res), branch = both<V>(s.branch);
+        const int64_t gate_at = s.gate_rows ? r / s.gate_rows * s.d : 0;
+        over([&](int q) {
+            const int c = c0 + q * step;
+            V f[N], v[N], k[N];
+            widen(*piece(stage, 0, q), f);
+#pragma unroll
+            for (int i = 0; i < N; ++i) f[i] = mul_(f[i], res);
+            if (u) {
+                widen(*piece(stage, 1, q), v);
+                if (s.post) {
+#pragma unroll
+                    for (int i = 0; i < N; ++i) v[i] = mul_(add_(v[i], neg), rs);
+                    if (w.post_w) {
+                        weight<T, VEC>(w, w.post_w, 1.f, c, k);
+#pragma unroll
+                        for (int i = 0; i < N; ++i) v[i] = mul_(v[i], k[i]);
+                    }
+                    if (w.post_b) {
+                        weight<T, VEC>(w, w.post_b, 0.f, c, k);
+#pragma unroll
+                        for (int i = 0; i < N; ++i) v[i] = add_(v[i], k[i]);
+                    }
+                }
+                if (s.gate_rows) {
+                    weight<T, VEC>(w, w.gate, 1.f, gate_at + c, k);
+#pragma unroll
+                    for (int i = 0; i < N; ++i) v[i] = mul_(v[i], k[i]);
+                }
+#pragma unroll
+                for (int i = 0; i < N; ++i) f[i] = fma_(v[i], branch, f[i]);
+            }
+            const P p = narrow<T, VEC>(f);
+            if (h) *reinterpret_cast<P*>(h + at + q * step) = p;
+            *piece(stage, 0, q) = p;
+        });
+        if (s.pre) {
+            const float2 ps = statistics(s.pre, stage, 0);
+            if (t == 0 && pre_stats) pre_stats[r] = ps;
+            const V pneg = both<V>(-ps.x), prs = both<V>(ps.y);
+            over([&](int q) {
+                const int c = c0 + q * step;
+                V f[N], k[N];
+                widen(*piece(stage, 0, q), f);
+#pragma unroll
+                for (int i = 0; i < N; ++i) f[i] = mul_(add_(f[i], pneg), prs);
+                if (w.pre_w) {
+                    weight<T, VEC>(w, w.pre_w, 1.f, c, k);
+#pragma unroll
+                    for (int i = 0; i < N; ++i) f[i] = mul_(f[i], k[i]);
+                }
+                if (w.pre_b) {
+                    weight<T, VEC>(w, w.pre_b, 0.f, c, k);
+#pragma unroll
+                    for (int i = 0; i < N; ++i) f[i] = add_(f[i], k[i]);
+                }
+                *reinterpret_cast<P*>(z + at + q * step) = narrow<T, VEC>(f);
+            });
+        }
+        if (++stage == s.slots) stage = 0;
+    }
+    fetched(0);
+}
+
+// The gradients of the weights from the CTAs' sums [parts][sums][d]: blockIdx.y 0 the norm before the next block
+// (sum 0, and 1 with full), 1 the norm behind this one and a gate that all rows share (the last one or two sums);
+// from 2 on the gates of groups of rows that lie in more than one group of warps.
+struct RnReduce {
+    const float* part;
+    const float* gpart;
+    int parts, d;
+    bool full, grouped, f32;
+    const void *post_w, *post_b, *gate;
+    void *dpost_w, *dpost_b, *dgate, *dpre_w, *dpre_b;
+    int64_t rows, gate_rows, chunk;
+};
+template <typename T>
+__device__ __forceinline__ void put_at(void* p, bool f32, int64_t i, float v) {
+    if (!p) return;
+    if (f32) static_cast<float*>(p)[i] = v;
+    else put(static_cast<T*>(p)[i], v);
+}
+template <typename T>
+__global__ void __launch_bounds__(RN_RED_COLS* RN_RED_ROWS) rn_reduce_kernel(RnReduce a) {
+    __shared__ float acc[2][RN_RED_ROWS][RN_RED_COLS];
+    griddep_wait();
+    griddep_launch();
+    const int lane = threadIdx.x % RN_RED_COLS, row = threadIdx.x / RN_RED_COLS, c = blockIdx.x * RN_RED_COLS + lane;
+    if (blockIdx.y >= 2) {
+        if (c >= a.d || row) return;
+        const int64_t gates = (a.rows + a.gate_rows - 1) / a.gate_rows;
+        for (int64_t g = blockIdx.y - 2; g < gates; g += gridDim.y - 2) {
+            const int64_t from = g * a.gate_rows, to = from + a.gate_rows < a.rows ? from + a.gate_rows : a.rows;
+            const int64_t w0 = from / a.chunk, w1 = (to - 1) / a.chunk;
+            if (w0 == w1) continue;  // the group of warps wrote it
+            float v = 0.f;
+            for (int64_t k = w0; k <= w1; ++k)  // a group of warps' first gate is in its first row of sums
+                v += a.gpart[(2 * k + (k * a.chunk / a.gate_rows == g ? 0 : 1)) * a.d + c];
+            put_at<T>(a.dgate, a.f32, g * a.d + c, v);
+        }
+        return;
+    }
+    const int sums = a.full ? 4 : 2, first = blockIdx.y == 0 ? 0 : sums / 2;
+    float v[2] = {0.f, 0.f};
+    if (c < a.d) {
+#pragma unroll
+        for (int n = 0; n < 2; ++n) {
+            if (n && !a.full) break;
+            const float* from = a.part + (size_t)(first + n) * a.d + c;
+            const size_t hop = (size_t)sums * a.d;
+            for (int q = row; q < a.parts; q += 8 * RN_RED_ROWS) {  // eight loads in flight
+                float e[8];
+#pragma unroll
+                for (int k = 0; k < 8; ++k) e[k] = q + k * RN_RED_ROWS < a.parts ? from[(size_t)(q + k * RN_RED_ROWS) * hop] : 0.f;
+#pragma unroll
+                for (int k = 0; k < 8; ++k) v[n] += e[k];
+            }
+        }
+    }
+    acc[0][row][lane] = v[0];
+    acc[1][row][lane] = v[1];
+    __syncthreads();
+    if (row || c >= a.d) return;
+    float x = 0.f, y = 0.f;
+#pragma unroll
+    for (int q = 0; q < RN_RED_ROWS; ++q) {
+        x += acc[0][q][lane];
+        y += acc[1][q][lane];
+    }
+    if (blockIdx.y == 0) {
+        put_at<T>(a.dpre_w, a.f32, c, x);
+        put_at<T>(a.dpre_b, a.f32, c, y);
+    } else if (a.grouped) {
+        put_at<T>(a.dpost_w, a.f32, c, x);
+        put_at<T>(a.dpost_b, a.f32, c, y);
+    } else {  // the sums lack the gate's factor
+        const float g = value_at<T>(a.gate, a.f32, c, 1.f);
+        put_at<T>(a.dpost_w, a.f32, c, x * g);
+        put_at<T>(a.dpost_b, a.f32, c, y * g);
+        put_at<T>(a.dgate, a.f32, c, value_at<T>(a.post_w, a.f32, c, 1.f) * x + value_at<T>(a.post_b, a.f32, c, 0.f) * y);
+    }
+}
+
+int check(const moe_residual_norm_config* c) {
+    if (!c) return fail(MOE_ERR_ARG, "config is NULL");
+    if (c->rows < 0 || c->gate_rows < 0)
+        return fail(MOE_ERR_ARG, "rows=%lld and gate_rows=%lld must be >= 0", (long long)c->rows, (long long)c->gate_rows);
+    if (c->d < 1 || c->d > RN_MAX_D) return fail(MOE_ERR_ARG, "d=%d must be in [1, %d]", c->d, RN_MAX_D);
+    if (c->rows > INT64_MAX / 8 / c->d) return fail(MOE_ERR_ARG, "rows=%lld is too large", (long long)c->rows);
+    if (c->dtype != MOE_DTYPE_F32 && c->dtype != MOE_DTYPE_BF16 && c->dtype != MOE_DTYPE_F16)
+        return fail(MOE_ERR_ARG, "dtype=%d is not a MOE_DTYPE", c->dtype);
+    if (c->wdtype != MOE_DTYPE_F32 && c->wdtype != c->dtype)
+        return fail(MOE_ERR_ARG, "wdtype=%d must be fp32 or dtype", c->wdtype);
+    for (int k : {c->post, c->pre})
+        if (k != MOE_NORM_NONE && k != MOE_NORM_RMS && k != MOE_NORM_LAYER)
+            return fail(MOE_ERR_ARG, "post=%d and pre=%d must be MOE_NORM_*", c->post, c->pre);
+    if (!(c->eps >= 0)) return fail(MOE_ERR_ARG, "eps=%g must be >= 0", (double)c->eps);
+    if (!isfinite(c->residual_scale) || !isfinite(c->branch_scale))
+        return fail(MOE_ERR_ARG, "residual_scale=%g and branch_scale=%g must be finite", (double)c->residual_scale,
+                    (double)c->branch_scale);
+    for (int i = 0; i < 4; ++i)
+        if (c->reserved[i]) return fail(MOE_ERR_ARG, "reserved fields must be zero");
+    return MOE_OK;
+}
+
+// Whether rows of outputs lie over one another or over rows that they may not: an output may be an input that its
+// elements replace one by one (the same pointer), and nothing else of it.
+bool apart(const void* a, const void* b, size_t bytes) {
+    if (!a || !b) return true;
+    const uintptr_t p = reinterpret_cast<uintptr_t>(a), q = reinterpret_cast<uintptr_t>(b);
+    return p >= q + bytes || q >= p + bytes;
+}
+bool apart_or_same(const void* a, const void* b, size_t bytes) { return a == b || apart(a, b, bytes); }
+
+// 16-byte pieces where they divide the rows and every row's pieces are aligned, else single values.
+template <typename... Ptr>
+int vector_width(const moe_residual_norm_config& c, Ptr... p) {
+    const int v = (int)(16 / dtype_size(c.dtype));
+    return c.d % v == 0 && (aligned(p, 16) && ...) ? v : 1;
+}
+RnWeights weights_of(const moe_residual_norm_config& c, int vec, const void* post_w, const void* post_b, const void* gate,
+                     const void* pre_w, const void* pre_b) {
+    const bool f32 = c.wdtype == MOE_DTYPE_F32;
+    const size_t piece = f32 ? (vec < 4 ? vec : 4) * 4 : vec * dtype_size(c.dtype);
+    const bool whole = aligned(post_w, piece) && aligned(post_b, piece) && aligned(gate, piece) && aligned(pre_w, piece) &&
+                       aligned(pre_b, piece);
+    return RnWeights{post_w, post_b, gate, pre_w, pre_b, !whole ? LN_W_ANY : f32 ? LN_W_F32 : LN_W_SAME, f32};
+}
+int check_weights(const moe_residual_norm_config& c, const void* post_w, const void* post_b, const void* gate,
+                  const void* pre_w, const void* pre_b) {
+    const size_t we = dtype_size(c.wdtype);
+    if (!aligned(post_w, we) || !aligned(post_b, we) || !aligned(gate, we) || !aligned(pre_w, we) || !aligned(pre_b, we))
+        return fail(MOE_ERR_ARG, "a weight is not aligned to its type");
+    if ((post_b && c.post != MOE_NORM_LAYER) || (pre_b && c.pre != MOE_NORM_LAYER))
+        return fail(MOE_ERR_ARG, "a bias goes with MOE_NORM_LAYER");
+    if ((post_w && !c.post) || (pre_w && !c.pre)) return fail(MOE_ERR_ARG, "a weight without its norm");
+    if (c.rows > 0 && (gate != nullptr) != (c.gate_rows > 0)) return fail(MOE_ERR_ARG, "gate goes with gate_rows=%lld", (long long)c.gate_rows);
+    return MOE_OK;
+}
+
+int warps_for(int d, int values) { return (d + 32 * values - 1) / (32 * values); }
+
+RnShape shape_of(const moe_residual_norm_config& c, int warps, int threads, int vec) {
+    RnShape s;
+    s.rows = c.rows;
+    s.gate_rows = c.gate_rows < c.rows ? c.gate_rows : c.rows;  // of one gate for all rows, as many as there are
+    s.chunk = 0;
+    s.d = c.d;
+    s.warps = warps;
+    s.groups = warps * 32 < threads ? threads / (warps * 32) : 1;
+    s.pieces = (c.d + warps * 32 * vec - 1) / (warps * 32 * vec);
+    s.slots = 1;
+    s.post = c.post, s.pre = c.pre;
+    s.eps = c.eps;
+    s.inv_d = 1.0f / (float)c.d;
+    s.res = c.residual_scale, s.branch = c.branch_scale;
+    return s;
+}
+
+bool full_of(const moe_residual_norm_config& c) { return c.post == MOE_NORM_LAYER || c.pre == MOE_NORM_LAYER; }
+bool grouped_of(const moe_residual_norm_config& c) { return c.gate_rows > 0 && c.gate_rows < c.rows; }
+
+// Backward: CTAs, and the consecutive rows of each group of warps.
+RnShape backward_shape(const moe_residual_norm_config& c, int vec, int sms, int* ctas) {
+    const int warps = warps_for(c.d, rn_backward_values(c.d));
+    RnShape s = shape_of(c, warps, 256, vec);
+    const int64_t most = (int64_t)sms * (s.warps * s.groups > 8 ? 1 : 2) * s.groups;
+    const int64_t workers = c.rows < most ? c.rows : most;
+    s.chunk = workers ? (c.rows + workers - 1) / workers : 1;
+    const int64_t used = (c.rows + s.chunk - 1) / s.chunk;
+    *ctas = (int)((used + s.groups - 1) / s.groups);
+    return s;
+}
+size_t part_bytes(const moe_residual_norm_config& c, int ctas) { return (size_t)ctas * (full_of(c) ? 4 : 2) * c.d * 4; }
+size_t gpart_bytes(const moe_residual_norm_config& c, int workers) { return grouped_of(c) ? (size_t)workers * 2 * c.d * 4 : 0; }  // and gsum's
+
+// f(T(), Int<VEC>()) for the config's type and piece width.
+template <typename F>
+cudaError_t dispatch(int dtype, int vec, F f) {
+    if (dtype == MOE_DTYPE_F32) return vec == 4 ? f(float(), Int<4>()) : f(float(), Int<1>());
+    if (dtype == MOE_DTYPE_BF16) return vec == 8 ? f(__nv_bfloat16(), Int<8>()) : f(__nv_bfloat16(), Int<1>());
+    return vec == 8 ? f(__half(), Int<8>()) : f(__half(), Int<1>());
+}
+
+constexpr size_t RN_FWD_SMEM = 220 * 1024;
+
+}  // namespace
+}  // namespace moe
+
+using namespace moe;
+
+extern "C" {
+
+MOE_API int moe_residual_norm_forward(const moe_residual_norm_config* c, const void* x, const void* u, const void* post_w,
+                                      const void* post_b, const void* gate, const void* pre_w, const void* pre_b, void* h,
+                                      void* z, float* post_stats, float* pre_stats, void* stream) {
+    clear_error();
+    int rc = check(c);
+    if (rc) return rc;
+    if ((rc = check_weights(*c, post_w, post_b, gate, pre_w, pre_b))) return rc;
+    if (c->rows == 0) return MOE_OK;
+    if (!x || (!h && !z)) return fail(MOE_ERR_ARG, "x is NULL, or both outputs are");
+    if (!u && (c->post || c->gate_rows)) return fail(MOE_ERR_ARG, "a post norm or a gate without u");
+    if ((z != nullptr) != (c->pre != MOE_NORM_NONE)) return fail(MOE_ERR_ARG, "z goes with a pre norm");
+    const size_t e = dtype_size(c->dtype), bytes = (size_t)c->rows * c->d * e;
+    if (!aligned(x, e) || !aligned(u, e) || !aligned(h, e) || !aligned(z, e) || !aligned(post_stats, 8) || !aligned(pre_stats, 8))
+        return fail(MOE_ERR_ARG, "a pointer is not aligned (the statistics to 8 bytes, the others to their type)");
+    if (!apart_or_same(h, x, bytes) || !apart_or_same(h, u, bytes) || !apart_or_same(z, x, bytes) ||
+        !apart_or_same(z, u, bytes) || !apart(h, z, bytes))
+        return fail(MOE_ERR_ARG, "an output shares memory with another, or with part of an input");
+    DeviceInfo di;
+    if ((rc = check_device(&di))) return rc;
+    const int vec = vector_width(*c, x, u, h, z);
+    // 64 bytes of a row a thread (four pieces), in more warps where there are too few rows to fill the device
+    int values = 64 / (int)e;
+    while (warps_for(c->d, values) > RN_FWD_THREADS / 32) values *= 2;
+    while (values > 16 / (int)e && (c->d <= 32 * values / 2 || c->rows * warps_for(c->d, values) < 16 * di.sms) &&
+           warps_for(c->d, values / 2) <= RN_FWD_THREADS / 32)
+        values /= 2;
+    RnShape s = shape_of(*c, warps_for(c->d, values), RN_FWD_THREADS, vec);
+    const int threads = 32 * s.warps * s.groups;
+    const size_t slot = (size_t)threads * s.pieces * vec * e * 2;
+    // as many CTAs as find room with two slots each, up to three
+    s.slots = 2 * slot <= RN_FWD_SMEM ? 2 : 1;
+    const int64_t n = (c->rows + s.groups - 1) / s.groups;
+    int per_sm = (int)(RN_FWD_SMEM / (s.slots * slot));
+    if (per_sm > 3) per_sm = 3;
+    const int64_t most = (int64_t)di.sms * per_sm;
+    const dim3 grid((unsigned)(n < most ? n : most)), block(threads);
+    const RnWeights w = weights_of(*c, vec, post_w, post_b, gate, pre_w, pre_b);
+    const cudaError_t err = dispatch(c->dtype, vec, [&](auto type, auto width) {
+        typedef decltype(type) T;
+        constexpr auto kernel = &rn_forward_kernel<T, decltype(width)::value>;
+        const cudaError_t e0 = allow_smem<kernel>(RN_FWD_SMEM);
+        if (e0 != cudaSuccess) return e0;
+        return launch_k(kernel, grid, block, s.slots * slot, static_cast<cudaStream_t>(stream), true, s,
+                        static_cast<const T*>(x), static_cast<const T*>(u), w, static_cast<T*>(h), static_cast<T*>(z),
+                        reinterpret_cast<float2*>(post_stats), reinterpret_cast<float2*>(pre_stats));
+    });
+    return err == cudaSuccess ? MOE_OK : cuda_fail(err, "residual norm launch");
+}
+
+MOE_API int moe_residual_norm_workspace_size(const moe_residual_norm_config* c, size_t* bytes) {
+    clear_error();
+    const int rc = check(c);
+    if (rc) return rc;
+    if (!bytes) return fail(MOE_ERR_ARG, "bytes is NULL");
+    size_t most = 16;
+    for (int vec : {1, (int)(16 / dtype_size(c->dtype))}) {
+        int ctas;
+        const RnShape s = backward_shape(*c, vec, RN_MAX_SMS, &ctas);
+        const size_t need = part_bytes(*c, ctas) + 2 * gpart_bytes(*c, ctas * s.groups);
+        if (need > most) most = need;
+    }
+    *bytes = most;
+    return MOE_OK;
+}
+
+MOE_API int moe_residual_norm_backward(const moe_residual_norm_config* c, const void* dz, const void* dh, const void* u,
+                                       const void* h, const void* post_w, const void* post_b, const void* gate,
+                                       const void* pre_w, const float* post_stats, const float* pre_stats, void* dx,
+                                       void* du, void* dpost_w, void* dpost_b, void* dgate, void* dpre_w, void* dpre_b,
+                                       void* ws, size_t ws_bytes, void* stream) {
+    clear_error();
+    int rc = check(c);
+    if (rc) return rc;
+    if ((rc = check_weights(*c, post_w, post_b, gate, pre_w, nullptr))) return rc;
+    const size_t e = dtype_size(c->dtype), we = dtype_size(c->wdtype), bytes = (size_t)c->rows * c->d * e;
+    void* const grads[5] = {dpost_w, dpost_b, dgate, dpre_w, dpre_b};
+    const bool there[5] = {c->post != 0, c->post == MOE_NORM_LAYER, c->gate_rows > 0, c->pre != 0, c->pre == MOE_NORM_LAYER};
+    bool any = false;
+    for (int i = 0; i < 5; ++i) {
+        if (grads[i] && !there[i]) return fail(MOE_ERR_ARG, "the gradient of a weight, bias or gate that the config lacks");
+        if (!aligned(grads[i], we)) return fail(MOE_ERR_ARG, "a weight's gradient is not aligned to its type");
+        any |= grads[i] != nullptr;
+    }
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    DeviceInfo di;
+    if (c->rows == 0) {
+        if (!any) return MOE_OK;
+        if ((rc = check_device(&di))) return rc;
+        for (int i = 0; i < 5; ++i) {
+            const cudaError_t err = grads[i] && i != 2 ? cudaMemsetAsync(grads[i], 0, we * c->d, st) : cudaSuccess;
+            if (err != cudaSuccess) return cuda_fail(err, "clearing the weights' gradients");
+        }
+        return MOE_OK;
+    }
+    const bool uses_u = c->post || c->gate_rows;
+    if (!dx) return fail(MOE_ERR_ARG, "dx is NULL");
+    if (c->pre ? !dz || !h || !pre_stats : !!dz) return fail(MOE_ERR_ARG, "dz, h and pre_stats go with a pre norm");
+    if (!c->pre && !dh) return fail(MOE_ERR_ARG, "neither dz nor dh");
+    if ((uses_u && !u) || (c->post && !post_stats)) return fail(MOE_ERR_ARG, "u or post_stats is NULL");
+    if (!aligned(dz, e) || !aligned(dh, e) || !aligned(u, e) || !aligned(h, e) || !aligned(dx, e) || !aligned(du, e) ||
+        !aligned(post_stats, 8) || !aligned(pre_stats, 8))
+        return fail(MOE_ERR_ARG, "a pointer is not aligned (the statistics to 8 bytes, the others to their type)");
+    for (const void* in : {dz, dh, u, h})
+        if (!apart_or_same(dx, in, bytes) || !apart_or_same(du, in, bytes))
+            return fail(MOE_ERR_ARG, "dx or du shares memory with part of an input");
+    if (!apart(dx, du, bytes)) return fail(MOE_ERR_ARG, "dx and du share memory");
+    if ((rc = check_device(&di))) return rc;
+    const int vec = vector_width(*c, dz, dh, uses_u ? u : nullptr, c->pre ? h : nullptr, dx, du);
+    int ctas;
+    const RnShape s = backward_shape(*c, vec, di.sms, &ctas);
+    const bool full = full_of(*c), grouped = grouped_of(*c);
+    float *part = nullptr, *gpart = nullptr, *gsum = nullptr;
+    if (any) {
+        const size_t p = part_bytes(*c, ctas), gp = gpart_bytes(*c, ctas * s.groups), need = p + 2 * gp;
+        if (!ws) return fail(MOE_ERR_ARG, "workspace is NULL");
+        if (!aligned(ws, 16)) return fail(MOE_ERR_ARG, "workspace must be 16-byte aligned");
+        if (ws_bytes < need) return fail(MOE_ERR_WORKSPACE, "workspace has %zu bytes, needs %zu", ws_bytes, need);
+        part = static_cast<float*>(ws);
+        gpart = part + p / 4;
+        gsum = gpart + gp / 4;
+    }
+    const RnWeights w = weights_of(*c, vec, post_w, post_b, gate, pre_w, nullptr);
+    const RnBackward b{c->pre ? dz : nullptr, dh, uses_u ? u : nullptr, c->pre ? h : nullptr,
+                       reinterpret_cast<const float2*>(post_stats), reinterpret_cast<const float2*>(pre_stats), dx, du, part,
+                       gpart, gsum, dgate};
+    const cudaError_t err = dispatch(c->dtype, 1, [&](auto type, auto) {
+        typedef decltype(type) T;
+        const cudaError_t e0 = launch_residual_backward<T>(s, w, b, vec, full, grouped, ctas, st);
+        if (e0 != cudaSuccess || !any) return e0;
+        const RnReduce a{part, gpart, ctas, c->d, full, grouped, w.f32, post_w, post_b, gate, dpost_w, dpost_b, dgate, dpre_w,
+                         dpre_b, c->rows, c->gate_rows, s.chunk};
+        int gates = 0;
+        if (grouped && dgate) {
+            const int64_t g = (c->rows + c->gate_rows - 1) / c->gate_rows;
+            gates = (int)(g < 64 ? g : 64);
+        }
+        return launch_k(rn_reduce_kernel<T>, dim3((c->d + RN_RED_COLS - 1) / RN_RED_COLS, 2 + gates),
+                        dim3(RN_RED_COLS * RN_RED_ROWS), 0, st, true, a);
+    });
+    return err == cudaSuccess ? MOE_OK : cuda_fail(err, "residual norm backward launch");
+}
+
+}  // extern "C"
