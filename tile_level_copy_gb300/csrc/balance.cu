@@ -209,21 +209,9 @@ struct BlEnd {
     float* saved;
 };
 
-__device__ __forceinline__ double cta_sum(double a, double* red) {  // all threads get it
-#pragma unroll
-    for (int o = 16; o; o >>= 1) a += __shfl_xor_sync(0xffffffffu, a, o);
-    __syncthreads();
-    if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = a;
-    __syncthreads();
-    a = 0.0;
-    for (int i = 0; i < BL_END_WARPS; ++i) a += red[i];
-    return a;
-}
-
 __global__ void __launch_bounds__(BL_END_WARPS * 32) balance_end_kernel(BlShape s, BlSpace w, BlEnd f) {
     __shared__ float ps[BL_END_WARPS][32], zs[BL_END_WARPS];
     __shared__ int cs[BL_END_WARPS][32], ns[BL_END_WARPS];
-    __shared__ double red[BL_END_WARPS];
     __shared__ bool am_last;
     griddep_wait();
     griddep_launch();
@@ -288,7 +276,8 @@ __global__ void __launch_bounds__(BL_END_WARPS * 32) balance_end_kernel(BlShape 
     __syncthreads();
     if (!am_last) return;
     __threadfence();
-    double v = 0.0, z = 0.0, n = 0.0, used = 0.0;
+    float v = 0.f, z = 0.f;
+    int n = 0, used = 0;
     for (int64_t i = threadIdx.x; i < jobs; i += blockDim.x) v += __ldcg(w.value + i);
     for (int i = threadIdx.x; i < s.S; i += blockDim.x) {
         const int k = __ldcg(w.n + i);
@@ -296,19 +285,31 @@ __global__ void __launch_bounds__(BL_END_WARPS * 32) balance_end_kernel(BlShape 
         n += k;
         used += k > 0;
     }
-    v = cta_sum(v, red);
-    z = cta_sum(z, red);
-    n = cta_sum(n, red);
-    used = cta_sum(used, red);
-    if (threadIdx.x) return;
-    const double bal = used > 0 ? v / used : 0.0, zl = n > 0 ? z / n : 0.0;
+    v = warp_sum(v);
+    z = warp_sum(z);
+    n = __reduce_add_sync(0xffffffffu, n);
+    used = __reduce_add_sync(0xffffffffu, used);
+    if (lane == 0) {
+        ps[warp][0] = v;
+        zs[warp] = z;
+        ns[warp] = n;
+        cs[warp][0] = used;
+    }
+    __syncthreads();
+    if (warp) return;
+    v = warp_sum(ps[lane][0]);
+    z = warp_sum(zs[lane]);
+    n = __reduce_add_sync(0xffffffffu, ns[lane]);
+    used = __reduce_add_sync(0xffffffffu, cs[lane][0]);
+    if (lane) return;
+    const float bal = used ? v / (float)used : 0.f, zl = n ? z / (float)n : 0.f;
     // (a loss without weight leaves the sum alone, infinite or not)
-    f.loss[0] = (float)((f.wb != 0.f ? f.wb * bal : 0.0) + (f.wz != 0.f ? f.wz * zl : 0.0));
-    f.loss[1] = (float)bal;
-    f.loss[2] = (float)zl;
+    f.loss[0] = (f.wb != 0.f ? f.wb * bal : 0.f) + (f.wz != 0.f ? f.wz * zl : 0.f);
+    f.loss[1] = bal;
+    f.loss[2] = zl;
     if (f.saved) {
-        f.saved[0] = used > 0 ? (float)(f.wb / used) : 0.f;
-        f.saved[1] = n > 0 ? (float)(2.0 * f.wz / n) : 0.f;
+        f.saved[0] = used ? f.wb / (float)used : 0.f;
+        f.saved[1] = n ? 2.f * f.wz / (float)n : 0.f;
     }
 }
 

@@ -20,66 +20,108 @@
 namespace moe {
 namespace {
 
-constexpr int RB_MOST = 512;
+// CTAs on a SM
+__host__ __device__ constexpr int rb_ctas(int values, int threads) { return threads > 256 ? 1 : values == 8 ? 3 : 2; }
 constexpr size_t RB_SMEM_MOST = 224 * 1024;
 
 
+// Two neighbouring values of a piece of 16-bit or 32-bit values, or its only one, as fp32; and back. (By words: pieces of
+// two 16-bit values that are copied one by one cost a byte permutation each, a quarter of the kernel's instructions.)
+template <typename T, int VEC>
+__device__ __forceinline__ typename Lanes<VEC>::V unit_of(const Pack<T, VEC>& p, int j) {
+    if constexpr (VEC == 1) {
+        return num(p.v[0]);
+    } else if constexpr (sizeof(T) == 4) {
+        return pair(p.v[2 * j], p.v[2 * j + 1]);
+    } else {
+        const uint32_t w = reinterpret_cast<const uint32_t*>(&p)[j];
+        if constexpr (std::is_same_v<T, __nv_bfloat16>) {
+            return pair(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
+        } else {
+            const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w));
+            return pair(f.x, f.y);
+        }
+    }
+}
+template <typename T, int VEC>
+__device__ __forceinline__ void put_unit(Pack<T, VEC>& p, int j, typename Lanes<VEC>::V v) {
+    if constexpr (VEC == 1) {
+        put(p.v[0], v);
+    } else {
+        const float2 f = split(v);
+        if constexpr (sizeof(T) == 4) {
+            p.v[2 * j] = f.x;
+            p.v[2 * j + 1] = f.y;
+        } else if constexpr (std::is_same_v<T, __nv_bfloat16>) {
+            reinterpret_cast<uint32_t*>(&p)[j] = pack_bf16x2(f.x, f.y);
+        } else {
+            const __half2 h = __floats2half2_rn(f.x, f.y);
+            reinterpret_cast<uint32_t*>(&p)[j] = *reinterpret_cast<const uint32_t*>(&h);
+        }
+    }
+}
+
 // DIRECT: rows are read from global memory in both passes over them (2-byte pieces, rows too wide for a slot).
-template <typename T, int VEC, int NV, bool FULL, bool DIRECT>
-__global__ void __launch_bounds__(RB_MOST, 1) rn_backward_kernel(RnShape s, RnWeights w, RnBackward b, int grouped, int wbytes) {
-    constexpr int U = VEC < 2 ? VEC : 2;  // values worked on at a time, a unit (4 spill more)
-    typedef typename Lanes<U>::V V;
+// THREADS: at most so many in a CTA, and the stride of a thread's places in shared memory, so that they have fixed
+// distances. Rows that are not there count as zeros, a norm that is not there as one with mean 0 and rstd 1 whose
+// sums are left out: the same instructions serve every kind.
+template <typename T, int VEC, int NV, int THREADS, bool FULL, bool DIRECT>
+__global__ void __launch_bounds__(THREADS, rb_ctas(NV, THREADS)) rn_backward_kernel(RnShape s, RnWeights w, RnBackward b, int grouped) {
+    typedef typename Lanes<VEC>::V V;  // a unit: two values, or one
     typedef Pack<T, VEC> P;
+    constexpr int U = VEC < 2 ? 1 : 2, NP = NV / VEC, UN = VEC / U, NU = NP * UN, K = FULL ? 8 : 4, A = FULL ? 7 : 3;
     typedef Pack<float, U> F;
-    constexpr int NP = NV / VEC, UN = VEC / U, NU = NP * UN, N = Lanes<U>::N, K = FULL ? 8 : 4;
-    __shared__ float red[2][16 * K];
+    __shared__ float red[2][THREADS / 32 * K];
     extern __shared__ __align__(16) uint8_t rb_smem[];
     griddep_wait();
     griddep_launch();
     const int tpr = s.warps * 32, t = threadIdx.x % tpr, group = threadIdx.x / tpr, lane = threadIdx.x & 31;
-    const int threads = blockDim.x, step = tpr * VEC, c0 = t * VEC;
+    const int step = tpr * VEC, c0 = t * VEC;
     const int np = c0 < s.d ? min(NP, (s.d - c0 + step - 1) / step) : 0;
     const bool pre = s.pre != 0, post = s.post != 0, lay1 = s.post == MOE_NORM_LAYER, lay2 = s.pre == MOE_NORM_LAYER;
-    const T *const gz = static_cast<const T*>(b.dz), *const gh = static_cast<const T*>(b.h);
-    const T *const gd = static_cast<const T*>(b.dh), *const gu = static_cast<const T*>(b.u);
+    const T* const rows[4] = {static_cast<const T*>(b.dz), static_cast<const T*>(b.h), static_cast<const T*>(b.dh),
+                              static_cast<const T*>(b.u)};
     T *const dx = static_cast<T*>(b.dx), *const du = static_cast<T*>(b.du);
     const int64_t worker = (int64_t)blockIdx.x * s.groups + group;
     const int64_t first = worker * s.chunk, last = first + s.chunk < s.rows ? first + s.chunk : s.rows;
 
     // this thread's units of w2 and of k
-    F* const wsm = reinterpret_cast<F*>(rb_smem) + threadIdx.x;
-    auto at_w2 = [&](int j) { return wsm + j * threads; };
-    auto at_k = [&](int j) { return wsm + (NU + j) * threads; };
+    V* const wsm = reinterpret_cast<V*>(rb_smem) + threadIdx.x;
+    auto at_w2 = [&](int j) { return wsm + j * THREADS; };
+    auto at_k = [&](int j) { return wsm + (NU + j) * THREADS; };
     auto column = [&](int j) { return c0 + (j / UN) * step + (j % UN) * U; };
     // with a gate for each group of rows: dw1 and db1 so far
-    auto at_sum = [&](int n, int j) { return reinterpret_cast<F*>(b.gsum + (2 * worker + n) * s.d + column(j)); };
-    // tensors in a slot, one behind the other: dz, h, dh, u, as far as they are there
-    const int at_d = pre ? 2 : 0, at_u = at_d + (gd ? 1 : 0), tensors = at_u + (gu ? 1 : 0);
-    P* const slot = reinterpret_cast<P*>(rb_smem + wbytes) + threadIdx.x;
-    auto piece = [&](int stage, int tensor, int q) { return slot + ((stage * tensors + tensor) * s.pieces + q) * threads; };
+    auto at_sum = [&](int n, int j) { return reinterpret_cast<V*>(b.gsum + (2 * worker + n) * s.d + column(j)); };
+    // a slot: pieces of the four tensors
+    P* const slots = reinterpret_cast<P*>(rb_smem + 2 * NU * THREADS * sizeof(V)) + threadIdx.x;
+    auto piece = [&](int stage, int tensor, int q) { return slots + stage * (4 * NP * THREADS) + (tensor * NP + q) * THREADS; };
     auto issue = [&](int64_t r, int stage) {
         if (DIRECT) return;
         if (r < last) {
             const int64_t at = r * s.d + c0;
 #pragma unroll
-            for (int q = 0; q < NP; ++q) {
-                if (q >= np) break;
-                if (pre) {
-                    fetch(piece(stage, 0, q), reinterpret_cast<const P*>(gz + at + q * step));
-                    fetch(piece(stage, 1, q), reinterpret_cast<const P*>(gh + at + q * step));
+            for (int n = 0; n < 4; ++n) {
+                if (!rows[n]) continue;
+#pragma unroll
+                for (int q = 0; q < NP; ++q) {
+                    if (q >= np) break;
+                    fetch(piece(stage, n, q), reinterpret_cast<const P*>(rows[n] + at + q * step));
                 }
-                if (gd) fetch(piece(stage, at_d, q), reinterpret_cast<const P*>(gd + at + q * step));
-                if (gu) fetch(piece(stage, at_u, q), reinterpret_cast<const P*>(gu + at + q * step));
             }
         }
         asm volatile("cp.async.commit_group;" ::: "memory");
     };
-    auto take = [&](const T* from, int stage, int tensor, int64_t at, int q) {
-        return DIRECT ? *reinterpret_cast<const P*>(from + at + q * step) : *piece(stage, tensor, q);
+    auto take = [&](int n, int stage, int64_t at, int q) {
+        if (!DIRECT) return *piece(stage, n, q);
+        P p;
+        if (rows[n]) p = *reinterpret_cast<const P*>(rows[n] + at + q * step);
+        else memset(&p, 0, sizeof(p));
+        return p;
     };
-    auto unit = [](const P& p, int j) { return *reinterpret_cast<const Pack<T, U>*>(&p.v[j * U]); };
-    // w2, and k of the rows that share gate g
+    // w2, and k of the rows that share gate g; the sum of this thread's k
+    float ksum = 0.f;
     auto make_w = [&](int64_t g) {
+        ksum = 0.f;
 #pragma unroll 1
         for (int j = 0; j < np * UN; ++j) {
             F f, k;
@@ -88,12 +130,21 @@ __global__ void __launch_bounds__(RB_MOST, 1) rn_backward_kernel(RnShape s, RnWe
                 const int col = column(j) + i;
                 f.v[i] = value_at<T>(w.pre_w, w.f32, col, 1.f);
                 k.v[i] = value_at<T>(w.post_w, w.f32, col, 1.f) * value_at<T>(w.gate, w.f32, g * s.d + col, 1.f);
+                ksum += k.v[i];
             }
-            *at_w2(j) = f;
-            *at_k(j) = k;
+            *at_w2(j) = *reinterpret_cast<const V*>(&f);
+            *at_k(j) = *reinterpret_cast<const V*>(&k);
         }
     };
 
+    if (!DIRECT) {
+        P zero;
+        memset(&zero, 0, sizeof(zero));
+        for (int n = 0; n < 4; ++n)
+            if (!rows[n])
+                for (int k = 0; k < s.slots; ++k)
+                    for (int q = 0; q < NP; ++q) *piece(k, n, q) = zero;
+    }
     int flip = 0, stage = 0;
     for (int k = 0; k < s.slots - 1; ++k) issue(first + k, k);
     const float2 plain = make_float2(0.f, 1.f);
@@ -109,23 +160,18 @@ __global__ void __launch_bounds__(RB_MOST, 1) rn_backward_kernel(RnShape s, RnWe
         if (grouped && b.part) {
 #pragma unroll 1
             for (int j = 0; j < np * UN; ++j) {
-                F zero;
-#pragma unroll
-                for (int i = 0; i < U; ++i) zero.v[i] = 0.f;
-                *at_sum(0, j) = zero;
-                if (FULL) *at_sum(1, j) = zero;
+                *at_sum(0, j) = both<V>(0.f);
+                if (FULL) *at_sum(1, j) = both<V>(0.f);
             }
         }
     }
     // sums of a thread's columns: dw2, db2, S, B
-    V sp[NU][N], sq[FULL ? NU : 1][N], s1[NU][N], s2[FULL ? NU : 1][N];
+    V sp[NU], sq[FULL ? NU : 1], s1[NU], s2[FULL ? NU : 1];
 #pragma unroll
-    for (int j = 0; j < NU; ++j)
-#pragma unroll
-        for (int i = 0; i < N; ++i) {
-            sp[j][i] = s1[j][i] = both<V>(0.f);
-            if (FULL) sq[FULL ? j : 0][i] = s2[FULL ? j : 0][i] = both<V>(0.f);
-        }
+    for (int j = 0; j < NU; ++j) {
+        sp[j] = s1[j] = both<V>(0.f);
+        if (FULL) sq[FULL ? j : 0] = s2[FULL ? j : 0] = both<V>(0.f);
+    }
 
     const V branch = both<V>(s.branch), res = both<V>(s.res);
     for (int64_t r = first; r < last; ++r) {
@@ -135,78 +181,36 @@ __global__ void __launch_bounds__(RB_MOST, 1) rn_backward_kernel(RnShape s, RnWe
         if (pre && r + 1 < last) next2 = b.pre_stats[r + 1];
         if (!DIRECT) fetched(s.slots - 1);
         const int64_t at = r * s.d + c0;
-        const V neg1 = both<V>(-st1.x), rs1 = both<V>(st1.y), neg2 = both<V>(-st2.x), rs2 = both<V>(st2.y);
-        // e and hn of a unit, dz in z, gy = dz w2 in y
-        auto above = [&](const P& pz, const P& ph, const P& pd, int j, V (&e)[N], V (&hn)[N], V (&z)[N], V (&y)[N]) {
-            if (gd) {
-                widen(unit(pd, j % UN), e);
-            } else {
-#pragma unroll
-                for (int i = 0; i < N; ++i) e[i] = both<V>(0.f);
-            }
-            if (pre) {
-                widen(unit(ph, j % UN), hn);
-                widen(unit(pz, j % UN), z);
-                widen(*at_w2(j), y);
-#pragma unroll
-                for (int i = 0; i < N; ++i) {
-                    hn[i] = mul_(add_(hn[i], neg2), rs2);
-                    y[i] = mul_(z[i], y[i]);
-                    e[i] = fma_(rs2, y[i], e[i]);
-                }
-            }
-        };
+        const V neg1 = both<V>(-st1.x * st1.y), rs1 = both<V>(st1.y), neg2 = both<V>(-st2.x * st2.y), rs2 = both<V>(st2.y);
         float v[K];
         {
-            V a[K];
+            V a[A];
 #pragma unroll
-            for (int i = 0; i < K; ++i) a[i] = both<V>(0.f);
+            for (int i = 0; i < A; ++i) a[i] = both<V>(0.f);
 #pragma unroll
             for (int q = 0; q < NP; ++q) {
                 if (q >= np) break;
-                P pz, ph, pd, pu;
-                if (pre) {
-                    pz = take(gz, stage, 0, at, q);
-                    ph = take(gh, stage, 1, at, q);
-                }
-                if (gd) pd = take(gd, stage, at_d, at, q);
-                if (post) pu = take(gu, stage, at_u, at, q);
+                const P pz = take(0, stage, at, q), ph = take(1, stage, at, q), pd = take(2, stage, at, q), pu = take(3, stage, at, q);
 #pragma unroll
-                for (int j = q * UN; j < (q + 1) * UN; ++j) {
-                    V e[N], hn[N], z[N], y[N];
-                    above(pz, ph, pd, j, e, hn, z, y);
-                    if (pre) {
-#pragma unroll
-                        for (int i = 0; i < N; ++i) {
-                            sp[j][i] = fma_(z[i], hn[i], sp[j][i]);
-                            a[0] = fma_(y[i], hn[i], a[0]);
-                            if (FULL) {
-                                sq[FULL ? j : 0][i] = add_(sq[FULL ? j : 0][i], z[i]);
-                                a[3] = add_(a[3], y[i]);
-                            }
-                        }
-                    }
-                    if (post) {
-                        V un[N], k[N];
-                        widen(unit(pu, j % UN), un);
-                        widen(*at_k(j), k);
-#pragma unroll
-                        for (int i = 0; i < N; ++i) {
-                            const V ku = mul_(k[i], mul_(add_(un[i], neg1), rs1));
-                            a[1] = fma_(ku, e[i], a[1]);
-                            if (pre) a[2] = fma_(ku, hn[i], a[2]);
-                            if (FULL) {
-                                a[4] = fma_(k[i], e[i], a[4]);
-                                a[5] = add_(a[5], k[i]);
-                                a[6] = add_(a[6], ku);
-                                if (pre) a[7] = fma_(k[i], hn[i], a[7]);
-                            }
-                        }
+                for (int i = 0; i < UN; ++i) {
+                    const int j = q * UN + i;
+                    const V z = unit_of(pz, i), hn = fma_(unit_of(ph, i), rs2, neg2), gy = mul_(z, *at_w2(j));
+                    const V e = fma_(rs2, gy, unit_of(pd, i)), k = *at_k(j), ku = mul_(k, fma_(unit_of(pu, i), rs1, neg1));
+                    sp[j] = fma_(z, hn, sp[j]);
+                    a[0] = fma_(gy, hn, a[0]);
+                    a[1] = fma_(ku, e, a[1]);
+                    a[2] = fma_(ku, hn, a[2]);
+                    if (FULL) {
+                        sq[FULL ? j : 0] = add_(sq[FULL ? j : 0], z);
+                        a[FULL ? 3 : 0] = add_(a[FULL ? 3 : 0], gy);
+                        a[FULL ? 4 : 0] = fma_(k, e, a[FULL ? 4 : 0]);
+                        a[FULL ? 5 : 0] = add_(a[FULL ? 5 : 0], ku);
+                        a[FULL ? 6 : 0] = fma_(k, hn, a[FULL ? 6 : 0]);
                     }
                 }
             }
 #pragma unroll
-            for (int i = 0; i < K; ++i) v[i] = total(a[i]);
+            for (int i = 0; i < K; ++i) v[i] = i < A ? total(a[i < A ? i : 0]) : ksum;
         }
         // sums over the row: warp by shuffles, warps through shared memory, [value][warp]
         float c[K];
@@ -229,62 +233,35 @@ __global__ void __launch_bounds__(RB_MOST, 1) rn_backward_kernel(RnShape s, RnWe
         }
         // dt = e - p0 - hn p1; m0, m1: the sums of k dt and of k un dt
         const float p1 = pre ? st2.y * c[0] * s.inv_d : 0.f, p0 = FULL && lay2 ? st2.y * c[FULL ? 3 : 0] * s.inv_d : 0.f;
-        float m1 = c[1] - p1 * c[2], m0 = 0.f;
+        float m1 = post ? c[1] - p1 * c[2] : 0.f, m0 = 0.f;
         if (FULL) {
-            m1 -= p0 * c[FULL ? 6 : 0];
-            if (lay1) m0 = c[FULL ? 4 : 0] - p0 * c[FULL ? 5 : 0] - p1 * c[FULL ? 7 : 0];
+            if (post) m1 -= p0 * c[FULL ? 5 : 0];
+            if (lay1) m0 = c[FULL ? 4 : 0] - p0 * c[FULL ? 7 : 0] - p1 * c[FULL ? 6 : 0];
         }
         const V n0 = both<V>(-p0), n1 = both<V>(-p1), k0 = both<V>(-m0 * s.inv_d), k1 = both<V>(-m1 * s.inv_d);
         const V out1 = both<V>(s.branch * st1.y);
 #pragma unroll
         for (int q = 0; q < NP; ++q) {
             if (q >= np) break;
-            P pz, ph, pd, pu, px;
-            if (pre) {
-                pz = take(gz, stage, 0, at, q);
-                ph = take(gh, stage, 1, at, q);
-            }
-            if (gd) pd = take(gd, stage, at_d, at, q);
-            if (gu) pu = take(gu, stage, at_u, at, q);
+            const P pz = take(0, stage, at, q), ph = take(1, stage, at, q), pd = take(2, stage, at, q), pu = take(3, stage, at, q);
+            P px, pv;
 #pragma unroll
-            for (int j = q * UN; j < (q + 1) * UN; ++j) {
-                V e[N], hn[N], f[N], y[N];
-                above(pz, ph, pd, j, e, hn, f, y);
-                if (pre) {
-#pragma unroll
-                    for (int i = 0; i < N; ++i) {
-                        if (FULL) e[i] = add_(e[i], n0);
-                        e[i] = fma_(hn[i], n1, e[i]);
-                    }
-                }
-#pragma unroll
-                for (int i = 0; i < N; ++i) f[i] = mul_(e[i], res);
-                *reinterpret_cast<Pack<T, U>*>(&px.v[(j % UN) * U]) = narrow<T, U>(f);
-                if (gu) {
-                    V un[N], k[N];
-                    widen(unit(pu, j % UN), un);
-                    widen(*at_k(j), k);
-#pragma unroll
-                    for (int i = 0; i < N; ++i) {
-                        if (post) un[i] = mul_(add_(un[i], neg1), rs1);
-                        const V d = mul_(e[i], branch);
-                        s1[j][i] = fma_(d, un[i], s1[j][i]);
-                        if (FULL) s2[FULL ? j : 0][i] = add_(s2[FULL ? j : 0][i], d);
-                        if (post) {
-                            e[i] = fma_(e[i], k[i], FULL ? fma_(un[i], k1, k0) : mul_(un[i], k1));
-                            e[i] = mul_(e[i], out1);
-                        } else {
-                            e[i] = mul_(d, k[i]);
-                        }
-                    }
-                } else {
-#pragma unroll
-                    for (int i = 0; i < N; ++i) e[i] = mul_(e[i], branch);
-                }
-                *reinterpret_cast<Pack<T, U>*>(&pu.v[(j % UN) * U]) = narrow<T, U>(e);
+            for (int i = 0; i < UN; ++i) {
+                const int j = q * UN + i;
+                const V hn = fma_(unit_of(ph, i), rs2, neg2), gy = mul_(unit_of(pz, i), *at_w2(j));
+                V e = fma_(rs2, gy, unit_of(pd, i));
+                if (FULL) e = add_(e, n0);
+                e = fma_(hn, n1, e);
+                put_unit(px, i, mul_(e, res));
+                const V un = fma_(unit_of(pu, i), rs1, neg1), d = mul_(e, branch);
+                s1[j] = fma_(d, un, s1[j]);
+                if (FULL) s2[FULL ? j : 0] = add_(s2[FULL ? j : 0], d);
+                V m = k0;  // (0 without a post norm: u may be infinite)
+                if (post) m = FULL ? fma_(un, k1, k0) : mul_(un, k1);
+                put_unit(pv, i, mul_(fma_(e, *at_k(j), m), out1));
             }
             *reinterpret_cast<P*>(dx + at + q * step) = px;
-            if (du) *reinterpret_cast<P*>(du + at + q * step) = pu;
+            if (du) *reinterpret_cast<P*>(du + at + q * step) = pv;
         }
         if (++stage == s.slots) stage = 0;
         if (grouped && (r + 1 == g_end || r + 1 == last)) {
@@ -295,18 +272,20 @@ __global__ void __launch_bounds__(RB_MOST, 1) rn_backward_kernel(RnShape s, RnWe
 #pragma unroll
             for (int j = 0; j < NU; ++j) {
                 if (j / UN >= np) break;
-                *at_k(j) = *reinterpret_cast<const F*>(s1[j]);
-                if (FULL) *at_w2(j) = *reinterpret_cast<const F*>(s2[FULL ? j : 0]);
-#pragma unroll
-                for (int i = 0; i < N; ++i) {
-                    s1[j][i] = both<V>(0.f);
-                    if (FULL) s2[FULL ? j : 0][i] = both<V>(0.f);
-                }
+                *at_k(j) = s1[j];
+                if (FULL) *at_w2(j) = s2[FULL ? j : 0];
+                s1[j] = both<V>(0.f);
+                if (FULL) s2[FULL ? j : 0] = both<V>(0.f);
             }
 #pragma unroll 1
             for (int j = 0; b.part && j < np * UN; ++j) {
-                const F x = *at_k(j), y = FULL ? *at_w2(j) : x;
-                F a = *at_sum(0, j), e = FULL ? *at_sum(1, j) : x;
+                F x, y, a, e;
+                *reinterpret_cast<V*>(&x) = *at_k(j);
+                *reinterpret_cast<V*>(&a) = *at_sum(0, j);
+                if (FULL) {
+                    *reinterpret_cast<V*>(&y) = *at_w2(j);
+                    *reinterpret_cast<V*>(&e) = *at_sum(1, j);
+                }
 #pragma unroll
                 for (int i = 0; i < U; ++i) {
                     const int col = column(j) + i;
@@ -321,8 +300,8 @@ __global__ void __launch_bounds__(RB_MOST, 1) rn_backward_kernel(RnShape s, RnWe
                         else put(static_cast<T*>(b.dgate)[g * s.d + col], out);
                     }
                 }
-                *at_sum(0, j) = a;
-                if (FULL) *at_sum(1, j) = e;
+                *at_sum(0, j) = *reinterpret_cast<const V*>(&a);
+                if (FULL) *at_sum(1, j) = *reinterpret_cast<const V*>(&e);
             }
             if (r + 1 < last) {
                 ++g;
@@ -337,8 +316,8 @@ __global__ void __launch_bounds__(RB_MOST, 1) rn_backward_kernel(RnShape s, RnWe
 #pragma unroll
         for (int j = 0; j < NU; ++j) {
             if (j / UN >= np) break;
-            widen(*at_sum(0, j), s1[j]);
-            if (FULL) widen(*at_sum(1, j), s2[FULL ? j : 0]);
+            s1[j] = *at_sum(0, j);
+            if (FULL) s2[FULL ? j : 0] = *at_sum(1, j);
         }
     }
     // the groups' sums one after another in shared memory, so that the order is the same every time
@@ -354,15 +333,9 @@ __global__ void __launch_bounds__(RB_MOST, 1) rn_backward_kernel(RnShape s, RnWe
                 if (j / UN >= np) break;
 #pragma unroll
                 for (int n = 0; n < SUMS; ++n) {
-                    const V* from = n == 0 ? sp[j] : n == SUMS / 2 ? s1[j] : n == 1 ? sq[FULL ? j : 0] : s2[FULL ? j : 0];
-                    F f = *reinterpret_cast<const F*>(from);
-                    F* const p = reinterpret_cast<F*>(to + n * s.d + column(j));  // d is a multiple of the unit
-                    if (k) {
-                        const F old = *p;
-#pragma unroll
-                        for (int i = 0; i < U; ++i) f.v[i] += old.v[i];
-                    }
-                    *p = f;
+                    const V v = n == 0 ? sp[j] : n == SUMS / 2 ? s1[j] : n == 1 ? sq[FULL ? j : 0] : s2[FULL ? j : 0];
+                    V* const p = reinterpret_cast<V*>(to + n * s.d + column(j));  // d is a multiple of the unit
+                    *p = k ? add_(*p, v) : v;
                 }
             }
         }
@@ -379,29 +352,30 @@ cudaError_t launch_residual_backward(const RnShape& shape, const RnWeights& w, c
                                      bool grouped, int ctas, cudaStream_t st) {
     RnShape s = shape;
     const int threads = 32 * s.warps * s.groups, values = rn_backward_values(s.d);
-    const int tensors = (b.dz ? 2 : 0) + (b.dh ? 1 : 0) + (b.u ? 1 : 0);
-    const size_t slot = (size_t)threads * s.pieces * vec * sizeof(T) * tensors;
-    const size_t wbytes = (size_t)threads * values * 4 * 2;
-    const size_t room = threads > 256 ? RB_SMEM_MOST : RB_SMEM_MOST / 2;  // two CTAs of up to 256 threads a SM
-    const bool direct = vec * sizeof(T) < 4 || values == 32;  // 2-byte pieces cannot be fetched asynchronously
-    s.slots = direct ? 1 : wbytes + 3 * slot <= room ? 3 : wbytes + 2 * slot <= room ? 2 : 1;
-    size_t smem = wbytes + (direct ? 0 : s.slots * slot);
-    if (s.groups > 1 && smem < (size_t)(full ? 4 : 2) * s.d * 4) smem = (size_t)(full ? 4 : 2) * s.d * 4;
-    auto go = [&](auto width, auto columns, auto whole, auto straight) {
-        constexpr auto kernel =
-            &rn_backward_kernel<T, decltype(width)::value, decltype(columns)::value, decltype(whole)::value, decltype(straight)::value>;
+    auto go = [&](auto width, auto columns, auto most, auto whole, auto straight) {
+        constexpr int VEC = decltype(width)::value, NV = decltype(columns)::value, THREADS = decltype(most)::value;
+        constexpr bool DIRECT = decltype(straight)::value;
+        constexpr auto kernel = &rn_backward_kernel<T, VEC, NV, THREADS, decltype(whole)::value, DIRECT>;
+        constexpr size_t weights = (size_t)2 * NV * THREADS * 4, slot = DIRECT ? 0 : (size_t)4 * NV * THREADS * sizeof(T);
+        constexpr size_t room = RB_SMEM_MOST / rb_ctas(NV, THREADS);
+        static_assert(weights + slot <= RB_SMEM_MOST, "room for a row");
+        s.slots = DIRECT ? 1 : weights + 3 * slot <= room ? 3 : weights + 2 * slot <= room ? 2 : 1;
+        size_t smem = weights + s.slots * slot;
+        if (s.groups > 1 && smem < (size_t)(full ? 4 : 2) * s.d * 4) smem = (size_t)(full ? 4 : 2) * s.d * 4;
         const cudaError_t e = allow_smem<kernel>(RB_SMEM_MOST);
         if (e != cudaSuccess) return e;
-        return launch_k(kernel, dim3(ctas), dim3(threads), smem, st, true, s, w, b, (int)grouped, (int)wbytes);
+        return launch_k(kernel, dim3(ctas), dim3(threads), smem, st, true, s, w, b, (int)grouped);
     };
-    auto kinds = [&](auto width, auto columns, auto straight) {
-        return full ? go(width, columns, std::true_type(), straight) : go(width, columns, std::false_type(), straight);
+    auto kinds = [&](auto width, auto columns, auto most, auto straight) {
+        return full ? go(width, columns, most, std::true_type(), straight) : go(width, columns, most, std::false_type(), straight);
     };
     constexpr int VEC = 16 / sizeof(T);
-    if (vec == 1)
-        return values == 32 ? kinds(Int<1>(), Int<32>(), std::true_type())
-                            : kinds(Int<1>(), Int<16>(), std::integral_constant<bool, (sizeof(T) < 4)>());
-    return values == 32 ? kinds(Int<VEC>(), Int<32>(), std::true_type()) : kinds(Int<VEC>(), Int<16>(), std::false_type());
+    typedef std::integral_constant<bool, (sizeof(T) < 4)> Two;  // 2-byte pieces cannot be fetched asynchronously
+    const bool one = vec == 1;
+    if (values == 32) return one ? kinds(Int<1>(), Int<32>(), Int<512>(), std::true_type()) : kinds(Int<VEC>(), Int<32>(), Int<512>(), std::true_type());
+    if (threads > 256) return one ? kinds(Int<1>(), Int<16>(), Int<512>(), Two()) : kinds(Int<VEC>(), Int<16>(), Int<512>(), std::false_type());
+    if (values == 16) return one ? kinds(Int<1>(), Int<16>(), Int<256>(), Two()) : kinds(Int<VEC>(), Int<16>(), Int<256>(), std::false_type());
+    return one ? kinds(Int<1>(), Int<8>(), Int<256>(), Two()) : kinds(Int<VEC>(), Int<8>(), Int<256>(), std::false_type());
 }
 
 }  // namespace moe
