@@ -15,7 +15,7 @@ namespace {
 
 constexpr int RN_FWD_THREADS = 256;
 constexpr int RN_UNROLL = 4;        // pieces worked on at a time
-constexpr int RN_RED_COLS = 32, RN_RED_ROWS = 32;
+constexpr int RN_RED_COLS = 32, RN_RED_ROWS = 32, RN_RED_FLY = 10;
 constexpr int RN_MAX_SMS = 256;
 
 template <typename T, int VEC>
@@ -192,15 +192,23 @@ __global__ void __launch_bounds__(RN_RED_COLS* RN_RED_ROWS) rn_reduce_kernel(RnR
     griddep_launch();
     const int lane = threadIdx.x % RN_RED_COLS, row = threadIdx.x / RN_RED_COLS, c = blockIdx.x * RN_RED_COLS + lane;
     if (blockIdx.y >= 2) {
-        if (c >= a.d || row) return;
         const int64_t gates = (a.rows + a.gate_rows - 1) / a.gate_rows;
         for (int64_t g = blockIdx.y - 2; g < gates; g += gridDim.y - 2) {
             const int64_t from = g * a.gate_rows, to = from + a.gate_rows < a.rows ? from + a.gate_rows : a.rows;
             const int64_t w0 = from / a.chunk, w1 = (to - 1) / a.chunk;
             if (w0 == w1) continue;  // the group of warps wrote it
             float v = 0.f;
-            for (int64_t k = w0; k <= w1; ++k)  // a group of warps' first gate is in its first row of sums
-                v += a.gpart[(2 * k + (k * a.chunk / a.gate_rows == g ? 0 : 1)) * a.d + c];
+            if (c < a.d) {  // only the first group of warps may have begun with an earlier gate
+                for (int64_t k = w0 + row; k <= w1; k += RN_RED_ROWS)
+                    v += a.gpart[(2 * k + (k == w0 && w0 * a.chunk < from ? 1 : 0)) * a.d + c];
+            }
+            __syncthreads();
+            acc[0][row][lane] = v;
+            __syncthreads();
+            if (row || c >= a.d) continue;
+            v = 0.f;
+#pragma unroll
+            for (int q = 0; q < RN_RED_ROWS; ++q) v += acc[0][q][lane];
             put_at<T>(a.dgate, a.f32, g * a.d + c, v);
         }
         return;
@@ -208,17 +216,22 @@ __global__ void __launch_bounds__(RN_RED_COLS* RN_RED_ROWS) rn_reduce_kernel(RnR
     const int sums = a.full ? 4 : 2, first = blockIdx.y == 0 ? 0 : sums / 2;
     float v[2] = {0.f, 0.f};
     if (c < a.d) {
+        const float* const from = a.part + (size_t)first * a.d + c;
+        const size_t hop = (size_t)sums * a.d;
+        const int second = a.full ? a.d : 0;
+        for (int q = row; q < a.parts; q += RN_RED_FLY * RN_RED_ROWS) {  // all loads of both sums in flight
+            float e[RN_RED_FLY], f[RN_RED_FLY];
 #pragma unroll
-        for (int n = 0; n < 2; ++n) {
-            if (n && !a.full) break;
-            const float* from = a.part + (size_t)(first + n) * a.d + c;
-            const size_t hop = (size_t)sums * a.d;
-            for (int q = row; q < a.parts; q += 8 * RN_RED_ROWS) {  // eight loads in flight
-                float e[8];
+            for (int k = 0; k < RN_RED_FLY; ++k) {
+                const bool there = q + k * RN_RED_ROWS < a.parts;
+                const float* const p = from + (size_t)(q + k * RN_RED_ROWS) * hop;
+                e[k] = there ? *p : 0.f;
+                f[k] = there && a.full ? p[second] : 0.f;
+            }
 #pragma unroll
-                for (int k = 0; k < 8; ++k) e[k] = q + k * RN_RED_ROWS < a.parts ? from[(size_t)(q + k * RN_RED_ROWS) * hop] : 0.f;
-#pragma unroll
-                for (int k = 0; k < 8; ++k) v[n] += e[k];
+            for (int k = 0; k < RN_RED_FLY; ++k) {
+                v[0] += e[k];
+                v[1] += f[k];
             }
         }
     }
@@ -251,7 +264,7 @@ int check(const moe_residual_norm_config* c) {
     if (c->rows < 0 || c->gate_rows < 0)
         return fail(MOE_ERR_ARG, "rows=%lld and gate_rows=%lld must be >= 0", (long long)c->rows, (long long)c->gate_rows);
     if (c->d < 1 || c->d > RN_MAX_D) return fail(MOE_ERR_ARG, "d=%d must be in [1, %d]", c->d, RN_MAX_D);
-    if (c->rows > INT64_MAX / 8 / c->d) return fail(MOE_ERR_ARG, "rows=%lld is too large", (long long)c->rows);
+    if (c->rows > INT64_MAX / 8 / c->d || c->rows > INT64_C(1) << 38) return fail(MOE_ERR_ARG, "rows=%lld is too large", (long long)c->rows);
     if (c->dtype != MOE_DTYPE_F32 && c->dtype != MOE_DTYPE_BF16 && c->dtype != MOE_DTYPE_F16)
         return fail(MOE_ERR_ARG, "dtype=%d is not a MOE_DTYPE", c->dtype);
     if (c->wdtype != MOE_DTYPE_F32 && c->wdtype != c->dtype)

@@ -6,9 +6,6 @@
 namespace moe {
 
 constexpr int RN_MAX_D = 16384;
-#ifndef RN_NV8
-#define RN_NV8 0
-#endif
 
 // How a launch's threads share the rows: groups of `warps` warps, `groups` of them in a CTA; a thread holds up to
 // `pieces` pieces of each row in every one of `slots` slots of shared memory.
@@ -41,7 +38,7 @@ cudaError_t launch_residual_backward(const RnShape& s, const RnWeights& w, const
                                      bool grouped, int ctas, cudaStream_t st);
 
 // Backward: values of a thread (32 of them spill; only rows above 8192 need them).
-inline int rn_backward_values(int d) { return d <= RN_NV8 ? 8 : d <= 8192 ? 16 : 32; }
+inline int rn_backward_values(int d) { return d <= 8192 ? 16 : 32; }
 
 namespace {
 
