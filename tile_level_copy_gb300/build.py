@@ -19,8 +19,7 @@ INCLUDE = os.path.join(ROOT, "include")
 OUT_DIR = os.path.join(HERE, "_lib")
 LIB = os.path.join(OUT_DIR, "libmoe.so")
 SOURCES = ["route_plan.cu", "gemm.cu", "combine.cu", "moe_abi.cu", "ffn.cu", "layernorm.cu", "adamw.cu",
-           "grad_norm.cu", "balance.cu", "residual_norm.cu", "residual_norm_bwd_f32.cu", "residual_norm_bwd_bf16.cu",
-           "residual_norm_bwd_f16.cu"]
+           "grad_norm.cu", "balance.cu", "residual_norm.cu", *(f"residual_norm_{d}_{t}.cu" for d in ("bwd", "fwd") for t in ("bf16", "f16", "f32"))]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC,-fvisibility=hidden", "-I", INCLUDE]
 

@@ -1,11 +1,5 @@
-// Norms around a block fused with its gate and the residual sum: forward pass, sums over the rows, C entries.
-//
-//   h = a x + c gate * post(u), z = pre(h); a norm is (v - mean) rstd w + b, with mean 0 for the mean-square kind
-//
-// The pass reads x and u and writes h and z: HBM bounds it. A row lies in shared memory in the slots of the warps
-// that share it, fetched by cp.async while the rows before are worked on; a thread reads only pieces that it fetched
-// itself, so no barrier guards the slots. h is rounded to its type before the second norm (the value the backward
-// pass and every other reader sees) and waits in x's slot for the pass that writes z.
+// Norms around a block fused with its gate and the residual sum: the C entries, and the sums over the rows that end the
+// backward pass.
 #include "residual_norm.cuh"
 
 #include <math.h>
@@ -13,159 +7,8 @@
 namespace moe {
 namespace {
 
-constexpr int RN_FWD_THREADS = 256;
-constexpr int RN_UNROLL = 4;        // pieces worked on at a time
 constexpr int RN_RED_COLS = 32, RN_RED_ROWS = 32, RN_RED_FLY = 10;
 constexpr int RN_MAX_SMS = 256;
-
-template <typename T, int VEC>
-__global__ void __launch_bounds__(RN_FWD_THREADS, 3)
-    rn_forward_kernel(RnShape s, const T* x, const T* u, RnWeights w, T* h, T* z, float2* post_stats, float2* pre_stats) {
-    typedef typename Lanes<VEC>::V V;
-    typedef Pack<T, VEC> P;
-    constexpr int N = Lanes<VEC>::N;
-    __shared__ float red[2][RN_FWD_THREADS / 32];
-    extern __shared__ __align__(16) uint8_t rn_smem[];
-    griddep_wait();
-    griddep_launch();
-    const int tpr = s.warps * 32, t = threadIdx.x % tpr, group = threadIdx.x / tpr, lane = threadIdx.x & 31;
-    const int threads = blockDim.x, step = tpr * VEC, c0 = t * VEC;
-    const int np = c0 < s.d ? (s.d - c0 + step - 1) / step : 0;  // this thread's pieces, at most s.pieces
-    P* const slot = reinterpret_cast<P*>(rn_smem) + threadIdx.x;
-    const int64_t stride = (int64_t)gridDim.x * s.groups;
-    auto piece = [&](int stage, int tensor, int q) { return slot + ((stage * 2 + tensor) * s.pieces + q) * threads; };
-    auto issue = [&](int64_t r, int stage) {
-        if (r < s.rows) {
-            const T* xr = x + r * s.d + c0;
-            const T* ur = u + r * s.d + c0;
-            for (int q = 0; q < np; ++q) fetch(piece(stage, 0, q), reinterpret_cast<const P*>(xr + q * step));
-            if (u)
-                for (int q = 0; q < np; ++q) fetch(piece(stage, 1, q), reinterpret_cast<const P*>(ur + q * step));
-        }
-        asm volatile("cp.async.commit_group;" ::: "memory");
-    };
-    int flip = 0;
-    auto row_sum = [&](V v) {
-        float a = warp_sum(total(v));
-        if (s.warps == 1) return a;
-        float* r = red[flip] + group * s.warps;  // the two halves in turn: one barrier a sum is enough
-        flip ^= 1;
-        if (lane == 0) r[t >> 5] = a;
-        named_bar_sync(1 + group, tpr);
-        a = 0.f;
-        for (int i = 0; i < s.warps; ++i) a += r[i];
-        return a;
-    };
-    // f(q) for every piece of the thread
-    auto over = [&](auto f) {
-        for (int q0 = 0; q0 < np; q0 += RN_UNROLL) {
-#pragma unroll
-            for (int k = 0; k < RN_UNROLL; ++k) {
-                if (q0 + k >= np) break;
-                f(q0 + k);
-            }
-        }
-    };
-    // mean and 1 / sqrt(mean square + eps) of the pieces of a tensor in a slot
-    auto statistics = [&](int kind, int stage, int tensor) {
-        V f[N], acc = both<V>(0.f);
-        float mu = 0.f;
-        if (kind == MOE_NORM_LAYER) {
-            over([&](int q) {
-                widen(*piece(stage, tensor, q), f);
-#pragma unroll
-                for (int i = 0; i < N; ++i) acc = add_(acc, f[i]);
-            });
-            mu = row_sum(acc) * s.inv_d;
-        }
-        const V neg = both<V>(-mu);
-        V sq[2] = {both<V>(0.f), both<V>(0.f)};
-        over([&](int q) {
-            widen(*piece(stage, tensor, q), f);
-#pragma unroll
-            for (int i = 0; i < N; ++i) {
-                f[i] = add_(f[i], neg);
-                sq[i & 1] = fma_(f[i], f[i], sq[i & 1]);
-            }
-        });
-        return make_float2(mu, rsqrtf(fmaf(row_sum(add_(sq[0], sq[1])), s.inv_d, s.eps)));
-    };
-
-    int stage = 0;
-    int64_t r = (int64_t)blockIdx.x * s.groups + group;
-    for (int k = 0; k < s.slots - 1; ++k) issue(r + k * stride, k);
-    for (; r < s.rows; r += stride) {
-        issue(r + (s.slots - 1) * stride, stage == 0 ? s.slots - 1 : stage - 1);
-        fetched(s.slots - 1);
-        const int64_t at = r * s.d + c0;
-        float2 st = make_float2(0.f, 1.f);
-        if (s.post) {
-            st = statistics(s.post, stage, 1);
-            if (t == 0 && post_stats) post_stats[r] = st;
-        }
-        const V neg = both<V>(-st.x), rs = both<V>(st.y), res = both<V>(s.res), branch = both<V>(s.branch);
-        const int64_t gate_at = s.gate_rows ? r / s.gate_rows * s.d : 0;
-        over([&](int q) {
-            const int c = c0 + q * step;
-            V f[N], v[N], k[N];
-            widen(*piece(stage, 0, q), f);
-#pragma unroll
-            for (int i = 0; i < N; ++i) f[i] = mul_(f[i], res);
-            if (u) {
-                widen(*piece(stage, 1, q), v);
-                if (s.post) {
-#pragma unroll
-                    for (int i = 0; i < N; ++i) v[i] = mul_(add_(v[i], neg), rs);
-                    if (w.post_w) {
-                        weight<T, VEC>(w, w.post_w, 1.f, c, k);
-#pragma unroll
-                        for (int i = 0; i < N; ++i) v[i] = mul_(v[i], k[i]);
-                    }
-                    if (w.post_b) {
-                        weight<T, VEC>(w, w.post_b, 0.f, c, k);
-#pragma unroll
-                        for (int i = 0; i < N; ++i) v[i] = add_(v[i], k[i]);
-                    }
-                }
-                if (s.gate_rows) {
-                    weight<T, VEC>(w, w.gate, 1.f, gate_at + c, k);
-#pragma unroll
-                    for (int i = 0; i < N; ++i) v[i] = mul_(v[i], k[i]);
-                }
-#pragma unroll
-                for (int i = 0; i < N; ++i) f[i] = fma_(v[i], branch, f[i]);
-            }
-            const P p = narrow<T, VEC>(f);
-            if (h) *reinterpret_cast<P*>(h + at + q * step) = p;
-            *piece(stage, 0, q) = p;
-        });
-        if (s.pre) {
-            const float2 ps = statistics(s.pre, stage, 0);
-            if (t == 0 && pre_stats) pre_stats[r] = ps;
-            const V pneg = both<V>(-ps.x), prs = both<V>(ps.y);
-            over([&](int q) {
-                const int c = c0 + q * step;
-                V f[N], k[N];
-                widen(*piece(stage, 0, q), f);
-#pragma unroll
-                for (int i = 0; i < N; ++i) f[i] = mul_(add_(f[i], pneg), prs);
-                if (w.pre_w) {
-                    weight<T, VEC>(w, w.pre_w, 1.f, c, k);
-#pragma unroll
-                    for (int i = 0; i < N; ++i) f[i] = mul_(f[i], k[i]);
-                }
-                if (w.pre_b) {
-                    weight<T, VEC>(w, w.pre_b, 0.f, c, k);
-#pragma unroll
-                    for (int i = 0; i < N; ++i) f[i] = add_(f[i], k[i]);
-                }
-                *reinterpret_cast<P*>(z + at + q * step) = narrow<T, VEC>(f);
-            });
-        }
-        if (++stage == s.slots) stage = 0;
-    }
-    fetched(0);
-}
 
 // The gradients of the weights from the CTAs' sums [parts][sums][d]: blockIdx.y 0 the norm before the next block
 // (sum 0, and 1 with full), 1 the norm behind this one and a gate that all rows share (the last one or two sums);
@@ -296,13 +139,10 @@ int vector_width(const moe_residual_norm_config& c, Ptr... p) {
     const int v = (int)(16 / dtype_size(c.dtype));
     return c.d % v == 0 && (aligned(p, 16) && ...) ? v : 1;
 }
-RnWeights weights_of(const moe_residual_norm_config& c, int vec, const void* post_w, const void* post_b, const void* gate,
+RnWeights weights_of(const moe_residual_norm_config& c, const void* post_w, const void* post_b, const void* gate,
                      const void* pre_w, const void* pre_b) {
-    const bool f32 = c.wdtype == MOE_DTYPE_F32;
-    const size_t piece = f32 ? (vec < 4 ? vec : 4) * 4 : vec * dtype_size(c.dtype);
-    const bool whole = aligned(post_w, piece) && aligned(post_b, piece) && aligned(gate, piece) && aligned(pre_w, piece) &&
-                       aligned(pre_b, piece);
-    return RnWeights{post_w, post_b, gate, pre_w, pre_b, !whole ? LN_W_ANY : f32 ? LN_W_F32 : LN_W_SAME, f32};
+    const bool whole = aligned(post_w, 16) && aligned(post_b, 16) && aligned(gate, 16) && aligned(pre_w, 16) && aligned(pre_b, 16);
+    return RnWeights{post_w, post_b, gate, pre_w, pre_b, c.wdtype == MOE_DTYPE_F32, whole};
 }
 int check_weights(const moe_residual_norm_config& c, const void* post_w, const void* post_b, const void* gate,
                   const void* pre_w, const void* pre_b) {
@@ -316,18 +156,13 @@ int check_weights(const moe_residual_norm_config& c, const void* post_w, const v
     return MOE_OK;
 }
 
-int warps_for(int d, int values) { return (d + 32 * values - 1) / (32 * values); }
-
-RnShape shape_of(const moe_residual_norm_config& c, int warps, int threads, int vec) {
+RnShape shape_of(const moe_residual_norm_config& c) {
     RnShape s;
     s.rows = c.rows;
     s.gate_rows = c.gate_rows < c.rows ? c.gate_rows : c.rows;  // of one gate for all rows, as many as there are
     s.chunk = 0;
     s.d = c.d;
-    s.warps = warps;
-    s.groups = warps * 32 < threads ? threads / (warps * 32) : 1;
-    s.pieces = (c.d + warps * 32 * vec - 1) / (warps * 32 * vec);
-    s.slots = 1;
+    s.warps = s.groups = s.slots = 1;
     s.post = c.post, s.pre = c.pre;
     s.eps = c.eps;
     s.inv_d = 1.0f / (float)c.d;
@@ -339,9 +174,10 @@ bool full_of(const moe_residual_norm_config& c) { return c.post == MOE_NORM_LAYE
 bool grouped_of(const moe_residual_norm_config& c) { return c.gate_rows > 0 && c.gate_rows < c.rows; }
 
 // Backward: CTAs, and the consecutive rows of each group of warps.
-RnShape backward_shape(const moe_residual_norm_config& c, int vec, int sms, int* ctas) {
-    const int warps = warps_for(c.d, rn_backward_values(c.d));
-    RnShape s = shape_of(c, warps, 256, vec);
+RnShape backward_shape(const moe_residual_norm_config& c, int sms, int* ctas) {
+    RnShape s = shape_of(c);
+    s.warps = rn_warps(c.d, rn_backward_values(c.d));
+    s.groups = s.warps < 8 ? 8 / s.warps : 1;
     const int64_t most = (int64_t)sms * (s.warps * s.groups > 8 ? 1 : 2) * s.groups;
     const int64_t workers = c.rows < most ? c.rows : most;
     s.chunk = workers ? (c.rows + workers - 1) / workers : 1;
@@ -352,15 +188,11 @@ RnShape backward_shape(const moe_residual_norm_config& c, int vec, int sms, int*
 size_t part_bytes(const moe_residual_norm_config& c, int ctas) { return (size_t)ctas * (full_of(c) ? 4 : 2) * c.d * 4; }
 size_t gpart_bytes(const moe_residual_norm_config& c, int workers) { return grouped_of(c) ? (size_t)workers * 2 * c.d * 4 : 0; }  // and gsum's
 
-// f(T(), Int<VEC>()) for the config's type and piece width.
+// f(T()) for the config's type.
 template <typename F>
-cudaError_t dispatch(int dtype, int vec, F f) {
-    if (dtype == MOE_DTYPE_F32) return vec == 4 ? f(float(), Int<4>()) : f(float(), Int<1>());
-    if (dtype == MOE_DTYPE_BF16) return vec == 8 ? f(__nv_bfloat16(), Int<8>()) : f(__nv_bfloat16(), Int<1>());
-    return vec == 8 ? f(__half(), Int<8>()) : f(__half(), Int<1>());
+cudaError_t dispatch(int dtype, F f) {
+    return dtype == MOE_DTYPE_F32 ? f(float()) : dtype == MOE_DTYPE_BF16 ? f(__nv_bfloat16()) : f(__half());
 }
-
-constexpr size_t RN_FWD_SMEM = 220 * 1024;
 
 }  // namespace
 }  // namespace moe
@@ -389,31 +221,10 @@ MOE_API int moe_residual_norm_forward(const moe_residual_norm_config* c, const v
     DeviceInfo di;
     if ((rc = check_device(&di))) return rc;
     const int vec = vector_width(*c, x, u, h, z);
-    // 64 bytes of a row a thread (four pieces), in more warps where there are too few rows to fill the device
-    int values = 64 / (int)e;
-    while (warps_for(c->d, values) > RN_FWD_THREADS / 32) values *= 2;
-    while (values > 16 / (int)e && (c->d <= 32 * values / 2 || c->rows * warps_for(c->d, values) < 16 * di.sms) &&
-           warps_for(c->d, values / 2) <= RN_FWD_THREADS / 32)
-        values /= 2;
-    RnShape s = shape_of(*c, warps_for(c->d, values), RN_FWD_THREADS, vec);
-    const int threads = 32 * s.warps * s.groups;
-    const size_t slot = (size_t)threads * s.pieces * vec * e * 2;
-    // as many CTAs as find room with two slots each, up to three
-    s.slots = 2 * slot <= RN_FWD_SMEM ? 2 : 1;
-    const int64_t n = (c->rows + s.groups - 1) / s.groups;
-    int per_sm = (int)(RN_FWD_SMEM / (s.slots * slot));
-    if (per_sm > 3) per_sm = 3;
-    const int64_t most = (int64_t)di.sms * per_sm;
-    const dim3 grid((unsigned)(n < most ? n : most)), block(threads);
-    const RnWeights w = weights_of(*c, vec, post_w, post_b, gate, pre_w, pre_b);
-    const cudaError_t err = dispatch(c->dtype, vec, [&](auto type, auto width) {
-        typedef decltype(type) T;
-        constexpr auto kernel = &rn_forward_kernel<T, decltype(width)::value>;
-        const cudaError_t e0 = allow_smem<kernel>(RN_FWD_SMEM);
-        if (e0 != cudaSuccess) return e0;
-        return launch_k(kernel, grid, block, s.slots * slot, static_cast<cudaStream_t>(stream), true, s,
-                        static_cast<const T*>(x), static_cast<const T*>(u), w, static_cast<T*>(h), static_cast<T*>(z),
-                        reinterpret_cast<float2*>(post_stats), reinterpret_cast<float2*>(pre_stats));
+    const RnForward f{x, u, h, z, reinterpret_cast<float2*>(post_stats), reinterpret_cast<float2*>(pre_stats)};
+    const cudaError_t err = dispatch(c->dtype, [&](auto type) {
+        return launch_residual_forward<decltype(type)>(shape_of(*c), weights_of(*c, post_w, post_b, gate, pre_w, pre_b), f, vec,
+                                                       di.sms, static_cast<cudaStream_t>(stream));
     });
     return err == cudaSuccess ? MOE_OK : cuda_fail(err, "residual norm launch");
 }
@@ -423,13 +234,9 @@ MOE_API int moe_residual_norm_workspace_size(const moe_residual_norm_config* c, 
     const int rc = check(c);
     if (rc) return rc;
     if (!bytes) return fail(MOE_ERR_ARG, "bytes is NULL");
-    size_t most = 16;
-    for (int vec : {1, (int)(16 / dtype_size(c->dtype))}) {
-        int ctas;
-        const RnShape s = backward_shape(*c, vec, RN_MAX_SMS, &ctas);
-        const size_t need = part_bytes(*c, ctas) + 2 * gpart_bytes(*c, ctas * s.groups);
-        if (need > most) most = need;
-    }
+    int ctas;
+    const RnShape s = backward_shape(*c, RN_MAX_SMS, &ctas);
+    const size_t need = part_bytes(*c, ctas) + 2 * gpart_bytes(*c, ctas * s.groups), most = need > 16 ? need : 16;
     *bytes = most;
     return MOE_OK;
 }
@@ -478,7 +285,7 @@ MOE_API int moe_residual_norm_backward(const moe_residual_norm_config* c, const 
     if ((rc = check_device(&di))) return rc;
     const int vec = vector_width(*c, dz, dh, uses_u ? u : nullptr, c->pre ? h : nullptr, dx, du);
     int ctas;
-    const RnShape s = backward_shape(*c, vec, di.sms, &ctas);
+    const RnShape s = backward_shape(*c, di.sms, &ctas);
     const bool full = full_of(*c), grouped = grouped_of(*c);
     float *part = nullptr, *gpart = nullptr, *gsum = nullptr;
     if (any) {
@@ -490,11 +297,11 @@ MOE_API int moe_residual_norm_backward(const moe_residual_norm_config* c, const 
         gpart = part + p / 4;
         gsum = gpart + gp / 4;
     }
-    const RnWeights w = weights_of(*c, vec, post_w, post_b, gate, pre_w, nullptr);
+    const RnWeights w = weights_of(*c, post_w, post_b, gate, pre_w, nullptr);
     const RnBackward b{c->pre ? dz : nullptr, dh, uses_u ? u : nullptr, c->pre ? h : nullptr,
                        reinterpret_cast<const float2*>(post_stats), reinterpret_cast<const float2*>(pre_stats), dx, du, part,
                        gpart, gsum, dgate};
-    const cudaError_t err = dispatch(c->dtype, 1, [&](auto type, auto) {
+    const cudaError_t err = dispatch(c->dtype, [&](auto type) {
         typedef decltype(type) T;
         const cudaError_t e0 = launch_residual_backward<T>(s, w, b, vec, full, grouped, ctas, st);
         if (e0 != cudaSuccess || !any) return e0;

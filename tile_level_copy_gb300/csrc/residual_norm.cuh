@@ -1,4 +1,4 @@
-// Shapes and values that the passes of the residual norm share.
+// Shapes, columns and values that the passes of the residual norm share.
 #pragma once
 
 #include "row_values.cuh"
@@ -7,20 +7,24 @@ namespace moe {
 
 constexpr int RN_MAX_D = 16384;
 
-// How a launch's threads share the rows: groups of `warps` warps, `groups` of them in a CTA; a thread holds up to
-// `pieces` pieces of each row in every one of `slots` slots of shared memory.
+// How a launch's threads share the rows: groups of `warps` warps, `groups` of them in a CTA, with `slots` rows of each
+// group in shared memory.
 struct RnShape {
     int64_t rows, gate_rows;  // gate_rows 0: no gate
     int64_t chunk;            // backward: consecutive rows of a group of warps
-    int d, warps, groups, pieces, slots;
+    int d, warps, groups, slots;
     int post, pre;            // MOE_NORM_*
     float eps, inv_d, res, branch;
 };
-// form: how the vectors that are there lie, LN_W_*.
 struct RnWeights {
     const void *post_w, *post_b, *gate, *pre_w, *pre_b;
-    int form;
-    bool f32;
+    bool f32;    // fp32, or the rows' type
+    bool whole;  // every vector that is there is aligned for whole pieces
+};
+struct RnForward {
+    const void *x, *u;
+    void *h, *z;
+    float2 *post_stats, *pre_stats;
 };
 struct RnBackward {
     const void *dz, *dh, *u, *h;
@@ -32,40 +36,132 @@ struct RnBackward {
     void* dgate;
 };
 
-// Launches the backward kernel on rows of T (one file for each type).
+// Launch the passes on rows of T (files of their own for each type); vec: values of a 16-byte piece, or 1.
 template <typename T>
-cudaError_t launch_residual_backward(const RnShape& s, const RnWeights& w, const RnBackward& b, int vec, bool full,
-                                     bool grouped, int ctas, cudaStream_t st);
+cudaError_t launch_residual_forward(RnShape s, const RnWeights& w, const RnForward& f, int vec, int sms, cudaStream_t st);
+template <typename T>
+cudaError_t launch_residual_backward(RnShape s, const RnWeights& w, const RnBackward& b, int vec, bool full, bool grouped,
+                                     int ctas, cudaStream_t st);
 
+inline int rn_warps(int d, int values) { return (d + 32 * values - 1) / (32 * values); }
 // Backward: values of a thread (32 of them spill; only rows above 8192 need them).
 inline int rn_backward_values(int d) { return d <= 8192 ? 16 : 32; }
 
 namespace {
 
-// VEC weights from column c on (null: `none`).
-template <typename T, int VEC>
-__device__ __forceinline__ void weight(const RnWeights& w, const void* p, float none, int64_t c,
-                                       typename Lanes<VEC>::V (&o)[Lanes<VEC>::N]) {
-    if (!p) {
-#pragma unroll
-        for (int i = 0; i < Lanes<VEC>::N; ++i) o[i] = both<typename Lanes<VEC>::V>(none);
-        return;
+// How rows reach their readers. RN_OWN: a thread fetches the pieces that it reads itself, so no barrier guards the slots.
+// RN_RAGGED: rows of odd addresses, whose values only loads of one value could fetch: the threads of a row fetch the
+// 16-byte pieces that cover it and read single values from them, one barrier a row. RN_DIRECT: values are read from
+// global memory wherever they are needed (rows too wide for a slot).
+enum RnMode : int { RN_OWN, RN_RAGGED, RN_DIRECT };
+
+// The columns of a thread, in units of two. VEC > 1: pieces of VEC neighbouring values, piece q of thread t at
+// column (q * threads of the row + t) VEC. VEC = 1: a unit is two values a row's threads apart (single values of
+// neighbouring threads lie beside one another), a piece is a unit.
+template <typename T, int VEC, int NV>
+struct RnColumns {
+    static constexpr int PV = VEC == 1 ? 2 : VEC, NP = NV / PV, UN = PV / 2, NU = NV / 2;
+    typedef Pack<T, PV> P;
+    int t, tpr, d, np;  // thread of the row, threads of the row, values of the row, this thread's pieces
+    __device__ __forceinline__ RnColumns(int t, int tpr, int d) : t(t), tpr(tpr), d(d) {
+        const int c0 = VEC == 1 ? t : t * VEC, step = VEC == 1 ? 2 * tpr : tpr * VEC;
+        np = c0 < d ? min(NP, (d - c0 + step - 1) / step) : 0;
     }
-    if (w.form == LN_W_F32) weights<T, VEC, LN_W_F32>(static_cast<const float*>(p) + c, true, none, 0, o);
-    else if (w.form == LN_W_SAME) weights<T, VEC, LN_W_SAME>(static_cast<const T*>(p) + c, false, none, 0, o);
-    else if (w.f32) weights<T, VEC, LN_W_ANY>(static_cast<const float*>(p) + c, true, none, 0, o);
-    else weights<T, VEC, LN_W_ANY>(static_cast<const T*>(p) + c, false, none, 0, o);
+    __device__ __forceinline__ int column(int j, int i) const {  // of value i of unit j
+        return VEC == 1 ? t + (2 * j + i) * tpr : t * VEC + (j / UN) * (tpr * VEC) + (j % UN) * 2 + i;
+    }
+    __device__ __forceinline__ bool inside(int j, int i) const { return VEC == 1 ? column(j, i) < d : j / UN < np; }
+    __device__ __forceinline__ int start(int q) const { return VEC == 1 ? t + 2 * q * tpr : t * VEC + q * (tpr * VEC); }
+    // piece q of the row at p (global memory, or its bytes in a slot); values beyond the row are zero
+    __device__ __forceinline__ P load(const T* p, int q) const {
+        P r;
+        if constexpr (VEC == 1) {
+            const int c = start(q);
+            put(r.v[0], 0.f);
+            put(r.v[1], 0.f);
+            if (c < d) r.v[0] = p[c];
+            if (c + tpr < d) r.v[1] = p[c + tpr];
+        } else {
+            if (q < np) r = *reinterpret_cast<const P*>(p + start(q));
+            else memset(&r, 0, sizeof(r));
+        }
+        return r;
+    }
+    __device__ __forceinline__ void store(T* p, int q, const P& r) const {
+        if constexpr (VEC == 1) {
+            const int c = start(q);
+            if (c < d) p[c] = r.v[0];
+            if (c + tpr < d) p[c + tpr] = r.v[1];
+        } else {
+            if (q < np) *reinterpret_cast<P*>(p + start(q)) = r;
+        }
+    }
+};
+
+// Unit j of a piece as fp32; and back. (By words: pieces of two 16-bit values that are copied one by one cost a byte
+// permutation each, a quarter of the backward kernel's instructions.)
+template <typename T, int VEC>
+__device__ __forceinline__ f2 unit_of(const Pack<T, VEC>& p, int j) {
+    if constexpr (sizeof(T) == 4) {
+        return pair(p.v[2 * j], p.v[2 * j + 1]);
+    } else {
+        const uint32_t w = reinterpret_cast<const uint32_t*>(&p)[j];
+        if constexpr (std::is_same_v<T, __nv_bfloat16>) {
+            return pair(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
+        } else {
+            const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w));
+            return pair(f.x, f.y);
+        }
+    }
+}
+template <typename T, int VEC>
+__device__ __forceinline__ void put_unit(Pack<T, VEC>& p, int j, f2 v) {
+    const float2 f = split(v);
+    if constexpr (sizeof(T) == 4) {
+        p.v[2 * j] = f.x;
+        p.v[2 * j + 1] = f.y;
+    } else if constexpr (std::is_same_v<T, __nv_bfloat16>) {
+        reinterpret_cast<uint32_t*>(&p)[j] = pack_bf16x2(f.x, f.y);
+    } else {
+        const __half2 h = __floats2half2_rn(f.x, f.y);
+        reinterpret_cast<uint32_t*>(&p)[j] = *reinterpret_cast<const uint32_t*>(&h);
+    }
 }
 
 template <typename T>
 __device__ __forceinline__ float value_at(const void* p, bool f32, int64_t i, float none) {
     return !p ? none : f32 ? static_cast<const float*>(p)[i] : num(static_cast<const T*>(p)[i]);
 }
-template <typename P>
-__device__ __forceinline__ void fetch(P* to, const P* from) {  // asynchronous where the piece allows it
-    if constexpr (sizeof(P) >= 4) copy_async<sizeof(P)>(to, from);
-    else *to = *from;
+
+// ---- ragged rows
+// Bytes of a tensor in a slot: the rows of up to eight groups, each with what covers its ends.
+template <typename T>
+__host__ __device__ constexpr int rn_cover(int values, int threads) { return values * threads * (int)sizeof(T) + 8 * 32; }
+// Where a group's rows start in it.
+template <typename T>
+__device__ __forceinline__ int cover_at(int group, int tpr, int values) { return group * (tpr * values * (int)sizeof(T) + 32); }
+// Where a row's values start behind a 16-byte boundary.
+__device__ __forceinline__ int offset_of(const void* p) { return (int)(reinterpret_cast<uintptr_t>(p) & 15); }
+// Thread t of `threads` fetches its share of the 16-byte pieces that cover the d values from `at` on. A piece that
+// reaches beyond the tensor's n values is copied value by value.
+template <typename T>
+__device__ __forceinline__ void cover_row(uint8_t* to, const T* rows, int64_t n, int64_t at, int d, int t, int threads) {
+    const T* const from = rows + at;
+    const int off = offset_of(from), pieces = (off + d * (int)sizeof(T) + 15) / 16;
+    const uint8_t* const start = reinterpret_cast<const uint8_t*>(from) - off;
+    const uint8_t *const lo = reinterpret_cast<const uint8_t*>(rows), *const hi = reinterpret_cast<const uint8_t*>(rows + n);
+    for (int i = t; i < pieces; i += threads) {
+        const uint8_t* const p = start + 16 * i;
+        if (p >= lo && p + 16 <= hi) {
+            copy_async<16>(to + 16 * i, p);
+        } else {
+            for (int k = 0; k < 16; k += (int)sizeof(T))
+                if (p + k >= lo && p + k < hi) *reinterpret_cast<T*>(to + 16 * i + k) = *reinterpret_cast<const T*>(p + k);
+        }
+    }
 }
+
+__device__ __forceinline__ void committed() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 __device__ __forceinline__ void fetched(int pending) {  // all but the last `pending` groups are there
     if (pending == 0) asm volatile("cp.async.wait_group 0;" ::: "memory");
     else if (pending == 1) asm volatile("cp.async.wait_group 1;" ::: "memory");

@@ -21,91 +21,26 @@ namespace moe {
 namespace {
 
 // CTAs on a SM
-__host__ __device__ constexpr int rb_ctas(int, int threads) { return threads > 256 ? 1 : 2; }
+__host__ __device__ constexpr int rb_ctas(int threads) { return threads > 256 ? 1 : 2; }
 constexpr size_t RB_SMEM_MOST = 224 * 1024;
-
-
-// Two neighbouring values of a piece of 16-bit or 32-bit values, or its only one, as fp32; and back. (By words: pieces of
-// two 16-bit values that are copied one by one cost a byte permutation each, a quarter of the kernel's instructions.)
-template <typename T, int VEC>
-__device__ __forceinline__ typename Lanes<VEC>::V unit_of(const Pack<T, VEC>& p, int j) {
-    if constexpr (VEC == 1) {
-        return num(p.v[0]);
-    } else if constexpr (sizeof(T) == 4) {
-        return pair(p.v[2 * j], p.v[2 * j + 1]);
-    } else {
-        const uint32_t w = reinterpret_cast<const uint32_t*>(&p)[j];
-        if constexpr (std::is_same_v<T, __nv_bfloat16>) {
-            return pair(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
-        } else {
-            const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w));
-            return pair(f.x, f.y);
-        }
-    }
-}
-template <typename T, int VEC>
-__device__ __forceinline__ void put_unit(Pack<T, VEC>& p, int j, typename Lanes<VEC>::V v) {
-    if constexpr (VEC == 1) {
-        put(p.v[0], v);
-    } else {
-        const float2 f = split(v);
-        if constexpr (sizeof(T) == 4) {
-            p.v[2 * j] = f.x;
-            p.v[2 * j + 1] = f.y;
-        } else if constexpr (std::is_same_v<T, __nv_bfloat16>) {
-            reinterpret_cast<uint32_t*>(&p)[j] = pack_bf16x2(f.x, f.y);
-        } else {
-            const __half2 h = __floats2half2_rn(f.x, f.y);
-            reinterpret_cast<uint32_t*>(&p)[j] = *reinterpret_cast<const uint32_t*>(&h);
-        }
-    }
-}
-
-// Bytes of a tensor in a slot of ragged rows: the rows of up to eight groups, each with what covers its ends.
-template <typename T>
-__host__ __device__ constexpr int rb_cover(int values, int threads) { return values * threads * (int)sizeof(T) + 8 * 32; }
-// Where a row's values start behind a 16-byte boundary.
-__device__ __forceinline__ int offset_of(const void* p) { return (int)(reinterpret_cast<uintptr_t>(p) & 15); }
-// Thread t of `threads` fetches its share of the 16-byte pieces that cover the d values from `at` on. A piece that
-// reaches beyond the tensor's n values is copied value by value.
-template <typename T>
-__device__ __forceinline__ void cover_row(uint8_t* to, const T* rows, int64_t n, int64_t at, int d, int t, int threads) {
-    const T* const from = rows + at;
-    const int off = offset_of(from), pieces = (off + d * (int)sizeof(T) + 15) / 16;
-    const uint8_t* const start = reinterpret_cast<const uint8_t*>(from) - off;
-    const uint8_t *const lo = reinterpret_cast<const uint8_t*>(rows), *const hi = reinterpret_cast<const uint8_t*>(rows + n);
-    for (int i = t; i < pieces; i += threads) {
-        const uint8_t* const p = start + 16 * i;
-        if (p >= lo && p + 16 <= hi) {
-            copy_async<16>(to + 16 * i, p);
-        } else {
-            for (int k = 0; k < 16; k += (int)sizeof(T))
-                if (p + k >= lo && p + k < hi) *reinterpret_cast<T*>(to + 16 * i + k) = *reinterpret_cast<const T*>(p + k);
-        }
-    }
-}
-// A thread's columns in units of U values, UN of them in a piece, `np` pieces in the row; and where its units of w2 and,
-// behind all of those, of k lie in shared memory.
-template <int U_, int UN_, int NU_, int THREADS_>
-struct RbColumns {
-    static constexpr int U = U_, UN = UN_, NU = NU_, THREADS = THREADS_;
-    typedef typename Lanes<U>::V V;
-    int c0, step, np, d;
-    V* at;
-    __device__ __forceinline__ int column(int j) const { return c0 + (j / UN) * step + (j % UN) * U; }
-    __device__ __forceinline__ bool inside(int j) const { return j / UN < np; }
-    __device__ __forceinline__ V* w2(int j) const { return at + j * THREADS; }
-    __device__ __forceinline__ V* k(int j) const { return at + (NU + j) * THREADS; }
-};
 constexpr int RB_BATCH = 4;  // units whose loads are in flight together
+
+// A thread's units of w2 and, behind all of those, of k in shared memory.
+template <typename C, int THREADS>
+struct RbPlaces {
+    f2* at;
+    __device__ __forceinline__ f2* w2(int j) const { return at + j * THREADS; }
+    __device__ __forceinline__ f2* k(int j) const { return at + (C::NU + j) * THREADS; }
+};
+// Units of a vector from j0 on (null, and beyond the row: `none`).
 template <typename T, typename C>
 __device__ __forceinline__ void vector_units(const C& c, const void* p, bool f32, float none, int64_t at, int j0,
-                                             Pack<float, C::U> (&o)[RB_BATCH]) {
+                                             float (&o)[RB_BATCH][2]) {
     auto each = [&](auto value) {
 #pragma unroll
         for (int k = 0; k < RB_BATCH; ++k)
 #pragma unroll
-            for (int i = 0; i < C::U; ++i) o[k].v[i] = c.inside(j0 + k) ? value(at + c.column(j0 + k) + i) : none;
+            for (int i = 0; i < 2; ++i) o[k][i] = c.inside(j0 + k, i) ? value(at + c.column(j0 + k, i)) : none;
     };
     if (!p) each([&](int64_t) { return none; });
     else if (f32) each([&](int64_t i) { return static_cast<const float*>(p)[i]; });
@@ -113,62 +48,58 @@ __device__ __forceinline__ void vector_units(const C& c, const void* p, bool f32
 }
 // Writes w2, and k of the rows that share gate g; zeros beyond the row. The sum of the thread's k. (This and
 // gate_end are calls, made once a gate: inlined they took registers from the loop over the rows.)
-template <typename T, typename C>
-__device__ __noinline__ float make_weights(const C c, const RnWeights& w, int64_t g) {
-    typedef typename C::V V;
+template <typename T, typename C, typename Q>
+__device__ __noinline__ float make_weights(const C c, const Q places, const RnWeights& w, int64_t g) {
     float sum = 0.f;
 #pragma unroll 1
     for (int j0 = 0; j0 < C::NU; j0 += RB_BATCH) {
-        Pack<float, C::U> a[RB_BATCH], k[RB_BATCH], gate[RB_BATCH];
+        float a[RB_BATCH][2], k[RB_BATCH][2], gate[RB_BATCH][2];
         vector_units<T>(c, w.pre_w, w.f32, 1.f, 0, j0, a);
         vector_units<T>(c, w.post_w, w.f32, 1.f, 0, j0, k);
         vector_units<T>(c, w.gate, w.f32, 1.f, g * c.d, j0, gate);
 #pragma unroll
         for (int n = 0; n < RB_BATCH; ++n) {
 #pragma unroll
-            for (int i = 0; i < C::U; ++i) {
-                a[n].v[i] = c.inside(j0 + n) ? a[n].v[i] : 0.f;
-                k[n].v[i] = c.inside(j0 + n) ? k[n].v[i] * gate[n].v[i] : 0.f;
-                sum += k[n].v[i];
+            for (int i = 0; i < 2; ++i) {
+                const bool in = c.inside(j0 + n, i);
+                a[n][i] = in ? a[n][i] : 0.f;
+                k[n][i] = in ? k[n][i] * gate[n][i] : 0.f;
+                sum += k[n][i];
             }
-            *c.w2(j0 + n) = *reinterpret_cast<const V*>(&a[n]);
-            *c.k(j0 + n) = *reinterpret_cast<const V*>(&k[n]);
+            *places.w2(j0 + n) = pair(a[n][0], a[n][1]);
+            *places.k(j0 + n) = pair(k[n][0], k[n][1]);
         }
     }
     return sum;
 }
 // The end of the rows that share gate g: S lies in the places of k, B in those of w2. dw1 += gate S and db1 += gate B
 // in sums [2][d], and w1 S + b1 B to part (a gate whose other rows lie elsewhere) or into dgate.
-template <typename T, bool FULL, typename C>
-__device__ __noinline__ void gate_end(const C c, const RnWeights& w, int64_t g, float* sums, float* part, void* dgate) {
-    typedef typename C::V V;
+template <typename T, bool FULL, typename C, typename Q>
+__device__ __noinline__ void gate_end(const C c, const Q places, const RnWeights& w, int64_t g, float* sums, float* part,
+                                      void* dgate) {
 #pragma unroll 1
     for (int j0 = 0; j0 < C::NU; j0 += RB_BATCH) {
-        Pack<float, C::U> gate[RB_BATCH], w1[RB_BATCH], b1[RB_BATCH];
-        V a[RB_BATCH], e[RB_BATCH];
+        float gate[RB_BATCH][2], w1[RB_BATCH][2], b1[RB_BATCH][2], a[RB_BATCH][2], e[RB_BATCH][2];
         vector_units<T>(c, w.gate, w.f32, 1.f, g * c.d, j0, gate);
         vector_units<T>(c, w.post_w, w.f32, 1.f, 0, j0, w1);
-        if (FULL) vector_units<T>(c, w.post_b, w.f32, 0.f, 0, j0, b1);
-        auto at = [&](int n, int k) { return reinterpret_cast<V*>(sums + (int64_t)n * c.d + c.column(j0 + k)); };
-#pragma unroll
-        for (int k = 0; k < RB_BATCH; ++k) {
-            if (!c.inside(j0 + k)) continue;
-            a[k] = *at(0, k);
-            if (FULL) e[k] = *at(1, k);
+        vector_units<T>(c, sums, true, 0.f, 0, j0, a);
+        if (FULL) {
+            vector_units<T>(c, w.post_b, w.f32, 0.f, 0, j0, b1);
+            vector_units<T>(c, sums, true, 0.f, c.d, j0, e);
         }
 #pragma unroll
         for (int k = 0; k < RB_BATCH; ++k) {
-            if (!c.inside(j0 + k)) continue;
-            const V x = *c.k(j0 + k), y = *c.w2(j0 + k), gt = *reinterpret_cast<const V*>(&gate[k]);
-            *at(0, k) = fma_(gt, x, a[k]);
-            if (FULL) *at(1, k) = fma_(gt, y, e[k]);
-            if (!dgate) continue;
-            V o = mul_(*reinterpret_cast<const V*>(&w1[k]), x);
-            if (FULL) o = fma_(*reinterpret_cast<const V*>(&b1[k]), y, o);
+            const float2 x = split(*places.k(j0 + k)), y = split(*places.w2(j0 + k));
 #pragma unroll
-            for (int i = 0; i < C::U; ++i) {
-                const int col = c.column(j0 + k) + i;
-                const float out = reinterpret_cast<const float*>(&o)[i];
+            for (int i = 0; i < 2; ++i) {
+                if (!c.inside(j0 + k, i)) continue;
+                const int col = c.column(j0 + k, i);
+                const float xs = i ? x.y : x.x, ys = i ? y.y : y.x;
+                sums[col] = fmaf(gate[k][i], xs, a[k][i]);
+                if (FULL) sums[c.d + col] = fmaf(gate[k][i], ys, e[k][i]);
+                if (!dgate) continue;
+                float out = w1[k][i] * xs;
+                if (FULL) out = fmaf(b1[k][i], ys, out);
                 if (part) part[col] = out;
                 else if (w.f32) static_cast<float*>(dgate)[g * c.d + col] = out;
                 else put(static_cast<T*>(dgate)[g * c.d + col], out);
@@ -177,98 +108,82 @@ __device__ __noinline__ void gate_end(const C c, const RnWeights& w, int64_t g, 
     }
 }
 
-// How rows reach their readers. RB_OWN: a thread fetches the pieces that it reads itself, so no barrier guards the slots.
-// RB_RAGGED: rows of odd addresses, whose values only 2-byte or 4-byte loads could fetch one by one: the threads of a row
-// fetch the 16-byte pieces that cover it and read single values from them, one barrier a row. RB_DIRECT: values are
-// read from global memory in both passes over them (rows too wide for a slot).
-enum RbMode : int { RB_OWN, RB_RAGGED, RB_DIRECT };
-
 // THREADS: at most so many in a CTA, and the stride of a thread's places in shared memory, so that they have fixed
 // distances. Rows that are not there count as zeros, a norm that is not there as one with mean 0 and rstd 1 whose
 // sums are left out: the same instructions serve every kind.
 template <typename T, int VEC, int NV, int THREADS, bool FULL, int MODE>
-__global__ void __launch_bounds__(THREADS, rb_ctas(NV, THREADS)) rn_backward_kernel(RnShape s, RnWeights w, RnBackward b, int grouped) {
-    typedef typename Lanes<VEC>::V V;  // a unit: two values, or one
-    typedef Pack<T, VEC> P;
-    constexpr int U = VEC < 2 ? 1 : 2, NP = NV / VEC, UN = VEC / U, NU = NP * UN, K = FULL ? 8 : 4, A = FULL ? 7 : 3;
-    constexpr int SLOT = MODE == RB_OWN ? 4 * NV * THREADS * (int)sizeof(T) : 4 * rb_cover<T>(NV, THREADS);  // bytes
+__global__ void __launch_bounds__(THREADS, rb_ctas(THREADS)) rn_backward_kernel(RnShape s, RnWeights w, RnBackward b, int grouped) {
+    typedef RnColumns<T, VEC, NV> C;
+    typedef typename C::P P;
+    typedef f2 V;
+    constexpr int NP = C::NP, UN = C::UN, NU = C::NU, K = FULL ? 8 : 4, A = FULL ? 7 : 3;
+    constexpr int NEXT = MODE == RN_OWN ? NV * THREADS * (int)sizeof(T) : rn_cover<T>(NV, THREADS);  // from tensor to tensor, bytes
+    constexpr int SLOT = 4 * NEXT;
     __shared__ float red[2][THREADS / 32 * K];
     extern __shared__ __align__(16) uint8_t rb_smem[];
     griddep_wait();
     griddep_launch();
     const int tpr = s.warps * 32, t = threadIdx.x % tpr, group = threadIdx.x / tpr, lane = threadIdx.x & 31;
-    const int step = tpr * VEC, c0 = t * VEC;
-    const int np = c0 < s.d ? min(NP, (s.d - c0 + step - 1) / step) : 0;
+    const C cols(t, tpr, s.d);
     const bool post = s.post != 0;
     const T* const rows[4] = {static_cast<const T*>(b.dz), static_cast<const T*>(b.h), static_cast<const T*>(b.dh),
                               static_cast<const T*>(b.u)};
     const int64_t worker = (int64_t)blockIdx.x * s.groups + group, first = worker * s.chunk;
     const int total_rows = first < s.rows ? (int)(s.rows - first < s.chunk ? s.rows - first : s.chunk) : 0;
 
-    // this thread's units of w2 and of k
-    V* const wsm = reinterpret_cast<V*>(rb_smem) + threadIdx.x;
-    const RbColumns<U, UN, NU, THREADS> cols{c0, step, np, s.d, wsm};
+    const RbPlaces<C, THREADS> places{reinterpret_cast<V*>(rb_smem) + threadIdx.x};
     // A slot: the thread's pieces of the four tensors (own points at the first of them), or the 16-byte pieces that cover
     // the groups' rows.
-    uint8_t* const slots = rb_smem + 2 * NU * THREADS * sizeof(V);
-    uint8_t* const own = slots + (MODE == RB_OWN ? threadIdx.x * sizeof(P) : group * (tpr * NV * (int)sizeof(T) + 32));
-    constexpr int NEXT = MODE == RB_OWN ? NP * THREADS * (int)sizeof(P) : rb_cover<T>(NV, THREADS);  // from tensor to tensor
-    // fetches row i of this worker, whose first value of the thread is value `at` of the tensors
+    uint8_t* const own = rb_smem + 2 * NU * THREADS * sizeof(V) + (MODE == RN_OWN ? threadIdx.x * sizeof(P) : cover_at<T>(group, tpr, NV));
+    // fetches row i of this worker, which starts at value `at` of the tensors
     auto issue = [&](int i, int64_t at, uint8_t* to) {
-        if (MODE == RB_DIRECT) return;
+        if (MODE == RN_DIRECT) return;
         if (i < total_rows) {
 #pragma unroll
             for (int n = 0; n < 4; ++n) {
                 if (!rows[n]) continue;
-                if (MODE == RB_RAGGED) {
-                    cover_row(to + n * NEXT, rows[n], s.rows * s.d, at - c0, s.d, t, tpr);
+                if (MODE == RN_RAGGED) {
+                    cover_row(to + n * NEXT, rows[n], s.rows * s.d, at, s.d, t, tpr);
                     continue;
                 }
                 const T* const from = rows[n] + at;
 #pragma unroll
                 for (int q = 0; q < NP; ++q)
-                    if (q < np) fetch(reinterpret_cast<P*>(to + n * NEXT + q * THREADS * sizeof(P)), reinterpret_cast<const P*>(from + q * step));
+                    if (q < cols.np) copy_async<sizeof(P)>(to + n * NEXT + q * THREADS * sizeof(P), from + cols.start(q));
             }
         }
-        asm volatile("cp.async.commit_group;" ::: "memory");
+        committed();
     };
     // Piece q of tensor n. Beyond the row and of tensors that are not there: zeros, which lie in the slots.
-    auto take = [&](int n, const uint8_t* here, int64_t at, int q) {
+    auto take = [&](int n, const T* from, int q) {
+        if (MODE == RN_OWN) return *reinterpret_cast<const P*>(reinterpret_cast<const uint8_t*>(from) + q * THREADS * sizeof(P));
+        if (rows[n]) return cols.load(from, q);
         P p;
-        if (MODE == RB_OWN) {
-            p = *reinterpret_cast<const P*>(here + n * NEXT + q * THREADS * sizeof(P));
-        } else {
-            memset(&p, 0, sizeof(p));
-            if (rows[n] && q < np) {
-                if (MODE == RB_DIRECT) p = *reinterpret_cast<const P*>(rows[n] + at + q * step);
-                else p = *reinterpret_cast<const P*>(here + n * NEXT + offset_of(rows[n] + (at - c0)) + (c0 + q * step) * (int)sizeof(T));
-            }
-        }
+        memset(&p, 0, sizeof(p));
         return p;
     };
 
-    if (MODE == RB_OWN) {
+    if (MODE == RN_OWN) {
         P zero;
         memset(&zero, 0, sizeof(zero));
         for (int n = 0; n < 4; ++n)
             for (int k = 0; k < s.slots; ++k)
-                for (int q = rows[n] ? np : 0; q < NP; ++q)
+                for (int q = rows[n] ? cols.np : 0; q < NP; ++q)
                     *reinterpret_cast<P*>(own + k * SLOT + n * NEXT + q * THREADS * sizeof(P)) = zero;
     }
-    int64_t at = first * s.d + c0;
+    int64_t at = first * s.d;
     for (int k = 0; k < s.slots - 1; ++k) issue(k, at + (int64_t)k * s.d, own + k * SLOT);
     const float2 plain = make_float2(0.f, 1.f);
     const float2 *const stats1 = post ? b.post_stats + first : nullptr, *const stats2 = s.pre ? b.pre_stats + first : nullptr;
     float2 next1 = post && total_rows ? stats1[0] : plain, next2 = s.pre && total_rows ? stats2[0] : plain;
     float ksum = 0.f;
     if (total_rows) {
-        ksum = make_weights<T>(cols, w, grouped ? first / s.gate_rows : 0);
+        ksum = make_weights<T>(cols, places, w, grouped ? first / s.gate_rows : 0);
         if (grouped && b.part) {
             float* const sums = b.gsum + 2 * worker * s.d;
-            for (int j = 0; j < np * UN; ++j) {
-                *reinterpret_cast<V*>(sums + cols.column(j)) = both<V>(0.f);
-                if (FULL) *reinterpret_cast<V*>(sums + s.d + cols.column(j)) = both<V>(0.f);
-            }
+            for (int c = t; c < (FULL ? 2 : 1) * s.d; c += tpr) sums[c] = 0.f;
+            __threadfence_block();
+            named_bar_sync(1 + group, tpr);
         }
     }
     // sums of a thread's columns: dw2, db2, S / c, B / c
@@ -291,16 +206,21 @@ __global__ void __launch_bounds__(THREADS, rb_ctas(NV, THREADS)) rn_backward_ker
         }
 #pragma unroll 1
         for (; row < stop; ++row) {
-            if (MODE == RB_RAGGED) {  // the row is there for all its threads, and they are done with the one before
+            if (MODE == RN_RAGGED) {  // the row is there for all its threads, and they are done with the one before
                 fetched(s.slots > 1 ? s.slots - 2 : 0);
                 named_bar_sync(1 + group, tpr);
             }
             issue(row + s.slots - 1, at + (int64_t)(s.slots - 1) * s.d, here == own ? own + (s.slots - 1) * SLOT : here - SLOT);
-            if (MODE == RB_RAGGED && s.slots == 1) {
+            if (MODE == RN_RAGGED && s.slots == 1) {
                 fetched(0);
                 named_bar_sync(1 + group, tpr);
             }
-            if (MODE == RB_OWN) fetched(s.slots - 1);
+            if (MODE == RN_OWN) fetched(s.slots - 1);
+            const T* from[4];
+#pragma unroll
+            for (int n = 0; n < 4; ++n)
+                from[n] = MODE == RN_DIRECT ? rows[n] + at
+                                            : reinterpret_cast<const T*>(here + n * NEXT + (MODE == RN_RAGGED ? offset_of(rows[n] + at) : 0));
             const V neg1 = both<V>(-next1.x * next1.y), rs1 = both<V>(next1.y), rs2 = both<V>(next2.y);
             const float rstd1 = next1.y, rstd2 = next2.y, off2 = -next2.x * next2.y;
             if (row + 1 < total_rows) {
@@ -315,12 +235,12 @@ __global__ void __launch_bounds__(THREADS, rb_ctas(NV, THREADS)) rn_backward_ker
                 for (int i = 0; i < A; ++i) a[i] = both<V>(0.f);
 #pragma unroll
                 for (int q = 0; q < NP; ++q) {
-                    const P pz = take(0, here, at, q), ph = take(1, here, at, q), pd = take(2, here, at, q), pu = take(3, here, at, q);
+                    const P pz = take(0, from[0], q), ph = take(1, from[1], q), pd = take(2, from[2], q), pu = take(3, from[3], q);
 #pragma unroll
                     for (int i = 0; i < UN; ++i) {
                         const int j = q * UN + i;
-                        const V z = unit_of(pz, i), hn = fma_(unit_of(ph, i), rs2, neg2), gy = mul_(z, *cols.w2(j));
-                        const V e = fma_(rs2, gy, unit_of(pd, i)), k = *cols.k(j), ku = mul_(k, fma_(unit_of(pu, i), rs1, neg1));
+                        const V z = unit_of(pz, i), hn = fma_(unit_of(ph, i), rs2, neg2), gy = mul_(z, *places.w2(j));
+                        const V e = fma_(rs2, gy, unit_of(pd, i)), k = *places.k(j), ku = mul_(k, fma_(unit_of(pu, i), rs1, neg1));
                         sp[j] = fma_(z, hn, sp[j]);
                         a[0] = fma_(gy, hn, a[0]);
                         a[1] = fma_(ku, e, a[1]);
@@ -370,26 +290,24 @@ __global__ void __launch_bounds__(THREADS, rb_ctas(NV, THREADS)) rn_backward_ker
             const V o1 = both<V>(scale), o2 = both<V>(back * m1), o3 = both<V>(back * m0);
 #pragma unroll
             for (int q = 0; q < NP; ++q) {
-                const P pz = take(0, here, at, q), ph = take(1, here, at, q), pd = take(2, here, at, q), pu = take(3, here, at, q);
+                const P pz = take(0, from[0], q), ph = take(1, from[1], q), pd = take(2, from[2], q), pu = take(3, from[3], q);
                 P px, pv;
 #pragma unroll
                 for (int i = 0; i < UN; ++i) {
                     const int j = q * UN + i;
                     V dt = unit_of(pd, i);
                     if (FULL) dt = add_(dt, b1);
-                    dt = fma_(unit_of(ph, i), a1, fma_(rs2, mul_(unit_of(pz, i), *cols.w2(j)), dt));
+                    dt = fma_(unit_of(ph, i), a1, fma_(rs2, mul_(unit_of(pz, i), *places.w2(j)), dt));
                     put_unit(px, i, mul_(dt, res));
                     const V un = fma_(unit_of(pu, i), rs1, neg1);
                     s1[j] = fma_(dt, un, s1[j]);
                     if (FULL) s2[FULL ? j : 0] = add_(s2[FULL ? j : 0], dt);
                     V m = o3;  // (0 without a post norm: u may be infinite)
                     if (post) m = FULL ? fma_(un, o2, o3) : mul_(un, o2);
-                    put_unit(pv, i, fma_(mul_(dt, *cols.k(j)), o1, m));
+                    put_unit(pv, i, fma_(mul_(dt, *places.k(j)), o1, m));
                 }
-                if (q < np) {
-                    *reinterpret_cast<P*>(static_cast<T*>(b.dx) + at + q * step) = px;
-                    if (b.du) *reinterpret_cast<P*>(static_cast<T*>(b.du) + at + q * step) = pv;
-                }
+                cols.store(static_cast<T*>(b.dx) + at, q, px);
+                if (b.du) cols.store(static_cast<T*>(b.du) + at, q, pv);
             }
             here = here == own + (s.slots - 1) * SLOT ? own : here + SLOT;
             at += s.d;
@@ -403,16 +321,16 @@ __global__ void __launch_bounds__(THREADS, rb_ctas(NV, THREADS)) rn_backward_ker
             const V branch = both<V>(s.branch);
 #pragma unroll
             for (int j = 0; j < NU; ++j) {
-                *cols.k(j) = mul_(s1[j], branch);
-                if (FULL) *cols.w2(j) = mul_(s2[FULL ? j : 0], branch);
+                *places.k(j) = mul_(s1[j], branch);
+                if (FULL) *places.w2(j) = mul_(s2[FULL ? j : 0], branch);
                 s1[j] = both<V>(0.f);
                 if (FULL) s2[FULL ? j : 0] = both<V>(0.f);
             }
-            if (b.part) gate_end<T, FULL>(cols, w, g, b.gsum + 2 * worker * s.d, whole ? nullptr : p, b.dgate);
-            if (row < total_rows) ksum = make_weights<T>(cols, w, g + 1);
+            if (b.part) gate_end<T, FULL>(cols, places, w, g, b.gsum + 2 * worker * s.d, whole ? nullptr : p, b.dgate);
+            if (row < total_rows) ksum = make_weights<T>(cols, places, w, g + 1);
         }
     }
-    if (MODE != RB_DIRECT) fetched(0);
+    if (MODE != RN_DIRECT) fetched(0);
     if (!b.part) return;
     const V branch = both<V>(s.branch);
 #pragma unroll
@@ -420,10 +338,17 @@ __global__ void __launch_bounds__(THREADS, rb_ctas(NV, THREADS)) rn_backward_ker
         if (!grouped) {
             s1[j] = mul_(s1[j], branch);
             if (FULL) s2[FULL ? j : 0] = mul_(s2[FULL ? j : 0], branch);
-        } else if (total_rows && cols.inside(j)) {  // dw1 and db1 in the place of S and B
-            const float* const sums = b.gsum + 2 * worker * s.d + cols.column(j);
-            s1[j] = *reinterpret_cast<const V*>(sums);
-            if (FULL) s2[FULL ? j : 0] = *reinterpret_cast<const V*>(sums + s.d);
+        } else if (total_rows) {  // dw1 and db1 in the place of S and B
+            const float* const sums = b.gsum + 2 * worker * s.d;
+            float v[2][2] = {{0.f, 0.f}, {0.f, 0.f}};
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                if (!cols.inside(j, i)) continue;
+                v[0][i] = sums[cols.column(j, i)];
+                if (FULL) v[1][i] = sums[s.d + cols.column(j, i)];
+            }
+            s1[j] = pair(v[0][0], v[0][1]);
+            if (FULL) s2[FULL ? j : 0] = pair(v[1][0], v[1][1]);
         }
     }
     // the groups' sums one after another in shared memory, so that the order is the same every time
@@ -436,12 +361,22 @@ __global__ void __launch_bounds__(THREADS, rb_ctas(NV, THREADS)) rn_backward_ker
             float* to = s.groups == 1 ? pw : sums;
 #pragma unroll
             for (int j = 0; j < NU; ++j) {
-                if (!cols.inside(j)) break;
 #pragma unroll
                 for (int n = 0; n < SUMS; ++n) {
                     const V v = n == 0 ? sp[j] : n == SUMS / 2 ? s1[j] : n == 1 ? sq[FULL ? j : 0] : s2[FULL ? j : 0];
-                    V* const p = reinterpret_cast<V*>(to + n * s.d + cols.column(j));  // d is a multiple of the unit
-                    *p = k ? add_(*p, v) : v;
+                    if constexpr (VEC > 1) {
+                        if (!cols.inside(j, 0)) continue;
+                        V* const p = reinterpret_cast<V*>(to + n * s.d + cols.column(j, 0));
+                        *p = k ? add_(*p, v) : v;
+                    } else {
+                        const float2 e = split(v);
+#pragma unroll
+                        for (int i = 0; i < 2; ++i) {
+                            if (!cols.inside(j, i)) continue;
+                            float* const p = to + n * s.d + cols.column(j, i);
+                            *p = (k ? *p : 0.f) + (i ? e.y : e.x);
+                        }
+                    }
                 }
             }
         }
@@ -454,34 +389,34 @@ __global__ void __launch_bounds__(THREADS, rb_ctas(NV, THREADS)) rn_backward_ker
 }  // namespace
 
 template <typename T>
-cudaError_t launch_residual_backward(const RnShape& shape, const RnWeights& w, const RnBackward& b, int vec, bool full,
-                                     bool grouped, int ctas, cudaStream_t st) {
-    RnShape s = shape;
-    const int threads = 32 * s.warps * s.groups, values = rn_backward_values(s.d);
-    auto go = [&](auto width, auto columns, auto most, auto whole, auto how) {
-        constexpr int VEC = decltype(width)::value, NV = decltype(columns)::value, THREADS = decltype(most)::value;
+cudaError_t launch_residual_backward(RnShape s, const RnWeights& w, const RnBackward& b, int vec, bool full, bool grouped,
+                                     int ctas, cudaStream_t st) {
+    const int threads = 32 * s.warps * s.groups;
+    auto go = [&](auto width, auto values, auto most, auto whole, auto how) {
+        constexpr int VEC = decltype(width)::value, NV = decltype(values)::value, THREADS = decltype(most)::value;
         constexpr int MODE = decltype(how)::value;
         constexpr auto kernel = &rn_backward_kernel<T, VEC, NV, THREADS, decltype(whole)::value, MODE>;
-        constexpr size_t weights = (size_t)2 * NV * THREADS * 4;
-        constexpr size_t slot = MODE == RB_DIRECT ? 0 : MODE == RB_OWN ? (size_t)4 * NV * THREADS * sizeof(T) : (size_t)4 * rb_cover<T>(NV, THREADS);
-        constexpr size_t room = RB_SMEM_MOST / rb_ctas(NV, THREADS);
+        constexpr size_t weights = (size_t)2 * NV * THREADS * 4, row = (size_t)4 * NV * THREADS * sizeof(T);
+        constexpr size_t slot = MODE == RN_DIRECT ? 0 : MODE == RN_OWN ? row : (size_t)4 * rn_cover<T>(NV, THREADS);
+        constexpr size_t room = RB_SMEM_MOST / rb_ctas(THREADS);
         static_assert(weights + slot <= RB_SMEM_MOST, "room for a row");
-        s.slots = MODE == RB_DIRECT ? 1 : weights + 3 * slot <= room ? 3 : weights + 2 * slot <= room ? 2 : 1;
+        s.slots = MODE == RN_DIRECT ? 1 : weights + 3 * slot <= room ? 3 : weights + 2 * slot <= room ? 2 : 1;
         size_t smem = weights + s.slots * slot;
         if (s.groups > 1 && smem < (size_t)(full ? 4 : 2) * s.d * 4) smem = (size_t)(full ? 4 : 2) * s.d * 4;
         const cudaError_t e = allow_smem<kernel>(RB_SMEM_MOST);
         if (e != cudaSuccess) return e;
         return launch_k(kernel, dim3(ctas), dim3(threads), smem, st, true, s, w, b, (int)grouped);
     };
-    auto kinds = [&](auto width, auto columns, auto most, auto how) {
-        return full ? go(width, columns, most, std::true_type(), how) : go(width, columns, most, std::false_type(), how);
+    auto kinds = [&](auto width, auto values, auto most, auto how) {
+        return full ? go(width, values, most, std::true_type(), how) : go(width, values, most, std::false_type(), how);
     };
     constexpr int VEC = 16 / sizeof(T);
-    typedef Int<RB_OWN> Own;
-    typedef Int<RB_RAGGED> Ragged;
-    typedef Int<RB_DIRECT> Direct;
+    typedef Int<RN_OWN> Own;
+    typedef Int<RN_RAGGED> Ragged;
+    typedef Int<RN_DIRECT> Direct;
     const bool one = vec == 1;
-    if (values == 32) return one ? kinds(Int<1>(), Int<32>(), Int<512>(), Direct()) : kinds(Int<VEC>(), Int<32>(), Int<512>(), Direct());
+    if (rn_backward_values(s.d) == 32)
+        return one ? kinds(Int<1>(), Int<32>(), Int<512>(), Direct()) : kinds(Int<VEC>(), Int<32>(), Int<512>(), Direct());
     if (threads > 256) return one ? kinds(Int<1>(), Int<16>(), Int<512>(), Ragged()) : kinds(Int<VEC>(), Int<16>(), Int<512>(), Own());
     return one ? kinds(Int<1>(), Int<16>(), Int<256>(), Ragged()) : kinds(Int<VEC>(), Int<16>(), Int<256>(), Own());
 }

@@ -2,6 +2,5 @@
 #include "residual_norm_bwd.cuh"
 
 namespace moe {
-template cudaError_t launch_residual_backward<float>(const RnShape&, const RnWeights&, const RnBackward&, int, bool, bool, int,
-                                                   cudaStream_t);
+template cudaError_t launch_residual_backward<float>(RnShape, const RnWeights&, const RnBackward&, int, bool, bool, int, cudaStream_t);
 }

@@ -1,0 +1,275 @@
+// Forward pass of the residual norm.
+//
+//   h = a x + c gate * post(u), z = pre(h); a norm is (v - mean) rstd w + b, with mean 0 for the mean-square kind
+//
+// The pass reads x and u and writes h and z: HBM bounds it. A group of warps shares a row, which comes through shared
+// memory by cp.async while the row before is worked on. h is rounded to its type before the second norm (the value
+// the backward pass and every other reader sees) and waits in x's place for the pass that writes z.
+#pragma once
+
+#include "residual_norm.cuh"
+
+namespace moe {
+namespace {
+
+constexpr size_t RF_SMEM_MOST = 224 * 1024;
+__host__ __device__ constexpr int rf_ctas(int threads) { return threads > 256 ? 1 : 3; }
+
+template <typename T, int VEC, int NV, int THREADS, bool WF32, int MODE>
+__global__ void __launch_bounds__(THREADS, rf_ctas(THREADS)) rn_forward_kernel(RnShape s, RnWeights w, RnForward f) {
+    typedef RnColumns<T, VEC, NV> C;
+    typedef typename C::P P;
+    constexpr int NP = C::NP, UN = C::UN;
+    constexpr int NEXT = MODE == RN_OWN ? NV * THREADS * (int)sizeof(T) : rn_cover<T>(NV, THREADS);  // from x to u, bytes
+    constexpr int SLOT = 2 * NEXT;
+    __shared__ __align__(16) float red[2][THREADS / 32];
+    extern __shared__ __align__(16) uint8_t rf_smem[];
+    griddep_wait();
+    griddep_launch();
+    const int tpr = s.warps * 32, t = threadIdx.x % tpr, group = threadIdx.x / tpr, lane = threadIdx.x & 31;
+    const C cols(t, tpr, s.d);
+    const T *const x = static_cast<const T*>(f.x), *const u = static_cast<const T*>(f.u);
+    T *const h = static_cast<T*>(f.h), *const z = static_cast<T*>(f.z);
+    const int64_t stride = (int64_t)gridDim.x * s.groups;
+    uint8_t* const own = rf_smem + (MODE == RN_OWN ? threadIdx.x * sizeof(P) : cover_at<T>(group, tpr, NV));
+    // the place of piece q of x (0) or u (1) in the slot at `here`: x's is h's later on
+    auto at = [&](uint8_t* here, int tensor, int q) { return reinterpret_cast<P*>(here + tensor * NEXT + q * THREADS * (int)sizeof(P)); };
+    auto issue = [&](int64_t r, uint8_t* to) {
+        if (r < s.rows) {
+#pragma unroll
+            for (int n = 0; n < 2; ++n) {
+                const T* const rows = n ? u : x;
+                if (!rows) continue;
+                if (MODE == RN_RAGGED) {
+                    cover_row(to + n * NEXT, rows, s.rows * s.d, r * s.d, s.d, t, tpr);
+                } else {
+                    const T* const from = rows + r * s.d;
+#pragma unroll
+                    for (int q = 0; q < NP; ++q)
+                        if (q < cols.np) copy_async<sizeof(P)>(at(to, n, q), from + cols.start(q));
+                }
+            }
+        }
+        committed();
+    };
+    int flip = 0;
+    auto row_sum = [&](f2 v) {
+        float a = warp_sum(total(v));
+        if (s.warps == 1) return a;
+        // [half][8 warps' sums]: the halves in turn, so one barrier a sum is enough
+        float* const r = red[flip] + group * s.warps;
+        flip ^= 1;
+        if (lane == 0) r[t >> 5] = a;
+        named_bar_sync(1 + group, tpr);
+        a = lane < s.warps ? r[lane] : 0.f;
+        return warp_sum(a);
+    };
+    // sum of the squares of values less mu, over the columns of the row
+    auto squares = [&](const P& p, f2 neg, int q, f2 (&sq)[2]) {
+#pragma unroll
+        for (int i = 0; i < UN; ++i) {
+            f2 v = add_(unit_of(p, i), neg);
+            if (VEC == 1) {  // a value beyond the row is no value
+                const float2 e = split(v);
+                v = pair(cols.inside(q, 0) ? e.x : 0.f, cols.inside(q, 1) ? e.y : 0.f);
+            }
+            sq[i & 1] = fma_(v, v, sq[i & 1]);
+        }
+    };
+    // vector p of the weights from the row's column on: unit i of piece q
+    auto coefficients = [&](const void* p, int64_t base, int q, f2 (&k)[UN]) {
+        if constexpr (VEC == 1) {
+            const int c = cols.start(q);
+            float a[2] = {0.f, 0.f};
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+                if (c + i * tpr < s.d) a[i] = WF32 ? static_cast<const float*>(p)[base + c + i * tpr] : num(static_cast<const T*>(p)[base + c + i * tpr]);
+            k[0] = pair(a[0], a[1]);
+        } else if (!w.whole) {
+            float a[VEC];
+#pragma unroll
+            for (int i = 0; i < VEC; ++i) a[i] = value_at<T>(p, WF32, base + cols.start(q) + i, 0.f);
+#pragma unroll
+            for (int i = 0; i < UN; ++i) k[i] = pair(a[2 * i], a[2 * i + 1]);
+        } else if constexpr (WF32) {
+            const float4* const v = reinterpret_cast<const float4*>(static_cast<const float*>(p) + base + cols.start(q));
+#pragma unroll
+            for (int i = 0; i < VEC / 4; ++i) {
+                const float4 e = v[i];
+                k[2 * i] = pair(e.x, e.y);
+                k[2 * i + 1] = pair(e.z, e.w);
+            }
+        } else {
+            const P e = *reinterpret_cast<const P*>(static_cast<const T*>(p) + base + cols.start(q));
+#pragma unroll
+            for (int i = 0; i < UN; ++i) k[i] = unit_of(e, i);
+        }
+    };
+
+    uint8_t* here = own;
+    int64_t r = (int64_t)blockIdx.x * s.groups + group;
+    for (int k = 0; k < s.slots - 1; ++k) issue(r + k * stride, own + k * SLOT);
+    const f2 zero = both<f2>(0.f);
+#pragma unroll 1
+    for (; r < s.rows; r += stride) {
+        if (MODE == RN_RAGGED) {  // the row is there for all its threads, and they are done with the one before
+            fetched(s.slots > 1 ? s.slots - 2 : 0);
+            named_bar_sync(1 + group, tpr);
+        }
+        issue(r + (s.slots - 1) * stride, here == own ? own + (s.slots - 1) * SLOT : here - SLOT);
+        if (MODE == RN_RAGGED && s.slots == 1) {
+            fetched(0);
+            named_bar_sync(1 + group, tpr);
+        }
+        if (MODE == RN_OWN) fetched(s.slots - 1);
+        const T* const rx = reinterpret_cast<const T*>(here + (MODE == RN_RAGGED ? offset_of(x + r * s.d) : 0));
+        const T* const ru = reinterpret_cast<const T*>(here + NEXT + (MODE == RN_RAGGED ? offset_of(u + r * s.d) : 0));
+        auto take = [&](int n, int q) {  // piece q of x (h) or u; pieces beyond the row are left out everywhere
+            if (MODE == RN_OWN) return *at(here, n, q);
+            return cols.load(n ? ru : rx, q);
+        };
+        float mu = 0.f, rs = 1.f;
+        if (s.post) {
+            f2 sq[2] = {zero, zero};
+            if (s.post == MOE_NORM_LAYER) {
+#pragma unroll
+                for (int q = 0; q < NP; ++q) {
+                    if (q >= cols.np) break;
+                    const P p = take(1, q);
+#pragma unroll
+                    for (int i = 0; i < UN; ++i) sq[i & 1] = add_(sq[i & 1], unit_of(p, i));
+                }
+                mu = row_sum(add_(sq[0], sq[1])) * s.inv_d;
+                sq[0] = sq[1] = zero;
+            }
+            const f2 neg = both<f2>(-mu);
+#pragma unroll
+            for (int q = 0; q < NP; ++q) {
+                if (q >= cols.np) break;
+                squares(take(1, q), neg, q, sq);
+            }
+            rs = rsqrtf(fmaf(row_sum(add_(sq[0], sq[1])), s.inv_d, s.eps));
+            if (t == 0 && f.post_stats) f.post_stats[r] = make_float2(mu, rs);
+        }
+        const f2 a = both<f2>(rs), b = both<f2>(-mu * rs), res = both<f2>(s.res), branch = both<f2>(s.branch);
+        const int64_t gate_at = s.gate_rows ? (s.gate_rows >= s.rows ? 0 : r / s.gate_rows * s.d) : 0;
+        f2 sum[2] = {zero, zero};  // of h, or of its squares
+#pragma unroll
+        for (int q = 0; q < NP; ++q) {
+            if (q >= cols.np) break;
+            P px = take(0, q);
+            if (u) {
+                const P pu = take(1, q);
+                f2 v[UN], k[UN];
+#pragma unroll
+                for (int i = 0; i < UN; ++i) v[i] = fma_(unit_of(pu, i), a, b);
+                if (w.post_w) {
+                    coefficients(w.post_w, 0, q, k);
+#pragma unroll
+                    for (int i = 0; i < UN; ++i) v[i] = mul_(v[i], k[i]);
+                }
+                if (w.post_b) {
+                    coefficients(w.post_b, 0, q, k);
+#pragma unroll
+                    for (int i = 0; i < UN; ++i) v[i] = add_(v[i], k[i]);
+                }
+                if (s.gate_rows) {
+                    coefficients(w.gate, gate_at, q, k);
+#pragma unroll
+                    for (int i = 0; i < UN; ++i) v[i] = mul_(v[i], k[i]);
+                }
+#pragma unroll
+                for (int i = 0; i < UN; ++i) put_unit(px, i, fma_(v[i], branch, mul_(unit_of(px, i), res)));
+            } else {
+#pragma unroll
+                for (int i = 0; i < UN; ++i) put_unit(px, i, mul_(unit_of(px, i), res));
+            }
+            if (h) cols.store(h + r * s.d, q, px);
+            if (MODE == RN_OWN) *at(here, 0, q) = px;
+            else cols.store(const_cast<T*>(rx), q, px);
+            if (s.pre == MOE_NORM_LAYER) {
+#pragma unroll
+                for (int i = 0; i < UN; ++i) sum[i & 1] = add_(sum[i & 1], unit_of(px, i));
+            } else {
+                squares(px, zero, q, sum);
+            }
+        }
+        if (s.pre) {
+            mu = 0.f;
+            if (s.pre == MOE_NORM_LAYER) {
+                mu = row_sum(add_(sum[0], sum[1])) * s.inv_d;
+                sum[0] = sum[1] = zero;
+                const f2 neg = both<f2>(-mu);
+#pragma unroll
+                for (int q = 0; q < NP; ++q) {
+                    if (q >= cols.np) break;
+                    squares(take(0, q), neg, q, sum);
+                }
+            }
+            rs = rsqrtf(fmaf(row_sum(add_(sum[0], sum[1])), s.inv_d, s.eps));
+            if (t == 0 && f.pre_stats) f.pre_stats[r] = make_float2(mu, rs);
+            const f2 a2 = both<f2>(rs), b2 = both<f2>(-mu * rs);
+#pragma unroll
+            for (int q = 0; q < NP; ++q) {
+                if (q >= cols.np) break;
+                P p = take(0, q);
+                f2 v[UN], k[UN];
+#pragma unroll
+                for (int i = 0; i < UN; ++i) v[i] = fma_(unit_of(p, i), a2, b2);
+                if (w.pre_w) {
+                    coefficients(w.pre_w, 0, q, k);
+#pragma unroll
+                    for (int i = 0; i < UN; ++i) v[i] = mul_(v[i], k[i]);
+                }
+                if (w.pre_b) {
+                    coefficients(w.pre_b, 0, q, k);
+#pragma unroll
+                    for (int i = 0; i < UN; ++i) v[i] = add_(v[i], k[i]);
+                }
+#pragma unroll
+                for (int i = 0; i < UN; ++i) put_unit(p, i, v[i]);
+                cols.store(z + r * s.d, q, p);
+            }
+        }
+        here = here == own + (s.slots - 1) * SLOT ? own : here + SLOT;
+    }
+    fetched(0);
+}
+
+}  // namespace
+
+template <typename T>
+cudaError_t launch_residual_forward(RnShape s, const RnWeights& w, const RnForward& f, int vec, int sms, cudaStream_t st) {
+    // 64 bytes of a row a thread where the rows fill the device; 16 where they would leave it empty (a row then has four
+    // times as many warps, and is done sooner)
+    constexpr int MANY = 64 / (int)sizeof(T), FEW = 16 / (int)sizeof(T);
+    const bool few = s.rows * rn_warps(s.d, MANY) < 16 * sms && rn_warps(s.d, FEW) <= 32;
+    s.warps = rn_warps(s.d, few ? FEW : MANY);
+    s.groups = s.warps < 8 && !few ? 8 / s.warps : 1;
+    const int threads = 32 * s.warps * s.groups;
+    const int64_t n = (s.rows + s.groups - 1) / s.groups;
+    auto go = [&](auto width, auto values, auto most, auto wide, auto how) {
+        constexpr int VEC = decltype(width)::value, NV = decltype(values)::value, THREADS = decltype(most)::value;
+        constexpr int MODE = decltype(how)::value;
+        constexpr auto kernel = &rn_forward_kernel<T, VEC, NV, THREADS, decltype(wide)::value, MODE>;
+        constexpr size_t slot = 2 * (MODE == RN_OWN ? (size_t)NV * THREADS * sizeof(T) : (size_t)rn_cover<T>(NV, THREADS));
+        constexpr size_t room = RF_SMEM_MOST / rf_ctas(THREADS);
+        s.slots = 3 * slot <= room ? 3 : 2 * slot <= room ? 2 : 1;
+        const int64_t ctas = (int64_t)sms * rf_ctas(THREADS);
+        if (n <= ctas) s.slots = 1;  // a row for each group: nothing to fetch ahead
+        const cudaError_t e = allow_smem<kernel>(RF_SMEM_MOST);
+        if (e != cudaSuccess) return e;
+        return launch_k(kernel, dim3((unsigned)(n < ctas ? n : ctas)), dim3(threads), s.slots * slot, st, true, s, w, f);
+    };
+    auto shaped = [&](auto width, auto wide, auto how) {
+        if (few) return threads <= 256 ? go(width, Int<FEW>(), Int<256>(), wide, how) : go(width, Int<FEW>(), Int<1024>(), wide, how);
+        return threads <= 256 ? go(width, Int<MANY>(), Int<256>(), wide, how) : go(width, Int<MANY>(), Int<1024>(), wide, how);
+    };
+    auto typed = [&](auto width, auto how) {
+        if constexpr (sizeof(T) == 4) return shaped(width, std::true_type(), how);
+        else return w.f32 ? shaped(width, std::true_type(), how) : shaped(width, std::false_type(), how);
+    };
+    return vec == 1 ? typed(Int<1>(), Int<RN_RAGGED>()) : typed(Int<16 / sizeof(T)>(), Int<RN_OWN>());
+}
+
+}  // namespace moe
