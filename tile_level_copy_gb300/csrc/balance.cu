@@ -17,12 +17,12 @@
 namespace moe {
 namespace {
 
-constexpr int BL_THREADS = 256, BL_WARPS = BL_THREADS / 32;
+constexpr int BL_THREADS = 1024, BL_WARPS = BL_THREADS / 32;       // forward: one CTA a SM, so few rows of sums
+constexpr int BL_BACK_THREADS = 256, BL_BACK_WARPS = BL_BACK_THREADS / 32, BL_BACK_CTAS = 4;
 constexpr int BL_NV = 8;           // logits of a lane
-constexpr int BL_CTAS = 4;         // on a SM
-constexpr int BL_MAX_CTAS = 1024;
+constexpr int BL_MAX_CTAS = 256;   // of the forward pass
 constexpr int BL_MAX_E = 256, BL_MAX_K = 8;
-constexpr int BL_END_WARPS = 32;
+constexpr int BL_END_WARPS = 32;   // of the second launch's CTAs, at most
 
 struct BlShape {
     int T, E, k, S, chunk, ctas;  // a CTA takes `chunk` consecutive tokens
@@ -76,6 +76,24 @@ __device__ __forceinline__ float group_sum(float a) {
     for (int o = LPT / 2; o; o >>= 1) a += __shfl_xor_sync(0xffffffffu, a, o);
     return a;
 }
+// Sums of two values over a token's lanes, side by side: one lane's half of the group takes each.
+template <int LPT>
+__device__ __forceinline__ void group_sums(float& a, float& b, int lane) {
+    if (LPT == 1) return;
+    const bool hi = lane & (LPT / 2);
+    const float send = hi ? a : b;
+    float v = (hi ? b : a) + __shfl_xor_sync(0xffffffffu, send, LPT / 2);
+#pragma unroll
+    for (int o = LPT / 4; o; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    const float w = __shfl_xor_sync(0xffffffffu, v, LPT / 2);
+    a = hi ? w : v;
+    b = hi ? v : w;
+}
+__device__ __forceinline__ float exponential(float v) {  // (below 2^-126: zero)
+    float r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v * 1.4426950408889634f));
+    return r;
+}
 // x becomes exp(x - max); returns the maximum (0 if every value is -inf). The difference is taken first: with logits at
 // the type's lowest value the product with log2(e) would overflow.
 template <int LPT>
@@ -87,7 +105,7 @@ __device__ __forceinline__ float exponentials(float (&x)[BL_NV]) {
     for (int o = LPT / 2; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
     if (m == -INFINITY) m = 0.f;
 #pragma unroll
-    for (int i = 0; i < BL_NV; ++i) x[i] = exp2f((x[i] - m) * 1.4426950408889634f);
+    for (int i = 0; i < BL_NV; ++i) x[i] = exponential(x[i] - m);
     return m;
 }
 __device__ __forceinline__ float sum_of(const float (&x)[BL_NV]) {
@@ -110,8 +128,8 @@ struct BlSpace {
 };
 
 template <int LPT, bool VEC>
-__global__ void __launch_bounds__(BL_THREADS, BL_CTAS)
-    balance_kernel(BlShape s, const float* logits, const int32_t* idx, float* lse_out, BlSpace w) {
+__global__ void __launch_bounds__(BL_THREADS, 1)
+    balance_kernel(BlShape s, const float* logits, const int32_t* idx, float* lse_out, float2* kept, BlSpace w) {
     constexpr int TPW = 32 / LPT;  // tokens of a warp
     __shared__ float psum[BL_WARPS][BL_MAX_E];
     __shared__ int cnt[BL_MAX_E];
@@ -133,25 +151,44 @@ __global__ void __launch_bounds__(BL_THREADS, BL_CTAS)
         int n = 0;
 #pragma unroll
         for (int i = 0; i < BL_NV; ++i) p[i] = 0.f;
-        for (int b = pos + warp * TPW; b < end; b += BL_WARPS * TPW) {
+        // a token's logits, mask and (its first LPT) choices are on their way while the token before is worked on
+        float next[BL_NV];
+        int next_e = -1;
+        bool next_live = false;
+        auto fetch = [&](int b) {
             const int t = b + tig;
             const bool there = t < end;
+            load_row<LPT, VEC>(logits + (size_t)t * s.E, there, s.E, lig, next);
+            next_live = there && counted && (!s.mask || s.mask[t]);
+            next_e = there && lig < s.k ? idx[(size_t)t * s.k + lig] : -1;
+        };
+        fetch(pos + warp * TPW);
+#pragma unroll 2
+        for (int b = pos + warp * TPW; b < end; b += BL_WARPS * TPW) {
+            const int t = b + tig, e0 = next_e;
+            const bool there = t < end, live = next_live;
             float x[BL_NV];
-            load_row<LPT, VEC>(logits + (size_t)t * s.E, there, s.E, lig, x);
+#pragma unroll
+            for (int i = 0; i < BL_NV; ++i) x[i] = next[i];
+            fetch(b + BL_WARPS * TPW);
             const float m = exponentials<LPT>(x), sum = group_sum<LPT>(sum_of(x));
-            const float lse = m + logf(sum);
-            if (there && lig == 0 && lse_out) lse_out[t] = lse;
-            if (there && counted && sum != 0.f && (!s.mask || s.mask[t])) {
-                const float inv = 1.0f / sum;
+            const float lse = m + __logf(sum);  // (off by 2^-21 at most: sums are at least 1)
+            const float inv = sum == 0.f ? 0.f : __fdividef(1.0f, sum);
+            if (there && lig == 0) {
+                if (lse_out) lse_out[t] = lse;
+                if (kept) kept[t] = make_float2(m, inv);
+            }
+            if (live && sum != 0.f) {
 #pragma unroll
                 for (int i = 0; i < BL_NV; ++i) p[i] = fmaf(x[i], inv, p[i]);
                 if (lig == 0) {
                     z = fmaf(lse, lse, z);
                     ++n;
                 }
-                for (int j = lig; j < s.k; j += LPT) {
+                if ((unsigned)e0 < (unsigned)s.E) atomicAdd(&cnt[e0], 1);
+                for (int j = lig + LPT; j < s.k; j += LPT) {
                     const int e = idx[(size_t)t * s.k + j];
-                    if (e >= 0 && e < s.E) atomicAdd(&cnt[e], 1);
+                    if ((unsigned)e < (unsigned)s.E) atomicAdd(&cnt[e], 1);
                 }
             }
         }
@@ -182,15 +219,13 @@ __global__ void __launch_bounds__(BL_THREADS, BL_CTAS)
                 row[e] = a;
                 reinterpret_cast<int32_t*>(row)[s.E + e] = cnt[e];
             }
-            if (tid == 0) {
-                float a = 0.f;
-                int c = 0;
-                for (int i = 0; i < BL_WARPS; ++i) {
-                    a += zsum[i];
-                    c += nsum[i];
+            if (warp == 0) {
+                z = warp_sum(zsum[lane]);
+                n = __reduce_add_sync(0xffffffffu, nsum[lane]);
+                if (lane == 0) {
+                    reinterpret_cast<int32_t*>(row)[2 * s.E] = n;
+                    row[2 * s.E + 1] = z;
                 }
-                reinterpret_cast<int32_t*>(row)[2 * s.E] = c;
-                row[2 * s.E + 1] = a;
             }
             __syncthreads();
         }
@@ -198,11 +233,13 @@ __global__ void __launch_bounds__(BL_THREADS, BL_CTAS)
     }
 }
 
-// What balance_backward reads: w_b / S', 2 w_z / N, then a [S, E] without the 1 / S'.
+// What balance_backward reads: w_b / S', 2 w_z / N, a [S, E] without the 1 / S'.
 constexpr int BL_SAVED_HEAD = 4;  // floats
+// Behind them, each token's largest logit and 1 / sum of exp(l - that) (0 for a token without probabilities).
+__host__ __device__ __forceinline__ size_t kept_at(int S, int E) { return (BL_SAVED_HEAD + (size_t)S * E + 1) / 2 * 2; }  // floats
 
 struct BlEnd {
-    int blocks, splits;  // blocks of 32 columns of a row; warps that share a job (a sequence's block)
+    int blocks, splits;  // blocks of 32 columns of a row; warps that share a job (a sequence's block), a power of two
     float wb, wz;
     float* loss;
     int32_t* counts;
@@ -215,27 +252,38 @@ __global__ void __launch_bounds__(BL_END_WARPS * 32) balance_end_kernel(BlShape 
     __shared__ bool am_last;
     griddep_wait();
     griddep_launch();
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, split = warp % f.splits;
-    const int64_t jobs = (int64_t)s.S * f.blocks, per = BL_END_WARPS / f.splits;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, split = warp & (f.splits - 1), warps = blockDim.x >> 5;
+    const int jobs = s.S * f.blocks, per = warps / f.splits;
     const size_t words = part_words(s.E);
-    for (int64_t j0 = blockIdx.x * per; j0 < jobs; j0 += gridDim.x * per) {
-        const int64_t job = j0 + warp / f.splits;
-        const int seq = (int)(job / f.blocks), c = (int)(job % f.blocks) * 32 + lane;
+    for (int j0 = blockIdx.x * per; j0 < jobs; j0 += gridDim.x * per) {
+        const int job = j0 + warp / f.splits;
+        const int seq = job / f.blocks, c = (job - seq * f.blocks) * 32 + lane;
         float a = 0.f, z = 0.f;
         int k = 0, n = 0;
         if (job < jobs) {
             const int from = start_of(s, seq), to = start_of(s, seq + 1);
             if (to > from) {
                 const int end = (to - 1) / s.chunk;
-                for (int b = from / s.chunk + split; b <= end; b += f.splits) {
-                    const float* row = w.part + (size_t)(b + seq) * words;
-                    const int32_t* irow = reinterpret_cast<const int32_t*>(row);
-                    if (c < s.E) {
-                        a += row[c];
-                        k += irow[s.E + c];
+                for (int b = from / s.chunk + split; b <= end; b += 8 * f.splits) {  // eight rows in flight
+                    float va[8], vz[8];
+                    int vk[8], vn[8];
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        const bool there = b + i * f.splits <= end;
+                        const float* row = w.part + (size_t)(b + i * f.splits + seq) * words;
+                        const int32_t* irow = reinterpret_cast<const int32_t*>(row);
+                        va[i] = there && c < s.E ? row[c] : 0.f;
+                        vk[i] = there && c < s.E ? irow[s.E + c] : 0;
+                        vn[i] = there ? irow[2 * s.E] : 0;
+                        vz[i] = there ? row[2 * s.E + 1] : 0.f;
                     }
-                    n += irow[2 * s.E];
-                    z += row[2 * s.E + 1];
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        a += va[i];
+                        k += vk[i];
+                        n += vn[i];
+                        z += vz[i];
+                    }
                 }
             }
         }
@@ -261,7 +309,7 @@ __global__ void __launch_bounds__(BL_END_WARPS * 32) balance_end_kernel(BlShape 
             const float v = warp_sum(slope * a);
             if (lane == 0) {
                 w.value[job] = v;
-                if (job % f.blocks == 0) {
+                if (c < 32) {
                     w.n[seq] = n;
                     w.z[seq] = z;
                 }
@@ -278,7 +326,7 @@ __global__ void __launch_bounds__(BL_END_WARPS * 32) balance_end_kernel(BlShape 
     __threadfence();
     float v = 0.f, z = 0.f;
     int n = 0, used = 0;
-    for (int64_t i = threadIdx.x; i < jobs; i += blockDim.x) v += __ldcg(w.value + i);
+    for (int i = threadIdx.x; i < jobs; i += blockDim.x) v += __ldcg(w.value + i);
     for (int i = threadIdx.x; i < s.S; i += blockDim.x) {
         const int k = __ldcg(w.n + i);
         z += __ldcg(w.z + i);
@@ -297,10 +345,11 @@ __global__ void __launch_bounds__(BL_END_WARPS * 32) balance_end_kernel(BlShape 
     }
     __syncthreads();
     if (warp) return;
-    v = warp_sum(ps[lane][0]);
-    z = warp_sum(zs[lane]);
-    n = __reduce_add_sync(0xffffffffu, ns[lane]);
-    used = __reduce_add_sync(0xffffffffu, cs[lane][0]);
+    const bool mine = lane < warps;
+    v = warp_sum(mine ? ps[lane][0] : 0.f);
+    z = warp_sum(mine ? zs[lane] : 0.f);
+    n = __reduce_add_sync(0xffffffffu, mine ? ns[lane] : 0);
+    used = __reduce_add_sync(0xffffffffu, mine ? cs[lane][0] : 0);
     if (lane) return;
     const float bal = used ? v / (float)used : 0.f, zl = n ? z / (float)n : 0.f;
     // (a loss without weight leaves the sum alone, infinite or not)
@@ -314,25 +363,54 @@ __global__ void __launch_bounds__(BL_END_WARPS * 32) balance_end_kernel(BlShape 
 }
 
 template <int LPT, bool VEC>
-__global__ void __launch_bounds__(BL_THREADS, BL_CTAS)
+__global__ void __launch_bounds__(BL_BACK_THREADS, BL_BACK_CTAS)
     balance_backward_kernel(BlShape s, const float* logits, const int32_t* idx, const float* saved, const float* gates,
                             const float* dgates, const float* dloss, float* dlogits) {
     constexpr int TPW = 32 / LPT;
+    __shared__ __align__(16) float rows[BL_BACK_WARPS][32 * BL_NV];
     griddep_wait();
     griddep_launch();
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, lig = lane % LPT, tig = lane / LPT;
     const int first = blockIdx.x * s.chunk, last = min(s.T, first + s.chunk);
     const float up = dloss ? *dloss : 1.0f, wb = saved[0] * up, wz = saved[1] * up;
     const float* slopes = saved + BL_SAVED_HEAD;
+    const float2* kept = reinterpret_cast<const float2*>(saved + kept_at(s.S, s.E));
     int seq = -2, seq_end = 0;  // this lane's token's, and where it ends
-    float a[BL_NV];
+    float a[BL_NV], next[BL_NV];
 #pragma unroll
     for (int i = 0; i < BL_NV; ++i) a[i] = 0.f;
-    for (int b = first + warp * TPW; b < last; b += BL_WARPS * TPW) {
+    // a token's logits, mask and (its first LPT) pairs are on their way while the token before is worked on
+    int next_e = -1;
+    float next_g = 0.f, next_d = 0.f;
+    float2 next_kept = make_float2(0.f, 0.f);
+    bool next_live = false;
+    auto fetch = [&](int b) {
         const int t = b + tig;
         const bool there = t < last;
+        load_row<LPT, VEC>(logits + (size_t)t * s.E, there, s.E, lig, next);
+        next_live = there && (!s.mask || s.mask[t]);
+        if (there) next_kept = kept[t];
+        if (gates) {
+            const bool pair = there && lig < s.k;
+            const size_t at = (size_t)t * s.k + lig;
+            next_e = pair ? idx[at] : -1;
+            next_g = pair ? gates[at] : 0.f;
+            next_d = pair ? dgates[at] : 0.f;
+        }
+    };
+    float* const mine = rows[warp] + tig * (BL_NV * LPT);  // the token's row, for the gates' part
+    fetch(first + warp * TPW);
+#pragma unroll 1
+    for (int b = first + warp * TPW; b < last; b += BL_BACK_WARPS * TPW) {
+        const int t = b + tig, e0 = next_e;
+        const bool there = t < last;
+        const float g0 = next_g, d0 = next_d;
+        const float m = next_kept.x, inv = next_kept.y;
+        bool live = next_live;
         float x[BL_NV];
-        load_row<LPT, VEC>(logits + (size_t)t * s.E, there, s.E, lig, x);
+#pragma unroll
+        for (int i = 0; i < BL_NV; ++i) x[i] = next[i];
+        fetch(b + BL_BACK_WARPS * TPW);
         if (there && (seq == -2 || t >= seq_end)) {
             seq = sequence_of(s, t);
             seq_end = seq < 0 ? start_of(s, 0) : seq < s.S ? start_of(s, seq + 1) : s.T;
@@ -342,34 +420,68 @@ __global__ void __launch_bounds__(BL_THREADS, BL_CTAS)
                 a[i] = seq >= 0 && seq < s.S && c < s.E ? slopes[(size_t)seq * s.E + c] : 0.f;
             }
         }
-        const float m = exponentials<LPT>(x);
-        float dot = 0.f;
+        float dot = 0.f, gd = g0 * d0;
 #pragma unroll
-        for (int i = 0; i < BL_NV; ++i) dot = fmaf(x[i], a[i], dot);
-        const float sum = group_sum<LPT>(sum_of(x));
-        dot = group_sum<LPT>(dot);
-        const bool live = there && seq >= 0 && seq < s.S && sum != 0.f && (!s.mask || s.mask[t]);
-        if (live) {
-            const float inv = 1.0f / sum;
-            dot *= inv;
-            const float zl = wz * (m + logf(sum)), ib = inv;
+        for (int i = 0; i < BL_NV; ++i) {
+            x[i] = exponential(x[i] - m);
+            dot = fmaf(x[i], a[i], dot);
+        }
+        if (gates) {
+            for (int j = lig + LPT; j < s.k; j += LPT)
+                if (there) gd = fmaf(gates[(size_t)t * s.k + j], dgates[(size_t)t * s.k + j], gd);
+        }
+        group_sums<LPT>(dot, gd, lane);
+        live = live && seq >= 0 && seq < s.S && inv != 0.f;
+        const float zl = wz * (m - __logf(inv));
+        dot *= inv;
 #pragma unroll
-            for (int i = 0; i < BL_NV; ++i) x[i] = x[i] * ib * fmaf(wb, a[i] - dot, zl);
-            if (gates) {
-                const size_t at = (size_t)t * s.k;
-                float gd = 0.f;
-                for (int j = 0; j < s.k; ++j) gd = fmaf(gates[at + j], dgates[at + j], gd);
-                for (int j = 0; j < s.k; ++j) {
-                    const int e = idx[at + j];
-                    const float v = gates[at + j] * (dgates[at + j] - gd);
+        for (int i = 0; i < BL_NV; ++i) x[i] = live ? x[i] * inv * fmaf(wb, a[i] - dot, zl) : 0.f;
+        if (gates) {
+            // through shared memory, where a pair's value finds its expert's place; pairs of one token that name the
+            // same expert go one after another
 #pragma unroll
-                    for (int i = 0; i < BL_NV; ++i)
-                        if (e == column<LPT, VEC>(lig, i) && e < s.E) x[i] += v;
+            for (int i = 0; i < BL_NV; i += 4) {
+                if (VEC) {
+                    *reinterpret_cast<float4*>(mine + column<LPT, VEC>(lig, i)) = make_float4(x[i], x[i + 1], x[i + 2], x[i + 3]);
+                } else {
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) mine[column<LPT, VEC>(lig, i + k)] = x[i + k];
                 }
             }
-        } else {
+            __syncwarp();
+            for (int j0 = 0; j0 < s.k; j0 += LPT) {
+                const int j = j0 + lig;
+                const size_t at = (size_t)t * s.k + j;
+                const bool pair = live && j < s.k;
+                const int e = j0 == 0 ? e0 : pair ? idx[at] : -1;
+                const float v = j0 == 0 ? g0 * (d0 - gd) : pair ? gates[at] * (dgates[at] - gd) : 0.f;
+                const bool good = pair && (unsigned)e < (unsigned)s.E;
+                if (LPT == 1) {
+                    if (good) mine[e] += v;
+                } else {
+                    const uint32_t same = __match_any_sync(0xffffffffu, good ? tig * BL_MAX_E + e : -1 - lane);
+                    if (__any_sync(0xffffffffu, same & (same - 1))) {
+                        for (int k = 0; k < LPT; ++k) {
+                            if (good && lig == k) mine[e] += v;
+                            __syncwarp();
+                        }
+                    } else if (good) {
+                        mine[e] += v;
+                    }
+                }
+                __syncwarp();
+            }
 #pragma unroll
-            for (int i = 0; i < BL_NV; ++i) x[i] = 0.f;
+            for (int i = 0; i < BL_NV; i += 4) {
+                if (VEC) {
+                    const float4 v = *reinterpret_cast<const float4*>(mine + column<LPT, VEC>(lig, i));
+                    x[i] = v.x, x[i + 1] = v.y, x[i + 2] = v.z, x[i + 3] = v.w;
+                } else {
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) x[i + k] = mine[column<LPT, VEC>(lig, i + k)];
+                }
+            }
+            __syncwarp();
         }
         if (!there) continue;
         float* row = dlogits + (size_t)t * s.E;
@@ -407,12 +519,12 @@ int lanes_of(int E) {  // of a token
     while (l * BL_NV < E) l *= 2;
     return l;
 }
-int ctas_of(const moe_balance_config& c, int most) {
-    const int pass = BL_WARPS * 32 / lanes_of(c.E);  // tokens that a CTA has in its registers at once
+int ctas_of(const moe_balance_config& c, int threads, int most) {
+    const int pass = threads / lanes_of(c.E);  // tokens that a CTA has in its registers at once
     const int n = (c.T + pass - 1) / pass;
     return n < 1 ? 1 : n < most ? n : most;
 }
-int most_ctas(const DeviceInfo& di) { return di.sms * BL_CTAS < BL_MAX_CTAS ? di.sms * BL_CTAS : BL_MAX_CTAS; }
+int most_ctas(const DeviceInfo& di) { return di.sms < BL_MAX_CTAS ? di.sms : BL_MAX_CTAS; }
 
 BlShape shape_of(const moe_balance_config& c, const int32_t* offsets, const uint8_t* mask, int ctas) {
     BlShape s;
@@ -465,7 +577,7 @@ MOE_API int moe_balance_workspace_size(const moe_balance_config* c, size_t* byte
     const int rc = check(c);
     if (rc) return rc;
     if (!bytes) return fail(MOE_ERR_ARG, "bytes is NULL");
-    *bytes = space_bytes(*c, ctas_of(*c, BL_MAX_CTAS));
+    *bytes = space_bytes(*c, ctas_of(*c, BL_THREADS, BL_MAX_CTAS));
     return MOE_OK;
 }
 
@@ -474,7 +586,7 @@ MOE_API int moe_balance_saved_size(const moe_balance_config* c, size_t* bytes) {
     const int rc = check(c);
     if (rc) return rc;
     if (!bytes) return fail(MOE_ERR_ARG, "bytes is NULL");
-    *bytes = 4 * (BL_SAVED_HEAD + (size_t)c->seqs * c->E);
+    *bytes = 4 * (kept_at(c->seqs, c->E) + 2 * (size_t)c->T);
     return MOE_OK;
 }
 
@@ -491,7 +603,7 @@ MOE_API int moe_balance_forward(const moe_balance_config* c, const float* logits
         return fail(MOE_ERR_ARG, "a pointer is not aligned (saved and ws to 16 bytes, the others to their type)");
     DeviceInfo di;
     if ((rc = check_device(&di))) return rc;
-    const int ctas = ctas_of(*c, most_ctas(di));
+    const int ctas = ctas_of(*c, BL_THREADS, most_ctas(di));
     const size_t need = space_bytes(*c, ctas);
     if (ws_bytes < need) return fail(MOE_ERR_WORKSPACE, "workspace has %zu bytes, needs %zu", ws_bytes, need);
     const BlShape s = shape_of(*c, offsets, mask, ctas);
@@ -499,7 +611,7 @@ MOE_API int moe_balance_forward(const moe_balance_config* c, const float* logits
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     cudaError_t e = dispatch(c->E, c->E % 4 == 0 && aligned(logits, 16), [&](auto lpt, auto vec) {
         return launch_k(balance_kernel<decltype(lpt)::value, decltype(vec)::value>, dim3(ctas), dim3(BL_THREADS), 0, st, true,
-                        s, logits, idx, lse, w);
+                        s, logits, idx, lse, saved ? reinterpret_cast<float2*>(static_cast<float*>(saved) + kept_at(c->seqs, c->E)) : nullptr, w);
     });
     if (e != cudaSuccess) return cuda_fail(e, "balance loss launch");
     BlEnd f;
@@ -509,9 +621,8 @@ MOE_API int moe_balance_forward(const moe_balance_config* c, const float* logits
     // as many warps on a job as it has rows on average, up to a CTA's
     f.splits = 1;
     while (f.splits < BL_END_WARPS && f.splits < (ctas + c->seqs - 1) / c->seqs) f.splits *= 2;
-    const int64_t jobs = (int64_t)c->seqs * f.blocks, per = BL_END_WARPS / f.splits, n = (jobs + per - 1) / per;
-    e = launch_k(balance_end_kernel, dim3((unsigned)(n < 2 * di.sms ? n : 2 * di.sms)), dim3(BL_END_WARPS * 32), 0, st, true,
-                 s, w, f);
+    const int warps = f.splits < 8 ? 8 : f.splits, jobs = c->seqs * f.blocks, per = warps / f.splits, n = (jobs + per - 1) / per;
+    e = launch_k(balance_end_kernel, dim3(n < 4 * di.sms ? n : 4 * di.sms), dim3(warps * 32), 0, st, true, s, w, f);
     return e == cudaSuccess ? MOE_OK : cuda_fail(e, "balance loss launch");
 }
 
@@ -530,11 +641,11 @@ MOE_API int moe_balance_backward(const moe_balance_config* c, const float* logit
         return fail(MOE_ERR_ARG, "a pointer is not aligned (saved to 16 bytes, the others to their type)");
     DeviceInfo di;
     if ((rc = check_device(&di))) return rc;
-    const int ctas = ctas_of(*c, most_ctas(di));
+    const int ctas = ctas_of(*c, BL_BACK_THREADS, BL_BACK_CTAS * di.sms);
     const BlShape s = shape_of(*c, offsets, mask, ctas);
     const bool vec = c->E % 4 == 0 && aligned(logits, 16) && aligned(dlogits, 16);
     const cudaError_t e = dispatch(c->E, vec, [&](auto lpt, auto v) {
-        return launch_k(balance_backward_kernel<decltype(lpt)::value, decltype(v)::value>, dim3(ctas), dim3(BL_THREADS), 0,
+        return launch_k(balance_backward_kernel<decltype(lpt)::value, decltype(v)::value>, dim3(ctas), dim3(BL_BACK_THREADS), 0,
                         static_cast<cudaStream_t>(stream), true, s, logits, idx, static_cast<const float*>(saved), gates,
                         dgates, dloss, dlogits);
     });

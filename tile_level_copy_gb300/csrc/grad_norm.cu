@@ -3,7 +3,7 @@
 //   norm = sqrt(sum over all tensors of g^2), scale = min(1, max_norm / (norm + eps)); g = g * scale
 //
 // Every value is read once for the norm, read and written once for clipping: HBM traffic bounds both. A CTA takes
-// chunks of 16 KB; a thread squares the 64 bytes of a chunk that it loads in fp32 and adds their sum to a pair of
+// chunks of 32 KB; a thread squares the 128 bytes of a chunk that it loads in fp32 and adds their sum to a pair of
 // floats (sum and what its rounding cut off), so the length of the list costs no precision. The CTAs' sums are added
 // up in 64 bits by the CTA that finishes last, in the order of the CTAs: the result repeats bit for bit.
 // Squares that leave fp32's range are taken again in 64 bits from the registers, so a norm that fp32 can hold is
@@ -16,9 +16,9 @@ namespace moe {
 namespace {
 
 constexpr int GN_THREADS = 256;
-constexpr int GN_VECS = 4;                         // 16-byte pieces of a thread in flight
+constexpr int GN_VECS = 8;                         // 16-byte pieces of a thread in flight
 constexpr int GN_CHUNK = GN_THREADS * GN_VECS;     // pieces of a chunk
-constexpr int GN_CTAS = 4;                         // on a SM
+constexpr int GN_CTAS = 3;                         // on a SM
 constexpr int GN_MOST = 2048;                      // CTAs of a launch
 // Workspace: ticket (zero between calls), sum of the launches before, the CTAs' sums.
 struct GnSpace {

@@ -55,45 +55,43 @@ namespace {
 // global memory wherever they are needed (rows too wide for a slot).
 enum RnMode : int { RN_OWN, RN_RAGGED, RN_DIRECT };
 
-// The columns of a thread, in units of two. VEC > 1: pieces of VEC neighbouring values, piece q of thread t at
-// column (q * threads of the row + t) VEC. VEC = 1: a unit is two values a row's threads apart (single values of
-// neighbouring threads lie beside one another), a piece is a unit.
+// The columns of a thread, in units of two: a warp has 32 NV neighbouring ones, so that a thread's lie at fixed distances.
+// VEC > 1: pieces of VEC neighbouring values, piece q at 32 VEC q. VEC = 1: a unit is two values 32 apart (single
+// values of neighbouring threads lie beside one another), a piece is a unit.
 template <typename T, int VEC, int NV>
 struct RnColumns {
-    static constexpr int PV = VEC == 1 ? 2 : VEC, NP = NV / PV, UN = PV / 2, NU = NV / 2;
+    static constexpr int PV = VEC == 1 ? 2 : VEC, NP = NV / PV, UN = PV / 2, NU = NV / 2, STEP = VEC == 1 ? 64 : 32 * VEC;
     typedef Pack<T, PV> P;
-    int t, tpr, d, np;  // thread of the row, threads of the row, values of the row, this thread's pieces
-    __device__ __forceinline__ RnColumns(int t, int tpr, int d) : t(t), tpr(tpr), d(d) {
-        const int c0 = VEC == 1 ? t : t * VEC, step = VEC == 1 ? 2 * tpr : tpr * VEC;
-        np = c0 < d ? min(NP, (d - c0 + step - 1) / step) : 0;
+    int c0, d, np;  // the first column, values of the row, this thread's pieces
+    __device__ __forceinline__ RnColumns(int t, int d) : d(d) {
+        c0 = (t >> 5) * (32 * NV) + (t & 31) * VEC;
+        np = c0 < d ? min(NP, (d - c0 + STEP - 1) / STEP) : 0;
     }
     __device__ __forceinline__ int column(int j, int i) const {  // of value i of unit j
-        return VEC == 1 ? t + (2 * j + i) * tpr : t * VEC + (j / UN) * (tpr * VEC) + (j % UN) * 2 + i;
+        return VEC == 1 ? c0 + j * STEP + i * 32 : c0 + (j / UN) * STEP + (j % UN) * 2 + i;
     }
     __device__ __forceinline__ bool inside(int j, int i) const { return VEC == 1 ? column(j, i) < d : j / UN < np; }
-    __device__ __forceinline__ int start(int q) const { return VEC == 1 ? t + 2 * q * tpr : t * VEC + q * (tpr * VEC); }
-    // piece q of the row at p (global memory, or its bytes in a slot); values beyond the row are zero
+    // piece q of a row, whose values from column c0 on lie at p (global memory, or its bytes in a slot); values
+    // beyond the row are zero
     __device__ __forceinline__ P load(const T* p, int q) const {
         P r;
         if constexpr (VEC == 1) {
-            const int c = start(q);
             put(r.v[0], 0.f);
             put(r.v[1], 0.f);
-            if (c < d) r.v[0] = p[c];
-            if (c + tpr < d) r.v[1] = p[c + tpr];
+            if (inside(q, 0)) r.v[0] = p[q * STEP];
+            if (inside(q, 1)) r.v[1] = p[q * STEP + 32];
         } else {
-            if (q < np) r = *reinterpret_cast<const P*>(p + start(q));
+            if (q < np) r = *reinterpret_cast<const P*>(p + q * STEP);
             else memset(&r, 0, sizeof(r));
         }
         return r;
     }
     __device__ __forceinline__ void store(T* p, int q, const P& r) const {
         if constexpr (VEC == 1) {
-            const int c = start(q);
-            if (c < d) p[c] = r.v[0];
-            if (c + tpr < d) p[c + tpr] = r.v[1];
+            if (inside(q, 0)) p[q * STEP] = r.v[0];
+            if (inside(q, 1)) p[q * STEP + 32] = r.v[1];
         } else {
-            if (q < np) *reinterpret_cast<P*>(p + start(q)) = r;
+            if (q < np) *reinterpret_cast<P*>(p + q * STEP) = r;
         }
     }
 };

@@ -124,7 +124,7 @@ __global__ void __launch_bounds__(THREADS, rb_ctas(THREADS)) rn_backward_kernel(
     griddep_wait();
     griddep_launch();
     const int tpr = s.warps * 32, t = threadIdx.x % tpr, group = threadIdx.x / tpr, lane = threadIdx.x & 31;
-    const C cols(t, tpr, s.d);
+    const C cols(t, s.d);
     const bool post = s.post != 0;
     const T* const rows[4] = {static_cast<const T*>(b.dz), static_cast<const T*>(b.h), static_cast<const T*>(b.dh),
                               static_cast<const T*>(b.u)};
@@ -146,10 +146,10 @@ __global__ void __launch_bounds__(THREADS, rb_ctas(THREADS)) rn_backward_kernel(
                     cover_row(to + n * NEXT, rows[n], s.rows * s.d, at, s.d, t, tpr);
                     continue;
                 }
-                const T* const from = rows[n] + at;
+                const T* const from = rows[n] + (at + cols.c0);
 #pragma unroll
                 for (int q = 0; q < NP; ++q)
-                    if (q < cols.np) copy_async<sizeof(P)>(to + n * NEXT + q * THREADS * sizeof(P), from + cols.start(q));
+                    if (q < cols.np) copy_async<sizeof(P)>(to + n * NEXT + q * THREADS * sizeof(P), from + q * C::STEP);
             }
         }
         committed();
@@ -219,8 +219,8 @@ __global__ void __launch_bounds__(THREADS, rb_ctas(THREADS)) rn_backward_kernel(
             const T* from[4];
 #pragma unroll
             for (int n = 0; n < 4; ++n)
-                from[n] = MODE == RN_DIRECT ? rows[n] + at
-                                            : reinterpret_cast<const T*>(here + n * NEXT + (MODE == RN_RAGGED ? offset_of(rows[n] + at) : 0));
+                from[n] = MODE == RN_DIRECT ? rows[n] + (at + cols.c0)
+                                            : reinterpret_cast<const T*>(here + n * NEXT + (MODE == RN_RAGGED ? offset_of(rows[n] + at) + cols.c0 * (int)sizeof(T) : 0));
             const V neg1 = both<V>(-next1.x * next1.y), rs1 = both<V>(next1.y), rs2 = both<V>(next2.y);
             const float rstd1 = next1.y, rstd2 = next2.y, off2 = -next2.x * next2.y;
             if (row + 1 < total_rows) {
@@ -306,8 +306,8 @@ __global__ void __launch_bounds__(THREADS, rb_ctas(THREADS)) rn_backward_kernel(
                     if (post) m = FULL ? fma_(un, o2, o3) : mul_(un, o2);
                     put_unit(pv, i, fma_(mul_(dt, *places.k(j)), o1, m));
                 }
-                cols.store(static_cast<T*>(b.dx) + at, q, px);
-                if (b.du) cols.store(static_cast<T*>(b.du) + at, q, pv);
+                cols.store(static_cast<T*>(b.dx) + (at + cols.c0), q, px);
+                if (b.du) cols.store(static_cast<T*>(b.du) + (at + cols.c0), q, pv);
             }
             here = here == own + (s.slots - 1) * SLOT ? own : here + SLOT;
             at += s.d;

@@ -27,7 +27,7 @@ __global__ void __launch_bounds__(THREADS, rf_ctas(THREADS)) rn_forward_kernel(R
     griddep_wait();
     griddep_launch();
     const int tpr = s.warps * 32, t = threadIdx.x % tpr, group = threadIdx.x / tpr, lane = threadIdx.x & 31;
-    const C cols(t, tpr, s.d);
+    const C cols(t, s.d);
     const T *const x = static_cast<const T*>(f.x), *const u = static_cast<const T*>(f.u);
     T *const h = static_cast<T*>(f.h), *const z = static_cast<T*>(f.z);
     const int64_t stride = (int64_t)gridDim.x * s.groups;
@@ -43,10 +43,10 @@ __global__ void __launch_bounds__(THREADS, rf_ctas(THREADS)) rn_forward_kernel(R
                 if (MODE == RN_RAGGED) {
                     cover_row(to + n * NEXT, rows, s.rows * s.d, r * s.d, s.d, t, tpr);
                 } else {
-                    const T* const from = rows + r * s.d;
+                    const T* const from = rows + (r * s.d + cols.c0);
 #pragma unroll
                     for (int q = 0; q < NP; ++q)
-                        if (q < cols.np) copy_async<sizeof(P)>(at(to, n, q), from + cols.start(q));
+                        if (q < cols.np) copy_async<sizeof(P)>(at(to, n, q), from + q * C::STEP);
                 }
             }
         }
@@ -64,35 +64,32 @@ __global__ void __launch_bounds__(THREADS, rf_ctas(THREADS)) rn_forward_kernel(R
         a = lane < s.warps ? r[lane] : 0.f;
         return warp_sum(a);
     };
-    // sum of the squares of values less mu, over the columns of the row
-    auto squares = [&](const P& p, f2 neg, int q, f2 (&sq)[2]) {
+    // adds the squares of a piece's values, less the mean where there is one, over the columns of the row
+    auto squares = [&](const P& p, bool centred, f2 neg, int q, f2 (&sq)[2]) {
 #pragma unroll
         for (int i = 0; i < UN; ++i) {
-            f2 v = add_(unit_of(p, i), neg);
-            if (VEC == 1) {  // a value beyond the row is no value
-                const float2 e = split(v);
-                v = pair(cols.inside(q, 0) ? e.x : 0.f, cols.inside(q, 1) ? e.y : 0.f);
+            f2 v = unit_of(p, i);
+            if (centred) {
+                v = add_(v, neg);
+                if (VEC == 1) {  // a value beyond the row is no value
+                    const float2 e = split(v);
+                    v = pair(cols.inside(q, 0) ? e.x : 0.f, cols.inside(q, 1) ? e.y : 0.f);
+                }
             }
             sq[i & 1] = fma_(v, v, sq[i & 1]);
         }
     };
     // vector p of the weights from the row's column on: unit i of piece q
     auto coefficients = [&](const void* p, int64_t base, int q, f2 (&k)[UN]) {
-        if constexpr (VEC == 1) {
-            const int c = cols.start(q);
-            float a[2] = {0.f, 0.f};
+        base += cols.c0 + q * C::STEP;
+        if (VEC == 1 || !w.whole) {
+            float a[C::PV];
 #pragma unroll
-            for (int i = 0; i < 2; ++i)
-                if (c + i * tpr < s.d) a[i] = WF32 ? static_cast<const float*>(p)[base + c + i * tpr] : num(static_cast<const T*>(p)[base + c + i * tpr]);
-            k[0] = pair(a[0], a[1]);
-        } else if (!w.whole) {
-            float a[VEC];
-#pragma unroll
-            for (int i = 0; i < VEC; ++i) a[i] = value_at<T>(p, WF32, base + cols.start(q) + i, 0.f);
+            for (int i = 0; i < C::PV; ++i) a[i] = VEC > 1 || cols.inside(q, i) ? value_at<T>(p, WF32, base + (VEC == 1 ? 32 * i : i), 0.f) : 0.f;
 #pragma unroll
             for (int i = 0; i < UN; ++i) k[i] = pair(a[2 * i], a[2 * i + 1]);
         } else if constexpr (WF32) {
-            const float4* const v = reinterpret_cast<const float4*>(static_cast<const float*>(p) + base + cols.start(q));
+            const float4* const v = reinterpret_cast<const float4*>(static_cast<const float*>(p) + base);
 #pragma unroll
             for (int i = 0; i < VEC / 4; ++i) {
                 const float4 e = v[i];
@@ -100,7 +97,7 @@ __global__ void __launch_bounds__(THREADS, rf_ctas(THREADS)) rn_forward_kernel(R
                 k[2 * i + 1] = pair(e.z, e.w);
             }
         } else {
-            const P e = *reinterpret_cast<const P*>(static_cast<const T*>(p) + base + cols.start(q));
+            const P e = *reinterpret_cast<const P*>(static_cast<const T*>(p) + base);
 #pragma unroll
             for (int i = 0; i < UN; ++i) k[i] = unit_of(e, i);
         }
@@ -122,8 +119,9 @@ __global__ void __launch_bounds__(THREADS, rf_ctas(THREADS)) rn_forward_kernel(R
             named_bar_sync(1 + group, tpr);
         }
         if (MODE == RN_OWN) fetched(s.slots - 1);
-        const T* const rx = reinterpret_cast<const T*>(here + (MODE == RN_RAGGED ? offset_of(x + r * s.d) : 0));
-        const T* const ru = reinterpret_cast<const T*>(here + NEXT + (MODE == RN_RAGGED ? offset_of(u + r * s.d) : 0));
+        const int64_t row = r * s.d + cols.c0;
+        T* const rx = reinterpret_cast<T*>(here + (MODE == RN_RAGGED ? offset_of(x + r * s.d) : 0)) + (MODE == RN_RAGGED ? cols.c0 : 0);
+        const T* const ru = reinterpret_cast<const T*>(here + NEXT + (MODE == RN_RAGGED ? offset_of(u + r * s.d) : 0)) + (MODE == RN_RAGGED ? cols.c0 : 0);
         auto take = [&](int n, int q) {  // piece q of x (h) or u; pieces beyond the row are left out everywhere
             if (MODE == RN_OWN) return *at(here, n, q);
             return cols.load(n ? ru : rx, q);
@@ -143,11 +141,15 @@ __global__ void __launch_bounds__(THREADS, rf_ctas(THREADS)) rn_forward_kernel(R
                 sq[0] = sq[1] = zero;
             }
             const f2 neg = both<f2>(-mu);
+            auto over = [&](auto centred) {
 #pragma unroll
-            for (int q = 0; q < NP; ++q) {
-                if (q >= cols.np) break;
-                squares(take(1, q), neg, q, sq);
-            }
+                for (int q = 0; q < NP; ++q) {
+                    if (q >= cols.np) break;
+                    squares(take(1, q), decltype(centred)::value, neg, q, sq);
+                }
+            };
+            if (s.post == MOE_NORM_LAYER) over(std::true_type());
+            else over(std::false_type());
             rs = rsqrtf(fmaf(row_sum(add_(sq[0], sq[1])), s.inv_d, s.eps));
             if (t == 0 && f.post_stats) f.post_stats[r] = make_float2(mu, rs);
         }
@@ -184,14 +186,14 @@ __global__ void __launch_bounds__(THREADS, rf_ctas(THREADS)) rn_forward_kernel(R
 #pragma unroll
                 for (int i = 0; i < UN; ++i) put_unit(px, i, mul_(unit_of(px, i), res));
             }
-            if (h) cols.store(h + r * s.d, q, px);
+            if (h) cols.store(h + row, q, px);
             if (MODE == RN_OWN) *at(here, 0, q) = px;
-            else cols.store(const_cast<T*>(rx), q, px);
+            else cols.store(rx, q, px);
             if (s.pre == MOE_NORM_LAYER) {
 #pragma unroll
                 for (int i = 0; i < UN; ++i) sum[i & 1] = add_(sum[i & 1], unit_of(px, i));
             } else {
-                squares(px, zero, q, sum);
+                squares(px, false, zero, q, sum);
             }
         }
         if (s.pre) {
@@ -203,7 +205,7 @@ __global__ void __launch_bounds__(THREADS, rf_ctas(THREADS)) rn_forward_kernel(R
 #pragma unroll
                 for (int q = 0; q < NP; ++q) {
                     if (q >= cols.np) break;
-                    squares(take(0, q), neg, q, sum);
+                    squares(take(0, q), true, neg, q, sum);
                 }
             }
             rs = rsqrtf(fmaf(row_sum(add_(sum[0], sum[1])), s.inv_d, s.eps));
@@ -228,7 +230,7 @@ __global__ void __launch_bounds__(THREADS, rf_ctas(THREADS)) rn_forward_kernel(R
                 }
 #pragma unroll
                 for (int i = 0; i < UN; ++i) put_unit(p, i, v[i]);
-                cols.store(z + r * s.d, q, p);
+                cols.store(z + row, q, p);
             }
         }
         here = here == own + (s.slots - 1) * SLOT ? own : here + SLOT;
