@@ -17,10 +17,9 @@
 namespace moe {
 namespace {
 
-constexpr int BL_THREADS = 1024, BL_WARPS = BL_THREADS / 32;       // forward: one CTA a SM, so few rows of sums
-constexpr int BL_BACK_THREADS = 256, BL_BACK_WARPS = BL_BACK_THREADS / 32, BL_BACK_CTAS = 4;
-constexpr int BL_NV = 8;           // logits of a lane
-constexpr int BL_MAX_CTAS = 256;   // of the forward pass
+constexpr int BL_THREADS = 768, BL_WARPS = BL_THREADS / 32;       // forward: one CTA a SM, so few rows of sums
+constexpr int BL_BACK_THREADS = 256, BL_BACK_WARPS = BL_BACK_THREADS / 32, BL_BACK_CTAS = 3;
+constexpr int BL_MAX_CTAS = 1024;  // of the forward pass
 constexpr int BL_MAX_E = 256, BL_MAX_K = 8;
 constexpr int BL_END_WARPS = 32;   // of the second launch's CTAs, at most
 
@@ -29,44 +28,80 @@ struct BlShape {
     const int32_t* offsets;
     const uint8_t* mask;
 };
-// Where sequence s starts (s = S: where the last one ends), within [0, T] whatever the caller's array holds.
-__device__ __forceinline__ int start_of(const BlShape& s, int i) {
-    if (!s.offsets) return i == 0 ? 0 : s.T;
-    return min(max(s.offsets[i], 0), s.T);
-}
-// The sequence of token t: -1 before the first, S behind the last.
-__device__ __forceinline__ int sequence_of(const BlShape& s, int t) {
-    if (t < start_of(s, 0)) return -1;
-    int lo = 0, hi = s.S;  // the last one that starts at or before t
-    while (lo < hi) {
-        const int mid = (lo + hi + 1) >> 1;
-        if (start_of(s, mid) <= t) lo = mid;
-        else hi = mid - 1;
+// Where sequence i starts (i = S: where the last one ends), within [0, T] whatever the caller's array holds. Up to
+// BL_STARTS - 1 sequences' starts are fetched at once into shared memory: a search through global memory is a chain
+// of waits.
+constexpr int BL_STARTS = 256;
+struct BlStarts {
+    const int32_t* in;  // clamped, in shared memory, or null
+    __device__ __forceinline__ BlStarts(const BlShape& s, int32_t* space) : in(nullptr) {
+        if (!s.offsets || s.S >= BL_STARTS) return;
+        for (int i = threadIdx.x; i <= s.S; i += blockDim.x) space[i] = min(max(s.offsets[i], 0), s.T);
+        __syncthreads();
+        in = space;
     }
-    return lo;
-}
+    __device__ __forceinline__ int operator()(const BlShape& s, int i) const {
+        if (in) return in[i];
+        if (!s.offsets) return i == 0 ? 0 : s.T;
+        return min(max(s.offsets[i], 0), s.T);
+    }
+    // The sequence of token t: -1 before the first, S behind the last.
+    __device__ __forceinline__ int find(const BlShape& s, int t) const {
+        if (!s.offsets) return t < s.T ? 0 : 1;
+        if (t < (*this)(s, 0)) return -1;
+        int lo = 0, hi = s.S;  // the last one that starts at or before t
+        while (lo < hi) {
+            const int mid = (lo + hi + 1) >> 1;
+            if ((*this)(s, mid) <= t) lo = mid;
+            else hi = mid - 1;
+        }
+        return lo;
+    }
+};
 
 // Column of a lane's value i: four neighbours (float4 loads) or every LPT-th.
 template <int LPT, bool VEC>
 __device__ __forceinline__ int column(int lig, int i) {
     return VEC ? ((i >> 2) * LPT + lig) * 4 + (i & 3) : i * LPT + lig;
 }
-// A lane's values of a row; -inf where there is none.
-template <int LPT, bool VEC>
-__device__ __forceinline__ void load_row(const float* row, bool there, int E, int lig, float (&x)[BL_NV]) {
+// A warp's tokens' logits lie side by side in memory, 32 NV of them at most. They come through a ring of BL_DEPTH places
+// of the warp's own in shared memory, fetched by cp.async that many steps ahead: one step held in registers left the
+// memory waiting (few bytes in flight).
+constexpr int BL_DEPTH = 3;
+template <int PLACE, bool VEC>
+__device__ __forceinline__ void fetch_rows(float* to, const float* from, int n, int lane) {
     if (VEC) {
 #pragma unroll
-        for (int q = 0; q < BL_NV / 4; ++q) {
+        for (int k = 0; k < PLACE / 128; ++k)
+            if ((lane + 32 * k) * 4 < n) copy_async<16>(to + (lane + 32 * k) * 4, from + (lane + 32 * k) * 4);
+    } else {
+#pragma unroll
+        for (int k = 0; k < PLACE / 32; ++k)
+            if (lane + 32 * k < n) copy_async<4>(to + lane + 32 * k, from + lane + 32 * k);
+    }
+}
+__device__ __forceinline__ void committed() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void fetched() {  // all but the last N groups
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+// A lane's values of a row, two and two; -inf where there is none.
+template <int LPT, bool VEC, int N2>
+__device__ __forceinline__ void load_row(const float* row, bool there, int E, int lig, f2 (&x)[N2]) {
+    if (VEC) {
+#pragma unroll
+        for (int q = 0; q < N2 / 2; ++q) {
             const int c = (q * LPT + lig) * 4;
             float4 v = make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY);
             if (there && c < E) v = *reinterpret_cast<const float4*>(row + c);
-            x[4 * q] = v.x, x[4 * q + 1] = v.y, x[4 * q + 2] = v.z, x[4 * q + 3] = v.w;
+            x[2 * q] = pair(v.x, v.y);
+            x[2 * q + 1] = pair(v.z, v.w);
         }
     } else {
 #pragma unroll
-        for (int i = 0; i < BL_NV; ++i) {
-            const int c = i * LPT + lig;
-            x[i] = there && c < E ? row[c] : -INFINITY;
+        for (int i = 0; i < N2; ++i) {
+            const int c = 2 * i * LPT + lig;
+            x[i] = pair(there && c < E ? row[c] : -INFINITY, there && c + LPT < E ? row[c + LPT] : -INFINITY);
         }
     }
 }
@@ -89,30 +124,47 @@ __device__ __forceinline__ void group_sums(float& a, float& b, int lane) {
     a = hi ? w : v;
     b = hi ? v : w;
 }
-__device__ __forceinline__ float exponential(float v) {  // (below 2^-126: zero)
+constexpr float BL_LOG2E = 1.4426950408889634f;
+__device__ __forceinline__ float exp2_of(float v) {  // (below 2^-126: zero)
     float r;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v * 1.4426950408889634f));
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
     return r;
 }
-// x becomes exp(x - max); returns the maximum (0 if every value is -inf). The difference is taken first: with logits at
-// the type's lowest value the product with log2(e) would overflow.
-template <int LPT>
-__device__ __forceinline__ float exponentials(float (&x)[BL_NV]) {
-    float m = x[0];
+// x becomes exp(x - m). By one product and sum: what m's product with log2(e) is rounded by is a factor of the whole row,
+// which its sum takes out again. Where that product would leave fp32's range the difference is taken first.
+template <int N2>
+__device__ __forceinline__ void exponentials(f2 (&x)[N2], float m) {
+    const bool far = fabsf(m) > 0x1p126f;
+    const f2 l = both<f2>(BL_LOG2E), c = both<f2>(far ? 0.f : -m * BL_LOG2E);
+    if (far) {
 #pragma unroll
-    for (int i = 1; i < BL_NV; ++i) m = fmaxf(m, x[i]);
+        for (int i = 0; i < N2; ++i) x[i] = add_(x[i], both<f2>(-m));
+    }
+#pragma unroll
+    for (int i = 0; i < N2; ++i) {
+        const float2 v = split(fma_(x[i], l, c));
+        x[i] = pair(exp2_of(v.x), exp2_of(v.y));
+    }
+}
+// The row's largest value, 0 if every one is -inf.
+template <int LPT, int N2>
+__device__ __forceinline__ float largest(const f2 (&x)[N2]) {
+    float m = -INFINITY;
+#pragma unroll
+    for (int i = 0; i < N2; ++i) {
+        const float2 v = split(x[i]);
+        m = fmaxf(m, fmaxf(v.x, v.y));
+    }
 #pragma unroll
     for (int o = LPT / 2; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-    if (m == -INFINITY) m = 0.f;
-#pragma unroll
-    for (int i = 0; i < BL_NV; ++i) x[i] = exponential(x[i] - m);
-    return m;
+    return m == -INFINITY ? 0.f : m;
 }
-__device__ __forceinline__ float sum_of(const float (&x)[BL_NV]) {
-    float a = x[0];
+template <int N2>
+__device__ __forceinline__ float sum_of(const f2 (&x)[N2]) {
+    f2 a = x[0];
 #pragma unroll
-    for (int i = 1; i < BL_NV; ++i) a += x[i];
-    return a;
+    for (int i = 1; i < N2; ++i) a = add_(a, x[i]);
+    return total(a);
 }
 
 // A row of the workspace: ps [E], c [E] (int), n (int), sum of lse^2; an even number of words.
@@ -127,51 +179,70 @@ struct BlSpace {
     float* part;
 };
 
-template <int LPT, bool VEC>
+template <int LPT, int NV, bool VEC>
 __global__ void __launch_bounds__(BL_THREADS, 1)
     balance_kernel(BlShape s, const float* logits, const int32_t* idx, float* lse_out, float2* kept, BlSpace w) {
-    constexpr int TPW = 32 / LPT;  // tokens of a warp
-    __shared__ float psum[BL_WARPS][BL_MAX_E];
+    constexpr int TPW = 32 / LPT, N2 = NV / 2, PLACE = 32 * NV;  // tokens of a warp, a lane's pairs of logits, floats of a place
+    extern __shared__ __align__(16) float bl_smem[];  // [warps][BL_DEPTH][PLACE]; at a sequence's end sums [warps][256]
     __shared__ int cnt[BL_MAX_E];
     __shared__ float zsum[BL_WARPS];
     __shared__ int nsum[BL_WARPS];
     griddep_wait();
     griddep_launch();
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, lig = lane % LPT, tig = lane / LPT;
+    __shared__ int32_t starts_space[BL_STARTS];
+    const BlStarts starts(s, starts_space);
+    const int tid = threadIdx.x, warps = blockDim.x >> 5, warp = tid >> 5, lane = tid & 31, lig = lane % LPT, tig = lane / LPT;
+    float* const ring = bl_smem + warp * (BL_DEPTH * PLACE);
     if (blockIdx.x == 0 && tid == 0) *w.ticket = 0;
     int pos = blockIdx.x * s.chunk;
     const int last = min(s.T, pos + s.chunk);
-    for (int seq = sequence_of(s, pos); pos < last && seq <= s.S; ++seq) {
-        const int end = min(last, seq < 0 ? start_of(s, 0) : seq < s.S ? start_of(s, seq + 1) : s.T);
+    for (int seq = starts.find(s, pos); pos < last && seq <= s.S; ++seq) {
+        const int end = min(last, seq < 0 ? starts(s, 0) : seq < s.S ? starts(s, seq + 1) : s.T);
         if (end <= pos) continue;
         const bool counted = seq >= 0 && seq < s.S;
-        for (int e = tid; e < s.E; e += BL_THREADS) cnt[e] = 0;
+        for (int e = tid; e < s.E; e += blockDim.x) cnt[e] = 0;
         __syncthreads();
-        float p[BL_NV], z = 0.f;
+        f2 p[N2];
+        float z = 0.f;
         int n = 0;
 #pragma unroll
-        for (int i = 0; i < BL_NV; ++i) p[i] = 0.f;
-        // a token's logits, mask and (its first LPT) choices are on their way while the token before is worked on
-        float next[BL_NV];
-        int next_e = -1;
-        bool next_live = false;
-        auto fetch = [&](int b) {
-            const int t = b + tig;
-            const bool there = t < end;
-            load_row<LPT, VEC>(logits + (size_t)t * s.E, there, s.E, lig, next);
-            next_live = there && counted && (!s.mask || s.mask[t]);
-            next_e = there && lig < s.k ? idx[(size_t)t * s.k + lig] : -1;
+        for (int i = 0; i < N2; ++i) p[i] = both<f2>(0.f);
+        // a token's mask and (its first LPT) choices are two steps ahead of it, its logits BL_DEPTH - 1
+        const int step = warps * TPW;
+        int e1 = -1, e2 = -1;
+        bool live1 = false, live2 = false;
+        auto fetch = [&](int t) {
+            const bool there = t < end && counted;
+            e1 = e2;
+            live1 = live2;
+            live2 = there && (!s.mask || s.mask[t]);
+            e2 = there && lig < s.k ? idx[(size_t)t * s.k + lig] : -1;
         };
-        fetch(pos + warp * TPW);
-#pragma unroll 2
-        for (int b = pos + warp * TPW; b < end; b += BL_WARPS * TPW) {
-            const int t = b + tig, e0 = next_e;
-            const bool there = t < end, live = next_live;
-            float x[BL_NV];
+        auto issue = [&](int b, float* to) {
+            if (b < end) fetch_rows<PLACE, VEC>(to, logits + (size_t)b * s.E, min(TPW, end - b) * s.E, lane);
+            committed();
+        };
+        int t = pos + warp * TPW + tig;
+        float* here = ring;
 #pragma unroll
-            for (int i = 0; i < BL_NV; ++i) x[i] = next[i];
-            fetch(b + BL_WARPS * TPW);
-            const float m = exponentials<LPT>(x), sum = group_sum<LPT>(sum_of(x));
+        for (int k = 0; k < BL_DEPTH - 1; ++k) issue(t - tig + k * step, ring + k * PLACE);
+        fetch(t);
+        fetch(t + step);
+#pragma unroll 1
+        for (; t - tig < end; t += step) {
+            const int e0 = e1;
+            const bool there = t < end, live = live1;
+            fetch(t + 2 * step);
+            issue(t - tig + (BL_DEPTH - 1) * step, here == ring ? ring + (BL_DEPTH - 1) * PLACE : here - PLACE);
+            fetched<BL_DEPTH - 1>();
+            __syncwarp();
+            f2 x[N2];
+            load_row<LPT, VEC>(here + tig * s.E, there, s.E, lig, x);
+            here = here == ring + (BL_DEPTH - 1) * PLACE ? ring : here + PLACE;
+            __syncwarp();
+            const float m = largest<LPT>(x);
+            exponentials(x, m);
+            const float sum = group_sum<LPT>(sum_of(x));
             const float lse = m + __logf(sum);  // (off by 2^-21 at most: sums are at least 1)
             const float inv = sum == 0.f ? 0.f : __fdividef(1.0f, sum);
             if (there && lig == 0) {
@@ -179,8 +250,9 @@ __global__ void __launch_bounds__(BL_THREADS, 1)
                 if (kept) kept[t] = make_float2(m, inv);
             }
             if (live && sum != 0.f) {
+                const f2 v = both<f2>(inv);
 #pragma unroll
-                for (int i = 0; i < BL_NV; ++i) p[i] = fmaf(x[i], inv, p[i]);
+                for (int i = 0; i < N2; ++i) p[i] = fma_(x[i], v, p[i]);
                 if (lig == 0) {
                     z = fmaf(lse, lse, z);
                     ++n;
@@ -192,18 +264,43 @@ __global__ void __launch_bounds__(BL_THREADS, 1)
                 }
             }
         }
+        fetched<0>();
+        __syncwarp();
         if (counted) {
+            float v[NV];
 #pragma unroll
-            for (int i = 0; i < BL_NV; ++i)
+            for (int i = 0; i < N2; ++i) {
+                const float2 e = split(p[i]);
+                v[2 * i] = e.x;
+                v[2 * i + 1] = e.y;
+            }
+            // over the warp's tokens: at each step a lane hands half of its columns over and keeps the other half
+            int kept_from = 0;
+            bool writer = true;
 #pragma unroll
-                for (int o = LPT; o < 32; o <<= 1) p[i] += __shfl_xor_sync(0xffffffffu, p[i], o);
+            for (int o = LPT, n = NV; o < 32; o <<= 1) {
+                const bool hi = lane & o;
+                if (n > 1) {
+                    n /= 2;
+#pragma unroll
+                    for (int i = 0; i < n; ++i) {
+                        const float send = hi ? v[i] : v[i + n], keep = hi ? v[i + n] : v[i];
+                        v[i] = keep + __shfl_xor_sync(0xffffffffu, send, o);
+                    }
+                    kept_from += hi ? n : 0;
+                } else {
+                    v[0] += __shfl_xor_sync(0xffffffffu, v[0], o);
+                    writer = writer && !hi;
+                }
+            }
             z = warp_sum(z);
             n = __reduce_add_sync(0xffffffffu, n);
-            if (tig == 0) {
+            constexpr int LEFT = NV > TPW ? NV / TPW : 1;
+            if (writer) {
 #pragma unroll
-                for (int i = 0; i < BL_NV; ++i) {
-                    const int c = column<LPT, VEC>(lig, i);
-                    if (c < s.E) psum[warp][c] = p[i];
+                for (int i = 0; i < LEFT; ++i) {
+                    const int c = column<LPT, VEC>(lig, kept_from + i);
+                    if (c < s.E) ring[c] = v[i];
                 }
             }
             if (lane == 0) {
@@ -212,16 +309,16 @@ __global__ void __launch_bounds__(BL_THREADS, 1)
             }
             __syncthreads();
             float* row = w.part + (size_t)(blockIdx.x + seq) * part_words(s.E);
-            for (int e = tid; e < s.E; e += BL_THREADS) {
+            for (int e = tid; e < s.E; e += blockDim.x) {
                 float a = 0.f;
-#pragma unroll
-                for (int i = 0; i < BL_WARPS; ++i) a += psum[i][e];
+#pragma unroll 8
+                for (int i = 0; i < warps; ++i) a += bl_smem[i * (BL_DEPTH * PLACE) + e];
                 row[e] = a;
                 reinterpret_cast<int32_t*>(row)[s.E + e] = cnt[e];
             }
             if (warp == 0) {
-                z = warp_sum(zsum[lane]);
-                n = __reduce_add_sync(0xffffffffu, nsum[lane]);
+                z = warp_sum(lane < warps ? zsum[lane] : 0.f);
+                n = __reduce_add_sync(0xffffffffu, lane < warps ? nsum[lane] : 0);
                 if (lane == 0) {
                     reinterpret_cast<int32_t*>(row)[2 * s.E] = n;
                     row[2 * s.E + 1] = z;
@@ -252,6 +349,8 @@ __global__ void __launch_bounds__(BL_END_WARPS * 32) balance_end_kernel(BlShape 
     __shared__ bool am_last;
     griddep_wait();
     griddep_launch();
+    __shared__ int32_t starts_space[BL_STARTS];
+    const BlStarts starts(s, starts_space);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, split = warp & (f.splits - 1), warps = blockDim.x >> 5;
     const int jobs = s.S * f.blocks, per = warps / f.splits;
     const size_t words = part_words(s.E);
@@ -261,7 +360,7 @@ __global__ void __launch_bounds__(BL_END_WARPS * 32) balance_end_kernel(BlShape 
         float a = 0.f, z = 0.f;
         int k = 0, n = 0;
         if (job < jobs) {
-            const int from = start_of(s, seq), to = start_of(s, seq + 1);
+            const int from = starts(s, seq), to = starts(s, seq + 1);
             if (to > from) {
                 const int end = (to - 1) / s.chunk;
                 for (int b = from / s.chunk + split; b <= end; b += 8 * f.splits) {  // eight rows in flight
@@ -295,6 +394,7 @@ __global__ void __launch_bounds__(BL_END_WARPS * 32) balance_end_kernel(BlShape 
         }
         __syncthreads();
         if (split == 0 && job < jobs) {
+#pragma unroll 8
             for (int i = 1; i < f.splits; ++i) {
                 a += ps[warp + i][lane];
                 k += cs[warp + i][lane];
@@ -317,13 +417,15 @@ __global__ void __launch_bounds__(BL_END_WARPS * 32) balance_end_kernel(BlShape 
         }
         __syncthreads();
     }
-    if (threadIdx.x == 0) {
+    if (gridDim.x > 1) {
+        if (threadIdx.x == 0) {
+            __threadfence();
+            am_last = atomicAdd(w.ticket, 1u) == gridDim.x - 1;
+        }
+        __syncthreads();
+        if (!am_last) return;
         __threadfence();
-        am_last = atomicAdd(w.ticket, 1u) == gridDim.x - 1;
     }
-    __syncthreads();
-    if (!am_last) return;
-    __threadfence();
     float v = 0.f, z = 0.f;
     int n = 0, used = 0;
     for (int i = threadIdx.x; i < jobs; i += blockDim.x) v += __ldcg(w.value + i);
@@ -362,100 +464,130 @@ __global__ void __launch_bounds__(BL_END_WARPS * 32) balance_end_kernel(BlShape 
     }
 }
 
-template <int LPT, bool VEC>
+template <int LPT, int NV, bool VEC>
 __global__ void __launch_bounds__(BL_BACK_THREADS, BL_BACK_CTAS)
     balance_backward_kernel(BlShape s, const float* logits, const int32_t* idx, const float* saved, const float* gates,
                             const float* dgates, const float* dloss, float* dlogits) {
-    constexpr int TPW = 32 / LPT;
-    __shared__ __align__(16) float rows[BL_BACK_WARPS][32 * BL_NV];
+    constexpr int TPW = 32 / LPT, N2 = NV / 2, PLACE = 32 * NV;
+    extern __shared__ __align__(16) float bl_smem[];  // [warps][BL_DEPTH][PLACE]
     griddep_wait();
     griddep_launch();
+    __shared__ int32_t starts_space[BL_STARTS];
+    const BlStarts starts(s, starts_space);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, lig = lane % LPT, tig = lane / LPT;
     const int first = blockIdx.x * s.chunk, last = min(s.T, first + s.chunk);
-    const float up = dloss ? *dloss : 1.0f, wb = saved[0] * up, wz = saved[1] * up;
+    const float up = dloss ? *dloss : 1.0f, wb = saved[0] * up, wz = saved[1] * up;  // dloss's factor in both
     const float* slopes = saved + BL_SAVED_HEAD;
     const float2* kept = reinterpret_cast<const float2*>(saved + kept_at(s.S, s.E));
     int seq = -2, seq_end = 0;  // this lane's token's, and where it ends
-    float a[BL_NV], next[BL_NV];
+    bool seq_live = false;
+    f2 a[N2];  // w_b / S' times the slopes
 #pragma unroll
-    for (int i = 0; i < BL_NV; ++i) a[i] = 0.f;
-    // a token's logits, mask and (its first LPT) pairs are on their way while the token before is worked on
-    int next_e = -1;
-    float next_g = 0.f, next_d = 0.f;
-    float2 next_kept = make_float2(0.f, 0.f);
-    bool next_live = false;
-    auto fetch = [&](int b) {
-        const int t = b + tig;
+    for (int i = 0; i < N2; ++i) a[i] = both<f2>(0.f);
+    // what a token needs beside its logits, with its first LPT pairs, is two steps ahead of it, the logits BL_DEPTH - 1
+    const int step = BL_BACK_WARPS * TPW;
+    float* const ring = bl_smem + warp * (BL_DEPTH * PLACE);
+    struct Small {
+        int e = -1;
+        float g = 0.f, d = 0.f;
+        float2 kept = {0.f, 0.f};
+        bool live = false;
+    } one, two;
+    auto fetch = [&](int t) {
         const bool there = t < last;
-        load_row<LPT, VEC>(logits + (size_t)t * s.E, there, s.E, lig, next);
-        next_live = there && (!s.mask || s.mask[t]);
-        if (there) next_kept = kept[t];
-        if (gates) {
-            const bool pair = there && lig < s.k;
+        one = two;
+        two.live = there && (!s.mask || s.mask[t]);
+        if (there) two.kept = kept[t];
+        if (gates && there && lig < s.k) {
             const size_t at = (size_t)t * s.k + lig;
-            next_e = pair ? idx[at] : -1;
-            next_g = pair ? gates[at] : 0.f;
-            next_d = pair ? dgates[at] : 0.f;
+            two.e = idx[at];
+            two.g = gates[at];
+            two.d = dgates[at];
         }
     };
-    float* const mine = rows[warp] + tig * (BL_NV * LPT);  // the token's row, for the gates' part
-    fetch(first + warp * TPW);
+    auto issue = [&](int b, float* to) {
+        if (b < last) fetch_rows<PLACE, VEC>(to, logits + (size_t)b * s.E, min(TPW, last - b) * s.E, lane);
+        committed();
+    };
+    int t = first + warp * TPW + tig;
+    float* here = ring;
+#pragma unroll
+    for (int k = 0; k < BL_DEPTH - 1; ++k) issue(t - tig + k * step, ring + k * PLACE);
+    fetch(t);
+    fetch(t + step);
 #pragma unroll 1
-    for (int b = first + warp * TPW; b < last; b += BL_BACK_WARPS * TPW) {
-        const int t = b + tig, e0 = next_e;
+    for (; t - tig < last; t += step) {
+        const int e0 = one.e;
         const bool there = t < last;
-        const float g0 = next_g, d0 = next_d;
-        const float m = next_kept.x, inv = next_kept.y;
-        bool live = next_live;
-        float x[BL_NV];
-#pragma unroll
-        for (int i = 0; i < BL_NV; ++i) x[i] = next[i];
-        fetch(b + BL_BACK_WARPS * TPW);
+        const float g0 = one.g, d0 = one.d, m = one.kept.x, inv = one.kept.y;
+        bool live = one.live;
+        const size_t at = (size_t)t * s.k + lig;
+        fetch(t + 2 * step);
+        issue(t - tig + (BL_DEPTH - 1) * step, here == ring ? ring + (BL_DEPTH - 1) * PLACE : here - PLACE);
+        fetched<BL_DEPTH - 1>();
+        __syncwarp();
+        float* const mine = here + tig * s.E;  // the token's row; then that of its gradient
+        f2 x[N2];
+        load_row<LPT, VEC>(mine, there, s.E, lig, x);
+        here = here == ring + (BL_DEPTH - 1) * PLACE ? ring : here + PLACE;
+        __syncwarp();
         if (there && (seq == -2 || t >= seq_end)) {
-            seq = sequence_of(s, t);
-            seq_end = seq < 0 ? start_of(s, 0) : seq < s.S ? start_of(s, seq + 1) : s.T;
+            seq = starts.find(s, t);
+            seq_end = seq < 0 ? starts(s, 0) : seq < s.S ? starts(s, seq + 1) : s.T;
+            seq_live = seq >= 0 && seq < s.S;
 #pragma unroll
-            for (int i = 0; i < BL_NV; ++i) {
-                const int c = column<LPT, VEC>(lig, i);
-                a[i] = seq >= 0 && seq < s.S && c < s.E ? slopes[(size_t)seq * s.E + c] : 0.f;
+            for (int i = 0; i < N2; ++i) {
+                float v[2];
+#pragma unroll
+                for (int k = 0; k < 2; ++k) {
+                    const int c = column<LPT, VEC>(lig, 2 * i + k);
+                    v[k] = seq_live && c < s.E ? wb * slopes[(size_t)seq * s.E + c] : 0.f;
+                }
+                a[i] = pair(v[0], v[1]);
             }
         }
-        float dot = 0.f, gd = g0 * d0;
+        exponentials(x, m);
+        f2 dots = mul_(x[0], a[0]);
 #pragma unroll
-        for (int i = 0; i < BL_NV; ++i) {
-            x[i] = exponential(x[i] - m);
-            dot = fmaf(x[i], a[i], dot);
-        }
+        for (int i = 1; i < N2; ++i) dots = fma_(x[i], a[i], dots);
+        float dot = total(dots), gd = g0 * d0;
         if (gates) {
-            for (int j = lig + LPT; j < s.k; j += LPT)
-                if (there) gd = fmaf(gates[(size_t)t * s.k + j], dgates[(size_t)t * s.k + j], gd);
+            for (int j = LPT; lig + j < s.k; j += LPT)
+                if (there) gd = fmaf(gates[at + j], dgates[at + j], gd);
         }
         group_sums<LPT>(dot, gd, lane);
-        live = live && seq >= 0 && seq < s.S && inv != 0.f;
-        const float zl = wz * (m - __logf(inv));
-        dot *= inv;
+        live = live && seq_live && inv != 0.f;
+        // p (a - sum p a + z's part): exp(l - m) times inv (a + c)
+        const float c = wz * (m - __logf(inv)) - dot * inv;
+        const f2 vi = both<f2>(inv), vc = both<f2>(c * inv);
 #pragma unroll
-        for (int i = 0; i < BL_NV; ++i) x[i] = live ? x[i] * inv * fmaf(wb, a[i] - dot, zl) : 0.f;
+        for (int i = 0; i < N2; ++i) x[i] = mul_(x[i], fma_(a[i], vi, vc));
+        if (!live) {
+#pragma unroll
+            for (int i = 0; i < N2; ++i) x[i] = both<f2>(0.f);
+        }
         if (gates) {
             // through shared memory, where a pair's value finds its expert's place; pairs of one token that name the
             // same expert go one after another
+            if (VEC) {
 #pragma unroll
-            for (int i = 0; i < BL_NV; i += 4) {
-                if (VEC) {
-                    *reinterpret_cast<float4*>(mine + column<LPT, VEC>(lig, i)) = make_float4(x[i], x[i + 1], x[i + 2], x[i + 3]);
-                } else {
+                for (int q = 0; q < NV / 4; ++q)
+                    if (column<LPT, VEC>(lig, 4 * q) < s.E)
+                        *reinterpret_cast<ulonglong2*>(mine + column<LPT, VEC>(lig, 4 * q)) = make_ulonglong2(x[2 * q], x[2 * q + 1]);
+            } else {
 #pragma unroll
-                    for (int k = 0; k < 4; ++k) mine[column<LPT, VEC>(lig, i + k)] = x[i + k];
+                for (int i = 0; i < N2; ++i) {
+                    const float2 v = split(x[i]);
+                    if (column<LPT, VEC>(lig, 2 * i) < s.E) mine[column<LPT, VEC>(lig, 2 * i)] = v.x;
+                    if (column<LPT, VEC>(lig, 2 * i + 1) < s.E) mine[column<LPT, VEC>(lig, 2 * i + 1)] = v.y;
                 }
             }
             __syncwarp();
             for (int j0 = 0; j0 < s.k; j0 += LPT) {
-                const int j = j0 + lig;
-                const size_t at = (size_t)t * s.k + j;
-                const bool pair = live && j < s.k;
-                const int e = j0 == 0 ? e0 : pair ? idx[at] : -1;
-                const float v = j0 == 0 ? g0 * (d0 - gd) : pair ? gates[at] * (dgates[at] - gd) : 0.f;
-                const bool good = pair && (unsigned)e < (unsigned)s.E;
+                const bool own = live && j0 + lig < s.k;
+                const int e = j0 == 0 ? e0 : own ? idx[at + j0] : -1;
+                const float v = j0 == 0 ? g0 * (d0 - gd) : own ? gates[at + j0] * (dgates[at + j0] - gd) : 0.f;
+                const bool good = own && (unsigned)e < (unsigned)s.E;
                 if (LPT == 1) {
                     if (good) mine[e] += v;
                 } else {
@@ -471,34 +603,42 @@ __global__ void __launch_bounds__(BL_BACK_THREADS, BL_BACK_CTAS)
                 }
                 __syncwarp();
             }
+            if (VEC) {
 #pragma unroll
-            for (int i = 0; i < BL_NV; i += 4) {
-                if (VEC) {
-                    const float4 v = *reinterpret_cast<const float4*>(mine + column<LPT, VEC>(lig, i));
-                    x[i] = v.x, x[i + 1] = v.y, x[i + 2] = v.z, x[i + 3] = v.w;
-                } else {
+                for (int q = 0; q < NV / 4; ++q) {
+                    if (column<LPT, VEC>(lig, 4 * q) >= s.E) continue;
+                    const ulonglong2 v = *reinterpret_cast<const ulonglong2*>(mine + column<LPT, VEC>(lig, 4 * q));
+                    x[2 * q] = v.x;
+                    x[2 * q + 1] = v.y;
+                }
+            } else {
 #pragma unroll
-                    for (int k = 0; k < 4; ++k) x[i + k] = mine[column<LPT, VEC>(lig, i + k)];
+                for (int i = 0; i < N2; ++i) {
+                    const int c = column<LPT, VEC>(lig, 2 * i), d = column<LPT, VEC>(lig, 2 * i + 1);
+                    x[i] = pair(c < s.E ? mine[c] : 0.f, d < s.E ? mine[d] : 0.f);
                 }
             }
             __syncwarp();
         }
         if (!there) continue;
-        float* row = dlogits + (size_t)t * s.E;
+        float* const out = dlogits + (size_t)t * s.E;
         if (VEC) {
 #pragma unroll
-            for (int q = 0; q < BL_NV / 4; ++q) {
+            for (int q = 0; q < NV / 4; ++q) {
                 const int c = (q * LPT + lig) * 4;
-                if (c < s.E) *reinterpret_cast<float4*>(row + c) = make_float4(x[4 * q], x[4 * q + 1], x[4 * q + 2], x[4 * q + 3]);
+                if (c < s.E) *reinterpret_cast<ulonglong2*>(out + c) = make_ulonglong2(x[2 * q], x[2 * q + 1]);
             }
         } else {
 #pragma unroll
-            for (int i = 0; i < BL_NV; ++i) {
-                const int c = i * LPT + lig;
-                if (c < s.E) row[c] = x[i];
+            for (int i = 0; i < N2; ++i) {
+                const float2 v = split(x[i]);
+                const int c = 2 * i * LPT + lig;
+                if (c < s.E) out[c] = v.x;
+                if (c + LPT < s.E) out[c + LPT] = v.y;
             }
         }
     }
+    fetched<0>();
 }
 
 int check(const moe_balance_config* c) {
@@ -514,17 +654,31 @@ int check(const moe_balance_config* c) {
     return MOE_OK;
 }
 
-int lanes_of(int E) {  // of a token
+// Lanes of a token: with eight logits each, as few as hold a row; with more than 128 experts 16 lanes of sixteen: a warp
+// that has one token only spends most of its instructions on what a token costs whatever its row's length
+// (131072 tokens of 256 experts, both passes: 80 us instead of 92).
+int lanes_of(int E) {
     int l = 1;
-    while (l * BL_NV < E) l *= 2;
+    while (l * 8 < E && l < 16) l *= 2;
     return l;
 }
+int values_of(int E) { return E > 128 ? 16 : 8; }
 int ctas_of(const moe_balance_config& c, int threads, int most) {
     const int pass = threads / lanes_of(c.E);  // tokens that a CTA has in its registers at once
     const int n = (c.T + pass - 1) / pass;
     return n < 1 ? 1 : n < most ? n : most;
 }
-int most_ctas(const DeviceInfo& di) { return di.sms < BL_MAX_CTAS ? di.sms : BL_MAX_CTAS; }
+int most_ctas(const DeviceInfo& di, int threads) {
+    const int n = di.sms * (threads < BL_THREADS ? 3 : 1);
+    return n < BL_MAX_CTAS ? n : BL_MAX_CTAS;
+}
+// Large CTAs leave few rows of sums behind (131072 tokens of 256 experts in 67 sequences: the second launch takes 8.7 us
+// instead of 13). Where they would not all have work, or several sequences would end in one of them, small
+// ones are faster (509 tokens of 64 experts in 3 sequences, both passes: 11.7 us instead of 14.3).
+int threads_of(const moe_balance_config& c, int sms) {
+    const int pass = BL_THREADS / lanes_of(c.E);
+    return c.T / pass >= sms / 2 && c.T / c.seqs >= pass ? BL_THREADS : 256;
+}
 
 BlShape shape_of(const moe_balance_config& c, const int32_t* offsets, const uint8_t* mask, int ctas) {
     BlShape s;
@@ -536,6 +690,7 @@ BlShape shape_of(const moe_balance_config& c, const int32_t* offsets, const uint
     return s;
 }
 
+size_t ring_bytes(int threads, int E) { return (size_t)threads / 32 * BL_DEPTH * 32 * values_of(E) * 4; }
 size_t blocks_of(int E) { return ((size_t)E + 31) / 32; }
 size_t space_bytes(const moe_balance_config& c, int ctas) {
     return 256 + align_up(4 * (size_t)c.seqs * (blocks_of(c.E) + 2), 16) + 4 * part_words(c.E) * ((size_t)ctas + c.seqs);
@@ -551,17 +706,17 @@ BlSpace space_of(const moe_balance_config& c, void* ws) {
     return w;
 }
 
-// f(lanes of a token, whole vectors?) for the config.
+// f(lanes of a token, a lane's values, whole vectors?) for the config.
 template <typename F>
 cudaError_t dispatch(int E, bool vec, F f) {
-    auto on = [&](auto lpt) { return vec ? f(lpt, std::true_type()) : f(lpt, std::false_type()); };
+    auto on = [&](auto lpt, auto nv) { return vec ? f(lpt, nv, std::true_type()) : f(lpt, nv, std::false_type()); };
+    if (values_of(E) == 16) return on(Int<16>(), Int<16>());
     switch (lanes_of(E)) {
-        case 1: return on(Int<1>());
-        case 2: return on(Int<2>());
-        case 4: return on(Int<4>());
-        case 8: return on(Int<8>());
-        case 16: return on(Int<16>());
-        default: return on(Int<32>());
+        case 1: return on(Int<1>(), Int<8>());
+        case 2: return on(Int<2>(), Int<8>());
+        case 4: return on(Int<4>(), Int<8>());
+        case 8: return on(Int<8>(), Int<8>());
+        default: return on(Int<16>(), Int<8>());
     }
 }
 
@@ -577,7 +732,7 @@ MOE_API int moe_balance_workspace_size(const moe_balance_config* c, size_t* byte
     const int rc = check(c);
     if (rc) return rc;
     if (!bytes) return fail(MOE_ERR_ARG, "bytes is NULL");
-    *bytes = space_bytes(*c, ctas_of(*c, BL_THREADS, BL_MAX_CTAS));
+    *bytes = space_bytes(*c, ctas_of(*c, 256, BL_MAX_CTAS));
     return MOE_OK;
 }
 
@@ -603,14 +758,17 @@ MOE_API int moe_balance_forward(const moe_balance_config* c, const float* logits
         return fail(MOE_ERR_ARG, "a pointer is not aligned (saved and ws to 16 bytes, the others to their type)");
     DeviceInfo di;
     if ((rc = check_device(&di))) return rc;
-    const int ctas = ctas_of(*c, BL_THREADS, most_ctas(di));
+    const int threads = threads_of(*c, di.sms), ctas = ctas_of(*c, threads, most_ctas(di, threads));
     const size_t need = space_bytes(*c, ctas);
     if (ws_bytes < need) return fail(MOE_ERR_WORKSPACE, "workspace has %zu bytes, needs %zu", ws_bytes, need);
     const BlShape s = shape_of(*c, offsets, mask, ctas);
     const BlSpace w = space_of(*c, ws);
     cudaStream_t st = static_cast<cudaStream_t>(stream);
-    cudaError_t e = dispatch(c->E, c->E % 4 == 0 && aligned(logits, 16), [&](auto lpt, auto vec) {
-        return launch_k(balance_kernel<decltype(lpt)::value, decltype(vec)::value>, dim3(ctas), dim3(BL_THREADS), 0, st, true,
+    cudaError_t e = dispatch(c->E, c->E % 4 == 0 && aligned(logits, 16), [&](auto lpt, auto nv, auto vec) {
+        constexpr auto kernel = &balance_kernel<decltype(lpt)::value, decltype(nv)::value, decltype(vec)::value>;
+        const cudaError_t e0 = allow_smem<kernel>(ring_bytes(BL_THREADS, c->E));
+        if (e0 != cudaSuccess) return e0;
+        return launch_k(kernel, dim3(ctas), dim3(threads), ring_bytes(threads, c->E), st, true,
                         s, logits, idx, lse, saved ? reinterpret_cast<float2*>(static_cast<float*>(saved) + kept_at(c->seqs, c->E)) : nullptr, w);
     });
     if (e != cudaSuccess) return cuda_fail(e, "balance loss launch");
@@ -621,7 +779,7 @@ MOE_API int moe_balance_forward(const moe_balance_config* c, const float* logits
     // as many warps on a job as it has rows on average, up to a CTA's
     f.splits = 1;
     while (f.splits < BL_END_WARPS && f.splits < (ctas + c->seqs - 1) / c->seqs) f.splits *= 2;
-    const int warps = f.splits < 8 ? 8 : f.splits, jobs = c->seqs * f.blocks, per = warps / f.splits, n = (jobs + per - 1) / per;
+    const int jobs = c->seqs * f.blocks, warps = jobs <= BL_END_WARPS / f.splits ? jobs * f.splits : f.splits < 8 ? 8 : f.splits, per = warps / f.splits, n = (jobs + per - 1) / per;
     e = launch_k(balance_end_kernel, dim3(n < 4 * di.sms ? n : 4 * di.sms), dim3(warps * 32), 0, st, true, s, w, f);
     return e == cudaSuccess ? MOE_OK : cuda_fail(e, "balance loss launch");
 }
@@ -644,8 +802,11 @@ MOE_API int moe_balance_backward(const moe_balance_config* c, const float* logit
     const int ctas = ctas_of(*c, BL_BACK_THREADS, BL_BACK_CTAS * di.sms);
     const BlShape s = shape_of(*c, offsets, mask, ctas);
     const bool vec = c->E % 4 == 0 && aligned(logits, 16) && aligned(dlogits, 16);
-    const cudaError_t e = dispatch(c->E, vec, [&](auto lpt, auto v) {
-        return launch_k(balance_backward_kernel<decltype(lpt)::value, decltype(v)::value>, dim3(ctas), dim3(BL_BACK_THREADS), 0,
+    const cudaError_t e = dispatch(c->E, vec, [&](auto lpt, auto nv, auto v) {
+        constexpr auto kernel = &balance_backward_kernel<decltype(lpt)::value, decltype(nv)::value, decltype(v)::value>;
+        const cudaError_t e0 = allow_smem<kernel>(ring_bytes(BL_BACK_THREADS, c->E));
+        if (e0 != cudaSuccess) return e0;
+        return launch_k(kernel, dim3(ctas), dim3(BL_BACK_THREADS), ring_bytes(BL_BACK_THREADS, c->E),
                         static_cast<cudaStream_t>(stream), true, s, logits, idx, static_cast<const float*>(saved), gates,
                         dgates, dloss, dlogits);
     });

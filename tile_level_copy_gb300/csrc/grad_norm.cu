@@ -18,7 +18,7 @@ namespace {
 constexpr int GN_THREADS = 256;
 constexpr int GN_VECS = 8;                         // 16-byte pieces of a thread in flight
 constexpr int GN_CHUNK = GN_THREADS * GN_VECS;     // pieces of a chunk
-constexpr int GN_CTAS = 3;                         // on a SM
+constexpr int GN_CTAS = 4;                         // on a SM
 constexpr int GN_MOST = 2048;                      // CTAs of a launch
 // Workspace: ticket (zero between calls), sum of the launches before, the CTAs' sums.
 struct GnSpace {
@@ -63,10 +63,25 @@ __host__ __device__ __forceinline__ GnSpan span_of(const void* g, int64_t n, int
     return s;
 }
 
+// Sum of the squares of a thread's n pieces at p, a chunk's width apart, in 64 bits. A call, and the values are read again:
+// inlined, on registers, it made the loop over the chunks spill.
+template <typename T>
+__device__ __noinline__ double wide_squares(const Pack<T, 16 / sizeof(T)>* p, int n) {
+    double a = 0.0;
+    for (int k = 0; k < n; ++k) {
+        const Pack<T, 16 / sizeof(T)> e = p[k * GN_THREADS];
+#pragma unroll
+        for (int i = 0; i < 16 / (int)sizeof(T); ++i) {
+            const double v = num(e.v[i]);
+            a += v * v;
+        }
+    }
+    return a;
+}
 // Sum of the squares of a thread's part of a chunk: in fp32 when every square that matters is a normal fp32
 // number, else in 64 bits. Below 2^-110 what subnormal squares lose (2^-150 each) could matter.
 template <typename T, int N, typename Sum>
-__device__ __forceinline__ void add_squares(const Pack<T, 16 / sizeof(T)> (&p)[N], Sum&& sum) {
+__device__ __forceinline__ void add_squares(const Pack<T, 16 / sizeof(T)> (&p)[N], const Pack<T, 16 / sizeof(T)>* from, int n, Sum&& sum) {
     constexpr int VEC = 16 / sizeof(T);
     f2 acc[2] = {pair(0.f, 0.f), pair(0.f, 0.f)};
 #pragma unroll
@@ -87,13 +102,7 @@ __device__ __forceinline__ void add_squares(const Pack<T, 16 / sizeof(T)> (&p)[N
 #pragma unroll
         for (int i = 0; i < 4; ++i) any |= reinterpret_cast<const uint32_t*>(&p[k])[i];
     if (!(any & (sizeof(T) == 4 ? 0x7fffffffu : 0x7fff7fffu))) return;  // nothing but zeros
-#pragma unroll
-    for (int k = 0; k < N; ++k)
-#pragma unroll
-        for (int i = 0; i < VEC; ++i) {
-            const double v = num(p[k].v[i]);
-            sum.far += v * v;
-        }
+    sum.far += wide_squares<T>(from, n);
 }
 
 // A thread's sum: hi + lo, and what fp32 cannot hold.
@@ -127,7 +136,8 @@ __device__ __forceinline__ void chunk_squares(const GnTensor& t, int64_t chunk, 
             else memset(&p[k], 0, sizeof(p[k]));
         }
     }
-    add_squares<T>(p, sum);
+    const int64_t left = sp.pieces - at - threadIdx.x;
+    add_squares<T>(p, body + at + threadIdx.x, left <= 0 ? 0 : left >= GN_CHUNK ? GN_VECS : min(GN_VECS, (int)((left + GN_THREADS - 1) / GN_THREADS)), sum);
     // the values around the pieces: fewer than 8 on each side, in the first chunk
     if (chunk == 0 && threadIdx.x < 16) {
         const int64_t i = threadIdx.x < 8 ? threadIdx.x : threadIdx.x - 8;
@@ -204,20 +214,23 @@ __device__ __forceinline__ void chunk_scale(const GnTensor& t, int64_t chunk, fl
     const GnSpan sp = span_of(t.g, t.n, sizeof(T));
     T* const g = static_cast<T*>(t.g);
     Pack<T, VEC>* const body = reinterpret_cast<Pack<T, VEC>*>(g + sp.head);
-    const int64_t at = chunk * GN_CHUNK + threadIdx.x;
     const f2 by = pair(scale, scale);
-    Pack<T, VEC> p[GN_VECS];
+#pragma unroll 1
+    for (int half = 0; half < 2; ++half) {  // half the pieces at a time: all of them took more registers than there are
+        const int64_t at = chunk * GN_CHUNK + half * (GN_CHUNK / 2) + threadIdx.x;
+        Pack<T, VEC> p[GN_VECS / 2];
 #pragma unroll
-    for (int k = 0; k < GN_VECS; ++k)
-        if (at + k * GN_THREADS < sp.pieces) p[k] = body[at + k * GN_THREADS];
+        for (int k = 0; k < GN_VECS / 2; ++k)
+            if (at + k * GN_THREADS < sp.pieces) p[k] = body[at + k * GN_THREADS];
 #pragma unroll
-    for (int k = 0; k < GN_VECS; ++k) {
-        if (at + k * GN_THREADS >= sp.pieces) break;
-        f2 f[VEC / 2];
-        widen(p[k], f);
+        for (int k = 0; k < GN_VECS / 2; ++k) {
+            if (at + k * GN_THREADS >= sp.pieces) break;
+            f2 f[VEC / 2];
+            widen(p[k], f);
 #pragma unroll
-        for (int i = 0; i < VEC / 2; ++i) f[i] = mul_(f[i], by);
-        body[at + k * GN_THREADS] = narrow<T, VEC>(f);
+            for (int i = 0; i < VEC / 2; ++i) f[i] = mul_(f[i], by);
+            body[at + k * GN_THREADS] = narrow<T, VEC>(f);
+        }
     }
     if (chunk == 0 && threadIdx.x < 16) {
         const int64_t i = threadIdx.x < 8 ? threadIdx.x : threadIdx.x - 8;
