@@ -15,7 +15,7 @@ namespace {
 constexpr size_t RF_SMEM_MOST = 224 * 1024;
 __host__ __device__ constexpr int rf_ctas(int threads) { return threads > 256 ? 1 : 3; }
 
-template <typename T, int VEC, int NV, int THREADS, bool WF32, int MODE>
+template <typename T, int VEC, int NV, int THREADS, bool WF32, bool LAYER, int MODE>
 __global__ void __launch_bounds__(THREADS, rf_ctas(THREADS)) rn_forward_kernel(RnShape s, RnWeights w, RnForward f) {
     typedef RnColumns<T, VEC, NV> C;
     typedef typename C::P P;
@@ -82,12 +82,11 @@ __global__ void __launch_bounds__(THREADS, rf_ctas(THREADS)) rn_forward_kernel(R
     // vector p of the weights from the row's column on: unit i of piece q
     auto coefficients = [&](const void* p, int64_t base, int q, f2 (&k)[UN]) {
         base += cols.c0 + q * C::STEP;
-        if (VEC == 1 || !w.whole) {
-            float a[C::PV];
+        if constexpr (VEC == 1) {
+            float a[2];
 #pragma unroll
-            for (int i = 0; i < C::PV; ++i) a[i] = VEC > 1 || cols.inside(q, i) ? value_at<T>(p, WF32, base + (VEC == 1 ? 32 * i : i), 0.f) : 0.f;
-#pragma unroll
-            for (int i = 0; i < UN; ++i) k[i] = pair(a[2 * i], a[2 * i + 1]);
+            for (int i = 0; i < 2; ++i) a[i] = cols.inside(q, i) ? value_at<T>(p, WF32, base + 32 * i, 0.f) : 0.f;
+            k[0] = pair(a[0], a[1]);
         } else if constexpr (WF32) {
             const float4* const v = reinterpret_cast<const float4*>(static_cast<const float*>(p) + base);
 #pragma unroll
@@ -129,7 +128,7 @@ __global__ void __launch_bounds__(THREADS, rf_ctas(THREADS)) rn_forward_kernel(R
         float mu = 0.f, rs = 1.f;
         if (s.post) {
             f2 sq[2] = {zero, zero};
-            if (s.post == MOE_NORM_LAYER) {
+            if (LAYER && s.post == MOE_NORM_LAYER) {
 #pragma unroll
                 for (int q = 0; q < NP; ++q) {
                     if (q >= cols.np) break;
@@ -148,7 +147,7 @@ __global__ void __launch_bounds__(THREADS, rf_ctas(THREADS)) rn_forward_kernel(R
                     squares(take(1, q), decltype(centred)::value, neg, q, sq);
                 }
             };
-            if (s.post == MOE_NORM_LAYER) over(std::true_type());
+            if (LAYER && s.post == MOE_NORM_LAYER) over(std::true_type());
             else over(std::false_type());
             rs = rsqrtf(fmaf(row_sum(add_(sq[0], sq[1])), s.inv_d, s.eps));
             if (t == 0 && f.post_stats) f.post_stats[r] = make_float2(mu, rs);
@@ -164,13 +163,13 @@ __global__ void __launch_bounds__(THREADS, rf_ctas(THREADS)) rn_forward_kernel(R
                 const P pu = take(1, q);
                 f2 v[UN], k[UN];
 #pragma unroll
-                for (int i = 0; i < UN; ++i) v[i] = fma_(unit_of(pu, i), a, b);
+                for (int i = 0; i < UN; ++i) v[i] = LAYER ? fma_(unit_of(pu, i), a, b) : mul_(unit_of(pu, i), a);
                 if (w.post_w) {
                     coefficients(w.post_w, 0, q, k);
 #pragma unroll
                     for (int i = 0; i < UN; ++i) v[i] = mul_(v[i], k[i]);
                 }
-                if (w.post_b) {
+                if (LAYER && w.post_b) {
                     coefficients(w.post_b, 0, q, k);
 #pragma unroll
                     for (int i = 0; i < UN; ++i) v[i] = add_(v[i], k[i]);
@@ -189,7 +188,7 @@ __global__ void __launch_bounds__(THREADS, rf_ctas(THREADS)) rn_forward_kernel(R
             if (h) cols.store(h + row, q, px);
             if (MODE == RN_OWN) *at(here, 0, q) = px;
             else cols.store(rx, q, px);
-            if (s.pre == MOE_NORM_LAYER) {
+            if (LAYER && s.pre == MOE_NORM_LAYER) {
 #pragma unroll
                 for (int i = 0; i < UN; ++i) sum[i & 1] = add_(sum[i & 1], unit_of(px, i));
             } else {
@@ -198,7 +197,7 @@ __global__ void __launch_bounds__(THREADS, rf_ctas(THREADS)) rn_forward_kernel(R
         }
         if (s.pre) {
             mu = 0.f;
-            if (s.pre == MOE_NORM_LAYER) {
+            if (LAYER && s.pre == MOE_NORM_LAYER) {
                 mu = row_sum(add_(sum[0], sum[1])) * s.inv_d;
                 sum[0] = sum[1] = zero;
                 const f2 neg = both<f2>(-mu);
@@ -217,13 +216,13 @@ __global__ void __launch_bounds__(THREADS, rf_ctas(THREADS)) rn_forward_kernel(R
                 P p = take(0, q);
                 f2 v[UN], k[UN];
 #pragma unroll
-                for (int i = 0; i < UN; ++i) v[i] = fma_(unit_of(p, i), a2, b2);
+                for (int i = 0; i < UN; ++i) v[i] = LAYER ? fma_(unit_of(p, i), a2, b2) : mul_(unit_of(p, i), a2);
                 if (w.pre_w) {
                     coefficients(w.pre_w, 0, q, k);
 #pragma unroll
                     for (int i = 0; i < UN; ++i) v[i] = mul_(v[i], k[i]);
                 }
-                if (w.pre_b) {
+                if (LAYER && w.pre_b) {
                     coefficients(w.pre_b, 0, q, k);
 #pragma unroll
                     for (int i = 0; i < UN; ++i) v[i] = add_(v[i], k[i]);
@@ -250,10 +249,10 @@ cudaError_t launch_residual_forward(RnShape s, const RnWeights& w, const RnForwa
     s.groups = s.warps < 8 && !few ? 8 / s.warps : 1;
     const int threads = 32 * s.warps * s.groups;
     const int64_t n = (s.rows + s.groups - 1) / s.groups;
-    auto go = [&](auto width, auto values, auto most, auto wide, auto how) {
+    auto go = [&](auto width, auto values, auto most, auto wide, auto layer, auto how) {
         constexpr int VEC = decltype(width)::value, NV = decltype(values)::value, THREADS = decltype(most)::value;
         constexpr int MODE = decltype(how)::value;
-        constexpr auto kernel = &rn_forward_kernel<T, VEC, NV, THREADS, decltype(wide)::value, MODE>;
+        constexpr auto kernel = &rn_forward_kernel<T, VEC, NV, THREADS, decltype(wide)::value, decltype(layer)::value, MODE>;
         constexpr size_t slot = 2 * (MODE == RN_OWN ? (size_t)NV * THREADS * sizeof(T) : (size_t)rn_cover<T>(NV, THREADS));
         constexpr size_t room = RF_SMEM_MOST / rf_ctas(THREADS);
         s.slots = 3 * slot <= room ? 3 : 2 * slot <= room ? 2 : 1;
@@ -263,15 +262,19 @@ cudaError_t launch_residual_forward(RnShape s, const RnWeights& w, const RnForwa
         if (e != cudaSuccess) return e;
         return launch_k(kernel, dim3((unsigned)(n < ctas ? n : ctas)), dim3(threads), s.slots * slot, st, true, s, w, f);
     };
-    auto shaped = [&](auto width, auto wide, auto how) {
-        if (few) return threads <= 256 ? go(width, Int<FEW>(), Int<256>(), wide, how) : go(width, Int<FEW>(), Int<1024>(), wide, how);
-        return threads <= 256 ? go(width, Int<MANY>(), Int<256>(), wide, how) : go(width, Int<MANY>(), Int<1024>(), wide, how);
+    auto shaped = [&](auto width, auto wide, auto layer, auto how) {
+        if (few) return threads <= 256 ? go(width, Int<FEW>(), Int<256>(), wide, layer, how) : go(width, Int<FEW>(), Int<1024>(), wide, layer, how);
+        return threads <= 256 ? go(width, Int<MANY>(), Int<256>(), wide, layer, how) : go(width, Int<MANY>(), Int<1024>(), wide, layer, how);
+    };
+    auto kinds = [&](auto width, auto wide, auto how) {
+        return s.post == MOE_NORM_LAYER || s.pre == MOE_NORM_LAYER ? shaped(width, wide, std::true_type(), how)
+                                                                   : shaped(width, wide, std::false_type(), how);
     };
     auto typed = [&](auto width, auto how) {
-        if constexpr (sizeof(T) == 4) return shaped(width, std::true_type(), how);
-        else return w.f32 ? shaped(width, std::true_type(), how) : shaped(width, std::false_type(), how);
+        if constexpr (sizeof(T) == 4) return kinds(width, std::true_type(), how);
+        else return w.f32 ? kinds(width, std::true_type(), how) : kinds(width, std::false_type(), how);
     };
-    return vec == 1 ? typed(Int<1>(), Int<RN_RAGGED>()) : typed(Int<16 / sizeof(T)>(), Int<RN_OWN>());
+    return vec == 1 || !w.whole ? typed(Int<1>(), Int<RN_RAGGED>()) : typed(Int<16 / sizeof(T)>(), Int<RN_OWN>());
 }
 
 }  // namespace moe
