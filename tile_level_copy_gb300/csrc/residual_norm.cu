@@ -8,11 +8,11 @@ namespace moe {
 namespace {
 
 constexpr int RN_RED_COLS = 32, RN_RED_ROWS = 32, RN_RED_FLY = 10;
+constexpr int RN_GATE_ROWS = 8;  // of a CTA of the gates' sums
 constexpr int RN_MAX_SMS = 256;
 
 // The gradients of the weights from the CTAs' sums [parts][sums][d]: blockIdx.y 0 the norm before the next block
-// (sum 0, and 1 with full), 1 the norm behind this one and a gate that all rows share (the last one or two sums);
-// from 2 on the gates of groups of rows that lie in more than one group of warps.
+// (sum 0, and 1 with full), 1 the norm behind this one and a gate that all rows share (the last one or two sums).
 struct RnReduce {
     const float* part;
     const float* gpart;
@@ -34,28 +34,6 @@ __global__ void __launch_bounds__(RN_RED_COLS* RN_RED_ROWS) rn_reduce_kernel(RnR
     griddep_wait();
     griddep_launch();
     const int lane = threadIdx.x % RN_RED_COLS, row = threadIdx.x / RN_RED_COLS, c = blockIdx.x * RN_RED_COLS + lane;
-    if (blockIdx.y >= 2) {
-        const int64_t gates = (a.rows + a.gate_rows - 1) / a.gate_rows;
-        for (int64_t g = blockIdx.y - 2; g < gates; g += gridDim.y - 2) {
-            const int64_t from = g * a.gate_rows, to = from + a.gate_rows < a.rows ? from + a.gate_rows : a.rows;
-            const int64_t w0 = from / a.chunk, w1 = (to - 1) / a.chunk;
-            if (w0 == w1) continue;  // the group of warps wrote it
-            float v = 0.f;
-            if (c < a.d) {  // only the first group of warps may have begun with an earlier gate
-                for (int64_t k = w0 + row; k <= w1; k += RN_RED_ROWS)
-                    v += a.gpart[(2 * k + (k == w0 && w0 * a.chunk < from ? 1 : 0)) * a.d + c];
-            }
-            __syncthreads();
-            acc[0][row][lane] = v;
-            __syncthreads();
-            if (row || c >= a.d) continue;
-            v = 0.f;
-#pragma unroll
-            for (int q = 0; q < RN_RED_ROWS; ++q) v += acc[0][q][lane];
-            put_at<T>(a.dgate, a.f32, g * a.d + c, v);
-        }
-        return;
-    }
     const int sums = a.full ? 4 : 2, first = blockIdx.y == 0 ? 0 : sums / 2;
     float v[2] = {0.f, 0.f};
     if (c < a.d) {
@@ -99,6 +77,43 @@ __global__ void __launch_bounds__(RN_RED_COLS* RN_RED_ROWS) rn_reduce_kernel(RnR
         put_at<T>(a.dpost_w, a.f32, c, x * g);
         put_at<T>(a.dpost_b, a.f32, c, y * g);
         put_at<T>(a.dgate, a.f32, c, value_at<T>(a.post_w, a.f32, c, 1.f) * x + value_at<T>(a.post_b, a.f32, c, 0.f) * y);
+    }
+}
+
+// The gradients of the gates whose rows lie in more than one group of warps, from those groups' sums: gates
+// blockIdx.y, blockIdx.y + gridDim.y, ...
+template <typename T>
+__global__ void __launch_bounds__(RN_RED_COLS* RN_GATE_ROWS) rn_gate_kernel(RnReduce a) {
+    __shared__ float acc[RN_GATE_ROWS][RN_RED_COLS];
+    griddep_wait();
+    griddep_launch();
+    const int lane = threadIdx.x % RN_RED_COLS, row = threadIdx.x / RN_RED_COLS, c = blockIdx.x * RN_RED_COLS + lane;
+    const int64_t gates = (a.rows + a.gate_rows - 1) / a.gate_rows;
+    for (int64_t g = blockIdx.y; g < gates; g += gridDim.y) {
+        const int64_t from = g * a.gate_rows, to = from + a.gate_rows < a.rows ? from + a.gate_rows : a.rows;
+        const int64_t w0 = from / a.chunk, w1 = (to - 1) / a.chunk;
+        if (w0 == w1) continue;  // the group of warps wrote it
+        float v = 0.f;
+        if (c < a.d) {  // only the first group of warps may have begun with an earlier gate
+            for (int64_t k = w0 + row; k <= w1; k += 4 * RN_GATE_ROWS) {  // four loads in flight
+                float e[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const int64_t at = k + i * RN_GATE_ROWS;
+                    e[i] = at <= w1 ? a.gpart[(2 * at + (at == w0 && w0 * a.chunk < from ? 1 : 0)) * a.d + c] : 0.f;
+                }
+#pragma unroll
+                for (int i = 0; i < 4; ++i) v += e[i];
+            }
+        }
+        __syncthreads();
+        acc[row][lane] = v;
+        __syncthreads();
+        if (row || c >= a.d) continue;
+        v = 0.f;
+#pragma unroll
+        for (int q = 0; q < RN_GATE_ROWS; ++q) v += acc[q][lane];
+        put_at<T>(a.dgate, a.f32, g * a.d + c, v);
     }
 }
 
@@ -170,13 +185,14 @@ RnShape shape_of(const moe_residual_norm_config& c) {
     return s;
 }
 
+
 bool full_of(const moe_residual_norm_config& c) { return c.post == MOE_NORM_LAYER || c.pre == MOE_NORM_LAYER; }
 bool grouped_of(const moe_residual_norm_config& c) { return c.gate_rows > 0 && c.gate_rows < c.rows; }
 
 // Backward: CTAs, and the consecutive rows of each group of warps.
 RnShape backward_shape(const moe_residual_norm_config& c, int sms, int* ctas) {
     RnShape s = shape_of(c);
-    s.warps = rn_warps(c.d, rn_backward_values(c.d));
+    s.warps = rn_warps(c.d, rn_backward_values(c.d, full_of(c)));
     s.groups = s.warps < 8 ? 8 / s.warps : 1;
     const int64_t most = (int64_t)sms * (s.warps * s.groups > 8 ? 1 : 2) * s.groups;
     const int64_t workers = c.rows < most ? c.rows : most;
@@ -307,13 +323,11 @@ MOE_API int moe_residual_norm_backward(const moe_residual_norm_config* c, const 
         if (e0 != cudaSuccess || !any) return e0;
         const RnReduce a{part, gpart, ctas, c->d, full, grouped, w.f32, post_w, post_b, gate, dpost_w, dpost_b, dgate, dpre_w,
                          dpre_b, c->rows, c->gate_rows, s.chunk};
-        int gates = 0;
-        if (grouped && dgate) {
-            const int64_t g = (c->rows + c->gate_rows - 1) / c->gate_rows;
-            gates = (int)(g < 64 ? g : 64);
-        }
-        return launch_k(rn_reduce_kernel<T>, dim3((c->d + RN_RED_COLS - 1) / RN_RED_COLS, 2 + gates),
-                        dim3(RN_RED_COLS * RN_RED_ROWS), 0, st, true, a);
+        const unsigned columns = (c->d + RN_RED_COLS - 1) / RN_RED_COLS;
+        const cudaError_t e1 = launch_k(rn_reduce_kernel<T>, dim3(columns, 2), dim3(RN_RED_COLS * RN_RED_ROWS), 0, st, true, a);
+        if (e1 != cudaSuccess || !grouped || !dgate) return e1;
+        const int64_t g = (c->rows + c->gate_rows - 1) / c->gate_rows;
+        return launch_k(rn_gate_kernel<T>, dim3(columns, (unsigned)(g < 64 ? g : 64)), dim3(RN_RED_COLS * RN_GATE_ROWS), 0, st, true, a);
     });
     return err == cudaSuccess ? MOE_OK : cuda_fail(err, "residual norm backward launch");
 }

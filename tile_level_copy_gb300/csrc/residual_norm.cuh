@@ -45,7 +45,7 @@ cudaError_t launch_residual_backward(RnShape s, const RnWeights& w, const RnBack
 
 inline int rn_warps(int d, int values) { return (d + 32 * values - 1) / (32 * values); }
 // Backward: values of a thread (32 of them spill; only rows above 8192 need them).
-inline int rn_backward_values(int d) { return d <= 8192 ? 16 : 32; }
+inline int rn_backward_values(int d, bool full) { return full && d <= 2048 ? 8 : d <= 8192 ? 16 : 32; }
 
 namespace {
 
@@ -84,6 +84,13 @@ struct RnColumns {
             if (q < np) r = *reinterpret_cast<const P*>(p + q * STEP);
             else memset(&r, 0, sizeof(r));
         }
+        return r;
+    }
+    // the same from a slot of ragged rows, which holds zeros behind the row
+    __device__ __forceinline__ P load_padded(const T* p, int q) const {
+        P r;
+        r.v[0] = p[q * STEP];
+        r.v[1] = p[q * STEP + 32];
         return r;
     }
     __device__ __forceinline__ void store(T* p, int q, const P& r) const {
@@ -157,6 +164,16 @@ __device__ __forceinline__ void cover_row(uint8_t* to, const T* rows, int64_t n,
                 if (p + k >= lo && p + k < hi) *reinterpret_cast<T*>(to + 16 * i + k) = *reinterpret_cast<const T*>(p + k);
         }
     }
+}
+
+// Zeros behind a row in its slot, up to the end of the pieces that a row may take, by the thread that fetched the row's
+// last piece, once it is there. (What lies behind those pieces is zeroed once.)
+template <typename T>
+__device__ __forceinline__ void pad_row(uint8_t* to, const T* rows, int64_t at, int d, int t, int threads) {
+    constexpr int size = (int)sizeof(T);
+    const int end = offset_of(rows + at) + d * size, last = (end + 15) / 16 - 1, most = (16 - size + d * size + 15) / 16 * 16;
+    if ((last - t) % threads) return;
+    for (int b = end; b < most; b += size) put(*reinterpret_cast<T*>(to + b), 0.f);
 }
 
 __device__ __forceinline__ void committed() { asm volatile("cp.async.commit_group;" ::: "memory"); }

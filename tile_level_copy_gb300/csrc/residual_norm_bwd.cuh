@@ -23,7 +23,7 @@ namespace {
 // CTAs on a SM
 __host__ __device__ constexpr int rb_ctas(int threads) { return threads > 256 ? 1 : 2; }
 constexpr size_t RB_SMEM_MOST = 224 * 1024;
-constexpr int RB_BATCH = 4;  // units whose loads are in flight together
+constexpr int RB_BATCH = 8;  // units whose loads are in flight together
 
 // A thread's units of w2 and, behind all of those, of k in shared memory.
 template <typename C, int THREADS>
@@ -157,12 +157,23 @@ __global__ void __launch_bounds__(THREADS, rb_ctas(THREADS)) rn_backward_kernel(
     // Piece q of tensor n. Beyond the row and of tensors that are not there: zeros, which lie in the slots.
     auto take = [&](int n, const T* from, int q) {
         if (MODE == RN_OWN) return *reinterpret_cast<const P*>(reinterpret_cast<const uint8_t*>(from) + q * THREADS * sizeof(P));
+        if constexpr (MODE == RN_RAGGED) return cols.load_padded(from, q);
         if (rows[n]) return cols.load(from, q);
         P p;
         memset(&p, 0, sizeof(p));
         return p;
     };
 
+    auto pad = [&](int64_t at, uint8_t* to) {
+#pragma unroll
+        for (int n = 0; n < 4; ++n)
+            if (rows[n]) pad_row(to + n * NEXT, rows[n], at, s.d, t, tpr);
+    };
+    if (MODE == RN_RAGGED) {
+        uint8_t* const slots = rb_smem + 2 * NU * THREADS * sizeof(V);
+        for (int i = threadIdx.x * 16; i < s.slots * SLOT; i += blockDim.x * 16) *reinterpret_cast<uint4*>(slots + i) = make_uint4(0, 0, 0, 0);
+        __syncthreads();
+    }
     if (MODE == RN_OWN) {
         P zero;
         memset(&zero, 0, sizeof(zero));
@@ -208,11 +219,13 @@ __global__ void __launch_bounds__(THREADS, rb_ctas(THREADS)) rn_backward_kernel(
         for (; row < stop; ++row) {
             if (MODE == RN_RAGGED) {  // the row is there for all its threads, and they are done with the one before
                 fetched(s.slots > 1 ? s.slots - 2 : 0);
+                if (s.slots > 1) pad(at, here);
                 named_bar_sync(1 + group, tpr);
             }
             issue(row + s.slots - 1, at + (int64_t)(s.slots - 1) * s.d, here == own ? own + (s.slots - 1) * SLOT : here - SLOT);
             if (MODE == RN_RAGGED && s.slots == 1) {
                 fetched(0);
+                pad(at, here);
                 named_bar_sync(1 + group, tpr);
             }
             if (MODE == RN_OWN) fetched(s.slots - 1);
@@ -415,7 +428,9 @@ cudaError_t launch_residual_backward(RnShape s, const RnWeights& w, const RnBack
     typedef Int<RN_RAGGED> Ragged;
     typedef Int<RN_DIRECT> Direct;
     const bool one = vec == 1;
-    if (rn_backward_values(s.d) == 32)
+    if (full && rn_backward_values(s.d, full) == 8)
+        return one ? go(Int<1>(), Int<8>(), Int<256>(), std::true_type(), Ragged()) : go(Int<VEC>(), Int<8>(), Int<256>(), std::true_type(), Own());
+    if (rn_backward_values(s.d, full) == 32)
         return one ? kinds(Int<1>(), Int<32>(), Int<512>(), Direct()) : kinds(Int<VEC>(), Int<32>(), Int<512>(), Direct());
     if (threads > 256) return one ? kinds(Int<1>(), Int<16>(), Int<512>(), Ragged()) : kinds(Int<VEC>(), Int<16>(), Int<512>(), Own());
     return one ? kinds(Int<1>(), Int<16>(), Int<256>(), Ragged()) : kinds(Int<VEC>(), Int<16>(), Int<256>(), Own());
