@@ -213,3 +213,24 @@ def test_with_the_routers_plan():
     got = run(bc, t)
     check(bc, t, got)
     assert torch.equal(got[1][0], ws.view("counts").sum(1).to(I32))
+
+
+def test_refusals():
+    t = make(100, 8, 2, 3, seed=10)
+    cfg = tlc.BalanceConfig(100, 8, 2, 3)
+    loss, counts, lse, ws = torch.empty(3, device="cuda"), torch.empty(3, 8, dtype=I32, device="cuda"), None, tlc.BalanceWorkspace(cfg)
+    small = torch.empty(16, dtype=U8, device="cuda")
+    with pytest.raises(ValueError, match="needs"):
+        tlc.balance_forward(cfg, t["logits"], t["idx"], loss, counts, lse, ws, offsets=t["offsets"], saved=small)
+    with pytest.raises(ValueError, match="needs"):
+        tlc.balance_backward(cfg, t["logits"], t["idx"], small, t["logits"], offsets=t["offsets"])
+    with pytest.raises(tlc.MoEError) as e:  # several sequences without offsets
+        tlc.balance_forward(cfg, t["logits"], t["idx"], loss, counts, lse, ws)
+    assert e.value.code == tlc.MOE_ERR_ARG
+    with pytest.raises(tlc.MoEError) as e:  # gates without their gradients
+        tlc.balance_backward(cfg, t["logits"], t["idx"], tlc.balance_saved(cfg), t["logits"], offsets=t["offsets"], gates=t["gates"])
+    assert e.value.code == tlc.MOE_ERR_ARG
+    ws.nbytes = 64
+    with pytest.raises(tlc.MoEError) as e:
+        tlc.balance_forward(cfg, t["logits"], t["idx"], loss, counts, lse, ws, offsets=t["offsets"])
+    assert e.value.code == tlc.MOE_ERR_WORKSPACE

@@ -320,3 +320,25 @@ def test_captured_and_replayed():
     torch.cuda.synchronize()
     for a, b in zip(outs, (h, z, dx, du, *(g for g in grads if g is not None))):
         assert torch.equal(a, b)
+
+
+def test_refusals():
+    t = make(5, 64, BF, F32, "layer", "rms", 5, 9)
+    cfg = config(5, 64, BF, F32, "layer", "rms", 5)
+    h, z, stats = forward(cfg, t)
+    for bad in (dict(x=t["x"].float()), dict(x=t["x"][:3]), dict(post_w=t["post_w"].to(BF)), dict(gate=t["post_w"].repeat(2)),
+                dict(u=t["u"].cpu()), dict(pre_w=t["pre_w"][:5]), dict(x=t["x"].t().contiguous().t())):
+        with pytest.raises(ValueError):
+            forward(cfg, {**t, **bad})
+    for bad in (dict(z=None), dict(h=z, z=z), dict(pre_b=t["post_b"]), dict(gate=None), dict(u=None)):
+        a = {**t, "h": h, "z": z, **bad}
+        with pytest.raises(tlc.MoEError) as e:
+            tlc.residual_norm_forward(cfg, *(a[n] for n in ("x", "u", "post_w", "post_b", "gate", "pre_w", "pre_b", "h", "z")))
+        assert e.value.code == tlc.MOE_ERR_ARG
+    ws = tlc.ResidualNormWorkspace(cfg)
+    ws.nbytes = 64
+    for w, code in ((None, tlc.MOE_ERR_ARG), (ws, tlc.MOE_ERR_WORKSPACE)):
+        with pytest.raises(tlc.MoEError) as e:
+            tlc.residual_norm_backward(cfg, t["dz"], t["dh"], t["u"], h, t["post_w"], t["post_b"], t["gate"], t["pre_w"], *stats,
+                                       torch.empty_like(h), torch.empty_like(h), torch.empty_like(t["post_w"]), ws=w)
+        assert e.value.code == code

@@ -23,7 +23,8 @@ namespace {
 // CTAs on a SM
 __host__ __device__ constexpr int rb_ctas(int threads) { return threads > 256 ? 1 : 2; }
 constexpr size_t RB_SMEM_MOST = 224 * 1024;
-constexpr int RB_BATCH = 8;  // units whose loads are in flight together
+template <typename C>
+constexpr int RB_BATCH = C::NU < 8 ? C::NU : 8;  // units whose loads are in flight together
 
 // A thread's units of w2 and, behind all of those, of k in shared memory.
 template <typename C, int THREADS>
@@ -35,10 +36,10 @@ struct RbPlaces {
 // Units of a vector from j0 on (null, and beyond the row: `none`).
 template <typename T, typename C>
 __device__ __forceinline__ void vector_units(const C& c, const void* p, bool f32, float none, int64_t at, int j0,
-                                             float (&o)[RB_BATCH][2]) {
+                                             float (&o)[RB_BATCH<C>][2]) {
     auto each = [&](auto value) {
 #pragma unroll
-        for (int k = 0; k < RB_BATCH; ++k)
+        for (int k = 0; k < RB_BATCH<C>; ++k)
 #pragma unroll
             for (int i = 0; i < 2; ++i) o[k][i] = c.inside(j0 + k, i) ? value(at + c.column(j0 + k, i)) : none;
     };
@@ -50,15 +51,16 @@ __device__ __forceinline__ void vector_units(const C& c, const void* p, bool f32
 // gate_end are calls, made once a gate: inlined they took registers from the loop over the rows.)
 template <typename T, typename C, typename Q>
 __device__ __noinline__ float make_weights(const C c, const Q places, const RnWeights& w, int64_t g) {
+    static_assert(C::NU % RB_BATCH<C> == 0, "whole batches");
     float sum = 0.f;
 #pragma unroll 1
-    for (int j0 = 0; j0 < C::NU; j0 += RB_BATCH) {
-        float a[RB_BATCH][2], k[RB_BATCH][2], gate[RB_BATCH][2];
+    for (int j0 = 0; j0 < C::NU; j0 += RB_BATCH<C>) {
+        float a[RB_BATCH<C>][2], k[RB_BATCH<C>][2], gate[RB_BATCH<C>][2];
         vector_units<T>(c, w.pre_w, w.f32, 1.f, 0, j0, a);
         vector_units<T>(c, w.post_w, w.f32, 1.f, 0, j0, k);
         vector_units<T>(c, w.gate, w.f32, 1.f, g * c.d, j0, gate);
 #pragma unroll
-        for (int n = 0; n < RB_BATCH; ++n) {
+        for (int n = 0; n < RB_BATCH<C>; ++n) {
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
                 const bool in = c.inside(j0 + n, i);
@@ -78,8 +80,8 @@ template <typename T, bool FULL, typename C, typename Q>
 __device__ __noinline__ void gate_end(const C c, const Q places, const RnWeights& w, int64_t g, float* sums, float* part,
                                       void* dgate) {
 #pragma unroll 1
-    for (int j0 = 0; j0 < C::NU; j0 += RB_BATCH) {
-        float gate[RB_BATCH][2], w1[RB_BATCH][2], b1[RB_BATCH][2], a[RB_BATCH][2], e[RB_BATCH][2];
+    for (int j0 = 0; j0 < C::NU; j0 += RB_BATCH<C>) {
+        float gate[RB_BATCH<C>][2], w1[RB_BATCH<C>][2], b1[RB_BATCH<C>][2], a[RB_BATCH<C>][2], e[RB_BATCH<C>][2];
         vector_units<T>(c, w.gate, w.f32, 1.f, g * c.d, j0, gate);
         vector_units<T>(c, w.post_w, w.f32, 1.f, 0, j0, w1);
         vector_units<T>(c, sums, true, 0.f, 0, j0, a);
@@ -88,7 +90,7 @@ __device__ __noinline__ void gate_end(const C c, const Q places, const RnWeights
             vector_units<T>(c, sums, true, 0.f, c.d, j0, e);
         }
 #pragma unroll
-        for (int k = 0; k < RB_BATCH; ++k) {
+        for (int k = 0; k < RB_BATCH<C>; ++k) {
             const float2 x = split(*places.k(j0 + k)), y = split(*places.w2(j0 + k));
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
