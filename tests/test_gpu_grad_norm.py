@@ -57,7 +57,7 @@ def test_norm_and_clipping(sizes, types, shift):
             assert torch.equal(g._base[:shift], a)
 
 
-def test_below_the_limit_nothing_is_written():
+def test_below_the_limit_the_gradients_stay():
     gs = grads([1000, 7], (BF,), 1)
     out, lst = run(gs, 1e3)
     assert out[1] == 1

@@ -668,6 +668,11 @@ int ctas_of(const moe_balance_config& c, int threads, int most) {
     const int n = (c.T + pass - 1) / pass;
     return n < 1 ? 1 : n < most ? n : most;
 }
+// Forward: as many CTAs as sequences at least, as each ends with barriers and a row of sums, one after another.
+int forward_ctas(const moe_balance_config& c, int threads, int most) {
+    const int n = ctas_of(c, threads, most), m = c.seqs < c.T ? c.seqs : c.T;
+    return n >= m ? n : m < most ? m : most;
+}
 int most_ctas(const DeviceInfo& di, int threads) {
     const int n = di.sms * (threads < BL_THREADS ? 3 : 1);
     return n < BL_MAX_CTAS ? n : BL_MAX_CTAS;
@@ -732,7 +737,7 @@ MOE_API int moe_balance_workspace_size(const moe_balance_config* c, size_t* byte
     const int rc = check(c);
     if (rc) return rc;
     if (!bytes) return fail(MOE_ERR_ARG, "bytes is NULL");
-    *bytes = space_bytes(*c, ctas_of(*c, 256, BL_MAX_CTAS));
+    *bytes = space_bytes(*c, forward_ctas(*c, 256, BL_MAX_CTAS));
     return MOE_OK;
 }
 
@@ -758,7 +763,7 @@ MOE_API int moe_balance_forward(const moe_balance_config* c, const float* logits
         return fail(MOE_ERR_ARG, "a pointer is not aligned (saved and ws to 16 bytes, the others to their type)");
     DeviceInfo di;
     if ((rc = check_device(&di))) return rc;
-    const int threads = threads_of(*c, di.sms), ctas = ctas_of(*c, threads, most_ctas(di, threads));
+    const int threads = threads_of(*c, di.sms), ctas = forward_ctas(*c, threads, most_ctas(di, threads));
     const size_t need = space_bytes(*c, ctas);
     if (ws_bytes < need) return fail(MOE_ERR_WORKSPACE, "workspace has %zu bytes, needs %zu", ws_bytes, need);
     const BlShape s = shape_of(*c, offsets, mask, ctas);

@@ -247,7 +247,6 @@ __global__ void __launch_bounds__(GN_THREADS, GN_CTAS)
     griddep_wait();
     griddep_launch();
     const float s = *scale;
-    if (s == 1.0f) return;
     for (int c = l.first[l.count] - 1 - (int)blockIdx.x; c >= 0; c -= gridDim.x) {
         const int i = tensor_of(l, c);
         const int64_t chunk = c - l.first[i];
