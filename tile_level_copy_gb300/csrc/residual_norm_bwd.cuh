@@ -366,39 +366,33 @@ __global__ void __launch_bounds__(THREADS, rb_ctas(THREADS)) rn_backward_kernel(
             if (FULL) s2[FULL ? j : 0] = pair(v[1][0], v[1][1]);
         }
     }
-    // the groups' sums one after another in shared memory, so that the order is the same every time
+    // the groups' sums side by side in shared memory, then added up in the order of the groups
     constexpr int SUMS = FULL ? 4 : 2;
-    float* const sums = reinterpret_cast<float*>(rb_smem);
     float* const pw = b.part + (size_t)blockIdx.x * SUMS * s.d;
+    float* const sums = reinterpret_cast<float*>(rb_smem);
     if (s.groups > 1) __syncthreads();
-    for (int k = 0; k < s.groups; ++k) {
-        if (group == k) {
-            float* to = s.groups == 1 ? pw : sums;
+    float* const to = s.groups == 1 ? pw : sums + (size_t)group * SUMS * s.d;
 #pragma unroll
-            for (int j = 0; j < NU; ++j) {
+    for (int j = 0; j < NU; ++j) {
 #pragma unroll
-                for (int n = 0; n < SUMS; ++n) {
-                    const V v = n == 0 ? sp[j] : n == SUMS / 2 ? s1[j] : n == 1 ? sq[FULL ? j : 0] : s2[FULL ? j : 0];
-                    if constexpr (VEC > 1) {
-                        if (!cols.inside(j, 0)) continue;
-                        V* const p = reinterpret_cast<V*>(to + n * s.d + cols.column(j, 0));
-                        *p = k ? add_(*p, v) : v;
-                    } else {
-                        const float2 e = split(v);
-#pragma unroll
-                        for (int i = 0; i < 2; ++i) {
-                            if (!cols.inside(j, i)) continue;
-                            float* const p = to + n * s.d + cols.column(j, i);
-                            *p = (k ? *p : 0.f) + (i ? e.y : e.x);
-                        }
-                    }
-                }
+        for (int n = 0; n < SUMS; ++n) {
+            const V v = n == 0 ? sp[j] : n == SUMS / 2 ? s1[j] : n == 1 ? sq[FULL ? j : 0] : s2[FULL ? j : 0];
+            if constexpr (VEC > 1) {
+                if (cols.inside(j, 0)) *reinterpret_cast<V*>(to + n * s.d + cols.column(j, 0)) = v;
+            } else {
+                const float2 e = split(v);
+                if (cols.inside(j, 0)) to[n * s.d + cols.column(j, 0)] = e.x;
+                if (cols.inside(j, 1)) to[n * s.d + cols.column(j, 1)] = e.y;
             }
         }
-        if (s.groups > 1) __syncthreads();
     }
-    if (s.groups > 1)
-        for (int c = threadIdx.x; c < SUMS * s.d; c += blockDim.x) pw[c] = sums[c];
+    if (s.groups == 1) return;
+    __syncthreads();
+    for (int c = threadIdx.x; c < SUMS * s.d; c += blockDim.x) {
+        float a = 0.f;
+        for (int k = 0; k < s.groups; ++k) a += sums[k * SUMS * s.d + c];
+        pw[c] = a;
+    }
 }
 
 }  // namespace
@@ -417,7 +411,8 @@ cudaError_t launch_residual_backward(RnShape s, const RnWeights& w, const RnBack
         static_assert(weights + slot <= RB_SMEM_MOST, "room for a row");
         s.slots = MODE == RN_DIRECT ? 1 : weights + 3 * slot <= room ? 3 : weights + 2 * slot <= room ? 2 : 1;
         size_t smem = weights + s.slots * slot;
-        if (s.groups > 1 && smem < (size_t)(full ? 4 : 2) * s.d * 4) smem = (size_t)(full ? 4 : 2) * s.d * 4;
+        const size_t sums = (size_t)(full ? 4 : 2) * s.d * 4 * s.groups;  // of every group, at the end
+        if (s.groups > 1 && smem < sums) smem = sums;
         const cudaError_t e = allow_smem<kernel>(RB_SMEM_MOST);
         if (e != cudaSuccess) return e;
         return launch_k(kernel, dim3(ctas), dim3(threads), smem, st, true, s, w, b, (int)grouped);
