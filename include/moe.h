@@ -579,7 +579,7 @@ MOE_API int moe_adamw_read_state(const moe_adamw_tensor* tensors, int32_t count,
  */
 #define MOE_GRAD_NORM_WORKSPACE_BYTES 32768
 typedef struct moe_grad_norm_config {
-    double max_norm; /* > 0; infinite: never clipped */
+    double max_norm; /* >= 0; infinite: never clipped */
     double eps;      /* >= 0 */
     int32_t reserved[4];
 } moe_grad_norm_config;
@@ -598,7 +598,7 @@ MOE_API int moe_grad_norm(const moe_grad_norm_config* cfg, const moe_grad_tensor
                           void* ws, size_t ws_bytes, void* stream);
 
 /* g = g * scale in place for every tensor of the list, in fp32, rounded once; scale: device fp32 scalar (1 leaves every
- * value as it is). Tensors must not overlap, nor hold scale. */
+ * value as it is). Tensors must not overlap; a scale inside of one is refused. */
 MOE_API int moe_grad_clip(const moe_grad_tensor* tensors, int32_t count, const float* scale, void* stream);
 
 /*
@@ -641,7 +641,8 @@ MOE_API int moe_residual_norm_workspace_size(const moe_residual_norm_config* cfg
  * pre = MOE_NORM_NONE, dh may be NULL (0) otherwise. u: as in the forward pass, needed with a post norm or a gate; h: with a pre norm.
  *   dx = residual_scale * (dh + pre' dz), du = post' (branch_scale * gate * (the same)); du NULL: not wanted
  *   dpost_w, dpost_b, dgate, dpre_w, dpre_b: summed over the rows (dgate over the rows of each gate), each NULL when
- *   not wanted; ws may be NULL when all are. dx may be dh or dz, du may be u or dz (not all at once); no other sharing.
+ *   not wanted; ws may be NULL when all are. dx and du may each be one of dz, dh, u and h (not the same one); no other
+ *   sharing.
  * The order of the sums depends on the config, the pointers' alignment and the device alone. With rows = 0 the
  * weights' gradients are set to zero.
  */
@@ -686,9 +687,10 @@ MOE_API int moe_balance_forward(const moe_balance_config* cfg, const float* logi
 /*
  * The gradient at the logits, every row of dlogits [T, E] written (zeros for padding); dlogits may be logits.
  *   dloss * (cfg.balance d balance / dl + cfg.z dz / dl)  + the gradient of the gates
- * (counts are constants). dloss: device f32 scalar, or NULL for 1. gates, dgates device f32 [T, topk], or both NULL: gates as
- * moe_plan's topk_w (softmax over the chosen logits) and the loss's gradients at them; to the logit of pair (t, j)
- * comes gates[t, j] * (dgates[t, j] - sum_i gates[t, i] dgates[t, i]), to that of a dropped pair nothing.
+ * (counts are constants; cfg, idx, offsets and mask as in the forward pass, whose losses' weights lie in saved). dloss:
+ * device f32 scalar, or NULL for 1. gates, dgates device f32 [T, topk], or both NULL: gates as moe_plan's topk_w
+ * (softmax over the chosen logits) and the loss's gradients at them; to the logit of pair (t, j) comes
+ * gates[t, j] * (dgates[t, j] - sum_i gates[t, i] dgates[t, i]), to that of a dropped pair nothing.
  */
 MOE_API int moe_balance_backward(const moe_balance_config* cfg, const float* logits, const int32_t* idx,
                                  const int32_t* offsets, const uint8_t* mask, const void* saved, const float* gates,

@@ -180,6 +180,42 @@ def test_offsets_that_are_out_of_range_stay_inside():
     assert all(torch.equal(x, y) for x, y in zip(a, b))
 
 
+def test_many_empty_sequences():
+    """A few tokens' sequences among 200000 empty ones, in which a CTA's next sequence is found by a search."""
+    T, E, k, S = 5000, 16, 2, 200000
+    t = make(T, E, k, 1, seed=11)
+    cut = torch.zeros(S + 1, dtype=I32)
+    cut[50000:], cut[120000:], cut[120001:], cut[199999:] = 1000, 1003, 4000, T
+    t["offsets"] = cut.cuda()
+    cfg = tlc.BalanceConfig(T, E, k, S, balance=0.3, z=0.1)
+    got = run(cfg, t)
+    few = {**t, "offsets": torch.tensor([0, 1000, 1003, 4000, T], dtype=I32, device="cuda")}
+    want = run(tlc.BalanceConfig(T, E, k, 4, balance=0.3, z=0.1), few)
+    where = torch.tensor([49999, 119999, 120000, 199998], device="cuda")
+    assert torch.equal(got[1][where], want[1]) and got[1].sum() == want[1].sum() and torch.equal(got[2], want[2])
+    check(tlc.BalanceConfig(T, E, k, 4, balance=0.3, z=0.1), few, (got[0], got[1][where], *got[2:]))
+
+
+def test_more_values_than_32_bits_count():
+    """The last tokens' logits lie beyond value 2^31."""
+    T, E, k = 2 ** 23 + 1001, 256, 2
+    cfg, end = tlc.BalanceConfig(T, E, k, balance=0.3, z=0.1), slice(T - 2000, T)
+    logits = torch.empty(T, E, device="cuda").normal_()
+    idx = torch.randint(0, E, (T, k), device="cuda", dtype=I32)
+    loss, counts = torch.empty(3, device="cuda"), torch.empty(1, E, dtype=I32, device="cuda")
+    lse, saved = torch.empty(T, device="cuda"), tlc.balance_saved(cfg)
+    tlc.balance_forward(cfg, logits, idx, loss, counts, lse, tlc.BalanceWorkspace(cfg), saved=saved)
+    c = torch.bincount(idx.flatten(), minlength=E)
+    assert torch.equal(counts[0].long(), c)
+    l = logits[end].double()
+    p, want = torch.softmax(l, 1), torch.logsumexp(l, 1)
+    assert ((lse[end] - want).abs() <= 16 * ULP * (1 + want.abs() + l.abs().amax(1))).all()
+    tlc.balance_backward(cfg, logits, idx, saved, logits)
+    a = 0.3 * E / (k * T ** 2) * c.double()
+    dl = p * (a - (p * a).sum(1, keepdim=True) + 0.2 / T * want[:, None])
+    assert ((logits[end] - dl).abs() <= 128 * ULP * p * (2 * a.max() + 0.2 / T * want.abs()[:, None])).all()
+
+
 def test_captured_and_replayed():
     t = make(2000, 64, 6, 5, seed=8)
     cfg = tlc.BalanceConfig(2000, 64, 6, 5, balance=0.3, z=0.1)
@@ -229,6 +265,10 @@ def test_refusals():
     assert e.value.code == tlc.MOE_ERR_ARG
     with pytest.raises(tlc.MoEError) as e:  # gates without their gradients
         tlc.balance_backward(cfg, t["logits"], t["idx"], tlc.balance_saved(cfg), t["logits"], offsets=t["offsets"], gates=t["gates"])
+    assert e.value.code == tlc.MOE_ERR_ARG
+    wide = torch.empty(101, 8, device="cuda")
+    with pytest.raises(tlc.MoEError) as e:  # dlogits a row beside logits
+        tlc.balance_backward(cfg, wide[:100], t["idx"], tlc.balance_saved(cfg), wide[1:], offsets=t["offsets"])
     assert e.value.code == tlc.MOE_ERR_ARG
     ws.nbytes = 64
     with pytest.raises(tlc.MoEError) as e:

@@ -100,6 +100,28 @@ def test_long_list_of_equal_values():
     assert abs(out[0].item() / 2.0 ** 3.5 - 1) <= REL
 
 
+def test_more_values_than_32_bits_count():
+    """A tensor of more than 2^32 values among short ones: 2^-10 each but for large ones at its ends."""
+    n = 2 ** 32 + 12345
+    g = [torch.ones(7, device="cuda"), torch.full((n + 1,), 2.0 ** -10, dtype=BF, device="cuda")[1:], torch.ones(9, dtype=F16, device="cuda")]
+    g[1][0] = g[1][-1] = 64.0
+    out, lst = run(g, max_norm=2.0)
+    norm = np.sqrt(16 + (n - 2) * 2.0 ** -20 + 2 * 64.0 ** 2)
+    assert abs(out[0].item() / norm - 1) <= REL and abs(out[1].item() / (2 / (norm + 1e-6)) - 1) <= REL
+    tlc.grad_clip(lst, torch.full((1,), 0.5, device="cuda"))
+    assert (g[0] == 0.5).all() and (g[2] == 0.5).all() and g[1][0] == 32 and g[1][-1] == 32
+    lo, hi = g[1][1:-1].aminmax()
+    assert lo == hi == 2.0 ** -11
+
+
+def test_nothing_is_left_with_a_limit_of_zero():
+    g = grads([100, 7], (F32, BF))
+    out, lst = run(g, 0.0)
+    assert out[0] > 0 and out[1] == 0
+    tlc.grad_clip(lst, out[1:])
+    assert not any(t.any() for t in g)
+
+
 def test_stream_capture_and_adamw():
     """Norm, clipped step: captured together on a stream; adamw_step with grad_scale takes the step that clipped
     gradients give, up to the rounding of the clipped values (none in fp32 with a scale that is a power of two)."""
@@ -131,7 +153,7 @@ def test_refusals():
         with pytest.raises(ValueError):
             tlc.GradList(bad)
     lst, ws, out = tlc.GradList(g), tlc.GradNormWorkspace(), torch.empty(2, device="cuda")
-    for cfg in (tlc.GradNormConfig(0.0), tlc.GradNormConfig(float("nan")), tlc.GradNormConfig(1.0, -1.0), tlc.GradNormConfig(1.0, float("inf"))):
+    for cfg in (tlc.GradNormConfig(-0.5), tlc.GradNormConfig(float("nan")), tlc.GradNormConfig(1.0, -1.0), tlc.GradNormConfig(1.0, float("inf"))):
         with pytest.raises(tlc.MoEError) as e:
             tlc.grad_norm(cfg, lst, out, ws)
         assert e.value.code == tlc.MOE_ERR_ARG
@@ -140,3 +162,7 @@ def test_refusals():
             tlc.grad_norm(tlc.GradNormConfig(1.0), lst, o, ws)
     with pytest.raises(ValueError):
         tlc.grad_clip(lst, out)
+    for call in (lambda: tlc.grad_clip(lst, g[1][99:]), lambda: tlc.grad_norm(tlc.GradNormConfig(1.0), lst, g[0][:2], ws)):
+        with pytest.raises(tlc.MoEError) as e:  # the factor or the norm in a gradient
+            call()
+        assert e.value.code == tlc.MOE_ERR_ARG

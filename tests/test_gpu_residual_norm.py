@@ -215,6 +215,48 @@ def test_in_place_and_optional(dt, d):
         assert torch.equal(a, b)
 
 
+@pytest.mark.parametrize("d", [776, 777, 8191, 8200, 9001])
+def test_in_place_beside_other_rows(d):
+    """Rows whose 16-byte pieces hold values of their neighbours, which others write meanwhile; rows that are read twice."""
+    rows = 3001
+    t = make(rows, d, BF, F32, "layer", "layer", rows, 13)
+    cfg = config(rows, d, BF, F32, "layer", "layer", rows)
+    h, z, stats = forward(cfg, t)
+    check_forward(cfg, t, "layer", "layer", h, z, stats)
+    dx, du, grads = backward(cfg, t, h, stats)
+    for a, b in (("x", "u"), ("u", "x")):
+        c = {**t, "x": t["x"].clone(), "u": t["u"].clone()}
+        h2, z2, _ = forward(cfg, c, h=c[a], z=c[b])
+        assert torch.equal(h2, h) and torch.equal(z2, z)
+    for a, b in (("dz", "dh"), ("dh", "dz"), ("u", "h"), ("h", "u")):
+        c = {n: None if v is None else v.clone() for n, v in {**t, "h": h}.items()}
+        dx2, du2, g2 = backward(cfg, c, c["h"], stats, dx=c[a], du=c[b])
+        assert torch.equal(dx2, dx) and torch.equal(du2, du) and all(torch.equal(x, y) for x, y in zip(grads, g2))
+
+
+@pytest.mark.parametrize("d", [4096, 4095])
+def test_more_values_than_32_bits_count(d):
+    """The last rows lie beyond value 2^31; in place, so that only the rows that are compared are kept."""
+    rows = 2 ** 31 // d + 1000
+    near_end = torch.cat([torch.arange(2), 2 ** 31 // d + torch.arange(-2, 2), rows - torch.arange(4, 0, -1)]).cuda()
+    t = make(1, d, BF, F32, "rms", "rms", 0, 14)
+    for n in ("x", "u", "dz", "dh"):
+        t[n] = torch.empty(rows, d, dtype=BF, device="cuda").normal_()
+    cfg, few = config(rows, d, BF, F32, "rms", "rms", 0), config(len(near_end), d, BF, F32, "rms", "rms", 0)
+    part = {n: v[near_end] if n in ("x", "u", "dz", "dh") else v for n, v in t.items()}
+    h, z, stats = forward(cfg, t, h=t["x"])
+    some = [s[near_end] for s in stats]
+    check_forward(few, part, "rms", "rms", h[near_end], z[near_end], some)
+    want, size = torch.zeros(d, dtype=torch.float64, device="cuda"), torch.zeros(d, dtype=torch.float64, device="cuda")
+    for i in range(0, rows, 4000):
+        v = t["dz"][i:i + 4000].double() * h[i:i + 4000].double() * stats[1][i:i + 4000, 1:].double()
+        want += v.sum(0)
+        size += v.square().sum(0)
+    dx, du, grads = backward(cfg, t, h, stats, dx=t["dz"], du=t["u"], want=("pre_w",))
+    check_backward(few, part, "rms", "rms", h[near_end], some, dx[near_end], du[near_end], [None] * 5)
+    near(grads[3], f64(want), ULP * (64 + 4 * np.sqrt(rows)) * f64(size.sqrt()))
+
+
 @pytest.mark.parametrize("groups", [0, 4])
 def test_no_weight_gradients_with_gates_of_groups(groups):
     rows, d = 37, 256

@@ -115,9 +115,9 @@ def test_grad_norm_arguments_are_refused(built_library):
     f, clip = built_library.moe_grad_norm, built_library.moe_grad_clip
     cfg = lambda m=1.0, e=1e-6: ctypes.byref(tlc.GradNormConfig(m, e).to_c())  # noqa: E731
     t = (tlc._GradTensor * 2)()
-    t[0].g, t[0].n = 1 << 30, 10
+    t[0].g, t[0].n = 1 << 31, 10
     call = lambda c=cfg(), ts=t, n=2, out=OK, ws=OK, size=1 << 20: f(c, ts, n, out, ws, size, None)  # noqa: E731
-    for bad in (dict(c=cfg(0.0)), dict(c=cfg(-1.0)), dict(c=cfg(float("nan"))), dict(c=cfg(1.0, -1.0)), dict(c=cfg(1.0, float("inf"))),
+    for bad in (dict(c=cfg(-0.5)), dict(c=cfg(-1.0)), dict(c=cfg(float("nan"))), dict(c=cfg(1.0, -1.0)), dict(c=cfg(1.0, float("inf"))),
                 dict(ts=None), dict(n=-1), dict(out=None), dict(out=ODD), dict(ws=None), dict(ws=ctypes.c_void_p(8))):
         assert call(**bad) == ARG, bad
     assert call(size=100) == tlc.MOE_ERR_WORKSPACE

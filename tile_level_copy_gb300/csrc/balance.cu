@@ -198,7 +198,10 @@ __global__ void __launch_bounds__(BL_THREADS, 1)
     const int last = min(s.T, pos + s.chunk);
     for (int seq = starts.find(s, pos); pos < last && seq <= s.S; ++seq) {
         const int end = min(last, seq < 0 ? starts(s, 0) : seq < s.S ? starts(s, seq + 1) : s.T);
-        if (end <= pos) continue;
+        if (end <= pos) {  // past all empty sequences at once
+            seq = max(seq, starts.find(s, pos) - 1);
+            continue;
+        }
         const bool counted = seq >= 0 && seq < s.S;
         for (int e = tid; e < s.E; e += blockDim.x) cnt[e] = 0;
         __syncthreads();
@@ -802,6 +805,9 @@ MOE_API int moe_balance_backward(const moe_balance_config* c, const float* logit
     if (!aligned(logits, 4) || !aligned(idx, 4) || !aligned(offsets, 4) || !aligned(gates, 4) || !aligned(dgates, 4) ||
         !aligned(dloss, 4) || !aligned(dlogits, 4) || !aligned(saved, 16))
         return fail(MOE_ERR_ARG, "a pointer is not aligned (saved to 16 bytes, the others to their type)");
+    const uintptr_t in = reinterpret_cast<uintptr_t>(logits), to = reinterpret_cast<uintptr_t>(dlogits);
+    const size_t bytes = 4 * (size_t)c->T * c->E;
+    if (in != to && in < to + bytes && to < in + bytes) return fail(MOE_ERR_ARG, "dlogits shares memory with part of logits");
     DeviceInfo di;
     if ((rc = check_device(&di))) return rc;
     const int ctas = ctas_of(*c, BL_BACK_THREADS, BL_BACK_CTAS * di.sms);

@@ -291,7 +291,8 @@ __global__ void __launch_bounds__(GN_THREADS, GN_CTAS)
 constexpr int GN_SMALL = 72, GN_LARGE = 1300;
 static_assert(sizeof(GnList<GN_LARGE>) + sizeof(GnEnd) < 32000, "launch parameters");
 
-int check_list(const moe_grad_tensor* ts, int32_t count, int64_t* values) {
+// `apart`: `bytes` of the caller's that lie in no tensor.
+int check_list(const moe_grad_tensor* ts, int32_t count, const void* apart, size_t bytes, int64_t* values) {
     if (count < 0) return fail(MOE_ERR_ARG, "count=%d must be >= 0", count);
     if (count && !ts) return fail(MOE_ERR_ARG, "tensors is NULL");
     *values = 0;
@@ -304,6 +305,9 @@ int check_list(const moe_grad_tensor* ts, int32_t count, int64_t* values) {
         if (t.n == 0) continue;
         if (!t.g) return fail(MOE_ERR_ARG, "tensor %d: g is NULL", i);
         if (!aligned(t.g, dtype_size(t.dtype))) return fail(MOE_ERR_ARG, "tensor %d is not aligned to its type", i);
+        const uintptr_t from = reinterpret_cast<uintptr_t>(t.g), at = reinterpret_cast<uintptr_t>(apart);
+        if (apart && at + bytes > from && at < from + dtype_size(t.dtype) * (size_t)t.n)
+            return fail(MOE_ERR_ARG, "tensor %d holds the factor or the norm", i);
         *values += t.n;
     }
     return MOE_OK;
@@ -373,12 +377,12 @@ MOE_API int moe_grad_norm(const moe_grad_norm_config* c, const moe_grad_tensor* 
                           size_t ws_bytes, void* stream) {
     clear_error();
     if (!c) return fail(MOE_ERR_ARG, "config is NULL");
-    if (!(c->max_norm > 0)) return fail(MOE_ERR_ARG, "max_norm=%g must be > 0", c->max_norm);
+    if (!(c->max_norm >= 0)) return fail(MOE_ERR_ARG, "max_norm=%g must be >= 0", c->max_norm);
     if (!(c->eps >= 0) || !isfinite(c->eps)) return fail(MOE_ERR_ARG, "eps=%g must be >= 0 and finite", c->eps);
     for (int i = 0; i < 4; ++i)
         if (c->reserved[i]) return fail(MOE_ERR_ARG, "reserved fields must be zero");
     int64_t values;
-    int rc = check_list(ts, count, &values);
+    int rc = check_list(ts, count, out, 8, &values);
     if (rc) return rc;
     if (!out || !ws) return fail(MOE_ERR_ARG, "out or workspace is NULL");
     if (!aligned(out, 4) || !aligned(ws, 16)) return fail(MOE_ERR_ARG, "out must be 4-byte and ws 16-byte aligned");
@@ -394,7 +398,7 @@ MOE_API int moe_grad_norm(const moe_grad_norm_config* c, const moe_grad_tensor* 
 MOE_API int moe_grad_clip(const moe_grad_tensor* ts, int32_t count, const float* scale, void* stream) {
     clear_error();
     int64_t values;
-    int rc = check_list(ts, count, &values);
+    int rc = check_list(ts, count, scale, 4, &values);
     if (rc) return rc;
     if (!scale) return fail(MOE_ERR_ARG, "scale is NULL");
     if (!aligned(scale, 4)) return fail(MOE_ERR_ARG, "scale must be 4-byte aligned");
