@@ -58,9 +58,9 @@ enum RnMode : int { RN_OWN, RN_RAGGED, RN_DIRECT };
 // The columns of a thread, in units of two: a warp has 32 NV neighbouring ones, so that a thread's lie at fixed distances.
 // VEC > 1: pieces of VEC neighbouring values, piece q at 32 VEC q. VEC = 1: a unit is two values 32 apart (single
 // values of neighbouring threads lie beside one another), a piece is a unit.
-template <typename T, int VEC, int NV>
+template <typename T, int VEC_, int NV>
 struct RnColumns {
-    static constexpr int PV = VEC == 1 ? 2 : VEC, NP = NV / PV, UN = PV / 2, NU = NV / 2, STEP = VEC == 1 ? 64 : 32 * VEC;
+    static constexpr int VEC = VEC_, PV = VEC == 1 ? 2 : VEC, NP = NV / PV, UN = PV / 2, NU = NV / 2, STEP = VEC == 1 ? 64 : 32 * VEC;
     typedef Pack<T, PV> P;
     int c0, d, np;  // the first column, values of the row, this thread's pieces
     __device__ __forceinline__ RnColumns(int t, int d) : d(d) {

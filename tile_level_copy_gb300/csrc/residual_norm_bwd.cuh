@@ -24,7 +24,7 @@ namespace {
 __host__ __device__ constexpr int rb_ctas(int threads) { return threads > 256 ? 1 : 2; }
 constexpr size_t RB_SMEM_MOST = 224 * 1024;
 template <typename C>
-constexpr int RB_BATCH = C::NU < 8 ? C::NU : 8;  // units whose loads are in flight together
+constexpr int RB_BATCH = C::NU < 8 ? 4 : 8;  // units whose loads are in flight together
 
 // A thread's units of w2 and, behind all of those, of k in shared memory.
 template <typename C, int THREADS>
@@ -33,43 +33,113 @@ struct RbPlaces {
     __device__ __forceinline__ f2* w2(int j) const { return at + j * THREADS; }
     __device__ __forceinline__ f2* k(int j) const { return at + (C::NU + j) * THREADS; }
 };
-// Units of a vector from j0 on (null, and beyond the row: `none`).
+// A batch of units of a vector, from unit j0 on.
+template <typename C>
+struct RbUnits {
+    float v[RB_BATCH<C>][2];
+};
+// Reads them (null, and beyond the row: `none`) and writes them, in 16-byte pieces where the vector's alignment allows
+// (`whole`). With a gate for every row single values bound the pass: a warp's lie 16 or 32 bytes apart (16384 x 2048
+// bf16: 400 us; in pieces 239).
 template <typename T, typename C>
-__device__ __forceinline__ void vector_units(const C& c, const void* p, bool f32, float none, int64_t at, int j0,
-                                             float (&o)[RB_BATCH<C>][2]) {
-    auto each = [&](auto value) {
+__device__ __forceinline__ RbUnits<C> vector_units(const C& c, const void* p, bool f32, bool whole, float none, int64_t at, int j0) {
+    RbUnits<C> o;
+    auto single = [&](auto value) {
 #pragma unroll
         for (int k = 0; k < RB_BATCH<C>; ++k)
 #pragma unroll
-            for (int i = 0; i < 2; ++i) o[k][i] = c.inside(j0 + k, i) ? value(at + c.column(j0 + k, i)) : none;
+            for (int i = 0; i < 2; ++i) o.v[k][i] = c.inside(j0 + k, i) ? value(at + c.column(j0 + k, i)) : none;
     };
-    if (!p) each([&](int64_t) { return none; });
-    else if (f32) each([&](int64_t i) { return static_cast<const float*>(p)[i]; });
-    else each([&](int64_t i) { return num(static_cast<const T*>(p)[i]); });
+    auto pieces = [&](auto from) {  // of type F
+        typedef std::remove_const_t<std::remove_pointer_t<decltype(from)>> F;
+#pragma unroll
+        for (int k = 0; k < RB_BATCH<C>; k += C::UN) {
+            const int q = (j0 + k) / C::UN;
+            Pack<F, C::PV> e;
+            if (q < c.np) {
+#pragma unroll
+                for (int n = 0; n < (int)sizeof(e) / 16; ++n)
+                    reinterpret_cast<uint4*>(&e)[n] = reinterpret_cast<const uint4*>(from + (at + c.c0 + q * C::STEP))[n];
+            }
+#pragma unroll
+            for (int n = 0; n < C::UN; ++n) {
+                const float2 f = split(unit_of(e, n));
+                o.v[k + n][0] = q < c.np ? f.x : none;
+                o.v[k + n][1] = q < c.np ? f.y : none;
+            }
+        }
+    };
+    if (!p) {
+        single([&](int64_t) { return none; });
+        return o;
+    }
+    if constexpr (C::VEC > 1) {
+        if (whole) {
+            if (f32) pieces(static_cast<const float*>(p));
+            else pieces(static_cast<const T*>(p));
+            return o;
+        }
+    }
+    if (f32) single([&](int64_t i) { return static_cast<const float*>(p)[i]; });
+    else single([&](int64_t i) { return num(static_cast<const T*>(p)[i]); });
+    return o;
 }
-// Writes w2, and k of the rows that share gate g; zeros beyond the row. The sum of the thread's k. (This and
-// gate_end are calls, made once a gate: inlined they took registers from the loop over the rows.)
+template <typename T, typename C>
+__device__ __forceinline__ void put_units(const C& c, void* p, bool f32, bool whole, int64_t at, int j0, const RbUnits<C>& o) {
+    auto pieces = [&](auto to) {
+        typedef std::remove_pointer_t<decltype(to)> F;
+#pragma unroll
+        for (int k = 0; k < RB_BATCH<C>; k += C::UN) {
+            const int q = (j0 + k) / C::UN;
+            Pack<F, C::PV> e;
+#pragma unroll
+            for (int n = 0; n < C::UN; ++n) put_unit(e, n, pair(o.v[k + n][0], o.v[k + n][1]));
+            if (q >= c.np) continue;
+#pragma unroll
+            for (int n = 0; n < (int)sizeof(e) / 16; ++n)
+                reinterpret_cast<uint4*>(to + (at + c.c0 + q * C::STEP))[n] = reinterpret_cast<const uint4*>(&e)[n];
+        }
+    };
+    if constexpr (C::VEC > 1) {
+        if (whole) {
+            if (f32) pieces(static_cast<float*>(p));
+            else pieces(static_cast<T*>(p));
+            return;
+        }
+    }
+#pragma unroll
+    for (int k = 0; k < RB_BATCH<C>; ++k)
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            if (!c.inside(j0 + k, i)) continue;
+            const int64_t to = at + c.column(j0 + k, i);
+            if (f32) static_cast<float*>(p)[to] = o.v[k][i];
+            else put(static_cast<T*>(p)[to], o.v[k][i]);
+        }
+}
+// Writes k of the rows that share gate g and, where its places hold something else, w2; zeros beyond the row. The sum
+// of the thread's k. (This and gate_end are calls, made once a gate: inlined they took registers from the loop over the
+// rows.)
 template <typename T, typename C, typename Q>
-__device__ __noinline__ float make_weights(const C c, const Q places, const RnWeights& w, int64_t g) {
-    static_assert(C::NU % RB_BATCH<C> == 0, "whole batches");
+__device__ __noinline__ float make_weights(const C c, const Q places, const RnWeights& w, int64_t g, bool with_w2) {
+    static_assert(C::NU % RB_BATCH<C> == 0 && RB_BATCH<C> % C::UN == 0, "whole batches of whole pieces");
     float sum = 0.f;
 #pragma unroll 1
     for (int j0 = 0; j0 < C::NU; j0 += RB_BATCH<C>) {
-        float a[RB_BATCH<C>][2], k[RB_BATCH<C>][2], gate[RB_BATCH<C>][2];
-        vector_units<T>(c, w.pre_w, w.f32, 1.f, 0, j0, a);
-        vector_units<T>(c, w.post_w, w.f32, 1.f, 0, j0, k);
-        vector_units<T>(c, w.gate, w.f32, 1.f, g * c.d, j0, gate);
+        RbUnits<C> a, k = vector_units<T>(c, w.post_w, w.f32, w.whole, 1.f, 0, j0);
+        const RbUnits<C> gate = vector_units<T>(c, w.gate, w.f32, w.whole, 1.f, g * c.d, j0);
+        if (with_w2) a = vector_units<T>(c, w.pre_w, w.f32, w.whole, 1.f, 0, j0);
 #pragma unroll
         for (int n = 0; n < RB_BATCH<C>; ++n) {
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
                 const bool in = c.inside(j0 + n, i);
-                a[n][i] = in ? a[n][i] : 0.f;
-                k[n][i] = in ? k[n][i] * gate[n][i] : 0.f;
-                sum += k[n][i];
+                a.v[n][i] = in ? a.v[n][i] : 0.f;
+                k.v[n][i] = in ? k.v[n][i] * gate.v[n][i] : 0.f;
+                sum += k.v[n][i];
             }
-            *places.w2(j0 + n) = pair(a[n][0], a[n][1]);
-            *places.k(j0 + n) = pair(k[n][0], k[n][1]);
+            if (with_w2) *places.w2(j0 + n) = pair(a.v[n][0], a.v[n][1]);
+            *places.k(j0 + n) = pair(k.v[n][0], k.v[n][1]);
         }
     }
     return sum;
@@ -78,43 +148,44 @@ __device__ __noinline__ float make_weights(const C c, const Q places, const RnWe
 // in sums [2][d], and w1 S + b1 B to part (a gate whose other rows lie elsewhere) or into dgate.
 template <typename T, bool FULL, typename C, typename Q>
 __device__ __noinline__ void gate_end(const C c, const Q places, const RnWeights& w, int64_t g, float* sums, float* part,
-                                      void* dgate) {
+                                      void* dgate, bool whole_dgate) {
 #pragma unroll 1
     for (int j0 = 0; j0 < C::NU; j0 += RB_BATCH<C>) {
-        float gate[RB_BATCH<C>][2], w1[RB_BATCH<C>][2], b1[RB_BATCH<C>][2], a[RB_BATCH<C>][2], e[RB_BATCH<C>][2];
-        vector_units<T>(c, w.gate, w.f32, 1.f, g * c.d, j0, gate);
-        vector_units<T>(c, w.post_w, w.f32, 1.f, 0, j0, w1);
-        vector_units<T>(c, sums, true, 0.f, 0, j0, a);
+        const RbUnits<C> gate = vector_units<T>(c, w.gate, w.f32, w.whole, 1.f, g * c.d, j0);
+        const RbUnits<C> w1 = vector_units<T>(c, w.post_w, w.f32, w.whole, 1.f, 0, j0);
+        RbUnits<C> a = vector_units<T>(c, sums, true, true, 0.f, 0, j0), b1, e, out;
         if (FULL) {
-            vector_units<T>(c, w.post_b, w.f32, 0.f, 0, j0, b1);
-            vector_units<T>(c, sums, true, 0.f, c.d, j0, e);
+            b1 = vector_units<T>(c, w.post_b, w.f32, w.whole, 0.f, 0, j0);
+            e = vector_units<T>(c, sums, true, true, 0.f, c.d, j0);
         }
 #pragma unroll
         for (int k = 0; k < RB_BATCH<C>; ++k) {
             const float2 x = split(*places.k(j0 + k)), y = split(*places.w2(j0 + k));
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
-                if (!c.inside(j0 + k, i)) continue;
-                const int col = c.column(j0 + k, i);
                 const float xs = i ? x.y : x.x, ys = i ? y.y : y.x;
-                sums[col] = fmaf(gate[k][i], xs, a[k][i]);
-                if (FULL) sums[c.d + col] = fmaf(gate[k][i], ys, e[k][i]);
-                if (!dgate) continue;
-                float out = w1[k][i] * xs;
-                if (FULL) out = fmaf(b1[k][i], ys, out);
-                if (part) part[col] = out;
-                else if (w.f32) static_cast<float*>(dgate)[g * c.d + col] = out;
-                else put(static_cast<T*>(dgate)[g * c.d + col], out);
+                a.v[k][i] = fmaf(gate.v[k][i], xs, a.v[k][i]);
+                out.v[k][i] = w1.v[k][i] * xs;
+                if (FULL) {
+                    e.v[k][i] = fmaf(gate.v[k][i], ys, e.v[k][i]);
+                    out.v[k][i] = fmaf(b1.v[k][i], ys, out.v[k][i]);
+                }
             }
         }
+        put_units<T>(c, sums, true, true, 0, j0, a);
+        if (FULL) put_units<T>(c, sums, true, true, c.d, j0, e);
+        if (!dgate) continue;
+        if (part) put_units<T>(c, part, true, true, 0, j0, out);
+        else put_units<T>(c, dgate, w.f32, whole_dgate, g * c.d, j0, out);
     }
 }
 
 // THREADS: at most so many in a CTA, and the stride of a thread's places in shared memory, so that they have fixed
 // distances. Rows that are not there count as zeros, a norm that is not there as one with mean 0 and rstd 1 whose
-// sums are left out: the same instructions serve every kind.
-template <typename T, int VEC, int NV, int THREADS, bool FULL, int MODE>
-__global__ void __launch_bounds__(THREADS, rb_ctas(THREADS)) rn_backward_kernel(RnShape s, RnWeights w, RnBackward b, int grouped) {
+// sums are left out: the same instructions serve every kind. GROUPED: more gates than one (a kernel of its own: the calls
+// at a gate's end take registers from the loop over the rows).
+template <typename T, int VEC, int NV, int THREADS, bool FULL, int MODE, bool GROUPED>
+__global__ void __launch_bounds__(THREADS, rb_ctas(THREADS)) rn_backward_kernel(RnShape s, RnWeights w, RnBackward b) {
     typedef RnColumns<T, VEC, NV> C;
     typedef typename C::P P;
     typedef f2 V;
@@ -191,8 +262,8 @@ __global__ void __launch_bounds__(THREADS, rb_ctas(THREADS)) rn_backward_kernel(
     float2 next1 = post && total_rows ? stats1[0] : plain, next2 = s.pre && total_rows ? stats2[0] : plain;
     float ksum = 0.f;
     if (total_rows) {
-        ksum = make_weights<T>(cols, places, w, grouped ? first / s.gate_rows : 0);
-        if (grouped && b.part) {
+        ksum = make_weights<T>(cols, places, w, GROUPED ? first / s.gate_rows : 0, true);
+        if (GROUPED && b.part) {
             float* const sums = b.gsum + 2 * worker * s.d;
             for (int c = t; c < (FULL ? 2 : 1) * s.d; c += tpr) sums[c] = 0.f;
             __threadfence_block();
@@ -213,7 +284,7 @@ __global__ void __launch_bounds__(THREADS, rb_ctas(THREADS)) rn_backward_kernel(
     // rows that share a gate; what a gate's end takes stays out of the loop over them
     for (int row = 0; row < total_rows;) {
         int stop = total_rows;
-        if (grouped) {
+        if (GROUPED) {
             const int64_t left = s.gate_rows - (first + row) % s.gate_rows;
             if (left < stop - row) stop = row + (int)left;
         }
@@ -327,7 +398,7 @@ __global__ void __launch_bounds__(THREADS, rb_ctas(THREADS)) rn_backward_kernel(
             here = here == own + (s.slots - 1) * SLOT ? own : here + SLOT;
             at += s.d;
         }
-        if (grouped) {
+        if (GROUPED) {
             // A gate whose rows all lie here is done; else these rows' sums: in the first row those of a gate that began
             // earlier or that the worker begins with. S and B pass through the weights' places.
             const int64_t g = (first + row - 1) / s.gate_rows;
@@ -341,8 +412,9 @@ __global__ void __launch_bounds__(THREADS, rb_ctas(THREADS)) rn_backward_kernel(
                 s1[j] = both<V>(0.f);
                 if (FULL) s2[FULL ? j : 0] = both<V>(0.f);
             }
-            if (b.part) gate_end<T, FULL>(cols, places, w, g, b.gsum + 2 * worker * s.d, whole ? nullptr : p, b.dgate);
-            if (row < total_rows) ksum = make_weights<T>(cols, places, w, g + 1);
+            if (b.part) gate_end<T, FULL>(cols, places, w, g, b.gsum + 2 * worker * s.d, whole ? nullptr : p, b.dgate,
+                                          (reinterpret_cast<uintptr_t>(b.dgate) & 15) == 0);
+            if (row < total_rows) ksum = make_weights<T>(cols, places, w, g + 1, FULL);
         }
     }
     if (MODE != RN_DIRECT) fetched(0);
@@ -350,7 +422,7 @@ __global__ void __launch_bounds__(THREADS, rb_ctas(THREADS)) rn_backward_kernel(
     const V branch = both<V>(s.branch);
 #pragma unroll
     for (int j = 0; j < NU; ++j) {
-        if (!grouped) {
+        if (!GROUPED) {
             s1[j] = mul_(s1[j], branch);
             if (FULL) s2[FULL ? j : 0] = mul_(s2[FULL ? j : 0], branch);
         } else if (total_rows) {  // dw1 and db1 in the place of S and B
@@ -401,10 +473,10 @@ template <typename T>
 cudaError_t launch_residual_backward(RnShape s, const RnWeights& w, const RnBackward& b, int vec, bool full, bool grouped,
                                      int ctas, cudaStream_t st) {
     const int threads = 32 * s.warps * s.groups;
-    auto go = [&](auto width, auto values, auto most, auto whole, auto how) {
+    auto launch = [&](auto width, auto values, auto most, auto whole, auto how, auto gates) {
         constexpr int VEC = decltype(width)::value, NV = decltype(values)::value, THREADS = decltype(most)::value;
         constexpr int MODE = decltype(how)::value;
-        constexpr auto kernel = &rn_backward_kernel<T, VEC, NV, THREADS, decltype(whole)::value, MODE>;
+        constexpr auto kernel = &rn_backward_kernel<T, VEC, NV, THREADS, decltype(whole)::value, MODE, decltype(gates)::value>;
         constexpr size_t weights = (size_t)2 * NV * THREADS * 4, row = (size_t)4 * NV * THREADS * sizeof(T);
         constexpr size_t slot = MODE == RN_DIRECT ? 0 : MODE == RN_OWN ? row : (size_t)4 * rn_cover<T>(NV, THREADS);
         constexpr size_t room = RB_SMEM_MOST / rb_ctas(THREADS);
@@ -415,7 +487,10 @@ cudaError_t launch_residual_backward(RnShape s, const RnWeights& w, const RnBack
         if (s.groups > 1 && smem < sums) smem = sums;
         const cudaError_t e = allow_smem<kernel>(RB_SMEM_MOST);
         if (e != cudaSuccess) return e;
-        return launch_k(kernel, dim3(ctas), dim3(threads), smem, st, true, s, w, b, (int)grouped);
+        return launch_k(kernel, dim3(ctas), dim3(threads), smem, st, true, s, w, b);
+    };
+    auto go = [&](auto width, auto values, auto most, auto whole, auto how) {
+        return grouped ? launch(width, values, most, whole, how, std::true_type()) : launch(width, values, most, whole, how, std::false_type());
     };
     auto kinds = [&](auto width, auto values, auto most, auto how) {
         return full ? go(width, values, most, std::true_type(), how) : go(width, values, most, std::false_type(), how);
