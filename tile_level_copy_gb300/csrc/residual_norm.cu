@@ -8,11 +8,11 @@ namespace moe {
 namespace {
 
 constexpr int RN_RED_COLS = 32, RN_RED_ROWS = 32, RN_RED_FLY = 10;
-constexpr int RN_GATE_ROWS = 8;  // of a CTA of the gates' sums
 constexpr int RN_MAX_SMS = 256;
 
 // The gradients of the weights from the CTAs' sums [parts][sums][d]: blockIdx.y 0 the norm before the next block
 // (sum 0, and 1 with full), 1 the norm behind this one and a gate that all rows share (the last one or two sums).
+// blockIdx.y from 2 on: the gradients of the gates whose rows lie in more than one group of warps.
 struct RnReduce {
     const float* part;
     const float* gpart;
@@ -21,6 +21,9 @@ struct RnReduce {
     const void *post_w, *post_b, *gate;
     void *dpost_w, *dpost_b, *dgate, *dpre_w, *dpre_b;
     int64_t rows, gate_rows, chunk;
+    int64_t shared;  // gates, or places between groups of warps, whichever are fewer
+    bool at_places;
+    int each;  // warps for one of them, a power of two: four rows of sums in flight each
 };
 template <typename T>
 __device__ __forceinline__ void put_at(void* p, bool f32, int64_t i, float v) {
@@ -28,12 +31,61 @@ __device__ __forceinline__ void put_at(void* p, bool f32, int64_t i, float v) {
     if (f32) static_cast<float*>(p)[i] = v;
     else put(static_cast<T*>(p)[i], v);
 }
+__device__ __forceinline__ int64_t over(int64_t a, int64_t b) {  // (a quotient of 64 bits takes four times as long)
+    return (uint64_t)(a | b) >> 32 ? a / b : (int64_t)((uint32_t)a / (uint32_t)b);
+}
+// These gates' gradients from the groups' sums, as many at once as a CTA's warps do. The gates are found among all or, where these
+// are more, among the places where one group's rows end and the next one's begin: at row b chunk; a gate that lies
+// around several such places is that of the first. (With a gate for each of 16384 rows most need nothing: going over them
+// took 600 us.)
+template <typename T>
+__device__ __forceinline__ void shared_gates(const RnReduce& a, float (*acc)[RN_RED_COLS], int lane, int row, int c) {
+    const int each = a.each, gates = RN_RED_ROWS / each, mine = row / each, first = row % each;
+    for (int64_t i0 = (int64_t)(blockIdx.y - 2) * gates; i0 < a.shared; i0 += (int64_t)(gridDim.y - 2) * gates) {
+        const int64_t i = i0 + mine;
+        int64_t g = 0, from = 0, w0 = 0, w1 = 0;
+        bool there = i < a.shared;
+        if (there) {
+            g = a.at_places ? over((i + 1) * a.chunk, a.gate_rows) : i;
+            from = g * a.gate_rows;
+            const int64_t to = from + a.gate_rows < a.rows ? from + a.gate_rows : a.rows;
+            if (a.at_places) there = from < (i + 1) * a.chunk && from >= i * a.chunk;
+            w0 = a.at_places ? i : over(from, a.chunk);
+            w1 = over(to - 1, a.chunk);
+            there = there && w0 < w1;  // (else the group of warps wrote it)
+        }
+        float v = 0.f;
+        if (there && c < a.d) {  // only the first group of warps may have begun with an earlier gate
+            for (int64_t k = w0 + first; k <= w1; k += 4 * each) {  // four loads in flight
+                float e[4];
+#pragma unroll
+                for (int n = 0; n < 4; ++n) {
+                    const int64_t at = k + n * each;
+                    e[n] = at <= w1 ? a.gpart[(2 * at + (at == w0 && w0 * a.chunk < from ? 1 : 0)) * a.d + c] : 0.f;
+                }
+#pragma unroll
+                for (int n = 0; n < 4; ++n) v += e[n];
+            }
+        }
+        if (!__syncthreads_or(there)) continue;
+        acc[row][lane] = v;
+        __syncthreads();
+        if (there && first == 0 && c < a.d) {
+            for (int q = 1; q < each; ++q) v += acc[row + q][lane];
+            put_at<T>(a.dgate, a.f32, g * a.d + c, v);
+        }
+    }
+}
 template <typename T>
 __global__ void __launch_bounds__(RN_RED_COLS* RN_RED_ROWS) rn_reduce_kernel(RnReduce a) {
     __shared__ float acc[2][RN_RED_ROWS][RN_RED_COLS];
     griddep_wait();
     griddep_launch();
     const int lane = threadIdx.x % RN_RED_COLS, row = threadIdx.x / RN_RED_COLS, c = blockIdx.x * RN_RED_COLS + lane;
+    if (blockIdx.y >= 2) {
+        shared_gates<T>(a, acc[0], lane, row, c);
+        return;
+    }
     const int sums = a.full ? 4 : 2, first = blockIdx.y == 0 ? 0 : sums / 2;
     float v[2] = {0.f, 0.f};
     if (c < a.d) {
@@ -77,49 +129,6 @@ __global__ void __launch_bounds__(RN_RED_COLS* RN_RED_ROWS) rn_reduce_kernel(RnR
         put_at<T>(a.dpost_w, a.f32, c, x * g);
         put_at<T>(a.dpost_b, a.f32, c, y * g);
         put_at<T>(a.dgate, a.f32, c, value_at<T>(a.post_w, a.f32, c, 1.f) * x + value_at<T>(a.post_b, a.f32, c, 0.f) * y);
-    }
-}
-
-// The gradients of the gates whose rows lie in more than one group of warps, from those groups' sums. They are found
-// among the gates or, where these are more, among the places where one group's rows end and the next one's begin: at row
-// b chunk; a gate that lies around several such places is that of the first. (With a gate for each of 16384 rows most
-// gates need nothing: going over them took 600 us.)
-__device__ __forceinline__ int64_t over(int64_t a, int64_t b) {  // (a quotient of 64 bits takes four times as long)
-    return (uint64_t)(a | b) >> 32 ? a / b : (int64_t)((uint32_t)a / (uint32_t)b);
-}
-template <typename T>
-__global__ void __launch_bounds__(RN_RED_COLS* RN_GATE_ROWS) rn_gate_kernel(RnReduce a, int64_t n, bool at_places) {
-    __shared__ float acc[RN_GATE_ROWS][RN_RED_COLS];
-    griddep_wait();
-    griddep_launch();
-    const int lane = threadIdx.x % RN_RED_COLS, row = threadIdx.x / RN_RED_COLS, c = blockIdx.x * RN_RED_COLS + lane;
-    for (int64_t i = blockIdx.y; i < n; i += gridDim.y) {
-        const int64_t g = at_places ? over((i + 1) * a.chunk, a.gate_rows) : i, from = g * a.gate_rows;
-        if (at_places && (from == (i + 1) * a.chunk || from < i * a.chunk)) continue;
-        const int64_t to = from + a.gate_rows < a.rows ? from + a.gate_rows : a.rows;
-        const int64_t w0 = at_places ? i : over(from, a.chunk), w1 = over(to - 1, a.chunk);
-        if (w0 == w1) continue;  // the group of warps wrote it
-        float v = 0.f;
-        if (c < a.d) {  // only the first group of warps may have begun with an earlier gate
-            for (int64_t k = w0 + row; k <= w1; k += 4 * RN_GATE_ROWS) {  // four loads in flight
-                float e[4];
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const int64_t at = k + i * RN_GATE_ROWS;
-                    e[i] = at <= w1 ? a.gpart[(2 * at + (at == w0 && w0 * a.chunk < from ? 1 : 0)) * a.d + c] : 0.f;
-                }
-#pragma unroll
-                for (int i = 0; i < 4; ++i) v += e[i];
-            }
-        }
-        __syncthreads();
-        acc[row][lane] = v;
-        __syncthreads();
-        if (row || c >= a.d) continue;
-        v = 0.f;
-#pragma unroll
-        for (int q = 0; q < RN_GATE_ROWS; ++q) v += acc[q][lane];
-        put_at<T>(a.dgate, a.f32, g * a.d + c, v);
     }
 }
 
@@ -198,11 +207,14 @@ bool grouped_of(const moe_residual_norm_config& c) { return c.gate_rows > 0 && c
 // Backward: CTAs, and the consecutive rows of each group of warps.
 RnShape backward_shape(const moe_residual_norm_config& c, int sms, int* ctas) {
     RnShape s = shape_of(c);
-    s.warps = rn_warps(c.d, rn_backward_values(c.d, full_of(c)));
+    s.warps = rn_warps(c.d, rn_backward_values(c.d, c.dtype, full_of(c), grouped_of(c)));
     s.groups = s.warps < 8 ? 8 / s.warps : 1;
     const int64_t most = (int64_t)sms * (s.warps * s.groups > 8 ? 1 : 2) * s.groups;
     const int64_t workers = c.rows < most ? c.rows : most;
     s.chunk = workers ? (c.rows + workers - 1) / workers : 1;
+    // whole gates where a sixteenth more rows do: their gradients then need no sums over groups
+    const int64_t even = grouped_of(c) ? (s.chunk + c.gate_rows - 1) / c.gate_rows * c.gate_rows : s.chunk;
+    if ((even - s.chunk) * 16 <= s.chunk) s.chunk = even;
     const int64_t used = (c.rows + s.chunk - 1) / s.chunk;
     *ctas = (int)((used + s.groups - 1) / s.groups);
     return s;
@@ -327,16 +339,17 @@ MOE_API int moe_residual_norm_backward(const moe_residual_norm_config* c, const 
         typedef decltype(type) T;
         const cudaError_t e0 = launch_residual_backward<T>(s, w, b, vec, full, grouped, ctas, st);
         if (e0 != cudaSuccess || !any) return e0;
-        const RnReduce a{part, gpart, ctas, c->d, full, grouped, w.f32, post_w, post_b, gate, dpost_w, dpost_b, dgate, dpre_w,
-                         dpre_b, c->rows, c->gate_rows, s.chunk};
-        const unsigned columns = (c->d + RN_RED_COLS - 1) / RN_RED_COLS;
-        const cudaError_t e1 = launch_k(rn_reduce_kernel<T>, dim3(columns, 2), dim3(RN_RED_COLS * RN_RED_ROWS), 0, st, true, a);
-        if (e1 != cudaSuccess || !grouped || !dgate) return e1;
-        const int64_t places = (c->rows + s.chunk - 1) / s.chunk - 1;
-        const int64_t gates = (c->rows + c->gate_rows - 1) / c->gate_rows, n = places < gates ? places : gates;
-        if (n == 0) return e1;
-        return launch_k(rn_gate_kernel<T>, dim3(columns, (unsigned)(n < 64 ? n : 64)), dim3(RN_RED_COLS * RN_GATE_ROWS), 0, st, true,
-                        a, n, places < gates);
+        RnReduce a{part, gpart, ctas, c->d, full, grouped, w.f32, post_w, post_b, gate, dpost_w, dpost_b, dgate, dpre_w, dpre_b,
+                   c->rows, c->gate_rows, s.chunk, 0, false, 1};
+        if (grouped && dgate && s.chunk % c->gate_rows) {
+            const int64_t places = (c->rows - 1) / s.chunk, gates = (c->rows + c->gate_rows - 1) / c->gate_rows;
+            a.at_places = places < gates;
+            a.shared = a.at_places ? places : gates;
+        }
+        while (a.each < RN_RED_ROWS && a.each * 4 < c->gate_rows / s.chunk + 2) a.each *= 2;
+        const int64_t more = (a.shared * a.each + RN_RED_ROWS - 1) / RN_RED_ROWS;
+        return launch_k(rn_reduce_kernel<T>, dim3((c->d + RN_RED_COLS - 1) / RN_RED_COLS, (unsigned)(2 + (more < 32 ? more : 32))),
+                        dim3(RN_RED_COLS * RN_RED_ROWS), 0, st, true, a);
     });
     return err == cudaSuccess ? MOE_OK : cuda_fail(err, "residual norm backward launch");
 }

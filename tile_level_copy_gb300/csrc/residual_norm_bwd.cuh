@@ -500,9 +500,15 @@ cudaError_t launch_residual_backward(RnShape s, const RnWeights& w, const RnBack
     typedef Int<RN_RAGGED> Ragged;
     typedef Int<RN_DIRECT> Direct;
     const bool one = vec == 1;
-    if (full && rn_backward_values(s.d, full) == 8)
-        return one ? go(Int<1>(), Int<8>(), Int<256>(), std::true_type(), Ragged()) : go(Int<VEC>(), Int<8>(), Int<256>(), std::true_type(), Own());
-    if (rn_backward_values(s.d, full) == 32)
+    if (full && (grouped || sizeof(T) == 4) && s.d <= 2048) {
+        auto short_rows = [&](auto gates) {
+            return one ? launch(Int<1>(), Int<8>(), Int<256>(), std::true_type(), Ragged(), gates)
+                       : launch(Int<VEC>(), Int<8>(), Int<256>(), std::true_type(), Own(), gates);
+        };
+        if (grouped) return short_rows(std::true_type());
+        if constexpr (sizeof(T) == 4) return short_rows(std::false_type());
+    }
+    if (s.d > 8192)
         return one ? kinds(Int<1>(), Int<32>(), Int<512>(), Direct()) : kinds(Int<VEC>(), Int<32>(), Int<512>(), Direct());
     if (threads > 256) return one ? kinds(Int<1>(), Int<16>(), Int<512>(), Ragged()) : kinds(Int<VEC>(), Int<16>(), Int<512>(), Own());
     return one ? kinds(Int<1>(), Int<16>(), Int<256>(), Ragged()) : kinds(Int<VEC>(), Int<16>(), Int<256>(), Own());
