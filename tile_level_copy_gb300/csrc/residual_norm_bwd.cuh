@@ -145,18 +145,18 @@ __device__ __noinline__ float make_weights(const C c, const Q places, const RnWe
     return sum;
 }
 // The end of the rows that share gate g: S lies in the places of k, B in those of w2. dw1 += gate S and db1 += gate B
-// in sums [2][d], and w1 S + b1 B to part (a gate whose other rows lie elsewhere) or into dgate.
+// in sums [2][d] (fresh: nothing is there yet), and w1 S + b1 B to part (a gate whose other rows lie elsewhere) or into dgate.
 template <typename T, bool FULL, typename C, typename Q>
 __device__ __noinline__ void gate_end(const C c, const Q places, const RnWeights& w, int64_t g, float* sums, float* part,
-                                      void* dgate, bool whole_dgate) {
+                                      void* dgate, bool whole_dgate, bool fresh) {
 #pragma unroll 1
     for (int j0 = 0; j0 < C::NU; j0 += RB_BATCH<C>) {
         const RbUnits<C> gate = vector_units<T>(c, w.gate, w.f32, w.whole, 1.f, g * c.d, j0);
         const RbUnits<C> w1 = vector_units<T>(c, w.post_w, w.f32, w.whole, 1.f, 0, j0);
-        RbUnits<C> a = vector_units<T>(c, sums, true, true, 0.f, 0, j0), b1, e, out;
+        RbUnits<C> a = vector_units<T>(c, fresh ? nullptr : sums, true, true, 0.f, 0, j0), b1, e, out;
         if (FULL) {
             b1 = vector_units<T>(c, w.post_b, w.f32, w.whole, 0.f, 0, j0);
-            e = vector_units<T>(c, sums, true, true, 0.f, c.d, j0);
+            e = vector_units<T>(c, fresh ? nullptr : sums, true, true, 0.f, c.d, j0);
         }
 #pragma unroll
         for (int k = 0; k < RB_BATCH<C>; ++k) {
@@ -263,12 +263,6 @@ __global__ void __launch_bounds__(THREADS, rb_ctas(THREADS)) rn_backward_kernel(
     float ksum = 0.f;
     if (total_rows) {
         ksum = make_weights<T>(cols, places, w, GROUPED ? first / s.gate_rows : 0, true);
-        if (GROUPED && b.part) {
-            float* const sums = b.gsum + 2 * worker * s.d;
-            for (int c = t; c < (FULL ? 2 : 1) * s.d; c += tpr) sums[c] = 0.f;
-            __threadfence_block();
-            named_bar_sync(1 + group, tpr);
-        }
     }
     // sums of a thread's columns: dw2, db2, S / c, B / c
     V sp[NU], sq[FULL ? NU : 1], s1[NU], s2[FULL ? NU : 1];
@@ -413,7 +407,7 @@ __global__ void __launch_bounds__(THREADS, rb_ctas(THREADS)) rn_backward_kernel(
                 if (FULL) s2[FULL ? j : 0] = both<V>(0.f);
             }
             if (b.part) gate_end<T, FULL>(cols, places, w, g, b.gsum + 2 * worker * s.d, whole ? nullptr : p, b.dgate,
-                                          (reinterpret_cast<uintptr_t>(b.dgate) & 15) == 0);
+                                          (reinterpret_cast<uintptr_t>(b.dgate) & 15) == 0, g == first / s.gate_rows);
             if (row < total_rows) ksum = make_weights<T>(cols, places, w, g + 1, FULL);
         }
     }
