@@ -66,15 +66,16 @@ template <typename T, int VEC_, int NV>
 struct RnColumns {
     static constexpr int VEC = VEC_, PV = VEC == 1 ? 2 : VEC, NP = NV / PV, UN = PV / 2, NU = NV / 2, STEP = VEC == 1 ? 64 : 32 * VEC;
     typedef Pack<T, PV> P;
-    int c0, d, np;  // the first column, values of the row, this thread's pieces
+    int c0, d, np, nv;  // the first column, values of the row, this thread's pieces, its values (VEC = 1)
     __device__ __forceinline__ RnColumns(int t, int d) : d(d) {
         c0 = (t >> 5) * (32 * NV) + (t & 31) * VEC;
         np = c0 < d ? min(NP, (d - c0 + STEP - 1) / STEP) : 0;
+        nv = c0 < d ? min(NV, (d - c0 + 31) / 32) : 0;
     }
     __device__ __forceinline__ int column(int j, int i) const {  // of value i of unit j
         return VEC == 1 ? c0 + j * STEP + i * 32 : c0 + (j / UN) * STEP + (j % UN) * 2 + i;
     }
-    __device__ __forceinline__ bool inside(int j, int i) const { return VEC == 1 ? column(j, i) < d : j / UN < np; }
+    __device__ __forceinline__ bool inside(int j, int i) const { return VEC == 1 ? 2 * j + i < nv : j / UN < np; }
     // piece q of a row, whose values from column c0 on lie at p (global memory, or its bytes in a slot); values
     // beyond the row are zero
     __device__ __forceinline__ P load(const T* p, int q) const {
@@ -159,6 +160,10 @@ __device__ __forceinline__ void cover_row(uint8_t* to, const T* rows, int64_t n,
     const int off = offset_of(from), pieces = (off + d * (int)sizeof(T) + 15) / 16;
     const uint8_t* const start = reinterpret_cast<const uint8_t*>(from) - off;
     const uint8_t *const lo = reinterpret_cast<const uint8_t*>(rows), *const hi = reinterpret_cast<const uint8_t*>(rows + n);
+    if (start >= lo && start + 16 * pieces <= hi) {
+        for (int i = t; i < pieces; i += threads) copy_async<16>(to + 16 * i, start + 16 * i);
+        return;
+    }
     for (int i = t; i < pieces; i += threads) {
         const uint8_t* const p = start + 16 * i;
         if (p >= lo && p + 16 <= hi) {
@@ -170,14 +175,17 @@ __device__ __forceinline__ void cover_row(uint8_t* to, const T* rows, int64_t n,
     }
 }
 
-// Zeros behind a row in its slot, up to the end of the pieces that a row may take, by the thread that fetched the row's
-// last piece, once it is there. (What lies behind those pieces is zeroed once.)
+// Zeros behind a row in its slot, up to the end of the pieces that a row may take, by the lanes of the warp that fetched the
+// row's last piece (its number modulo the row's threads tells which did), once it is there for all of them. A row's last piece is
+// last_piece or one more. (What lies behind those that a row may take is zeroed once.)
 template <typename T>
-__device__ __forceinline__ void pad_row(uint8_t* to, const T* rows, int64_t at, int d, int t, int threads) {
+__device__ __forceinline__ int last_piece(int d) { return (d * (int)sizeof(T) + 15) / 16 - 1; }
+template <typename T>
+__device__ __forceinline__ void pad_row(uint8_t* to, const T* rows, int64_t at, int d, bool owner, bool next_owner, int lane) {
     constexpr int size = (int)sizeof(T);
-    const int end = offset_of(rows + at) + d * size, last = (end + 15) / 16 - 1, most = (16 - size + d * size + 15) / 16 * 16;
-    if ((last - t) % threads) return;
-    for (int b = end; b < most; b += size) put(*reinterpret_cast<T*>(to + b), 0.f);
+    const int end = offset_of(rows + at) + d * size, most = (16 - size + d * size + 15) / 16 * 16;
+    const int b = end + lane * size;  // (fewer than 32 bytes)
+    if (((end + 15) / 16 - 1 == last_piece<T>(d) ? owner : next_owner) && b < most) put(*reinterpret_cast<T*>(to + b), 0.f);
 }
 
 __device__ __forceinline__ void committed() { asm volatile("cp.async.commit_group;" ::: "memory"); }

@@ -145,10 +145,10 @@ __device__ __noinline__ float make_weights(const C c, const Q places, const RnWe
     return sum;
 }
 // The end of the rows that share gate g: S lies in the places of k, B in those of w2. dw1 += gate S and db1 += gate B
-// in sums [2][d] (fresh: nothing is there yet), and w1 S + b1 B to part (a gate whose other rows lie elsewhere) or into dgate.
+// in sums [2][d] (fresh: nothing is there yet; last: they go to the places of k and w2), and w1 S + b1 B to part (a gate whose other rows lie elsewhere) or into dgate.
 template <typename T, bool FULL, typename C, typename Q>
 __device__ __noinline__ void gate_end(const C c, const Q places, const RnWeights& w, int64_t g, float* sums, float* part,
-                                      void* dgate, bool whole_dgate, bool fresh) {
+                                      void* dgate, bool whole_dgate, bool fresh, bool last) {
 #pragma unroll 1
     for (int j0 = 0; j0 < C::NU; j0 += RB_BATCH<C>) {
         const RbUnits<C> gate = vector_units<T>(c, w.gate, w.f32, w.whole, 1.f, g * c.d, j0);
@@ -172,8 +172,16 @@ __device__ __noinline__ void gate_end(const C c, const Q places, const RnWeights
                 }
             }
         }
-        put_units<T>(c, sums, true, true, 0, j0, a);
-        if (FULL) put_units<T>(c, sums, true, true, c.d, j0, e);
+        if (last) {
+#pragma unroll
+            for (int k = 0; k < RB_BATCH<C>; ++k) {
+                *places.k(j0 + k) = pair(a.v[k][0], a.v[k][1]);
+                if (FULL) *places.w2(j0 + k) = pair(e.v[k][0], e.v[k][1]);
+            }
+        } else {
+            put_units<T>(c, sums, true, true, 0, j0, a);
+            if (FULL) put_units<T>(c, sums, true, true, c.d, j0, e);
+        }
         if (!dgate) continue;
         if (part) put_units<T>(c, part, true, true, 0, j0, out);
         else put_units<T>(c, dgate, w.f32, whole_dgate, g * c.d, j0, out);
@@ -237,10 +245,13 @@ __global__ void __launch_bounds__(THREADS, rb_ctas(THREADS)) rn_backward_kernel(
         return p;
     };
 
+    const bool owner = MODE == RN_RAGGED && last_piece<T>(s.d) % tpr / 32 == t / 32;
+    const bool next_owner = MODE == RN_RAGGED && (last_piece<T>(s.d) + 1) % tpr / 32 == t / 32;
     auto pad = [&](int64_t at, uint8_t* to) {
+        __syncwarp();
 #pragma unroll
         for (int n = 0; n < 4; ++n)
-            if (rows[n]) pad_row(to + n * NEXT, rows[n], at, s.d, t, tpr);
+            if (rows[n]) pad_row(to + n * NEXT, rows[n], at, s.d, owner, next_owner, lane);
     };
     if (MODE == RN_RAGGED) {
         uint8_t* const slots = rb_smem + 2 * NU * THREADS * sizeof(V);
@@ -407,7 +418,7 @@ __global__ void __launch_bounds__(THREADS, rb_ctas(THREADS)) rn_backward_kernel(
                 if (FULL) s2[FULL ? j : 0] = both<V>(0.f);
             }
             if (b.part) gate_end<T, FULL>(cols, places, w, g, b.gsum + 2 * worker * s.d, whole ? nullptr : p, b.dgate,
-                                          (reinterpret_cast<uintptr_t>(b.dgate) & 15) == 0, g == first / s.gate_rows);
+                                          (reinterpret_cast<uintptr_t>(b.dgate) & 15) == 0, g == first / s.gate_rows, row == total_rows);
             if (row < total_rows) ksum = make_weights<T>(cols, places, w, g + 1, FULL);
         }
     }
@@ -420,16 +431,8 @@ __global__ void __launch_bounds__(THREADS, rb_ctas(THREADS)) rn_backward_kernel(
             s1[j] = mul_(s1[j], branch);
             if (FULL) s2[FULL ? j : 0] = mul_(s2[FULL ? j : 0], branch);
         } else if (total_rows) {  // dw1 and db1 in the place of S and B
-            const float* const sums = b.gsum + 2 * worker * s.d;
-            float v[2][2] = {{0.f, 0.f}, {0.f, 0.f}};
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                if (!cols.inside(j, i)) continue;
-                v[0][i] = sums[cols.column(j, i)];
-                if (FULL) v[1][i] = sums[s.d + cols.column(j, i)];
-            }
-            s1[j] = pair(v[0][0], v[0][1]);
-            if (FULL) s2[FULL ? j : 0] = pair(v[1][0], v[1][1]);
+            s1[j] = *places.k(j);
+            if (FULL) s2[FULL ? j : 0] = *places.w2(j);
         }
     }
     // the groups' sums side by side in shared memory, then added up in the order of the groups
