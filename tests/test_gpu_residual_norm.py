@@ -257,6 +257,22 @@ def test_more_values_than_32_bits_count(d):
     near(grads[3], f64(want), ULP * (64 + 4 * np.sqrt(rows)) * f64(size.sqrt()))
 
 
+@pytest.mark.parametrize("dt", [BF, F32])
+@pytest.mark.parametrize("rows,d", [(5, 33), (4, 777), (3001, 777), (700, 1411), (6, 16383)])
+def test_norms_without_weights_or_gate(rows, d, dt):
+    """No factor takes what lies beyond a row of odd width to zero: a mean is taken off nothing there."""
+    for post, pre in KINDS:
+        t = make(rows, d, dt, F32, post, pre, 0, rows + d)
+        t.update(post_w=None, post_b=None, pre_w=None, pre_b=None)
+        cfg = config(rows, d, dt, F32, post, pre, 0)
+        h, z, stats = forward(cfg, t)
+        check_forward(cfg, t, post, pre, h, z, stats)
+        check_backward(cfg, t, post, pre, h, stats, *backward(cfg, t, h, stats))
+        t["post_b"] = torch.ones(d, device="cuda") if post == "layer" else None
+        h, z, stats = forward(cfg, t)
+        check_forward(cfg, t, post, pre, h, z, stats)
+
+
 @pytest.mark.parametrize("groups", [0, 4])
 def test_no_weight_gradients_with_gates_of_groups(groups):
     rows, d = 37, 256

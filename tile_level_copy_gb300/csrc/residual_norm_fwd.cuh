@@ -22,6 +22,9 @@ __global__ void __launch_bounds__(THREADS, rf_ctas(THREADS)) rn_forward_kernel(R
     constexpr int NP = C::NP, UN = C::UN;
     constexpr int NEXT = MODE == RN_OWN ? NV * THREADS * (int)sizeof(T) : rn_cover<T>(NV, THREADS);  // from x to u, bytes
     constexpr int SLOT = 2 * NEXT;
+    // Pieces beyond the row are left out; of ragged rows, whose pieces are two values, they are zeros: a branch a piece kept
+    // the loads apart.
+    constexpr bool CUT = MODE == RN_OWN;
     __shared__ __align__(16) float red[2][THREADS / 32];
     extern __shared__ __align__(16) uint8_t rf_smem[];
     griddep_wait();
@@ -121,7 +124,7 @@ __global__ void __launch_bounds__(THREADS, rf_ctas(THREADS)) rn_forward_kernel(R
         const int64_t row = r * s.d + cols.c0;
         T* const rx = reinterpret_cast<T*>(here + (MODE == RN_RAGGED ? offset_of(x + r * s.d) : 0)) + (MODE == RN_RAGGED ? cols.c0 : 0);
         const T* const ru = reinterpret_cast<const T*>(here + NEXT + (MODE == RN_RAGGED ? offset_of(u + r * s.d) : 0)) + (MODE == RN_RAGGED ? cols.c0 : 0);
-        auto take = [&](int n, int q) {  // piece q of x (h) or u; pieces beyond the row are left out everywhere
+        auto take = [&](int n, int q) {  // piece q of x (h) or u
             if (MODE == RN_OWN) return *at(here, n, q);
             return cols.load(n ? ru : rx, q);
         };
@@ -131,7 +134,7 @@ __global__ void __launch_bounds__(THREADS, rf_ctas(THREADS)) rn_forward_kernel(R
             if (LAYER && s.post == MOE_NORM_LAYER) {
 #pragma unroll
                 for (int q = 0; q < NP; ++q) {
-                    if (q >= cols.np) break;
+                    if (CUT && q >= cols.np) break;
                     const P p = take(1, q);
 #pragma unroll
                     for (int i = 0; i < UN; ++i) sq[i & 1] = add_(sq[i & 1], unit_of(p, i));
@@ -143,7 +146,7 @@ __global__ void __launch_bounds__(THREADS, rf_ctas(THREADS)) rn_forward_kernel(R
             auto over = [&](auto centred) {
 #pragma unroll
                 for (int q = 0; q < NP; ++q) {
-                    if (q >= cols.np) break;
+                    if (CUT && q >= cols.np) break;
                     squares(take(1, q), decltype(centred)::value, neg, q, sq);
                 }
             };
@@ -157,7 +160,7 @@ __global__ void __launch_bounds__(THREADS, rf_ctas(THREADS)) rn_forward_kernel(R
         f2 sum[2] = {zero, zero};  // of h, or of its squares
 #pragma unroll
         for (int q = 0; q < NP; ++q) {
-            if (q >= cols.np) break;
+            if (CUT && q >= cols.np) break;
             P px = take(0, q);
             if (u) {
                 const P pu = take(1, q);
@@ -181,6 +184,11 @@ __global__ void __launch_bounds__(THREADS, rf_ctas(THREADS)) rn_forward_kernel(R
                 }
 #pragma unroll
                 for (int i = 0; i < UN; ++i) put_unit(px, i, fma_(v[i], branch, mul_(unit_of(px, i), res)));
+                if constexpr (LAYER && VEC == 1) {  // (the mean was taken off zeros beyond the row as well)
+#pragma unroll
+                    for (int i = 0; i < 2; ++i)
+                        if (!cols.inside(q, i)) put(px.v[i], 0.f);
+                }
             } else {
 #pragma unroll
                 for (int i = 0; i < UN; ++i) put_unit(px, i, mul_(unit_of(px, i), res));
@@ -203,7 +211,7 @@ __global__ void __launch_bounds__(THREADS, rf_ctas(THREADS)) rn_forward_kernel(R
                 const f2 neg = both<f2>(-mu);
 #pragma unroll
                 for (int q = 0; q < NP; ++q) {
-                    if (q >= cols.np) break;
+                    if (CUT && q >= cols.np) break;
                     squares(take(0, q), true, neg, q, sum);
                 }
             }
@@ -212,7 +220,7 @@ __global__ void __launch_bounds__(THREADS, rf_ctas(THREADS)) rn_forward_kernel(R
             const f2 a2 = both<f2>(rs), b2 = both<f2>(-mu * rs);
 #pragma unroll
             for (int q = 0; q < NP; ++q) {
-                if (q >= cols.np) break;
+                if (CUT && q >= cols.np) break;
                 P p = take(0, q);
                 f2 v[UN], k[UN];
 #pragma unroll
