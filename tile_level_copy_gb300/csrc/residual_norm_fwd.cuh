@@ -25,6 +25,7 @@ __global__ void __launch_bounds__(THREADS, rf_ctas(THREADS)) rn_forward_kernel(R
     // Pieces beyond the row are left out; of ragged rows, whose pieces are two values, they are zeros: a branch a piece kept
     // the loads apart.
     constexpr bool CUT = MODE == RN_OWN;
+    constexpr bool KEEP = MODE == RN_RAGGED;  // whether h stays in registers
     __shared__ __align__(16) float red[2][THREADS / 32];
     extern __shared__ __align__(16) uint8_t rf_smem[];
     griddep_wait();
@@ -158,6 +159,7 @@ __global__ void __launch_bounds__(THREADS, rf_ctas(THREADS)) rn_forward_kernel(R
         const f2 a = both<f2>(rs), b = both<f2>(-mu * rs), res = both<f2>(s.res), branch = both<f2>(s.branch);
         const int64_t gate_at = s.gate_rows ? (s.gate_rows >= s.rows ? 0 : r / s.gate_rows * s.d) : 0;
         f2 sum[2] = {zero, zero};  // of h, or of its squares
+        P kept[KEEP ? NP : 1];
 #pragma unroll
         for (int q = 0; q < NP; ++q) {
             if (CUT && q >= cols.np) break;
@@ -194,8 +196,8 @@ __global__ void __launch_bounds__(THREADS, rf_ctas(THREADS)) rn_forward_kernel(R
                 for (int i = 0; i < UN; ++i) put_unit(px, i, mul_(unit_of(px, i), res));
             }
             if (h) cols.store(h + row, q, px);
-            if (MODE == RN_OWN) *at(here, 0, q) = px;
-            else cols.store(rx, q, px);
+            if (KEEP) kept[KEEP ? q : 0] = px;
+            else *at(here, 0, q) = px;
             if (LAYER && s.pre == MOE_NORM_LAYER) {
 #pragma unroll
                 for (int i = 0; i < UN; ++i) sum[i & 1] = add_(sum[i & 1], unit_of(px, i));
@@ -212,7 +214,7 @@ __global__ void __launch_bounds__(THREADS, rf_ctas(THREADS)) rn_forward_kernel(R
 #pragma unroll
                 for (int q = 0; q < NP; ++q) {
                     if (CUT && q >= cols.np) break;
-                    squares(take(0, q), true, neg, q, sum);
+                    squares(KEEP ? kept[KEEP ? q : 0] : take(0, q), true, neg, q, sum);
                 }
             }
             rs = rsqrtf(fmaf(row_sum(add_(sum[0], sum[1])), s.inv_d, s.eps));
@@ -221,7 +223,7 @@ __global__ void __launch_bounds__(THREADS, rf_ctas(THREADS)) rn_forward_kernel(R
 #pragma unroll
             for (int q = 0; q < NP; ++q) {
                 if (CUT && q >= cols.np) break;
-                P p = take(0, q);
+                P p = KEEP ? kept[KEEP ? q : 0] : take(0, q);
                 f2 v[UN], k[UN];
 #pragma unroll
                 for (int i = 0; i < UN; ++i) v[i] = LAYER ? fma_(unit_of(p, i), a2, b2) : mul_(unit_of(p, i), a2);
