@@ -15,6 +15,23 @@ namespace {
 constexpr size_t RF_SMEM_MOST = 224 * 1024;
 __host__ __device__ constexpr int rf_ctas(int threads) { return threads > 256 ? 1 : 3; }
 
+// Weights are loaded as values that no store changes (no output may share memory with them): else a piece's loads would wait
+// for the stores of the piece before.
+// One value: `none` where it is not `there`, by a predicated load.
+__device__ __forceinline__ float weight(const float* p, bool there, float none) {
+    asm("{\n.reg .pred q;\nsetp.ne.u32 q, %2, 0;\n@q ld.global.nc.f32 %0, [%1];\n}" : "+f"(none) : "l"(p), "r"((uint32_t)there));
+    return none;
+}
+template <typename T>
+__device__ __forceinline__ float weight(const T* p, bool there, float none) {
+    static_assert(sizeof(T) == 2, "16-bit values");
+    T v;
+    put(v, none);  // (0 and 1 are values of every type)
+    uint16_t bits = *reinterpret_cast<const uint16_t*>(&v);
+    asm("{\n.reg .pred q;\nsetp.ne.u32 q, %2, 0;\n@q ld.global.nc.u16 %0, [%1];\n}" : "+h"(bits) : "l"(p), "r"((uint32_t)there));
+    return num(*reinterpret_cast<const T*>(&bits));
+}
+
 template <typename T, int VEC, int NV, int THREADS, bool WF32, bool LAYER, int MODE>
 __global__ void __launch_bounds__(THREADS, rf_ctas(THREADS)) rn_forward_kernel(RnShape s, RnWeights w, RnForward f) {
     typedef RnColumns<T, VEC, NV> C;
@@ -83,26 +100,33 @@ __global__ void __launch_bounds__(THREADS, rf_ctas(THREADS)) rn_forward_kernel(R
             sq[i & 1] = fma_(v, v, sq[i & 1]);
         }
     };
-    // vector p of the weights from the row's column on: unit i of piece q
-    auto coefficients = [&](const void* p, int64_t base, int q, f2 (&k)[UN]) {
+    // vector p of the weights from the row's column on: unit i of piece q; `none` where p is null, 0 beyond the row (where a
+    // layer norm takes its mean off as well). Predicated loads: a branch a vector and piece kept them apart.
+    auto coefficients = [&](const void* p, float none, int64_t base, int q, f2 (&k)[UN]) {
         base += cols.c0 + q * C::STEP;
         if constexpr (VEC == 1) {
             float a[2];
 #pragma unroll
-            for (int i = 0; i < 2; ++i) a[i] = cols.inside(q, i) ? value_at<T>(p, WF32, base + 32 * i, 0.f) : 0.f;
+            for (int i = 0; i < 2; ++i) {
+                const bool in = cols.inside(q, i);
+                if constexpr (WF32) a[i] = weight(static_cast<const float*>(p) + base + 32 * i, in && p, in ? none : 0.f);
+                else a[i] = weight(static_cast<const T*>(p) + base + 32 * i, in && p, in ? none : 0.f);
+            }
             k[0] = pair(a[0], a[1]);
         } else if constexpr (WF32) {
             const float4* const v = reinterpret_cast<const float4*>(static_cast<const float*>(p) + base);
 #pragma unroll
             for (int i = 0; i < VEC / 4; ++i) {
-                const float4 e = v[i];
+                const float4 e = p ? __ldg(v + i) : make_float4(none, none, none, none);
                 k[2 * i] = pair(e.x, e.y);
                 k[2 * i + 1] = pair(e.z, e.w);
             }
         } else {
-            const P e = *reinterpret_cast<const P*>(static_cast<const T*>(p) + base);
+            uint4 v = make_uint4(0, 0, 0, 0);
+            if (p) v = __ldg(reinterpret_cast<const uint4*>(static_cast<const T*>(p) + base));
+            const P e = *reinterpret_cast<const P*>(&v);
 #pragma unroll
-            for (int i = 0; i < UN; ++i) k[i] = unit_of(e, i);
+            for (int i = 0; i < UN; ++i) k[i] = p ? unit_of(e, i) : both<f2>(none);
         }
     };
 
@@ -160,51 +184,46 @@ __global__ void __launch_bounds__(THREADS, rf_ctas(THREADS)) rn_forward_kernel(R
         const int64_t gate_at = s.gate_rows ? (s.gate_rows >= s.rows ? 0 : r / s.gate_rows * s.d) : 0;
         f2 sum[2] = {zero, zero};  // of h, or of its squares
         P kept[KEEP ? NP : 1];
+        auto residual = [&](auto branched) {
 #pragma unroll
-        for (int q = 0; q < NP; ++q) {
-            if (CUT && q >= cols.np) break;
-            P px = take(0, q);
-            if (u) {
-                const P pu = take(1, q);
-                f2 v[UN], k[UN];
+            for (int q = 0; q < NP; ++q) {
+                if (CUT && q >= cols.np) break;
+                P px = take(0, q);
+                if (decltype(branched)::value) {
+                    const P pu = take(1, q);
+                    f2 v[UN], k[UN];
 #pragma unroll
-                for (int i = 0; i < UN; ++i) v[i] = LAYER ? fma_(unit_of(pu, i), a, b) : mul_(unit_of(pu, i), a);
-                if (w.post_w) {
-                    coefficients(w.post_w, 0, q, k);
-#pragma unroll
-                    for (int i = 0; i < UN; ++i) v[i] = mul_(v[i], k[i]);
-                }
-                if (LAYER && w.post_b) {
-                    coefficients(w.post_b, 0, q, k);
-#pragma unroll
-                    for (int i = 0; i < UN; ++i) v[i] = add_(v[i], k[i]);
-                }
-                if (s.gate_rows) {
-                    coefficients(w.gate, gate_at, q, k);
+                    for (int i = 0; i < UN; ++i) v[i] = LAYER ? fma_(unit_of(pu, i), a, b) : mul_(unit_of(pu, i), a);
+                    coefficients(w.post_w, 1.f, 0, q, k);
 #pragma unroll
                     for (int i = 0; i < UN; ++i) v[i] = mul_(v[i], k[i]);
+                    if (LAYER) {
+                        coefficients(w.post_b, 0.f, 0, q, k);
+#pragma unroll
+                        for (int i = 0; i < UN; ++i) v[i] = add_(v[i], k[i]);
+                    }
+                    coefficients(w.gate, 1.f, gate_at, q, k);
+#pragma unroll
+                    for (int i = 0; i < UN; ++i) v[i] = mul_(v[i], k[i]);
+#pragma unroll
+                    for (int i = 0; i < UN; ++i) put_unit(px, i, fma_(v[i], branch, mul_(unit_of(px, i), res)));
+                } else {
+#pragma unroll
+                    for (int i = 0; i < UN; ++i) put_unit(px, i, mul_(unit_of(px, i), res));
                 }
+                if (h) cols.store(h + row, q, px);
+                if (KEEP) kept[KEEP ? q : 0] = px;
+                else *at(here, 0, q) = px;
+                if (LAYER && s.pre == MOE_NORM_LAYER) {
 #pragma unroll
-                for (int i = 0; i < UN; ++i) put_unit(px, i, fma_(v[i], branch, mul_(unit_of(px, i), res)));
-                if constexpr (LAYER && VEC == 1) {  // (the mean was taken off zeros beyond the row as well)
-#pragma unroll
-                    for (int i = 0; i < 2; ++i)
-                        if (!cols.inside(q, i)) put(px.v[i], 0.f);
+                    for (int i = 0; i < UN; ++i) sum[i & 1] = add_(sum[i & 1], unit_of(px, i));
+                } else {
+                    squares(px, false, zero, q, sum);
                 }
-            } else {
-#pragma unroll
-                for (int i = 0; i < UN; ++i) put_unit(px, i, mul_(unit_of(px, i), res));
             }
-            if (h) cols.store(h + row, q, px);
-            if (KEEP) kept[KEEP ? q : 0] = px;
-            else *at(here, 0, q) = px;
-            if (LAYER && s.pre == MOE_NORM_LAYER) {
-#pragma unroll
-                for (int i = 0; i < UN; ++i) sum[i & 1] = add_(sum[i & 1], unit_of(px, i));
-            } else {
-                squares(px, false, zero, q, sum);
-            }
-        }
+        };
+        if (u) residual(std::true_type());
+        else residual(std::false_type());
         if (s.pre) {
             mu = 0.f;
             if (LAYER && s.pre == MOE_NORM_LAYER) {
@@ -227,13 +246,11 @@ __global__ void __launch_bounds__(THREADS, rf_ctas(THREADS)) rn_forward_kernel(R
                 f2 v[UN], k[UN];
 #pragma unroll
                 for (int i = 0; i < UN; ++i) v[i] = LAYER ? fma_(unit_of(p, i), a2, b2) : mul_(unit_of(p, i), a2);
-                if (w.pre_w) {
-                    coefficients(w.pre_w, 0, q, k);
+                coefficients(w.pre_w, 1.f, 0, q, k);
 #pragma unroll
-                    for (int i = 0; i < UN; ++i) v[i] = mul_(v[i], k[i]);
-                }
-                if (LAYER && w.pre_b) {
-                    coefficients(w.pre_b, 0, q, k);
+                for (int i = 0; i < UN; ++i) v[i] = mul_(v[i], k[i]);
+                if (LAYER) {
+                    coefficients(w.pre_b, 0.f, 0, q, k);
 #pragma unroll
                     for (int i = 0; i < UN; ++i) v[i] = add_(v[i], k[i]);
                 }
