@@ -272,7 +272,10 @@ cudaError_t launch_residual_forward(RnShape s, const RnWeights& w, const RnForwa
     // times as many warps, and is done sooner)
     constexpr int MANY = 64 / (int)sizeof(T), FEW = 16 / (int)sizeof(T);
     const bool few = s.rows * rn_warps(s.d, MANY) < 16 * sms && rn_warps(s.d, FEW) <= 32;
-    s.warps = rn_warps(s.d, few ? FEW : MANY);
+    // ragged rows of half a warp's values or less: all places of a thread cost their instructions there
+    // (40001 x 301 bf16: 63 us instead of 87)
+    const bool ragged = vec == 1 || !w.whole, small = few || (ragged && s.d <= 16 * MANY);
+    s.warps = rn_warps(s.d, small ? FEW : MANY);
     s.groups = s.warps < 8 && !few ? 8 / s.warps : 1;
     const int threads = 32 * s.warps * s.groups;
     const int64_t n = (s.rows + s.groups - 1) / s.groups;
@@ -290,7 +293,7 @@ cudaError_t launch_residual_forward(RnShape s, const RnWeights& w, const RnForwa
         return launch_k(kernel, dim3((unsigned)(n < ctas ? n : ctas)), dim3(threads), s.slots * slot, st, true, s, w, f);
     };
     auto shaped = [&](auto width, auto wide, auto layer, auto how) {
-        if (few) return threads <= 256 ? go(width, Int<FEW>(), Int<256>(), wide, layer, how) : go(width, Int<FEW>(), Int<1024>(), wide, layer, how);
+        if (small) return threads <= 256 ? go(width, Int<FEW>(), Int<256>(), wide, layer, how) : go(width, Int<FEW>(), Int<1024>(), wide, layer, how);
         return threads <= 256 ? go(width, Int<MANY>(), Int<256>(), wide, layer, how) : go(width, Int<MANY>(), Int<1024>(), wide, layer, how);
     };
     auto kinds = [&](auto width, auto wide, auto how) {
@@ -301,7 +304,7 @@ cudaError_t launch_residual_forward(RnShape s, const RnWeights& w, const RnForwa
         if constexpr (sizeof(T) == 4) return kinds(width, std::true_type(), how);
         else return w.f32 ? kinds(width, std::true_type(), how) : kinds(width, std::false_type(), how);
     };
-    return vec == 1 || !w.whole ? typed(Int<1>(), Int<RN_RAGGED>()) : typed(Int<16 / sizeof(T)>(), Int<RN_OWN>());
+    return ragged ? typed(Int<1>(), Int<RN_RAGGED>()) : typed(Int<16 / sizeof(T)>(), Int<RN_OWN>());
 }
 
 }  // namespace moe
