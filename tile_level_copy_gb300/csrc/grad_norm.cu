@@ -7,7 +7,7 @@
 // floats (sum and what its rounding cut off), so the length of the list costs no precision. The CTAs' sums are added
 // up in 64 bits by the CTA that finishes last, in the order of the CTAs: the result repeats bit for bit.
 // Squares that leave fp32's range are taken again in 64 bits, so a norm that fp32 can hold is found whatever the
-// values' size. 24 tensors, 149 million bf16 values: norm 47 us, 6.3 TB/s (93 % of a copy's rate); 64 bytes a thread in
+// values' size. 24 tensors, 149 million bf16 values: norm 47 us, 6.3 TB/s (92 % of a copy's rate); 64 bytes a thread in
 // flight: 52 us. 67 tensors, 1 million values: 6.5 us, one launch and the call on the host.
 #include <math.h>
 
