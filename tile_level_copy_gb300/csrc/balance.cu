@@ -132,11 +132,13 @@ __device__ __forceinline__ float exp2_of(float v) {  // (below 2^-126: zero)
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
     return r;
 }
-// x becomes exp(x - m). By one product and sum: what m's product with log2(e) is rounded by is a factor of the whole row,
-// which its sum takes out again. Where that product would leave fp32's range the difference is taken first.
+// x becomes exp(x - m). By one product and sum: what m's product with log2(e) is rounded by (2^-14 at most up to BL_FAR) is
+// a factor of the whole row, which its sum takes out again, and which leaves a row's largest value within 2^-14 of 1. In
+// rows beyond (from 2^31 on that factor itself could leave fp32's range) the difference is taken first.
+constexpr float BL_FAR = 1024.f;
 template <int N2>
 __device__ __forceinline__ void exponentials(f2 (&x)[N2], float m) {
-    const bool far = fabsf(m) > 0x1p126f;
+    const bool far = fabsf(m) > BL_FAR;
     const f2 l = both<f2>(BL_LOG2E), c = both<f2>(far ? 0.f : -m * BL_LOG2E);
     if (far) {
 #pragma unroll
