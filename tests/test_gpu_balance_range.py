@@ -1,4 +1,4 @@
-"""Balance loss at logits of every size that fp32 holds on the GPU against the 64-bit oracle.
+"""Balance loss at logits of every size that fp32 holds, and log-sum-exps next to zero, on the GPU against the 64-bit oracle.
 
 Tolerances, with u = 2^-24. Rows whose largest logit m is at most 1024 in magnitude have exponents (l - m) log2(e) off by one
 rounding of them and one of the constant, and by what the row's m log2(e) is rounded by, which p does not see; beyond, l - m
@@ -75,3 +75,22 @@ def test_a_batch_of_masked_rows_alone():
         assert (lse.double() - v).abs().max() <= np.log(E) + 2 * U * abs(v)
         a = counts.double() * E / (k * T ** 2)
         assert (dl.double() - (a - a.mean()) / E).abs().max() <= 128 * U * 2 * a.max() / E
+
+
+@pytest.mark.parametrize("E", [2, 3, 64, 256])
+def test_log_sum_exps_next_to_zero(E):
+    """Largest logit 0, the others x below: lse = log(1 + q), q = sum of exp(-x). exp is off by (1.5 x + 4) u of itself (its
+    argument by two roundings, of the constant and of the product, at most 1.5 x u together), the sum 1 + q by u for each of its
+    n <= 13 additions, the logarithm by one unit in its last place, 2 u: u ((1.5 x + 4) q / (1 + q) + n + 2 lse) in all."""
+    T, g = 4096, torch.Generator().manual_seed(E)
+    x = 16 * torch.rand(T, 1, generator=g)
+    logits = (-x).expand(T, E).clone()
+    at = torch.randint(0, E, (T,), generator=g)
+    logits[torch.arange(T), at] = 0
+    t = {"logits": logits.cuda(), "idx": at[:, None].to(torch.int32).cuda(), "offsets": None, "mask": None, "dloss": None}
+    got = f64(run(tlc.BalanceConfig(T, E, 1, balance=0.0, z=1.0), t, gates=False)[2])
+    x = f64(x)[:, 0]
+    q = (E - 1) * np.exp(-x)
+    want = np.log1p(q)
+    err = U * ((1.5 * x + 4) * q / (1 + q) + min(E - 1, 13) + 2 * want)
+    assert (np.abs(got - want) <= err).all(), (np.abs(got - want) / err).max()

@@ -250,8 +250,11 @@ __global__ void __launch_bounds__(BL_THREADS, 1)
             const float m = largest<LPT>(x);
             exponentials(x, m);
             const float sum = group_sum<LPT>(sum_of(x));
-            const float lse = m + __logf(sum);  // (off by 2^-21 at most: sums are at least 1)
-            const float inv = sum == 0.f ? 0.f : __fdividef(1.0f, sum);
+            // A logarithm and a division of full precision, once a token: an lse next to zero is the logarithm of a sum next to
+            // 1 (or, in the backward pass, of its inverse), where __logf is off by 2^-21 and __fdividef's inverse by 2^-22.
+            // (131072 tokens of 256 experts, both passes: 90.5 us; 89.1 with these two.)
+            const float lse = m + logf(sum);
+            const float inv = sum == 0.f ? 0.f : 1.0f / sum;
             if (there && lig == 0) {
                 if (lse_out) lse_out[t] = lse;
                 if (kept) kept[t] = make_float2(m, inv);
@@ -565,7 +568,7 @@ __global__ void __launch_bounds__(BL_BACK_THREADS, BL_BACK_CTAS)
         group_sums<LPT>(dot, gd, lane);
         live = live && seq_live && inv != 0.f;
         // p (a - sum p a + z's part): exp(l - m) times inv (a + c)
-        const float c = wz * (m - __logf(inv)) - dot * inv;
+        const float c = wz * (m - logf(inv)) - dot * inv;
         const f2 vi = both<f2>(inv), vc = both<f2>(c * inv);
 #pragma unroll
         for (int i = 0; i < N2; ++i) x[i] = mul_(x[i], fma_(a[i], vi, vc));
