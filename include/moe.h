@@ -573,13 +573,14 @@ MOE_API int moe_adamw_read_state(const moe_adamw_tensor* tensors, int32_t count,
  * Global norm of a list of gradients and the factor that clips it:
  *   out[0] = norm = sqrt(sum over all tensors of g^2), out[1] = scale = min(1, max_norm / (norm + eps)).
  * The squares' sum is held beyond fp32 in precision and range. A gradient that is infinite or NaN makes the norm so;
- * scale is then 0 or NaN, as the formula gives it. An empty list has norm 0. out + 1 may be handed to
+ * scale is then 0 or NaN. An infinite max_norm never clips (scale 1 unless the norm is NaN), nor does a norm + eps of 0:
+ * there is nothing to scale. An empty list has norm 0. out + 1 may be handed to
  * moe_adamw_step as grad_scale and to moe_grad_clip. The order of the sums depends on the list, the pointers'
  * alignment and the device alone, so results repeat bit for bit.
  */
 #define MOE_GRAD_NORM_WORKSPACE_BYTES 32768
 typedef struct moe_grad_norm_config {
-    double max_norm; /* >= 0; infinite: never clipped */
+    double max_norm; /* >= 0; infinite: never clipped, whatever the norm but NaN */
     double eps;      /* >= 0 */
     int32_t reserved[4];
 } moe_grad_norm_config;

@@ -1,0 +1,39 @@
+"""Gradient norm and clipping where the formula ends: limits of zero and infinity."""
+import pytest
+import torch
+
+import tile_level_copy_gb300 as tlc
+from tests.test_gpu_grad_norm import run
+
+pytestmark = pytest.mark.gpu
+F32, BF, F16 = torch.float32, torch.bfloat16, torch.float16
+INF, NAN = float("inf"), float("nan")
+
+
+@pytest.mark.parametrize("dt", [F32, BF, F16])
+def test_an_infinite_limit_never_clips(dt):
+    g = [torch.ones(1000, dtype=dt, device="cuda"), torch.ones(33, device="cuda")]
+    g[0][123] = INF
+    out, lst = run(g, INF)
+    assert out.tolist() == [INF, 1.0]
+    before = [t.clone() for t in g]
+    tlc.grad_clip(lst, out[1:])
+    assert all(torch.equal(a, b) for a, b in zip(g, before))
+    out, _ = run(g, 1.0)
+    assert out.tolist() == [INF, 0.0]
+    g[1][5] = NAN
+    assert torch.isnan(run(g, INF)[0]).all() and torch.isnan(run(g, 1.0)[0]).all()
+
+
+@pytest.mark.parametrize("max_norm", [0.0, 1.0, INF])
+def test_nothing_to_clip_without_eps(max_norm):
+    """Norm and eps 0: there is nothing to scale, and the factor leaves it so."""
+    z = [torch.zeros(5000, device="cuda"), torch.zeros(3, dtype=BF, device="cuda")]
+    for gs in (z, [], [z[0][:0]]):
+        out, lst = run(gs, max_norm, eps=0.0)
+        assert out.tolist() == [0.0, 1.0]
+        tlc.grad_clip(lst, out[1:])
+    assert not any(t.any() for t in z)
+    z[0][7] = 2.0
+    out, lst = run(z, 0.0, eps=0.0)
+    assert out.tolist() == [2.0, 0.0]
