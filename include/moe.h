@@ -598,8 +598,8 @@ typedef struct moe_grad_tensor {
 MOE_API int moe_grad_norm(const moe_grad_norm_config* cfg, const moe_grad_tensor* tensors, int32_t count, float* out,
                           void* ws, size_t ws_bytes, void* stream);
 
-/* g = g * scale in place for every tensor of the list, in fp32, rounded once; scale: device fp32 scalar (1 leaves every
- * value as it is). Tensors must not overlap; a scale inside of one is refused. */
+/* g = g * scale in place for every tensor of the list, in fp32, rounded once; scale: device fp32 scalar. With scale 1
+ * nothing is read or written. Tensors must not overlap; a scale inside of one is refused. */
 MOE_API int moe_grad_clip(const moe_grad_tensor* tensors, int32_t count, const float* scale, void* stream);
 
 /*

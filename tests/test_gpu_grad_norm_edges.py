@@ -1,4 +1,4 @@
-"""Gradient norm and clipping where the formula ends: limits of zero and infinity."""
+"""Gradient norm and clipping where the formula ends: limits of zero and infinity, a factor of 1."""
 import pytest
 import torch
 
@@ -37,3 +37,18 @@ def test_nothing_to_clip_without_eps(max_norm):
     z[0][7] = 2.0
     out, lst = run(z, 0.0, eps=0.0)
     assert out.tolist() == [2.0, 0.0]
+
+
+@pytest.mark.parametrize("dt", [F32, BF, F16])
+@pytest.mark.parametrize("shift", [0, 1])
+def test_a_factor_of_one_writes_nothing(dt, shift):
+    """Every bit stays, those of a NaN among them (arithmetic would leave its own NaN)."""
+    bits = torch.int32 if dt == F32 else torch.int16
+    g = torch.randn(40001 + shift, device="cuda").to(dt)[shift:]
+    quiet = torch.full((1,), NAN, dtype=dt).view(bits).item()
+    g.view(bits)[::1000] = quiet | 0x5
+    want, lst = g.view(bits).clone(), tlc.GradList([g])
+    tlc.grad_clip(lst, torch.ones(1, device="cuda"))
+    assert torch.equal(g.view(bits), want)
+    tlc.grad_clip(lst, torch.full((1,), 0.5, device="cuda"))
+    assert not torch.equal(g.view(bits), want)

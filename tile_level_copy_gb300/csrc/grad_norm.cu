@@ -279,6 +279,7 @@ __global__ void __launch_bounds__(GN_THREADS, GN_CTAS)
     griddep_wait();
     griddep_launch();
     const float s = *scale;
+    if (s == 1.0f) return;  // the usual step of a settled run: every bit stays, a NaN's too, and nothing is read or written
     const uint64_t policy = l2_policy(l.first[l.count]);
     for (int c = l.first[l.count] - 1 - (int)blockIdx.x; c >= 0; c -= gridDim.x) {
         const int i = tensor_of(l, c);
