@@ -233,11 +233,10 @@ __global__ void __launch_bounds__(GN_THREADS, GN_CTAS)
     ws->total = a;
     ws->ticket = 0;
     if (!end.last) return;
-    const double norm = sqrt(a), under = norm + end.eps;
-    // (without a limit, or without anything to scale, 1 and not infinity / infinity or 0 / 0)
-    const double f = (isinf(end.max_norm) && !isnan(norm)) || under == 0.0 ? 1.0 : end.max_norm / under;
+    const double norm = sqrt(a), f = end.max_norm / (norm + end.eps);
     end.out[0] = (float)norm;
-    end.out[1] = f >= 1.0 ? 1.0f : (float)f;  // NaN stays NaN
+    // 1 also for infinity / infinity (no limit) and 0 / 0 (nothing to scale); a norm that is NaN makes the factor so
+    end.out[1] = f < 1.0 || norm != norm ? (float)f : 1.0f;
 }
 
 template <typename T>
