@@ -1,9 +1,9 @@
-"""Gradient norm and clipping where the formula ends: limits of zero and infinity, a factor of 1."""
+"""Gradient norm and clipping where the formula ends: limits of zero and infinity, a factor of 1, sums that round one way."""
 import pytest
 import torch
 
 import tile_level_copy_gb300 as tlc
-from tests.test_gpu_grad_norm import run
+from tests.test_gpu_grad_norm import REL, run
 
 pytestmark = pytest.mark.gpu
 F32, BF, F16 = torch.float32, torch.bfloat16, torch.float16
@@ -52,3 +52,19 @@ def test_a_factor_of_one_writes_nothing(dt, shift):
     assert torch.equal(g.view(bits), want)
     tlc.grad_clip(lst, torch.full((1,), 0.5, device="cuda"))
     assert not torch.equal(g.view(bits), want)
+
+
+@pytest.mark.parametrize("dt", [BF, F16])
+@pytest.mark.parametrize("first", [1, 2, 4, 8])
+def test_sums_that_round_one_way(dt, first):
+    """Squares that are each just too small to change a sum that began with 1: what a chain of n additions loses is (n - 1)
+    times 2^-24 of it. With the 64 squares of a thread's 128 bytes added in chains of 8 on each of 8 sums, 3 steps to add
+    these up and one more rounding of each, the sum is off by at most 11 * 2^-24, the norm by half of that and its
+    own rounding: 6.5 * 2^-24 < REL, whichever value of a piece is large."""
+    n = 16384 * 5
+    g = torch.full((n,), 2.0 ** -12 * (1 - 2.0 ** -7), dtype=dt, device="cuda").view(-1, 8)
+    g.view(5, 8, 256, 8)[:, 0, :, :first] = 1.0           # the first piece of every thread
+    g = g.view(-1)
+    out, _ = run([g])
+    norm = g.double().square().sum().sqrt().item()
+    assert abs(out[0].item() / norm - 1) <= REL

@@ -112,15 +112,19 @@ __device__ __noinline__ double wide_squares(const Pack<T, 16 / sizeof(T)>* p, in
 template <typename T, int N, typename Sum>
 __device__ __forceinline__ void add_squares(const Pack<T, 16 / sizeof(T)> (&p)[N], const Pack<T, 16 / sizeof(T)>* from, int n, Sum&& sum) {
     constexpr int VEC = 16 / sizeof(T);
-    f2 acc[2] = {pair(0.f, 0.f), pair(0.f, 0.f)};
+    f2 acc[VEC / 2];  // one for each pair of a piece: chains of N additions, whatever the type
+#pragma unroll
+    for (int i = 0; i < VEC / 2; ++i) acc[i] = both<f2>(0.f);
 #pragma unroll
     for (int k = 0; k < N; ++k) {
         f2 f[VEC / 2];
         widen(p[k], f);
 #pragma unroll
-        for (int i = 0; i < VEC / 2; ++i) acc[i & 1] = fma_(f[i], f[i], acc[i & 1]);
+        for (int i = 0; i < VEC / 2; ++i) acc[i] = fma_(f[i], f[i], acc[i]);
     }
-    const float s = total(add_(acc[0], acc[1]));
+    f2 sums = add_(acc[0], acc[1]);
+    if constexpr (VEC == 8) sums = add_(sums, add_(acc[2], acc[3]));
+    const float s = total(sums);
     if (s >= 0x1p-110f && s <= 0x1p100f) {
         sum.add(s);
         return;
