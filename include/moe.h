@@ -628,7 +628,8 @@ typedef struct moe_residual_norm_config {
 
 /* post_w, pre_w: NULL for 1; post_b, pre_b: NULL for 0 (NULL with MOE_NORM_RMS). post_stats, pre_stats: fp32 [rows, 2],
  * mean (0 for MOE_NORM_RMS) and 1 / sqrt(...) of each row for the backward pass, or NULL. h may be x or u, or NULL when
- * it is not wanted; z is NULL exactly with pre = MOE_NORM_NONE and may be u, or x when that is not h. No other sharing. */
+ * it is not wanted; z is NULL exactly with pre = MOE_NORM_NONE and may be u, or x when that is not h. Any other
+ * overlap of an output with an input or another output is refused. */
 MOE_API int moe_residual_norm_forward(const moe_residual_norm_config* cfg, const void* x, const void* u,
                                       const void* post_w, const void* post_b, const void* gate, const void* pre_w,
                                       const void* pre_b, void* h, void* z, float* post_stats, float* pre_stats,
@@ -642,8 +643,8 @@ MOE_API int moe_residual_norm_workspace_size(const moe_residual_norm_config* cfg
  * pre = MOE_NORM_NONE, dh may be NULL (0) otherwise. u: as in the forward pass, needed with a post norm or a gate; h: with a pre norm.
  *   dx = residual_scale * (dh + pre' dz), du = post' (branch_scale * gate * (the same)); du NULL: not wanted
  *   dpost_w, dpost_b, dgate, dpre_w, dpre_b: summed over the rows (dgate over the rows of each gate), each NULL when
- *   not wanted; ws may be NULL when all are. dx and du may each be one of dz, dh, u and h (not the same one); no other
- *   sharing.
+ *   not wanted; ws may be NULL when all are. dx and du may each be one of dz, dh, u and h (not the same one). Any other
+ *   overlap of an output or the workspace with an input or an output is refused.
  * The order of the sums depends on the config, the pointers' alignment and the device alone. With rows = 0 the
  * weights' gradients are set to zero.
  */

@@ -4,6 +4,8 @@
 
 #include <math.h>
 
+#include <initializer_list>
+
 namespace moe {
 namespace {
 
@@ -156,12 +158,31 @@ int check(const moe_residual_norm_config* c) {
 
 // Whether rows of outputs lie over one another or over rows that they may not: an output may be an input that its
 // elements replace one by one (the same pointer), and nothing else of it.
-bool apart(const void* a, const void* b, size_t bytes) {
-    if (!a || !b) return true;
-    const uintptr_t p = reinterpret_cast<uintptr_t>(a), q = reinterpret_cast<uintptr_t>(b);
-    return p >= q + bytes || q >= p + bytes;
+struct Span {
+    const void* p;
+    size_t bytes;
+};
+bool apart(const Span& a, const Span& b) {
+    if (!a.p || !b.p) return true;
+    const uintptr_t p = reinterpret_cast<uintptr_t>(a.p), q = reinterpret_cast<uintptr_t>(b.p);
+    return p >= q + b.bytes || q >= p + a.bytes;
 }
-bool apart_or_same(const void* a, const void* b, size_t bytes) { return a == b || apart(a, b, bytes); }
+bool apart_or_same(const void* a, const void* b, size_t bytes) { return a == b || apart({a, bytes}, {b, bytes}); }
+// Every output lies apart from these inputs and from the outputs behind it in the list. (Weights, gates and statistics are read
+// while other rows' outputs are written, in the forward pass by loads that no store may change.)
+int check_apart(std::initializer_list<Span> outs, std::initializer_list<Span> ins) {
+    for (const Span* o = outs.begin(); o != outs.end(); ++o) {
+        if (!o->p) continue;
+        for (const Span* i = o + 1; i != outs.end(); ++i)
+            if (!apart(*o, *i)) return fail(MOE_ERR_ARG, "two outputs share memory");
+        for (const Span& i : ins)
+            if (!apart(*o, i)) return fail(MOE_ERR_ARG, "an output shares memory with a weight, a gate, statistics or the workspace");
+    }
+    return MOE_OK;
+}
+size_t gate_bytes(const moe_residual_norm_config& c) {
+    return c.gate_rows > 0 ? (size_t)((c.rows - 1) / c.gate_rows + 1) * c.d * dtype_size(c.wdtype) : 0;
+}
 
 // 16-byte pieces where they divide the rows and every row's pieces are aligned, else single values.
 template <typename... Ptr>
@@ -249,9 +270,14 @@ MOE_API int moe_residual_norm_forward(const moe_residual_norm_config* c, const v
     const size_t e = dtype_size(c->dtype), bytes = (size_t)c->rows * c->d * e;
     if (!aligned(x, e) || !aligned(u, e) || !aligned(h, e) || !aligned(z, e) || !aligned(post_stats, 8) || !aligned(pre_stats, 8))
         return fail(MOE_ERR_ARG, "a pointer is not aligned (the statistics to 8 bytes, the others to their type)");
-    if (!apart_or_same(h, x, bytes) || !apart_or_same(h, u, bytes) || !apart_or_same(z, x, bytes) ||
-        !apart_or_same(z, u, bytes) || !apart(h, z, bytes))
-        return fail(MOE_ERR_ARG, "an output shares memory with another, or with part of an input");
+    if (!apart_or_same(h, x, bytes) || !apart_or_same(h, u, bytes) || !apart_or_same(z, x, bytes) || !apart_or_same(z, u, bytes))
+        return fail(MOE_ERR_ARG, "an output shares memory with part of an input");
+    const size_t vec_bytes = dtype_size(c->wdtype) * c->d, stat_bytes = 8 * (size_t)c->rows;
+    const Span ps{c->post ? post_stats : nullptr, stat_bytes}, qs{c->pre ? pre_stats : nullptr, stat_bytes};
+    if ((rc = check_apart({{h, bytes}, {z, bytes}, ps, qs}, {{post_w, vec_bytes}, {post_b, vec_bytes}, {gate, gate_bytes(*c)},
+                                                           {pre_w, vec_bytes}, {pre_b, vec_bytes}})))
+        return rc;
+    if ((rc = check_apart({ps, qs}, {{x, bytes}, {u, bytes}}))) return rc;
     DeviceInfo di;
     if ((rc = check_device(&di))) return rc;
     const int vec = vector_width(*c, x, u, h, z);
@@ -315,7 +341,13 @@ MOE_API int moe_residual_norm_backward(const moe_residual_norm_config* c, const 
     for (const void* in : {dz, dh, u, h})
         if (!apart_or_same(dx, in, bytes) || !apart_or_same(du, in, bytes))
             return fail(MOE_ERR_ARG, "dx or du shares memory with part of an input");
-    if (!apart(dx, du, bytes)) return fail(MOE_ERR_ARG, "dx and du share memory");
+    const size_t vec_bytes = we * c->d, stat_bytes = 8 * (size_t)c->rows;
+    const Span dw[5] = {{dpost_w, vec_bytes}, {dpost_b, vec_bytes}, {dgate, gate_bytes(*c)}, {dpre_w, vec_bytes}, {dpre_b, vec_bytes}};
+    const Span post_wt{post_w, vec_bytes}, post_bt{post_b, vec_bytes}, gt{gate, gate_bytes(*c)}, pre_wt{pre_w, vec_bytes};
+    const Span ps{c->post ? post_stats : nullptr, stat_bytes}, qs{c->pre ? pre_stats : nullptr, stat_bytes};
+    if ((rc = check_apart({{dx, bytes}, {du, bytes}, dw[0], dw[1], dw[2], dw[3], dw[4]}, {post_wt, post_bt, gt, pre_wt, ps, qs}))) return rc;
+    const Span rows_in[4] = {{dz, bytes}, {dh, bytes}, {uses_u ? u : nullptr, bytes}, {c->pre ? h : nullptr, bytes}};
+    if ((rc = check_apart({dw[0], dw[1], dw[2], dw[3], dw[4]}, {rows_in[0], rows_in[1], rows_in[2], rows_in[3]}))) return rc;
     if ((rc = check_device(&di))) return rc;
     const int vec = vector_width(*c, dz, dh, uses_u ? u : nullptr, c->pre ? h : nullptr, dx, du);
     int ctas;
@@ -327,6 +359,9 @@ MOE_API int moe_residual_norm_backward(const moe_residual_norm_config* c, const 
         if (!ws) return fail(MOE_ERR_ARG, "workspace is NULL");
         if (!aligned(ws, 16)) return fail(MOE_ERR_ARG, "workspace must be 16-byte aligned");
         if (ws_bytes < need) return fail(MOE_ERR_WORKSPACE, "workspace has %zu bytes, needs %zu", ws_bytes, need);
+        if ((rc = check_apart({{ws, need}}, {{dx, bytes}, {du, bytes}, dw[0], dw[1], dw[2], dw[3], dw[4], post_wt, post_bt, gt, pre_wt, ps, qs,
+                                             rows_in[0], rows_in[1], rows_in[2], rows_in[3]})))
+            return rc;
         part = static_cast<float*>(ws);
         gpart = part + p / 4;
         gsum = gpart + gp / 4;
