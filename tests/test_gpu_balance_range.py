@@ -3,7 +3,7 @@
 Tolerances, with u = 2^-24. Rows whose largest logit m is at most 1024 in magnitude have exponents (l - m) log2(e) off by one
 rounding of them and one of the constant, and by what the row's m log2(e) is rounded by, which p does not see; beyond, l - m
 is rounded once and its product once: with d = |l - m|, exp is off by less than 3 d u of itself. exp2 adds 4 u (2 units in the
-last place), a sum of E <= 256 terms 13 u (a chain of 8 pairs and 5 steps), the inverse and the product u each: p is off by
+last place), a sum of E <= 256 terms 13 u (a chain of 8 pairs and 5 steps), the inverse 4 u (as exp2), the product u: p is off by
 (3 d + 24) u of itself. sum p a is off by the mean of that, with sum p d <= log 256, and by its own chain, 54 u in all; lse by
 the rounding of m log2(e) and its own, 16 u; a and the last products by 10 u: a gradient's terms by (3 d + 104) u. Losses
 are sums of positive terms: relative error 2e-5 allows 300 roundings of each.
@@ -93,4 +93,19 @@ def test_log_sum_exps_next_to_zero(E):
     q = (E - 1) * np.exp(-x)
     want = np.log1p(q)
     err = U * ((1.5 * x + 4) * q / (1 + q) + min(E - 1, 13) + 2 * want)
+    assert (np.abs(got - want) <= err).all(), (np.abs(got - want) / err).max()
+
+
+def test_the_z_loss_gradient_next_to_zero():
+    """2 lse p / T, with lse as above and p off by (1.5 x + 10) u of itself: two experts, so one addition in the sum."""
+    T, g = 4096, torch.Generator().manual_seed(1)
+    x = 16 * torch.rand(T, 1, generator=g)
+    logits = torch.cat([torch.zeros(T, 1), -x], 1).cuda()
+    t = {"logits": logits, "idx": torch.zeros(T, 1, dtype=torch.int32, device="cuda"), "offsets": None, "mask": None, "dloss": None}
+    got = f64(run(tlc.BalanceConfig(T, 2, 1, balance=0.0, z=1.0), t, gates=False)[3])
+    x = f64(x)
+    q = np.exp(-x)
+    lse, p = np.log1p(q), np.concatenate([1 / (1 + q), q / (1 + q)], 1)
+    err = U * p * ((1.5 * x + 4) * q / (1 + q) + 1 + 2 * lse + (1.5 * x + 12) * lse) * 2 / T
+    want = 2 * lse * p / T
     assert (np.abs(got - want) <= err).all(), (np.abs(got - want) / err).max()

@@ -183,9 +183,23 @@ struct BlSpace {
     float* part;
 };
 
+// What balance_backward reads: w_b / S', 2 w_z / N, a [S, E] without the 1 / S'.
+constexpr int BL_SAVED_HEAD = 4;  // floats
+// Behind them, of each token the largest logit and 1 / sum of exp(l - that) (0 for a token without probabilities), then lse (from
+// the inverse it would carry that one's rounding as well, which is much of an lse next to zero, and cost a logarithm).
+struct BlKept {
+    float2* row;  // or null: nothing is kept
+    float* lse;
+};
+__host__ __device__ __forceinline__ size_t kept_at(int S, int E) { return (BL_SAVED_HEAD + (size_t)S * E + 1) / 2 * 2; }  // floats
+__host__ __device__ __forceinline__ BlKept kept_of(float* saved, int S, int E, int T) {
+    float2* const row = saved ? reinterpret_cast<float2*>(saved + kept_at(S, E)) : nullptr;
+    return BlKept{row, row ? reinterpret_cast<float*>(row + T) : nullptr};
+}
+
 template <int LPT, int NV, bool VEC>
 __global__ void __launch_bounds__(BL_THREADS, 1)
-    balance_kernel(BlShape s, const float* logits, const int32_t* idx, float* lse_out, float2* kept, BlSpace w) {
+    balance_kernel(BlShape s, const float* logits, const int32_t* idx, float* lse_out, BlKept kept, BlSpace w) {
     constexpr int TPW = 32 / LPT, N2 = NV / 2, PLACE = 32 * NV;  // tokens of a warp, a lane's pairs of logits, floats of a place
     extern __shared__ __align__(16) float bl_smem[];  // [warps][BL_DEPTH][PLACE]; at a sequence's end sums [warps][256]
     __shared__ int cnt[BL_MAX_E];
@@ -250,14 +264,17 @@ __global__ void __launch_bounds__(BL_THREADS, 1)
             const float m = largest<LPT>(x);
             exponentials(x, m);
             const float sum = group_sum<LPT>(sum_of(x));
-            // A logarithm and a division of full precision, once a token: an lse next to zero is the logarithm of a sum next to
-            // 1 (or, in the backward pass, of its inverse), where __logf is off by 2^-21 and __fdividef's inverse by 2^-22.
-            // (131072 tokens of 256 experts, both passes: 90.5 us; 89.1 with these two.)
+            // logf: an lse next to zero is the logarithm of a sum next to 1, where __logf is off by 2^-21 (131072 tokens of 256
+            // experts, both passes: 90.8 us; 89.3 with __logf). The inverse is off by 2 units in the last place, as every
+            // exponential that it multiplies is (2000 tokens of 64 experts in 100 sequences: 17.5 us; 18.2 with a division).
             const float lse = m + logf(sum);
-            const float inv = sum == 0.f ? 0.f : 1.0f / sum;
+            const float inv = sum == 0.f ? 0.f : __fdividef(1.0f, sum);
             if (there && lig == 0) {
                 if (lse_out) lse_out[t] = lse;
-                if (kept) kept[t] = make_float2(m, inv);
+                if (kept.row) {
+                    kept.row[t] = make_float2(m, inv);
+                    kept.lse[t] = lse;
+                }
             }
             if (live && sum != 0.f) {
                 const f2 v = both<f2>(inv);
@@ -339,11 +356,6 @@ __global__ void __launch_bounds__(BL_THREADS, 1)
         pos = end;
     }
 }
-
-// What balance_backward reads: w_b / S', 2 w_z / N, a [S, E] without the 1 / S'.
-constexpr int BL_SAVED_HEAD = 4;  // floats
-// Behind them, each token's largest logit and 1 / sum of exp(l - that) (0 for a token without probabilities).
-__host__ __device__ __forceinline__ size_t kept_at(int S, int E) { return (BL_SAVED_HEAD + (size_t)S * E + 1) / 2 * 2; }  // floats
 
 struct BlEnd {
     int blocks, splits;  // blocks of 32 columns of a row; warps that share a job (a sequence's block), a power of two
@@ -488,7 +500,7 @@ __global__ void __launch_bounds__(BL_BACK_THREADS, BL_BACK_CTAS)
     const int first = blockIdx.x * s.chunk, last = min(s.T, first + s.chunk);
     const float up = dloss ? *dloss : 1.0f, wb = saved[0] * up, wz = saved[1] * up;  // dloss's factor in both
     const float* slopes = saved + BL_SAVED_HEAD;
-    const float2* kept = reinterpret_cast<const float2*>(saved + kept_at(s.S, s.E));
+    const BlKept kept = kept_of(const_cast<float*>(saved), s.S, s.E, s.T);
     int seq = -2, seq_end = 0;  // this lane's token's, and where it ends
     bool seq_live = false;
     f2 a[N2];  // w_b / S' times the slopes
@@ -501,13 +513,17 @@ __global__ void __launch_bounds__(BL_BACK_THREADS, BL_BACK_CTAS)
         int e = -1;
         float g = 0.f, d = 0.f;
         float2 kept = {0.f, 0.f};
+        float lse = 0.f;
         bool live = false;
     } one, two;
     auto fetch = [&](int t) {
         const bool there = t < last;
         one = two;
         two.live = there && (!s.mask || s.mask[t]);
-        if (there) two.kept = kept[t];
+        if (there) {
+            two.kept = kept.row[t];
+            two.lse = kept.lse[t];
+        }
         if (gates && there && lig < s.k) {
             const size_t at = (size_t)t * s.k + lig;
             two.e = idx[at];
@@ -529,7 +545,7 @@ __global__ void __launch_bounds__(BL_BACK_THREADS, BL_BACK_CTAS)
     for (; t - tig < last; t += step) {
         const int e0 = one.e;
         const bool there = t < last;
-        const float g0 = one.g, d0 = one.d, m = one.kept.x, inv = one.kept.y;
+        const float g0 = one.g, d0 = one.d, m = one.kept.x, inv = one.kept.y, lse = one.lse;
         bool live = one.live;
         const size_t at = (size_t)t * s.k + lig;
         fetch(t + 2 * step);
@@ -568,7 +584,7 @@ __global__ void __launch_bounds__(BL_BACK_THREADS, BL_BACK_CTAS)
         group_sums<LPT>(dot, gd, lane);
         live = live && seq_live && inv != 0.f;
         // p (a - sum p a + z's part): exp(l - m) times inv (a + c)
-        const float c = wz * (m - logf(inv)) - dot * inv;
+        const float c = wz * lse - dot * inv;
         const f2 vi = both<f2>(inv), vc = both<f2>(c * inv);
 #pragma unroll
         for (int i = 0; i < N2; ++i) x[i] = mul_(x[i], fma_(a[i], vi, vc));
@@ -756,7 +772,7 @@ MOE_API int moe_balance_saved_size(const moe_balance_config* c, size_t* bytes) {
     const int rc = check(c);
     if (rc) return rc;
     if (!bytes) return fail(MOE_ERR_ARG, "bytes is NULL");
-    *bytes = 4 * (kept_at(c->seqs, c->E) + 2 * (size_t)c->T);
+    *bytes = 4 * (kept_at(c->seqs, c->E) + 3 * (size_t)c->T);
     return MOE_OK;
 }
 
@@ -784,7 +800,7 @@ MOE_API int moe_balance_forward(const moe_balance_config* c, const float* logits
         const cudaError_t e0 = allow_smem<kernel>(ring_bytes(BL_THREADS, c->E));
         if (e0 != cudaSuccess) return e0;
         return launch_k(kernel, dim3(ctas), dim3(threads), ring_bytes(threads, c->E), st, true,
-                        s, logits, idx, lse, saved ? reinterpret_cast<float2*>(static_cast<float*>(saved) + kept_at(c->seqs, c->E)) : nullptr, w);
+                        s, logits, idx, lse, kept_of(static_cast<float*>(saved), c->seqs, c->E, c->T), w);
     });
     if (e != cudaSuccess) return cuda_fail(e, "balance loss launch");
     BlEnd f;
