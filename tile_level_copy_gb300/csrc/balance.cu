@@ -26,7 +26,7 @@ constexpr int BL_MAX_E = 256, BL_MAX_K = 8;
 constexpr int BL_END_WARPS = 32;   // of the second launch's CTAs, at most
 
 struct BlShape {
-    int T, E, k, S, chunk, ctas;  // a CTA takes `chunk` consecutive tokens
+    int T, E, k, S, chunk;  // a CTA takes `chunk` consecutive tokens
     const int32_t* offsets;
     const uint8_t* mask;
 };
@@ -82,7 +82,6 @@ __device__ __forceinline__ void fetch_rows(float* to, const float* from, int n, 
             if (lane + 32 * k < n) copy_async<4>(to + lane + 32 * k, from + lane + 32 * k);
     }
 }
-__device__ __forceinline__ void committed() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N>
 __device__ __forceinline__ void fetched() {  // all but the last N groups
     asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
@@ -715,7 +714,6 @@ BlShape shape_of(const moe_balance_config& c, const int32_t* offsets, const uint
     BlShape s;
     s.T = c.T, s.E = c.E, s.k = c.topk, s.S = c.seqs;
     s.chunk = c.T ? (c.T + ctas - 1) / ctas : 1;
-    s.ctas = ctas;
     s.offsets = offsets;
     s.mask = mask;
     return s;

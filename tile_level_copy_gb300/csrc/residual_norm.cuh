@@ -188,7 +188,6 @@ __device__ __forceinline__ void pad_row(uint8_t* to, const T* rows, int64_t at, 
     if (((end + 15) / 16 - 1 == last_piece<T>(d) ? owner : next_owner) && b < most) put(*reinterpret_cast<T*>(to + b), 0.f);
 }
 
-__device__ __forceinline__ void committed() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 __device__ __forceinline__ void fetched(int pending) {  // all but the last `pending` groups are there
     if (pending == 0) asm volatile("cp.async.wait_group 0;" ::: "memory");
     else if (pending == 1) asm volatile("cp.async.wait_group 1;" ::: "memory");

@@ -181,6 +181,8 @@ __device__ __forceinline__ void copy_async(void* to, const void* from) {
         asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(smem_u32(to)), "l"(from), "n"(BYTES) : "memory");
 }
 
+__device__ __forceinline__ void committed() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+
 // Sums of K values (a power of two up to 32) over a warp: lane l gets the total of value l / (32 / K).
 template <int K>
 __device__ __forceinline__ float warp_sums(float (&v)[K], int lane) {
