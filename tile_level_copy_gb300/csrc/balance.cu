@@ -184,21 +184,16 @@ struct BlSpace {
 
 // What balance_backward reads: w_b / S', 2 w_z / N, a [S, E] without the 1 / S'.
 constexpr int BL_SAVED_HEAD = 4;  // floats
-// Behind them, of each token the largest logit and 1 / sum of exp(l - that) (0 for a token without probabilities), then lse (from
+// Behind them, of each token the largest logit, 1 / sum of exp(l - that) (0 for a token without probabilities) and lse (from
 // the inverse it would carry that one's rounding as well, which is much of an lse next to zero, and cost a logarithm).
 struct BlKept {
-    float2* row;  // or null: nothing is kept
-    float* lse;
+    float m, inv, lse;
 };
-__host__ __device__ __forceinline__ size_t kept_at(int S, int E) { return (BL_SAVED_HEAD + (size_t)S * E + 1) / 2 * 2; }  // floats
-__host__ __device__ __forceinline__ BlKept kept_of(float* saved, int S, int E, int T) {
-    float2* const row = saved ? reinterpret_cast<float2*>(saved + kept_at(S, E)) : nullptr;
-    return BlKept{row, row ? reinterpret_cast<float*>(row + T) : nullptr};
-}
+__host__ __device__ __forceinline__ size_t kept_at(int S, int E) { return BL_SAVED_HEAD + (size_t)S * E; }  // floats
 
 template <int LPT, int NV, bool VEC>
 __global__ void __launch_bounds__(BL_THREADS, 1)
-    balance_kernel(BlShape s, const float* logits, const int32_t* idx, float* lse_out, BlKept kept, BlSpace w) {
+    balance_kernel(BlShape s, const float* logits, const int32_t* idx, float* lse_out, BlKept* kept, BlSpace w) {
     constexpr int TPW = 32 / LPT, N2 = NV / 2, PLACE = 32 * NV;  // tokens of a warp, a lane's pairs of logits, floats of a place
     extern __shared__ __align__(16) float bl_smem[];  // [warps][BL_DEPTH][PLACE]; at a sequence's end sums [warps][256]
     __shared__ int cnt[BL_MAX_E];
@@ -270,10 +265,7 @@ __global__ void __launch_bounds__(BL_THREADS, 1)
             const float inv = sum == 0.f ? 0.f : __fdividef(1.0f, sum);
             if (there && lig == 0) {
                 if (lse_out) lse_out[t] = lse;
-                if (kept.row) {
-                    kept.row[t] = make_float2(m, inv);
-                    kept.lse[t] = lse;
-                }
+                if (kept) kept[t] = BlKept{m, inv, lse};
             }
             if (live && sum != 0.f) {
                 const f2 v = both<f2>(inv);
@@ -499,7 +491,7 @@ __global__ void __launch_bounds__(BL_BACK_THREADS, BL_BACK_CTAS)
     const int first = blockIdx.x * s.chunk, last = min(s.T, first + s.chunk);
     const float up = dloss ? *dloss : 1.0f, wb = saved[0] * up, wz = saved[1] * up;  // dloss's factor in both
     const float* slopes = saved + BL_SAVED_HEAD;
-    const BlKept kept = kept_of(const_cast<float*>(saved), s.S, s.E, s.T);
+    const BlKept* kept = reinterpret_cast<const BlKept*>(saved + kept_at(s.S, s.E));
     int seq = -2, seq_end = 0;  // this lane's token's, and where it ends
     bool seq_live = false;
     f2 a[N2];  // w_b / S' times the slopes
@@ -511,18 +503,14 @@ __global__ void __launch_bounds__(BL_BACK_THREADS, BL_BACK_CTAS)
     struct Small {
         int e = -1;
         float g = 0.f, d = 0.f;
-        float2 kept = {0.f, 0.f};
-        float lse = 0.f;
+        BlKept kept = {0.f, 0.f, 0.f};
         bool live = false;
     } one, two;
     auto fetch = [&](int t) {
         const bool there = t < last;
         one = two;
         two.live = there && (!s.mask || s.mask[t]);
-        if (there) {
-            two.kept = kept.row[t];
-            two.lse = kept.lse[t];
-        }
+        if (there) two.kept = kept[t];
         if (gates && there && lig < s.k) {
             const size_t at = (size_t)t * s.k + lig;
             two.e = idx[at];
@@ -544,7 +532,7 @@ __global__ void __launch_bounds__(BL_BACK_THREADS, BL_BACK_CTAS)
     for (; t - tig < last; t += step) {
         const int e0 = one.e;
         const bool there = t < last;
-        const float g0 = one.g, d0 = one.d, m = one.kept.x, inv = one.kept.y, lse = one.lse;
+        const float g0 = one.g, d0 = one.d, m = one.kept.m, inv = one.kept.inv, lse = one.kept.lse;
         bool live = one.live;
         const size_t at = (size_t)t * s.k + lig;
         fetch(t + 2 * step);
@@ -798,7 +786,7 @@ MOE_API int moe_balance_forward(const moe_balance_config* c, const float* logits
         const cudaError_t e0 = allow_smem<kernel>(ring_bytes(BL_THREADS, c->E));
         if (e0 != cudaSuccess) return e0;
         return launch_k(kernel, dim3(ctas), dim3(threads), ring_bytes(threads, c->E), st, true,
-                        s, logits, idx, lse, kept_of(static_cast<float*>(saved), c->seqs, c->E, c->T), w);
+                        s, logits, idx, lse, saved ? reinterpret_cast<BlKept*>(static_cast<float*>(saved) + kept_at(c->seqs, c->E)) : nullptr, w);
     });
     if (e != cudaSuccess) return cuda_fail(e, "balance loss launch");
     BlEnd f;
