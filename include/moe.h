@@ -662,9 +662,11 @@ MOE_API int moe_residual_norm_backward(const moe_residual_norm_config* cfg, cons
  *   z = mean over all tokens of lse^2, lse[t] = log(sum_e exp(l[t, e]))
  *   loss = cfg.balance * balance + cfg.z * z
  * A sequence is the tokens offsets[s] <= t < offsets[s + 1] (offsets [seqs + 1], not decreasing, within [0, T]; NULL: one
- * sequence of all tokens, seqs = 1). Tokens outside of every sequence, tokens with mask[t] = 0 and tokens whose logits
+ * sequence of all tokens, seqs = 1. Offsets outside of [0, T] are taken as its ends; with decreasing ones the results mean
+ * nothing, but nothing outside of the buffers is touched). Tokens outside of every sequence, tokens with mask[t] = 0 and tokens whose logits
  * are all -inf are padding: they count nowhere and have no gradient. An entry of idx outside [0, E) is a dropped pair: it
- * counts nowhere (topk stays the divisor). An expert that occurs twice in a token's idx counts twice. No token: losses 0.
+ * counts nowhere (topk stays the divisor). Logits may have any finite size; z is infinite where the sum of lse^2 is beyond
+ * fp32 (from lse of about 1e19 on). An expert that occurs twice in a token's idx counts twice. No token: losses 0.
  * Limits: 0 <= T < 2^24, 1 <= E <= 256, 1 <= topk <= 8, 1 <= seqs < 2^24.
  */
 typedef struct moe_balance_config {
@@ -673,8 +675,8 @@ typedef struct moe_balance_config {
     int32_t reserved[4];
 } moe_balance_config;
 
-/* Bytes of the forward pass's workspace (partial sums), and of the buffer that it keeps for moe_balance_backward. Host
- * arithmetic only. */
+/* Bytes of the forward pass's workspace (partial sums; 8 E + 8 bytes and a little for each of seqs, used or not), and of the
+ * buffer that it keeps for moe_balance_backward. Host arithmetic only. */
 MOE_API int moe_balance_workspace_size(const moe_balance_config* cfg, size_t* bytes);
 MOE_API int moe_balance_saved_size(const moe_balance_config* cfg, size_t* bytes);
 
@@ -692,7 +694,8 @@ MOE_API int moe_balance_forward(const moe_balance_config* cfg, const float* logi
  * (counts are constants; cfg, idx, offsets and mask as in the forward pass, whose losses' weights lie in saved). dloss:
  * device f32 scalar, or NULL for 1. gates, dgates device f32 [T, topk], or both NULL: gates as moe_plan's topk_w
  * (softmax over the chosen logits) and the loss's gradients at them; to the logit of pair (t, j) comes
- * gates[t, j] * (dgates[t, j] - sum_i gates[t, i] dgates[t, i]), to that of a dropped pair nothing.
+ * gates[t, j] * (dgates[t, j] - sum_i gates[t, i] dgates[t, i]), to that of a dropped pair nothing: its entry of idx no longer
+ * names an expert. (Where pairs were dropped behind that softmax, their logits' share of it is the caller's to add.)
  */
 MOE_API int moe_balance_backward(const moe_balance_config* cfg, const float* logits, const int32_t* idx,
                                  const int32_t* offsets, const uint8_t* mask, const void* saved, const float* gates,

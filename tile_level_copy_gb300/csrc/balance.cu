@@ -5,13 +5,15 @@
 //   dl = dloss p (w_b / S' (a - sum_e p a) + 2 w_z / N lse) + the gates' part,  a[e] = E / (k n^2) c[e]
 //
 // The logits are read once in each direction and dlogits written once: HBM traffic bounds both passes. A row lies in
-// the registers of as many lanes as hold it with eight values a lane, so a warp works on 1 to 32 tokens at once.
+// the registers of as many lanes as hold it with eight values a lane (of 16 lanes with sixteen beyond 128 experts), so a
+// warp works on 2 to 32 tokens at once.
 // Forward: a CTA takes consecutive tokens and keeps its sums of p in registers until the sequence ends; counts
 // are integers in shared memory. What it has of a sequence goes to a row of the workspace: CTA and sequence both
 // grow along the tokens, so the pair's rank is their sum. A second launch adds the rows up in the order of the
 // CTAs (no sum depends on which CTA was first) and its last CTA makes the losses.
-// 131072 tokens of 256 experts in 67 sequences: 89 us for both passes (402 MB with the second read of the logits, 4.5 TB/s;
-// issue slots 57 to 61 % used). 16384 tokens of 64 experts: 17 us; 4096 of 8, forward: 8 us, two launches and the call.
+// Times here are those of calls that run one behind the other on the device. 131072 tokens of 256 experts in 67 sequences: 90 us
+// for both passes (402 MB with the second read of the logits, 4.5 TB/s; issue slots 54 to 63 % used). 16384 tokens of 64
+// experts: 15 us; 4096 of 8, forward: 6.7 us, two dependent launches.
 #include <math.h>
 
 #include "row_values.cuh"
@@ -259,7 +261,7 @@ __global__ void __launch_bounds__(BL_THREADS, 1)
             exponentials(x, m);
             const float sum = group_sum<LPT>(sum_of(x));
             // logf: an lse next to zero is the logarithm of a sum next to 1, where __logf is off by 2^-21 (131072 tokens of 256
-            // experts, both passes: 90.8 us; 89.3 with __logf). The inverse is off by 2 units in the last place, as every
+            // experts, both passes: 90.1 us; 89.3 with __logf). The inverse is off by 2 units in the last place, as every
             // exponential that it multiplies is (2000 tokens of 64 experts in 100 sequences: 17.5 us; 18.2 with a division).
             const float lse = m + logf(sum);
             const float inv = sum == 0.f ? 0.f : __fdividef(1.0f, sum);
@@ -669,7 +671,7 @@ int check(const moe_balance_config* c) {
 
 // Lanes of a token: with eight logits each, as few as hold a row; with more than 128 experts 16 lanes of sixteen: a warp
 // that has one token only spends most of its instructions on what a token costs whatever its row's length
-// (131072 tokens of 256 experts, both passes: 80 us instead of 92).
+// (131072 tokens of 256 experts in 67 sequences, both passes: 91 us instead of 112).
 int lanes_of(int E) {
     int l = 1;
     while (l * 8 < E && l < 16) l *= 2;
@@ -690,9 +692,12 @@ int most_ctas(const DeviceInfo& di, int threads) {
     const int n = di.sms * (threads < BL_THREADS ? 3 : 1);
     return n < BL_MAX_CTAS ? n : BL_MAX_CTAS;
 }
-// Large CTAs leave few rows of sums behind (131072 tokens of 256 experts in 67 sequences: the second launch takes 8.7 us
-// instead of 13). Where they would not all have work, or several sequences would end in one of them, small
-// ones are faster (509 tokens of 64 experts in 3 sequences, both passes: 11.7 us instead of 14.3).
+// Large CTAs leave few rows of sums behind (both passes over 16384 tokens of 64 experts: 15.1 us instead of 16.4, over 131072
+// 38.2 instead of 40.4). Where they would not all have work, or several sequences would end in one of them, small ones are
+// faster (16384 tokens of 64 experts in 300 sequences: 25.5 us instead of 30.5; 2000 in 100: 18.2 instead of 19.7). With 256
+// experts the two are close, and small ones ahead where there are many sequences (131072 tokens: 83.5 us with large and 84.4
+// with small ones in one sequence, 90.7 and 88.6 in 67); of few tokens and experts large ones are a little (4096 of 8,
+// forward: 6.3 us, 6.7 with small ones).
 int threads_of(const moe_balance_config& c, int sms) {
     const int pass = BL_THREADS / lanes_of(c.E);
     return c.T / pass >= sms / 2 && c.T / c.seqs >= pass ? BL_THREADS : 256;

@@ -3,12 +3,14 @@
 //   norm = sqrt(sum over all tensors of g^2), scale = min(1, max_norm / (norm + eps)); g = g * scale
 //
 // Every value is read once for the norm, read and written once for clipping: HBM traffic bounds both. A CTA takes
-// chunks of 32 KB; a thread squares the 128 bytes of a chunk that it loads in fp32 and adds their sum to a pair of
-// floats (sum and what its rounding cut off), so the length of the list costs no precision. The CTAs' sums are added
+// chunks of 32 KB; a thread squares the 128 bytes of a chunk that it loads in fp32, adds them in chains of eight (off by 11 *
+// 2^-24 of their sum at most) and that sum to a pair of floats (sum and what its rounding cut off, by the two-sum of
+// Knuth and Moller), so the length of the list costs no precision. The CTAs' sums are added
 // up in 64 bits by the CTA that finishes last, in the order of the CTAs: the result repeats bit for bit.
 // Squares that leave fp32's range are taken again in 64 bits, so a norm that fp32 can hold is found whatever the
 // values' size. 24 tensors, 149 million bf16 values: norm 47 us, 6.3 TB/s (92 % of a copy's rate); 64 bytes a thread in
-// flight: 52 us. 67 tensors, 1 million values: 6.5 us, one launch and the call on the host.
+// flight: 52 us. 67 tensors, 1 million values: 6.5 us, one launch and the call on the host. Clipping the long list
+// after its norm: 139 us for both; 48 where the factor is 1, which ends the clipping launch at once.
 #include <math.h>
 
 #include "row_values.cuh"

@@ -44,9 +44,9 @@ cudaError_t launch_residual_backward(RnShape s, const RnWeights& w, const RnBack
                                      int ctas, cudaStream_t st);
 
 inline int rn_warps(int d, int values) { return (d + 32 * values - 1) / (32 * values); }
-// Backward: values of a thread. With layer norms short rows take 8 where the rows are fp32 (8192 x 2048: 75 us instead of 81)
-// or groups of them have gates (a gate a row, 16384 x 2048 bf16: 375 us instead of 478), else 16 (16384 x 2048 bf16: 92 us
-// instead of 99); 32 of them spill, and only rows above 8192 need them.
+// Backward: values of a thread. With layer norms short rows take 8 where the rows are fp32 (8192 x 2048: 74 us instead of 80)
+// or groups of them have gates (a gate a row, 16384 x 2048 bf16: 425 us instead of 514), else 16 (16384 x 2048 bf16: 92 us
+// instead of 98); 32 of them spill, and only rows above 8192 need them.
 inline int rn_backward_values(int d, int dtype, bool full, bool grouped) {
     return full && (grouped || dtype == MOE_DTYPE_F32) && d <= 2048 ? 8 : d <= 8192 ? 16 : 32;
 }

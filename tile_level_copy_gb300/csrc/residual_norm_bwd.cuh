@@ -13,9 +13,10 @@
 // that share a gate: where these end, dgate is written and dw1 and db1, in the workspace, take them up. With one
 // gate for all rows that happens after the CTAs' sums are added up. Rows above 8192 values are read from global memory
 // twice: their slots would find no room beside the weights.
-// 16384 x 2048 bf16: layer norms 91 us (4.4 TB/s, 65 % of a copy's rate), mean-square norms 69 us (85 %). 51 instructions
+// Calls that run one behind the other, 16384 x 2048 bf16, fp32 weights: layer norms 92 us (4.4 TB/s, 64 % of a copy's rate),
+// mean-square norms 71 us (84 %; 72 with a gate). Layer norms take 51 instructions
 // a value at 128 registers, with which 16 warps fit a SM, fill 53 % of the issue slots. 3001 x 1411 fp16 with a gate for
-// each 250 rows: 34 us, five rows a group of warps between the kernel's start and the gates' ends.
+// each 250 rows: 35 us, five rows a group of warps between the kernel's start and the gates' ends.
 #pragma once
 
 #include "residual_norm.cuh"
@@ -43,7 +44,7 @@ struct RbUnits {
 };
 // Reads them (null, and beyond the row: `none`) and writes them, in 16-byte pieces where the vector's alignment allows
 // (`whole`). With a gate for every row single values bound the pass: a warp's lie 16 or 32 bytes apart (16384 x 2048
-// bf16: 400 us; in pieces 239).
+// bf16, mean-square norms: 254 us; in pieces 217).
 template <typename T, typename C>
 __device__ __forceinline__ RbUnits<C> vector_units(const C& c, const void* p, bool f32, bool whole, float none, int64_t at, int j0) {
     RbUnits<C> o;

@@ -6,8 +6,8 @@
 // memory by cp.async while the row before is worked on. h is rounded to its type before the second norm (the value
 // the backward pass and every other reader sees) and waits in x's place, or in registers, for the pass that writes z.
 // 16384 x 4096 bf16, mean-square norms: 101 us, 5.3 TB/s (78 % of a copy's rate); the warps wait for rows and at the sums'
-// barriers. 8192 x 4096 fp32 without a norm behind the block: 89 us (89 %). Rows of odd width, 8001 x 2047 bf16: 43 us
-// (45 %), as single values are loaded, checked and stored. 5 rows of 4096: 3 us.
+// barriers. 8192 x 4096 fp32 without a norm behind the block: 89 us (89 %). Rows of odd width, 8001 x 2047 bf16: 45 us
+// (43 %), as single values are loaded, checked and stored. 5 rows of 4096: 3 us. (Calls that run one behind the other.)
 #pragma once
 
 #include "residual_norm.cuh"
@@ -277,7 +277,7 @@ cudaError_t launch_residual_forward(RnShape s, const RnWeights& w, const RnForwa
     constexpr int MANY = 64 / (int)sizeof(T), FEW = 16 / (int)sizeof(T);
     const bool few = s.rows * rn_warps(s.d, MANY) < 16 * sms && rn_warps(s.d, FEW) <= 32;
     // ragged rows of half a warp's values or less: all places of a thread cost their instructions there
-    // (40001 x 301 bf16: 63 us instead of 87)
+    // (40001 x 301 bf16: 64 us instead of 87)
     const bool ragged = vec == 1 || !w.whole, small = few || (ragged && s.d <= 16 * MANY);
     s.warps = rn_warps(s.d, small ? FEW : MANY);
     s.groups = s.warps < 8 && !few ? 8 / s.warps : 1;
